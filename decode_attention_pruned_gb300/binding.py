@@ -24,6 +24,7 @@ POLICY_FULL, POLICY_LOCAL, POLICY_SPECIAL = 0, 1, 2
 
 # Every symbol include/leank.h declares, with (restype, argtypes).
 _vp, _i32, _sz, _u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_uint64
+_i64 = ctypes.c_int64
 
 
 class PlanDesc(ctypes.Structure):
@@ -48,6 +49,22 @@ STEP_AUTO, STEP_FUSED, STEP_SPLIT = 0, 1, 2
 
 class CacheOptions(ctypes.Structure):
     _fields_ = [("middle_tokens", ctypes.c_int64), ("kv_format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_YARN, ROPE_SCALE_BANDS = range(5)
+
+
+class Chunk(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ids", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("n_max", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("trained_positions", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double), ("magnitude", ctypes.c_double)]
 
 
 SIGNATURES = {
@@ -83,6 +100,13 @@ SIGNATURES = {
     "lk_step_host": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "lk_step_host_packed": (ctypes.c_int, [_vp, _i32, _vp, _i32, _vp, _vp, _sz, _vp]),
     "lk_step_layers_host_packed": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i32, _vp, _vp, _sz, _vp]),
+    "lk_chunk_workspace_bytes": (ctypes.c_int, [_vp, _i32, _i32, ctypes.POINTER(_sz)]),
+    "lk_chunk_attn": (ctypes.c_int, [_vp, _i32, ctypes.POINTER(Chunk), _vp, _vp, _sz, _vp]),
+    "lk_append_chunk": (ctypes.c_int, [_vp, _i32, ctypes.POINTER(Chunk), _vp]),
+    "lk_extend": (ctypes.c_int, [_vp, _i32, ctypes.POINTER(Chunk), _vp, _vp, _sz, _vp]),
+    "lk_build_rope": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(_vp)]),
+    "lk_rope_destroy": (None, [_vp]),
+    "lk_rope_apply": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
     "lk_cache_length": (ctypes.c_int, [_vp, _i32, ctypes.POINTER(_i32)]),
     "lk_cache_lengths": (ctypes.c_int, [_vp, _i32, _vp]),
     "lk_cache_region": (ctypes.c_int, [_vp, _i32, _i32, _i32, ctypes.POINTER(RegionInfo)]),
@@ -150,6 +174,82 @@ def _need(t, dtype, shape, what, device_kind="cuda"):
         raise TypeError(f"{what} must be a torch tensor") from None
     raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)} on {device_kind}, got "
                      f"{t.dtype} {tuple(t.shape)} on {t.device.type}")
+
+
+def _token_stride(t, heads, lead, what):
+    """Elements between consecutive tokens of a bf16 [*lead, heads, 128] CUDA
+    tensor whose heads are dense and whose tokens are evenly spaced."""
+    import torch
+    try:
+        shape, stride = t.shape, t.stride()
+    except AttributeError:
+        raise TypeError(f"{what} must be a torch tensor") from None
+    if t.dtype is not torch.bfloat16 or t.device.type != "cuda" or shape != (*lead, heads, 128):
+        raise ValueError(f"{what}: expected {torch.bfloat16} {(*lead, heads, 128)} on cuda, got {t.dtype} "
+                         f"{tuple(shape)} on {t.device.type}")
+    if t.is_contiguous():
+        return heads * 128
+    even, step, rows = True, None, 1
+    for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+        if n > 1:
+            if step is None:
+                step = s // rows if s % rows == 0 else -1
+            even = even and s == step * rows
+        rows *= n
+    if not even or stride[-1] != 1 or (heads > 1 and stride[-2] != 128):
+        raise ValueError(f"{what}: heads must be dense and tokens evenly spaced, got strides {stride} for "
+                         f"{tuple(shape)}")
+    return heads * 128 if step is None else step
+
+
+class Rope:
+    """lk_build_rope: rotary positions of heads of 128 channels."""
+
+    def __init__(self, rotary_dim=128, base=10000.0, layout=ROPE_HALF, scaling=ROPE_SCALE_NONE, factor=1.0,
+                 trained_positions=0, low_turns=0.0, high_turns=0.0, magnitude=0.0):
+        lib = load()
+        self.desc = RopeDesc(rotary_dim, layout, scaling, trained_positions, base, factor, low_turns, high_turns,
+                             magnitude)
+        h = ctypes.c_void_p()
+        _check(lib.lk_build_rope(ctypes.byref(self.desc), ctypes.byref(h)))
+        self._h = h
+
+    def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        """lk_rope_apply: q [..., Hq, 128] and k [..., Hkv, 128] bf16 (tokens
+        evenly spaced, e.g. views of one projection's rows), positions int32
+        [...]; q or k may be None.  Returns (q_out, k_out), new dense tensors
+        unless given; q and k themselves may be given."""
+        import torch
+        if q is None and k is None:
+            raise ValueError("q and k are both None")
+        lead = tuple((q if q is not None else k).shape[:-2])
+        tokens = 1
+        for n in lead:
+            tokens *= n
+        _need(positions, torch.int32, lead, "positions")
+        args, outs = [], []
+        for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
+            if x is None:
+                if y is not None:
+                    raise ValueError(f"{what}_out without {what}")
+                args.append((None, 0, 0, None, 0))
+                outs.append(None)
+                continue
+            heads = x.shape[-2]
+            step = _token_stride(x, heads, lead, what)
+            if y is None:
+                y = torch.empty((*lead, heads, 128), dtype=torch.bfloat16, device=x.device)
+            args.append((x.data_ptr(), step, heads, y.data_ptr(), _token_stride(y, heads, lead, what + "_out")))
+            outs.append(y)
+        (qp, qs, hq, qo, qos), (kp, ks, hk, ko, kos) = args
+        _check(_lib.lk_rope_apply(self._h, qp, qs, kp, ks, positions.data_ptr(), tokens, hq, hk, qo, qos, ko, kos,
+                                  _stream(stream)))
+        return tuple(outs)
+
+    def __del__(self):
+        if getattr(self, "_h", None) and _lib is not None:
+            _lib.lk_rope_destroy(self._h)
+            self._h = None
 
 
 def build_masks(alpha, prune_pct, align=32, exact=False, eligible=None, stream=None):
@@ -247,6 +347,7 @@ class Cache:
         nbytes = plan.cache_bytes(batch, capacity, middle_tokens, kv_format)
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         self.workspace = torch.empty(plan.workspace_bytes(batch), dtype=torch.uint8, device=dev)
+        self.chunk_workspace = None          # made by the first chunk_attn or extend
         h = ctypes.c_void_p()
         s = _stream(stream)
         if kv_format != KV_BF16:
@@ -486,6 +587,64 @@ class Cache:
         _check(_lib.lk_step_layers_host_packed(self._h, layer0, nlayers, host_in.data_ptr(), 1 if with_ids else 0,
                                                o.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(),
                                                _stream(stream)))
+
+    # -- chunks of new tokens
+    def _chunk(self, q, k, v, lens, ids):
+        """The lk_chunk of a call, and the host lengths that it points to."""
+        import torch
+        B, H = self.batch, self.plan.num_kv_heads
+        n = k.shape[1] if k.dim() == 4 else -1
+        c = Chunk()
+        if q is not None:
+            c.q, c.q_stride = q.data_ptr(), _token_stride(q, self.plan.num_q_heads, (B, n), "q")
+        c.k, c.k_stride = k.data_ptr(), _token_stride(k, H, (B, n), "k")
+        c.v, c.v_stride = v.data_ptr(), _token_stride(v, H, (B, n), "v")
+        c.n_max = n
+        if ids is not None:
+            _need(ids, torch.int32, (B, n), "ids")
+            c.ids = ids.data_ptr()
+        if lens is not None:
+            lens = np.ascontiguousarray(lens, dtype=np.int32)
+            if lens.shape != (B,):
+                raise ValueError(f"lens shape {lens.shape}")
+            c.lens = lens.ctypes.data
+        return c, lens
+
+    def _chunk_out(self, q, o):
+        import torch
+        shape = (self.batch, q.shape[1], self.plan.num_q_heads, 128)
+        if o is None:
+            o = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        _need(o, torch.bfloat16, shape, "o")
+        if self.chunk_workspace is None:
+            # of the size that no chunk exceeds, and kept: a captured call finds it again
+            n = ctypes.c_size_t()
+            _check(_lib.lk_chunk_workspace_bytes(self.plan._h, self.batch, (1 << 31) - 1, ctypes.byref(n)))
+            self.chunk_workspace = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        return o
+
+    def chunk_attn(self, layer, q, k, v, lens=None, ids=None, o=None, stream=None):
+        """lk_chunk_attn: q [B, n, Hq, 128], k, v [B, n, Hkv, 128] bf16 (tokens
+        evenly spaced), lens: B host ints -> o [B, n, Hq, 128] bf16.  The cache
+        is only read; rows of o past a sequence's length are left as they are."""
+        c, lens = self._chunk(q, k, v, lens, ids)
+        o = self._chunk_out(q, o)
+        _check(_lib.lk_chunk_attn(self._h, layer, ctypes.byref(c), o.data_ptr(), self.chunk_workspace.data_ptr(),
+                                  self.chunk_workspace.numel(), _stream(stream)))
+        return o
+
+    def append_chunk(self, layer, k, v, lens=None, ids=None, stream=None):
+        """lk_append_chunk: the first lens[b] of the chunk's tokens enter the layer."""
+        c, lens = self._chunk(None, k, v, lens, ids)
+        _check(_lib.lk_append_chunk(self._h, layer, ctypes.byref(c), _stream(stream)))
+
+    def extend(self, layer, q, k, v, lens=None, ids=None, o=None, stream=None):
+        """lk_extend: chunk_attn, then append_chunk of the same tokens."""
+        c, lens = self._chunk(q, k, v, lens, ids)
+        o = self._chunk_out(q, o)
+        _check(_lib.lk_extend(self._h, layer, ctypes.byref(c), o.data_ptr(), self.chunk_workspace.data_ptr(),
+                              self.chunk_workspace.numel(), _stream(stream)))
+        return o
 
     # -- queries
     def length(self, layer):

@@ -12,6 +12,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -46,6 +47,8 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 constexpr uint64_t kWaitLimitNs = 1000000000ull;      // 1 s bound on device waits
 constexpr uint64_t kMaxWaitLimitNs = 10000000000ull;  // lk_set_wait_limit: at most 10 s
 constexpr int64_t kMaxPoolRows = (1ll << 31) - 2 * kTmaBoxRows;
+constexpr int64_t kMaxTokenStride = 1ll << 32;        // elements between tokens of a chunk (TMA strides are 40-bit)
+constexpr int kMaxRopeHeads = 1 << 14;
 
 }  // namespace
 
@@ -56,6 +59,12 @@ struct lk_plan_s {
   std::vector<int16_t> kept;        // [L][Hkv][128] kept channels ascending, then the pruned ones
   std::vector<uint8_t> is_special;  // [vocab]
   std::vector<uint8_t> layer_special;
+};
+
+struct lk_rope_s {
+  lk_rope_desc d;
+  float magnitude;
+  uint64_t freq[kHeadDim / 2] = {};  // turns per position x 2^64
 };
 
 namespace {
@@ -286,6 +295,13 @@ WsLayout ws_layout(const lk_plan_desc& d, int B) {
   off = align_up(off + (size_t)B * d.num_q_heads * kHeadDim * 4, 256);
   w.total = off;
   return w;
+}
+
+// Workspace of lk_chunk_attn for chunks of up to n_max tokens.
+size_t chunk_workspace(const lk_plan_desc& d, int n_max) {
+  (void)d;
+  (void)n_max;
+  return 256;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -1183,6 +1199,267 @@ lk_status lk_step_layers_host_packed(lk_cache cache, int32_t layer0, int32_t nla
   if (st != LK_OK) return st;
   cudaError_t err = launch_decode(cache->maps, a, ctas, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_fail(err, "lk_step_layers_host_packed decode launch");
+  return LK_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Chunks of new tokens
+namespace {
+
+// Tokens of the chunk that sequence b takes: none while its slot is released.
+int32_t chunk_tokens(const lk_cache_s* cache, const lk_chunk* c, int b) {
+  return !cache->active[b] ? 0 : c->lens ? c->lens[b] : c->n_max;
+}
+
+// Checks of a chunk and its launch arguments; need: the pages its append pops
+// (taken off nothing here).  `write`: the append's checks, else the attention's.
+lk_status chunk_prepare(lk_cache cache, int32_t layer, const lk_chunk* c, bool write, const char* what, ChunkArgs& a,
+                        int64_t need[kNumPools]) {
+  if (!cache) return fail(LK_ERR_ARG, "%s: null cache", what);
+  if (layer < 0 || layer >= cache->cv.L) return fail(LK_ERR_ARG, "%s: layer %d out of range", what, layer);
+  if (!c) return fail(LK_ERR_ARG, "%s: null chunk", what);
+  if (c->n_max < 0) return fail(LK_ERR_ARG, "%s: n_max = %d < 0", what, c->n_max);
+  if (c->reserved != 0) return fail(LK_ERR_ARG, "%s: reserved must be 0", what);
+  const CacheView& cv = cache->cv;
+  const int B = cache->B;
+  for (int pl = 0; pl < kNumPools; ++pl) need[pl] = 0;
+  for (int b = 0; b < B; ++b) {
+    if (c->lens && (c->lens[b] < 0 || c->lens[b] > c->n_max))
+      return fail(LK_ERR_ARG, "%s: length %d of sequence %d outside [0, %d]", what, c->lens[b], b, c->n_max);
+    const int32_t n = chunk_tokens(cache, c, b);
+    if (!write || n == 0) continue;
+    const int32_t held = cache->host_len[(size_t)layer * B + b];
+    if (n > cache->cap - held)
+      return fail(LK_ERR_CAPACITY, "%s: sequence %d of layer %d holds %d tokens; %d more exceed %d", what, b, layer,
+                  held, n, cache->cap);
+    cache->pages_needed(layer, held, held + n, need);
+  }
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return cuda_fail(err, what);
+  if (dev != cache->device)
+    return fail(LK_ERR_STATE, "%s: the cache is on device %d; the current device is %d", what, cache->device, dev);
+  a = ChunkArgs{};
+  a.cv = cv;
+  a.layer = layer;
+  a.n_max = c->n_max;
+  if (c->n_max == 0) return LK_OK;
+  if ((!write && !c->q) || !c->k || !c->v) return fail(LK_ERR_ARG, "%s: null q, k or v", what);
+  if ((!write && !aligned(c->q, 16)) || !aligned(c->k, 16) || !aligned(c->v, 16))
+    return fail(LK_ERR_ALIGN, "%s: q, k and v must be 16-byte aligned", what);
+  if (c->ids && !aligned(c->ids, 4)) return fail(LK_ERR_ALIGN, "%s: ids must be 4-byte aligned", what);
+  const int64_t dense[3] = {(int64_t)cv.Hq * kHeadDim, (int64_t)cv.Hkv * kHeadDim, (int64_t)cv.Hkv * kHeadDim};
+  const int64_t given[3] = {write ? 0 : c->q_stride, c->k_stride, c->v_stride};
+  int64_t stride[3];
+  for (int i = 0; i < 3; ++i) {
+    stride[i] = given[i] == 0 ? dense[i] : given[i];
+    if (stride[i] < dense[i] || stride[i] % 8 != 0 || stride[i] > kMaxTokenStride)
+      return fail(LK_ERR_ARG, "%s: %c_stride %lld is not 0 or a multiple of 8 in [%lld, %lld]", what, "qkv"[i],
+                  (long long)given[i], (long long)dense[i], (long long)kMaxTokenStride);
+  }
+  a.q = static_cast<const uint16_t*>(c->q);
+  a.k = static_cast<const uint16_t*>(c->k);
+  a.v = static_cast<const uint16_t*>(c->v);
+  a.q_stride = stride[0];
+  a.k_stride = stride[1];
+  a.v_stride = stride[2];
+  a.ids = c->ids;
+  return LK_OK;
+}
+
+// Launches in groups of kChunkSeqs sequences; groups without a token are left out.
+template <typename Launch>
+cudaError_t chunk_groups(const lk_cache_s* cache, const lk_chunk* c, ChunkArgs& a, Launch launch) {
+  for (int b0 = 0; b0 < cache->B; b0 += kChunkSeqs) {
+    a.b0 = b0;
+    a.nb = std::min(kChunkSeqs, cache->B - b0);
+    for (int i = 0; i < a.nb; ++i) a.lens[i] = chunk_tokens(cache, c, b0 + i);
+    if (*std::max_element(a.lens, a.lens + a.nb) == 0) continue;
+    cudaError_t err = launch(a);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+lk_status chunk_attn_ready(lk_cache cache, const void* o, const void* workspace, size_t ws_bytes, int32_t n_max,
+                           const char* what) {
+  if (n_max == 0) return LK_OK;
+  if (!o || !workspace) return fail(LK_ERR_ARG, "%s: null o or workspace", what);
+  if (!aligned(o, 16)) return fail(LK_ERR_ALIGN, "%s: o must be 16-byte aligned", what);
+  if (!aligned(workspace, 256)) return fail(LK_ERR_ALIGN, "%s: workspace must be 256-byte aligned", what);
+  const size_t need = chunk_workspace(cache->plan.d, n_max);
+  if (ws_bytes < need) return fail(LK_ERR_CAPACITY, "%s: workspace has %zu bytes; %zu needed", what, ws_bytes, need);
+  return LK_OK;
+}
+
+lk_status chunk_append_run(lk_cache cache, const lk_chunk* c, ChunkArgs& a, const int64_t need[kNumPools],
+                           const char* what, cudaStream_t s) {
+  lk_status st = cache->take_pages(need, what);
+  if (st != LK_OK) return st;
+  bool middle = false;
+  for (int h = 0; h < cache->cv.Hkv; ++h) middle |= cache->lay.heads[(size_t)a.layer * cache->cv.Hkv + h].cap_b > 0;
+  cudaError_t err = chunk_groups(
+      cache, c, a, [&](const ChunkArgs& g) { return launch_chunk_append(g, middle, cache->num_sms, s); });
+  if (err != cudaSuccess) {
+    return_pages(cache, need);
+    return cuda_fail(err, what);
+  }
+  for (int b = 0; b < cache->B; ++b) cache->host_len[(size_t)a.layer * cache->B + b] += chunk_tokens(cache, c, b);
+  return LK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lk_status lk_chunk_workspace_bytes(lk_plan plan, int32_t batch, int32_t n_max, size_t* bytes) {
+  if (!plan || !bytes) return fail(LK_ERR_ARG, "lk_chunk_workspace_bytes: null argument");
+  if (batch < 1 || (int64_t)batch * plan->d.num_kv_heads > (1 << 20))
+    return fail(LK_ERR_ARG, "batch %d out of range", batch);
+  if (n_max < 0) return fail(LK_ERR_ARG, "lk_chunk_workspace_bytes: n_max = %d < 0", n_max);
+  *bytes = chunk_workspace(plan->d, n_max);
+  return LK_OK;
+}
+
+lk_status lk_chunk_attn(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* o, void* workspace,
+                        size_t ws_bytes, void* stream) {
+  ChunkArgs a;
+  int64_t need[kNumPools];
+  lk_status st = chunk_prepare(cache, layer, chunk, false, "lk_chunk_attn", a, need);
+  if (st == LK_OK) st = chunk_attn_ready(cache, o, workspace, ws_bytes, chunk->n_max, "lk_chunk_attn");
+  if (st != LK_OK) return st;
+  a.o = static_cast<uint16_t*>(o);
+  cudaError_t err = chunk_groups(cache, chunk, a, [&](const ChunkArgs& g) {
+    return launch_chunk_attn(g, cache->num_sms, static_cast<cudaStream_t>(stream));
+  });
+  if (err != cudaSuccess) return cuda_fail(err, "lk_chunk_attn launch");
+  return LK_OK;
+}
+
+lk_status lk_append_chunk(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* stream) {
+  ChunkArgs a;
+  int64_t need[kNumPools];
+  lk_status st = chunk_prepare(cache, layer, chunk, true, "lk_append_chunk", a, need);
+  if (st != LK_OK) return st;
+  return chunk_append_run(cache, chunk, a, need, "lk_append_chunk", static_cast<cudaStream_t>(stream));
+}
+
+lk_status lk_extend(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* o, void* workspace, size_t ws_bytes,
+                    void* stream) {
+  ChunkArgs a, w;
+  int64_t need[kNumPools];
+  lk_status st = chunk_prepare(cache, layer, chunk, false, "lk_extend", a, need);
+  if (st == LK_OK) st = chunk_attn_ready(cache, o, workspace, ws_bytes, chunk->n_max, "lk_extend");
+  if (st == LK_OK) st = chunk_prepare(cache, layer, chunk, true, "lk_extend", w, need);
+  if (st != LK_OK) return st;
+  for (int pl = 0; pl < kNumPools; ++pl)
+    if (need[pl] > cache->host_free[pl]) return cache->take_pages(need, "lk_extend");   // says which, takes none
+  a.o = static_cast<uint16_t*>(o);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err = chunk_groups(cache, chunk, a, [&](const ChunkArgs& g) { return launch_chunk_attn(g, cache->num_sms, s); });
+  if (err != cudaSuccess) return cuda_fail(err, "lk_extend launch");
+  return chunk_append_run(cache, chunk, w, need, "lk_extend", s);
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions
+lk_status lk_build_rope(const lk_rope_desc* desc, lk_rope* out) {
+  if (!desc || !out) return fail(LK_ERR_ARG, "lk_build_rope: null argument");
+  *out = nullptr;
+  const lk_rope_desc& d = *desc;
+  if (d.rotary_dim < 16 || d.rotary_dim > kHeadDim || d.rotary_dim % 16 != 0)
+    return fail(LK_ERR_UNSUPPORTED, "rotary_dim %d is not a multiple of 16 in [16, 128]", d.rotary_dim);
+  if (d.layout != LK_ROPE_HALF && d.layout != LK_ROPE_INTERLEAVED)
+    return fail(LK_ERR_ARG, "layout %d is not LK_ROPE_HALF or LK_ROPE_INTERLEAVED", d.layout);
+  if (d.scaling < LK_ROPE_SCALE_NONE || d.scaling > LK_ROPE_SCALE_BANDS)
+    return fail(LK_ERR_ARG, "scaling %d is not an lk_rope_scaling", d.scaling);
+  if (!(d.base > 1.0) || !std::isfinite(d.base)) return fail(LK_ERR_ARG, "base %g must be finite and > 1", d.base);
+  const bool scaled = d.scaling != LK_ROPE_SCALE_NONE;
+  if (scaled && (!(d.factor >= 1.0) || !std::isfinite(d.factor)))
+    return fail(LK_ERR_ARG, "factor %g must be finite and >= 1", d.factor);
+  const bool yarn = d.scaling == LK_ROPE_SCALE_YARN, bands = d.scaling == LK_ROPE_SCALE_BANDS;
+  const double low = d.low_turns != 0.0 ? d.low_turns : 1.0;
+  const double high = d.high_turns != 0.0 ? d.high_turns : yarn ? 32.0 : 4.0;
+  if (yarn || bands) {
+    if (d.trained_positions < 1) return fail(LK_ERR_ARG, "trained_positions %d < 1", d.trained_positions);
+    if (!(low > 0.0) || !(high > low) || !std::isfinite(high))
+      return fail(LK_ERR_ARG, "turns (%g, %g) must be 0 < low < high", low, high);
+  }
+  if (!(d.magnitude >= 0.0) || !std::isfinite(d.magnitude))
+    return fail(LK_ERR_ARG, "magnitude %g must be finite and >= 0", d.magnitude);
+  auto r = new (std::nothrow) lk_rope_s();
+  if (!r) return fail(LK_ERR_CAPACITY, "lk_build_rope: out of host memory");
+  r->d = d;
+  const double dim = d.rotary_dim, two_pi = 6.283185307179586476925;
+  const double base = d.scaling == LK_ROPE_SCALE_NTK ? d.base * std::pow(d.factor, dim / (dim - 2.0)) : d.base;
+  auto at = [&](double turns) {
+    return dim * std::log(d.trained_positions / (turns * two_pi)) / (2.0 * std::log(base));
+  };
+  const double lo = yarn ? std::max(std::floor(at(high)), 0.0) : 0.0;
+  const double hi = yarn ? std::min(std::ceil(at(low)), dim - 1.0) : 0.0;
+  for (int i = 0; i < d.rotary_dim / 2; ++i) {
+    double w = std::pow(base, -2.0 * i / dim);
+    double keep = d.scaling == LK_ROPE_SCALE_LINEAR ? 0.0 : 1.0;      // share of w that is not stretched
+    if (yarn) keep = 1.0 - std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+    if (bands) keep = std::min(std::max((d.trained_positions * w / two_pi - low) / (high - low), 0.0), 1.0);
+    if (scaled && d.scaling != LK_ROPE_SCALE_NTK) w = w * keep + w / d.factor * (1.0 - keep);
+    r->freq[i] = (uint64_t)std::ldexp(w / two_pi, 64);                // w <= 1: below 2^62
+  }
+  r->magnitude = d.magnitude != 0.0 ? (float)d.magnitude : yarn ? (float)(0.1 * std::log(d.factor) + 1.0) : 1.f;
+  *out = r;
+  return LK_OK;
+}
+
+void lk_rope_destroy(lk_rope rope) { delete rope; }
+
+lk_status lk_rope_apply(lk_rope rope, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const int32_t* positions, int64_t tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                        void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  if (!rope) return fail(LK_ERR_ARG, "lk_rope_apply: null rope");
+  if (num_q_heads < 0 || num_kv_heads < 0 || num_q_heads > kMaxRopeHeads || num_kv_heads > kMaxRopeHeads)
+    return fail(LK_ERR_ARG, "lk_rope_apply: head counts (%d, %d) outside [0, %d]", num_q_heads, num_kv_heads,
+                kMaxRopeHeads);
+  if (tokens < 0 || tokens > INT32_MAX)
+    return fail(LK_ERR_ARG, "lk_rope_apply: tokens %lld outside [0, 2^31)", (long long)tokens);
+  if (tokens == 0 || num_q_heads + num_kv_heads == 0) return LK_OK;
+  if (!positions) return fail(LK_ERR_ARG, "lk_rope_apply: null positions");
+  if (!aligned(positions, 4)) return fail(LK_ERR_ALIGN, "lk_rope_apply: positions must be 4-byte aligned");
+  const void* ptr[4] = {q, q_out, k, k_out};
+  int64_t stride[4] = {q_stride, q_out_stride, k_stride, k_out_stride};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t dense = (int64_t)(i < 2 ? num_q_heads : num_kv_heads) * kHeadDim;
+    const char* name = i < 2 ? "q" : "k";
+    if (dense == 0) continue;
+    if (!ptr[i]) return fail(LK_ERR_ARG, "lk_rope_apply: null %s or %s_out", name, name);
+    if (!aligned(ptr[i], 16)) return fail(LK_ERR_ALIGN, "lk_rope_apply: %s and %s_out must be 16-byte aligned", name, name);
+    if (stride[i] == 0) stride[i] = dense;
+    if (stride[i] < dense || stride[i] % 8 != 0 || stride[i] > kMaxTokenStride)
+      return fail(LK_ERR_ARG, "lk_rope_apply: a stride of %s, %lld, is not 0 or a multiple of 8 in [%lld, %lld]", name,
+                  (long long)stride[i], (long long)dense, (long long)kMaxTokenStride);
+    if (i % 2 == 1 && ptr[i] == ptr[i - 1] && stride[i] != stride[i - 1])
+      return fail(LK_ERR_ARG, "lk_rope_apply: %s in place needs equal strides", name);
+  }
+  RopeArgs a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.q_stride = stride[0];
+  a.q_out_stride = stride[1];
+  a.k_stride = stride[2];
+  a.k_out_stride = stride[3];
+  a.positions = positions;
+  a.tokens = tokens;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.rotary_dim = rope->d.rotary_dim;
+  a.layout = rope->d.layout;
+  a.magnitude = rope->magnitude;
+  std::memcpy(a.freq, rope->freq, sizeof(a.freq));
+  cudaError_t err = launch_rope(a, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "lk_rope_apply launch");
   return LK_OK;
 }
 

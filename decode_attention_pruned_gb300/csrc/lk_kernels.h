@@ -86,6 +86,39 @@ struct PrefillArgs {
   int32_t n;                // tokens per sequence in k / v / ids (the longest length)
 };
 
+// One chunk of new tokens for up to kChunkSeqs sequences b0 .. b0 + nb - 1 (a
+// batch of more is several launches).  The lengths travel by value, so that a
+// captured launch keeps its own.
+constexpr int kChunkSeqs = 256;
+struct ChunkArgs {
+  CacheView cv;
+  int32_t layer;
+  int32_t b0, nb;
+  int32_t n_max;            // tokens per sequence in q / k / v / ids / o
+  const uint16_t* q;        // bf16 [B][n_max][Hq][128], tokens q_stride elements apart
+  const uint16_t* k;        // bf16 [B][n_max][Hkv][128]
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* ids;       // [B][n_max] or null
+  uint16_t* o;              // bf16 [B][n_max][Hq][128]
+  int32_t lens[kChunkSeqs]; // new tokens of sequence b0 + i
+};
+
+enum RopeLayout : int32_t { kRopeHalf = 0, kRopeInterleaved = 1 };
+struct RopeArgs {
+  const uint16_t* q;        // bf16 [tokens][Hq][128], tokens q_stride elements apart
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  const int32_t* positions; // [tokens]
+  int64_t tokens;
+  int32_t Hq, Hkv;
+  int32_t rotary_dim, layout;
+  float magnitude;          // multiplies cosine and sine
+  uint64_t freq[kHeadDim / 2];   // turns per position x 2^64
+};
+
 // Raise kernel `fn`'s dynamic shared-memory limit to `bytes` on the current
 // device the first time it launches there: the attribute is per device, so
 // `done` keeps one bit per device ordinal (ordinals past 63 set it every
@@ -109,5 +142,9 @@ cudaError_t launch_prefill(const PrefillArgs& args, bool has_special, int num_sm
 cudaError_t launch_release(const CacheView& cv, int b, cudaStream_t stream);
 cudaError_t launch_build_masks(const float* alpha, const uint8_t* eligible, int nh, double pct, int align,
                                int exact, uint8_t* masks, cudaStream_t stream);
+
+cudaError_t launch_chunk_append(const ChunkArgs& args, bool has_middle, int num_sms, cudaStream_t stream);
+cudaError_t launch_chunk_attn(const ChunkArgs& args, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs& args, cudaStream_t stream);
 
 }  // namespace lk

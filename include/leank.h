@@ -381,6 +381,129 @@ lk_status lk_step_layers_host_packed(lk_cache cache, int32_t layer0, int32_t nla
                                      int32_t has_ids, float* o_host, void* workspace, size_t ws_bytes,
                                      void* stream);
 
+/* A chunk of new tokens for every sequence of a cache: the tokens of a prompt
+ * that arrives in pieces, or drafted tokens to be verified.  Sequence b's token
+ * i is row b * n_max + i of the tensors; its position is the number of tokens
+ * that the sequence holds plus i.
+ *   q          device bf16 [B][n_max][Hq][128] (lk_append_chunk ignores it)
+ *   k, v       device bf16 [B][n_max][Hkv][128]
+ *   ids        device int32 [B][n_max] or NULL (no token is special)
+ *   lens       host int32 [B], each in [0, n_max], or NULL (n_max each); read
+ *              before the call returns.  Rows past lens[b] are never read and,
+ *              in the output, never written.
+ *   n_max      tokens per sequence of the tensors
+ *   *_stride   elements between consecutive tokens of q, k and v: at least
+ *              heads * 128 and a multiple of 8, or 0 for dense rows.  A row's
+ *              heads are dense, so q, k and v may be views of one projection's
+ *              rows.
+ * Released slots take no tokens, as if their length here were 0. */
+typedef struct lk_chunk {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* ids;
+  const int32_t* lens;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  int32_t n_max;
+  int32_t reserved;           /* 0 */
+} lk_chunk;
+
+/* Bytes of lk_chunk_attn's workspace for chunks of up to n_max tokens.  It
+ * needs no initialisation and may be shared by calls that do not overlap on
+ * the GPU. */
+lk_status lk_chunk_workspace_bytes(lk_plan plan, int32_t batch, int32_t n_max, size_t* bytes);
+
+/* Attention of a chunk's queries over the cache and the chunk itself (chunked
+ * prefill and draft verification over the split cache of LeanK 3.1 with
+ * FastGen 3.2's per-policy ranges).  The cache is only read: append the chunk,
+ * or the part of it that was accepted, afterwards.
+ *   o  device bf16 [B][n_max][Hq][128], dense.
+ * Query i of sequence b, at position p, sees of the token at position t <= p
+ * what a decode step at p would have seen had the chunk been appended token by
+ * token: FULL heads score it at all channels if t < S or p - t < W, else at
+ * the kept channels (not at all when none is kept); LOCAL heads see the last
+ * local_only_window tokens; SPECIAL heads the special ones that they have rows
+ * for.  One softmax runs over all of it; a query that sees nothing gives 0.
+ * Middle tokens are read as the cache holds them when the call runs: sealed
+ * INT8 / FP8 blocks as their dequantised values, everything else, the chunk's
+ * own tokens included, in bf16.
+ * k, v and the cache must hold finite values.  workspace: >=
+ * lk_chunk_workspace_bytes bytes, 256-byte aligned.  Errors: LK_ERR_ARG,
+ * LK_ERR_ALIGN (16 bytes for q, k, v, o; 4 for ids), LK_ERR_CAPACITY
+ * (workspace), LK_ERR_STATE (the current device is not the cache's). */
+lk_status lk_chunk_attn(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* o, void* workspace,
+                        size_t ws_bytes, void* stream);
+
+/* Append a chunk to a layer that may already hold tokens: sequence b takes the
+ * chunk's first lens[b] tokens, and the layer is left, byte for byte, as that
+ * many lk_append calls would leave it (a paged cache may hand out its free
+ * pages in another order).  Errors as lk_chunk_attn; LK_ERR_CAPACITY when an
+ * active sequence would exceed capacity_tokens or a paged cache has too few
+ * free pages (nothing is launched then). */
+lk_status lk_append_chunk(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* stream);
+
+/* lk_chunk_attn, then lk_append_chunk of the same chunk: what lk_step does for
+ * one token.  Nothing is launched on an error of either. */
+lk_status lk_extend(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* o, void* workspace,
+                    size_t ws_bytes, void* stream);
+
+/* Which channels of a head turn together: (i, i + rotary_dim / 2), or
+ * (2 i, 2 i + 1). */
+typedef enum lk_rope_layout { LK_ROPE_HALF = 0, LK_ROPE_INTERLEAVED = 1 } lk_rope_layout;
+
+/* How the angle w_i = base^(-2 i / rotary_dim) that pair i turns per position
+ * is stretched for contexts of `factor` times the trained length T:
+ *   NONE    not at all
+ *   LINEAR  w_i / factor
+ *   NTK     base * factor^(d / (d - 2)) in the place of base, d = rotary_dim
+ *   YARN    w_i (1 - r_i) + w_i / factor * r_i with r_i = clamp((i - lo) /
+ *           (hi - lo), 0, 1); lo = floor(at(high_turns)) >= 0 and hi =
+ *           ceil(at(low_turns)) <= d - 1 are the pairs that turn so often in T
+ *           positions, at(n) = d ln(T / (2 pi n)) / (2 ln base)
+ *   BANDS   w_i s_i + w_i / factor * (1 - s_i) with s_i = clamp((T w_i / 2 pi -
+ *           low_turns) / (high_turns - low_turns), 0, 1) */
+typedef enum lk_rope_scaling {
+  LK_ROPE_SCALE_NONE = 0,
+  LK_ROPE_SCALE_LINEAR = 1,
+  LK_ROPE_SCALE_NTK = 2,
+  LK_ROPE_SCALE_YARN = 3,
+  LK_ROPE_SCALE_BANDS = 4
+} lk_rope_scaling;
+
+typedef struct lk_rope_desc {
+  int32_t rotary_dim;         /* channels that turn, the first of each head: a multiple of 16 in [16, 128] */
+  int32_t layout;             /* lk_rope_layout */
+  int32_t scaling;            /* lk_rope_scaling */
+  int32_t trained_positions;  /* T >= 1 (YARN, BANDS) */
+  double base;                /* > 1 */
+  double factor;              /* >= 1; ignored by NONE */
+  double low_turns;           /* 0: 1 */
+  double high_turns;          /* > low_turns; 0: 32 (YARN), 4 (BANDS) */
+  double magnitude;           /* multiplies cosine and sine; 0: 0.1 ln(factor) + 1 (YARN), else 1 */
+} lk_rope_desc;
+
+typedef struct lk_rope_s* lk_rope;    /* host object owned by the library */
+
+/* Rotary positions for heads of 128 channels (host only; touches no GPU). */
+lk_status lk_build_rope(const lk_rope_desc* desc, lk_rope* out);
+void lk_rope_destroy(lk_rope rope);
+
+/* Turn the heads of q and k by their tokens' positions, before they enter
+ * lk_prefill, lk_append, lk_step, lk_chunk_attn and so on:
+ *   q [tokens][num_q_heads][128], k [tokens][num_kv_heads][128]  device bf16;
+ *   positions  device int32 [tokens], any value (negative ones turn back);
+ *   q_out, k_out  as q and k; may be q and k themselves (with the same
+ *   stride), else must not overlap the inputs.
+ * Strides are elements between consecutive tokens: at least heads * 128 and a
+ * multiple of 8, or 0 for dense rows.  q or k may be left out with a head
+ * count of 0.  Each result is rounded once to bf16 from fp32; the angle keeps
+ * its fraction of a turn exactly, however far the position. */
+lk_status lk_rope_apply(lk_rope rope, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const int32_t* positions, int64_t tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                        void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
 /* Host-tracked token count of a layer: the longest sequence's length. */
 lk_status lk_cache_length(lk_cache cache, int32_t layer, int32_t* n);
 
