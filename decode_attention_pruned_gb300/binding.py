@@ -347,7 +347,7 @@ class Cache:
         nbytes = plan.cache_bytes(batch, capacity, middle_tokens, kv_format)
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         self.workspace = torch.empty(plan.workspace_bytes(batch), dtype=torch.uint8, device=dev)
-        self.chunk_workspace = None          # made by the first chunk_attn or extend
+        self._chunk_tokens, self._chunk_workspaces = 0, []      # made by chunk_attn and extend
         h = ctypes.c_void_p()
         s = _stream(stream)
         if kv_format != KV_BF16:
@@ -616,12 +616,19 @@ class Cache:
         if o is None:
             o = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
         _need(o, torch.bfloat16, shape, "o")
-        if self.chunk_workspace is None:
-            # of the size that no chunk exceeds, and kept: a captured call finds it again
-            n = ctypes.c_size_t()
-            _check(_lib.lk_chunk_workspace_bytes(self.plan._h, self.batch, (1 << 31) - 1, ctypes.byref(n)))
-            self.chunk_workspace = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        n = q.shape[1]
+        if n > self._chunk_tokens or not self._chunk_workspaces:
+            # for chunks of up to the next power of two; earlier ones stay, as
+            # captured calls may still use them
+            self._chunk_tokens = 1 << max(n - 1, 0).bit_length()
+            size = ctypes.c_size_t()
+            _check(_lib.lk_chunk_workspace_bytes(self.plan._h, self.batch, self._chunk_tokens, ctypes.byref(size)))
+            self._chunk_workspaces.append(torch.empty(size.value, dtype=torch.uint8, device=self.device))
         return o
+
+    @property
+    def chunk_workspace(self):
+        return self._chunk_workspaces[-1]
 
     def chunk_attn(self, layer, q, k, v, lens=None, ids=None, o=None, stream=None):
         """lk_chunk_attn: q [B, n, Hq, 128], k, v [B, n, Hkv, 128] bf16 (tokens

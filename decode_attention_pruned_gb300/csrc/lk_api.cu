@@ -297,11 +297,54 @@ WsLayout ws_layout(const lk_plan_desc& d, int B) {
   return w;
 }
 
-// Workspace of lk_chunk_attn for chunks of up to n_max tokens.
-size_t chunk_workspace(const lk_plan_desc& d, int n_max) {
-  (void)d;
-  (void)n_max;
-  return 256;
+// How lk_chunk_attn cuts chunks of up to n_max tokens of up to B sequences,
+// and its workspace (one launch group's: groups run one after another):
+// CTA starts, special-token flags, partials, F tile images.  `layer` < 0:
+// what any layer needs.
+struct ChunkLayout {
+  size_t off_special, off_ml, off_part, off_far, total;
+  ChunkWork w;
+};
+ChunkLayout chunk_layout(const lk_plan_s& p, int B, int n_max, int layer, int ctas) {
+  ChunkLayout c = {};
+  const lk_plan_desc& d = p.d;
+  const int G = d.num_q_heads / d.num_kv_heads, H = d.num_kv_heads;
+  const int seqs = std::min(B, kChunkSeqs);
+  ChunkWork& w = c.w;
+  w.tile_tokens = 128 / G;
+  // one query tile a CTA while a chunk fits it (its two softmax groups then
+  // share the keys), else two (they share every key tile)
+  w.dual = n_max > w.tile_tokens;
+  w.item_tokens = w.dual ? 2 * w.tile_tokens : w.tile_tokens;
+  w.items_q = (int)(((int64_t)n_max + w.item_tokens - 1) / w.item_tokens);
+  w.box_tokens = std::min(w.tile_tokens, n_max);
+  w.max_ctas = std::max(1, std::min(ctas, kChunkMaxCtas));
+  w.part_rows = w.dual ? 256 : w.box_tokens * G;
+  int kfar = 0;
+  bool special = false;
+  for (int l = layer < 0 ? 0 : layer; l < (layer < 0 ? d.num_layers : layer + 1); ++l) {
+    special = special || p.layer_special[l];
+    for (int h = 0; h < H; ++h) {
+      const int i = l * H + h;
+      if (p.policy[i] == kFull && p.n_kept[i] < kHeadDim) kfar = std::max(kfar, (int)p.n_kept[i]);
+    }
+  }
+  const int64_t tiles = ((int64_t)n_max + 127) / 128;
+  w.far_tiles = kfar > 0 ? (int)tiles : 0;
+  w.far_bytes = (kfar + kHeadDim) * 2 * 128;
+  w.special_seqs = special ? seqs : 0;
+  w.special_words = special ? (int)(4 * tiles) : 0;
+  size_t off = align_up((kChunkMaxCtas + 2) * sizeof(int2), 256);
+  c.off_special = off;
+  off = align_up(off + (size_t)w.special_seqs * w.special_words * 4, 256);
+  c.off_ml = off;
+  off = align_up(off + (size_t)2 * w.max_ctas * w.part_rows * 8, 256);
+  c.off_part = off;
+  off = align_up(off + (size_t)2 * w.max_ctas * w.part_rows * kHeadDim * 4, 1024);
+  c.off_far = off;
+  off = align_up(off + (size_t)seqs * H * w.far_tiles * w.far_bytes, 256);
+  c.total = off;
+  return c;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -1283,14 +1326,63 @@ cudaError_t chunk_groups(const lk_cache_s* cache, const lk_chunk* c, ChunkArgs& 
   return cudaSuccess;
 }
 
-lk_status chunk_attn_ready(lk_cache cache, const void* o, const void* workspace, size_t ws_bytes, int32_t n_max,
-                           const char* what) {
-  if (n_max == 0) return LK_OK;
+// The rest of an attention's checks, its cut and its tensor maps.
+lk_status chunk_attn_prepare(lk_cache cache, void* o, void* workspace, size_t ws_bytes, const char* what, ChunkArgs& a,
+                             ChunkWork& w, ChunkMaps& maps) {
+  if (a.n_max == 0) return LK_OK;
   if (!o || !workspace) return fail(LK_ERR_ARG, "%s: null o or workspace", what);
   if (!aligned(o, 16)) return fail(LK_ERR_ALIGN, "%s: o must be 16-byte aligned", what);
   if (!aligned(workspace, 256)) return fail(LK_ERR_ALIGN, "%s: workspace must be 256-byte aligned", what);
-  const size_t need = chunk_workspace(cache->plan.d, n_max);
-  if (ws_bytes < need) return fail(LK_ERR_CAPACITY, "%s: workspace has %zu bytes; %zu needed", what, ws_bytes, need);
+  const ChunkLayout need = chunk_layout(cache->plan, cache->B, a.n_max, -1, kChunkMaxCtas);
+  if (ws_bytes < need.total)
+    return fail(LK_ERR_CAPACITY, "%s: workspace has %zu bytes; %zu needed", what, ws_bytes, need.total);
+  const CacheView& cv = cache->cv;
+  const int64_t tokens = (int64_t)cache->B * a.n_max;
+  const ChunkLayout lay = chunk_layout(cache->plan, cache->B, a.n_max, a.layer, cache->num_sms);
+  if (tokens > INT32_MAX || (int64_t)kChunkSeqs * cv.Hkv * std::max(lay.w.items_q, lay.w.far_tiles) > (1 << 30))
+    return fail(LK_ERR_UNSUPPORTED, "%s: %d sequences of %d tokens are too many for one call", what, cache->B, a.n_max);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  w = lay.w;
+  w.start = reinterpret_cast<int2*>(ws);
+  w.special = reinterpret_cast<uint32_t*>(ws + lay.off_special);
+  w.part_ml = reinterpret_cast<float2*>(ws + lay.off_ml);
+  w.part = reinterpret_cast<float*>(ws + lay.off_part);
+  w.far = ws + lay.off_far;
+  a.o = static_cast<uint16_t*>(o);
+  a.wait_limit_ns = cache->wait_limit_ns;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return fail(LK_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  auto map = [&](CUtensorMap* m, const uint16_t* p, cuuint32_t rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t*>(p), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  const cuuint64_t qdims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)cv.Hq, (cuuint64_t)tokens};
+  const cuuint64_t qstrides[2] = {kHeadDim * 2, (cuuint64_t)a.q_stride * 2};
+  const cuuint32_t qbox[3] = {64, (cuuint32_t)cv.G, (cuuint32_t)w.box_tokens};
+  const cuuint64_t kvdims[4] = {64, (cuuint64_t)tokens, 2, (cuuint64_t)cv.Hkv};
+  const cuuint32_t kvbox[4] = {64, 128, 2, 1};
+  CUresult r = map(&maps.q, a.q, 3, qdims, qstrides, qbox);
+  for (int i = 0; i < 2 && r == CUDA_SUCCESS; ++i) {
+    const cuuint64_t strides[3] = {(cuuint64_t)(i ? a.v_stride : a.k_stride) * 2, 128, kHeadDim * 2};
+    r = map(i ? &maps.v : &maps.k, i ? a.v : a.k, 4, kvdims, strides, kvbox);
+  }
+  if (r != CUDA_SUCCESS) return fail(LK_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (CUresult %d)", what, (int)r);
+  for (int pl = 0; pl < kNumPools; ++pl) maps.pool[pl] = cache->maps.m[kMapFlat + pl];
+  return LK_OK;
+}
+
+lk_status chunk_attn_run(lk_cache cache, const lk_chunk* c, ChunkArgs& a, ChunkWork& w, const ChunkMaps& maps,
+                         const char* what, cudaStream_t s) {
+  const int special = w.special_seqs;
+  cudaError_t err = chunk_groups(cache, c, a, [&](const ChunkArgs& g) {
+    if (kv_quantized(cache->lay.kv_format)) return launch_chunk_simple(g, s);
+    w.special_seqs = special > 0 ? g.nb : 0;
+    return launch_chunk_attn(maps, g, w, s);
+  });
+  if (err != cudaSuccess) return cuda_fail(err, what);
   return LK_OK;
 }
 
@@ -1319,48 +1411,46 @@ lk_status lk_chunk_workspace_bytes(lk_plan plan, int32_t batch, int32_t n_max, s
   if (batch < 1 || (int64_t)batch * plan->d.num_kv_heads > (1 << 20))
     return fail(LK_ERR_ARG, "batch %d out of range", batch);
   if (n_max < 0) return fail(LK_ERR_ARG, "lk_chunk_workspace_bytes: n_max = %d < 0", n_max);
-  *bytes = chunk_workspace(plan->d, n_max);
+  *bytes = chunk_layout(*plan, batch, n_max, -1, kChunkMaxCtas).total;
   return LK_OK;
 }
 
 lk_status lk_chunk_attn(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* o, void* workspace,
                         size_t ws_bytes, void* stream) {
   ChunkArgs a;
+  ChunkWork w;
+  ChunkMaps maps;
   int64_t need[kNumPools];
   lk_status st = chunk_prepare(cache, layer, chunk, false, "lk_chunk_attn", a, need);
-  if (st == LK_OK) st = chunk_attn_ready(cache, o, workspace, ws_bytes, chunk->n_max, "lk_chunk_attn");
-  if (st != LK_OK) return st;
-  a.o = static_cast<uint16_t*>(o);
-  cudaError_t err = chunk_groups(cache, chunk, a, [&](const ChunkArgs& g) {
-    return launch_chunk_attn(g, cache->num_sms, static_cast<cudaStream_t>(stream));
-  });
-  if (err != cudaSuccess) return cuda_fail(err, "lk_chunk_attn launch");
-  return LK_OK;
+  if (st == LK_OK) st = chunk_attn_prepare(cache, o, workspace, ws_bytes, "lk_chunk_attn", a, w, maps);
+  if (st != LK_OK || a.n_max == 0) return st;
+  return chunk_attn_run(cache, chunk, a, w, maps, "lk_chunk_attn", static_cast<cudaStream_t>(stream));
 }
 
 lk_status lk_append_chunk(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* stream) {
   ChunkArgs a;
   int64_t need[kNumPools];
   lk_status st = chunk_prepare(cache, layer, chunk, true, "lk_append_chunk", a, need);
-  if (st != LK_OK) return st;
+  if (st != LK_OK || a.n_max == 0) return st;
   return chunk_append_run(cache, chunk, a, need, "lk_append_chunk", static_cast<cudaStream_t>(stream));
 }
 
 lk_status lk_extend(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* o, void* workspace, size_t ws_bytes,
                     void* stream) {
-  ChunkArgs a, w;
+  ChunkArgs a, write;
+  ChunkWork w;
+  ChunkMaps maps;
   int64_t need[kNumPools];
   lk_status st = chunk_prepare(cache, layer, chunk, false, "lk_extend", a, need);
-  if (st == LK_OK) st = chunk_attn_ready(cache, o, workspace, ws_bytes, chunk->n_max, "lk_extend");
-  if (st == LK_OK) st = chunk_prepare(cache, layer, chunk, true, "lk_extend", w, need);
-  if (st != LK_OK) return st;
+  if (st == LK_OK) st = chunk_attn_prepare(cache, o, workspace, ws_bytes, "lk_extend", a, w, maps);
+  if (st == LK_OK) st = chunk_prepare(cache, layer, chunk, true, "lk_extend", write, need);
+  if (st != LK_OK || a.n_max == 0) return st;
   for (int pl = 0; pl < kNumPools; ++pl)
     if (need[pl] > cache->host_free[pl]) return cache->take_pages(need, "lk_extend");   // says which, takes none
-  a.o = static_cast<uint16_t*>(o);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t err = chunk_groups(cache, chunk, a, [&](const ChunkArgs& g) { return launch_chunk_attn(g, cache->num_sms, s); });
-  if (err != cudaSuccess) return cuda_fail(err, "lk_extend launch");
-  return chunk_append_run(cache, chunk, w, need, "lk_extend", s);
+  st = chunk_attn_run(cache, chunk, a, w, maps, "lk_extend", s);
+  if (st != LK_OK) return st;
+  return chunk_append_run(cache, chunk, write, need, "lk_extend", s);
 }
 
 // ---------------------------------------------------------------------------

@@ -101,7 +101,38 @@ struct ChunkArgs {
   int64_t q_stride, k_stride, v_stride;
   const int32_t* ids;       // [B][n_max] or null
   uint16_t* o;              // bf16 [B][n_max][Hq][128]
+  uint64_t wait_limit_ns;   // bound of every mbarrier wait
   int32_t lens[kChunkSeqs]; // new tokens of sequence b0 + i
+};
+
+// Tensor maps of chunk attention: the chunk's tensors, and the flat maps of
+// the cache's pools.
+struct ChunkMaps {
+  CUtensorMap q;            // {128, Hq, tokens}: 64 channels, G heads, box_tokens tokens
+  CUtensorMap k, v;         // {64, tokens, 2, Hkv}: both halves of 128 tokens of a head
+  CUtensorMap pool[kNumPools];
+};
+
+// How a chunk attention is cut, and its workspace.
+constexpr int kChunkMaxCtas = 160;
+struct ChunkWork {
+  int32_t dual;             // two query tiles per CTA, else one
+  int32_t tile_tokens;      // queries per tile of 128 rows: 128 / G
+  int32_t item_tokens;      // queries per item
+  int32_t items_q;          // items per (sequence, head)
+  int32_t box_tokens;       // queries per load of q
+  int32_t max_ctas;
+  int32_t part_rows;        // rows of a partial
+  int32_t far_tiles;        // F tile images per (sequence, head); 0: no head has kept channels and pruned ones
+  int32_t far_bytes;        // of one image
+  int32_t special_seqs;     // sequences whose special tokens are flagged (0: no SPECIAL head)
+  int32_t special_words;    // 32-token words per sequence
+  int32_t pad;
+  int2* start;              // [max_ctas + 2]: (item, tile) where each CTA starts, the end; then (CTAs, -)
+  float2* part_ml;          // [2 max_ctas][part_rows]
+  float* part;              // [2 max_ctas][part_rows][128]
+  uint32_t* special;
+  uint8_t* far;
 };
 
 enum RopeLayout : int32_t { kRopeHalf = 0, kRopeInterleaved = 1 };
@@ -144,7 +175,8 @@ cudaError_t launch_build_masks(const float* alpha, const uint8_t* eligible, int 
                                int exact, uint8_t* masks, cudaStream_t stream);
 
 cudaError_t launch_chunk_append(const ChunkArgs& args, bool has_middle, int num_sms, cudaStream_t stream);
-cudaError_t launch_chunk_attn(const ChunkArgs& args, int num_sms, cudaStream_t stream);
+cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& work, cudaStream_t stream);
+cudaError_t launch_chunk_simple(const ChunkArgs& args, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs& args, cudaStream_t stream);
 
 }  // namespace lk
