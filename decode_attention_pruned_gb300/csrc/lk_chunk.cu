@@ -33,6 +33,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "lk_append.cuh"
 #include "lk_device.cuh"
 #include "lk_internal.h"
@@ -83,14 +85,16 @@ __device__ __forceinline__ bool item_info(const ChunkArgs& a, const ChunkWork& w
   it.h = sh % cv.Hkv;
   it.seq = sh / cv.Hkv;
   it.b = a.b0 + it.seq;
-  it.n = chunk_len(a, it.seq);
+  // (all loads at once: none waits for another)
+  const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + it.h];
+  const int active = __ldcg(&cv.active[it.b]), cnt = __ldcg(&cv.cnt[a.layer * cv.B + it.b]);
+  const int N = it.N = __ldcg(&cv.len[a.layer * cv.B + it.b]);
+  it.policy = hd.policy;
+  it.k = hd.n_kept;
+  it.n = active != 0 ? a.lens[it.seq] : 0;
   it.i0 = qi * w.item_tokens;
   it.ntok = min(w.item_tokens, it.n - it.i0);
   if (it.ntok <= 0) return false;
-  const int N = it.N = __ldcg(&cv.len[a.layer * cv.B + it.b]);
-  const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + it.h];
-  it.policy = hd.policy;
-  it.k = hd.n_kept;
   it.win = kFar;
   it.sinks = 0;
   it.mid = it.rows_f = it.far0 = 0;
@@ -110,7 +114,7 @@ __device__ __forceinline__ bool item_info(const ChunkArgs& a, const ChunkWork& w
     na = min(N, cv.W_loc);
     it.win = cv.W_loc;
   } else {
-    na = __ldcg(&cv.cnt[a.layer * cv.B + it.b]);
+    na = cnt;
   }
   na = min(na, hd.cap_a);
   // past the window's length no held window token is near any more
@@ -149,6 +153,10 @@ __device__ __forceinline__ Tile tile_at(const Item& it, int j) {
   t.rows = min(t.rows, kTile);
   return t;
 }
+
+// Whether values behind the tile's last key must be cleared (F images end in
+// zeros).
+__device__ __forceinline__ bool needs_fix(const Tile& t) { return t.type != kTileF && (t.rows & 15) != 0; }
 
 // Image of one F tile: kept channels as the middle's tiles lie in shared
 // memory, then V.
@@ -260,34 +268,51 @@ __device__ void plan_far(const ChunkArgs& a, const ChunkWork& w, int seq, int h,
   uint8_t* image = far_tile(a, w, seq, h, tile);
   const int64_t abase = hd.row_a + (int64_t)b * hd.cap_a;
   const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim;
-  const int kg = k / 8, groups = kg + kHeadDim / 8;
-  for (int x = threadIdx.x; x < rows16 * groups; x += blockDim.x) {
-    const int r = x / groups, c = x - r * groups;
+  // every load of a thread is issued before its first store: 8 groups of V,
+  // then up to 6 of K
+  static_assert(kPlanThreads == 256, "rows of V per pass");
+  const int tid = threadIdx.x;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  auto src = [&](int r, bool isv) {
     const int t = first + tile * kTile + r;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    const bool held = t < N;
     const int64_t ring = abase + cv.S + (t - cv.S) % cv.W;
     const int64_t at = (int64_t)b * a.n_max + (t - N);
-    if (c >= kg) {
-      const uint16_t* src = held ? cv.pool[kPoolV] + ring * kHeadDim : a.v + at * a.v_stride + h * kHeadDim;
-      if (r < rows) v = *reinterpret_cast<const uint4*>(src + (c - kg) * 8);
-      *reinterpret_cast<uint4*>(image + kTile * 2 * k + kept_byte(kHeadDim, r, c - kg)) = v;
-    } else {
-      const uint16_t* src = held ? cv.pool[kPoolK128] + ring * kHeadDim : a.k + at * a.k_stride + h * kHeadDim;
-      if (r < rows) {
-        const int16_t* kc = kept + c * 8;
-        v.x = src[kc[0]] | (uint32_t)src[kc[1]] << 16;
-        v.y = src[kc[2]] | (uint32_t)src[kc[3]] << 16;
-        v.z = src[kc[4]] | (uint32_t)src[kc[5]] << 16;
-        v.w = src[kc[6]] | (uint32_t)src[kc[7]] << 16;
-      }
-      *reinterpret_cast<uint4*>(image + kept_byte(k, r, c)) = v;
-    }
+    return t < N ? (isv ? cv.pool[kPoolV] : cv.pool[kPoolK128]) + ring * kHeadDim
+                 : (isv ? a.v + at * a.v_stride : a.k + at * a.k_stride) + h * kHeadDim;
+  };
+  uint4 v[8], kv[6];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int r = 16 * x + tid / 16;
+    v[x] = r < rows ? *reinterpret_cast<const uint4*>(src(r, true) + tid % 16 * 8) : zero;
+  }
+  const int kg = k / 8;
+#pragma unroll
+  for (int x = 0; x < 6; ++x) {
+    const int y = x * kPlanThreads + tid, r = y / kg, c = y - r * kg;
+    kv[x] = zero;
+    if (r >= rows) continue;
+    const uint16_t* p = src(r, false);
+    const uint4 kc = *reinterpret_cast<const uint4*>(kept + c * 8);
+    auto two = [&](uint32_t ch) { return p[ch & 0xffffu] | (uint32_t)p[ch >> 16] << 16; };
+    kv[x] = make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
+  }
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int r = 16 * x + tid / 16;
+    if (r < rows16) *reinterpret_cast<uint4*>(image + kTile * 2 * k + kept_byte(kHeadDim, r, tid % 16)) = v[x];
+  }
+#pragma unroll
+  for (int x = 0; x < 6; ++x) {
+    const int y = x * kPlanThreads + tid, r = y / kg, c = y - r * kg;
+    if (r < rows16) *reinterpret_cast<uint4*>(image + kept_byte(k, r, c)) = kv[x];
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a,
                                                                   const ChunkWork w) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   int x = blockIdx.x;
   if (x == 0) {
     plan_line(a, w);
@@ -303,26 +328,35 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 
 // ------------------------------------------------------------- attention
 constexpr int kThreads = 384;              // warps: TMA, MMA, two that gather q, two softmax groups of four
-constexpr int kKeptBytes = kTile * 96 * 2;
 constexpr int kWideBytes = kTile * kHeadDim * 2;
 
 // kDual: a CTA works on two query tiles, which share every key tile, one per
 // softmax group.  Else on one, and the groups take alternate key tiles.
+//
+// Shared memory: q at full width, q on the kept channels (as wide as the
+// layer's widest such head), and a byte ring that the key and value tiles go
+// through in order, each taking what it needs (a key tile on 32 channels 8 KB,
+// full-width ones and values 32 KB), so that narrow heads have the more tiles
+// in flight.
+constexpr int kSlots = 16;                 // tiles in flight at most
 template <bool kDual>
 struct Smem {
   static constexpr int kQTiles = kDual ? 2 : 1;
-  static constexpr int kSlots = kDual ? 3 : 5;           // ring of K and V tiles
-  static constexpr int kQ = 0;
+  static constexpr int kML = 0;                          // second group's (m, l)
+  static constexpr int kFull = kML + kTile * 8, kEmpty = kFull + 8 * kSlots, kQFull = kEmpty + 8 * kSlots,
+                       kQEmpty = kQFull + 8, kQKFull = kQEmpty + 8, kSFull = kQKFull + 8, kPFull = kSFull + 16,
+                       kOFull = kPFull + 16, kMerge = kOFull + 16, kMerged = kMerge + 8, kAsk = kMerged + 8,
+                       kFixed = kAsk + 16, kDrain = kFixed + 8, kTmem = kDrain + 8, kOffs = kTmem + 16,
+                       kTask = (kOffs + 4 * kSlots + 15) / 16 * 16;
+  static constexpr int kQ = 2048;
+  static_assert(kTask + 32 <= kQ, "barriers, offsets and tasks");
   static constexpr int kQKept = kQ + kQTiles * kWideBytes;
-  static constexpr int kRing = kQKept + kQTiles * kKeptBytes;
-  static constexpr int kML = kRing + kSlots * kWideBytes; // second group's (m, l)
-  static constexpr int kBar = kML + kTile * 8;
-  static constexpr int kFull = kBar, kEmpty = kFull + 8 * kSlots, kQFull = kEmpty + 8 * kSlots, kQEmpty = kQFull + 8,
-                       kQKFull = kQEmpty + 8, kSFull = kQKFull + 8, kPFull = kSFull + 16, kOFull = kPFull + 16,
-                       kMerge = kOFull + 16, kMerged = kMerge + 8, kDrain = kMerged + 8, kTmem = kDrain + 8;
-  static constexpr int kBytes = kTmem + 16 + 1024;
+  static constexpr int kBytes = 227 * 1024;
+  static constexpr int kEnd = kBytes - 1024;             // after aligning the base
 };
-static_assert(Smem<true>::kBytes <= 227 * 1024 && Smem<false>::kBytes <= 227 * 1024, "shared memory per block");
+
+constexpr uint64_t kDrainNs = 1000000000ull;      // bound of the waits for copies and MMAs still in flight
+constexpr uint64_t kIdleNs = 60000000000ull;      // bound of the aides' waits for a task
 
 struct Wait {
   uint64_t limit;
@@ -349,6 +383,31 @@ struct Wait {
     return __all_sync(0xffffffffu, (*this)(bar, parity));
   }
 };
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations in one instruction; a pair in one 64-bit register.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -413,18 +472,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const CacheView& cv = a.cv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
-  const int P = w.start[w.max_ctas + 1].x;
-  if (cta >= P) return;
-  const int2 first = w.start[cta], last = w.start[cta + 1];
   volatile int* gone = reinterpret_cast<volatile int*>(sm + L::kTmem + 8);
   if (tid == 0) {
-    for (int i = 0; i < L::kSlots; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(base + L::kFull + 8 * i, 1);
       mbar_init(base + L::kEmpty + 8 * i, 1);
     }
     mbar_init(base + L::kQFull, 1);
     mbar_init(base + L::kQEmpty, 1);
-    mbar_init(base + L::kQKFull, 2);
+    mbar_init(base + L::kQKFull, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(base + L::kSFull + 8 * s, 1);
       mbar_init(base + L::kPFull + 8 * s, 4);
@@ -432,19 +488,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(base + L::kMerge, 4);
     mbar_init(base + L::kMerged, 4);
+    mbar_init(base + L::kAsk, 1);
+    mbar_init(base + L::kAsk + 8, 1);
+    mbar_init(base + L::kFixed, 1);
     mbar_init(base + L::kDrain, 1);
     fence_barrier_init();
     *gone = 0;
   }
+  const uint32_t ring = L::kQKept + L::kQTiles * w.kept_bytes;       // offsets from base
   // rows of the query tiles that no load writes stay zero
-  for (int x = tid; x < L::kRing / 16; x += kThreads)
+  for (int x = L::kQ / 16 + tid; x < (int)ring / 16; x += kThreads)
     reinterpret_cast<uint4*>(sm)[x] = make_uint4(0u, 0u, 0u, 0u);
   fence_async_smem();
+  if (warp == 0 && lane < 3 + kNumPools) tma_prefetch_map(&maps.q + lane);
   if (warp == 1) tmem_alloc_all(base + L::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::kTmem);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int P = __ldcg(&w.start[w.max_ctas + 1].x);
+  const bool idle = cta >= P;
+  const int2 first = idle ? make_int2(0, 0) : __ldcg(&w.start[cta]);
+  const int2 last = idle ? make_int2(0, 0) : __ldcg(&w.start[cta + 1]);
   // columns: scores of the two groups (their P takes the place of the scores), outputs of the two
   const uint32_t tm_s = tmem, tm_o = tmem + 256;
   const Wait wait{a.wait_limit_ns, gone, cv.hdr};
@@ -480,15 +547,56 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------- loads
-    uint32_t put = 0;
     if (lane == 0) {
-      const uint64_t keep = l2_policy_evict_first();
+      // The ring is a FIFO of runs of bytes: the oldest tile in flight starts
+      // at `tail`, the next goes to `head`, or to the ring's start when it
+      // does not fit before the end.
+      const uint32_t size = L::kEnd - ring;
+      uint32_t* offs = reinterpret_cast<uint32_t*>(sm + L::kOffs);
+      uint32_t put = 0, freed = 0, head = 0, tail = 0;
+      bool wrapped = false;
+      // Keys that one query tile reads are read once; those that several read
+      // should stay in L2.
+      const uint64_t once = l2_policy_evict_first(), keep = w.items_q > 1 ? l2_policy_evict_normal() : once;
+      auto reserve = [&](uint32_t bytes, uint32_t& at) -> bool {
+        while (true) {
+          if (put == freed) {
+            head = tail = 0;
+            wrapped = false;
+          }
+          if (put - freed < kSlots) {
+            if (!wrapped && head + bytes <= size) break;
+            if (!wrapped && bytes <= tail) {
+              head = 0;
+              wrapped = true;
+              break;
+            }
+            if (wrapped && head + bytes <= tail) break;
+          }
+          if (!wait(base + L::kEmpty + 8 * (freed % kSlots), (freed / kSlots) & 1)) return false;
+          if (++freed != put) {
+            const uint32_t t = offs[freed % kSlots];
+            if (t < tail) wrapped = false;
+            tail = t;
+          }
+        }
+        at = head;
+        head += bytes;
+        return true;
+      };
       Segment s;
       begin(s);
       bool ok = true;
       while (ok && advance(s)) {
         const Item& it = s.it;
         const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + it.h];
+        const int kb = hd.pool_kb;
+        const int64_t krow_b = hd.krow_b, vrow_b = hd.vrow_b;
+        const int64_t abase = hd.row_a + (int64_t)it.b * hd.cap_a, bbase = (int64_t)it.b * hd.cap_b;
+        const int32_t* pages = cv.max_pages > 0 ? page_row(cv, a.layer, it.b, it.h) : nullptr;
+        // page ids are read a tile or two ahead of the loads that need them
+        const int m0 = it.nA + it.nC;
+        int32_t page = 0, next_page = 0;
         if (s.idx > 0) ok = wait(base + L::kQEmpty, (s.idx - 1) & 1);
         if (!ok) break;
         const int nq = kDual && it.ntok > tq ? 2 : 1;
@@ -496,14 +604,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < nq; ++x)
           for (int half = 0; half < 2; ++half)
             tma_load_3d(base + L::kQ + x * kWideBytes + half * (kWideBytes / 2), &maps.q, half * 64, it.h * G,
-                        it.b * a.n_max + it.i0 + x * tq, base + L::kQFull, keep);
-        const int64_t abase = hd.row_a + (int64_t)it.b * hd.cap_a;
-        auto load = [&](int j, bool isv) -> bool {
-          const uint32_t slot = put % L::kSlots, round = put / L::kSlots;
-          if (round > 0 && !wait(base + L::kEmpty + 8 * slot, (round - 1) & 1)) return false;
-          ++put;
-          const uint32_t dst = base + L::kRing + slot * kWideBytes, bar = base + L::kFull + 8 * slot;
+                        it.b * a.n_max + it.i0 + x * tq, base + L::kQFull, once);
+        auto load = [&](int j, bool isv, int32_t pg) -> bool {
           const Tile t = tile_at(it, j);
+          const bool wide = isv || t.type <= kTileC || it.k == kHeadDim;
+          uint32_t at;
+          if (!reserve(wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * 2 * it.k), at)) return false;
+          const uint32_t slot = put % kSlots;
+          offs[slot] = at;
+          ++put;
+          const uint32_t dst = base + ring + at, bar = base + L::kFull + 8 * slot;
           if (t.type == kTileC) {
             mbar_arrive_expect_tx(bar, kWideBytes);
             tma_load_4d(dst, isv ? &maps.v : &maps.k, 0, it.b * a.n_max + t.r0, 0, it.h, bar, keep);
@@ -511,17 +621,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(bar, kWideBytes);
             tma_load_3d(dst, &maps.pool[isv ? kPoolV : kPoolK128], 0, (int)(abase + t.r0), 0, bar, keep);
           } else if (t.type == kTileM) {
-            const int64_t page = cv.max_pages > 0
-                                     ? (int64_t)max(0, __ldcg(&page_row(cv, a.layer, it.b, it.h)[t.r0 / kPageRows])) * kPageRows
-                                     : (int64_t)it.b * hd.cap_b + t.r0;
+            const int64_t r = pages != nullptr ? (int64_t)max(0, pg) * kPageRows : bbase + t.r0;
             if (isv) {
               mbar_arrive_expect_tx(bar, kWideBytes);
-              tma_load_3d(dst, &maps.pool[kPoolV], 0, (int)(hd.vrow_b + page), 0, bar, keep);
+              tma_load_3d(dst, &maps.pool[kPoolV], 0, (int)(vrow_b + r), 0, bar, keep);
             } else {
               mbar_arrive_expect_tx(bar, (uint32_t)(kTile * 2 * it.k));
-              const CUtensorMap* m = &maps.pool[hd.pool_kb];
-              if (it.k == 32 || it.k == 64) tma_load_2d(dst, m, 0, (int)(hd.krow_b + page), bar, keep);
-              else tma_load_3d(dst, m, 0, (int)(hd.krow_b + page), 0, bar, keep);
+              if (it.k == 32 || it.k == 64) tma_load_2d(dst, &maps.pool[kb], 0, (int)(krow_b + r), bar, keep);
+              else tma_load_3d(dst, &maps.pool[kb], 0, (int)(krow_b + r), 0, bar, keep);
             }
           } else {
             // whole 16-row groups of each run of the image
@@ -537,182 +644,235 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
+        // page id of the middle tile that key tile j is, if any
+        auto page_at = [&](int j) -> int32_t {
+          return pages != nullptr && j >= m0 && j < m0 + it.nM ? __ldcg(pages + (j - m0)) : 0;
+        };
         for (int j = s.t0; ok && j < s.t1; ++j) {
+          const int32_t after = page_at(j + (kDual ? 1 : 2));
           if (kDual) {
-            ok = load(j, false) && load(j, true);
+            if (j == s.t0) page = page_at(j);
+            ok = load(j, false, page) && load(j, true, page);
+            page = after;
           } else {
-            if (j == s.t0) ok = load(j, false);
-            if (ok && j + 1 < s.t1) ok = load(j + 1, false);
-            if (ok) ok = load(j, true);
+            if (j == s.t0) {
+              page = page_at(j);
+              next_page = page_at(j + 1);
+              ok = load(j, false, page);
+            }
+            if (ok && j + 1 < s.t1) ok = load(j + 1, false, next_page);
+            if (ok) ok = load(j, true, page);
+            page = next_page;
+            next_page = after;
           }
         }
       }
       // copies still in flight must land before the block ends
-      const Wait drain{1000000000ull, gone, cv.hdr};
       if (!ok) {
-        for (uint32_t x = put > L::kSlots ? put - L::kSlots : 0; x < put; ++x)
-          mbar_wait_bounded(base + L::kFull + 8 * (x % L::kSlots), (x / L::kSlots) & 1, drain.limit);
-        if (s.idx >= 0) mbar_wait_bounded(base + L::kQFull, s.idx & 1, drain.limit);
+        for (uint32_t x = freed; x < put; ++x)
+          mbar_wait_bounded(base + L::kFull + 8 * (x % kSlots), (x / kSlots) & 1, kDrainNs);
+        if (s.idx >= 0) mbar_wait_bounded(base + L::kQFull, s.idx & 1, kDrainNs);
       }
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMAs
-    uint32_t got = 0, gathered = 0, nq[2] = {0, 0}, nv[2] = {0, 0};
-    constexpr uint32_t kDescS = mma_desc(128, kTile, false), kDescO = mma_desc(128, kHeadDim, true);
-    Segment s;
-    begin(s);
-    bool ok = true;
-    while (ok && advance(s)) {
-      const Item& it = s.it;
-      const int streams = kDual && it.ntok <= tq ? 1 : 2;
-      bool have_kept = false;
-      ok = wait.warp(base + L::kQFull, s.idx & 1);
-      // scores of key tile j: both query tiles, or the one for group j mod 2
-      auto scores = [&](int j, int st, uint32_t kslot) {
-        const Tile t = tile_at(it, j);
-        const bool wide = t.type == kTileA || t.type == kTileC || it.k == kHeadDim;
-        const uint32_t q = base + (wide ? L::kQ + (kDual ? st : 0) * kWideBytes
-                                        : L::kQKept + (kDual ? st : 0) * kKeptBytes);
-        const uint32_t kt = base + L::kRing + kslot * kWideBytes;
-        const int width = wide ? kHeadDim : it.k;
-        if (lane == 0) {
-          if ((width & 63) == 0) {
-            for (int x = 0; x < width / 16; ++x) {
-              const uint32_t at = (uint32_t)((x >> 2) * (kTile * 128) + (x & 3) * 32);
-              mma_ss(tm_s + st * 128, smem_desc(q + at, 16, 1024, kSwizzle128),
-                     smem_desc(kt + at, 16, 1024, kSwizzle128), kDescS, x > 0);
+    // One thread issues them all; what it does per tile is kept short, as the
+    // tensor core waits for it.
+    if (elect_one()) {
+      constexpr uint32_t kDescS = mma_desc(128, kTile, false), kDescO = mma_desc(128, kHeadDim, true);
+      const uint64_t wide_desc = smem_desc(0, 16, 1024, kSwizzle128), thin_desc = smem_desc(0, 16, 512, kSwizzle64);
+      const uint64_t v_desc = smem_desc(0, kWideBytes / 2, 1024, kSwizzle128);
+      uint32_t got = 0, asked = 0, gathered = 0, fixed = 0, nv[2] = {0, 0};
+      // Hands a task to warp 2 (gather) or 3 (clear); the last one is done by then.
+      auto ask = [&](int who, int4 task) {
+        *reinterpret_cast<volatile int*>(sm + L::kTask + 16 * who) = task.x;
+        *reinterpret_cast<volatile int*>(sm + L::kTask + 16 * who + 4) = task.y;
+        *reinterpret_cast<volatile int*>(sm + L::kTask + 16 * who + 8) = task.z;
+        *reinterpret_cast<volatile int*>(sm + L::kTask + 16 * who + 12) = task.w;
+        mbar_arrive(base + L::kAsk + 8 * who);
+      };
+      Segment s;
+      begin(s);
+      bool ok = true;
+      while (ok && advance(s)) {
+        const Item& it = s.it;
+        const int streams = kDual && it.ntok <= tq ? 1 : 2;
+        const int m0 = it.nA + it.nC, m1 = m0 + it.mid / kTile;
+        const bool gather = gathers(s);
+        bool have_kept = !gather;
+        // 16-byte units of the two operands
+        const uint32_t q_wide = (base + L::kQ) >> 4, q_kept = (base + L::kQKept) >> 4;
+        // scores of a key tile: both query tiles', or the one's for group `st`
+        auto scores = [&](int j, int st, uint32_t kt) {
+          const uint32_t d = tm_s + st * 128, x = kDual ? st : 0;
+          const int width = j < m0 ? kHeadDim : it.k;
+          auto run = [&](auto steps, uint64_t desc, uint32_t q) {
+            constexpr int kSteps = decltype(steps)::value;
+            constexpr bool kThin = kSteps == 2 || kSteps == 6;
+            const uint64_t qd = desc | q, kd = desc | (kt >> 4);
+            mma_ss<false>(d, qd, kd, kDescS);
+#pragma unroll
+            for (int y = 1; y < kSteps; ++y) {
+              const uint32_t at = kThin ? (y >> 1) * (kTile * 4) + (y & 1) * 2 : (y >> 2) * (kTile * 8) + (y & 3) * 2;
+              mma_ss<true>(d, qd + at, kd + at, kDescS);
             }
+          };
+          if (width == kHeadDim) {
+            run(std::integral_constant<int, 8>(), wide_desc, q_wide + x * (kWideBytes >> 4));
           } else {
-            for (int x = 0; x < width / 16; ++x) {
-              const uint32_t at = (uint32_t)((x >> 1) * (kTile * 64) + (x & 1) * 32);
-              mma_ss(tm_s + st * 128, smem_desc(q + at, 16, 512, kSwizzle64),
-                     smem_desc(kt + at, 16, 512, kSwizzle64), kDescS, x > 0);
-            }
+            const uint32_t q = q_kept + x * ((uint32_t)w.kept_bytes >> 4);
+            if (width == 32) run(std::integral_constant<int, 2>(), thin_desc, q);
+            else if (width == 64) run(std::integral_constant<int, 4>(), wide_desc, q);
+            else run(std::integral_constant<int, 6>(), thin_desc, q);
           }
           mma_commit(base + L::kSFull + 8 * st);
-        }
-        ++nq[st];
-      };
-      // waits for the next slot of the ring (and for the gathered q before the
-      // first tile that uses it)
-      auto take = [&](int j, bool isv, uint32_t& slot) -> bool {
-        slot = got % L::kSlots;
-        if (!wait.warp(base + L::kFull + 8 * slot, (got / L::kSlots) & 1)) return false;
-        ++got;
-        const Tile t = tile_at(it, j);
-        if (!isv) {
-          if (t.type >= kTileM && !have_kept && gathers(s)) {
-            if (!wait.warp(base + L::kQKFull, gathered & 1)) return false;
+        };
+        // next tile of the ring: its slot and address
+        auto take = [&](uint32_t& slot, uint32_t& addr) -> bool {
+          slot = got % kSlots;
+          if (!wait(base + L::kFull + 8 * slot, (got / kSlots) & 1)) return false;
+          ++got;
+          addr = base + ring + *reinterpret_cast<volatile uint32_t*>(sm + L::kOffs + 4 * slot);
+          return true;
+        };
+        auto take_k = [&](int j, uint32_t& slot, uint32_t& addr) -> bool {
+          if (!have_kept && j >= m0) {
+            if (!wait(base + L::kQKFull, gathered & 1)) return false;
             have_kept = true;
+            ++gathered;
           }
-        } else if (t.type != kTileF && (t.rows & 15) != 0) {
-          // rows past the last key hold anything: P is 0 there, but 0 * NaN is not
-          uint8_t* v = sm + L::kRing + slot * kWideBytes;
-          const int lo = t.rows, hi = (t.rows + 15) & ~15;
-          for (int x = lane; x < (hi - lo) * 16; x += 32)
-            *reinterpret_cast<uint4*>(v + kept_byte(kHeadDim, lo + x / 16, x % 16)) = make_uint4(0u, 0u, 0u, 0u);
-          fence_async_smem();
-          __syncwarp();
+          return take(slot, addr);
+        };
+        // steps: 16-key groups of the tile that hold keys
+        auto take_v = [&](int j, uint32_t& slot, uint32_t& addr, int& steps) -> bool {
+          if (!take(slot, addr)) return false;
+          steps = kTile / 16;
+          if (j >= m0 && j < m1) return true;
+          const Tile t = tile_at(it, j);
+          steps = (t.rows + 15) / 16;
+          if (!needs_fix(t)) return true;
+          ask(1, make_int4((int)(addr - base), t.rows, steps * 16, 0));
+          return wait(base + L::kFixed, fixed++ & 1);
+        };
+        auto values = [&](int st, uint32_t vt, int steps, bool accumulate) {
+          const uint32_t d = tm_o + st * 128, p = tm_s + st * 128;
+          const uint64_t vd = v_desc | (vt >> 4);
+          if (steps == kTile / 16) {
+#pragma unroll
+            for (int y = 0; y < kTile / 16; ++y) mma_ts(d, p + y * 8, vd + y * 128, kDescO, accumulate || y > 0);
+          } else {
+            for (int y = 0; y < steps; ++y) mma_ts(d, p + y * 8, vd + y * 128, kDescO, accumulate || y > 0);
+          }
+          ++nv[st];
+        };
+        auto release = [&](uint32_t slot) { mma_commit(base + L::kEmpty + 8 * slot); };
+        ok = wait(base + L::kQFull, s.idx & 1);
+        if (ok && gather) {
+          const int rows = min(tq, it.ntok) * G, rows2 = kDual && it.ntok > tq ? (it.ntok - tq) * G : 0;
+          ask(0, make_int4(it.h, it.k, rows, rows2));
+          ++asked;
         }
-        tc_fence_after();
-        return true;
-      };
-      auto values = [&](int j, int st, uint32_t vslot, bool accumulate) {
-        const Tile t = tile_at(it, j);
-        const uint32_t vt = base + L::kRing + vslot * kWideBytes;
-        if (lane == 0) {
-          for (int x = 0; x < (t.rows + 15) / 16; ++x)
-            mma_ts(tm_o + st * 128, tm_s + st * 128 + x * 8,
-                   smem_desc(vt + x * 2048, kWideBytes / 2, 1024, kSwizzle128), kDescO, accumulate || x > 0);
-          mma_commit(base + L::kOFull + 8 * st);
-        }
-        ++nv[st];
-      };
-      auto release = [&](uint32_t slot) {
-        if (lane == 0) mma_commit(base + L::kEmpty + 8 * slot);
-      };
-      uint32_t slot;
-      if (kDual) {
-        ok = ok && take(s.t0, false, slot);
-        if (ok) {
-          for (int st = 0; st < streams; ++st) scores(s.t0, st, slot);
-          release(slot);
-        }
-        for (int j = s.t0; ok && j < s.t1; ++j) {
-          uint32_t vslot = 0, kslot = 0;
-          for (int st = 0; ok && st < streams; ++st) {
-            ok = wait.warp(base + L::kPFull + 8 * st, nv[st] & 1);
-            if (ok && st == 0) ok = take(j, true, vslot);
+        uint32_t vslot, kslot, vt, kt;
+        int steps;
+        if (kDual) {
+          ok = ok && take_k(s.t0, kslot, kt);
+          if (ok) {
+            tc_fence_after();
+            for (int st = 0; st < streams; ++st) scores(s.t0, st, kt);
+            release(kslot);
+          }
+          for (int j = s.t0; ok && j < s.t1; ++j) {
+            const bool more = j + 1 < s.t1;
+            ok = take_v(j, vslot, vt, steps) && (!more || take_k(j + 1, kslot, kt));
+            for (int st = 0; ok && st < streams; ++st) {
+              ok = wait(base + L::kPFull + 8 * st, nv[st] & 1);
+              if (!ok) break;
+              tc_fence_after();
+              values(st, vt, steps, j > s.t0);
+              if (st == streams - 1) release(vslot);
+              if (more) {
+                scores(j + 1, st, kt);
+                if (st == streams - 1) release(kslot);
+              } else {
+                mma_commit(base + L::kOFull + 8 * st);
+              }
+            }
+          }
+        } else {
+          for (int j = s.t0; ok && j < min(s.t0 + 2, s.t1); ++j) {
+            ok = take_k(j, kslot, kt);
             if (!ok) break;
             tc_fence_after();
-            values(j, st, vslot, j > s.t0);
-            if (st == streams - 1) release(vslot);
-            if (j + 1 < s.t1) {
-              if (st == 0) ok = take(j + 1, false, kslot);
-              if (!ok) break;
-              scores(j + 1, st, kslot);
-              if (st == streams - 1) release(kslot);
+            scores(j, (j - s.t0) & 1, kt);
+            release(kslot);
+          }
+          for (int j = s.t0; ok && j < s.t1; ++j) {
+            const int st = (j - s.t0) & 1;
+            const bool more = j + 2 < s.t1;
+            ok = take_v(j, vslot, vt, steps) && (!more || take_k(j + 2, kslot, kt)) &&
+                 wait(base + L::kPFull + 8 * st, nv[st] & 1);
+            if (!ok) break;
+            tc_fence_after();
+            values(st, vt, steps, j > s.t0 + 1);
+            release(vslot);
+            if (more) {
+              scores(j + 2, st, kt);
+              release(kslot);
+            } else {
+              mma_commit(base + L::kOFull + 8 * st);
             }
+          }
+        }
+        if (ok) mma_commit(base + L::kQEmpty);
+      }
+      if (gathered != asked) mbar_wait_bounded(base + L::kQKFull, gathered & 1, kDrainNs);
+      ask(0, make_int4(-1, 0, 0, 0));
+      ask(1, make_int4(-1, 0, 0, 0));
+      if (!ok) {
+        mma_commit(base + L::kDrain);
+        mbar_wait_bounded(base + L::kDrain, 0, kDrainNs);
+      }
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------- the MMAs' aides
+    // Warp 2 gathers q to the kept channels; warp 3 clears the rows behind the
+    // last key of a tile of values (the MMA takes 16 keys at a time: P is 0
+    // there, but 0 * NaN is not).  The MMA thread asks, and always says when
+    // it is done, so these waits end with its own.
+    const int who = warp - 2;
+    for (uint32_t n = 0;; ++n) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(base + L::kAsk + 8 * who, n & 1, kIdleNs))) {
+        *gone = 1;
+        break;
+      }
+      const int4 task = *reinterpret_cast<const int4*>(sm + L::kTask + 16 * who);
+      if (task.x < 0) break;
+      if (who == 0) {
+        const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + task.x) * kHeadDim;
+        const int groups = task.y / 8;
+        for (int x = 0; x < L::kQTiles; ++x) {
+          const uint8_t* q = sm + L::kQ + x * kWideBytes;
+          uint8_t* out = sm + L::kQKept + x * w.kept_bytes;
+          const int rows = x == 0 ? task.z : task.w;
+          for (int y = lane; y < rows * groups; y += 32) {
+            const int r = y / groups, c = y - r * groups;
+            const uint4 kc = *reinterpret_cast<const uint4*>(kept + 8 * c);
+            auto at = [&](uint32_t ch) {
+              return (uint32_t)*reinterpret_cast<const uint16_t*>(q + kept_byte(kHeadDim, r, (int)ch >> 3) + (ch & 7) * 2);
+            };
+            auto two = [&](uint32_t p) { return at(p & 0xffffu) | at(p >> 16) << 16; };
+            *reinterpret_cast<uint4*>(out + kept_byte(task.y, r, c)) =
+                make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
           }
         }
       } else {
-        for (int j = s.t0; ok && j < min(s.t0 + 2, s.t1); ++j) {
-          ok = take(j, false, slot);
-          if (!ok) break;
-          scores(j, (j - s.t0) & 1, slot);
-          release(slot);
-          if (j == s.t0 && s.t0 + 1 < s.t1) continue;
-        }
-        for (int j = s.t0; ok && j < s.t1; ++j) {
-          const int st = (j - s.t0) & 1;
-          ok = wait.warp(base + L::kPFull + 8 * st, nv[st] & 1) && take(j, true, slot);
-          if (!ok) break;
-          tc_fence_after();
-          values(j, st, slot, j > s.t0 + 1);
-          release(slot);
-          if (j + 2 < s.t1) {
-            ok = take(j + 2, false, slot);
-            if (!ok) break;
-            scores(j + 2, st, slot);
-            release(slot);
-          }
-        }
-      }
-      if (ok && lane == 0) mma_commit(base + L::kQEmpty);
-      if (gathers(s)) ++gathered;
-      __syncwarp();
-    }
-    if (!ok && lane == 0) {
-      mma_commit(base + L::kDrain);
-      mbar_wait_bounded(base + L::kDrain, 0, 1000000000ull);
-    }
-  } else if (warp < 4) {
-    // ------------------------------------------------ q on the kept channels
-    Segment s;
-    begin(s);
-    while (advance(s)) {
-      if (!wait.warp(base + L::kQFull, s.idx & 1)) break;
-      if (!gathers(s)) continue;
-      const Item& it = s.it;
-      const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + it.h) * kHeadDim;
-      const int groups = it.k / 8;
-      for (int x = 0; x < (kDual && it.ntok > tq ? 2 : 1); ++x) {
-        const uint8_t* q = sm + L::kQ + x * kWideBytes;
-        uint8_t* out = sm + L::kQKept + x * kKeptBytes;
-        const int rows = min(tq, it.ntok - x * tq) * G;
-        for (int y = tid - 64; y < rows * groups; y += 64) {
-          const int r = y / groups, c = y - r * groups;
-          const uint4 kc = *reinterpret_cast<const uint4*>(kept + 8 * c);
-          auto at = [&](uint32_t ch) {
-            return (uint32_t)*reinterpret_cast<const uint16_t*>(q + kept_byte(kHeadDim, r, (int)ch >> 3) + (ch & 7) * 2);
-          };
-          auto two = [&](uint32_t p) { return at(p & 0xffffu) | at(p >> 16) << 16; };
-          *reinterpret_cast<uint4*>(out + kept_byte(it.k, r, c)) = make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
-        }
+        for (int z = lane; z < (task.z - task.y) * 16; z += 32)
+          *reinterpret_cast<uint4*>(sm + task.x + kept_byte(kHeadDim, task.y + z / 16, z % 16)) =
+              make_uint4(0u, 0u, 0u, 0u);
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(base + L::kQKFull);
+      if (lane == 0) mbar_arrive(base + (who == 0 ? L::kQKFull : L::kFixed));
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -722,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t my_s = tm_s + st * 128 + quarter, my_o = tm_o + st * 128 + quarter;
     const int tok = row / G, g = row - tok * G;
-    uint32_t tiles = 0, merges = 0;       // key tiles and merges this group has seen
+    uint32_t tiles = 0, outs = 0, merges = 0;       // key tiles, outputs and merges of this group
     Segment s;
     begin(s);
     bool ok = true;
@@ -733,11 +893,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = tok < tq && i < it.i0 + it.ntok;
       float m = -INFINITY, l = 0.f;
       int done = 0;                       // key tiles of this segment
+      const int m0 = it.nA + it.nC, m1 = m0 + it.mid / kTile;
       for (int j = s.t0 + (kDual ? 0 : st); j < s.t1; j += kDual ? 1 : 2) {
-        const Tile t = tile_at(it, j);
-        uint32_t vis[4];
-        visible(a, w, it, t, i, vis);
-        const bool all = __all_sync(0xffffffffu, !mine || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
+        uint32_t vis[4] = {};
+        bool all = j >= m0 && j < m1;      // whole middle tiles, the common case, are seen by all
+        if (!all) {
+          visible(a, w, it, tile_at(it, j), i, vis);
+          all = __all_sync(0xffffffffu, !mine || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
+        }
         ok = wait.warp(base + L::kSFull + 8 * st, tiles & 1);
         if (!ok) break;
         tc_fence_after();
@@ -750,9 +913,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 128; ++c)
             if ((vis[c >> 5] >> (c & 31) & 1u) == 0) x[c] = 0xff800000u;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[4];
 #pragma unroll
-        for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+#pragma unroll
+        for (int c = 8; c < 128; c += 2)
+          mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
         // The maximum moves only when a score exceeds it by 2^8: below that p
         // stays exact in fp32 and bf16 alike.
@@ -762,9 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mn;
           l *= f;
           if (done > 0) {
-            ok = wait.warp(base + L::kOFull + 8 * st, (tiles - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
+            // (this tile's scores came after the last tile's P.V)
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t o[32];
@@ -777,15 +941,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pair(kScaleLog2, kScaleLog2), off2 = pair(off, off);
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < 128; c += 2) {
-          const float p0 = ex2(fmaf(__uint_as_float(x[c]), kScaleLog2, off));
-          const float p1 = ex2(fmaf(__uint_as_float(x[c + 1]), kScaleLog2, off));
-          sum[c >> 1 & 3] += p0 + p1;
+          float p0, p1;
+          unpair(fma2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, off2), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          sum[c >> 1 & 3] = add2(sum[c >> 1 & 3], pair(p0, p1));
           x[c >> 1] = pack_bf16x2(p0, p1);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float l0, l1;
+        unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+        l += l0 + l1;
         tmem_st32(my_s, x);
         tmem_st32(my_s + 32, x + 32);
         tmem_wait_st();
@@ -797,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (done > 0) {
-        ok = wait.warp(base + L::kOFull + 8 * st, (tiles - 1) & 1);
+        ok = wait.warp(base + L::kOFull + 8 * st, outs++ & 1);
         if (!ok) break;
         tc_fence_after();
       }
@@ -881,42 +1050,86 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ----------------------------------------------------------------- merge
 // Block (i - 1, y): if the item that CTA i starts inside of has no earlier
 // such CTA, its partials are CTA i - 1's last one and the first ones of CTA
-// i, i + 1, ... while they start inside the same item.  16 rows a block, 16
-// threads a row.
-__global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const ChunkWork w) {
-  const int P = w.start[w.max_ctas + 1].x, i = blockIdx.x + 1;
+// i, i + 1, ... while they start inside the same item.  8 rows a block, a warp
+// a row: the lanes read the row's (m, l) of all partials at once (32 at a
+// time), then the warp its outputs, four partials in flight.
+constexpr int kMergeRows = 8;
+__global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const __grid_constant__ ChunkArgs a,
+                                                                      const ChunkWork w) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int P = __ldcg(&w.start[w.max_ctas + 1].x), i = blockIdx.x + 1;
   if (i >= P) return;
-  const int2 at = w.start[i], before = w.start[i - 1];
+  const int lane = threadIdx.x & 31;
+  const int2 at = __ldcg(&w.start[i]), before = __ldcg(&w.start[i - 1]);
   if (at.y == 0 || (before.x == at.x && before.y > 0)) return;
   Item it;
   if (!item_info(a, w, at.x, it)) return;
-  const int row = blockIdx.y * 16 + threadIdx.x / 16, ch = threadIdx.x % 16 * 8;
+  const int row = blockIdx.y * kMergeRows + threadIdx.x / 32;
   const int stream = row / kTile, r = row % kTile;
   const int tok = r / a.cv.G, q = stream * w.tile_tokens + tok;
   if (tok >= w.tile_tokens || q >= it.ntok) return;
-  float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int c = i - 1; c < P; ++c) {
-    if (c >= i) {
-      const int2 x = w.start[c];
-      if (x.x != at.x || x.y == 0) break;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = i - 1; c0 < P; c0 += 32) {
+    const int c = c0 + lane;
+    bool in = c < P;
+    if (in && c >= i) {
+      const int2 x = __ldcg(&w.start[c]);
+      in = x.x == at.x && x.y > 0;
     }
-    const int64_t prow = (int64_t)(2 * c + (c < i ? 1 : 0)) * w.part_rows + row;
-    const float2 ml = __ldcg(&w.part_ml[prow]);
-    const float4 u = __ldcg(reinterpret_cast<const float4*>(w.part + prow * kHeadDim + ch));
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(w.part + prow * kHeadDim + ch) + 1);
-    const float mn = fmaxf(m, ml.x);
-    if (mn == -INFINITY) continue;
-    const float f = ex2(m - mn), e = ex2(ml.x - mn);
-    m = mn;
-    l = l * f + ml.y * e;
-    const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    const int n = __ffs(~__ballot_sync(0xffffffffu, in)) - 1;      // -1: all 32
+    const int count = n < 0 ? 32 : n;
+    const auto slot = [&](int x) { return (int64_t)(2 * x + (x < i ? 1 : 0)) * w.part_rows + row; };
+    const float2 ml = lane < count ? __ldcg(&w.part_ml[slot(c)]) : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
 #pragma unroll
-    for (int z = 0; z < 8; ++z) o[z] = o[z] * f + y[z] * e;
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float mn = fmaxf(m, top);
+    if (mn > -INFINITY) {
+      const float f = ex2(m - mn), e = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+      float sum = ml.y * e;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      m = mn;
+      l = l * f + sum;
+      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll 4
+      for (int x = 0; x < count; ++x) {
+        const float ex = __shfl_sync(0xffffffffu, e, x);
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(w.part + slot(c0 + x) * kHeadDim) + lane);
+        // a partial without a key holds nothing to add
+        if (ex > 0.f) {
+          o.x += ex * u.x;
+          o.y += ex * u.y;
+          o.z += ex * u.z;
+          o.w += ex * u.w;
+        }
+      }
+    }
+    if (count < 32) break;
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint16_t* out = a.o + (((int64_t)it.b * a.n_max + it.i0 + q) * a.cv.Hq + it.h * a.cv.G + r % a.cv.G) * kHeadDim + ch;
-  *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
-                                              pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+  uint16_t* out = a.o + (((int64_t)it.b * a.n_max + it.i0 + q) * a.cv.Hq + it.h * a.cv.G + r % a.cv.G) * kHeadDim;
+  reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+
+// A launch that may begin while the stream's preceding kernel ends; every
+// block of such a kernel waits for that one before it leaves.
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                         const std::decay_t<Args>&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <bool kDual>
@@ -924,21 +1137,20 @@ cudaError_t launch_attn(const ChunkMaps& maps, const ChunkArgs& args, const Chun
   static std::atomic<uint64_t> done{0};
   cudaError_t err = set_smem_limit_once(chunk_attn_kernel<kDual>, Smem<kDual>::kBytes, done);
   if (err != cudaSuccess) return err;
-  chunk_attn_kernel<kDual><<<(unsigned)w.max_ctas, kThreads, Smem<kDual>::kBytes, stream>>>(maps, args, w);
-  return cudaGetLastError();
+  return launch_after(chunk_attn_kernel<kDual>, dim3((unsigned)w.max_ctas), kThreads, Smem<kDual>::kBytes, stream, maps,
+                      args, w);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& w, cudaStream_t stream) {
-  const int plan_blocks = 1 + w.special_seqs + args.nb * args.cv.Hkv * w.far_tiles;
-  chunk_plan_kernel<<<(unsigned)plan_blocks, kPlanThreads, 0, stream>>>(args, w);
-  cudaError_t err = cudaGetLastError();
+  const unsigned plan_blocks = 1u + w.special_seqs + (unsigned)(args.nb * args.cv.Hkv) * w.far_tiles;
+  cudaError_t err = launch_after(chunk_plan_kernel, dim3(plan_blocks), kPlanThreads, 0, stream, args, w);
   if (err != cudaSuccess) return err;
   err = w.dual ? launch_attn<true>(maps, args, w, stream) : launch_attn<false>(maps, args, w, stream);
   if (err != cudaSuccess || w.max_ctas < 2) return err;
-  chunk_merge_kernel<<<dim3((unsigned)w.max_ctas - 1, (unsigned)(w.part_rows + 15) / 16), 256, 0, stream>>>(args, w);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)w.max_ctas - 1, (unsigned)(w.part_rows + kMergeRows - 1) / kMergeRows);
+  return launch_after(chunk_merge_kernel, grid, 32 * kMergeRows, 0, stream, args, w);
 }
 
 }  // namespace lk

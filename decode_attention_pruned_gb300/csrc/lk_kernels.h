@@ -127,7 +127,7 @@ struct ChunkWork {
   int32_t far_bytes;        // of one image
   int32_t special_seqs;     // sequences whose special tokens are flagged (0: no SPECIAL head)
   int32_t special_words;    // 32-token words per sequence
-  int32_t pad;
+  int32_t kept_bytes;       // of a query tile on the kept channels
   int2* start;              // [max_ctas + 2]: (item, tile) where each CTA starts, the end; then (CTAs, -)
   float2* part_ml;          // [2 max_ctas][part_rows]
   float* part;              // [2 max_ctas][part_rows][128]

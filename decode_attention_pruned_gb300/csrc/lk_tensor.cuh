@@ -7,6 +7,12 @@
 
 namespace lk {
 
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
 // ------------------------------------------------------------ tensor memory
 // All of an SM's tensor memory (128 lanes x 512 columns of 32 bits); the
 // address lands in shared memory.  One whole warp allocates and frees.
@@ -78,11 +84,12 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn_major) {
 // D (tensor memory) = A B (+ D): A from shared memory, or from tensor memory
 // (bf16 pairs packed two to a column).  One thread issues; the operations of
 // a thread run in the order it issues them.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+      "l"(a), "l"(b), "r"(desc), "n"(kAccumulate ? 1 : 0)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool accumulate) {
@@ -91,6 +98,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
       : "memory");
+}
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
 }
 // The barrier gets one arrival once everything this thread has issued is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
