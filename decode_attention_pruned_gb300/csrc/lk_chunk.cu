@@ -154,10 +154,6 @@ __device__ __forceinline__ Tile tile_at(const Item& it, int j) {
   return t;
 }
 
-// Whether values behind the tile's last key must be cleared (F images end in
-// zeros).
-__device__ __forceinline__ bool needs_fix(const Tile& t) { return t.type != kTileF && (t.rows & 15) != 0; }
-
 // Image of one F tile: kept channels as the middle's tiles lie in shared
 // memory, then V.
 __device__ __forceinline__ uint8_t* far_tile(const ChunkArgs& a, const ChunkWork& w, int seq, int h, int tile) {
@@ -327,7 +323,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------- attention
-constexpr int kThreads = 384;              // warps: TMA, MMA, two that gather q, two softmax groups of four
+constexpr int kThreads = 384;              // warps: TMA, two for MMA, an aide, two softmax groups of four
+constexpr int kHalf = kTile / 2;           // keys per step of the softmax
 constexpr int kWideBytes = kTile * kHeadDim * 2;
 
 // kDual: a CTA works on two query tiles, which share every key tile, one per
@@ -338,25 +335,27 @@ constexpr int kWideBytes = kTile * kHeadDim * 2;
 // through in order, each taking what it needs (a key tile on 32 channels 8 KB,
 // full-width ones and values 32 KB), so that narrow heads have the more tiles
 // in flight.
-constexpr int kSlots = 16;                 // tiles in flight at most
 template <bool kDual>
 struct Smem {
   static constexpr int kQTiles = kDual ? 2 : 1;
+  static constexpr int kRings = kDual ? 1 : 2;           // one that both groups read, or one for each
+  static constexpr int kSlots = 16;                      // tiles in flight per ring at most
   static constexpr int kML = 0;                          // second group's (m, l)
-  static constexpr int kFull = kML + kTile * 8, kEmpty = kFull + 8 * kSlots, kQFull = kEmpty + 8 * kSlots,
-                       kQEmpty = kQFull + 8, kQKFull = kQEmpty + 8, kSFull = kQKFull + 8, kPFull = kSFull + 16,
-                       kOFull = kPFull + 16, kMerge = kOFull + 16, kMerged = kMerge + 8, kAsk = kMerged + 8,
-                       kFixed = kAsk + 16, kDrain = kFixed + 8, kTmem = kDrain + 8, kOffs = kTmem + 16,
-                       kTask = (kOffs + 4 * kSlots + 15) / 16 * 16;
+  static constexpr int kFull = kML + kTile * 8, kEmpty = kFull + 8 * kSlots * kRings,
+                       kQFull = kEmpty + 8 * kSlots * kRings, kQEmpty = kQFull + 8, kQKFull = kQEmpty + 8,
+                       kSFull = kQKFull + 16, kPFull = kSFull + 32, kOFull = kPFull + 32, kOEnd = kOFull + 16, kMerge = kOEnd + 16,
+                       kMerged = kMerge + 8, kAsk = kMerged + 8, kLanded = kAsk + 8, kCleared = kLanded + 8,
+                       kDrain = kCleared + 8, kTmem = kDrain + 16, kOffs = kTmem + 16,
+                       kTask = (kOffs + 4 * kSlots * kRings + 15) / 16 * 16;
   static constexpr int kQ = 2048;
-  static_assert(kTask + 32 <= kQ, "barriers, offsets and tasks");
+  static_assert(kTask + 16 <= kQ, "barriers, offsets and tasks");
   static constexpr int kQKept = kQ + kQTiles * kWideBytes;
   static constexpr int kBytes = 227 * 1024;
   static constexpr int kEnd = kBytes - 1024;             // after aligning the base
 };
 
 constexpr uint64_t kDrainNs = 1000000000ull;      // bound of the waits for copies and MMAs still in flight
-constexpr uint64_t kIdleNs = 60000000000ull;      // bound of the aides' waits for a task
+constexpr uint64_t kIdleNs = 60000000000ull;      // bound of the aide's wait for a task
 
 struct Wait {
   uint64_t limit;
@@ -474,24 +473,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cta = blockIdx.x;
   volatile int* gone = reinterpret_cast<volatile int*>(sm + L::kTmem + 8);
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < L::kSlots * L::kRings; ++i) {
       mbar_init(base + L::kFull + 8 * i, 1);
-      mbar_init(base + L::kEmpty + 8 * i, 1);
+      mbar_init(base + L::kEmpty + 8 * i, kDual ? 2 : 1);
     }
     mbar_init(base + L::kQFull, 1);
-    mbar_init(base + L::kQEmpty, 1);
-    mbar_init(base + L::kQKFull, 1);
+    mbar_init(base + L::kQEmpty, 10);                     // both MMA threads and the softmax warps
     for (int s = 0; s < 2; ++s) {
-      mbar_init(base + L::kSFull + 8 * s, 1);
-      mbar_init(base + L::kPFull + 8 * s, 4);
+      mbar_init(base + L::kQKFull + 8 * s, kDual ? 4 : 8);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(base + L::kSFull + 16 * s + 8 * x, 1);
+        mbar_init(base + L::kPFull + 16 * s + 8 * x, 4);
+      }
       mbar_init(base + L::kOFull + 8 * s, 1);
+      mbar_init(base + L::kOEnd + 8 * s, 1);
+      mbar_init(base + L::kDrain + 8 * s, 1);
     }
     mbar_init(base + L::kMerge, 4);
     mbar_init(base + L::kMerged, 4);
     mbar_init(base + L::kAsk, 1);
-    mbar_init(base + L::kAsk + 8, 1);
-    mbar_init(base + L::kFixed, 1);
-    mbar_init(base + L::kDrain, 1);
+    mbar_init(base + L::kLanded, 1);
+    mbar_init(base + L::kCleared, 1);
     fence_barrier_init();
     *gone = 0;
   }
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     reinterpret_cast<uint4*>(sm)[x] = make_uint4(0u, 0u, 0u, 0u);
   fence_async_smem();
   if (warp == 0 && lane < 3 + kNumPools) tma_prefetch_map(&maps.q + lane);
-  if (warp == 1) tmem_alloc_all(base + L::kTmem);
+  if (warp == 3) tmem_alloc_all(base + L::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -548,40 +550,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------- loads
     if (lane == 0) {
-      // The ring is a FIFO of runs of bytes: the oldest tile in flight starts
-      // at `tail`, the next goes to `head`, or to the ring's start when it
-      // does not fit before the end.
-      const uint32_t size = L::kEnd - ring;
+      // A ring is a FIFO of runs of bytes: the oldest tile in flight starts at
+      // `tail`, the next goes to `head`, or to the ring's start when it does
+      // not fit before the end.
+      const uint32_t size = (L::kEnd - ring) / L::kRings & ~1023u;
       uint32_t* offs = reinterpret_cast<uint32_t*>(sm + L::kOffs);
-      uint32_t put = 0, freed = 0, head = 0, tail = 0;
-      bool wrapped = false;
+      struct Ring {
+        uint32_t put, freed, head, tail;
+        bool wrapped;
+      } rings[L::kRings] = {};
       // Keys that one query tile reads are read once; those that several read
       // should stay in L2.
       const uint64_t once = l2_policy_evict_first(), keep = w.items_q > 1 ? l2_policy_evict_normal() : once;
-      auto reserve = [&](uint32_t bytes, uint32_t& at) -> bool {
+      auto reserve = [&](int ri, uint32_t bytes, uint32_t& at) -> bool {
+        Ring& r = rings[ri];
         while (true) {
-          if (put == freed) {
-            head = tail = 0;
-            wrapped = false;
+          if (r.put == r.freed) {
+            r.head = r.tail = 0;
+            r.wrapped = false;
           }
-          if (put - freed < kSlots) {
-            if (!wrapped && head + bytes <= size) break;
-            if (!wrapped && bytes <= tail) {
-              head = 0;
-              wrapped = true;
+          if (r.put - r.freed < L::kSlots) {
+            if (!r.wrapped && r.head + bytes <= size) break;
+            if (!r.wrapped && bytes <= r.tail) {
+              r.head = 0;
+              r.wrapped = true;
               break;
             }
-            if (wrapped && head + bytes <= tail) break;
+            if (r.wrapped && r.head + bytes <= r.tail) break;
           }
-          if (!wait(base + L::kEmpty + 8 * (freed % kSlots), (freed / kSlots) & 1)) return false;
-          if (++freed != put) {
-            const uint32_t t = offs[freed % kSlots];
-            if (t < tail) wrapped = false;
-            tail = t;
+          if (!wait(base + L::kEmpty + 8 * (ri * L::kSlots + r.freed % L::kSlots), (r.freed / L::kSlots) & 1)) return false;
+          if (++r.freed != r.put) {
+            const uint32_t t = offs[ri * L::kSlots + r.freed % L::kSlots];
+            if (t < r.tail) r.wrapped = false;
+            r.tail = t;
           }
         }
-        at = head;
-        head += bytes;
+        at = r.head;
+        r.head += bytes;
+        return true;
+      };
+      uint32_t tasks = 0;                 // given to the aide
+      auto ask = [&](int4 task) -> bool {
+        if (tasks > 0 && !wait(base + L::kCleared, (tasks - 1) & 1)) return false;
+        ++tasks;
+        volatile int* t = reinterpret_cast<volatile int*>(sm + L::kTask);
+        t[0] = task.x, t[1] = task.y, t[2] = task.z, t[3] = task.w;
+        mbar_arrive(base + L::kAsk);
         return true;
       };
       Segment s;
@@ -594,9 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t krow_b = hd.krow_b, vrow_b = hd.vrow_b;
         const int64_t abase = hd.row_a + (int64_t)it.b * hd.cap_a, bbase = (int64_t)it.b * hd.cap_b;
         const int32_t* pages = cv.max_pages > 0 ? page_row(cv, a.layer, it.b, it.h) : nullptr;
-        // page ids are read a tile or two ahead of the loads that need them
         const int m0 = it.nA + it.nC;
-        int32_t page = 0, next_page = 0;
         if (s.idx > 0) ok = wait(base + L::kQEmpty, (s.idx - 1) & 1);
         if (!ok) break;
         const int nq = kDual && it.ntok > tq ? 2 : 1;
@@ -608,12 +620,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto load = [&](int j, bool isv, int32_t pg) -> bool {
           const Tile t = tile_at(it, j);
           const bool wide = isv || t.type <= kTileC || it.k == kHeadDim;
+          const int ri = kDual ? 0 : (j - s.t0) & 1;
           uint32_t at;
-          if (!reserve(wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * 2 * it.k), at)) return false;
-          const uint32_t slot = put % kSlots;
+          if (!reserve(ri, wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * 2 * it.k), at)) return false;
+          const uint32_t slot = ri * L::kSlots + rings[ri].put % L::kSlots;
           offs[slot] = at;
-          ++put;
-          const uint32_t dst = base + ring + at, bar = base + L::kFull + 8 * slot;
+          const uint32_t dst = base + ring + ri * size + at;
+          uint32_t bar = base + L::kFull + 8 * slot;
+          if (isv && t.type != kTileF && (t.rows & 15) != 0) {
+            // the aide clears what lies behind the last key, then signals the slot
+            if (!ask(make_int4((int)(dst - base), t.rows, (t.rows + 15) & ~15, (int)slot))) return false;
+            bar = base + L::kLanded;
+          }
+          ++rings[ri].put;
           if (t.type == kTileC) {
             mbar_arrive_expect_tx(bar, kWideBytes);
             tma_load_4d(dst, isv ? &maps.v : &maps.k, 0, it.b * a.n_max + t.r0, 0, it.h, bar, keep);
@@ -644,72 +663,112 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        // page id of the middle tile that key tile j is, if any
+        // page id of the middle tile that key tile j is, if any; read two
+        // tiles before the loads that need it
         auto page_at = [&](int j) -> int32_t {
           return pages != nullptr && j >= m0 && j < m0 + it.nM ? __ldcg(pages + (j - m0)) : 0;
         };
+        int32_t page = page_at(s.t0), next_page = page_at(s.t0 + 1);
         for (int j = s.t0; ok && j < s.t1; ++j) {
-          const int32_t after = page_at(j + (kDual ? 1 : 2));
-          if (kDual) {
-            if (j == s.t0) page = page_at(j);
-            ok = load(j, false, page) && load(j, true, page);
-            page = after;
-          } else {
-            if (j == s.t0) {
-              page = page_at(j);
-              next_page = page_at(j + 1);
-              ok = load(j, false, page);
-            }
-            if (ok && j + 1 < s.t1) ok = load(j + 1, false, next_page);
-            if (ok) ok = load(j, true, page);
-            page = next_page;
-            next_page = after;
-          }
+          const int32_t after = page_at(j + 2);
+          ok = load(j, false, page) && load(j, true, page);
+          page = next_page;
+          next_page = after;
         }
       }
       // copies still in flight must land before the block ends
       if (!ok) {
-        for (uint32_t x = freed; x < put; ++x)
-          mbar_wait_bounded(base + L::kFull + 8 * (x % kSlots), (x / kSlots) & 1, kDrainNs);
+        for (int ri = 0; ri < L::kRings; ++ri)
+          for (uint32_t x = rings[ri].freed; x < rings[ri].put; ++x)
+            mbar_wait_bounded(base + L::kFull + 8 * (ri * L::kSlots + x % L::kSlots), (x / L::kSlots) & 1, kDrainNs);
         if (s.idx >= 0) mbar_wait_bounded(base + L::kQFull, s.idx & 1, kDrainNs);
+        if (tasks > 0) mbar_wait_bounded(base + L::kCleared, (tasks - 1) & 1, kDrainNs);
+        volatile int* t = reinterpret_cast<volatile int*>(sm + L::kTask);
+        t[0] = -1;
+        mbar_arrive(base + L::kAsk);
+      } else if (!ask(make_int4(-1, 0, 0, 0))) {
+        mbar_arrive(base + L::kAsk);
       }
     }
-  } else if (warp == 1) {
+  } else if (warp < 3) {
     // -------------------------------------------------------------- MMAs
-    // One thread issues them all; what it does per tile is kept short, as the
-    // tensor core waits for it.
+    // A thread for each softmax group issues its scores S = Q K^T and outputs
+    // O += P V, half a key tile (64 keys) at a time: the scores of one half are
+    // made while the group works on the half before.  What the thread does per
+    // half is kept short, as the tensor core waits for it.
+    const int st = warp - 1;
     if (elect_one()) {
-      constexpr uint32_t kDescS = mma_desc(128, kTile, false), kDescO = mma_desc(128, kHeadDim, true);
+      constexpr uint32_t kDescS = mma_desc(128, kHalf, false), kDescO = mma_desc(128, kHeadDim, true);
       const uint64_t wide_desc = smem_desc(0, 16, 1024, kSwizzle128), thin_desc = smem_desc(0, 16, 512, kSwizzle64);
       const uint64_t v_desc = smem_desc(0, kWideBytes / 2, 1024, kSwizzle128);
-      uint32_t got = 0, asked = 0, gathered = 0, fixed = 0, nv[2] = {0, 0};
-      // Hands a task to warp 2 (gather) or 3 (clear); the last one is done by then.
-      auto ask = [&](int who, int4 task) {
-        *reinterpret_cast<volatile int*>(sm + L::kTask + 16 * who) = task.x;
-        *reinterpret_cast<volatile int*>(sm + L::kTask + 16 * who + 4) = task.y;
-        *reinterpret_cast<volatile int*>(sm + L::kTask + 16 * who + 8) = task.z;
-        *reinterpret_cast<volatile int*>(sm + L::kTask + 16 * who + 12) = task.w;
-        mbar_arrive(base + L::kAsk + 8 * who);
-      };
+      const uint32_t ring_at = base + ring + (kDual ? 0u : st * ((L::kEnd - ring) / L::kRings & ~1023u));
+      const uint32_t full = base + L::kFull + (kDual ? 0 : st * 8 * L::kSlots);
+      const uint32_t empty = base + L::kEmpty + (kDual ? 0 : st * 8 * L::kSlots);
+      volatile uint32_t* offs = reinterpret_cast<volatile uint32_t*>(sm + L::kOffs) + (kDual ? 0 : st * L::kSlots);
+      uint32_t taken = 0, gathered = 0, hs = 0, ho = 0;   // ring tiles before this segment; halves scored, put out
       Segment s;
       begin(s);
       bool ok = true;
       while (ok && advance(s)) {
         const Item& it = s.it;
-        const int streams = kDual && it.ntok <= tq ? 1 : 2;
         const int m0 = it.nA + it.nC, m1 = m0 + it.mid / kTile;
         const bool gather = gathers(s);
+        constexpr int kStep = kDual ? 1 : 2;
+        const int j0 = s.t0 + (kDual ? 0 : st);
+        const int mine = j0 < s.t1 ? (s.t1 - j0 + kStep - 1) / kStep : 0;      // this ring's key tiles
+        ok = wait(base + L::kQFull, s.idx & 1);
+        if (kDual && st == 1 && it.ntok <= tq) {
+          // no second query tile: its share of the releases
+          for (int x = 0; ok && x < 2 * mine; ++x) {
+            const uint32_t e = taken + x, slot = e % L::kSlots;
+            ok = wait(full + 8 * slot, (e / L::kSlots) & 1);
+            if (ok) mbar_arrive(empty + 8 * slot);
+          }
+          taken += 2 * mine;
+          if (ok) mbar_arrive(base + L::kQEmpty);
+          continue;
+        }
         bool have_kept = !gather;
-        // 16-byte units of the two operands
-        const uint32_t q_wide = (base + L::kQ) >> 4, q_kept = (base + L::kQKept) >> 4;
-        // scores of a key tile: both query tiles', or the one's for group `st`
-        auto scores = [&](int j, int st, uint32_t kt) {
-          const uint32_t d = tm_s + st * 128, x = kDual ? st : 0;
-          const int width = j < m0 ? kHeadDim : it.k;
+        const uint32_t q_wide = (base + L::kQ + (kDual ? st * kWideBytes : 0)) >> 4;       // in 16 bytes
+        const uint32_t q_kept = (base + L::kQKept + (kDual ? st * w.kept_bytes : 0)) >> 4;
+        auto rows_at = [&](int j) { return j >= m0 && j < m1 ? kTile : tile_at(it, j).rows; };
+        // cursors of the scores and of the outputs: tile (of mine), half, rows, ring slot, address
+        struct Cursor {
+          int x, half, rows;
+          uint32_t slot, addr;
+        } cs{0, 0, 0, 0, 0}, co{0, 0, 0, 0, 0};
+        auto enter = [&](Cursor& c, int which) -> bool {
+          const uint32_t e = taken + 2 * c.x + which;
+          c.slot = e % L::kSlots;
+          if (!wait(full + 8 * c.slot, (e / L::kSlots) & 1)) return false;
+          c.addr = ring_at + offs[c.slot];
+          c.rows = rows_at(j0 + c.x * kStep);
+          return true;
+        };
+        auto leave = [&](Cursor& c) {
+          if (c.half == 0 && c.rows > kHalf) {
+            c.half = 1;
+          } else {
+            mma_commit(empty + 8 * c.slot);
+            c.half = 0;
+            ++c.x;
+          }
+        };
+        auto scores = [&]() -> bool {
+          const int j = j0 + cs.x * kStep;
+          if (cs.half == 0) {
+            if (!have_kept && j >= m0) {
+              if (!wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1)) return false;
+              have_kept = true;
+            }
+            if (!enter(cs, 0)) return false;
+            tc_fence_after();
+          }
+          const uint32_t buf = hs & 1, d = tm_s + st * 128 + buf * kHalf;
           auto run = [&](auto steps, uint64_t desc, uint32_t q) {
             constexpr int kSteps = decltype(steps)::value;
             constexpr bool kThin = kSteps == 2 || kSteps == 6;
-            const uint64_t qd = desc | q, kd = desc | (kt >> 4);
+            const uint64_t qd = desc | q, kd = desc | ((cs.addr >> 4) + cs.half * (kHalf * (kThin ? 4 : 8)));
             mma_ss<false>(d, qd, kd, kDescS);
 #pragma unroll
             for (int y = 1; y < kSteps; ++y) {
@@ -717,162 +776,74 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_ss<true>(d, qd + at, kd + at, kDescS);
             }
           };
-          if (width == kHeadDim) {
-            run(std::integral_constant<int, 8>(), wide_desc, q_wide + x * (kWideBytes >> 4));
-          } else {
-            const uint32_t q = q_kept + x * ((uint32_t)w.kept_bytes >> 4);
-            if (width == 32) run(std::integral_constant<int, 2>(), thin_desc, q);
-            else if (width == 64) run(std::integral_constant<int, 4>(), wide_desc, q);
-            else run(std::integral_constant<int, 6>(), thin_desc, q);
-          }
-          mma_commit(base + L::kSFull + 8 * st);
-        };
-        // next tile of the ring: its slot and address
-        auto take = [&](uint32_t& slot, uint32_t& addr) -> bool {
-          slot = got % kSlots;
-          if (!wait(base + L::kFull + 8 * slot, (got / kSlots) & 1)) return false;
-          ++got;
-          addr = base + ring + *reinterpret_cast<volatile uint32_t*>(sm + L::kOffs + 4 * slot);
+          const int width = j < m0 ? kHeadDim : it.k;
+          if (width == 32) run(std::integral_constant<int, 2>(), thin_desc, q_kept);
+          else if (width == kHeadDim) run(std::integral_constant<int, 8>(), wide_desc, q_wide);
+          else if (width == 64) run(std::integral_constant<int, 4>(), wide_desc, q_kept);
+          else run(std::integral_constant<int, 6>(), thin_desc, q_kept);
+          mma_commit(base + L::kSFull + 16 * st + 8 * buf);
+          ++hs;
+          leave(cs);
           return true;
         };
-        auto take_k = [&](int j, uint32_t& slot, uint32_t& addr) -> bool {
-          if (!have_kept && j >= m0) {
-            if (!wait(base + L::kQKFull, gathered & 1)) return false;
-            have_kept = true;
-            ++gathered;
-          }
-          return take(slot, addr);
-        };
-        // steps: 16-key groups of the tile that hold keys
-        auto take_v = [&](int j, uint32_t& slot, uint32_t& addr, int& steps) -> bool {
-          if (!take(slot, addr)) return false;
-          steps = kTile / 16;
-          if (j >= m0 && j < m1) return true;
-          const Tile t = tile_at(it, j);
-          steps = (t.rows + 15) / 16;
-          if (!needs_fix(t)) return true;
-          ask(1, make_int4((int)(addr - base), t.rows, steps * 16, 0));
-          return wait(base + L::kFixed, fixed++ & 1);
-        };
-        auto values = [&](int st, uint32_t vt, int steps, bool accumulate) {
-          const uint32_t d = tm_o + st * 128, p = tm_s + st * 128;
-          const uint64_t vd = v_desc | (vt >> 4);
-          if (steps == kTile / 16) {
+        for (int x = 0; ok && x < 2 && cs.x < mine; ++x) ok = scores();
+        bool started = false;
+        while (ok && co.x < mine) {
+          if (co.half == 0) ok = enter(co, 1);
+          const uint32_t buf = ho & 1;
+          ok = ok && wait(base + L::kPFull + 16 * st + 8 * buf, (ho >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tm_o + st * 128, p = tm_s + st * 128 + buf * kHalf;
+          const uint64_t vd = v_desc | ((co.addr >> 4) + co.half * (kHalf * 8));
+          const int left = co.rows - co.half * kHalf;
+          if (left >= kHalf) {
 #pragma unroll
-            for (int y = 0; y < kTile / 16; ++y) mma_ts(d, p + y * 8, vd + y * 128, kDescO, accumulate || y > 0);
+            for (int y = 0; y < kHalf / 16; ++y) mma_ts(d, p + y * 8, vd + y * 128, kDescO, started || y > 0);
           } else {
-            for (int y = 0; y < steps; ++y) mma_ts(d, p + y * 8, vd + y * 128, kDescO, accumulate || y > 0);
+            for (int y = 0; y < (left + 15) / 16; ++y) mma_ts(d, p + y * 8, vd + y * 128, kDescO, started || y > 0);
           }
-          ++nv[st];
-        };
-        auto release = [&](uint32_t slot) { mma_commit(base + L::kEmpty + 8 * slot); };
-        ok = wait(base + L::kQFull, s.idx & 1);
-        if (ok && gather) {
-          const int rows = min(tq, it.ntok) * G, rows2 = kDual && it.ntok > tq ? (it.ntok - tq) * G : 0;
-          ask(0, make_int4(it.h, it.k, rows, rows2));
-          ++asked;
+          started = true;
+          mma_commit(base + L::kOFull + 8 * st);
+          ++ho;
+          leave(co);
+          if (co.x == mine) mma_commit(base + L::kOEnd + 8 * st);
+          // The next scores overwrite the P that this product reads: nothing
+          // orders the two but its end.
+          if (cs.x < mine) ok = wait(base + L::kOFull + 8 * st, (ho - 1) & 1) && scores();
         }
-        uint32_t vslot, kslot, vt, kt;
-        int steps;
-        if (kDual) {
-          ok = ok && take_k(s.t0, kslot, kt);
-          if (ok) {
-            tc_fence_after();
-            for (int st = 0; st < streams; ++st) scores(s.t0, st, kt);
-            release(kslot);
-          }
-          for (int j = s.t0; ok && j < s.t1; ++j) {
-            const bool more = j + 1 < s.t1;
-            ok = take_v(j, vslot, vt, steps) && (!more || take_k(j + 1, kslot, kt));
-            for (int st = 0; ok && st < streams; ++st) {
-              ok = wait(base + L::kPFull + 8 * st, nv[st] & 1);
-              if (!ok) break;
-              tc_fence_after();
-              values(st, vt, steps, j > s.t0);
-              if (st == streams - 1) release(vslot);
-              if (more) {
-                scores(j + 1, st, kt);
-                if (st == streams - 1) release(kslot);
-              } else {
-                mma_commit(base + L::kOFull + 8 * st);
-              }
-            }
-          }
-        } else {
-          for (int j = s.t0; ok && j < min(s.t0 + 2, s.t1); ++j) {
-            ok = take_k(j, kslot, kt);
-            if (!ok) break;
-            tc_fence_after();
-            scores(j, (j - s.t0) & 1, kt);
-            release(kslot);
-          }
-          for (int j = s.t0; ok && j < s.t1; ++j) {
-            const int st = (j - s.t0) & 1;
-            const bool more = j + 2 < s.t1;
-            ok = take_v(j, vslot, vt, steps) && (!more || take_k(j + 2, kslot, kt)) &&
-                 wait(base + L::kPFull + 8 * st, nv[st] & 1);
-            if (!ok) break;
-            tc_fence_after();
-            values(st, vt, steps, j > s.t0 + 1);
-            release(vslot);
-            if (more) {
-              scores(j + 2, st, kt);
-              release(kslot);
-            } else {
-              mma_commit(base + L::kOFull + 8 * st);
-            }
-          }
-        }
+        // (one that no tile of this thread needed must be seen all the same)
+        if (ok && !have_kept) ok = wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
+        taken += 2 * mine;
         if (ok) mma_commit(base + L::kQEmpty);
       }
-      if (gathered != asked) mbar_wait_bounded(base + L::kQKFull, gathered & 1, kDrainNs);
-      ask(0, make_int4(-1, 0, 0, 0));
-      ask(1, make_int4(-1, 0, 0, 0));
       if (!ok) {
-        mma_commit(base + L::kDrain);
-        mbar_wait_bounded(base + L::kDrain, 0, kDrainNs);
+        mma_commit(base + L::kDrain + 8 * st);
+        mbar_wait_bounded(base + L::kDrain + 8 * st, 0, kDrainNs);
       }
     }
-  } else if (warp < 4) {
-    // ------------------------------------------------------- the MMAs' aides
-    // Warp 2 gathers q to the kept channels; warp 3 clears the rows behind the
-    // last key of a tile of values (the MMA takes 16 keys at a time: P is 0
-    // there, but 0 * NaN is not).  The MMA thread asks, and always says when
-    // it is done, so these waits end with its own.
-    const int who = warp - 2;
+  } else if (warp == 3) {
+    // -------------------------------------------------------- the loads' aide
+    // Clears the rows behind the last key of a tile of values (the MMA takes 16
+    // keys at a time: P is 0 there, but 0 * NaN is not), then signals the
+    // tile's slot.  The loading thread always says when it is done, so the
+    // wait for a task ends with that thread's own.
     for (uint32_t n = 0;; ++n) {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(base + L::kAsk + 8 * who, n & 1, kIdleNs))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(base + L::kAsk, n & 1, kIdleNs))) {
         *gone = 1;
         break;
       }
-      const int4 task = *reinterpret_cast<const int4*>(sm + L::kTask + 16 * who);
-      if (task.x < 0) break;
-      if (who == 0) {
-        const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + task.x) * kHeadDim;
-        const int groups = task.y / 8;
-        for (int x = 0; x < L::kQTiles; ++x) {
-          const uint8_t* q = sm + L::kQ + x * kWideBytes;
-          uint8_t* out = sm + L::kQKept + x * w.kept_bytes;
-          const int rows = x == 0 ? task.z : task.w;
-          for (int y = lane; y < rows * groups; y += 32) {
-            const int r = y / groups, c = y - r * groups;
-            const uint4 kc = *reinterpret_cast<const uint4*>(kept + 8 * c);
-            auto at = [&](uint32_t ch) {
-              return (uint32_t)*reinterpret_cast<const uint16_t*>(q + kept_byte(kHeadDim, r, (int)ch >> 3) + (ch & 7) * 2);
-            };
-            auto two = [&](uint32_t p) { return at(p & 0xffffu) | at(p >> 16) << 16; };
-            *reinterpret_cast<uint4*>(out + kept_byte(task.y, r, c)) =
-                make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
-          }
-        }
-      } else {
-        for (int z = lane; z < (task.z - task.y) * 16; z += 32)
-          *reinterpret_cast<uint4*>(sm + task.x + kept_byte(kHeadDim, task.y + z / 16, z % 16)) =
-              make_uint4(0u, 0u, 0u, 0u);
-      }
+      const int4 task = *reinterpret_cast<const int4*>(sm + L::kTask);
+      if (task.x < 0 || !__all_sync(0xffffffffu, mbar_wait_bounded(base + L::kLanded, n & 1, kDrainNs))) break;
+      for (int z = lane; z < (task.z - task.y) * 16; z += 32)
+        *reinterpret_cast<uint4*>(sm + task.x + kept_byte(kHeadDim, task.y + z / 16, z % 16)) =
+            make_uint4(0u, 0u, 0u, 0u);
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(base + (who == 0 ? L::kQKFull : L::kFixed));
+      if (lane == 0) {
+        mbar_arrive(base + L::kFull + 8 * task.w);
+        mbar_arrive(base + L::kCleared);
+      }
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -882,91 +853,128 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t my_s = tm_s + st * 128 + quarter, my_o = tm_o + st * 128 + quarter;
     const int tok = row / G, g = row - tok * G;
-    uint32_t tiles = 0, outs = 0, merges = 0;       // key tiles, outputs and merges of this group
+    uint32_t hs = 0, ends = 0, merges = 0;          // halves, segments and merges this group has done
     Segment s;
     begin(s);
     bool ok = true;
     while (ok && advance(s)) {
       const Item& it = s.it;
-      if (kDual && st == 1 && it.ntok <= tq) continue;
+      const bool idle_group = kDual && st == 1 && it.ntok <= tq;
+      ok = wait.warp(base + L::kQFull, s.idx & 1);
+      if (!ok) break;
+      if (gathers(s) && !idle_group) {
+        // q on the kept channels: each group its query tile's, or both the one's
+        const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + it.h) * kHeadDim;
+        const uint8_t* q = sm + L::kQ + (kDual ? st * kWideBytes : 0);
+        uint8_t* to = sm + L::kQKept + (kDual ? st * w.kept_bytes : 0);
+        const int groups = it.k / 8, rows = min(tq, it.ntok - (kDual ? st * tq : 0)) * G;
+        for (int y = tid - 128 - (kDual ? st * 128 : 0); y < rows * groups; y += kDual ? 128 : 256) {
+          const int r = y / groups, c = y - r * groups;
+          const uint4 kc = *reinterpret_cast<const uint4*>(kept + 8 * c);
+          auto at = [&](uint32_t ch) {
+            return (uint32_t)*reinterpret_cast<const uint16_t*>(q + kept_byte(kHeadDim, r, (int)ch >> 3) + (ch & 7) * 2);
+          };
+          auto two = [&](uint32_t p) { return at(p & 0xffffu) | at(p >> 16) << 16; };
+          *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c)) = make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(base + L::kQKFull + (kDual ? 8 * st : 0));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + L::kQEmpty);
+      if (idle_group) continue;
       const int i = it.i0 + (kDual ? st * tq : 0) + tok;
       const bool mine = tok < tq && i < it.i0 + it.ntok;
       float m = -INFINITY, l = 0.f;
-      int done = 0;                       // key tiles of this segment
+      bool begun = false;                 // a half of this segment is done
       const int m0 = it.nA + it.nC, m1 = m0 + it.mid / kTile;
-      for (int j = s.t0 + (kDual ? 0 : st); j < s.t1; j += kDual ? 1 : 2) {
+      for (int j = s.t0 + (kDual ? 0 : st); ok && j < s.t1; j += kDual ? 1 : 2) {
         uint32_t vis[4] = {};
         bool all = j >= m0 && j < m1;      // whole middle tiles, the common case, are seen by all
+        int halves = 2;
         if (!all) {
-          visible(a, w, it, tile_at(it, j), i, vis);
+          const Tile t = tile_at(it, j);
+          visible(a, w, it, t, i, vis);
           all = __all_sync(0xffffffffu, !mine || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
+          if (t.rows <= kHalf) halves = 1;
         }
-        ok = wait.warp(base + L::kSFull + 8 * st, tiles & 1);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(my_s + 32 * c, x + 32 * c);
-        tmem_wait_ld();
-        if (!all) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if ((vis[c >> 5] >> (c & 31) & 1u) == 0) x[c] = 0xff800000u;
-        }
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-#pragma unroll
-        for (int c = 8; c < 128; c += 2)
-          mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
-        // The maximum moves only when a score exceeds it by 2^8: below that p
-        // stays exact in fp32 and bf16 alike.
-        if (__any_sync(0xffffffffu, top > m + 8.f)) {
-          const float mn = fmaxf(m, top);
-          const float f = m == -INFINITY ? 0.f : ex2(m - mn);
-          m = mn;
-          l *= f;
-          if (done > 0) {
-            // (this tile's scores came after the last tile's P.V)
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32(my_o + 32 * c, o);
-              tmem_wait_ld();
+        for (int half = 0; half < halves; ++half) {
+          const uint32_t buf = hs & 1, at = my_s + buf * kHalf;
+          ok = wait.warp(base + L::kSFull + 16 * st + 8 * buf, (hs >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t x[kHalf];
+          tmem_ld32(at, x);
+          tmem_ld32(at + 32, x + 32);
+          tmem_loaded<kHalf>(x);
+          if (!all) {
+            const uint32_t v0 = half == 0 ? vis[0] : vis[2], v1 = half == 0 ? vis[1] : vis[3];
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_st32(my_o + 32 * c, o);
+            for (int c = 0; c < 32; ++c) {
+              if ((v0 >> c & 1u) == 0) x[c] = 0xff800000u;
+              if ((v1 >> c & 1u) == 0) x[32 + c] = 0xff800000u;
             }
           }
-        }
-        const float off = m == -INFINITY ? 0.f : -m;
-        const uint64_t scale2 = pair(kScaleLog2, kScaleLog2), off2 = pair(off, off);
-        uint64_t sum[4] = {0, 0, 0, 0};
+          float mx[4];
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) {
-          float p0, p1;
-          unpair(fma2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, off2), p0, p1);
-          p0 = ex2(p0);
-          p1 = ex2(p1);
-          sum[c >> 1 & 3] = add2(sum[c >> 1 & 3], pair(p0, p1));
-          x[c >> 1] = pack_bf16x2(p0, p1);
+          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+#pragma unroll
+          for (int c = 8; c < kHalf; c += 2)
+            mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+          // The maximum moves only when a score exceeds it by 2^8: below that p
+          // stays exact in fp32 and bf16 alike.
+          if (__any_sync(0xffffffffu, top > m + 8.f)) {
+            const float mn = fmaxf(m, top);
+            const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+            m = mn;
+            l *= f;
+            if (begun) {
+              // (these scores came after the product before the last one was
+              // done, so its phase is the one before this)
+              ok = wait.warp(base + L::kOFull + 8 * st, (hs - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld32(my_o + 32 * c, o);
+                tmem_loaded<32>(o);
+#pragma unroll
+                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                tmem_st32(my_o + 32 * c, o);
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : -m;
+          const uint64_t scale2 = pair(kScaleLog2, kScaleLog2), off2 = pair(off, off);
+          uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 2) {
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, off2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[c >> 1 & 3] = add2(sum[c >> 1 & 3], pair(p0, p1));
+            x[c >> 1] = pack_bf16x2(p0, p1);
+          }
+          tmem_st32(at, x);
+          float l0, l1;
+          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+          l += l0 + l1;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8 * buf);
+          ++hs;
+          begun = true;
         }
-        float l0, l1;
-        unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
-        l += l0 + l1;
-        tmem_st32(my_s, x);
-        tmem_st32(my_s + 32, x + 32);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(base + L::kPFull + 8 * st);
-        ++tiles;
-        ++done;
       }
       if (!ok) break;
-      if (done > 0) {
-        ok = wait.warp(base + L::kOFull + 8 * st, outs++ & 1);
+      if (begun) {
+        ok = wait.warp(base + L::kOEnd + 8 * st, ends++ & 1);
         if (!ok) break;
         tc_fence_after();
       }
@@ -1008,13 +1016,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         __syncwarp();
         tmem_ld32(my_o + 32 * c, o);
-        tmem_wait_ld();
+        tmem_loaded<32>(o);
         float y[32];
 #pragma unroll
         for (int z = 0; z < 32; ++z) y[z] = __uint_as_float(o[z]) * f0;
         if (two) {
           tmem_ld32(my_o + 128 + 32 * c, o);
-          tmem_wait_ld();
+          tmem_loaded<32>(o);
 #pragma unroll
           for (int z = 0; z < 32; ++z) y[z] = fmaf(__uint_as_float(o[z]), f1, y[z]);
         }
@@ -1044,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_free_all(tmem);
+  if (warp == 3) tmem_free_all(tmem);
 }
 
 // ----------------------------------------------------------------- merge
