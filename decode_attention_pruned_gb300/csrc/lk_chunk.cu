@@ -346,7 +346,8 @@ struct Smem {
                        kSFull = kQKFull + 16, kPFull = kSFull + 32, kOFull = kPFull + 32, kOEnd = kOFull + 16, kMerge = kOEnd + 16,
                        kMerged = kMerge + 8, kAsk = kMerged + 8, kLanded = kAsk + 8, kCleared = kLanded + 8,
                        kDrain = kCleared + 8, kTmem = kDrain + 16, kOffs = kTmem + 16,
-                       kTask = (kOffs + 4 * kSlots * kRings + 15) / 16 * 16;
+                       kInfo = kOffs + 4 * kSlots * kRings,
+                       kTask = (kInfo + 4 * kSlots * kRings + 15) / 16 * 16;
   static constexpr int kQ = 2048;
   static_assert(kTask + 16 <= kQ, "barriers, offsets and tasks");
   static constexpr int kQKept = kQ + kQTiles * kWideBytes;
@@ -357,25 +358,29 @@ struct Smem {
 constexpr uint64_t kDrainNs = 1000000000ull;      // bound of the waits for copies and MMAs still in flight
 constexpr uint64_t kIdleNs = 60000000000ull;      // bound of the aide's wait for a task
 
+// The rest of a wait whose phase was not complete at once (out of line: the
+// waits sit in loops that should stay small).
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit, volatile int* gone, DevHeader* hdr) {
+  const uint64_t t0 = global_timer_ns();
+  while (limit != 0) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*gone) return false;
+    if (global_timer_ns() - t0 > limit) break;
+  }
+  *gone = 1;
+  atomicOr(&hdr->status, (uint32_t)kStatusTimeout);
+  return false;
+}
+
 struct Wait {
   uint64_t limit;
   volatile int* gone;      // set once some wait of the CTA ran out
   DevHeader* hdr;
   // Waits for the phase of `parity`; false once a wait of the CTA ran out.
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    if (limit != 0 && mbar_try_wait(bar, parity)) return true;
-    if (limit == 0 && mbar_test_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (limit != 0) {
-#pragma unroll 1
-      for (int i = 0; i < 16; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-      if (*gone) return false;
-      if (global_timer_ns() - t0 > limit) break;
-    }
-    *gone = 1;
-    atomicOr(&hdr->status, (uint32_t)kStatusTimeout);
-    return false;
+    return mbar_test_wait(bar, parity) || wait_on(bar, parity, limit, gone, hdr);
   }
   // The same for a whole warp, with one answer.
   __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
@@ -625,6 +630,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!reserve(ri, wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * 2 * it.k), at)) return false;
           const uint32_t slot = ri * L::kSlots + rings[ri].put % L::kSlots;
           offs[slot] = at;
+          // what the MMA thread has to know of the tile
+          reinterpret_cast<volatile uint32_t*>(sm + L::kInfo)[slot] =
+              (base + ring + ri * size + at) >> 4 | (uint32_t)t.rows << 16 | (wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
           const uint32_t dst = base + ring + ri * size + at;
           uint32_t bar = base + L::kFull + 8 * slot;
           if (isv && t.type != kTileF && (t.rows & 15) != 0) {
@@ -701,74 +709,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kDescS = mma_desc(128, kHalf, false), kDescO = mma_desc(128, kHeadDim, true);
       const uint64_t wide_desc = smem_desc(0, 16, 1024, kSwizzle128), thin_desc = smem_desc(0, 16, 512, kSwizzle64);
       const uint64_t v_desc = smem_desc(0, kWideBytes / 2, 1024, kSwizzle128);
-      const uint32_t ring_at = base + ring + (kDual ? 0u : st * ((L::kEnd - ring) / L::kRings & ~1023u));
       const uint32_t full = base + L::kFull + (kDual ? 0 : st * 8 * L::kSlots);
       const uint32_t empty = base + L::kEmpty + (kDual ? 0 : st * 8 * L::kSlots);
-      volatile uint32_t* offs = reinterpret_cast<volatile uint32_t*>(sm + L::kOffs) + (kDual ? 0 : st * L::kSlots);
+      volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + (kDual ? 0 : st * L::kSlots);
+      const uint32_t q_wide = (base + L::kQ + (kDual ? st * kWideBytes : 0)) >> 4;       // in 16 bytes
+      const uint32_t q_kept = (base + L::kQKept + (kDual ? st * w.kept_bytes : 0)) >> 4;
+      const uint32_t s_at = tm_s + st * 128, o_at = tm_o + st * 128;
+      const uint32_t s_full = base + L::kSFull + 16 * st, p_full = base + L::kPFull + 16 * st,
+                     o_full = base + L::kOFull + 8 * st;
       uint32_t taken = 0, gathered = 0, hs = 0, ho = 0;   // ring tiles before this segment; halves scored, put out
       Segment s;
       begin(s);
       bool ok = true;
       while (ok && advance(s)) {
-        const Item& it = s.it;
-        const int m0 = it.nA + it.nC, m1 = m0 + it.mid / kTile;
         const bool gather = gathers(s);
         constexpr int kStep = kDual ? 1 : 2;
         const int j0 = s.t0 + (kDual ? 0 : st);
         const int mine = j0 < s.t1 ? (s.t1 - j0 + kStep - 1) / kStep : 0;      // this ring's key tiles
+        const uint32_t end = taken + 2 * mine;
         ok = wait(base + L::kQFull, s.idx & 1);
-        if (kDual && st == 1 && it.ntok <= tq) {
+        if (kDual && st == 1 && s.it.ntok <= tq) {
           // no second query tile: its share of the releases
-          for (int x = 0; ok && x < 2 * mine; ++x) {
-            const uint32_t e = taken + x, slot = e % L::kSlots;
-            ok = wait(full + 8 * slot, (e / L::kSlots) & 1);
-            if (ok) mbar_arrive(empty + 8 * slot);
+          for (uint32_t e = taken; ok && e < end; ++e) {
+            ok = wait(full + 8 * (e % L::kSlots), (e / L::kSlots) & 1);
+            if (ok) mbar_arrive(empty + 8 * (e % L::kSlots));
           }
-          taken += 2 * mine;
+          taken = end;
           if (ok) mbar_arrive(base + L::kQEmpty);
           continue;
         }
         bool have_kept = !gather;
-        const uint32_t q_wide = (base + L::kQ + (kDual ? st * kWideBytes : 0)) >> 4;       // in 16 bytes
-        const uint32_t q_kept = (base + L::kQKept + (kDual ? st * w.kept_bytes : 0)) >> 4;
-        auto rows_at = [&](int j) { return j >= m0 && j < m1 ? kTile : tile_at(it, j).rows; };
-        // cursors of the scores and of the outputs: tile (of mine), half, rows, ring slot, address
+        // tiles of keys and of values: ring entry, half, and what the loads said of it
         struct Cursor {
-          int x, half, rows;
-          uint32_t slot, addr;
-        } cs{0, 0, 0, 0, 0}, co{0, 0, 0, 0, 0};
-        auto enter = [&](Cursor& c, int which) -> bool {
-          const uint32_t e = taken + 2 * c.x + which;
-          c.slot = e % L::kSlots;
-          if (!wait(full + 8 * c.slot, (e / L::kSlots) & 1)) return false;
-          c.addr = ring_at + offs[c.slot];
-          c.rows = rows_at(j0 + c.x * kStep);
+          uint32_t e, half, info;
+        } ck{taken, 0, 0}, cv_{taken + 1, 0, 0};
+        auto enter = [&](Cursor& c) -> bool {
+          const uint32_t slot = c.e % L::kSlots;
+          if (!wait(full + 8 * slot, (c.e / L::kSlots) & 1)) return false;
+          c.info = info[slot];
           return true;
         };
+        // past this half: to the tile's second one, or to the next tile
         auto leave = [&](Cursor& c) {
-          if (c.half == 0 && c.rows > kHalf) {
+          if (c.half == 0 && (c.info >> 16 & 0xff) > kHalf) {
             c.half = 1;
           } else {
-            mma_commit(empty + 8 * c.slot);
+            mma_commit(empty + 8 * (c.e % L::kSlots));
             c.half = 0;
-            ++c.x;
+            c.e += 2;
           }
         };
         auto scores = [&]() -> bool {
-          const int j = j0 + cs.x * kStep;
-          if (cs.half == 0) {
-            if (!have_kept && j >= m0) {
+          if (ck.half == 0) {
+            if (!enter(ck)) return false;
+            if (!have_kept && ck.info >> 24 != 3) {
               if (!wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1)) return false;
               have_kept = true;
             }
-            if (!enter(cs, 0)) return false;
             tc_fence_after();
           }
-          const uint32_t buf = hs & 1, d = tm_s + st * 128 + buf * kHalf;
+          const uint32_t d = s_at + (hs & 1) * kHalf, k0 = ck.info & 0x3fff, width = ck.info >> 24;
           auto run = [&](auto steps, uint64_t desc, uint32_t q) {
             constexpr int kSteps = decltype(steps)::value;
             constexpr bool kThin = kSteps == 2 || kSteps == 6;
-            const uint64_t qd = desc | q, kd = desc | ((cs.addr >> 4) + cs.half * (kHalf * (kThin ? 4 : 8)));
+            const uint64_t qd = desc | q, kd = desc | (k0 + ck.half * (kHalf * (kThin ? 4 : 8)));
             mma_ss<false>(d, qd, kd, kDescS);
 #pragma unroll
             for (int y = 1; y < kSteps; ++y) {
@@ -776,45 +780,43 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_ss<true>(d, qd + at, kd + at, kDescS);
             }
           };
-          const int width = j < m0 ? kHeadDim : it.k;
-          if (width == 32) run(std::integral_constant<int, 2>(), thin_desc, q_kept);
-          else if (width == kHeadDim) run(std::integral_constant<int, 8>(), wide_desc, q_wide);
-          else if (width == 64) run(std::integral_constant<int, 4>(), wide_desc, q_kept);
+          if (width == 0) run(std::integral_constant<int, 2>(), thin_desc, q_kept);
+          else if (width == 3) run(std::integral_constant<int, 8>(), wide_desc, q_wide);
+          else if (width == 1) run(std::integral_constant<int, 4>(), wide_desc, q_kept);
           else run(std::integral_constant<int, 6>(), thin_desc, q_kept);
-          mma_commit(base + L::kSFull + 16 * st + 8 * buf);
+          mma_commit(s_full + 8 * (hs & 1));
           ++hs;
-          leave(cs);
+          leave(ck);
           return true;
         };
-        for (int x = 0; ok && x < 2 && cs.x < mine; ++x) ok = scores();
+        for (int x = 0; ok && x < 2 && ck.e < end; ++x) ok = scores();
         bool started = false;
-        while (ok && co.x < mine) {
-          if (co.half == 0) ok = enter(co, 1);
-          const uint32_t buf = ho & 1;
-          ok = ok && wait(base + L::kPFull + 16 * st + 8 * buf, (ho >> 1) & 1);
+        while (ok && cv_.e < end) {
+          if (cv_.half == 0) ok = enter(cv_);
+          ok = ok && wait(p_full + 8 * (ho & 1), (ho >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d = tm_o + st * 128, p = tm_s + st * 128 + buf * kHalf;
-          const uint64_t vd = v_desc | ((co.addr >> 4) + co.half * (kHalf * 8));
-          const int left = co.rows - co.half * kHalf;
+          const uint32_t p = s_at + (ho & 1) * kHalf;
+          const uint64_t vd = v_desc | ((cv_.info & 0x3fff) + cv_.half * (kHalf * 8));
+          const int left = (int)(cv_.info >> 16 & 0xff) - (int)cv_.half * kHalf;
           if (left >= kHalf) {
 #pragma unroll
-            for (int y = 0; y < kHalf / 16; ++y) mma_ts(d, p + y * 8, vd + y * 128, kDescO, started || y > 0);
+            for (int y = 0; y < kHalf / 16; ++y) mma_ts(o_at, p + y * 8, vd + y * 128, kDescO, started || y > 0);
           } else {
-            for (int y = 0; y < (left + 15) / 16; ++y) mma_ts(d, p + y * 8, vd + y * 128, kDescO, started || y > 0);
+#pragma unroll 1
+            for (int y = 0; y < (left + 15) / 16; ++y) mma_ts(o_at, p + y * 8, vd + y * 128, kDescO, started || y > 0);
           }
           started = true;
-          mma_commit(base + L::kOFull + 8 * st);
+          mma_commit(o_full);
           ++ho;
-          leave(co);
-          if (co.x == mine) mma_commit(base + L::kOEnd + 8 * st);
-          // The next scores overwrite the P that this product reads: nothing
-          // orders the two but its end.
-          if (cs.x < mine) ok = wait(base + L::kOFull + 8 * st, (ho - 1) & 1) && scores();
+          leave(cv_);
+          if (cv_.e >= end) mma_commit(base + L::kOEnd + 8 * st);
+          // (these overwrite the P that the product reads, and run after it)
+          if (ck.e < end) ok = scores();
         }
         // (one that no tile of this thread needed must be seen all the same)
         if (ok && !have_kept) ok = wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
-        taken += 2 * mine;
+        taken = end;
         if (ok) mma_commit(base + L::kQEmpty);
       }
       if (!ok) {
