@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------- attention
-constexpr int kThreads = 384;              // warps: TMA, two for MMA, an aide, two softmax groups of four
+constexpr int kThreads = 384;              // warps: loads, MMA, MMA, loads (of the second ring), two softmax groups of four
 constexpr int kHalf = kTile / 2;           // keys per step of the softmax
 constexpr int kWideBytes = kTile * kHeadDim * 2;
 
@@ -344,19 +344,16 @@ struct Smem {
   static constexpr int kFull = kML + kTile * 8, kEmpty = kFull + 8 * kSlots * kRings,
                        kQFull = kEmpty + 8 * kSlots * kRings, kQEmpty = kQFull + 8, kQKFull = kQEmpty + 8,
                        kSFull = kQKFull + 16, kPFull = kSFull + 32, kOFull = kPFull + 32, kOEnd = kOFull + 16, kMerge = kOEnd + 16,
-                       kMerged = kMerge + 8, kAsk = kMerged + 8, kLanded = kAsk + 8, kCleared = kLanded + 8,
-                       kDrain = kCleared + 8, kTmem = kDrain + 16, kOffs = kTmem + 16,
-                       kInfo = kOffs + 4 * kSlots * kRings,
-                       kTask = (kInfo + 4 * kSlots * kRings + 15) / 16 * 16;
+                       kMerged = kMerge + 8, kDrain = kMerged + 8, kTmem = kDrain + 16, kOffs = kTmem + 16,
+                       kInfo = kOffs + 4 * kSlots * kRings;
   static constexpr int kQ = 2048;
-  static_assert(kTask + 16 <= kQ, "barriers, offsets and tasks");
+  static_assert(kInfo + 4 * kSlots * kRings <= kQ, "barriers and tiles");
   static constexpr int kQKept = kQ + kQTiles * kWideBytes;
   static constexpr int kBytes = 227 * 1024;
   static constexpr int kEnd = kBytes - 1024;             // after aligning the base
 };
 
 constexpr uint64_t kDrainNs = 1000000000ull;      // bound of the waits for copies and MMAs still in flight
-constexpr uint64_t kIdleNs = 60000000000ull;      // bound of the aide's wait for a task
 
 // The rest of a wait whose phase was not complete at once (out of line: the
 // waits sit in loops that should stay small).
@@ -496,9 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(base + L::kMerge, 4);
     mbar_init(base + L::kMerged, 4);
-    mbar_init(base + L::kAsk, 1);
-    mbar_init(base + L::kLanded, 1);
-    mbar_init(base + L::kCleared, 1);
     fence_barrier_init();
     *gone = 0;
   }
@@ -552,55 +546,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   // whether a segment has tiles on the kept channels only
   auto gathers = [&](const Segment& s) { return s.it.k > 0 && s.it.k < kHeadDim && s.t1 > s.it.nA + s.it.nC; };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------- loads
-    if (lane == 0) {
-      // A ring is a FIFO of runs of bytes: the oldest tile in flight starts at
-      // `tail`, the next goes to `head`, or to the ring's start when it does
-      // not fit before the end.
-      const uint32_t size = (L::kEnd - ring) / L::kRings & ~1023u;
-      uint32_t* offs = reinterpret_cast<uint32_t*>(sm + L::kOffs);
-      struct Ring {
-        uint32_t put, freed, head, tail;
-        bool wrapped;
-      } rings[L::kRings] = {};
+    // A thread per ring.  A ring is a FIFO of runs of bytes: the oldest tile in
+    // flight starts at `tail`, the next goes to `head`, or to the ring's start
+    // when it does not fit before the end.
+    const int ri = warp == 0 ? 0 : 1;
+    if (ri < L::kRings && elect_one()) {
+      const uint32_t size = (L::kEnd - ring) / L::kRings & ~1023u, ring_at = base + ring + ri * size;
+      const uint32_t full = base + L::kFull + ri * 8 * L::kSlots, empty = base + L::kEmpty + ri * 8 * L::kSlots;
+      volatile uint32_t* offs = reinterpret_cast<volatile uint32_t*>(sm + L::kOffs) + ri * L::kSlots;
+      volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + ri * L::kSlots;
+      uint32_t put = 0, freed = 0, head = 0, tail = 0;
+      bool wrapped = false;
       // Keys that one query tile reads are read once; those that several read
       // should stay in L2.
       const uint64_t once = l2_policy_evict_first(), keep = w.items_q > 1 ? l2_policy_evict_normal() : once;
-      auto reserve = [&](int ri, uint32_t bytes, uint32_t& at) -> bool {
-        Ring& r = rings[ri];
+      auto reserve = [&](uint32_t bytes, uint32_t& at) -> bool {
         while (true) {
-          if (r.put == r.freed) {
-            r.head = r.tail = 0;
-            r.wrapped = false;
+          if (put == freed) {
+            head = tail = 0;
+            wrapped = false;
           }
-          if (r.put - r.freed < L::kSlots) {
-            if (!r.wrapped && r.head + bytes <= size) break;
-            if (!r.wrapped && bytes <= r.tail) {
-              r.head = 0;
-              r.wrapped = true;
+          if (put - freed < L::kSlots) {
+            if (!wrapped && head + bytes <= size) break;
+            if (!wrapped && bytes <= tail) {
+              head = 0;
+              wrapped = true;
               break;
             }
-            if (r.wrapped && r.head + bytes <= r.tail) break;
+            if (wrapped && head + bytes <= tail) break;
           }
-          if (!wait(base + L::kEmpty + 8 * (ri * L::kSlots + r.freed % L::kSlots), (r.freed / L::kSlots) & 1)) return false;
-          if (++r.freed != r.put) {
-            const uint32_t t = offs[ri * L::kSlots + r.freed % L::kSlots];
-            if (t < r.tail) r.wrapped = false;
-            r.tail = t;
+          if (!wait(empty + 8 * (freed % L::kSlots), (freed / L::kSlots) & 1)) return false;
+          if (++freed != put) {
+            const uint32_t t = offs[freed % L::kSlots];
+            if (t < tail) wrapped = false;
+            tail = t;
           }
         }
-        at = r.head;
-        r.head += bytes;
-        return true;
-      };
-      uint32_t tasks = 0;                 // given to the aide
-      auto ask = [&](int4 task) -> bool {
-        if (tasks > 0 && !wait(base + L::kCleared, (tasks - 1) & 1)) return false;
-        ++tasks;
-        volatile int* t = reinterpret_cast<volatile int*>(sm + L::kTask);
-        t[0] = task.x, t[1] = task.y, t[2] = task.z, t[3] = task.w;
-        mbar_arrive(base + L::kAsk);
+        at = head;
+        head += bytes;
         return true;
       };
       Segment s;
@@ -614,33 +599,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t abase = hd.row_a + (int64_t)it.b * hd.cap_a, bbase = (int64_t)it.b * hd.cap_b;
         const int32_t* pages = cv.max_pages > 0 ? page_row(cv, a.layer, it.b, it.h) : nullptr;
         const int m0 = it.nA + it.nC;
-        if (s.idx > 0) ok = wait(base + L::kQEmpty, (s.idx - 1) & 1);
-        if (!ok) break;
-        const int nq = kDual && it.ntok > tq ? 2 : 1;
-        mbar_arrive_expect_tx(base + L::kQFull, (uint32_t)(nq * w.box_tokens * G * kHeadDim * 2));
-        for (int x = 0; x < nq; ++x)
-          for (int half = 0; half < 2; ++half)
-            tma_load_3d(base + L::kQ + x * kWideBytes + half * (kWideBytes / 2), &maps.q, half * 64, it.h * G,
-                        it.b * a.n_max + it.i0 + x * tq, base + L::kQFull, once);
+        if (ri == 0) {
+          if (s.idx > 0) ok = wait(base + L::kQEmpty, (s.idx - 1) & 1);
+          if (!ok) break;
+          const int nq = kDual && it.ntok > tq ? 2 : 1;
+          mbar_arrive_expect_tx(base + L::kQFull, (uint32_t)(nq * w.box_tokens * G * kHeadDim * 2));
+          for (int x = 0; x < nq; ++x)
+            for (int part = 0; part < 2; ++part)
+              tma_load_3d(base + L::kQ + x * kWideBytes + part * (kWideBytes / 2), &maps.q, part * 64, it.h * G,
+                          it.b * a.n_max + it.i0 + x * tq, base + L::kQFull, once);
+        }
         auto load = [&](int j, bool isv, int32_t pg) -> bool {
           const Tile t = tile_at(it, j);
           const bool wide = isv || t.type <= kTileC || it.k == kHeadDim;
-          const int ri = kDual ? 0 : (j - s.t0) & 1;
           uint32_t at;
-          if (!reserve(ri, wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * 2 * it.k), at)) return false;
-          const uint32_t slot = ri * L::kSlots + rings[ri].put % L::kSlots;
+          if (!reserve(wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * 2 * it.k), at)) return false;
+          const uint32_t slot = put % L::kSlots;
           offs[slot] = at;
-          // what the MMA thread has to know of the tile
-          reinterpret_cast<volatile uint32_t*>(sm + L::kInfo)[slot] =
-              (base + ring + ri * size + at) >> 4 | (uint32_t)t.rows << 16 | (wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
-          const uint32_t dst = base + ring + ri * size + at;
-          uint32_t bar = base + L::kFull + 8 * slot;
-          if (isv && t.type != kTileF && (t.rows & 15) != 0) {
-            // the aide clears what lies behind the last key, then signals the slot
-            if (!ask(make_int4((int)(dst - base), t.rows, (t.rows + 15) & ~15, (int)slot))) return false;
-            bar = base + L::kLanded;
-          }
-          ++rings[ri].put;
+          // what the other threads have to know of the tile
+          info[slot] = (ring_at + at) >> 4 | (uint32_t)t.rows << 16 | (wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
+          const uint32_t dst = ring_at + at, bar = full + 8 * slot;
+          ++put;
           if (t.type == kTileC) {
             mbar_arrive_expect_tx(bar, kWideBytes);
             tma_load_4d(dst, isv ? &maps.v : &maps.k, 0, it.b * a.n_max + t.r0, 0, it.h, bar, keep);
@@ -671,31 +650,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        // page id of the middle tile that key tile j is, if any; read two
-        // tiles before the loads that need it
+        // page id of the middle tile that key tile j is, if any; read a tile
+        // before the loads that need it
         auto page_at = [&](int j) -> int32_t {
           return pages != nullptr && j >= m0 && j < m0 + it.nM ? __ldcg(pages + (j - m0)) : 0;
         };
-        int32_t page = page_at(s.t0), next_page = page_at(s.t0 + 1);
-        for (int j = s.t0; ok && j < s.t1; ++j) {
-          const int32_t after = page_at(j + 2);
+        constexpr int kStep = kDual ? 1 : 2;
+        const int j0 = s.t0 + (kDual ? 0 : ri);
+        int32_t page = page_at(j0);
+        for (int j = j0; ok && j < s.t1; j += kStep) {
+          const int32_t after = page_at(j + kStep);
           ok = load(j, false, page) && load(j, true, page);
-          page = next_page;
-          next_page = after;
+          page = after;
         }
       }
       // copies still in flight must land before the block ends
       if (!ok) {
-        for (int ri = 0; ri < L::kRings; ++ri)
-          for (uint32_t x = rings[ri].freed; x < rings[ri].put; ++x)
-            mbar_wait_bounded(base + L::kFull + 8 * (ri * L::kSlots + x % L::kSlots), (x / L::kSlots) & 1, kDrainNs);
-        if (s.idx >= 0) mbar_wait_bounded(base + L::kQFull, s.idx & 1, kDrainNs);
-        if (tasks > 0) mbar_wait_bounded(base + L::kCleared, (tasks - 1) & 1, kDrainNs);
-        volatile int* t = reinterpret_cast<volatile int*>(sm + L::kTask);
-        t[0] = -1;
-        mbar_arrive(base + L::kAsk);
-      } else if (!ask(make_int4(-1, 0, 0, 0))) {
-        mbar_arrive(base + L::kAsk);
+        for (uint32_t x = freed; x < put; ++x)
+          mbar_wait_bounded(full + 8 * (x % L::kSlots), (x / L::kSlots) & 1, kDrainNs);
+        if (ri == 0 && s.idx >= 0) mbar_wait_bounded(base + L::kQFull, s.idx & 1, kDrainNs);
       }
     }
   } else if (warp < 3) {
@@ -824,29 +797,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(base + L::kDrain + 8 * st, 0, kDrainNs);
       }
     }
-  } else if (warp == 3) {
-    // -------------------------------------------------------- the loads' aide
-    // Clears the rows behind the last key of a tile of values (the MMA takes 16
-    // keys at a time: P is 0 there, but 0 * NaN is not), then signals the
-    // tile's slot.  The loading thread always says when it is done, so the
-    // wait for a task ends with that thread's own.
-    for (uint32_t n = 0;; ++n) {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(base + L::kAsk, n & 1, kIdleNs))) {
-        *gone = 1;
-        break;
-      }
-      const int4 task = *reinterpret_cast<const int4*>(sm + L::kTask);
-      if (task.x < 0 || !__all_sync(0xffffffffu, mbar_wait_bounded(base + L::kLanded, n & 1, kDrainNs))) break;
-      for (int z = lane; z < (task.z - task.y) * 16; z += 32)
-        *reinterpret_cast<uint4*>(sm + task.x + kept_byte(kHeadDim, task.y + z / 16, z % 16)) =
-            make_uint4(0u, 0u, 0u, 0u);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(base + L::kFull + 8 * task.w);
-        mbar_arrive(base + L::kCleared);
-      }
-    }
   } else {
     // ------------------------------------------------------------- softmax
     // A thread owns a row of its group's query tile.
@@ -856,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t my_s = tm_s + st * 128 + quarter, my_o = tm_o + st * 128 + quarter;
     const int tok = row / G, g = row - tok * G;
     uint32_t hs = 0, ends = 0, merges = 0;          // halves, segments and merges this group has done
+    uint32_t entries = 0;                 // ring tiles before this segment
     Segment s;
     begin(s);
     bool ok = true;
@@ -885,7 +836,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(base + L::kQEmpty);
-      if (idle_group) continue;
+      const uint32_t end = entries + 2 * (kDual ? s.t1 - s.t0 : (s.t1 - s.t0 - st + 1) / 2);
+      if (idle_group) {
+        entries = end;
+        continue;
+      }
       const int i = it.i0 + (kDual ? st * tq : 0) + tok;
       const bool mine = tok < tq && i < it.i0 + it.ntok;
       float m = -INFINITY, l = 0.f;
@@ -894,12 +849,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = s.t0 + (kDual ? 0 : st); ok && j < s.t1; j += kDual ? 1 : 2) {
         uint32_t vis[4] = {};
         bool all = j >= m0 && j < m1;      // whole middle tiles, the common case, are seen by all
-        int halves = 2;
+        int halves = 2, rows = kTile;
         if (!all) {
           const Tile t = tile_at(it, j);
           visible(a, w, it, t, i, vis);
           all = __all_sync(0xffffffffu, !mine || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
           if (t.rows <= kHalf) halves = 1;
+          if (t.type != kTileF) rows = t.rows;
+        }
+        if ((rows & 15) != 0) {
+          // The MMA takes 16 keys at a time: what lies behind the last one is
+          // cleared, as P is 0 there but 0 * NaN is not.  (F tiles end in zeros.)
+          const uint32_t e = entries + 2 * ((j - s.t0) / (kDual ? 1 : 2)) + 1;
+          const uint32_t slot = e % L::kSlots + (kDual ? 0 : st * L::kSlots);
+          ok = wait.warp(base + L::kFull + 8 * slot, (e / L::kSlots) & 1);
+          if (!ok) break;
+          const uint32_t at = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo)[slot] & 0x3fff;
+          const int lo = rows, hi = (rows + 15) & ~15;
+          for (int z = row; z < (hi - lo) * 16; z += kTile)
+            *reinterpret_cast<uint4*>(sm + (16 * at - base) + kept_byte(kHeadDim, lo + z / 16, z % 16)) =
+                make_uint4(0u, 0u, 0u, 0u);
+          fence_async_smem();
         }
 #pragma unroll 1
         for (int half = 0; half < halves; ++half) {
@@ -974,6 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           begun = true;
         }
       }
+      entries = end;
       if (!ok) break;
       if (begun) {
         ok = wait.warp(base + L::kOEnd + 8 * st, ends++ & 1);
