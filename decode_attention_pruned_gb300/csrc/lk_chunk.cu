@@ -340,14 +340,15 @@ struct Smem {
   static constexpr int kQTiles = kDual ? 2 : 1;
   static constexpr int kRings = kDual ? 1 : 2;           // one that both groups read, or one for each
   static constexpr int kSlots = 16;                      // tiles in flight per ring at most
-  static constexpr int kML = 0;                          // second group's (m, l)
-  static constexpr int kFull = kML + kTile * 8, kEmpty = kFull + 8 * kSlots * kRings,
+  static constexpr int kFull = 0, kEmpty = kFull + 8 * kSlots * kRings,
                        kQFull = kEmpty + 8 * kSlots * kRings, kQEmpty = kQFull + 8, kQKFull = kQEmpty + 8,
                        kSFull = kQKFull + 16, kPFull = kSFull + 32, kOFull = kPFull + 32, kOEnd = kOFull + 16, kMerge = kOEnd + 16,
                        kMerged = kMerge + 8, kDrain = kMerged + 8, kTmem = kDrain + 16, kOffs = kTmem + 16,
-                       kInfo = kOffs + 4 * kSlots * kRings;
-  static constexpr int kQ = 2048;
-  static_assert(kInfo + 4 * kSlots * kRings <= kQ, "barriers and tiles");
+                       kInfo = kOffs + 4 * kSlots * kRings, kSeg = kInfo + 4 * kSlots * kRings;
+  static constexpr int kSegBytes = 128;                  // two segments
+  static constexpr int kML = 2048;                       // second group's (m, l)
+  static constexpr int kQ = kDual ? 2048 : 4096;         // 1024-byte aligned
+  static_assert(kSeg + 2 * kSegBytes <= kQ, "barriers, tiles and segments");
   static constexpr int kQKept = kQ + kQTiles * kWideBytes;
   static constexpr int kBytes = 227 * 1024;
   static constexpr int kEnd = kBytes - 1024;             // after aligning the base
@@ -518,16 +519,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Wait wait{a.wait_limit_ns, gone, cv.hdr};
   const int G = cv.G, tq = w.tile_tokens;
 
-  // Segments: the CTA's tiles of one item.  Every role walks them alike.
+  // Segments: the CTA's tiles of one item.  The loading threads find them; the
+  // first one leaves each in shared memory for the other roles, which learn of
+  // it with the segment's q.
   struct Segment {
     int e, t0, t1, nt, idx;
-    bool whole, next;
+    bool whole;
     Item it;
   };
+  static_assert(sizeof(Segment) <= L::kSegBytes, "segment slot");
   auto begin = [&](Segment& s) {
     s.e = first.x - 1;
     s.idx = -1;
-    s.next = true;
   };
   auto advance = [&](Segment& s) -> bool {
     while (true) {
@@ -542,6 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++s.idx;
       return true;
     }
+  };
+  // the segment of number idx, once its q is there; its t1 is 0 after the last
+  auto segment = [&](int idx) -> const Segment& {
+    return *reinterpret_cast<const Segment*>(sm + L::kSeg + (idx & 1) * L::kSegBytes);
   };
   // whether a segment has tiles on the kept channels only
   auto gathers = [&](const Segment& s) { return s.it.k > 0 && s.it.k < kHeadDim && s.t1 > s.it.nA + s.it.nC; };
@@ -603,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (s.idx > 0) ok = wait(base + L::kQEmpty, (s.idx - 1) & 1);
           if (!ok) break;
           const int nq = kDual && it.ntok > tq ? 2 : 1;
+          *reinterpret_cast<Segment*>(sm + L::kSeg + (s.idx & 1) * L::kSegBytes) = s;
           mbar_arrive_expect_tx(base + L::kQFull, (uint32_t)(nq * w.box_tokens * G * kHeadDim * 2));
           for (int x = 0; x < nq; ++x)
             for (int part = 0; part < 2; ++part)
@@ -664,6 +672,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           page = after;
         }
       }
+      if (ok && ri == 0 && (s.idx < 0 || wait(base + L::kQEmpty, s.idx & 1))) {
+        reinterpret_cast<Segment*>(sm + L::kSeg + ((s.idx + 1) & 1) * L::kSegBytes)->t1 = 0;
+        mbar_arrive(base + L::kQFull);
+      }
       // copies still in flight must land before the block ends
       if (!ok) {
         for (uint32_t x = freed; x < put; ++x)
@@ -691,24 +703,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t s_full = base + L::kSFull + 16 * st, p_full = base + L::kPFull + 16 * st,
                      o_full = base + L::kOFull + 8 * st;
       uint32_t taken = 0, gathered = 0, hs = 0, ho = 0;   // ring tiles before this segment; halves scored, put out
-      Segment s;
-      begin(s);
       bool ok = true;
-      while (ok && advance(s)) {
+      for (int idx = 0; ok; ++idx) {
+        ok = wait(base + L::kQFull, idx & 1);
+        const Segment& s = segment(idx);
+        if (!ok || s.t1 == 0) break;
         const bool gather = gathers(s);
         constexpr int kStep = kDual ? 1 : 2;
         const int j0 = s.t0 + (kDual ? 0 : st);
         const int mine = j0 < s.t1 ? (s.t1 - j0 + kStep - 1) / kStep : 0;      // this ring's key tiles
         const uint32_t end = taken + 2 * mine;
-        ok = wait(base + L::kQFull, s.idx & 1);
         if (kDual && st == 1 && s.it.ntok <= tq) {
           // no second query tile: its share of the releases
+          mbar_arrive(base + L::kQEmpty);
           for (uint32_t e = taken; ok && e < end; ++e) {
             ok = wait(full + 8 * (e % L::kSlots), (e / L::kSlots) & 1);
             if (ok) mbar_arrive(empty + 8 * (e % L::kSlots));
           }
           taken = end;
-          if (ok) mbar_arrive(base + L::kQEmpty);
           continue;
         }
         bool have_kept = !gather;
@@ -762,7 +774,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           leave(ck);
           return true;
         };
+        // all scores are issued: q can go once they are done (and the gathered q
+        // must have been seen even if none of these tiles needed it)
+        auto q_read = [&]() {
+          if (!have_kept) ok = wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
+          if (ok) mma_commit(base + L::kQEmpty);
+        };
         for (int x = 0; ok && x < 2 && ck.e < end; ++x) ok = scores();
+        if (ok && ck.e >= end) q_read();
         bool started = false;
         while (ok && cv_.e < end) {
           if (cv_.half == 0) ok = enter(cv_);
@@ -785,12 +804,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           leave(cv_);
           if (cv_.e >= end) mma_commit(base + L::kOEnd + 8 * st);
           // (these overwrite the P that the product reads, and run after it)
-          if (ck.e < end) ok = scores();
+          if (ck.e < end) {
+            ok = scores();
+            if (ok && ck.e >= end) q_read();
+          }
         }
-        // (one that no tile of this thread needed must be seen all the same)
-        if (ok && !have_kept) ok = wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
         taken = end;
-        if (ok) mma_commit(base + L::kQEmpty);
       }
       if (!ok) {
         mma_commit(base + L::kDrain + 8 * st);
@@ -807,14 +826,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = row / G, g = row - tok * G;
     uint32_t hs = 0, ends = 0, merges = 0;          // halves, segments and merges this group has done
     uint32_t entries = 0;                 // ring tiles before this segment
-    Segment s;
-    begin(s);
     bool ok = true;
-    while (ok && advance(s)) {
+    for (int idx = 0; ok; ++idx) {
+      ok = wait.warp(base + L::kQFull, idx & 1);
+      if (!ok) break;
+      const Segment s = segment(idx);
+      if (s.t1 == 0) break;
       const Item& it = s.it;
       const bool idle_group = kDual && st == 1 && it.ntok <= tq;
-      ok = wait.warp(base + L::kQFull, s.idx & 1);
-      if (!ok) break;
       if (gathers(s) && !idle_group) {
         // q on the kept channels: each group its query tile's, or both the one's
         const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + it.h) * kHeadDim;
@@ -845,10 +864,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = tok < tq && i < it.i0 + it.ntok;
       float m = -INFINITY, l = 0.f;
       bool begun = false;                 // a half of this segment is done
-      const int m0 = it.nA + it.nC, m1 = m0 + it.mid / kTile;
+      const int m0 = it.nA + it.nC, m1 = m0 + it.mid / kTile, f0 = m0 + it.nM;
+      const int i_first = it.i0 + (kDual ? st * tq : 0), i_last = min(i_first + tq, it.i0 + it.ntok) - 1;
+      const int f1 = f0 + max(0, it.N + i_first - it.win + 1 - it.far0) / kTile;
       for (int j = s.t0 + (kDual ? 0 : st); ok && j < s.t1; j += kDual ? 1 : 2) {
         uint32_t vis[4] = {};
-        bool all = j >= m0 && j < m1;      // whole middle tiles, the common case, are seen by all
+        // tiles that every query of the group sees whole, the common case
+        bool all = j >= m0 && j < m1;
+        if (j >= f0) {
+          all = j < f1;
+        } else if (j >= it.nA && j < m0) {
+          const int r0 = tile_at(it, j).r0;
+          all = r0 + kTile - 1 <= i_first && i_last - r0 < it.win && it.policy != kSpecial;
+        }
         int halves = 2, rows = kTile;
         if (!all) {
           const Tile t = tile_at(it, j);
@@ -951,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      float f0 = 1.f, f1 = 0.f;
+      float w0 = 1.f, w1 = 0.f;
       bool two = false;
       if (!kDual) {
         // the second group hands its (m, l) over; the first merges both outputs
@@ -972,15 +1000,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const float2 other = ml[row];
           const float mn = fmaxf(m, other.x);
-          f0 = m == -INFINITY ? 0.f : ex2(m - mn);
-          f1 = other.x == -INFINITY ? 0.f : ex2(other.x - mn);
+          w0 = m == -INFINITY ? 0.f : ex2(m - mn);
+          w1 = other.x == -INFINITY ? 0.f : ex2(other.x - mn);
           m = mn;
-          l = l * f0 + other.y * f1;
+          l = l * w0 + other.y * w1;
         }
       }
       const float inv = s.whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-      f0 *= inv;
-      f1 *= inv;
+      w0 *= inv;
+      w1 *= inv;
       const int slot = 2 * cta + (s.t0 == 0 ? 1 : 0);
       const int64_t prow = (int64_t)slot * w.part_rows + (kDual ? st * kTile : 0) + row;
       uint16_t* out = a.o + (((int64_t)it.b * a.n_max + i) * cv.Hq + it.h * G + g) * kHeadDim;
@@ -992,12 +1020,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_loaded<32>(o);
         float y[32];
 #pragma unroll
-        for (int z = 0; z < 32; ++z) y[z] = __uint_as_float(o[z]) * f0;
+        for (int z = 0; z < 32; ++z) y[z] = __uint_as_float(o[z]) * w0;
         if (two) {
           tmem_ld32(my_o + 128 + 32 * c, o);
           tmem_loaded<32>(o);
 #pragma unroll
-          for (int z = 0; z < 32; ++z) y[z] = fmaf(__uint_as_float(o[z]), f1, y[z]);
+          for (int z = 0; z < 32; ++z) y[z] = fmaf(__uint_as_float(o[z]), w1, y[z]);
         }
         if (!mine) continue;
         if (s.whole) {
