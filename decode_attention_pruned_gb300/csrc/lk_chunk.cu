@@ -686,32 +686,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 3) {
     // -------------------------------------------------------------- MMAs
     // A thread for each softmax group issues its scores S = Q K^T and outputs
-    // O += P V, half a key tile (64 keys) at a time: the scores of one half are
-    // made while the group works on the half before.  What the thread does per
-    // half is kept short, as the tensor core waits for it.
+    // O += P V, half a key tile (64 keys) at a time: while the group works on
+    // one half, the other half's scores are made.  All instructions of the CTA
+    // come through one small cache, and this loop's from behind the group's, so
+    // that it costs what it is long: the loads leave each tile's address, rows
+    // and width as one word, and the halves are written out.
     const int st = warp - 1;
     if (elect_one()) {
       constexpr uint32_t kDescS = mma_desc(128, kHalf, false), kDescO = mma_desc(128, kHeadDim, true);
-      const uint64_t wide_desc = smem_desc(0, 16, 1024, kSwizzle128), thin_desc = smem_desc(0, 16, 512, kSwizzle64);
-      const uint64_t v_desc = smem_desc(0, kWideBytes / 2, 1024, kSwizzle128);
+      constexpr uint32_t kWideHi = desc_hi(1024, kSwizzle128), kThinHi = desc_hi(512, kSwizzle64);
       const uint32_t full = base + L::kFull + (kDual ? 0 : st * 8 * L::kSlots);
       const uint32_t empty = base + L::kEmpty + (kDual ? 0 : st * 8 * L::kSlots);
       volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + (kDual ? 0 : st * L::kSlots);
-      const uint32_t q_wide = (base + L::kQ + (kDual ? st * kWideBytes : 0)) >> 4;       // in 16 bytes
-      const uint32_t q_kept = (base + L::kQKept + (kDual ? st * w.kept_bytes : 0)) >> 4;
+      const uint32_t q_wide = desc_lo(16) | (base + L::kQ + (kDual ? st * kWideBytes : 0)) >> 4;
+      const uint32_t q_kept = desc_lo(16) | (base + L::kQKept + (kDual ? st * w.kept_bytes : 0)) >> 4;
       const uint32_t s_at = tm_s + st * 128, o_at = tm_o + st * 128;
       const uint32_t s_full = base + L::kSFull + 16 * st, p_full = base + L::kPFull + 16 * st,
                      o_full = base + L::kOFull + 8 * st;
-      uint32_t taken = 0, gathered = 0, hs = 0, ho = 0;   // ring tiles before this segment; halves scored, put out
+      uint32_t taken = 0, gathered = 0, phase = 0;   // ring tiles before this segment; of the P barriers
       bool ok = true;
       for (int idx = 0; ok; ++idx) {
         ok = wait(base + L::kQFull, idx & 1);
         const Segment& s = segment(idx);
         if (!ok || s.t1 == 0) break;
-        const bool gather = gathers(s);
-        constexpr int kStep = kDual ? 1 : 2;
-        const int j0 = s.t0 + (kDual ? 0 : st);
-        const int mine = j0 < s.t1 ? (s.t1 - j0 + kStep - 1) / kStep : 0;      // this ring's key tiles
+        // this ring's key tiles
+        const int mine = kDual ? s.t1 - s.t0 : (s.t1 - s.t0 - st + 1) / 2;
         const uint32_t end = taken + 2 * mine;
         if (kDual && st == 1 && s.it.ntok <= tq) {
           // no second query tile: its share of the releases
@@ -723,92 +722,98 @@ __global__ void __launch_bounds__(kThreads, 1)
           taken = end;
           continue;
         }
-        bool have_kept = !gather;
-        // tiles of keys and of values: ring entry, half, and what the loads said of it
-        struct Cursor {
-          uint32_t e, half, info;
-        } ck{taken, 0, 0}, cv_{taken + 1, 0, 0};
-        auto enter = [&](Cursor& c) -> bool {
-          const uint32_t slot = c.e % L::kSlots;
-          if (!wait(full + 8 * slot, (c.e / L::kSlots) & 1)) return false;
-          c.info = info[slot];
+        bool have_kept = !gathers(s);
+        auto enter = [&](uint32_t e, uint32_t& what) -> bool {
+          const uint32_t slot = e % L::kSlots;
+          if (!wait(full + 8 * slot, (e / L::kSlots) & 1)) return false;
+          what = info[slot];
           return true;
         };
-        // past this half: to the tile's second one, or to the next tile
-        auto leave = [&](Cursor& c) {
-          if (c.half == 0 && (c.info >> 16 & 0xff) > kHalf) {
-            c.half = 1;
-          } else {
-            mma_commit(empty + 8 * (c.e % L::kSlots));
-            c.half = 0;
-            c.e += 2;
+        auto enter_k = [&](uint32_t e, uint32_t& what) -> bool {
+          if (!enter(e, what)) return false;
+          if (!have_kept && what >> 24 != 3) {
+            have_kept = true;
+            return wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
           }
+          return true;
         };
-        auto scores = [&]() -> bool {
-          if (ck.half == 0) {
-            if (!enter(ck)) return false;
-            if (!have_kept && ck.info >> 24 != 3) {
-              if (!wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1)) return false;
-              have_kept = true;
-            }
-            tc_fence_after();
-          }
-          const uint32_t d = s_at + (hs & 1) * kHalf, k0 = ck.info & 0x3fff, width = ck.info >> 24;
-          auto run = [&](auto steps, uint64_t desc, uint32_t q) {
+        auto scores = [&](uint32_t what, auto which) {
+          constexpr int kWhich = decltype(which)::value;
+          const uint32_t d = s_at + kWhich * kHalf, k0 = desc_lo(16) | (what & 0x3fff), width = what >> 24;
+          auto run = [&](auto steps, uint32_t q) {
             constexpr int kSteps = decltype(steps)::value;
             constexpr bool kThin = kSteps == 2 || kSteps == 6;
-            const uint64_t qd = desc | q, kd = desc | (k0 + ck.half * (kHalf * (kThin ? 4 : 8)));
-            mma_ss<false>(d, qd, kd, kDescS);
+            constexpr uint32_t kHi = kThin ? kThinHi : kWideHi;
+            const uint32_t k = k0 + kWhich * kHalf * (kThin ? 4 : 8);
+            mma_ss<kHi, false>(d, q, k, kDescS);
 #pragma unroll
             for (int y = 1; y < kSteps; ++y) {
               const uint32_t at = kThin ? (y >> 1) * (kTile * 4) + (y & 1) * 2 : (y >> 2) * (kTile * 8) + (y & 3) * 2;
-              mma_ss<true>(d, qd + at, kd + at, kDescS);
+              mma_ss<kHi, true>(d, q + at, k + at, kDescS);
             }
           };
-          if (width == 0) run(std::integral_constant<int, 2>(), thin_desc, q_kept);
-          else if (width == 3) run(std::integral_constant<int, 8>(), wide_desc, q_wide);
-          else if (width == 1) run(std::integral_constant<int, 4>(), wide_desc, q_kept);
-          else run(std::integral_constant<int, 6>(), thin_desc, q_kept);
-          mma_commit(s_full + 8 * (hs & 1));
-          ++hs;
-          leave(ck);
-          return true;
+          if (width == 0) run(std::integral_constant<int, 2>(), q_kept);
+          else if (width == 3) run(std::integral_constant<int, 8>(), q_wide);
+          else if (width == 1) run(std::integral_constant<int, 4>(), q_kept);
+          else run(std::integral_constant<int, 6>(), q_kept);
+          mma_commit(s_full + 8 * kWhich);
         };
+        auto values = [&](uint32_t what, auto which, bool accumulate) {
+          constexpr int kWhich = decltype(which)::value;
+          const uint32_t p = s_at + kWhich * kHalf;
+          const uint32_t v = (desc_lo(kWideBytes / 2) | (what & 0x3fff)) + kWhich * kHalf * 8;
+          const int left = (int)(what >> 16 & 0xff) - kWhich * kHalf;
+          if (left >= kHalf) {
+#pragma unroll
+            for (int y = 0; y < kHalf / 16; ++y)
+              mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, kDescO, accumulate || y > 0);
+          } else {
+#pragma unroll 1
+            for (int y = 0; y < (left + 15) / 16; ++y)
+              mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, kDescO, accumulate || y > 0);
+          }
+          mma_commit(o_full);
+        };
+        const std::integral_constant<int, 0> h0;
+        const std::integral_constant<int, 1> h1;
         // all scores are issued: q can go once they are done (and the gathered q
         // must have been seen even if none of these tiles needed it)
         auto q_read = [&]() {
           if (!have_kept) ok = wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
           if (ok) mma_commit(base + L::kQEmpty);
         };
-        for (int x = 0; ok && x < 2 && ck.e < end; ++x) ok = scores();
-        if (ok && ck.e >= end) q_read();
-        bool started = false;
-        while (ok && cv_.e < end) {
-          if (cv_.half == 0) ok = enter(cv_);
-          ok = ok && wait(p_full + 8 * (ho & 1), (ho >> 1) & 1);
+        uint32_t k = 0, v = 0;
+        if (mine > 0) {
+          ok = enter_k(taken, k);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t p = s_at + (ho & 1) * kHalf;
-          const uint64_t vd = v_desc | ((cv_.info & 0x3fff) + cv_.half * (kHalf * 8));
-          const int left = (int)(cv_.info >> 16 & 0xff) - (int)cv_.half * kHalf;
-          if (left >= kHalf) {
-#pragma unroll
-            for (int y = 0; y < kHalf / 16; ++y) mma_ts(o_at, p + y * 8, vd + y * 128, kDescO, started || y > 0);
-          } else {
-#pragma unroll 1
-            for (int y = 0; y < (left + 15) / 16; ++y) mma_ts(o_at, p + y * 8, vd + y * 128, kDescO, started || y > 0);
-          }
-          started = true;
-          mma_commit(o_full);
-          ++ho;
-          leave(cv_);
-          if (cv_.e >= end) mma_commit(base + L::kOEnd + 8 * st);
-          // (these overwrite the P that the product reads, and run after it)
-          if (ck.e < end) {
-            ok = scores();
-            if (ok && ck.e >= end) q_read();
-          }
+          scores(k, h0);
+          scores(k, h1);
+          mma_commit(empty + 8 * (taken % L::kSlots));
         }
+        if (mine <= 1) q_read();
+        for (uint32_t e = taken; ok && e < end; e += 2) {
+          const bool more = e + 2 < end;
+          ok = enter(e + 1, v) && (!more || enter_k(e + 2, k)) && wait(p_full, phase);
+          if (!ok) break;
+          tc_fence_after();
+          values(v, h0, e != taken);
+          // (scores overwrite the P that the product before them reads, and run
+          // after it)
+          if (more) scores(k, h0);
+          ok = wait(p_full + 8, phase);
+          if (!ok) break;
+          tc_fence_after();
+          values(v, h1, true);
+          mma_commit(empty + 8 * ((e + 1) % L::kSlots));
+          if (more) {
+            scores(k, h1);
+            mma_commit(empty + 8 * ((e + 2) % L::kSlots));
+            if (e + 4 >= end) q_read();
+          }
+          phase ^= 1;
+        }
+        if (ok && mine > 0) mma_commit(base + L::kOEnd + 8 * st);
         taken = end;
       }
       if (!ok) {
@@ -882,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Tile t = tile_at(it, j);
           visible(a, w, it, t, i, vis);
           all = __all_sync(0xffffffffu, !mine || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
-          if (t.rows <= kHalf) halves = 1;
+          if (t.rows <= kHalf) halves = 1;      // no key in the second half
           if (t.type != kTileF) rows = t.rows;
         }
         if ((rows & 15) != 0) {
@@ -900,11 +905,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
         }
 #pragma unroll 1
-        for (int half = 0; half < halves; ++half) {
-          const uint32_t buf = hs & 1, at = my_s + buf * kHalf;
-          ok = wait.warp(base + L::kSFull + 16 * st + 8 * buf, (hs >> 1) & 1);
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t at = my_s + half * kHalf;
+          ok = wait.warp(base + L::kSFull + 16 * st + 8 * half, (hs >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
+          if (half == halves) {
+            if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8);
+            ++hs;
+            break;
+          }
           uint32_t x[kHalf];
           tmem_ld32(at, x);
           tmem_ld32(at + 32, x + 32);
@@ -967,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8 * buf);
+          if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8 * half);
           ++hs;
           begun = true;
         }

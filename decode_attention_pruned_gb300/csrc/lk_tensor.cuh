@@ -71,16 +71,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 }
 
 // -------------------------------------------------------------- descriptors
-// Shared-memory operand: address, the byte strides between core-matrix groups
-// (leading, stride), and the swizzle (2: 128-byte rows, 4: 64-byte rows).
+// Shared-memory operand, a 64-bit word: in the lower half the address and
+// `leading`, in the upper one `stride` (the byte strides between core-matrix
+// groups) and the swizzle (2: 128-byte rows, 4: 64-byte rows).
 //   K-major   rows of the operand are runs of K; `stride` between groups of 8
 //             rows, `leading` unused.
 //   MN-major  64-element runs of M or N; `leading` between those runs,
 //             `stride` between groups of 8 K.
+// Within one operand only the address moves: it is kept in units of 16 bytes
+// in the lower half, and the upper half is a constant.
 constexpr uint32_t kSwizzle128 = 2, kSwizzle64 = 4;
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading, uint32_t stride, uint32_t swizzle) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)swizzle << 61;
+__host__ __device__ constexpr uint32_t desc_lo(uint32_t leading) { return (leading >> 4) << 16; }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t stride, uint32_t swizzle) {
+  return stride >> 4 | 1u << 14 | swizzle << 29;
 }
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N, B K-major or MN-major.
 __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn_major) {
@@ -91,19 +94,21 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn_major) {
 // D (tensor memory) = A B (+ D): A from shared memory, or from tensor memory
 // (bf16 pairs packed two to a column).  One thread issues; the operations of
 // a thread run in the order it issues them.
-template <bool kAccumulate>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc) {
+template <uint32_t kHi, bool kAccumulate>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t desc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "n"(kAccumulate ? 1 : 0)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(desc), "n"(kAccumulate ? 1 : 0), "n"(kHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool accumulate) {
+template <uint32_t kHi>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t desc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(desc), "r"((uint32_t)accumulate), "n"(kHi)
       : "memory");
 }
 // True in one thread of a converged warp.
