@@ -1379,7 +1379,6 @@ lk_status chunk_attn_run(lk_cache cache, const lk_chunk* c, ChunkArgs& a, ChunkW
                          const char* what, cudaStream_t s) {
   const int special = w.special_seqs;
   cudaError_t err = chunk_groups(cache, c, a, [&](const ChunkArgs& g) {
-    if (kv_quantized(cache->lay.kv_format)) return launch_chunk_simple(g, s);
     w.special_seqs = special > 0 ? g.nb : 0;
     return launch_chunk_attn(maps, g, w, s);
   });

@@ -60,7 +60,8 @@ struct Item {
   int sinks;             // t < sinks: near
   int rows_a, nA;        // region-A rows the item looks at, and tiles
   int cs, c0, nC;        // chunk tiles 0 .. cs - 1, then c0 ..; nC in all
-  int mid, nM;           // middle rows and tiles
+  int mid, nM;           // middle rows and tiles (INT8 / FP8: the first nS of them sealed blocks)
+  int nS;
   int far0, rows_f, nF;  // position of F row 0, F rows the item looks at, tiles
 };
 
@@ -124,6 +125,7 @@ __device__ __forceinline__ bool item_info(const ChunkArgs& a, const ChunkWork& w
   it.cs = N < it.sinks ? min((it.sinks - N + kTile - 1) / kTile, it.c0) : 0;
   it.nC = it.cs + (it.i0 + it.ntok - 1) / kTile - it.c0 + 1;
   it.nM = (it.mid + kTile - 1) / kTile;
+  it.nS = kv_quantized(cv.kv_format) ? it.mid / kQBlockRows : 0;
   it.nF = (it.rows_f + kTile - 1) / kTile;
   return true;
 }
@@ -323,7 +325,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------- attention
-constexpr int kThreads = 384;              // warps: loads, MMA, MMA, loads (of the second ring), two softmax groups of four
+// warps: loads, MMA, MMA, loads (of the second ring), two softmax groups of
+// four, and where the cache has sealed blocks four that turn them into tiles
+constexpr int kThreads = 384, kThreadsQ = 512;
 constexpr int kHalf = kTile / 2;           // keys per step of the softmax
 constexpr int kWideBytes = kTile * kHeadDim * 2;
 
@@ -335,8 +339,9 @@ constexpr int kWideBytes = kTile * kHeadDim * 2;
 // through in order, each taking what it needs (a key tile on 32 channels 8 KB,
 // full-width ones and values 32 KB), so that narrow heads have the more tiles
 // in flight.
-template <bool kDual>
+template <bool kDual, int kFmt>
 struct Smem {
+  static constexpr bool kQuant = kFmt != kKvBf16;
   static constexpr int kQTiles = kDual ? 2 : 1;
   static constexpr int kRings = kDual ? 1 : 2;           // one that both groups read, or one for each
   static constexpr int kSlots = 16;                      // tiles in flight per ring at most
@@ -344,21 +349,27 @@ struct Smem {
                        kQFull = kEmpty + 8 * kSlots * kRings, kQEmpty = kQFull + 8, kQKFull = kQEmpty + 8,
                        kSFull = kQKFull + 16, kPFull = kSFull + 32, kOFull = kPFull + 32, kOEnd = kOFull + 16, kMerge = kOEnd + 16,
                        kMerged = kMerge + 8, kDrain = kMerged + 8, kTmem = kDrain + 16, kOffs = kTmem + 16,
-                       kInfo = kOffs + 4 * kSlots * kRings, kSeg = kInfo + 4 * kSlots * kRings;
+                       kInfo = kOffs + 4 * kSlots * kRings, kSeg = kInfo + 4 * kSlots * kRings, kAsk = kSeg + 256, kDone = kAsk + 16 * kRings,
+                       kJob = kDone + 16 * kRings;
   static constexpr int kSegBytes = 128;                  // two segments
   static constexpr int kML = 2048;                       // second group's (m, l)
-  static constexpr int kQ = kDual ? 2048 : 4096;         // 1024-byte aligned
-  static_assert(kSeg + 2 * kSegBytes <= kQ, "barriers, tiles and segments");
+  static constexpr int kVScale = kML + (kDual ? 0 : kTile * 8);          // of the tiles in flight, four per ring
+  static constexpr int kQ = (kVScale + (kQuant ? kRings * 4 * kTile * 4 : 0) + 1023) / 1024 * 1024;
+  static constexpr int kJobBytes = 32;                   // two jobs per ring
+  static constexpr int kMakers = kDual ? 4 : 2;          // warps that make a ring's tiles out of sealed blocks
+  static constexpr int kArrivals = kQuant ? kMakers : 1; // that complete a tile
+  static_assert(kJob + 2 * kJobBytes * kRings <= 2048 && kSegBytes == 128, "barriers, tiles, segments and jobs");
   static constexpr int kQKept = kQ + kQTiles * kWideBytes;
   static constexpr int kBytes = 227 * 1024;
   static constexpr int kEnd = kBytes - 1024;             // after aligning the base
 };
 
+constexpr uint64_t kIdleNs = 60000000000ull;      // bound of the makers' wait for a job
 constexpr uint64_t kDrainNs = 1000000000ull;      // bound of the waits for copies and MMAs still in flight
 
 // The rest of a wait whose phase was not complete at once (out of line: the
 // waits sit in loops that should stay small).
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit, volatile int* gone, DevHeader* hdr) {
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit, volatile int* gone, DevHeader* hdr) {
   const uint64_t t0 = global_timer_ns();
   while (limit != 0) {
 #pragma unroll 1
@@ -463,10 +474,31 @@ __device__ __forceinline__ void visible(const ChunkArgs& a, const ChunkWork& w, 
   }
 }
 
-template <bool kDual>
-__global__ void __launch_bounds__(kThreads, 1)
+// The keys or the values of a sealed block, to be turned into a tile.  (Not
+// both at once: the ring may have room for the values only when the tile
+// before them is used up, and that needs the keys.)
+struct Job {
+  const uint8_t* block;
+  int32_t k;                             // kept channels; 0: no more jobs
+  int32_t values;                        // keys: -1; values: where their scales go
+  uint32_t slot, at;                     // ring slot, offset in shared memory
+};
+static_assert(sizeof(Job) <= 32, "job slot");
+
+// Eight codes of a 16-byte group of a sealed block, as exact f16 pairs: the
+// even bytes of words w0 .. w3 (channels 0 .. 7), or the odd ones (8 .. 15).
+// V codes of INT8 blocks are offset binary.
+template <int kFmt, bool kV>
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& even, uint32_t& odd) {
+  if (kFmt == kKvFp8) e4m3x4_to_f16x2(w, even, odd);
+  else i8x4_to_f16x2(kV ? w ^ 0x80808080u : w, even, odd);
+}
+
+template <bool kDual, int kFmt>
+__global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
     chunk_attn_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a, const ChunkWork w) {
-  using L = Smem<kDual>;
+  using L = Smem<kDual, kFmt>;
+  constexpr bool kQuant = L::kQuant;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -477,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* gone = reinterpret_cast<volatile int*>(sm + L::kTmem + 8);
   if (tid == 0) {
     for (int i = 0; i < L::kSlots * L::kRings; ++i) {
-      mbar_init(base + L::kFull + 8 * i, 1);
+      mbar_init(base + L::kFull + 8 * i, L::kArrivals);
       mbar_init(base + L::kEmpty + 8 * i, kDual ? 2 : 1);
     }
     mbar_init(base + L::kQFull, 1);
@@ -492,6 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(base + L::kOEnd + 8 * s, 1);
       mbar_init(base + L::kDrain + 8 * s, 1);
     }
+    for (int i = 0; kQuant && i < 2 * L::kRings; ++i) {
+      mbar_init(base + L::kAsk + 8 * i, 1);
+      mbar_init(base + L::kDone + 8 * i, L::kMakers);
+    }
     mbar_init(base + L::kMerge, 4);
     mbar_init(base + L::kMerged, 4);
     fence_barrier_init();
@@ -499,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t ring = L::kQKept + L::kQTiles * w.kept_bytes;       // offsets from base
   // rows of the query tiles that no load writes stay zero
-  for (int x = L::kQ / 16 + tid; x < (int)ring / 16; x += kThreads)
+  for (int x = L::kQ / 16 + tid; x < (int)ring / 16; x += blockDim.x)
     reinterpret_cast<uint4*>(sm)[x] = make_uint4(0u, 0u, 0u, 0u);
   fence_async_smem();
   if (warp == 0 && lane < 3 + kNumPools) tma_prefetch_map(&maps.q + lane);
@@ -553,6 +589,110 @@ __global__ void __launch_bounds__(kThreads, 1)
   // whether a segment has tiles on the kept channels only
   auto gathers = [&](const Segment& s) { return s.it.k > 0 && s.it.k < kHeadDim && s.t1 > s.it.nA + s.it.nC; };
 
+  if (kQuant && warp >= 12) {
+    // ----------------------------------------------------------- the makers
+    // Turn sealed blocks into bf16 tiles: keys as code times scale, rounded
+    // once; values as their codes, which bf16 holds exactly (the weights take
+    // their scales).  All loads of a thread's share are issued before the
+    // first is used.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    constexpr int kMade = 32 * L::kMakers;                // threads per ring
+    const int ri = kDual ? 0 : (warp - 12) >> 1, mt = (tid - 384) % kMade;
+    for (uint32_t n = 0;; ++n) {
+      bool ok = false;
+      for (const uint64_t t0 = global_timer_ns(); !ok && global_timer_ns() - t0 < kIdleNs && *gone == 0;)
+        ok = mbar_wait_bounded(base + L::kAsk + 16 * ri + 8 * (n & 1), (n >> 1) & 1, 1000000);
+      if (!__all_sync(0xffffffffu, ok)) {
+        *gone = 1;
+        break;
+      }
+      const Job job = *reinterpret_cast<const Job*>(sm + L::kJob + (2 * ri + (n & 1)) * L::kJobBytes);
+      const int k = job.k, groups = k / 16;
+      if (k == 0) break;
+      const uint4* codes = reinterpret_cast<const uint4*>(job.block);
+      if (job.values < 0) {
+        // a thread keeps to one 16-channel group, whose scales it holds
+        const int lanes = kMade / groups * groups;        // (6 groups: not all threads)
+        if (mt < lanes) {
+          const int c = mt % groups;
+          const float* sc = reinterpret_cast<const float*>(job.block + qblock_ksoff(k)) + 16 * c;
+          float scale[16];
+#pragma unroll
+          for (int x = 0; x < 16; x += 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(sc + x));
+            scale[x] = f.x, scale[x + 1] = f.y, scale[x + 2] = f.z, scale[x + 3] = f.w;
+          }
+          uint8_t* to = sm + job.at;
+          const int step = lanes / groups;
+#pragma unroll 1
+          for (int r0 = mt / groups; r0 < kTile; r0 += 4 * step) {
+            uint4 u[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int r = min(r0 + y * step, kTile - 1);
+              u[y] = __ldcg(codes + r * groups + (c ^ qswz(k, r)));
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int r = r0 + y * step;
+              if (r >= kTile) break;
+              const uint32_t in[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
+              uint32_t lo[4], hi[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                uint32_t e, o;
+                codes_f16<kFmt, false>(in[x], e, o);
+                lo[x] = pack_bf16x2(f16_lo(e) * scale[2 * x], f16_hi(e) * scale[2 * x + 1]);
+                hi[x] = pack_bf16x2(f16_lo(o) * scale[8 + 2 * x], f16_hi(o) * scale[9 + 2 * x]);
+              }
+              *reinterpret_cast<uint4*>(to + kept_byte(k, r, 2 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              *reinterpret_cast<uint4*>(to + kept_byte(k, r, 2 * c + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            }
+          }
+        }
+      } else {
+        constexpr int kPart = 4, kParts = kTile * 8 / kMade / kPart;    // 4 groups at a time, the next 4 on their way
+        float* vs = reinterpret_cast<float*>(sm + L::kVScale) + (4 * ri + job.values) * kTile;
+        const uint4* from = codes + kTile * groups + mt;
+        uint4 v[kPart];
+#pragma unroll
+        for (int x = 0; x < kPart; ++x) v[x] = __ldcg(from + x * kMade);
+        for (int x = mt; x < kTile; x += kMade) vs[x] = __ldcg(reinterpret_cast<const float*>(job.block + qblock_vsoff(k)) + x);
+#pragma unroll 1
+        for (int part = 0; part < kParts; ++part) {
+          uint4 next[kPart];
+          from += part + 1 < kParts ? kPart * kMade : 0;
+#pragma unroll
+          for (int x = 0; x < kPart; ++x) next[x] = __ldcg(from + x * kMade);
+#pragma unroll
+          for (int x = 0; x < kPart; ++x) {
+            const int y = (part * kPart + x) * kMade + mt, r = y >> 3, c = (y & 7) ^ qswz(kHeadDim, r);
+            const uint32_t in[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              uint32_t e, o;
+              codes_f16<kFmt, true>(in[z], e, o);
+              lo[z] = pack_bf16x2(f16_lo(e), f16_hi(e));
+              hi[z] = pack_bf16x2(f16_lo(o), f16_hi(o));
+            }
+            uint8_t* to = sm + job.at;
+            *reinterpret_cast<uint4*>(to + kept_byte(kHeadDim, r, 2 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(to + kept_byte(kHeadDim, r, 2 * c + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          }
+#pragma unroll
+          for (int x = 0; x < kPart; ++x) v[x] = next[x];
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(base + L::kFull + 8 * (ri * L::kSlots + job.slot));
+        mbar_arrive(base + L::kDone + 16 * ri + 8 * (n & 1));
+      }
+    }
+  } else if (warp < 4) {
+  if (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------- loads
     // A thread per ring.  A ring is a FIFO of runs of bytes: the oldest tile in
@@ -564,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t full = base + L::kFull + ri * 8 * L::kSlots, empty = base + L::kEmpty + ri * 8 * L::kSlots;
       volatile uint32_t* offs = reinterpret_cast<volatile uint32_t*>(sm + L::kOffs) + ri * L::kSlots;
       volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + ri * L::kSlots;
-      uint32_t put = 0, freed = 0, head = 0, tail = 0;
+      uint32_t put = 0, freed = 0, head = 0, tail = 0, jobs = 0, sealed = 0;
       bool wrapped = false;
       // Keys that one query tile reads are read once; those that several read
       // should stay in L2.
@@ -617,6 +757,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(base + L::kQ + x * kWideBytes + part * (kWideBytes / 2), &maps.q, part * 64, it.h * G,
                           it.b * a.n_max + it.i0 + x * tq, base + L::kQFull, once);
         }
+        // first of the arrivals that complete a tile's slot, and the others
+        auto expect = [&](uint32_t bar, uint32_t bytes) {
+          if (L::kArrivals > 1) mbar_arrive_many(bar, L::kArrivals - 1);
+          mbar_arrive_expect_tx(bar, bytes);
+        };
         auto load = [&](int j, bool isv, int32_t pg) -> bool {
           const Tile t = tile_at(it, j);
           const bool wide = isv || t.type <= kTileC || it.k == kHeadDim;
@@ -628,19 +773,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           info[slot] = (ring_at + at) >> 4 | (uint32_t)t.rows << 16 | (wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
           const uint32_t dst = ring_at + at, bar = full + 8 * slot;
           ++put;
+          if (kQuant && t.type == kTileM && t.r0 < it.nS * kTile) {
+            // two jobs at most wait for the makers
+            if (jobs >= 2 && !wait(base + L::kDone + 16 * ri + 8 * (jobs & 1), ((jobs >> 1) - 1) & 1)) return false;
+            const int64_t block = hd.qoff + (pages != nullptr ? (int64_t)max(0, pg)
+                                                              : (int64_t)it.b * hd.qblocks + t.r0 / kTile) *
+                                                qblock_bytes(it.k);
+            *reinterpret_cast<Job*>(sm + L::kJob + (2 * ri + (jobs & 1)) * L::kJobBytes) =
+                Job{cv.qpool + block, it.k, isv ? (int)(sealed++ & 3) : -1, slot, dst - base};
+            mbar_arrive(base + L::kAsk + 16 * ri + 8 * (jobs & 1));
+            ++jobs;
+            return true;
+          }
           if (t.type == kTileC) {
-            mbar_arrive_expect_tx(bar, kWideBytes);
+            expect(bar, kWideBytes);
             tma_load_4d(dst, isv ? &maps.v : &maps.k, 0, it.b * a.n_max + t.r0, 0, it.h, bar, keep);
           } else if (t.type == kTileA) {
-            mbar_arrive_expect_tx(bar, kWideBytes);
+            expect(bar, kWideBytes);
             tma_load_3d(dst, &maps.pool[isv ? kPoolV : kPoolK128], 0, (int)(abase + t.r0), 0, bar, keep);
           } else if (t.type == kTileM) {
-            const int64_t r = pages != nullptr ? (int64_t)max(0, pg) * kPageRows : bbase + t.r0;
+            const int64_t r = !kQuant && pages != nullptr ? (int64_t)max(0, pg) * kPageRows : bbase + t.r0 - (kQuant ? it.nS * kTile : 0);
             if (isv) {
-              mbar_arrive_expect_tx(bar, kWideBytes);
+              expect(bar, kWideBytes);
               tma_load_3d(dst, &maps.pool[kPoolV], 0, (int)(vrow_b + r), 0, bar, keep);
             } else {
-              mbar_arrive_expect_tx(bar, (uint32_t)(kTile * 2 * it.k));
+              expect(bar, (uint32_t)(kTile * 2 * it.k));
               if (it.k == 32 || it.k == 64) tma_load_2d(dst, &maps.pool[kb], 0, (int)(krow_b + r), bar, keep);
               else tma_load_3d(dst, &maps.pool[kb], 0, (int)(krow_b + r), 0, bar, keep);
             }
@@ -652,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t row = (width & 63) == 0 ? 128u : 64u;
             const int runs = width * 2 / (int)row;
             if (isv) image += kTile * 2 * it.k;
-            mbar_arrive_expect_tx(bar, rows * row * runs);
+            expect(bar, rows * row * runs);
             for (int x = 0; x < runs; ++x)
               bulk_load(dst + x * kTile * row, image + x * kTile * row, rows * row, bar, keep);
           }
@@ -661,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // page id of the middle tile that key tile j is, if any; read a tile
         // before the loads that need it
         auto page_at = [&](int j) -> int32_t {
-          return pages != nullptr && j >= m0 && j < m0 + it.nM ? __ldcg(pages + (j - m0)) : 0;
+          return pages != nullptr && j >= m0 && j < m0 + (kQuant ? it.nS : it.nM) ? __ldcg(pages + (j - m0)) : 0;
         };
         constexpr int kStep = kDual ? 1 : 2;
         const int j0 = s.t0 + (kDual ? 0 : ri);
@@ -671,6 +828,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = load(j, false, page) && load(j, true, page);
           page = after;
         }
+      }
+      if (kQuant) {
+        // the makers' last job: none (once the one before the last is done)
+        if (jobs >= 2) mbar_wait_bounded(base + L::kDone + 16 * ri + 8 * (jobs & 1), ((jobs >> 1) - 1) & 1, kDrainNs);
+        reinterpret_cast<Job*>(sm + L::kJob + (2 * ri + (jobs & 1)) * L::kJobBytes)->k = 0;
+        mbar_arrive(base + L::kAsk + 16 * ri + 8 * (jobs & 1));
       }
       if (ok && ri == 0 && (s.idx < 0 || wait(base + L::kQEmpty, s.idx & 1))) {
         reinterpret_cast<Segment*>(sm + L::kSeg + ((s.idx + 1) & 1) * L::kSegBytes)->t1 = 0;
@@ -821,7 +984,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(base + L::kDrain + 8 * st, 0, kDrainNs);
       }
     }
+  }
   } else {
+    // (registers: 256 x 88 + 256 x 168 = 65536 of the 512 x 128 launched with)
+    if (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ------------------------------------------------------------- softmax
     // A thread owns a row of its group's query tile.
     const int st = (warp - 4) >> 2;
@@ -831,6 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = row / G, g = row - tok * G;
     uint32_t hs = 0, ends = 0, merges = 0;          // halves, segments and merges this group has done
     uint32_t entries = 0;                 // ring tiles before this segment
+    uint32_t sealed = 0;                  // tiles made of sealed blocks so far
     bool ok = true;
     for (int idx = 0; ok; ++idx) {
       ok = wait.warp(base + L::kQFull, idx & 1);
@@ -862,6 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(base + L::kQEmpty);
       const uint32_t end = entries + 2 * (kDual ? s.t1 - s.t0 : (s.t1 - s.t0 - st + 1) / 2);
       if (idle_group) {
+        if (kQuant) sealed += max(0, min(s.t1, it.nA + it.nC + it.nS) - max(s.t0, it.nA + it.nC));
         entries = end;
         continue;
       }
@@ -903,6 +1071,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(sm + (16 * at - base) + kept_byte(kHeadDim, lo + z / 16, z % 16)) =
                 make_uint4(0u, 0u, 0u, 0u);
           fence_async_smem();
+        }
+        // a sealed block's values are codes: their scales, once they are there
+        const float* vscale = nullptr;
+        if (kQuant && j >= m0 && j < m0 + it.nS) {
+          const uint32_t e = entries + 2 * ((j - s.t0) / (kDual ? 1 : 2)) + 1;
+          const uint32_t slot = e % L::kSlots + (kDual ? 0 : st * L::kSlots);
+          ok = wait.warp(base + L::kFull + 8 * slot, (e / L::kSlots) & 1);
+          if (!ok) break;
+          vscale = reinterpret_cast<const float*>(sm + L::kVScale) + ((kDual ? 0 : 4 * st) + (sealed++ & 3)) * kTile;
         }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -968,7 +1145,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             p0 = ex2(p0);
             p1 = ex2(p1);
             sum[c >> 1 & 3] = add2(sum[c >> 1 & 3], pair(p0, p1));
-            x[c >> 1] = pack_bf16x2(p0, p1);
+            if (kQuant) {
+              x[c] = __float_as_uint(p0);
+              x[c + 1] = __float_as_uint(p1);
+            } else {
+              x[c >> 1] = pack_bf16x2(p0, p1);
+            }
+          }
+          if (kQuant) {
+            if (vscale != nullptr) {
+              const float4* f = reinterpret_cast<const float4*>(vscale + half * kHalf);
+#pragma unroll
+              for (int c = 0; c < kHalf; c += 4) {
+                const float4 y = f[c / 4];
+                x[c] = __float_as_uint(__uint_as_float(x[c]) * y.x);
+                x[c + 1] = __float_as_uint(__uint_as_float(x[c + 1]) * y.y);
+                x[c + 2] = __float_as_uint(__uint_as_float(x[c + 2]) * y.z);
+                x[c + 3] = __float_as_uint(__uint_as_float(x[c + 3]) * y.w);
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 2) x[c >> 1] = pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
           }
           tmem_st32(at, x);
           float l0, l1;
@@ -1151,13 +1348,18 @@ cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, int sm
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <bool kDual>
+template <bool kDual, int kFmt>
 cudaError_t launch_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& w, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t err = set_smem_limit_once(chunk_attn_kernel<kDual>, Smem<kDual>::kBytes, done);
+  constexpr int kBytes = Smem<kDual, kFmt>::kBytes;
+  cudaError_t err = set_smem_limit_once(chunk_attn_kernel<kDual, kFmt>, kBytes, done);
   if (err != cudaSuccess) return err;
-  return launch_after(chunk_attn_kernel<kDual>, dim3((unsigned)w.max_ctas), kThreads, Smem<kDual>::kBytes, stream, maps,
-                      args, w);
+  return launch_after(chunk_attn_kernel<kDual, kFmt>, dim3((unsigned)w.max_ctas),
+                      kFmt == kKvBf16 ? kThreads : kThreadsQ, kBytes, stream, maps, args, w);
+}
+template <int kFmt>
+cudaError_t launch_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& w, cudaStream_t stream) {
+  return w.dual ? launch_attn<true, kFmt>(maps, args, w, stream) : launch_attn<false, kFmt>(maps, args, w, stream);
 }
 
 }  // namespace
@@ -1166,7 +1368,9 @@ cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, cons
   const unsigned plan_blocks = 1u + w.special_seqs + (unsigned)(args.nb * args.cv.Hkv) * w.far_tiles;
   cudaError_t err = launch_after(chunk_plan_kernel, dim3(plan_blocks), kPlanThreads, 0, stream, args, w);
   if (err != cudaSuccess) return err;
-  err = w.dual ? launch_attn<true>(maps, args, w, stream) : launch_attn<false>(maps, args, w, stream);
+  err = args.cv.kv_format == kKvInt8  ? launch_attn<kKvInt8>(maps, args, w, stream)
+        : args.cv.kv_format == kKvFp8 ? launch_attn<kKvFp8>(maps, args, w, stream)
+                                      : launch_attn<kKvBf16>(maps, args, w, stream);
   if (err != cudaSuccess || w.max_ctas < 2) return err;
   const dim3 grid((unsigned)w.max_ctas - 1, (unsigned)(w.part_rows + kMergeRows - 1) / kMergeRows);
   return launch_after(chunk_merge_kernel, grid, 32 * kMergeRows, 0, stream, args, w);

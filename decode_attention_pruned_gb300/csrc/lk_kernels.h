@@ -176,7 +176,6 @@ cudaError_t launch_build_masks(const float* alpha, const uint8_t* eligible, int 
 
 cudaError_t launch_chunk_append(const ChunkArgs& args, bool has_middle, int num_sms, cudaStream_t stream);
 cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& work, cudaStream_t stream);
-cudaError_t launch_chunk_simple(const ChunkArgs& args, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs& args, cudaStream_t stream);
 
 }  // namespace lk

@@ -13,6 +13,11 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
   return pol;
 }
 
+// `count` arrivals at once.
+__device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
 // ------------------------------------------------------------ tensor memory
 // All of an SM's tensor memory (128 lanes x 512 columns of 32 bits); the
 // address lands in shared memory.  One whole warp allocates and frees.
