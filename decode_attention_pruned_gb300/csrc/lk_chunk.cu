@@ -342,6 +342,7 @@ constexpr int kWideBytes = kTile * kHeadDim * 2;
 template <bool kDual, int kFmt>
 struct Smem {
   static constexpr bool kQuant = kFmt != kKvBf16;
+  static constexpr int kJobs = 4;                        // sealed blocks' halves on their way per ring
   static constexpr int kQTiles = kDual ? 2 : 1;
   static constexpr int kRings = kDual ? 1 : 2;           // one that both groups read, or one for each
   static constexpr int kSlots = 16;                      // tiles in flight per ring at most
@@ -349,16 +350,17 @@ struct Smem {
                        kQFull = kEmpty + 8 * kSlots * kRings, kQEmpty = kQFull + 8, kQKFull = kQEmpty + 8,
                        kSFull = kQKFull + 16, kPFull = kSFull + 32, kOFull = kPFull + 32, kOEnd = kOFull + 16, kMerge = kOEnd + 16,
                        kMerged = kMerge + 8, kDrain = kMerged + 8, kTmem = kDrain + 16, kOffs = kTmem + 16,
-                       kInfo = kOffs + 4 * kSlots * kRings, kSeg = kInfo + 4 * kSlots * kRings, kAsk = kSeg + 256, kDone = kAsk + 16 * kRings,
-                       kJob = kDone + 16 * kRings;
+                       kInfo = kOffs + 4 * kSlots * kRings, kSeg = kInfo + 4 * kSlots * kRings, kLanded = kSeg + 256, kDone = kLanded + 8 * kJobs * kRings,
+                       kJob = kDone + 8 * kJobs * kRings;
   static constexpr int kSegBytes = 128;                  // two segments
   static constexpr int kML = 2048;                       // second group's (m, l)
   static constexpr int kVScale = kML + (kDual ? 0 : kTile * 8);          // of the tiles in flight, four per ring
-  static constexpr int kQ = (kVScale + (kQuant ? kRings * 4 * kTile * 4 : 0) + 1023) / 1024 * 1024;
-  static constexpr int kJobBytes = 32;                   // two jobs per ring
+  static constexpr int kKScale = kVScale + (kQuant ? kRings * 4 * kTile * 4 : 0);       // of the jobs
+  static constexpr int kQ = (kKScale + (kQuant ? kRings * kJobs * kTile * 4 : 0) + 1023) / 1024 * 1024;
+  static constexpr int kJobBytes = 32;
   static constexpr int kMakers = kDual ? 4 : 2;          // warps that make a ring's tiles out of sealed blocks
   static constexpr int kArrivals = kQuant ? kMakers : 1; // that complete a tile
-  static_assert(kJob + 2 * kJobBytes * kRings <= 2048 && kSegBytes == 128, "barriers, tiles, segments and jobs");
+  static_assert(kJob + kJobBytes * kJobs * kRings <= 2048 && kSegBytes == 128, "barriers, tiles, segments and jobs");
   static constexpr int kQKept = kQ + kQTiles * kWideBytes;
   static constexpr int kBytes = 227 * 1024;
   static constexpr int kEnd = kBytes - 1024;             // after aligning the base
@@ -478,10 +480,9 @@ __device__ __forceinline__ void visible(const ChunkArgs& a, const ChunkWork& w, 
 // both at once: the ring may have room for the values only when the tile
 // before them is used up, and that needs the keys.)
 struct Job {
-  const uint8_t* block;
-  int32_t k;                             // kept channels; 0: no more jobs
-  int32_t values;                        // keys: -1; values: where their scales go
-  uint32_t slot, at;                     // ring slot, offset in shared memory
+  int32_t width;                         // channels; 0: no more jobs
+  int32_t values;                        // 0: keys, 1: values
+  uint32_t slot, at, scales;             // ring slot; offsets in shared memory
 };
 static_assert(sizeof(Job) <= 32, "job slot");
 
@@ -524,8 +525,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       mbar_init(base + L::kOEnd + 8 * s, 1);
       mbar_init(base + L::kDrain + 8 * s, 1);
     }
-    for (int i = 0; kQuant && i < 2 * L::kRings; ++i) {
-      mbar_init(base + L::kAsk + 8 * i, 1);
+    for (int i = 0; kQuant && i < L::kJobs * L::kRings; ++i) {
+      mbar_init(base + L::kLanded + 8 * i, 1);
       mbar_init(base + L::kDone + 8 * i, L::kMakers);
     }
     mbar_init(base + L::kMerge, 4);
@@ -593,102 +594,75 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
     // ----------------------------------------------------------- the makers
     // Turn sealed blocks into bf16 tiles: keys as code times scale, rounded
     // once; values as their codes, which bf16 holds exactly (the weights take
-    // their scales).  All loads of a thread's share are issued before the
-    // first is used.
+    // their scales).  The codes of a 128-channel row lie where the row's second
+    // half will: eight lanes read the row, then write it.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     constexpr int kMade = 32 * L::kMakers;                // threads per ring
     const int ri = kDual ? 0 : (warp - 12) >> 1, mt = (tid - 384) % kMade;
     for (uint32_t n = 0;; ++n) {
+      const uint32_t jn = ri * L::kJobs + n % L::kJobs, phase = (n / L::kJobs) & 1;
       bool ok = false;
       for (const uint64_t t0 = global_timer_ns(); !ok && global_timer_ns() - t0 < kIdleNs && *gone == 0;)
-        ok = mbar_wait_bounded(base + L::kAsk + 16 * ri + 8 * (n & 1), (n >> 1) & 1, 1000000);
+        ok = mbar_wait_bounded(base + L::kLanded + 8 * jn, phase, 1000000);
       if (!__all_sync(0xffffffffu, ok)) {
         *gone = 1;
         break;
       }
-      const Job job = *reinterpret_cast<const Job*>(sm + L::kJob + (2 * ri + (n & 1)) * L::kJobBytes);
-      const int k = job.k, groups = k / 16;
-      if (k == 0) break;
-      const uint4* codes = reinterpret_cast<const uint4*>(job.block);
-      if (job.values < 0) {
-        // a thread keeps to one 16-channel group, whose scales it holds
-        const int lanes = kMade / groups * groups;        // (6 groups: not all threads)
-        if (mt < lanes) {
-          const int c = mt % groups;
-          const float* sc = reinterpret_cast<const float*>(job.block + qblock_ksoff(k)) + 16 * c;
-          float scale[16];
+      const Job job = *reinterpret_cast<const Job*>(sm + L::kJob + jn * L::kJobBytes);
+      if (job.width == 0) break;
+      const int groups = job.width / 16;
+      // a thread keeps to one 16-channel group (of 6 groups not all threads have
+      // one); its rows are r0, r0 + step, ...
+      const int lanes = kMade / groups * groups, step = lanes / groups;
+      const int c = mt % groups, r0 = mt < lanes ? mt / groups : kTile;
+      uint8_t* to = sm + job.at;
+      const uint4* codes =
+          reinterpret_cast<const uint4*>(to + kTile * job.width * (job.width == kHeadDim ? 1 : 2));
+      auto convert = [&](auto values) {
+        constexpr bool kV = decltype(values)::value;
+        float scale[kV ? 1 : 16];
+        if (!kV) {
 #pragma unroll
           for (int x = 0; x < 16; x += 4) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(sc + x));
+            const float4 f = *reinterpret_cast<const float4*>(sm + job.scales + 4 * (16 * c + x));
             scale[x] = f.x, scale[x + 1] = f.y, scale[x + 2] = f.z, scale[x + 3] = f.w;
           }
-          uint8_t* to = sm + job.at;
-          const int step = lanes / groups;
-#pragma unroll 1
-          for (int r0 = mt / groups; r0 < kTile; r0 += 4 * step) {
-            uint4 u[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int r = min(r0 + y * step, kTile - 1);
-              u[y] = __ldcg(codes + r * groups + (c ^ qswz(k, r)));
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int r = r0 + y * step;
-              if (r >= kTile) break;
-              const uint32_t in[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
-              uint32_t lo[4], hi[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                uint32_t e, o;
-                codes_f16<kFmt, false>(in[x], e, o);
-                lo[x] = pack_bf16x2(f16_lo(e) * scale[2 * x], f16_hi(e) * scale[2 * x + 1]);
-                hi[x] = pack_bf16x2(f16_lo(o) * scale[8 + 2 * x], f16_hi(o) * scale[9 + 2 * x]);
-              }
-              *reinterpret_cast<uint4*>(to + kept_byte(k, r, 2 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              *reinterpret_cast<uint4*>(to + kept_byte(k, r, 2 * c + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            }
-          }
         }
-      } else {
-        constexpr int kPart = 4, kParts = kTile * 8 / kMade / kPart;    // 4 groups at a time, the next 4 on their way
-        float* vs = reinterpret_cast<float*>(sm + L::kVScale) + (4 * ri + job.values) * kTile;
-        const uint4* from = codes + kTile * groups + mt;
-        uint4 v[kPart];
-#pragma unroll
-        for (int x = 0; x < kPart; ++x) v[x] = __ldcg(from + x * kMade);
-        for (int x = mt; x < kTile; x += kMade) vs[x] = __ldcg(reinterpret_cast<const float*>(job.block + qblock_vsoff(k)) + x);
 #pragma unroll 1
-        for (int part = 0; part < kParts; ++part) {
-          uint4 next[kPart];
-          from += part + 1 < kParts ? kPart * kMade : 0;
+        for (int rb = 0; rb < kTile; rb += 2 * step) {
+          uint4 u[2];
 #pragma unroll
-          for (int x = 0; x < kPart; ++x) next[x] = __ldcg(from + x * kMade);
+          for (int y = 0; y < 2; ++y) {
+            const int r = min(rb + r0 + y * step, kTile - 1);
+            u[y] = codes[r * groups + (c ^ qswz(job.width, r))];
+          }
+          __syncwarp();
 #pragma unroll
-          for (int x = 0; x < kPart; ++x) {
-            const int y = (part * kPart + x) * kMade + mt, r = y >> 3, c = (y & 7) ^ qswz(kHeadDim, r);
-            const uint32_t in[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+          for (int y = 0; y < 2; ++y) {
+            const int r = rb + r0 + y * step;
+            const uint32_t in[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
             uint32_t lo[4], hi[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
+            for (int x = 0; x < 4; ++x) {
               uint32_t e, o;
-              codes_f16<kFmt, true>(in[z], e, o);
-              lo[z] = pack_bf16x2(f16_lo(e), f16_hi(e));
-              hi[z] = pack_bf16x2(f16_lo(o), f16_hi(o));
+              codes_f16<kFmt, kV>(in[x], e, o);
+              lo[x] = pack_bf16x2(f16_lo(e) * (kV ? 1.f : scale[2 * x]), f16_hi(e) * (kV ? 1.f : scale[2 * x + 1]));
+              hi[x] = pack_bf16x2(f16_lo(o) * (kV ? 1.f : scale[8 + 2 * x]), f16_hi(o) * (kV ? 1.f : scale[9 + 2 * x]));
             }
-            uint8_t* to = sm + job.at;
-            *reinterpret_cast<uint4*>(to + kept_byte(kHeadDim, r, 2 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            *reinterpret_cast<uint4*>(to + kept_byte(kHeadDim, r, 2 * c + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (r < kTile) {
+              *reinterpret_cast<uint4*>(to + kept_byte(job.width, r, 2 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              *reinterpret_cast<uint4*>(to + kept_byte(job.width, r, 2 * c + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            }
           }
-#pragma unroll
-          for (int x = 0; x < kPart; ++x) v[x] = next[x];
         }
-      }
+      };
+      if (job.values != 0) convert(std::true_type());
+      else convert(std::false_type());
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(base + L::kFull + 8 * (ri * L::kSlots + job.slot));
-        mbar_arrive(base + L::kDone + 16 * ri + 8 * (n & 1));
+        mbar_arrive(base + L::kDone + 8 * jn);
       }
     }
   } else if (warp < 4) {
@@ -765,23 +739,38 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         auto load = [&](int j, bool isv, int32_t pg) -> bool {
           const Tile t = tile_at(it, j);
           const bool wide = isv || t.type <= kTileC || it.k == kHeadDim;
-          uint32_t at;
-          if (!reserve(wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * 2 * it.k), at)) return false;
+          // (the codes of sealed keys on part of the channels land behind the tile)
+          const bool seal = kQuant && t.type == kTileM && t.r0 < it.nS * kTile;
+          // A tile's keys are waited for while the values before them are in use:
+          // keys never take more than the keys before them did, whose place they
+          // then find, so full-width ones take what sealed ones on 96 channels do.
+          uint32_t at, bytes = wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * (seal ? 3 : 2) * it.k);
+          if (kQuant && !isv && wide && w.kept_bytes == kTile * 2 * 96) bytes = kTile * 3 * 96;
+          if (!reserve(bytes, at)) return false;
           const uint32_t slot = put % L::kSlots;
           offs[slot] = at;
           // what the other threads have to know of the tile
           info[slot] = (ring_at + at) >> 4 | (uint32_t)t.rows << 16 | (wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
           const uint32_t dst = ring_at + at, bar = full + 8 * slot;
           ++put;
-          if (kQuant && t.type == kTileM && t.r0 < it.nS * kTile) {
-            // two jobs at most wait for the makers
-            if (jobs >= 2 && !wait(base + L::kDone + 16 * ri + 8 * (jobs & 1), ((jobs >> 1) - 1) & 1)) return false;
-            const int64_t block = hd.qoff + (pages != nullptr ? (int64_t)max(0, pg)
-                                                              : (int64_t)it.b * hd.qblocks + t.r0 / kTile) *
-                                                qblock_bytes(it.k);
-            *reinterpret_cast<Job*>(sm + L::kJob + (2 * ri + (jobs & 1)) * L::kJobBytes) =
-                Job{cv.qpool + block, it.k, isv ? (int)(sealed++ & 3) : -1, slot, dst - base};
-            mbar_arrive(base + L::kAsk + 16 * ri + 8 * (jobs & 1));
+          if (seal) {
+            // The codes land in the upper half of the tile's place, or behind it,
+            // their scales beside the job; the makers do the rest.
+            const uint32_t jn = jobs % L::kJobs, landed = base + L::kLanded + 8 * (ri * L::kJobs + jn);
+            if (jobs >= L::kJobs &&
+                !wait(base + L::kDone + 8 * (ri * L::kJobs + jn), (jobs / L::kJobs - 1) & 1)) return false;
+            const uint8_t* block = cv.qpool + hd.qoff +
+                                   (pages != nullptr ? (int64_t)max(0, pg)
+                                                     : (int64_t)it.b * hd.qblocks + t.r0 / kTile) * qblock_bytes(it.k);
+            const int width = isv ? kHeadDim : it.k, vn = (int)(sealed & 3);
+            const uint32_t codes = (uint32_t)(kTile * width), scales = isv ? kTile * 4u : (uint32_t)(4 * it.k);
+            const uint32_t sc = isv ? L::kVScale + (4 * ri + vn) * kTile * 4 : L::kKScale + (ri * L::kJobs + jn) * kTile * 4;
+            *reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes) =
+                Job{width, isv ? 1 : 0, slot, dst - base, sc};
+            mbar_arrive_expect_tx(landed, codes + scales);
+            bulk_load(dst + (wide ? 1 : 2) * codes, block + (isv ? qblock_voff(it.k) : 0), codes, landed, keep);
+            bulk_load(base + sc, block + (isv ? qblock_vsoff(it.k) : qblock_ksoff(it.k)), scales, landed, keep);
+            sealed += isv ? 1 : 0;
             ++jobs;
             return true;
           }
@@ -830,10 +819,12 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         }
       }
       if (kQuant) {
-        // the makers' last job: none (once the one before the last is done)
-        if (jobs >= 2) mbar_wait_bounded(base + L::kDone + 16 * ri + 8 * (jobs & 1), ((jobs >> 1) - 1) & 1, kDrainNs);
-        reinterpret_cast<Job*>(sm + L::kJob + (2 * ri + (jobs & 1)) * L::kJobBytes)->k = 0;
-        mbar_arrive(base + L::kAsk + 16 * ri + 8 * (jobs & 1));
+        // the makers' last job: none
+        const uint32_t jn = jobs % L::kJobs;
+        if (jobs >= L::kJobs)
+          mbar_wait_bounded(base + L::kDone + 8 * (ri * L::kJobs + jn), (jobs / L::kJobs - 1) & 1, kDrainNs);
+        reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes)->width = 0;
+        mbar_arrive(base + L::kLanded + 8 * (ri * L::kJobs + jn));
       }
       if (ok && ri == 0 && (s.idx < 0 || wait(base + L::kQEmpty, s.idx & 1))) {
         reinterpret_cast<Segment*>(sm + L::kSeg + ((s.idx + 1) & 1) * L::kSegBytes)->t1 = 0;
@@ -841,6 +832,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       }
       // copies still in flight must land before the block ends
       if (!ok) {
+        for (uint32_t x = jobs > L::kJobs ? jobs - L::kJobs : 0; kQuant && x < jobs; ++x)
+          mbar_wait_bounded(base + L::kLanded + 8 * (ri * L::kJobs + x % L::kJobs), (x / L::kJobs) & 1, kDrainNs);
         for (uint32_t x = freed; x < put; ++x)
           mbar_wait_bounded(full + 8 * (x % L::kSlots), (x / L::kSlots) & 1, kDrainNs);
         if (ri == 0 && s.idx >= 0) mbar_wait_bounded(base + L::kQFull, s.idx & 1, kDrainNs);
