@@ -181,14 +181,15 @@ def _token_stride(t, heads, lead, what):
     tensor whose heads are dense and whose tokens are evenly spaced."""
     import torch
     try:
-        shape, stride = t.shape, t.stride()
+        shape = t.shape
+        if not t.is_cuda or t.dtype is not torch.bfloat16 or shape != (*lead, heads, 128):
+            raise ValueError(f"{what}: expected {torch.bfloat16} {(*lead, heads, 128)} on cuda, got {t.dtype} "
+                             f"{tuple(shape)} on {t.device.type}")
+        if t.is_contiguous():
+            return heads * 128
+        stride = t.stride()
     except AttributeError:
         raise TypeError(f"{what} must be a torch tensor") from None
-    if t.dtype is not torch.bfloat16 or t.device.type != "cuda" or shape != (*lead, heads, 128):
-        raise ValueError(f"{what}: expected {torch.bfloat16} {(*lead, heads, 128)} on cuda, got {t.dtype} "
-                         f"{tuple(shape)} on {t.device.type}")
-    if t.is_contiguous():
-        return heads * 128
     even, step, rows = True, None, 1
     for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
         if n > 1:

@@ -173,17 +173,23 @@ __device__ __forceinline__ uint32_t kept_byte(int k, int r, int c) {
 // flags the chunk's special tokens; a block per F tile lays out its image.
 constexpr int kPlanThreads = 256;
 
+__device__ __forceinline__ uint64_t item_cost(const Item& it) {
+  return (uint64_t)(it.nA + it.nC) * cost_wide() + (uint64_t)(it.nM + it.nF) * cost_kept(it);
+}
+
+// Each thread sums a run of items, the block scans the sums; then a thread per
+// CTA finds the run its first offset floor(iC/P) falls into, by bisection, and
+// walks that run's items.
 __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
   __shared__ uint64_t s_warp[kPlanThreads / 32];
+  __shared__ uint64_t s_off[kPlanThreads + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int E = a.nb * a.cv.Hkv * w.items_q;
   const int per = (E + kPlanThreads - 1) / kPlanThreads;
-  const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
   uint64_t mine = 0;
   Item it;
-  for (int e = e0; e < e1; ++e)
-    if (item_info(a, w, e, it))
-      mine += (uint64_t)(it.nA + it.nC) * cost_wide() + (uint64_t)(it.nM + it.nF) * cost_kept(it);
+  for (int e = min(E, tid * per); e < min(E, (tid + 1) * per); ++e)
+    if (item_info(a, w, e, it)) mine += item_cost(it);
   uint64_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -197,27 +203,34 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
     if (x < warp) off += s_warp[x];
     C += s_warp[x];
   }
+  s_off[tid] = off;
+  __syncthreads();
   const uint64_t P = max((uint64_t)1, min((uint64_t)w.max_ctas, C / kMinCtaCost));
   if (tid == 0) {
     w.start[w.max_ctas + 1] = make_int2((int)P, 0);
     w.start[P] = make_int2(E, 0);
     if (C == 0) w.start[0] = make_int2(E, 0);
   }
-  for (int e = e0; e < e1; ++e) {
+  static_assert(kChunkMaxCtas <= kPlanThreads, "a thread per CTA");
+  if (tid >= P || C == 0) return;
+  const uint64_t x = (uint64_t)tid * C / P;
+  int run = 0;                            // the last run that starts at or before x
+#pragma unroll
+  for (int d = kPlanThreads / 2; d > 0; d >>= 1)
+    if (s_off[run + d] <= x) run += d;
+  // (runs without tiles share the next one's start: the bisection ends behind them)
+  uint64_t at = s_off[run];
+  for (int e = run * per; e < E; ++e) {
     if (!item_info(a, w, e, it)) continue;
-    const uint64_t wide = (uint64_t)(it.nA + it.nC) * cost_wide();
-    const uint64_t end = off + wide + (uint64_t)(it.nM + it.nF) * cost_kept(it);
-    // CTAs whose first offset floor(iC/P) lies in [off, end)
-    for (uint64_t i = (off * P + C - 1) / C; i < P; ++i) {
-      const uint64_t x = i * C / P;
-      if (x < off) continue;
-      if (x >= end) break;
-      const uint64_t r = x - off;
+    const uint64_t end = at + item_cost(it);
+    if (x < end) {
+      const uint64_t r = x - at, wide = (uint64_t)(it.nA + it.nC) * cost_wide();
       const int t = (int)(r <= wide ? (r + cost_wide() - 1) / cost_wide()
                                     : it.nA + it.nC + (r - wide + cost_kept(it) - 1) / cost_kept(it));
-      w.start[i] = t < tiles_of(it) ? make_int2(e, t) : make_int2(e + 1, 0);
+      w.start[tid] = t < tiles_of(it) ? make_int2(e, t) : make_int2(e + 1, 0);
+      break;
     }
-    off = end;
+    at = end;
   }
 }
 
@@ -1261,7 +1274,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 // such CTA, its partials are CTA i - 1's last one and the first ones of CTA
 // i, i + 1, ... while they start inside the same item.  8 rows a block, a warp
 // a row: the lanes read the row's (m, l) of all partials at once (32 at a
-// time), then the warp its outputs, four partials in flight.
+// time), then the warp its outputs, eight partials in flight.
 constexpr int kMergeRows = 8;
 __global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const __grid_constant__ ChunkArgs a,
                                                                       const ChunkWork w) {
@@ -1303,7 +1316,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const __gr
       m = mn;
       l = l * f + sum;
       o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-#pragma unroll 4
+#pragma unroll 8
       for (int x = 0; x < count; ++x) {
         const float ex = __shfl_sync(0xffffffffu, e, x);
         const float4 u = __ldcg(reinterpret_cast<const float4*>(w.part + slot(c0 + x) * kHeadDim) + lane);

@@ -238,15 +238,22 @@ __global__ void __launch_bounds__(256) chunk_append_kernel(const __grid_constant
       row8(va_pool, abase + arow)[lane] = vx;
     }
   }
-}
-
-// The lengths advance once no launch of the append reads them any more.
-__global__ void __launch_bounds__(kChunkSeqs) chunk_advance_kernel(const __grid_constant__ ChunkArgs a) {
-  const int i = threadIdx.x;
-  if (i >= a.nb) return;
-  int N;
-  const int n = chunk_len(a, i, N);
-  if (n > 0) a.cv.len[a.layer * a.cv.B + a.b0 + i] = N + n;
+  // The lengths advance once no block reads them any more: by the last one to
+  // get here (a word of the header counts them, and is left at zero).
+  __shared__ int s_last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int* count = reinterpret_cast<int*>(&cv.hdr->pad[0]);
+    s_last = atom_add_acq_rel_gpu(count, 1) == (int)gridDim.x - 1;
+    if (s_last) *count = 0;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  for (int i = threadIdx.x; i < a.nb; i += blockDim.x) {
+    int N;
+    const int n = chunk_len(a, i, N);
+    if (n > 0) cv.len[a.layer * cv.B + a.b0 + i] = N + n;
+  }
 }
 
 }  // namespace
@@ -275,9 +282,6 @@ cudaError_t launch_chunk_append(const ChunkArgs& args, bool has_middle, int num_
   const int64_t items = (int64_t)args.nb * args.n_max * cv.Hkv;
   const int64_t blocks = min((items + 7) / 8, (int64_t)num_sms * 16);
   chunk_append_kernel<<<(unsigned)blocks, 256, 0, stream>>>(args);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  chunk_advance_kernel<<<1, kChunkSeqs, 0, stream>>>(args);
   return cudaGetLastError();
 }
 
