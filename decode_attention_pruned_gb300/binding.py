@@ -159,11 +159,17 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_torch = None
+
+
 def _stream(stream=None):
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    global _torch
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    if _torch is None:
+        import torch as _torch
+    # the current stream's handle, without the Stream object around it
+    return ctypes.c_void_p(_torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device()))
 
 
 def _need(t, dtype, shape, what, device_kind="cuda"):

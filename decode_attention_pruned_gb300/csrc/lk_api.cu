@@ -1548,7 +1548,11 @@ lk_status lk_rope_apply(lk_rope rope, const void* q, int64_t q_stride, const voi
   a.layout = rope->d.layout;
   a.magnitude = rope->magnitude;
   std::memcpy(a.freq, rope->freq, sizeof(a.freq));
-  cudaError_t err = launch_rope(a, static_cast<cudaStream_t>(stream));
+  int dev = 0, sms = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err != cudaSuccess) return cuda_fail(err, "lk_rope_apply: device query");
+  err = launch_rope(a, sms, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_fail(err, "lk_rope_apply launch");
   return LK_OK;
 }

@@ -1336,24 +1336,6 @@ __global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const __gr
   reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-// A launch that may begin while the stream's preceding kernel ends; every
-// block of such a kernel waits for that one before it leaves.
-template <typename... Args>
-cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
-                         const std::decay_t<Args>&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <bool kDual, int kFmt>
 cudaError_t launch_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& w, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};

@@ -54,6 +54,8 @@ __device__ __forceinline__ const uint16_t* v_token(const ChunkArgs& a, int b, in
 // Paged caches: a thread per (sequence, head) pops the pages between the
 // held and the new length.
 __global__ void __launch_bounds__(256) chunk_pages_kernel(const __grid_constant__ ChunkArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const CacheView& cv = a.cv;
   const int x = blockIdx.x * blockDim.x + threadIdx.x;
   if (x >= a.nb * cv.Hkv) return;
@@ -72,6 +74,8 @@ __global__ void __launch_bounds__(256) chunk_pages_kernel(const __grid_constant_
 // in the tail if it has left the window already, in its ring row if it is
 // still held there, else in the chunk.
 __global__ void __launch_bounds__(256) chunk_seal_kernel(const __grid_constant__ ChunkArgs a, int max_blocks) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const CacheView& cv = a.cv;
   const int lane = threadIdx.x & 31;
   const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -113,6 +117,8 @@ __global__ void __launch_bounds__(256) chunk_seal_kernel(const __grid_constant__
 // order (ballot and warp scan per 1024 tokens), copies them to rows count,
 // count + 1, ... of the SPECIAL heads and advances the count.
 __global__ void __launch_bounds__(1024) chunk_special_kernel(const __grid_constant__ ChunkArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const CacheView& cv = a.cv;
   const int b = a.b0 + blockIdx.x;
   int N;
@@ -170,6 +176,8 @@ __global__ void __launch_bounds__(1024) chunk_special_kernel(const __grid_consta
 }
 
 __global__ void __launch_bounds__(256) chunk_append_kernel(const __grid_constant__ ChunkArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const CacheView& cv = a.cv;
   const int lane = threadIdx.x & 31;
   const int64_t items = (int64_t)a.nb * a.n_max * cv.Hkv;
@@ -261,28 +269,20 @@ __global__ void __launch_bounds__(256) chunk_append_kernel(const __grid_constant
 cudaError_t launch_chunk_append(const ChunkArgs& args, bool has_middle, int num_sms, cudaStream_t stream) {
   const CacheView& cv = args.cv;
   cudaError_t err = cudaSuccess;
-  if (has_middle && cv.max_pages > 0) {
-    chunk_pages_kernel<<<(args.nb * cv.Hkv + 255) / 256, 256, 0, stream>>>(args);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-  }
-  if (has_middle && kv_quantized(cv.kv_format)) {
+  if (has_middle && cv.max_pages > 0)
+    err = launch_after(chunk_pages_kernel, dim3((unsigned)(args.nb * cv.Hkv + 255) / 256), 256, 0, stream, args);
+  if (err == cudaSuccess && has_middle && kv_quantized(cv.kv_format)) {
     // a chunk of n tokens completes at most this many blocks of a head
     const int max_blocks = (args.n_max + kQBlockRows - 1) / kQBlockRows;
     const int64_t warps = (int64_t)args.nb * cv.Hkv * max_blocks;
-    chunk_seal_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(args, max_blocks);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
+    err = launch_after(chunk_seal_kernel, dim3((unsigned)((warps + 7) / 8)), 256, 0, stream, args, max_blocks);
   }
-  if (args.ids != nullptr) {
-    chunk_special_kernel<<<args.nb, 1024, 0, stream>>>(args);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-  }
+  if (err == cudaSuccess && args.ids != nullptr)
+    err = launch_after(chunk_special_kernel, dim3((unsigned)args.nb), 1024, 0, stream, args);
+  if (err != cudaSuccess) return err;
   const int64_t items = (int64_t)args.nb * args.n_max * cv.Hkv;
   const int64_t blocks = min((items + 7) / 8, (int64_t)num_sms * 16);
-  chunk_append_kernel<<<(unsigned)blocks, 256, 0, stream>>>(args);
-  return cudaGetLastError();
+  return launch_after(chunk_append_kernel, dim3((unsigned)blocks), 256, 0, stream, args);
 }
 
 }  // namespace lk

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "lk_internal.h"
 
@@ -166,6 +167,24 @@ inline cudaError_t set_smem_limit_once(F* fn, int bytes, std::atomic<uint64_t>& 
   return err;
 }
 
+// A launch that may begin while the stream's preceding kernel ends; every
+// block of such a kernel waits for that one before it leaves.
+template <typename... Args>
+inline cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                         const std::decay_t<Args>&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 size_t decode_smem_bytes();
 cudaError_t launch_decode(const DecodeMaps& maps, const DecodeArgs& args, int ctas, cudaStream_t stream);
 cudaError_t launch_append(const AppendArgs& args, cudaStream_t stream);
@@ -176,6 +195,6 @@ cudaError_t launch_build_masks(const float* alpha, const uint8_t* eligible, int 
 
 cudaError_t launch_chunk_append(const ChunkArgs& args, bool has_middle, int num_sms, cudaStream_t stream);
 cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& work, cudaStream_t stream);
-cudaError_t launch_rope(const RopeArgs& args, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs& args, int num_sms, cudaStream_t stream);
 
 }  // namespace lk
