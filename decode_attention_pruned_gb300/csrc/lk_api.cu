@@ -1344,6 +1344,15 @@ lk_status chunk_attn_prepare(lk_cache cache, void* o, void* workspace, size_t ws
     return fail(LK_ERR_UNSUPPORTED, "%s: %d sequences of %d tokens are too many for one call", what, cache->B, a.n_max);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   w = lay.w;
+  // Weights of the work line, fitted to clocks of CTAs over what they did: an
+  // item, a full-width tile, a tile on k channels.  One query tile (1 unit = 12
+  // clocks): the loads set the pace.  Two (16 clocks): the softmax does, and an
+  // item starts and ends slowly.  Sealed blocks: the warps that expand them do.
+  const bool sealed = kv_quantized(cv.kv_format);
+  w.cost_item = w.dual ? 448 : sealed ? 112 : 216;
+  w.cost_wide = w.dual ? 236 : 256;
+  w.cost_kept = w.dual ? (sealed ? 172 : 160) : (sealed ? 200 : 84);
+  w.cost_k = w.dual ? (sealed ? 19 : 3) : (sealed ? 21 : 13);
   w.start = reinterpret_cast<int2*>(ws);
   w.special = reinterpret_cast<uint32_t*>(ws + lay.off_special);
   w.part_ml = reinterpret_cast<float2*>(ws + lay.off_ml);

@@ -130,8 +130,9 @@ __device__ __forceinline__ bool item_info(const ChunkArgs& a, const ChunkWork& w
   return true;
 }
 __device__ __forceinline__ int tiles_of(const Item& it) { return it.nA + it.nC + it.nM + it.nF; }
-__device__ __forceinline__ uint32_t cost_wide() { return 2 * kHeadDim; }
-__device__ __forceinline__ uint32_t cost_kept(const Item& it) { return kHeadDim + it.k; }
+__device__ __forceinline__ uint32_t cost_kept(const ChunkWork& w, const Item& it) {
+  return (uint32_t)(w.cost_kept + (it.k * w.cost_k >> 3));
+}
 
 __device__ __forceinline__ Tile tile_at(const Item& it, int j) {
   Tile t;
@@ -173,8 +174,8 @@ __device__ __forceinline__ uint32_t kept_byte(int k, int r, int c) {
 // flags the chunk's special tokens; a block per F tile lays out its image.
 constexpr int kPlanThreads = 256;
 
-__device__ __forceinline__ uint64_t item_cost(const Item& it) {
-  return (uint64_t)(it.nA + it.nC) * cost_wide() + (uint64_t)(it.nM + it.nF) * cost_kept(it);
+__device__ __forceinline__ uint64_t item_cost(const ChunkWork& w, const Item& it) {
+  return (uint64_t)w.cost_item + (uint64_t)(it.nA + it.nC) * w.cost_wide + (uint64_t)(it.nM + it.nF) * cost_kept(w, it);
 }
 
 // Each thread sums a run of items, the block scans the sums; then a thread per
@@ -189,7 +190,7 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
   uint64_t mine = 0;
   Item it;
   for (int e = min(E, tid * per); e < min(E, (tid + 1) * per); ++e)
-    if (item_info(a, w, e, it)) mine += item_cost(it);
+    if (item_info(a, w, e, it)) mine += item_cost(w, it);
   uint64_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -222,11 +223,12 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
   uint64_t at = s_off[run];
   for (int e = run * per; e < E; ++e) {
     if (!item_info(a, w, e, it)) continue;
-    const uint64_t end = at + item_cost(it);
+    const uint64_t end = at + item_cost(w, it);
     if (x < end) {
-      const uint64_t r = x - at, wide = (uint64_t)(it.nA + it.nC) * cost_wide();
-      const int t = (int)(r <= wide ? (r + cost_wide() - 1) / cost_wide()
-                                    : it.nA + it.nC + (r - wide + cost_kept(it) - 1) / cost_kept(it));
+      // (an item's own share comes before its tiles)
+      const uint64_t r = x - at - min(x - at, (uint64_t)w.cost_item), wide = (uint64_t)(it.nA + it.nC) * w.cost_wide;
+      const uint32_t kept = cost_kept(w, it);
+      const int t = (int)(r <= wide ? (r + w.cost_wide - 1) / w.cost_wide : it.nA + it.nC + (r - wide + kept - 1) / kept);
       w.start[tid] = t < tiles_of(it) ? make_int2(e, t) : make_int2(e + 1, 0);
       break;
     }

@@ -129,6 +129,9 @@ struct ChunkWork {
   int32_t special_seqs;     // sequences whose special tokens are flagged (0: no SPECIAL head)
   int32_t special_words;    // 32-token words per sequence
   int32_t kept_bytes;       // of a query tile on the kept channels
+  int32_t cost_item;        // what an item weighs on the work line, a full-width key tile, and one on k
+  int32_t cost_wide;        //   channels: cost_kept + k cost_k / 8
+  int32_t cost_kept, cost_k;
   int2* start;              // [max_ctas + 2]: (item, tile) where each CTA starts, the end; then (CTAs, -)
   float2* part_ml;          // [2 max_ctas][part_rows]
   float* part;              // [2 max_ctas][part_rows][128]
