@@ -616,8 +616,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
     const int ri = kDual ? 0 : (warp - 12) >> 1, mt = (tid - 384) % kMade;
     for (uint32_t n = 0;; ++n) {
       const uint32_t jn = ri * L::kJobs + n % L::kJobs, phase = (n / L::kJobs) & 1;
-      bool ok = false;
-      for (const uint64_t t0 = global_timer_ns(); !ok && global_timer_ns() - t0 < kIdleNs && *gone == 0;)
+      bool ok = mbar_test_wait(base + L::kLanded + 8 * jn, phase);
+      for (const uint64_t t0 = ok ? 0 : global_timer_ns(); !ok && *gone == 0 && global_timer_ns() - t0 < kIdleNs;)
         ok = mbar_wait_bounded(base + L::kLanded + 8 * jn, phase, 1000000);
       if (!__all_sync(0xffffffffu, ok)) {
         *gone = 1;
@@ -625,16 +625,15 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       }
       const Job job = *reinterpret_cast<const Job*>(sm + L::kJob + jn * L::kJobBytes);
       if (job.width == 0) break;
-      const int groups = job.width / 16;
-      // a thread keeps to one 16-channel group (of 6 groups not all threads have
-      // one); its rows are r0, r0 + step, ...
-      const int lanes = kMade / groups * groups, step = lanes / groups;
-      const int c = mt % groups, r0 = mt < lanes ? mt / groups : kTile;
       uint8_t* to = sm + job.at;
-      const uint4* codes =
-          reinterpret_cast<const uint4*>(to + kTile * job.width * (job.width == kHeadDim ? 1 : 2));
-      auto convert = [&](auto values) {
+      auto convert = [&](auto channels, auto values) {
+        constexpr int kWidth = decltype(channels)::value, kGroups = kWidth / 16;
         constexpr bool kV = decltype(values)::value;
+        // A thread keeps to one 16-channel group (of 6 groups not all threads have
+        // one); its rows are r0, r0 + kRows, ..., four of them on their way at once.
+        constexpr int kRows = kMade / kGroups, kOnce = kRows * 4 <= kTile || kGroups == 6 ? 4 : kTile / kRows;
+        const int c = mt % kGroups, r0 = mt < kRows * kGroups ? mt / kGroups : kTile;
+        const uint4* codes = reinterpret_cast<const uint4*>(to + kTile * kWidth * (kWidth == kHeadDim ? 1 : 2));
         float scale[kV ? 1 : 16];
         if (!kV) {
 #pragma unroll
@@ -644,17 +643,17 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           }
         }
 #pragma unroll 1
-        for (int rb = 0; rb < kTile; rb += 2 * step) {
-          uint4 u[2];
+        for (int rb = r0; rb < (kGroups == 6 ? kTile + r0 : kTile); rb += kOnce * kRows) {
+          uint4 u[kOnce];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int r = min(rb + r0 + y * step, kTile - 1);
-            u[y] = codes[r * groups + (c ^ qswz(job.width, r))];
+          for (int y = 0; y < kOnce; ++y) {
+            const int r = kGroups == 6 ? min(rb + y * kRows, kTile - 1) : rb + y * kRows;
+            u[y] = codes[r * kGroups + (c ^ qswz(kWidth, r))];
           }
           __syncwarp();
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int r = rb + r0 + y * step;
+          for (int y = 0; y < kOnce; ++y) {
+            const int r = rb + y * kRows;
             const uint32_t in[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
             uint32_t lo[4], hi[4];
 #pragma unroll
@@ -664,15 +663,18 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               lo[x] = pack_bf16x2(f16_lo(e) * (kV ? 1.f : scale[2 * x]), f16_hi(e) * (kV ? 1.f : scale[2 * x + 1]));
               hi[x] = pack_bf16x2(f16_lo(o) * (kV ? 1.f : scale[8 + 2 * x]), f16_hi(o) * (kV ? 1.f : scale[9 + 2 * x]));
             }
-            if (r < kTile) {
-              *reinterpret_cast<uint4*>(to + kept_byte(job.width, r, 2 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              *reinterpret_cast<uint4*>(to + kept_byte(job.width, r, 2 * c + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (kGroups != 6 || r < kTile) {
+              *reinterpret_cast<uint4*>(to + kept_byte(kWidth, r, 2 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              *reinterpret_cast<uint4*>(to + kept_byte(kWidth, r, 2 * c + 1)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             }
           }
         }
       };
-      if (job.values != 0) convert(std::true_type());
-      else convert(std::false_type());
+      if (job.values != 0) convert(std::integral_constant<int, 128>(), std::true_type());
+      else if (job.width == 32) convert(std::integral_constant<int, 32>(), std::false_type());
+      else if (job.width == 64) convert(std::integral_constant<int, 64>(), std::false_type());
+      else if (job.width == 96) convert(std::integral_constant<int, 96>(), std::false_type());
+      else convert(std::integral_constant<int, 128>(), std::false_type());
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
