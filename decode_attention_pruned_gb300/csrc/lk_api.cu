@@ -332,7 +332,9 @@ ChunkLayout chunk_layout(const lk_plan_s& p, int B, int n_max, int layer, int ct
   const int64_t tiles = ((int64_t)n_max + 127) / 128;
   w.far_tiles = kfar > 0 ? (int)tiles : 0;
   w.far_bytes = (kfar + kHeadDim) * 2 * 128;
-  w.kept_bytes = kfar * 2 * 128;
+  w.q_rows = w.dual ? 128 : (w.part_rows + 7) / 8 * 8;
+  w.kept_width = kfar;
+  w.kept_bytes = kfar * 2 * w.q_rows;
   w.special_seqs = special ? seqs : 0;
   w.special_words = special ? (int)(4 * tiles) : 0;
   size_t off = align_up((kChunkMaxCtas + 2) * sizeof(int2), 256);

@@ -162,11 +162,12 @@ __device__ __forceinline__ Tile tile_at(const Item& it, int j) {
 __device__ __forceinline__ uint8_t* far_tile(const ChunkArgs& a, const ChunkWork& w, int seq, int h, int tile) {
   return w.far + (((int64_t)seq * a.cv.Hkv + h) * w.far_tiles + tile) * w.far_bytes;
 }
-// Byte of 16-byte group c of row r of a K tile of k channels (64-channel
-// halves with 128-byte swizzle, or 32-channel stripes with 64-byte swizzle)
-__device__ __forceinline__ uint32_t kept_byte(int k, int r, int c) {
-  return (k & 63) == 0 ? (uint32_t)((c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4))
-                       : (uint32_t)((c >> 2) * (kTile * 64) + r * 64 + (((c & 3) ^ ((r >> 1) & 3)) << 4));
+// Byte of 16-byte group c of row r of a tile of k channels and `rows` rows
+// (64-channel halves with 128-byte swizzle, or 32-channel stripes with 64-byte
+// swizzle)
+__device__ __forceinline__ uint32_t kept_byte(int k, int r, int c, int rows = kTile) {
+  return (k & 63) == 0 ? (uint32_t)((c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4))
+                       : (uint32_t)((c >> 2) * (rows * 64) + r * 64 + (((c & 3) ^ ((r >> 1) & 3)) << 4));
 }
 
 // ------------------------------------------------------------------ plan
@@ -376,7 +377,6 @@ struct Smem {
   static constexpr int kMakers = kDual ? 4 : 2;          // warps that make a ring's tiles out of sealed blocks
   static constexpr int kArrivals = kQuant ? kMakers : 1; // that complete a tile
   static_assert(kJob + kJobBytes * kJobs * kRings <= 2048 && kSegBytes == 128, "barriers, tiles, segments and jobs");
-  static constexpr int kQKept = kQ + kQTiles * kWideBytes;
   static constexpr int kBytes = 227 * 1024;
   static constexpr int kEnd = kBytes - 1024;             // after aligning the base
 };
@@ -549,11 +549,11 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
     fence_barrier_init();
     *gone = 0;
   }
-  const uint32_t ring = L::kQKept + L::kQTiles * w.kept_bytes;       // offsets from base
-  // rows of the query tiles that no load writes stay zero
-  for (int x = L::kQ / 16 + tid; x < (int)ring / 16; x += blockDim.x)
-    reinterpret_cast<uint4*>(sm)[x] = make_uint4(0u, 0u, 0u, 0u);
-  fence_async_smem();
+  // A query tile takes the rows that it can have: the MMA reads on to 128, into
+  // whatever lies behind, and those rows of S and O belong to nobody.
+  const uint32_t q_rows = kDual ? kTile : (uint32_t)w.q_rows, q_bytes = q_rows * kHeadDim * 2;
+  const uint32_t q_kept_at = L::kQ + L::kQTiles * q_bytes;           // offsets from base
+  const uint32_t ring = (q_kept_at + L::kQTiles * w.kept_bytes + 1023) & ~1023u;
   if (warp == 0 && lane < 3 + kNumPools) tma_prefetch_map(&maps.q + lane);
   if (warp == 3) tmem_alloc_all(base + L::kTmem);
   tc_fence_before();
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           mbar_arrive_expect_tx(base + L::kQFull, (uint32_t)(nq * w.box_tokens * G * kHeadDim * 2));
           for (int x = 0; x < nq; ++x)
             for (int part = 0; part < 2; ++part)
-              tma_load_3d(base + L::kQ + x * kWideBytes + part * (kWideBytes / 2), &maps.q, part * 64, it.h * G,
+              tma_load_3d(base + L::kQ + x * q_bytes + part * (q_bytes / 2), &maps.q, part * 64, it.h * G,
                           it.b * a.n_max + it.i0 + x * tq, base + L::kQFull, once);
         }
         // first of the arrivals that complete a tile's slot, and the others
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           // keys never take more than the keys before them did, whose place they
           // then find, so full-width ones take what sealed ones on 96 channels do.
           uint32_t at, bytes = wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * (seal ? 3 : 2) * it.k);
-          if (kQuant && !isv && wide && w.kept_bytes == kTile * 2 * 96) bytes = kTile * 3 * 96;
+          if (kQuant && !isv && wide && w.kept_width == 96) bytes = kTile * 3 * 96;
           if (!reserve(bytes, at)) return false;
           const uint32_t slot = put % L::kSlots;
           offs[slot] = at;
@@ -872,7 +872,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       const uint32_t empty = base + L::kEmpty + (kDual ? 0 : st * 8 * L::kSlots);
       volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + (kDual ? 0 : st * L::kSlots);
       const uint32_t q_wide = desc_lo(16) | (base + L::kQ + (kDual ? st * kWideBytes : 0)) >> 4;
-      const uint32_t q_kept = desc_lo(16) | (base + L::kQKept + (kDual ? st * w.kept_bytes : 0)) >> 4;
+      const uint32_t q_half = q_rows * 8, q_stripe = q_rows * 4;       // from 64 channels of q to the next, from 32
+      const uint32_t q_kept = desc_lo(16) | (base + q_kept_at + (kDual ? st * w.kept_bytes : 0)) >> 4;
       const uint32_t s_at = tm_s + st * 128, o_at = tm_o + st * 128;
       const uint32_t s_full = base + L::kSFull + 16 * st, p_full = base + L::kPFull + 16 * st,
                      o_full = base + L::kOFull + 8 * st;
@@ -922,7 +923,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 #pragma unroll
             for (int y = 1; y < kSteps; ++y) {
               const uint32_t at = kThin ? (y >> 1) * (kTile * 4) + (y & 1) * 2 : (y >> 2) * (kTile * 8) + (y & 3) * 2;
-              mma_ss<kHi, true>(d, q + at, k + at, kDescS);
+              const uint32_t q_at = kThin ? (y >> 1) * q_stripe + (y & 1) * 2 : (y >> 2) * q_half + (y & 3) * 2;
+              mma_ss<kHi, true>(d, q + q_at, k + at, kDescS);
             }
           };
           if (width == 0) run(std::integral_constant<int, 2>(), q_kept);
@@ -1020,16 +1022,16 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         // q on the kept channels: each group its query tile's, or both the one's
         const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + it.h) * kHeadDim;
         const uint8_t* q = sm + L::kQ + (kDual ? st * kWideBytes : 0);
-        uint8_t* to = sm + L::kQKept + (kDual ? st * w.kept_bytes : 0);
+        uint8_t* to = sm + q_kept_at + (kDual ? st * w.kept_bytes : 0);
         const int groups = it.k / 8, rows = min(tq, it.ntok - (kDual ? st * tq : 0)) * G;
         for (int y = tid - 128 - (kDual ? st * 128 : 0); y < rows * groups; y += kDual ? 128 : 256) {
           const int r = y / groups, c = y - r * groups;
           const uint4 kc = *reinterpret_cast<const uint4*>(kept + 8 * c);
           auto at = [&](uint32_t ch) {
-            return (uint32_t)*reinterpret_cast<const uint16_t*>(q + kept_byte(kHeadDim, r, (int)ch >> 3) + (ch & 7) * 2);
+            return (uint32_t)*reinterpret_cast<const uint16_t*>(q + kept_byte(kHeadDim, r, (int)ch >> 3, q_rows) + (ch & 7) * 2);
           };
           auto two = [&](uint32_t p) { return at(p & 0xffffu) | at(p >> 16) << 16; };
-          *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c)) = make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
+          *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c, q_rows)) = make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
         }
         fence_async_smem();
         __syncwarp();
@@ -1120,7 +1122,9 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 #pragma unroll
           for (int c = 8; c < kHalf; c += 2)
             mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+          // (nobody's rows score whatever lies behind q: they move no one's maximum)
+          if (!kDual && !mine) top = -INFINITY;
           // The maximum moves only when a score exceeds it by 2^8: below that p
           // stays exact in fp32 and bf16 alike.
           if (__any_sync(0xffffffffu, top > m + 8.f)) {

@@ -128,6 +128,8 @@ struct ChunkWork {
   int32_t far_bytes;        // of one image
   int32_t special_seqs;     // sequences whose special tokens are flagged (0: no SPECIAL head)
   int32_t special_words;    // 32-token words per sequence
+  int32_t q_rows;           // of a query tile in shared memory
+  int32_t kept_width;       // channels of the widest pruned head that keeps some
   int32_t kept_bytes;       // of a query tile on the kept channels
   int32_t cost_item;        // what an item weighs on the work line, a full-width key tile, and one on k
   int32_t cost_wide;        //   channels: cost_kept + k cost_k / 8
