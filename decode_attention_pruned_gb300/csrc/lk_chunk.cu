@@ -1126,9 +1126,10 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           // (nobody's rows score whatever lies behind q: they move no one's maximum)
           if (!kDual && !mine) top = -INFINITY;
           // The maximum moves only when a score exceeds it by 2^8: below that p
-          // stays exact in fp32 and bf16 alike.
+          // stays exact in fp32 and bf16 alike.  (Each row's by itself: what a row
+          // comes to does not depend on the others of its warp.)
           if (__any_sync(0xffffffffu, top > m + 8.f)) {
-            const float mn = fmaxf(m, top);
+            const float mn = top > m + 8.f ? top : m;
             const float f = m == -INFINITY ? 0.f : ex2(m - mn);
             m = mn;
             l *= f;
