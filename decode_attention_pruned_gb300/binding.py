@@ -640,7 +640,9 @@ class Cache:
     def chunk_attn(self, layer, q, k, v, lens=None, ids=None, o=None, stream=None):
         """lk_chunk_attn: q [B, n, Hq, 128], k, v [B, n, Hkv, 128] bf16 (tokens
         evenly spaced), lens: B host ints -> o [B, n, Hq, 128] bf16.  The cache
-        is only read; rows of o past a sequence's length are left as they are."""
+        is only read; rows of o past a sequence's length are left as they are.
+        The calls of a cache share its chunk workspace: they must not overlap on
+        the GPU."""
         c, lens = self._chunk(q, k, v, lens, ids)
         o = self._chunk_out(q, o)
         _check(_lib.lk_chunk_attn(self._h, layer, ctypes.byref(c), o.data_ptr(), self.chunk_workspace.data_ptr(),

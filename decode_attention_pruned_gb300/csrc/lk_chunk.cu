@@ -25,10 +25,19 @@
 // A pair that is far for an early layout of its token (ring row or chunk row)
 // is therefore scored once, on k channels, from F, and a tile needs no
 // element-by-element choice of score.
-// The tiles of all items form a line, each weighing what it costs (128 for
-// P.V plus the width of its keys); CTA i of P takes the tiles that start in
-// [iC/P, (i+1)C/P).  An item that spans CTAs leaves (o, m, l) partials, which
-// a last kernel merges.
+// The items and their tiles form a line, each weighing what it was measured to
+// cost; CTA i of P takes the tiles that start in [iC/P, (i+1)C/P).  An item that
+// spans CTAs leaves (o, m, l) partials, which a last kernel merges.
+//
+// What bounds it.  Chunks that fill two query tiles: the softmax of 128 x 64
+// scores (1300 clocks a group, of which the tensor cores need 800); 1000 queries
+// of 28 heads over 131072 tokens on 32 kept channels take 866 us, 54% of the
+// measured bf16 matrix rate.  Chunks of a few tokens: the cache's bytes, through
+// a ring that holds two to five tiles per group; 64 sequences of 4096 tokens
+// take 101 us, 1.45 times what a plain copy's rate gives their bytes.  Sealed
+// blocks: the four warps that expand them, which share instruction caches with
+// every other role; 16 sequences of 8192 tokens take 108 us, 3.7 times their
+// bytes.  One sequence: three dependent launches, 31 us over 32768 tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -47,7 +56,9 @@ namespace {
 constexpr int kTile = 128;                 // keys per tile, rows per query tile
 constexpr int kFar = 1 << 29;              // a window that nothing leaves
 constexpr float kScaleLog2 = 0.12751743f;  // log2(e) / sqrt(128)
-constexpr uint64_t kMinCtaCost = 768;      // line a CTA takes at least: three full-width tiles
+// line a CTA takes at least: about three tiles (one sequence of 32768 tokens: 31
+// us; with half of it the same, with three times as much 33)
+constexpr uint64_t kMinCtaCost = 768;
 
 enum TileType : int { kTileA = 0, kTileC = 1, kTileM = 2, kTileF = 3 };
 
@@ -229,7 +240,8 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
       // (an item's own share comes before its tiles)
       const uint64_t r = x - at - min(x - at, (uint64_t)w.cost_item), wide = (uint64_t)(it.nA + it.nC) * w.cost_wide;
       const uint32_t kept = cost_kept(w, it);
-      const int t = (int)(r <= wide ? (r + w.cost_wide - 1) / w.cost_wide : it.nA + it.nC + (r - wide + kept - 1) / kept);
+      const int t = (int)(r <= wide ? (r + w.cost_wide - 1) / w.cost_wide
+                                    : it.nA + it.nC + (r - wide + kept - 1) / kept);
       w.start[tid] = t < tiles_of(it) ? make_int2(e, t) : make_int2(e + 1, 0);
       break;
     }
@@ -384,9 +396,9 @@ struct Smem {
 constexpr uint64_t kIdleNs = 60000000000ull;      // bound of the makers' wait for a job
 constexpr uint64_t kDrainNs = 1000000000ull;      // bound of the waits for copies and MMAs still in flight
 
-// The rest of a wait whose phase was not complete at once (out of line: the
-// waits sit in loops that should stay small).
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit, volatile int* gone, DevHeader* hdr) {
+// The rest of a wait whose phase was not complete at once.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit, volatile int* gone,
+                                        DevHeader* hdr) {
   const uint64_t t0 = global_timer_ns();
   while (limit != 0) {
 #pragma unroll 1
@@ -690,320 +702,324 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       }
     }
   } else if (warp < 4) {
-  if (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 0 || warp == 3) {
-    // ------------------------------------------------------------- loads
-    // A thread per ring.  A ring is a FIFO of runs of bytes: the oldest tile in
-    // flight starts at `tail`, the next goes to `head`, or to the ring's start
-    // when it does not fit before the end.
-    const int ri = warp == 0 ? 0 : 1;
-    if (ri < L::kRings && elect_one()) {
-      const uint32_t size = (L::kEnd - ring) / L::kRings & ~1023u, ring_at = base + ring + ri * size;
-      const uint32_t full = base + L::kFull + ri * 8 * L::kSlots, empty = base + L::kEmpty + ri * 8 * L::kSlots;
-      volatile uint32_t* offs = reinterpret_cast<volatile uint32_t*>(sm + L::kOffs) + ri * L::kSlots;
-      volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + ri * L::kSlots;
-      uint32_t put = 0, freed = 0, head = 0, tail = 0, jobs = 0, sealed = 0;
-      bool wrapped = false;
-      // Keys that one query tile reads are read once; those that several read
-      // should stay in L2.
-      const uint64_t once = l2_policy_evict_first(), keep = w.items_q > 1 ? l2_policy_evict_normal() : once;
-      auto reserve = [&](uint32_t bytes, uint32_t& at) -> bool {
-        while (true) {
-          if (put == freed) {
-            head = tail = 0;
-            wrapped = false;
-          }
-          if (put - freed < L::kSlots) {
-            if (!wrapped && head + bytes <= size) break;
-            if (!wrapped && bytes <= tail) {
-              head = 0;
-              wrapped = true;
-              break;
+    if (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0 || warp == 3) {
+      // ------------------------------------------------------------- loads
+      // A thread per ring.  A ring is a FIFO of runs of bytes: the oldest tile in
+      // flight starts at `tail`, the next goes to `head`, or to the ring's start
+      // when it does not fit before the end.
+      const int ri = warp == 0 ? 0 : 1;
+      if (ri < L::kRings && elect_one()) {
+        const uint32_t size = (L::kEnd - ring) / L::kRings & ~1023u, ring_at = base + ring + ri * size;
+        const uint32_t full = base + L::kFull + ri * 8 * L::kSlots, empty = base + L::kEmpty + ri * 8 * L::kSlots;
+        volatile uint32_t* offs = reinterpret_cast<volatile uint32_t*>(sm + L::kOffs) + ri * L::kSlots;
+        volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + ri * L::kSlots;
+        uint32_t put = 0, freed = 0, head = 0, tail = 0, jobs = 0, sealed = 0;
+        uint32_t by_job = 0;                // slots whose tile the makers complete
+        bool wrapped = false;
+        // Keys that one query tile reads are read once; those that several read
+        // should stay in L2.
+        const uint64_t once = l2_policy_evict_first(), keep = w.items_q > 1 ? l2_policy_evict_normal() : once;
+        auto reserve = [&](uint32_t bytes, uint32_t& at) -> bool {
+          while (true) {
+            if (put == freed) {
+              head = tail = 0;
+              wrapped = false;
             }
-            if (wrapped && head + bytes <= tail) break;
-          }
-          if (!wait(empty + 8 * (freed % L::kSlots), (freed / L::kSlots) & 1)) return false;
-          if (++freed != put) {
-            const uint32_t t = offs[freed % L::kSlots];
-            if (t < tail) wrapped = false;
-            tail = t;
-          }
-        }
-        at = head;
-        head += bytes;
-        return true;
-      };
-      Segment s;
-      begin(s);
-      bool ok = true;
-      while (ok && advance(s)) {
-        const Item& it = s.it;
-        const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + it.h];
-        const int kb = hd.pool_kb;
-        const int64_t krow_b = hd.krow_b, vrow_b = hd.vrow_b;
-        const int64_t abase = hd.row_a + (int64_t)it.b * hd.cap_a, bbase = (int64_t)it.b * hd.cap_b;
-        const int32_t* pages = cv.max_pages > 0 ? page_row(cv, a.layer, it.b, it.h) : nullptr;
-        const int m0 = it.nA + it.nC;
-        if (ri == 0) {
-          if (s.idx > 0) ok = wait(base + L::kQEmpty, (s.idx - 1) & 1);
-          if (!ok) break;
-          const int nq = kDual && it.ntok > tq ? 2 : 1;
-          *reinterpret_cast<Segment*>(sm + L::kSeg + (s.idx & 1) * L::kSegBytes) = s;
-          mbar_arrive_expect_tx(base + L::kQFull, (uint32_t)(nq * w.box_tokens * G * kHeadDim * 2));
-          for (int x = 0; x < nq; ++x)
-            for (int part = 0; part < 2; ++part)
-              tma_load_3d(base + L::kQ + x * q_bytes + part * (q_bytes / 2), &maps.q, part * 64, it.h * G,
-                          it.b * a.n_max + it.i0 + x * tq, base + L::kQFull, once);
-        }
-        // first of the arrivals that complete a tile's slot, and the others
-        auto expect = [&](uint32_t bar, uint32_t bytes) {
-          if (L::kArrivals > 1) mbar_arrive_many(bar, L::kArrivals - 1);
-          mbar_arrive_expect_tx(bar, bytes);
-        };
-        auto load = [&](int j, bool isv, int32_t pg) -> bool {
-          const Tile t = tile_at(it, j);
-          const bool wide = isv || t.type <= kTileC || it.k == kHeadDim;
-          // (the codes of sealed keys on part of the channels land behind the tile)
-          const bool seal = kQuant && t.type == kTileM && t.r0 < it.nS * kTile;
-          // A tile's keys are waited for while the values before them are in use:
-          // keys never take more than the keys before them did, whose place they
-          // then find, so full-width ones take what sealed ones on 96 channels do.
-          uint32_t at, bytes = wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * (seal ? 3 : 2) * it.k);
-          if (kQuant && !isv && wide && w.kept_width == 96) bytes = kTile * 3 * 96;
-          if (!reserve(bytes, at)) return false;
-          const uint32_t slot = put % L::kSlots;
-          offs[slot] = at;
-          // what the other threads have to know of the tile
-          info[slot] = (ring_at + at) >> 4 | (uint32_t)t.rows << 16 | (wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
-          const uint32_t dst = ring_at + at, bar = full + 8 * slot;
-          ++put;
-          if (seal) {
-            // The codes land in the upper half of the tile's place, or behind it,
-            // their scales beside the job; the makers do the rest.
-            const uint32_t jn = jobs % L::kJobs, landed = base + L::kLanded + 8 * (ri * L::kJobs + jn);
-            if (jobs >= L::kJobs &&
-                !wait(base + L::kDone + 8 * (ri * L::kJobs + jn), (jobs / L::kJobs - 1) & 1)) return false;
-            const uint8_t* block = cv.qpool + hd.qoff +
-                                   (pages != nullptr ? (int64_t)max(0, pg)
-                                                     : (int64_t)it.b * hd.qblocks + t.r0 / kTile) * qblock_bytes(it.k);
-            const int width = isv ? kHeadDim : it.k, vn = (int)(sealed & 3);
-            const uint32_t codes = (uint32_t)(kTile * width), scales = isv ? kTile * 4u : (uint32_t)(4 * it.k);
-            const uint32_t sc = isv ? L::kVScale + (4 * ri + vn) * kTile * 4 : L::kKScale + (ri * L::kJobs + jn) * kTile * 4;
-            *reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes) =
-                Job{width, isv ? 1 : 0, slot, dst - base, sc};
-            mbar_arrive_expect_tx(landed, codes + scales);
-            bulk_load(dst + (wide ? 1 : 2) * codes, block + (isv ? qblock_voff(it.k) : 0), codes, landed, keep);
-            bulk_load(base + sc, block + (isv ? qblock_vsoff(it.k) : qblock_ksoff(it.k)), scales, landed, keep);
-            sealed += isv ? 1 : 0;
-            ++jobs;
-            return true;
-          }
-          if (t.type == kTileC) {
-            expect(bar, kWideBytes);
-            tma_load_4d(dst, isv ? &maps.v : &maps.k, 0, it.b * a.n_max + t.r0, 0, it.h, bar, keep);
-          } else if (t.type == kTileA) {
-            expect(bar, kWideBytes);
-            tma_load_3d(dst, &maps.pool[isv ? kPoolV : kPoolK128], 0, (int)(abase + t.r0), 0, bar, keep);
-          } else if (t.type == kTileM) {
-            const int64_t r = !kQuant && pages != nullptr ? (int64_t)max(0, pg) * kPageRows : bbase + t.r0 - (kQuant ? it.nS * kTile : 0);
-            if (isv) {
-              expect(bar, kWideBytes);
-              tma_load_3d(dst, &maps.pool[kPoolV], 0, (int)(vrow_b + r), 0, bar, keep);
-            } else {
-              expect(bar, (uint32_t)(kTile * 2 * it.k));
-              if (it.k == 32 || it.k == 64) tma_load_2d(dst, &maps.pool[kb], 0, (int)(krow_b + r), bar, keep);
-              else tma_load_3d(dst, &maps.pool[kb], 0, (int)(krow_b + r), 0, bar, keep);
+            if (put - freed < L::kSlots) {
+              if (!wrapped && head + bytes <= size) break;
+              if (!wrapped && bytes <= tail) {
+                head = 0;
+                wrapped = true;
+                break;
+              }
+              if (wrapped && head + bytes <= tail) break;
             }
-          } else {
-            // whole 16-row groups of each run of the image
-            const uint32_t rows = (uint32_t)((t.rows + 15) & ~15);
-            const uint8_t* image = far_tile(a, w, it.seq, it.h, t.r0 / kTile);
-            const int width = isv ? kHeadDim : it.k;
-            const uint32_t row = (width & 63) == 0 ? 128u : 64u;
-            const int runs = width * 2 / (int)row;
-            if (isv) image += kTile * 2 * it.k;
-            expect(bar, rows * row * runs);
-            for (int x = 0; x < runs; ++x)
-              bulk_load(dst + x * kTile * row, image + x * kTile * row, rows * row, bar, keep);
+            if (!wait(empty + 8 * (freed % L::kSlots), (freed / L::kSlots) & 1)) return false;
+            if (++freed != put) {
+              const uint32_t t = offs[freed % L::kSlots];
+              if (t < tail) wrapped = false;
+              tail = t;
+            }
           }
+          at = head;
+          head += bytes;
           return true;
         };
-        // page id of the middle tile that key tile j is, if any; read a tile
-        // before the loads that need it
-        auto page_at = [&](int j) -> int32_t {
-          return pages != nullptr && j >= m0 && j < m0 + (kQuant ? it.nS : it.nM) ? __ldcg(pages + (j - m0)) : 0;
-        };
-        constexpr int kStep = kDual ? 1 : 2;
-        const int j0 = s.t0 + (kDual ? 0 : ri);
-        int32_t page = page_at(j0);
-        for (int j = j0; ok && j < s.t1; j += kStep) {
-          const int32_t after = page_at(j + kStep);
-          ok = load(j, false, page) && load(j, true, page);
-          page = after;
-        }
-      }
-      if (kQuant) {
-        // the makers' last job: none
-        const uint32_t jn = jobs % L::kJobs;
-        if (jobs >= L::kJobs)
-          mbar_wait_bounded(base + L::kDone + 8 * (ri * L::kJobs + jn), (jobs / L::kJobs - 1) & 1, kDrainNs);
-        reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes)->width = 0;
-        mbar_arrive(base + L::kLanded + 8 * (ri * L::kJobs + jn));
-      }
-      if (ok && ri == 0 && (s.idx < 0 || wait(base + L::kQEmpty, s.idx & 1))) {
-        reinterpret_cast<Segment*>(sm + L::kSeg + ((s.idx + 1) & 1) * L::kSegBytes)->t1 = 0;
-        mbar_arrive(base + L::kQFull);
-      }
-      // copies still in flight must land before the block ends
-      if (!ok) {
-        for (uint32_t x = jobs > L::kJobs ? jobs - L::kJobs : 0; kQuant && x < jobs; ++x)
-          mbar_wait_bounded(base + L::kLanded + 8 * (ri * L::kJobs + x % L::kJobs), (x / L::kJobs) & 1, kDrainNs);
-        for (uint32_t x = freed; x < put; ++x)
-          mbar_wait_bounded(full + 8 * (x % L::kSlots), (x / L::kSlots) & 1, kDrainNs);
-        if (ri == 0 && s.idx >= 0) mbar_wait_bounded(base + L::kQFull, s.idx & 1, kDrainNs);
-      }
-    }
-  } else if (warp < 3) {
-    // -------------------------------------------------------------- MMAs
-    // A thread for each softmax group issues its scores S = Q K^T and outputs
-    // O += P V, half a key tile (64 keys) at a time: while the group works on
-    // one half, the other half's scores are made.  All instructions of the CTA
-    // come through one small cache, and this loop's from behind the group's, so
-    // that it costs what it is long: the loads leave each tile's address, rows
-    // and width as one word, and the halves are written out.
-    const int st = warp - 1;
-    if (elect_one()) {
-      constexpr uint32_t kDescS = mma_desc(128, kHalf, false), kDescO = mma_desc(128, kHeadDim, true);
-      constexpr uint32_t kWideHi = desc_hi(1024, kSwizzle128), kThinHi = desc_hi(512, kSwizzle64);
-      const uint32_t full = base + L::kFull + (kDual ? 0 : st * 8 * L::kSlots);
-      const uint32_t empty = base + L::kEmpty + (kDual ? 0 : st * 8 * L::kSlots);
-      volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + (kDual ? 0 : st * L::kSlots);
-      const uint32_t q_wide = desc_lo(16) | (base + L::kQ + (kDual ? st * kWideBytes : 0)) >> 4;
-      const uint32_t q_half = q_rows * 8, q_stripe = q_rows * 4;       // from 64 channels of q to the next, from 32
-      const uint32_t q_kept = desc_lo(16) | (base + q_kept_at + (kDual ? st * w.kept_bytes : 0)) >> 4;
-      const uint32_t s_at = tm_s + st * 128, o_at = tm_o + st * 128;
-      const uint32_t s_full = base + L::kSFull + 16 * st, p_full = base + L::kPFull + 16 * st,
-                     o_full = base + L::kOFull + 8 * st;
-      uint32_t taken = 0, gathered = 0, phase = 0;   // ring tiles before this segment; of the P barriers
-      bool ok = true;
-      for (int idx = 0; ok; ++idx) {
-        ok = wait(base + L::kQFull, idx & 1);
-        const Segment& s = segment(idx);
-        if (!ok || s.t1 == 0) break;
-        // this ring's key tiles
-        const int mine = kDual ? s.t1 - s.t0 : (s.t1 - s.t0 - st + 1) / 2;
-        const uint32_t end = taken + 2 * mine;
-        if (kDual && st == 1 && s.it.ntok <= tq) {
-          // no second query tile: its share of the releases
-          mbar_arrive(base + L::kQEmpty);
-          for (uint32_t e = taken; ok && e < end; ++e) {
-            ok = wait(full + 8 * (e % L::kSlots), (e / L::kSlots) & 1);
-            if (ok) mbar_arrive(empty + 8 * (e % L::kSlots));
+        Segment s;
+        begin(s);
+        bool ok = true;
+        while (ok && advance(s)) {
+          const Item& it = s.it;
+          const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + it.h];
+          const int kb = hd.pool_kb;
+          const int64_t krow_b = hd.krow_b, vrow_b = hd.vrow_b;
+          const int64_t abase = hd.row_a + (int64_t)it.b * hd.cap_a, bbase = (int64_t)it.b * hd.cap_b;
+          const int32_t* pages = cv.max_pages > 0 ? page_row(cv, a.layer, it.b, it.h) : nullptr;
+          const int m0 = it.nA + it.nC;
+          if (ri == 0) {
+            if (s.idx > 0) ok = wait(base + L::kQEmpty, (s.idx - 1) & 1);
+            if (!ok) break;
+            const int nq = kDual && it.ntok > tq ? 2 : 1;
+            *reinterpret_cast<Segment*>(sm + L::kSeg + (s.idx & 1) * L::kSegBytes) = s;
+            mbar_arrive_expect_tx(base + L::kQFull, (uint32_t)(nq * w.box_tokens * G * kHeadDim * 2));
+            for (int x = 0; x < nq; ++x)
+              for (int part = 0; part < 2; ++part)
+                tma_load_3d(base + L::kQ + x * q_bytes + part * (q_bytes / 2), &maps.q, part * 64, it.h * G,
+                            it.b * a.n_max + it.i0 + x * tq, base + L::kQFull, once);
           }
-          taken = end;
-          continue;
-        }
-        bool have_kept = !gathers(s);
-        auto enter = [&](uint32_t e, uint32_t& what) -> bool {
-          const uint32_t slot = e % L::kSlots;
-          if (!wait(full + 8 * slot, (e / L::kSlots) & 1)) return false;
-          what = info[slot];
-          return true;
-        };
-        auto enter_k = [&](uint32_t e, uint32_t& what) -> bool {
-          if (!enter(e, what)) return false;
-          if (!have_kept && what >> 24 != 3) {
-            have_kept = true;
-            return wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
-          }
-          return true;
-        };
-        auto scores = [&](uint32_t what, auto which) {
-          constexpr int kWhich = decltype(which)::value;
-          const uint32_t d = s_at + kWhich * kHalf, k0 = desc_lo(16) | (what & 0x3fff), width = what >> 24;
-          auto run = [&](auto steps, uint32_t q) {
-            constexpr int kSteps = decltype(steps)::value;
-            constexpr bool kThin = kSteps == 2 || kSteps == 6;
-            constexpr uint32_t kHi = kThin ? kThinHi : kWideHi;
-            const uint32_t k = k0 + kWhich * kHalf * (kThin ? 4 : 8);
-            mma_ss<kHi, false>(d, q, k, kDescS);
-#pragma unroll
-            for (int y = 1; y < kSteps; ++y) {
-              const uint32_t at = kThin ? (y >> 1) * (kTile * 4) + (y & 1) * 2 : (y >> 2) * (kTile * 8) + (y & 3) * 2;
-              const uint32_t q_at = kThin ? (y >> 1) * q_stripe + (y & 1) * 2 : (y >> 2) * q_half + (y & 3) * 2;
-              mma_ss<kHi, true>(d, q + q_at, k + at, kDescS);
-            }
+          // first of the arrivals that complete a tile's slot, and the others
+          auto expect = [&](uint32_t bar, uint32_t bytes) {
+            if (L::kArrivals > 1) mbar_arrive_many(bar, L::kArrivals - 1);
+            mbar_arrive_expect_tx(bar, bytes);
           };
-          if (width == 0) run(std::integral_constant<int, 2>(), q_kept);
-          else if (width == 3) run(std::integral_constant<int, 8>(), q_wide);
-          else if (width == 1) run(std::integral_constant<int, 4>(), q_kept);
-          else run(std::integral_constant<int, 6>(), q_kept);
-          mma_commit(s_full + 8 * kWhich);
-        };
-        auto values = [&](uint32_t what, auto which, bool accumulate) {
-          constexpr int kWhich = decltype(which)::value;
-          const uint32_t p = s_at + kWhich * kHalf;
-          const uint32_t v = (desc_lo(kWideBytes / 2) | (what & 0x3fff)) + kWhich * kHalf * 8;
-          const int left = (int)(what >> 16 & 0xff) - kWhich * kHalf;
-          if (left >= kHalf) {
-#pragma unroll
-            for (int y = 0; y < kHalf / 16; ++y)
-              mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, kDescO, accumulate || y > 0);
-          } else {
-#pragma unroll 1
-            for (int y = 0; y < (left + 15) / 16; ++y)
-              mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, kDescO, accumulate || y > 0);
+          auto load = [&](int j, bool isv, int32_t pg) -> bool {
+            const Tile t = tile_at(it, j);
+            const bool wide = isv || t.type <= kTileC || it.k == kHeadDim;
+            // (the codes of sealed keys on part of the channels land behind the tile)
+            const bool seal = kQuant && t.type == kTileM && t.r0 < it.nS * kTile;
+            // A tile's keys are waited for while the values before them are in use:
+            // keys never take more than the keys before them did, whose place they
+            // then find, so full-width ones take what sealed ones on 96 channels do.
+            uint32_t at, bytes = wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * (seal ? 3 : 2) * it.k);
+            if (kQuant && !isv && wide && w.kept_width == 96) bytes = kTile * 3 * 96;
+            if (!reserve(bytes, at)) return false;
+            const uint32_t slot = put % L::kSlots;
+            offs[slot] = at;
+            // what the other threads have to know of the tile
+            info[slot] = (ring_at + at) >> 4 | (uint32_t)t.rows << 16 | (wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
+            const uint32_t dst = ring_at + at, bar = full + 8 * slot;
+            ++put;
+            by_job = (by_job & ~(1u << slot)) | (seal ? 1u << slot : 0u);
+            if (seal) {
+              // The codes land in the upper half of the tile's place, or behind it,
+              // their scales beside the job; the makers do the rest.
+              const uint32_t jn = jobs % L::kJobs, landed = base + L::kLanded + 8 * (ri * L::kJobs + jn);
+              if (jobs >= L::kJobs &&
+                  !wait(base + L::kDone + 8 * (ri * L::kJobs + jn), (jobs / L::kJobs - 1) & 1)) return false;
+              const uint8_t* block = cv.qpool + hd.qoff +
+                                     (pages != nullptr ? (int64_t)max(0, pg)
+                                                       : (int64_t)it.b * hd.qblocks + t.r0 / kTile) * qblock_bytes(it.k);
+              const int width = isv ? kHeadDim : it.k, vn = (int)(sealed & 3);
+              const uint32_t codes = (uint32_t)(kTile * width), scales = isv ? kTile * 4u : (uint32_t)(4 * it.k);
+              const uint32_t sc = isv ? L::kVScale + (4 * ri + vn) * kTile * 4 : L::kKScale + (ri * L::kJobs + jn) * kTile * 4;
+              *reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes) =
+                  Job{width, isv ? 1 : 0, slot, dst - base, sc};
+              mbar_arrive_expect_tx(landed, codes + scales);
+              bulk_load(dst + (wide ? 1 : 2) * codes, block + (isv ? qblock_voff(it.k) : 0), codes, landed, keep);
+              bulk_load(base + sc, block + (isv ? qblock_vsoff(it.k) : qblock_ksoff(it.k)), scales, landed, keep);
+              sealed += isv ? 1 : 0;
+              ++jobs;
+              return true;
+            }
+            if (t.type == kTileC) {
+              expect(bar, kWideBytes);
+              tma_load_4d(dst, isv ? &maps.v : &maps.k, 0, it.b * a.n_max + t.r0, 0, it.h, bar, keep);
+            } else if (t.type == kTileA) {
+              expect(bar, kWideBytes);
+              tma_load_3d(dst, &maps.pool[isv ? kPoolV : kPoolK128], 0, (int)(abase + t.r0), 0, bar, keep);
+            } else if (t.type == kTileM) {
+              const int64_t r = !kQuant && pages != nullptr ? (int64_t)max(0, pg) * kPageRows : bbase + t.r0 - (kQuant ? it.nS * kTile : 0);
+              if (isv) {
+                expect(bar, kWideBytes);
+                tma_load_3d(dst, &maps.pool[kPoolV], 0, (int)(vrow_b + r), 0, bar, keep);
+              } else {
+                expect(bar, (uint32_t)(kTile * 2 * it.k));
+                if (it.k == 32 || it.k == 64) tma_load_2d(dst, &maps.pool[kb], 0, (int)(krow_b + r), bar, keep);
+                else tma_load_3d(dst, &maps.pool[kb], 0, (int)(krow_b + r), 0, bar, keep);
+              }
+            } else {
+              // whole 16-row groups of each run of the image
+              const uint32_t rows = (uint32_t)((t.rows + 15) & ~15);
+              const uint8_t* image = far_tile(a, w, it.seq, it.h, t.r0 / kTile);
+              const int width = isv ? kHeadDim : it.k;
+              const uint32_t row = (width & 63) == 0 ? 128u : 64u;
+              const int runs = width * 2 / (int)row;
+              if (isv) image += kTile * 2 * it.k;
+              expect(bar, rows * row * runs);
+              for (int x = 0; x < runs; ++x)
+                bulk_load(dst + x * kTile * row, image + x * kTile * row, rows * row, bar, keep);
+            }
+            return true;
+          };
+          // page id of the middle tile that key tile j is, if any; read a tile
+          // before the loads that need it
+          auto page_at = [&](int j) -> int32_t {
+            return pages != nullptr && j >= m0 && j < m0 + (kQuant ? it.nS : it.nM) ? __ldcg(pages + (j - m0)) : 0;
+          };
+          constexpr int kStep = kDual ? 1 : 2;
+          const int j0 = s.t0 + (kDual ? 0 : ri);
+          int32_t page = page_at(j0);
+          for (int j = j0; ok && j < s.t1; j += kStep) {
+            const int32_t after = page_at(j + kStep);
+            ok = load(j, false, page) && load(j, true, page);
+            page = after;
           }
-          mma_commit(o_full);
-        };
-        const std::integral_constant<int, 0> h0;
-        const std::integral_constant<int, 1> h1;
-        // all scores are issued: q can go once they are done (and the gathered q
-        // must have been seen even if none of these tiles needed it)
-        auto q_read = [&]() {
-          if (!have_kept) ok = wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
-          if (ok) mma_commit(base + L::kQEmpty);
-        };
-        uint32_t k = 0, v = 0;
-        if (mine > 0) {
-          ok = enter_k(taken, k);
-          if (!ok) break;
-          tc_fence_after();
-          scores(k, h0);
-          scores(k, h1);
-          mma_commit(empty + 8 * (taken % L::kSlots));
         }
-        if (mine <= 1) q_read();
-        for (uint32_t e = taken; ok && e < end; e += 2) {
-          const bool more = e + 2 < end;
-          ok = enter(e + 1, v) && (!more || enter_k(e + 2, k)) && wait(p_full, phase);
-          if (!ok) break;
-          tc_fence_after();
-          values(v, h0, e != taken);
-          // (scores overwrite the P that the product before them reads, and run
-          // after it)
-          if (more) scores(k, h0);
-          ok = wait(p_full + 8, phase);
-          if (!ok) break;
-          tc_fence_after();
-          values(v, h1, true);
-          mma_commit(empty + 8 * ((e + 1) % L::kSlots));
-          if (more) {
-            scores(k, h1);
-            mma_commit(empty + 8 * ((e + 2) % L::kSlots));
-            if (e + 4 >= end) q_read();
-          }
-          phase ^= 1;
+        if (kQuant) {
+          // the makers' last job: none
+          const uint32_t jn = jobs % L::kJobs;
+          if (jobs >= L::kJobs)
+            mbar_wait_bounded(base + L::kDone + 8 * (ri * L::kJobs + jn), (jobs / L::kJobs - 1) & 1, kDrainNs);
+          reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes)->width = 0;
+          mbar_arrive(base + L::kLanded + 8 * (ri * L::kJobs + jn));
         }
-        if (ok && mine > 0) mma_commit(base + L::kOEnd + 8 * st);
-        taken = end;
+        if (ok && ri == 0 && (s.idx < 0 || wait(base + L::kQEmpty, s.idx & 1))) {
+          reinterpret_cast<Segment*>(sm + L::kSeg + ((s.idx + 1) & 1) * L::kSegBytes)->t1 = 0;
+          mbar_arrive(base + L::kQFull);
+        }
+        // copies still in flight must land before the block ends
+        if (!ok) {
+          for (uint32_t x = jobs > L::kJobs ? jobs - L::kJobs : 0; kQuant && x < jobs; ++x)
+            mbar_wait_bounded(base + L::kLanded + 8 * (ri * L::kJobs + x % L::kJobs), (x / L::kJobs) & 1, kDrainNs);
+          for (uint32_t x = freed; x < put; ++x)
+            if ((by_job >> x % L::kSlots & 1) == 0)
+              mbar_wait_bounded(full + 8 * (x % L::kSlots), (x / L::kSlots) & 1, kDrainNs);
+          if (ri == 0 && s.idx >= 0) mbar_wait_bounded(base + L::kQFull, s.idx & 1, kDrainNs);
+        }
       }
-      if (!ok) {
-        mma_commit(base + L::kDrain + 8 * st);
-        mbar_wait_bounded(base + L::kDrain + 8 * st, 0, kDrainNs);
+    } else if (warp < 3) {
+      // -------------------------------------------------------------- MMAs
+      // A thread for each softmax group issues its scores S = Q K^T and outputs
+      // O += P V, half a key tile (64 keys) at a time: while the group works on
+      // one half, the other half's scores are made.  The group waits for these few
+      // instructions, so the loop is kept short: the loads leave each tile's
+      // address, rows and width as one word, descriptors are constants plus an
+      // offset, and the two halves are written out.  (A thread for each group
+      // instead of one for both: 340 -> 270 us for two prompts of 4096 tokens.)
+      const int st = warp - 1;
+      if (elect_one()) {
+        constexpr uint32_t kDescS = mma_desc(128, kHalf, false), kDescO = mma_desc(128, kHeadDim, true);
+        constexpr uint32_t kWideHi = desc_hi(1024, kSwizzle128), kThinHi = desc_hi(512, kSwizzle64);
+        const uint32_t full = base + L::kFull + (kDual ? 0 : st * 8 * L::kSlots);
+        const uint32_t empty = base + L::kEmpty + (kDual ? 0 : st * 8 * L::kSlots);
+        volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + (kDual ? 0 : st * L::kSlots);
+        const uint32_t q_wide = desc_lo(16) | (base + L::kQ + (kDual ? st * kWideBytes : 0)) >> 4;
+        const uint32_t q_half = q_rows * 8, q_stripe = q_rows * 4;       // from 64 channels of q to the next, from 32
+        const uint32_t q_kept = desc_lo(16) | (base + q_kept_at + (kDual ? st * w.kept_bytes : 0)) >> 4;
+        const uint32_t s_at = tm_s + st * 128, o_at = tm_o + st * 128;
+        const uint32_t s_full = base + L::kSFull + 16 * st, p_full = base + L::kPFull + 16 * st,
+                       o_full = base + L::kOFull + 8 * st;
+        uint32_t taken = 0, gathered = 0, phase = 0;   // ring tiles before this segment; of the P barriers
+        bool ok = true;
+        for (int idx = 0; ok; ++idx) {
+          ok = wait(base + L::kQFull, idx & 1);
+          const Segment& s = segment(idx);
+          if (!ok || s.t1 == 0) break;
+          // this ring's key tiles
+          const int mine = kDual ? s.t1 - s.t0 : (s.t1 - s.t0 - st + 1) / 2;
+          const uint32_t end = taken + 2 * mine;
+          if (kDual && st == 1 && s.it.ntok <= tq) {
+            // no second query tile: its share of the releases
+            mbar_arrive(base + L::kQEmpty);
+            for (uint32_t e = taken; ok && e < end; ++e) {
+              ok = wait(full + 8 * (e % L::kSlots), (e / L::kSlots) & 1);
+              if (ok) mbar_arrive(empty + 8 * (e % L::kSlots));
+            }
+            taken = end;
+            continue;
+          }
+          bool have_kept = !gathers(s);
+          auto enter = [&](uint32_t e, uint32_t& what) -> bool {
+            const uint32_t slot = e % L::kSlots;
+            if (!wait(full + 8 * slot, (e / L::kSlots) & 1)) return false;
+            what = info[slot];
+            return true;
+          };
+          auto enter_k = [&](uint32_t e, uint32_t& what) -> bool {
+            if (!enter(e, what)) return false;
+            if (!have_kept && what >> 24 != 3) {
+              have_kept = true;
+              return wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
+            }
+            return true;
+          };
+          auto scores = [&](uint32_t what, auto which) {
+            constexpr int kWhich = decltype(which)::value;
+            const uint32_t d = s_at + kWhich * kHalf, k0 = desc_lo(16) | (what & 0x3fff), width = what >> 24;
+            auto run = [&](auto steps, uint32_t q) {
+              constexpr int kSteps = decltype(steps)::value;
+              constexpr bool kThin = kSteps == 2 || kSteps == 6;
+              constexpr uint32_t kHi = kThin ? kThinHi : kWideHi;
+              const uint32_t k = k0 + kWhich * kHalf * (kThin ? 4 : 8);
+              mma_ss<kHi, false>(d, q, k, kDescS);
+#pragma unroll
+              for (int y = 1; y < kSteps; ++y) {
+                const uint32_t at = kThin ? (y >> 1) * (kTile * 4) + (y & 1) * 2 : (y >> 2) * (kTile * 8) + (y & 3) * 2;
+                const uint32_t q_at = kThin ? (y >> 1) * q_stripe + (y & 1) * 2 : (y >> 2) * q_half + (y & 3) * 2;
+                mma_ss<kHi, true>(d, q + q_at, k + at, kDescS);
+              }
+            };
+            if (width == 0) run(std::integral_constant<int, 2>(), q_kept);
+            else if (width == 3) run(std::integral_constant<int, 8>(), q_wide);
+            else if (width == 1) run(std::integral_constant<int, 4>(), q_kept);
+            else run(std::integral_constant<int, 6>(), q_kept);
+            mma_commit(s_full + 8 * kWhich);
+          };
+          auto values = [&](uint32_t what, auto which, bool accumulate) {
+            constexpr int kWhich = decltype(which)::value;
+            const uint32_t p = s_at + kWhich * kHalf;
+            const uint32_t v = (desc_lo(kWideBytes / 2) | (what & 0x3fff)) + kWhich * kHalf * 8;
+            const int left = (int)(what >> 16 & 0xff) - kWhich * kHalf;
+            if (left >= kHalf) {
+#pragma unroll
+              for (int y = 0; y < kHalf / 16; ++y)
+                mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, kDescO, accumulate || y > 0);
+            } else {
+#pragma unroll 1
+              for (int y = 0; y < (left + 15) / 16; ++y)
+                mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, kDescO, accumulate || y > 0);
+            }
+            mma_commit(o_full);
+          };
+          const std::integral_constant<int, 0> h0;
+          const std::integral_constant<int, 1> h1;
+          // all scores are issued: q can go once they are done (and the gathered q
+          // must have been seen even if none of these tiles needed it)
+          auto q_read = [&]() {
+            if (!have_kept) ok = wait(base + L::kQKFull + (kDual ? 8 * st : 0), gathered++ & 1);
+            if (ok) mma_commit(base + L::kQEmpty);
+          };
+          uint32_t k = 0, v = 0;
+          if (mine > 0) {
+            ok = enter_k(taken, k);
+            if (!ok) break;
+            tc_fence_after();
+            scores(k, h0);
+            scores(k, h1);
+            mma_commit(empty + 8 * (taken % L::kSlots));
+          }
+          if (mine <= 1) q_read();
+          for (uint32_t e = taken; ok && e < end; e += 2) {
+            const bool more = e + 2 < end;
+            ok = enter(e + 1, v) && (!more || enter_k(e + 2, k)) && wait(p_full, phase);
+            if (!ok) break;
+            tc_fence_after();
+            values(v, h0, e != taken);
+            // (scores overwrite the P that the product before them reads, and run
+            // after it)
+            if (more) scores(k, h0);
+            ok = wait(p_full + 8, phase);
+            if (!ok) break;
+            tc_fence_after();
+            values(v, h1, true);
+            mma_commit(empty + 8 * ((e + 1) % L::kSlots));
+            if (more) {
+              scores(k, h1);
+              mma_commit(empty + 8 * ((e + 2) % L::kSlots));
+              if (e + 4 >= end) q_read();
+            }
+            phase ^= 1;
+          }
+          if (ok && mine > 0) mma_commit(base + L::kOEnd + 8 * st);
+          taken = end;
+        }
+        if (!ok) {
+          mma_commit(base + L::kDrain + 8 * st);
+          mbar_wait_bounded(base + L::kDrain + 8 * st, 0, kDrainNs);
+        }
       }
     }
-  }
   } else {
     // (registers: 256 x 88 + 256 x 168 = 65536 of the 512 x 128 launched with)
     if (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
@@ -1294,7 +1310,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 // such CTA, its partials are CTA i - 1's last one and the first ones of CTA
 // i, i + 1, ... while they start inside the same item.  8 rows a block, a warp
 // a row: the lanes read the row's (m, l) of all partials at once (32 at a
-// time), then the warp its outputs, eight partials in flight.
+// time), then the warp its outputs, eight partials in flight (one sequence of
+// 32768 tokens: 150 partials; 40 -> 34 us with this and the plan's bisection).
 constexpr int kMergeRows = 8;
 __global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const __grid_constant__ ChunkArgs a,
                                                                       const ChunkWork w) {

@@ -102,6 +102,7 @@ struct ChunkArgs {
   int64_t q_stride, k_stride, v_stride;
   const int32_t* ids;       // [B][n_max] or null
   uint16_t* o;              // bf16 [B][n_max][Hq][128]
+  int32_t* ticket;          // append: the layer's count of blocks done, zero between launches
   uint64_t wait_limit_ns;   // bound of every mbarrier wait
   int32_t lens[kChunkSeqs]; // new tokens of sequence b0 + i
 };

@@ -389,9 +389,9 @@ lk_status lk_step_layers_host_packed(lk_cache cache, int32_t layer0, int32_t nla
  *   k, v       device bf16 [B][n_max][Hkv][128]
  *   ids        device int32 [B][n_max] or NULL (no token is special)
  *   lens       host int32 [B], each in [0, n_max], or NULL (n_max each); read
- *              before the call returns.  Rows past lens[b] are never read and,
- *              in the output, never written.
- *   n_max      tokens per sequence of the tensors
+ *              before the call returns.  What rows past lens[b] hold
+ *              never matters; in the output they are never written.
+ *   n_max      tokens per sequence of the tensors, at most 2^28
  *   *_stride   elements between consecutive tokens of q, k and v: at least
  *              heads * 128 and a multiple of 8, or 0 for dense rows.  A row's
  *              heads are dense, so q, k and v may be views of one projection's
@@ -429,10 +429,14 @@ lk_status lk_chunk_workspace_bytes(lk_plan plan, int32_t batch, int32_t n_max, s
  * Middle tokens are read as the cache holds them when the call runs: sealed
  * INT8 / FP8 blocks as their dequantised values, everything else, the chunk's
  * own tokens included, in bf16.
- * k, v and the cache must hold finite values.  workspace: >=
- * lk_chunk_workspace_bytes bytes, 256-byte aligned.  Errors: LK_ERR_ARG,
- * LK_ERR_ALIGN (16 bytes for q, k, v, o; 4 for ids), LK_ERR_CAPACITY
- * (workspace), LK_ERR_STATE (the current device is not the cache's). */
+ * k, v and the cache must hold finite values; o must not overlap the inputs.
+ * workspace: >= lk_chunk_workspace_bytes bytes, 256-byte aligned.  Calls on one
+ * cache may overlap on the GPU if each has its own workspace and nothing
+ * appends to the layer meanwhile.  A captured call keeps the lens it was given;
+ * the tokens held are those of the replay.  Errors: LK_ERR_ARG, LK_ERR_ALIGN (16
+ * bytes for q, k, v, o; 4 for ids), LK_ERR_CAPACITY (workspace), LK_ERR_STATE
+ * (the current device is not the cache's), LK_ERR_UNSUPPORTED (n_max, B n_max
+ * or a position too large), LK_ERR_CUDA (a launch, or the driver's tensor maps). */
 lk_status lk_chunk_attn(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* o, void* workspace,
                         size_t ws_bytes, void* stream);
 
@@ -441,7 +445,9 @@ lk_status lk_chunk_attn(lk_cache cache, int32_t layer, const lk_chunk* chunk, vo
  * many lk_append calls would leave it (a paged cache may hand out its free
  * pages in another order).  Errors as lk_chunk_attn; LK_ERR_CAPACITY when an
  * active sequence would exceed capacity_tokens or a paged cache has too few
- * free pages (nothing is launched then). */
+ * free pages (nothing is launched then).  Appends to different layers of a
+ * contiguous cache may overlap on the GPU; k and v must not be rows of the
+ * cache. */
 lk_status lk_append_chunk(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* stream);
 
 /* lk_chunk_attn, then lk_append_chunk of the same chunk: what lk_step does for
@@ -542,9 +548,10 @@ lk_status lk_step_is_fused(lk_cache cache, int32_t layer0, int32_t nlayers, int3
 lk_status lk_set_decode_ctas(lk_cache cache, int32_t ctas);
 
 /* Bound of the decode kernel's waits on its stage ring and on its warps'
- * segment barriers, in ns (default 1 s; at most 10 s).  A wait that runs out
- * records LK_ERR_TIMEOUT for lk_check and the launch's outputs are garbage;
- * after it, call lk_workspace_init before the next decode.  0 makes every
+ * segment barriers, and of chunk attention's waits, in ns (default 1 s; at
+ * most 10 s).  A wait that runs out records LK_ERR_TIMEOUT for lk_check and the
+ * launch's outputs are garbage; after it, call lk_workspace_init before the
+ * next decode (chunk attention's workspace needs nothing).  0 makes every
  * wait that is not already complete run out at once: a way to exercise that
  * failure path without a fault.  The kernel's final wait for its own copies
  * to land keeps its 1 s bound whatever this is.  Errors: LK_ERR_ARG. */
