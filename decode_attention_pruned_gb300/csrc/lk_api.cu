@@ -305,7 +305,7 @@ WsLayout ws_layout(const lk_plan_desc& d, int B) {
 // CTA starts, special-token flags, partials, F tile images.  `layer` < 0:
 // what any layer needs.
 struct ChunkLayout {
-  size_t off_special, off_ml, off_part, off_far, total;
+  size_t off_cut, off_special, off_ml, off_part, off_far, total;
   ChunkWork w;
 };
 ChunkLayout chunk_layout(const lk_plan_s& p, int B, int n_max, int layer, int ctas) {
@@ -343,6 +343,8 @@ ChunkLayout chunk_layout(const lk_plan_s& p, int B, int n_max, int layer, int ct
   w.special_seqs = special ? seqs : 0;
   w.special_words = special ? (int)(4 * tiles) : 0;
   size_t off = align_up((kChunkMaxCtas + 2) * sizeof(int2), 256);
+  c.off_cut = off;
+  off = align_up(off + (size_t)w.max_ctas * sizeof(int4), 256);
   c.off_special = off;
   off = align_up(off + (size_t)w.special_seqs * w.special_words * 4, 256);
   c.off_ml = off;
@@ -1367,6 +1369,7 @@ lk_status chunk_attn_prepare(lk_cache cache, void* o, void* workspace, size_t ws
   w.cost_kept = w.dual ? (sealed ? 172 : 160) : (sealed ? 200 : 84);
   w.cost_k = w.dual ? (sealed ? 19 : 3) : (sealed ? 21 : 13);
   w.start = reinterpret_cast<int2*>(ws);
+  w.cut = reinterpret_cast<int4*>(ws + lay.off_cut);
   w.special = reinterpret_cast<uint32_t*>(ws + lay.off_special);
   w.part_ml = reinterpret_cast<float2*>(ws + lay.off_ml);
   w.part = reinterpret_cast<float*>(ws + lay.off_part);

@@ -219,13 +219,7 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
   s_off[tid] = off;
   __syncthreads();
   const uint64_t P = max((uint64_t)1, min((uint64_t)w.max_ctas, C / kMinCtaCost));
-  if (tid == 0) {
-    w.start[w.max_ctas + 1] = make_int2((int)P, 0);
-    w.start[P] = make_int2(E, 0);
-    if (C == 0) w.start[0] = make_int2(E, 0);
-  }
   static_assert(kChunkMaxCtas <= kPlanThreads, "a thread per CTA");
-  if (tid >= P || C == 0) return;
   const uint64_t x = (uint64_t)tid * C / P;
   int run = 0;                            // the last run that starts at or before x
 #pragma unroll
@@ -233,7 +227,8 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
     if (s_off[run + d] <= x) run += d;
   // (runs without tiles share the next one's start: the bisection ends behind them)
   uint64_t at = s_off[run];
-  for (int e = run * per; e < E; ++e) {
+  int2 start = make_int2(E, 0);
+  for (int e = run * per; e < E && tid < P; ++e) {
     if (!item_info(a, w, e, it)) continue;
     const uint64_t end = at + item_cost(w, it);
     if (x < end) {
@@ -242,11 +237,28 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
       const uint32_t kept = cost_kept(w, it);
       const int t = (int)(r <= wide ? (r + w.cost_wide - 1) / w.cost_wide
                                     : it.nA + it.nC + (r - wide + kept - 1) / kept);
-      w.start[tid] = t < tiles_of(it) ? make_int2(e, t) : make_int2(e + 1, 0);
+      start = t < tiles_of(it) ? make_int2(e, t) : make_int2(e + 1, 0);
       break;
     }
     at = end;
   }
+  if (tid <= P) w.start[tid] = start;
+  // The items that are cut: thread c tells of the one that CTA c starts inside of
+  // if CTA c - 1 holds its first tiles.  (Later starts in the same item follow.)
+  __shared__ int2 s_start[kPlanThreads + 1];
+  __shared__ int s_cut;
+  if (tid == 0) s_cut = 0;
+  s_start[tid] = start;
+  __syncthreads();
+  if (tid > 0 && tid < P && start.y > 0 && (s_start[tid - 1].x != start.x || s_start[tid - 1].y == 0)) {
+    int last = tid;                       // the last CTA that starts there
+#pragma unroll
+    for (int d = kPlanThreads / 2; d > 0; d >>= 1)
+      if (last + d < (int)P && s_start[last + d].x == start.x) last += d;
+    w.cut[atomicAdd(&s_cut, 1)] = make_int4(tid - 1, last - tid + 2, start.x, 0);
+  }
+  __syncthreads();
+  if (tid == 0) w.start[w.max_ctas + 1] = make_int2((int)P, s_cut);
 }
 
 __device__ void plan_special(const ChunkArgs& a, const ChunkWork& w, int seq) {
@@ -1259,7 +1271,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       w0 *= inv;
       w1 *= inv;
       const int slot = 2 * cta + (s.t0 == 0 ? 1 : 0);
-      const int64_t prow = (int64_t)slot * w.part_rows + (kDual ? st * kTile : 0) + row;
+      const int prow = (kDual ? st * kTile : 0) + row;
+      float4* part = reinterpret_cast<float4*>(w.part) + (int64_t)slot * 32 * w.part_rows + prow;
       uint16_t* out = a.o + (((int64_t)it.b * a.n_max + i) * cv.Hq + it.h * G + g) * kHeadDim;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
@@ -1284,12 +1297,12 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             dst[z] = make_uint4(pack_bf16x2(y[8 * z], y[8 * z + 1]), pack_bf16x2(y[8 * z + 2], y[8 * z + 3]),
                                 pack_bf16x2(y[8 * z + 4], y[8 * z + 5]), pack_bf16x2(y[8 * z + 6], y[8 * z + 7]));
         } else {
-          float4* dst = reinterpret_cast<float4*>(w.part + prow * kHeadDim + 32 * c);
 #pragma unroll
-          for (int z = 0; z < 8; ++z) dst[z] = make_float4(y[4 * z], y[4 * z + 1], y[4 * z + 2], y[4 * z + 3]);
+          for (int z = 0; z < 8; ++z)
+            part[(8 * c + z) * w.part_rows] = make_float4(y[4 * z], y[4 * z + 1], y[4 * z + 2], y[4 * z + 3]);
         }
       }
-      if (mine && !s.whole) w.part_ml[prow] = make_float2(m, l);
+      if (mine && !s.whole) w.part_ml[(int64_t)slot * w.part_rows + prow] = make_float2(m, l);
       tc_fence_before();
       if (!kDual && two) {
         __syncwarp();
@@ -1306,71 +1319,120 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 }
 
 // ----------------------------------------------------------------- merge
-// Block (i - 1, y): if the item that CTA i starts inside of has no earlier
-// such CTA, its partials are CTA i - 1's last one and the first ones of CTA
-// i, i + 1, ... while they start inside the same item.  8 rows a block, a warp
-// a row: the lanes read the row's (m, l) of all partials at once (32 at a
-// time), then the warp its outputs, eight partials in flight (one sequence of
-// 32768 tokens: 150 partials; 40 -> 34 us with this and the plan's bisection).
-constexpr int kMergeRows = 8;
-__global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const __grid_constant__ ChunkArgs a,
-                                                                      const ChunkWork w) {
+// An item that is cut between CTAs c, c + 1, ...: CTA c's last partial and the
+// others' first ones.  A block takes 8 kRows rows of it at a time: its warps
+// make the rows' weights out of their (m, l), 32 partials at once, then a thread
+// adds up four channels of kRows rows, kAhead partials of each in flight.
+// Partials lie channel group by channel group, the rows of each side by side,
+// as the attention's threads, a row each, write them in whole lines (a row at a
+// time: 5 us of every CTA's time instead of 1).  The grid is one wave that goes
+// through a list: 1200 blocks of which most found nothing to do took 7 us.
+template <int kRows>
+__global__ void __launch_bounds__(256, kRows == 1 ? 2 : 3) chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const ChunkWork w) {
+  constexpr int kAhead = kRows == 1 ? 16 : 2;
+  __shared__ float s_e[8 * kRows][33], s_f[8 * kRows], s_inv[8 * kRows];
+  __shared__ int s_cut;
+  __shared__ int4 s_item;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int P = __ldcg(&w.start[w.max_ctas + 1].x), i = blockIdx.x + 1;
-  if (i >= P) return;
-  const int lane = threadIdx.x & 31;
-  const int2 at = __ldcg(&w.start[i]), before = __ldcg(&w.start[i - 1]);
-  if (at.y == 0 || (before.x == at.x && before.y > 0)) return;
-  Item it;
-  if (!item_info(a, w, at.x, it)) return;
-  const int row = blockIdx.y * kMergeRows + threadIdx.x / 32;
-  const int stream = row / kTile, r = row % kTile;
-  const int tok = r / a.cv.G, q = stream * w.tile_tokens + tok;
-  if (tok >= w.tile_tokens || q >= it.ntok) return;
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c0 = i - 1; c0 < P; c0 += 32) {
-    const int c = c0 + lane;
-    bool in = c < P;
-    if (in && c >= i) {
-      const int2 x = __ldcg(&w.start[c]);
-      in = x.x == at.x && x.y > 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int my_row = lane & 7, c4 = warp * 4 + (lane >> 3);            // of the sums: row (+ 8 r), 4-channel group
+  const int runs = (w.part_rows + 8 * kRows - 1) / (8 * kRows);
+  // (the first item is read before it is known that there is one)
+  if (tid == 0) {
+    s_cut = __ldcg(&w.start[w.max_ctas + 1].y);
+    s_item = __ldcg(&w.cut[blockIdx.x / runs]);
+  }
+  __syncthreads();
+  for (int x = blockIdx.x; x < s_cut * runs; x += gridDim.x) {
+    if (x != blockIdx.x) {
+      if (tid == 0) s_item = __ldcg(&w.cut[x / runs]);
+      __syncthreads();
     }
-    const int n = __ffs(~__ballot_sync(0xffffffffu, in)) - 1;      // -1: all 32
-    const int count = n < 0 ? 32 : n;
-    const auto slot = [&](int x) { return (int64_t)(2 * x + (x < i ? 1 : 0)) * w.part_rows + row; };
-    const float2 ml = lane < count ? __ldcg(&w.part_ml[slot(c)]) : make_float2(-INFINITY, 0.f);
-    float top = ml.x;
+    const int first = s_item.x, parts = s_item.y, item = s_item.z, row0 = x % runs * 8 * kRows;
+    const auto slot = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * w.part_rows; };
+    float m[kRows], l[kRows];
+    float4 o[kRows];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float mn = fmaxf(m, top);
-    if (mn > -INFINITY) {
-      const float f = ex2(m - mn), e = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
-      float sum = ml.y * e;
+    for (int r = 0; r < kRows; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+      o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+      float2 ml[kRows];
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      m = mn;
-      l = l * f + sum;
-      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-#pragma unroll 8
-      for (int x = 0; x < count; ++x) {
-        const float ex = __shfl_sync(0xffffffffu, e, x);
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(w.part + slot(c0 + x) * kHeadDim) + lane);
-        // a partial without a key holds nothing to add
-        if (ex > 0.f) {
-          o.x += ex * u.x;
-          o.y += ex * u.y;
-          o.z += ex * u.z;
-          o.w += ex * u.w;
+      for (int r = 0; r < kRows; ++r) {
+        const int row = row0 + warp + 8 * r;
+        ml[r] = p0 + lane < parts && row < w.part_rows ? __ldcg(&w.part_ml[slot(p0 + lane) + row])
+                                                       : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        float mn = ml[r].x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+        mn = fmaxf(m[r], mn);
+        const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn), e = ml[r].x == -INFINITY ? 0.f : ex2(ml[r].x - mn);
+        float sum = ml[r].y * e;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        m[r] = mn;
+        l[r] = l[r] * f + sum;
+        s_e[warp + 8 * r][lane] = e;
+        if (lane == 0) s_f[warp + 8 * r] = f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float f = s_f[my_row + 8 * r];
+        o[r].x *= f, o[r].y *= f, o[r].z *= f, o[r].w *= f;
+      }
+      const int count = min(32, parts - p0);
+      for (int x0 = 0; x0 < count; x0 += kAhead) {
+        float4 u[kRows][kAhead];
+        float e[kRows][kAhead];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+          for (int y = 0; y < kAhead; ++y) {
+            // a partial without a key holds nothing to add
+            e[r][y] = x0 + y < count ? s_e[my_row + 8 * r][x0 + y] : 0.f;
+            u[r][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (e[r][y] > 0.f)
+              u[r][y] = __ldcg(reinterpret_cast<const float4*>(w.part) + 32 * slot(p0 + x0 + y) +
+                               (int64_t)c4 * w.part_rows + row0 + my_row + 8 * r);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+          for (int y = 0; y < kAhead; ++y) {
+            o[r].x += e[r][y] * u[r][y].x;
+            o[r].y += e[r][y] * u[r][y].y;
+            o[r].z += e[r][y] * u[r][y].z;
+            o[r].w += e[r][y] * u[r][y].w;
+          }
         }
       }
+      __syncthreads();
     }
-    if (count < 32) break;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (lane == 0) s_inv[warp + 8 * r] = l[r] > 0.f ? 1.f / l[r] : 0.f;
+    __syncthreads();
+    const int G = a.cv.G, sh = item / w.items_q, seq = sh / a.cv.Hkv, h = sh - seq * a.cv.Hkv;
+    const int i0 = (item - sh * w.items_q) * w.item_tokens, ntok = min(w.item_tokens, a.lens[seq] - i0);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int row = row0 + my_row + 8 * r, tile = row / kTile, tok = row % kTile / G, q = tile * w.tile_tokens + tok;
+      if (row >= w.part_rows || tok >= w.tile_tokens || q >= ntok) continue;
+      const float inv = s_inv[my_row + 8 * r];
+      uint16_t* out = a.o + (((int64_t)(a.b0 + seq) * a.n_max + i0 + q) * a.cv.Hq + h * G + row % kTile % G) * kHeadDim;
+      reinterpret_cast<uint2*>(out)[c4] =
+          make_uint2(pack_bf16x2(o[r].x * inv, o[r].y * inv), pack_bf16x2(o[r].z * inv, o[r].w * inv));
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint16_t* out = a.o + (((int64_t)it.b * a.n_max + it.i0 + q) * a.cv.Hq + it.h * a.cv.G + r % a.cv.G) * kHeadDim;
-  reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
 template <bool kDual, int kFmt>
@@ -1397,8 +1459,11 @@ cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, cons
         : args.cv.kv_format == kKvFp8 ? launch_attn<kKvFp8>(maps, args, w, stream)
                                       : launch_attn<kKvBf16>(maps, args, w, stream);
   if (err != cudaSuccess || w.max_ctas < 2) return err;
-  const dim3 grid((unsigned)w.max_ctas - 1, (unsigned)(w.part_rows + kMergeRows - 1) / kMergeRows);
-  return launch_after(chunk_merge_kernel, grid, 32 * kMergeRows, 0, stream, args, w);
+  // (at most max_ctas - 1 items are cut, in runs of 8 or 32 rows)
+  const int run = w.dual ? 32 : 8;
+  const int blocks = min(3 * w.max_ctas, (w.max_ctas - 1) * ((w.part_rows + run - 1) / run));
+  return launch_after(w.dual ? chunk_merge_kernel<4> : chunk_merge_kernel<1>, dim3((unsigned)blocks), 256, 0, stream,
+                      args, w);
 }
 
 }  // namespace lk

@@ -135,9 +135,10 @@ struct ChunkWork {
   int32_t cost_item;        // what an item weighs on the work line, a full-width key tile, and one on k
   int32_t cost_wide;        //   channels: cost_kept + k cost_k / 8
   int32_t cost_kept, cost_k;
-  int2* start;              // [max_ctas + 2]: (item, tile) where each CTA starts, the end; then (CTAs, -)
+  int2* start;              // [max_ctas + 2]: (item, tile) where each CTA starts, the end; then (CTAs, cut items)
+  int4* cut;                // items cut between CTAs: (first CTA, CTAs, item, -)
   float2* part_ml;          // [2 max_ctas][part_rows]
-  float* part;              // [2 max_ctas][part_rows][128]
+  float* part;              // [2 max_ctas][32][part_rows][4]: groups of four channels
   uint32_t* special;
   uint8_t* far;
 };
