@@ -31,13 +31,13 @@
 //
 // What bounds it.  Chunks that fill two query tiles: the softmax of 128 x 64
 // scores (1300 clocks a group, of which the tensor cores need 800); 1000 queries
-// of 28 heads over 131072 tokens on 32 kept channels take 866 us, 54% of the
+// of 28 heads over 131072 tokens on 32 kept channels take 853 us, 55% of the
 // measured bf16 matrix rate.  Chunks of a few tokens: the cache's bytes, through
 // a ring that holds two to five tiles per group; 64 sequences of 4096 tokens
 // take 101 us, 1.45 times what a plain copy's rate gives their bytes.  Sealed
 // blocks: the four warps that expand them, which share instruction caches with
-// every other role; 16 sequences of 8192 tokens take 108 us, 3.7 times their
-// bytes.  One sequence: three dependent launches, 31 us over 32768 tokens.
+// every other role; 16 sequences of 8192 tokens take 107 us, 3.7 times their
+// bytes.  One sequence: three dependent launches, 29 us over 32768 tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -56,8 +56,9 @@ namespace {
 constexpr int kTile = 128;                 // keys per tile, rows per query tile
 constexpr int kFar = 1 << 29;              // a window that nothing leaves
 constexpr float kScaleLog2 = 0.12751743f;  // log2(e) / sqrt(128)
-// line a CTA takes at least: about three tiles (one sequence of 32768 tokens: 31
-// us; with half of it the same, with three times as much 33)
+// Line a CTA takes at least: about three tiles (one sequence of 32768 tokens: 29
+// us, with three times as much 31).  More than any tile and more than an item's
+// own share weigh, so that no two CTAs start at the same tile of an item.
 constexpr uint64_t kMinCtaCost = 768;
 
 enum TileType : int { kTileA = 0, kTileC = 1, kTileM = 2, kTileF = 3 };
@@ -1325,7 +1326,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 // adds up four channels of kRows rows, kAhead partials of each in flight.
 // Partials lie channel group by channel group, the rows of each side by side,
 // as the attention's threads, a row each, write them in whole lines (a row at a
-// time: 5 us of every CTA's time instead of 1).  The grid is one wave that goes
+// time: 5 us of a CTA's time for each, instead of 2).  The grid is one wave that goes
 // through a list: 1200 blocks of which most found nothing to do took 7 us.
 template <int kRows>
 __global__ void __launch_bounds__(256, kRows == 1 ? 2 : 3) chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const ChunkWork w) {
