@@ -209,6 +209,12 @@ def _token_stride(t, heads, lead, what):
     return heads * 128 if step is None else step
 
 
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"a tensor is on {t.device}, the call on {device}")
+
+
 class Rope:
     """lk_build_rope: rotary positions of heads of 128 channels."""
 
@@ -229,6 +235,9 @@ class Rope:
         import torch
         if q is None and k is None:
             raise ValueError("q and k are both None")
+        for x, what in ((q, "q"), (k, "k")):
+            if x is not None and x.ndim < 2:
+                raise ValueError(f"{what}: expected [..., heads, 128], got {tuple(x.shape)}")
         lead = tuple((q if q is not None else k).shape[:-2])
         tokens = 1
         for n in lead:
@@ -248,6 +257,7 @@ class Rope:
                 y = torch.empty((*lead, heads, 128), dtype=torch.bfloat16, device=x.device)
             args.append((x.data_ptr(), step, heads, y.data_ptr(), _token_stride(y, heads, lead, what + "_out")))
             outs.append(y)
+        _same_device(torch.device("cuda", torch.cuda.current_device()), positions, q, k, *outs)
         (qp, qs, hq, qo, qos), (kp, ks, hk, ko, kos) = args
         _check(_lib.lk_rope_apply(self._h, qp, qs, kp, ks, positions.data_ptr(), tokens, hq, hk, qo, qos, ko, kos,
                                   _stream(stream)))
@@ -615,6 +625,7 @@ class Cache:
             if lens.shape != (B,):
                 raise ValueError(f"lens shape {lens.shape}")
             c.lens = lens.ctypes.data
+        _same_device(self.buffer.device, q, k, v, ids)
         return c, lens
 
     def _chunk_out(self, q, o):
@@ -623,6 +634,7 @@ class Cache:
         if o is None:
             o = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
         _need(o, torch.bfloat16, shape, "o")
+        _same_device(self.buffer.device, o)
         n = q.shape[1]
         if n > self._chunk_tokens or not self._chunk_workspaces:
             # for chunks of up to the next power of two; earlier ones stay, as

@@ -197,3 +197,23 @@ def test_chunks_too_long(cuda):
         assert lkb._lib.lk_chunk_attn(case.cache._h, 0, ctypes.byref(c), o.data_ptr(), ws.data_ptr(), ws.numel(),
                                       None) == lkb.LK_ERR_UNSUPPORTED
         assert lkb._lib.lk_append_chunk(case.cache._h, 0, ctypes.byref(c), None) == lkb.LK_ERR_UNSUPPORTED
+
+
+def test_tensors_of_another_device(cuda, monkeypatch):
+    """Tensors that are not where the call runs are refused before any launch."""
+    case = Case(TINY, total=64)
+    _fill(case, [10])
+    q, (k, v, _) = _queries(case, 4), _chunk(case, 0, [10], 4)
+    for call in (lambda: case.cache.chunk_attn(0, q, k.cpu(), v), lambda: case.cache.append_chunk(0, k, v.cpu()),
+                 lambda: case.cache.extend(0, q, k, v, o=torch.empty_like(q, device="cpu"))):
+        with pytest.raises(ValueError):
+            call()
+    assert case.cache.length(0) == 10
+    rope = lkb.Rope()
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    rope.apply(q, k, pos)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:0"):
+        rope.apply(q, k, pos)
+    with pytest.raises(ValueError):
+        rope.apply(q[0, 0, 0], None, pos)
