@@ -387,12 +387,12 @@ struct Smem {
   static constexpr int kQTiles = kDual ? 2 : 1;
   static constexpr int kRings = kDual ? 1 : 2;           // one that both groups read, or one for each
   static constexpr int kSlots = 16;                      // tiles in flight per ring at most
-  static constexpr int kFull = 0, kEmpty = kFull + 8 * kSlots * kRings,
-                       kQFull = kEmpty + 8 * kSlots * kRings, kQEmpty = kQFull + 8, kQKFull = kQEmpty + 8,
-                       kSFull = kQKFull + 16, kPFull = kSFull + 32, kOFull = kPFull + 32, kOEnd = kOFull + 16, kMerge = kOEnd + 16,
-                       kMerged = kMerge + 8, kDrain = kMerged + 8, kTmem = kDrain + 16, kOffs = kTmem + 16,
-                       kInfo = kOffs + 4 * kSlots * kRings, kSeg = kInfo + 4 * kSlots * kRings, kLanded = kSeg + 256, kDone = kLanded + 8 * kJobs * kRings,
-                       kJob = kDone + 8 * kJobs * kRings;
+  static constexpr int kFull = 0, kEmpty = kFull + 8 * kSlots * kRings, kQFull = kEmpty + 8 * kSlots * kRings,
+                       kQEmpty = kQFull + 8, kQKFull = kQEmpty + 8, kSFull = kQKFull + 16, kPFull = kSFull + 32,
+                       kOFull = kPFull + 32, kOEnd = kOFull + 16, kMerge = kOEnd + 16, kMerged = kMerge + 8,
+                       kDrain = kMerged + 8, kTmem = kDrain + 16, kOffs = kTmem + 16,
+                       kInfo = kOffs + 4 * kSlots * kRings, kSeg = kInfo + 4 * kSlots * kRings, kLanded = kSeg + 256,
+                       kDone = kLanded + 8 * kJobs * kRings, kJob = kDone + 8 * kJobs * kRings;
   static constexpr int kSegBytes = 128;                  // two segments
   static constexpr int kML = 2048;                       // second group's (m, l)
   static constexpr int kVScale = kML + (kDual ? 0 : kTile * 8);          // of the tiles in flight, four per ring
@@ -404,6 +404,8 @@ struct Smem {
   static_assert(kJob + kJobBytes * kJobs * kRings <= 2048 && kSegBytes == 128, "barriers, tiles, segments and jobs");
   static constexpr int kBytes = 227 * 1024;
   static constexpr int kEnd = kBytes - 1024;             // after aligning the base
+  // (a fifth tile's scales take the first one's place: no five tiles' values fit a ring)
+  static_assert(!kQuant || (kEnd - kQ - (kDual ? 2 * kWideBytes : 0)) / kRings < 5 * kWideBytes, "places of scales");
 };
 
 constexpr uint64_t kIdleNs = 60000000000ull;      // bound of the makers' wait for a job
@@ -815,7 +817,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
                                                        : (int64_t)it.b * hd.qblocks + t.r0 / kTile) * qblock_bytes(it.k);
               const int width = isv ? kHeadDim : it.k, vn = (int)(sealed & 3);
               const uint32_t codes = (uint32_t)(kTile * width), scales = isv ? kTile * 4u : (uint32_t)(4 * it.k);
-              const uint32_t sc = isv ? L::kVScale + (4 * ri + vn) * kTile * 4 : L::kKScale + (ri * L::kJobs + jn) * kTile * 4;
+              const uint32_t sc =
+                  isv ? L::kVScale + (4 * ri + vn) * kTile * 4 : L::kKScale + (ri * L::kJobs + jn) * kTile * 4;
               *reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes) =
                   Job{width, isv ? 1 : 0, slot, dst - base, sc};
               mbar_arrive_expect_tx(landed, codes + scales);
@@ -832,7 +835,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               expect(bar, kWideBytes);
               tma_load_3d(dst, &maps.pool[isv ? kPoolV : kPoolK128], 0, (int)(abase + t.r0), 0, bar, keep);
             } else if (t.type == kTileM) {
-              const int64_t r = !kQuant && pages != nullptr ? (int64_t)max(0, pg) * kPageRows : bbase + t.r0 - (kQuant ? it.nS * kTile : 0);
+              const int64_t r = !kQuant && pages != nullptr ? (int64_t)max(0, pg) * kPageRows
+                                                            : bbase + t.r0 - (kQuant ? it.nS * kTile : 0);
               if (isv) {
                 expect(bar, kWideBytes);
                 tma_load_3d(dst, &maps.pool[kPoolV], 0, (int)(vrow_b + r), 0, bar, keep);
@@ -1064,10 +1068,12 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           const int r = y / groups, c = y - r * groups;
           const uint4 kc = *reinterpret_cast<const uint4*>(kept + 8 * c);
           auto at = [&](uint32_t ch) {
-            return (uint32_t)*reinterpret_cast<const uint16_t*>(q + kept_byte(kHeadDim, r, (int)ch >> 3, q_rows) + (ch & 7) * 2);
+            const uint8_t* from = q + kept_byte(kHeadDim, r, (int)ch >> 3, q_rows) + (ch & 7) * 2;
+            return (uint32_t)*reinterpret_cast<const uint16_t*>(from);
           };
           auto two = [&](uint32_t p) { return at(p & 0xffffu) | at(p >> 16) << 16; };
-          *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c, q_rows)) = make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
+          *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c, q_rows)) =
+              make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
         }
         fence_async_smem();
         __syncwarp();
@@ -1220,7 +1226,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               }
             }
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 2) x[c >> 1] = pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+            for (int c = 0; c < kHalf; c += 2)
+              x[c >> 1] = pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
           }
           tmem_st32(at, x);
           float l0, l1;
@@ -1329,7 +1336,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 // time: 5 us of a CTA's time for each, instead of 2).  The grid is one wave that goes
 // through a list: 1200 blocks of which most found nothing to do took 7 us.
 template <int kRows>
-__global__ void __launch_bounds__(256, kRows == 1 ? 2 : 3) chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const ChunkWork w) {
+__global__ void __launch_bounds__(256, kRows == 1 ? 2 : 3) chunk_merge_kernel(const __grid_constant__ ChunkArgs a,
+                                                                                  const ChunkWork w) {
   constexpr int kAhead = kRows == 1 ? 16 : 2;
   __shared__ float s_e[8 * kRows][33], s_f[8 * kRows], s_inv[8 * kRows];
   __shared__ int s_cut;

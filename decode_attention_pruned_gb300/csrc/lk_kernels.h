@@ -178,7 +178,7 @@ inline cudaError_t set_smem_limit_once(F* fn, int bytes, std::atomic<uint64_t>& 
 // block of such a kernel waits for that one before it leaves.
 template <typename... Args>
 inline cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
-                         const std::decay_t<Args>&... args) {
+                                const std::decay_t<Args>&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
