@@ -217,3 +217,22 @@ def test_tensors_of_another_device(cuda, monkeypatch):
         rope.apply(q, k, pos)
     with pytest.raises(ValueError):
         rope.apply(q[0, 0, 0], None, pos)
+
+
+@pytest.mark.parametrize("n", [3, 60])
+def test_policies_over_quantised_middles(cuda, n):
+    w = S.WORKLOADS[4].scaled(num_layers=1, batch=2, context=700, policy_counts=(2, 2, 4))
+    case = Case(w, total=800, kv_format=lkb.KV_FP8)
+    held = [700, 301]
+    _fill(case, held)
+    _attend(case, held, n, lens=[n, n - 2])
+
+
+@pytest.mark.parametrize("fmt", [lkb.KV_BF16, lkb.KV_INT8], ids=["bf16", "int8"])
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_one_item_over_every_block(cuda, fmt, n):
+    """One sequence, one kv head: its keys are cut into more partials than a warp has lanes."""
+    w = TINY.scaled(num_kv_heads=1, num_q_heads=8, batch=1, sink=4, local=64)
+    case = Case(w, total=60050, masks=S.masks_with_counts(w, (64,)), gen_device="cuda", kv_format=fmt)
+    _fill(case, [60000])
+    _attend(case, [60000], n)
