@@ -652,6 +652,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       for (const uint64_t t0 = ok ? 0 : global_timer_ns(); !ok && *gone == 0 && global_timer_ns() - t0 < kIdleNs;)
         ok = mbar_wait_bounded(base + L::kLanded + 8 * jn, phase, 1000000);
       if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0 && *gone == 0) atomicOr(&cv.hdr->status, (uint32_t)kStatusTimeout);
         *gone = 1;
         break;
       }
