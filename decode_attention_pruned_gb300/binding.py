@@ -206,7 +206,12 @@ def _token_stride(t, heads, lead, what):
     if not even or stride[-1] != 1 or (heads > 1 and stride[-2] != 128):
         raise ValueError(f"{what}: heads must be dense and tokens evenly spaced, got strides {stride} for "
                          f"{tuple(shape)}")
-    return heads * 128 if step is None else step
+    if step is None:
+        return heads * 128
+    if step < heads * 128:
+        # (0, one row for every token, would mean dense rows to the library)
+        raise ValueError(f"{what}: tokens share rows, got strides {stride} for {tuple(shape)}")
+    return step
 
 
 def _same_device(device, *tensors):

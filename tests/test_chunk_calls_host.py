@@ -1,0 +1,117 @@
+"""The Python side of the chunk and rotary calls, without a GPU: stand-ins that
+report a CUDA device carry the shapes and strides of CPU tensors, and a library
+that must not be reached takes the place of the real one."""
+import types
+
+import pytest
+import torch
+
+from decode_attention_pruned_gb300 import binding as lkb
+
+CUDA = torch.device("cuda", 0)
+
+
+class OnGpu:
+    """A CPU tensor that says it is on the GPU."""
+
+    def __init__(self, t):
+        self.t = t
+
+    is_cuda, device = True, CUDA
+    dtype = property(lambda self: self.t.dtype)
+    shape = property(lambda self: self.t.shape)
+    ndim = property(lambda self: self.t.ndim)
+
+    def dim(self):
+        return self.t.dim()
+
+    def stride(self):
+        return self.t.stride()
+
+    def is_contiguous(self):
+        return self.t.is_contiguous()
+
+    def data_ptr(self):
+        return self.t.data_ptr()
+
+
+class NoCalls:
+    """A library that no call may reach."""
+
+    def __getattr__(self, name):
+        raise AssertionError(f"{name} was reached")
+
+
+def _rows(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def _shared(B, n, H):
+    """[B, n, H, 128] tensors whose tokens lie on one another: one row for all,
+    for all of a sequence, for all sequences, or rows that overlap."""
+    out = [_rows(1, 1, H, 128).expand(B, n, H, 128)]
+    if n > 1:
+        out += [_rows(B, 1, H, 128).expand(B, n, H, 128), _rows(B * n * H + H, 128).as_strided((B, n, H, 128),
+                                                                                              (n * 128, 128, 128, 1))]
+    if B > 1:
+        out.append(_rows(1, n, H, 128).expand(B, n, H, 128))
+    return [t for t in out if not t.is_contiguous()]
+
+
+@pytest.mark.parametrize("B, n, H", [(1, 4, 8), (3, 1, 8), (4, 5, 2), (2, 2, 2)])
+def test_tokens_that_share_rows_are_refused(B, n, H):
+    cases = _shared(B, n, H)
+    assert cases
+    for t in cases:
+        with pytest.raises(ValueError):
+            lkb._token_stride(OnGpu(t), H, (B, n), "k")
+
+
+def test_spaced_tokens_are_taken():
+    stride = lkb._token_stride
+    assert stride(OnGpu(_rows(3, 5, 2, 128)), 2, (3, 5), "k") == 256
+    rows = _rows(3, 5, 7, 128)
+    assert stride(OnGpu(rows[:, :, 1:3]), 2, (3, 5), "k") == 7 * 128
+    assert stride(OnGpu(rows[:1, :, 1:3]), 2, (1, 5), "k") == 7 * 128
+    assert stride(OnGpu(rows[:, :1, 1:3]), 2, (3, 1), "k") == 5 * 7 * 128
+    assert stride(OnGpu(rows[:1, :1, 1:3]), 2, (1, 1), "k") == 2 * 128          # one token: nothing to step over
+    # sizes of one may have any stride
+    one = _rows(1, 2, 128).expand(1, 2, 128).unsqueeze(0)
+    assert stride(OnGpu(one), 2, (1, 1), "k") == 2 * 128
+
+
+def _cache(B, Hq, H):
+    """A cache's Python side only."""
+    c = object.__new__(lkb.Cache)
+    c.plan = types.SimpleNamespace(num_q_heads=Hq, num_kv_heads=H)
+    c.batch, c.buffer, c._h = B, OnGpu(torch.zeros(1)), None
+    return c
+
+
+@pytest.mark.parametrize("B, n", [(3, 1), (2, 4)])
+def test_chunk_calls_refuse_shared_rows(monkeypatch, B, n):
+    monkeypatch.setattr(lkb, "_lib", NoCalls())
+    c = _cache(B, 4, 2)
+    q, k = OnGpu(_rows(B, n, 4, 128)), OnGpu(_rows(B, n, 2, 128))
+    for bad in map(OnGpu, _shared(B, n, 2)):
+        for call in (lambda: c.append_chunk(0, bad, k), lambda: c.append_chunk(0, k, bad),
+                     lambda: c.chunk_attn(0, q, bad, k), lambda: c.extend(0, q, k, bad)):
+            with pytest.raises(ValueError):
+                call()
+    for bad in map(OnGpu, _shared(B, n, 4)):
+        with pytest.raises(ValueError):
+            c.chunk_attn(0, bad, k, k)
+
+
+def test_rope_refuses_shared_rows(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    rope = object.__new__(lkb.Rope)
+    rope._h = None
+    monkeypatch.setattr(lkb, "_lib", NoCalls())
+    x, pos = OnGpu(_rows(5, 8, 128)), OnGpu(torch.zeros(5, dtype=torch.int32))
+    bad = OnGpu(_rows(1, 8, 128).expand(5, 8, 128))
+    for call in (lambda: rope.apply(bad, None, pos, q_out=x), lambda: rope.apply(None, bad, pos, k_out=x),
+                 lambda: rope.apply(x, None, pos, q_out=bad), lambda: rope.apply(None, x, pos, k_out=bad),
+                 lambda: rope.apply(bad, None, pos, q_out=bad)):
+        with pytest.raises(ValueError):
+            call()
