@@ -732,6 +732,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + L::kInfo) + ri * L::kSlots;
         uint32_t put = 0, freed = 0, head = 0, tail = 0, jobs = 0, sealed = 0;
         uint32_t by_job = 0;                // slots whose tile the makers complete
+        int q_sent = -1;                    // last segment whose q is on its way
         bool wrapped = false;
         // Keys that one query tile reads are read once; those that several read
         // should stay in L2.
@@ -783,6 +784,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               for (int part = 0; part < 2; ++part)
                 tma_load_3d(base + L::kQ + x * q_bytes + part * (q_bytes / 2), &maps.q, part * 64, it.h * G,
                             it.b * a.n_max + it.i0 + x * tq, base + L::kQFull, once);
+            q_sent = s.idx;
           }
           // first of the arrivals that complete a tile's slot, and the others
           auto expect = [&](uint32_t bar, uint32_t bytes) {
@@ -874,26 +876,29 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             page = after;
           }
         }
+        // Every copy lands before this thread ends, whether or not its wait ran out
+        // and whether or not anyone still waits for the tile: some other role may
+        // have given up, or be about to, and the block must not end with copies on
+        // their way into its shared memory.  (A tile that the makers complete has
+        // landed when its codes and scales have.)
+        for (uint32_t x = jobs > L::kJobs ? jobs - L::kJobs : 0; kQuant && x < jobs; ++x)
+          mbar_wait_bounded(base + L::kLanded + 8 * (ri * L::kJobs + x % L::kJobs), (x / L::kJobs) & 1, kDrainNs);
+        for (uint32_t x = freed; x < put; ++x)
+          if ((by_job >> x % L::kSlots & 1) == 0)
+            mbar_wait_bounded(full + 8 * (x % L::kSlots), (x / L::kSlots) & 1, kDrainNs);
+        if (q_sent >= 0) mbar_wait_bounded(base + L::kQFull, q_sent & 1, kDrainNs);
         if (kQuant) {
-          // the makers' last job: none
-          const uint32_t jn = jobs % L::kJobs;
+          // the makers' last job: none (where they have left already, nobody reads it)
+          const uint32_t jn = jobs % L::kJobs, done = base + L::kDone + 8 * (ri * L::kJobs + jn);
           if (jobs >= L::kJobs)
-            mbar_wait_bounded(base + L::kDone + 8 * (ri * L::kJobs + jn), (jobs / L::kJobs - 1) & 1, kDrainNs);
+            for (const uint64_t t0 = global_timer_ns(); !mbar_wait_bounded(done, (jobs / L::kJobs - 1) & 1, 1000000) &&
+                                                        *gone == 0 && global_timer_ns() - t0 < kDrainNs;) {}
           reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes)->width = 0;
           mbar_arrive(base + L::kLanded + 8 * (ri * L::kJobs + jn));
         }
         if (ok && ri == 0 && (s.idx < 0 || wait(base + L::kQEmpty, s.idx & 1))) {
           reinterpret_cast<Segment*>(sm + L::kSeg + ((s.idx + 1) & 1) * L::kSegBytes)->t1 = 0;
           mbar_arrive(base + L::kQFull);
-        }
-        // copies still in flight must land before the block ends
-        if (!ok) {
-          for (uint32_t x = jobs > L::kJobs ? jobs - L::kJobs : 0; kQuant && x < jobs; ++x)
-            mbar_wait_bounded(base + L::kLanded + 8 * (ri * L::kJobs + x % L::kJobs), (x / L::kJobs) & 1, kDrainNs);
-          for (uint32_t x = freed; x < put; ++x)
-            if ((by_job >> x % L::kSlots & 1) == 0)
-              mbar_wait_bounded(full + 8 * (x % L::kSlots), (x / L::kSlots) & 1, kDrainNs);
-          if (ri == 0 && s.idx >= 0) mbar_wait_bounded(base + L::kQFull, s.idx & 1, kDrainNs);
         }
       }
     } else if (warp < 3) {
@@ -1032,10 +1037,9 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           if (ok && mine > 0) mma_commit(base + L::kOEnd + 8 * st);
           taken = end;
         }
-        if (!ok) {
-          mma_commit(base + L::kDrain + 8 * st);
-          mbar_wait_bounded(base + L::kDrain + 8 * st, 0, kDrainNs);
-        }
+        // (as for the copies: nothing that this thread issued outlives it)
+        mma_commit(base + L::kDrain + 8 * st);
+        mbar_wait_bounded(base + L::kDrain + 8 * st, 0, kDrainNs);
       }
     }
   } else {

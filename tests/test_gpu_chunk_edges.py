@@ -71,6 +71,39 @@ def test_waits_that_run_out(cuda, fmt, n):
     _attend(case, held, n)
 
 
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("held, n", [([90, 20], 2), ([1300, 801], 5), ([90, 20], 150), ([1300, 801], 300)], ids=str)
+def test_calls_right_behind_one_that_gave_up(cuda, fmt, held, n):
+    """Where some of a block's waits run out, its other threads may be done with
+    theirs: the block still ends only when its copies have landed, and what runs
+    next, with no synchronisation between, is as if nothing had happened."""
+    w = TINY.scaled(num_kv_heads=4, num_q_heads=16, batch=2)
+    case = Case(w, total=1700, masks=S.masks_with_counts(w, (32, 96, 0, 128)), kv_format=fmt)
+    _fill(case, held)
+    q, (k, v, _) = _queries(case, n), _chunk(case, 0, held, n)
+    want = _attend(case, held, n)
+    torch.cuda.synchronize()
+    for limit in (0, 1, 300, 1000, 3000, 10000) * 2:
+        outs = []
+        for _ in range(4):
+            case.cache.set_wait_limit(limit)
+            case.cache.chunk_attn(0, q, k, v)
+            case.cache.set_wait_limit(10 ** 9)
+            outs.append(case.cache.chunk_attn(0, q, k, v))
+        for o in outs:
+            assert torch.equal(o, want), limit
+        if limit == 0:
+            with pytest.raises(lkb.LeankError) as e:
+                case.cache.check()
+            assert e.value.status == lkb.LK_ERR_TIMEOUT
+        else:
+            try:
+                case.cache.check()
+            except lkb.LeankError as e:
+                assert e.status == lkb.LK_ERR_TIMEOUT
+    _attend(case, held, n)
+
+
 def test_captured_extend_and_append(cuda):
     """A captured extend and append take the tokens at the lengths of the replay."""
     w = TINY.scaled(num_kv_heads=4, num_q_heads=8, batch=2, sink=4, local=30)
