@@ -172,6 +172,16 @@ def _stream(stream=None):
     return ctypes.c_void_p(_torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device()))
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor, in memory that belongs to the stream of the call: what was
+    freed on another one may still be in use there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need(t, dtype, shape, what, device_kind="cuda"):
     try:
         if t.dtype is dtype and t.shape == shape and t.device.type == device_kind and t.is_contiguous():
@@ -259,7 +269,7 @@ class Rope:
             heads = x.shape[-2]
             step = _token_stride(x, heads, lead, what)
             if y is None:
-                y = torch.empty((*lead, heads, 128), dtype=torch.bfloat16, device=x.device)
+                y = _empty((*lead, heads, 128), torch.bfloat16, x.device, stream)
             args.append((x.data_ptr(), step, heads, y.data_ptr(), _token_stride(y, heads, lead, what + "_out")))
             outs.append(y)
         _same_device(torch.device("cuda", torch.cuda.current_device()), positions, q, k, *outs)
@@ -282,7 +292,7 @@ def build_masks(alpha, prune_pct, align=32, exact=False, eligible=None, stream=N
     _need(alpha, torch.float32, (L, H, 128), "alpha")
     if eligible is not None:
         _need(eligible, torch.uint8, (L, H), "eligible")
-    out = torch.empty((L, H, 128), dtype=torch.uint8, device=alpha.device)
+    out = _empty((L, H, 128), torch.uint8, alpha.device, stream)
     _check(_lib.lk_build_masks(alpha.data_ptr(), _ptr(eligible), L, H, float(prune_pct), align, 1 if exact else 0,
                                out.data_ptr(), _stream(stream)))
     return out
@@ -352,6 +362,10 @@ class Plan:
 class Cache:
     """A cache bound to a torch-allocated device buffer, plus its workspace.
 
+    Tensors that a call makes (outputs that were not given, workspaces) belong to
+    the stream that it runs on, the current one unless ``stream`` is given: use
+    them elsewhere as one uses any tensor of another stream.
+
     With ``middle_tokens`` the cache is paged (lk_cache_init_paged): the
     middle rows of all sequences share page pools sized for that many middle
     tokens in total.  ``kv_format=KV_INT8`` quantises complete 128-row
@@ -367,8 +381,8 @@ class Cache:
         dev = torch.device(device if device is not None else "cuda")
         self.device = dev
         nbytes = plan.cache_bytes(batch, capacity, middle_tokens, kv_format)
-        self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        self.workspace = torch.empty(plan.workspace_bytes(batch), dtype=torch.uint8, device=dev)
+        self.buffer = _empty(nbytes, torch.uint8, dev, stream)
+        self.workspace = _empty(plan.workspace_bytes(batch), torch.uint8, dev, stream)
         self._chunk_tokens, self._chunk_workspaces = 0, []      # made by chunk_attn and extend
         h = ctypes.c_void_p()
         s = _stream(stream)
@@ -487,7 +501,7 @@ class Cache:
         B, Hq = self.batch, self.plan.num_q_heads
         _need(q, torch.bfloat16, (nl, B, Hq, 128), "q")
         if o is None:
-            o = torch.empty((nl, B, Hq, 128), dtype=torch.float32, device=q.device)
+            o = _empty((nl, B, Hq, 128), torch.float32, q.device, stream)
         _need(o, torch.float32, (nl, B, Hq, 128), "o")
         _check(_lib.lk_decode_attn_layers(self._h, layer0, nl, q.data_ptr(), o.data_ptr(), self.workspace.data_ptr(),
                                           self.workspace.numel(), _stream(stream)))
@@ -507,7 +521,7 @@ class Cache:
         B, Hq = self.batch, self.plan.num_q_heads
         _need(q, torch.bfloat16, (B, Hq, 128), "q")
         if o is None:
-            o = torch.empty((B, Hq, 128), dtype=torch.float32, device=q.device)
+            o = _empty((B, Hq, 128), torch.float32, q.device, stream)
         _need(o, torch.float32, (B, Hq, 128), "o")
         _check(_lib.lk_decode_attn(self._h, layer, q.data_ptr(), o.data_ptr(), self.workspace.data_ptr(),
                                    self.workspace.numel(), _stream(stream)))
@@ -533,7 +547,7 @@ class Cache:
         if ids is not None:
             _need(ids, torch.int32, (B,), "ids")
         if o is None:
-            o = torch.empty((B, Hq, 128), dtype=torch.float32, device=q.device)
+            o = _empty((B, Hq, 128), torch.float32, q.device, stream)
         _need(o, torch.float32, (B, Hq, 128), "o")
         _check(_lib.lk_step(self._h, layer, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(ids), o.data_ptr(),
                             self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
@@ -550,7 +564,7 @@ class Cache:
         if ids is not None:
             _need(ids, torch.int32, (B,), "ids")
         if o is None:
-            o = torch.empty((nl, B, Hq, 128), dtype=torch.float32, device=q.device)
+            o = _empty((nl, B, Hq, 128), torch.float32, q.device, stream)
         _need(o, torch.float32, (nl, B, Hq, 128), "o")
         _check(_lib.lk_step_layers(self._h, layer0, nl, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(ids),
                                    o.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(),
@@ -633,11 +647,11 @@ class Cache:
         _same_device(self.buffer.device, q, k, v, ids)
         return c, lens
 
-    def _chunk_out(self, q, o):
+    def _chunk_out(self, q, o, stream):
         import torch
         shape = (self.batch, q.shape[1], self.plan.num_q_heads, 128)
         if o is None:
-            o = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            o = _empty(shape, torch.bfloat16, q.device, stream)
         _need(o, torch.bfloat16, shape, "o")
         _same_device(self.buffer.device, o)
         n = q.shape[1]
@@ -647,7 +661,7 @@ class Cache:
             self._chunk_tokens = 1 << max(n - 1, 0).bit_length()
             size = ctypes.c_size_t()
             _check(_lib.lk_chunk_workspace_bytes(self.plan._h, self.batch, self._chunk_tokens, ctypes.byref(size)))
-            self._chunk_workspaces.append(torch.empty(size.value, dtype=torch.uint8, device=self.device))
+            self._chunk_workspaces.append(_empty(size.value, torch.uint8, self.device, stream))
         return o
 
     @property
@@ -661,7 +675,7 @@ class Cache:
         The calls of a cache share its chunk workspace: they must not overlap on
         the GPU."""
         c, lens = self._chunk(q, k, v, lens, ids)
-        o = self._chunk_out(q, o)
+        o = self._chunk_out(q, o, stream)
         _check(_lib.lk_chunk_attn(self._h, layer, ctypes.byref(c), o.data_ptr(), self.chunk_workspace.data_ptr(),
                                   self.chunk_workspace.numel(), _stream(stream)))
         return o
@@ -674,7 +688,7 @@ class Cache:
     def extend(self, layer, q, k, v, lens=None, ids=None, o=None, stream=None):
         """lk_extend: chunk_attn, then append_chunk of the same tokens."""
         c, lens = self._chunk(q, k, v, lens, ids)
-        o = self._chunk_out(q, o)
+        o = self._chunk_out(q, o, stream)
         _check(_lib.lk_extend(self._h, layer, ctypes.byref(c), o.data_ptr(), self.chunk_workspace.data_ptr(),
                               self.chunk_workspace.numel(), _stream(stream)))
         return o

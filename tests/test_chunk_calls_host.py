@@ -115,3 +115,71 @@ def test_rope_refuses_shared_rows(monkeypatch):
                  lambda: rope.apply(bad, None, pos, q_out=bad)):
         with pytest.raises(ValueError):
             call()
+
+
+class Stream:
+    cuda_stream = 0x5150
+
+
+class Allocations:
+    """Stands in for torch.empty and torch.cuda.stream: which stream was current
+    when each tensor was made."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.made = None, []
+        real = torch.empty
+        outer = self
+
+        class On:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                self.before, outer.current = outer.current, self.stream
+
+            def __exit__(self, *_):
+                outer.current = self.before
+
+        def empty(*shape, dtype=None, device=None):
+            self.made.append(self.current)
+            return OnGpu(real(*shape, dtype=dtype))
+
+        monkeypatch.setattr(torch, "empty", empty)
+        monkeypatch.setattr(torch.cuda, "stream", On)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+
+class AllOk:
+    def __getattr__(self, name):
+        return lambda *a: lkb.LK_OK
+
+
+@pytest.mark.parametrize("given", [False, True], ids=["current", "given"])
+def test_new_tensors_belong_to_the_stream_of_the_call(monkeypatch, given):
+    """What a call makes is used on the call's stream; made on another one, it
+    could still be in use there."""
+    made = Allocations(monkeypatch)
+    monkeypatch.setattr(lkb, "_lib", AllOk())
+    monkeypatch.setattr(lkb, "load", lambda *a, **k: lkb._lib)
+    monkeypatch.setattr(lkb, "_stream", lambda stream=None: None)
+    monkeypatch.setattr(OnGpu, "numel", lambda self: 1, raising=False)
+    s = Stream() if given else None
+    c = _cache(2, 4, 2)
+    c.workspace, c.device, c.plan._h = OnGpu(torch.zeros(1)), CUDA, None
+    c._chunk_tokens, c._chunk_workspaces = 0, []
+    q, k = OnGpu(_rows(2, 3, 4, 128)), OnGpu(_rows(2, 3, 2, 128))
+    q1, k1 = OnGpu(_rows(2, 4, 128)), OnGpu(_rows(2, 2, 128))
+    ql, kl = OnGpu(_rows(1, 2, 4, 128)), OnGpu(_rows(1, 2, 2, 128))
+    rope = object.__new__(lkb.Rope)
+    rope._h = None
+    plan = types.SimpleNamespace(_h=None, cache_bytes=lambda *a: 8, workspace_bytes=lambda *a: 8)
+    alpha = OnGpu(torch.zeros(1, 2, 128))
+    for n, call in ((2, lambda: c.chunk_attn(0, q, k, k, stream=s)), (1, lambda: c.extend(0, q, k, k, stream=s)),
+                    (2, lambda: rope.apply(q1, k1, OnGpu(torch.zeros(2, dtype=torch.int32)), stream=s)),
+                    (1, lambda: c.decode(0, q1, stream=s)), (1, lambda: c.step(0, q1, k1, k1, stream=s)),
+                    (1, lambda: c.decode_layers(0, ql, stream=s)), (1, lambda: c.step_layers(0, ql, kl, kl, stream=s)),
+                    (1, lambda: lkb.build_masks(alpha, 50.0, stream=s)),
+                    (2, lambda: lkb.Cache(plan, 1, 8, stream=s))):
+        made.made.clear()
+        call()
+        assert made.made == [s] * n

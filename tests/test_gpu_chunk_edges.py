@@ -269,3 +269,29 @@ def test_one_item_over_every_block(cuda, fmt, n):
     case = Case(w, total=60050, masks=S.masks_with_counts(w, (64,)), gen_device="cuda", kv_format=fmt)
     _fill(case, [60000])
     _attend(case, [60000], n)
+
+
+def test_outputs_of_another_stream_are_its_own(cuda):
+    """What the current stream has freed, and may still be using, is not handed
+    to a call on another one."""
+    w = TINY.scaled(num_kv_heads=2, num_q_heads=8, batch=2)
+    case = Case(w, total=500, masks=S.masks_with_counts(w, (32, 96)))
+    _fill(case, [400, 170])
+    q, (k, v, _) = _queries(case, 20), _chunk(case, 0, [400, 170], 20)
+    ref = case.cache.chunk_attn(0, q, k, v)
+    rope, pos, one = lkb.Rope(), torch.zeros(2, 20, dtype=torch.int32, device="cuda"), q[:, 0].contiguous()
+    sizes = {t.numel() * t.element_size() for t in (ref, q, one.float(), case.cache.chunk_workspace)}
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in freed]
+    del freed
+    case.cache._chunk_tokens, spaces = 0, len(case.cache._chunk_workspaces)
+    outs = [case.cache.chunk_attn(0, q, k, v, stream=s), rope.apply(q, None, pos, stream=s)[0],
+            case.cache.decode(0, one, stream=s), case.cache._chunk_workspaces[-1]]
+    assert len(case.cache._chunk_workspaces) == spaces + 1
+    for t in outs:
+        at, end = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+        assert all(end <= a or b <= at for a, b in spans)
+    s.synchronize()
+    assert torch.equal(outs[0], ref) and torch.equal(outs[1], q)
