@@ -183,3 +183,17 @@ def test_new_tensors_belong_to_the_stream_of_the_call(monkeypatch, given):
         made.made.clear()
         call()
         assert made.made == [s] * n
+
+
+@pytest.mark.parametrize("has_raw", [True, False])
+def test_current_stream_with_and_without_the_short_way(monkeypatch, has_raw):
+    """The short way to the current stream's handle is torch's own affair: without
+    it the public one gives the same."""
+    if has_raw:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x5150 + device, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream())
+    assert lkb._stream().value == 0x5150
+    assert lkb._stream(Stream()).value == 0x5150
