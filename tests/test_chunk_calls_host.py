@@ -1,6 +1,8 @@
 """The Python side of the chunk and rotary calls, without a GPU: stand-ins that
 report a CUDA device carry the shapes and strides of CPU tensors, and a library
 that must not be reached takes the place of the real one."""
+import os
+import re
 import types
 
 import pytest
@@ -197,3 +199,12 @@ def test_current_stream_with_and_without_the_short_way(monkeypatch, has_raw):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream())
     assert lkb._stream().value == 0x5150
     assert lkb._stream(Stream()).value == 0x5150
+
+
+def test_every_tensor_core_helper_is_used():
+    csrc = os.path.join(os.path.dirname(lkb.__file__), "csrc")
+    text = {f: open(os.path.join(csrc, f)).read() for f in os.listdir(csrc)}
+    names = re.findall(r"__forceinline__ \w+ (\w+)\(", text["lk_tensor.cuh"])
+    assert len(names) > 10
+    for name in names:
+        assert sum(len(re.findall(rf"\b{name}\b", t)) for t in text.values()) > 1, name
