@@ -48,7 +48,7 @@ __device__ __forceinline__ uint32_t turn1(uint32_t x, float2 t) {
 // 8192 tokens of 32 heads.)
 template <int kTokens>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float2 turn[kTokens][kHeadDim / 2];
+  __shared__ float4 turn[kTokens][kHeadDim / 4];           // (cosine, sine) of two pairs each
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const uint64_t turns = (uint64_t)(int64_t)__ldg(a.positions + t0 + t) * a.freq[i];
     float s, c;
     sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
-    turn[t][i] = make_float2(c * a.magnitude, s * a.magnitude);
+    reinterpret_cast<float2*>(turn[t])[i] = make_float2(c * a.magnitude, s * a.magnitude);
   }
   __syncthreads();
   while (x < units) {
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                              : a.k_out + (t0 + t) * a.k_out_stride + (h - a.Hq) * kHeadDim;
     if (turned) {
       // eight pairs' cosines and sines
-      const float4* w = reinterpret_cast<const float4*>(turn[t] + 8 * slot);
+      const float4* w = turn[t] + 4 * slot;
       const float4 w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
       const float2 r[8] = {{w0.x, w0.y}, {w0.z, w0.w}, {w1.x, w1.y}, {w1.z, w1.w},
                            {w2.x, w2.y}, {w2.z, w2.w}, {w3.x, w3.y}, {w3.z, w3.w}};

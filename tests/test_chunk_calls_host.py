@@ -208,3 +208,14 @@ def test_every_tensor_core_helper_is_used():
     assert len(names) > 10
     for name in names:
         assert sum(len(re.findall(rf"\b{name}\b", t)) for t in text.values()) > 1, name
+
+
+def test_shared_arrays_have_the_alignment_of_their_reads():
+    """A __shared__ array of a smaller type is not read through a pointer to float4
+    or uint4: its place is aligned for its own type only."""
+    csrc = os.path.join(os.path.dirname(lkb.__file__), "csrc")
+    for f in ("lk_rope.cu", "lk_chunk.cu", "lk_chunk_append.cu"):
+        text = open(os.path.join(csrc, f)).read()
+        for kind, name in re.findall(r"__shared__ (\w+) (\w+)\[", text):
+            wide = re.findall(rf"reinterpret_cast<(?:const )?(\w+4)\*>\(&?{name}\b", text)
+            assert kind.endswith("4") or not wide, (f, name, wide)
