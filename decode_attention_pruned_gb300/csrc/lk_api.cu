@@ -303,12 +303,12 @@ WsLayout ws_layout(const lk_plan_desc& d, int B) {
 // How lk_chunk_attn cuts chunks of up to n_max tokens of up to B sequences,
 // and its workspace (one launch group's: groups run one after another):
 // CTA starts, special-token flags, partials, F tile images.  `layer` < 0:
-// what any layer needs.
+// what any layer needs, whatever the cache's format.
 struct ChunkLayout {
   size_t off_cut, off_special, off_ml, off_part, off_far, total;
   ChunkWork w;
 };
-ChunkLayout chunk_layout(const lk_plan_s& p, int B, int n_max, int layer, int ctas) {
+ChunkLayout chunk_layout(const lk_plan_s& p, int B, int n_max, int layer, int ctas, int fmt) {
   ChunkLayout c = {};
   const lk_plan_desc& d = p.d;
   const int G = d.num_q_heads / d.num_kv_heads, H = d.num_kv_heads;
@@ -325,21 +325,29 @@ ChunkLayout chunk_layout(const lk_plan_s& p, int B, int n_max, int layer, int ct
   w.box_tokens = std::min(w.tile_tokens, n_max);
   w.max_ctas = std::max(1, std::min(ctas, kChunkMaxCtas));
   w.part_rows = w.dual ? 256 : w.box_tokens * G;
-  int kfar = 0;
+  int kpart = 0, kmost = 0;    // channels of the widest pruned head that keeps some, of the widest head
   bool special = false;
   for (int l = layer < 0 ? 0 : layer; l < (layer < 0 ? d.num_layers : layer + 1); ++l) {
     special = special || p.layer_special[l];
     for (int h = 0; h < H; ++h) {
       const int i = l * H + h;
-      if (p.policy[i] == kFull && p.n_kept[i] < kHeadDim) kfar = std::max(kfar, (int)p.n_kept[i]);
+      if (p.policy[i] != kFull) continue;
+      kmost = std::max(kmost, (int)p.n_kept[i]);
+      if (p.n_kept[i] < kHeadDim) kpart = std::max(kpart, (int)p.n_kept[i]);
     }
   }
   const int64_t tiles = ((int64_t)n_max + 127) / 128;
-  w.far_tiles = kfar > 0 ? (int)tiles : 0;
-  w.far_bytes = (kfar + kHeadDim) * 2 * 128;
+  // F rows: the chunk's, K on the kept channels; INT8 / FP8 caches: up to 127 rows of
+  // an open block too, K at full width.
+  auto images = [&](bool quant) {
+    w.far_tiles = (quant ? kmost : kpart) == 0 ? 0 : quant ? (int)(((int64_t)n_max + 127 + 127) / 128) : (int)tiles;
+    w.far_bytes = ((quant ? kHeadDim : kpart) + kHeadDim) * 2 * 128;
+    return (size_t)seqs * H * w.far_tiles * w.far_bytes;
+  };
+  const bool quant = kv_quantized(fmt);
+  const size_t far = layer < 0 ? std::max(images(false), images(true)) : images(quant);
   w.q_rows = w.dual ? 128 : (w.part_rows + 7) / 8 * 8;
-  w.kept_width = kfar;
-  w.kept_bytes = kfar * 2 * w.q_rows;
+  w.kept_bytes = (quant ? kmost : kpart) * 2 * w.q_rows;
   w.special_seqs = special ? seqs : 0;
   w.special_words = special ? (int)(4 * tiles) : 0;
   size_t off = align_up((kChunkMaxCtas + 2) * sizeof(int2), 256);
@@ -352,7 +360,7 @@ ChunkLayout chunk_layout(const lk_plan_s& p, int B, int n_max, int layer, int ct
   c.off_part = off;
   off = align_up(off + (size_t)2 * w.max_ctas * w.part_rows * kHeadDim * 4, 1024);
   c.off_far = off;
-  off = align_up(off + (size_t)seqs * H * w.far_tiles * w.far_bytes, 256);
+  off = align_up(off + far, 256);
   c.total = off;
   return c;
 }
@@ -1347,12 +1355,12 @@ lk_status chunk_attn_prepare(lk_cache cache, void* o, void* workspace, size_t ws
   if (!o || !workspace) return fail(LK_ERR_ARG, "%s: null o or workspace", what);
   if (!aligned(o, 16)) return fail(LK_ERR_ALIGN, "%s: o must be 16-byte aligned", what);
   if (!aligned(workspace, 256)) return fail(LK_ERR_ALIGN, "%s: workspace must be 256-byte aligned", what);
-  const ChunkLayout need = chunk_layout(cache->plan, cache->B, a.n_max, -1, kChunkMaxCtas);
+  const ChunkLayout need = chunk_layout(cache->plan, cache->B, a.n_max, -1, kChunkMaxCtas, kKvBf16);
   if (ws_bytes < need.total)
     return fail(LK_ERR_CAPACITY, "%s: workspace has %zu bytes; %zu needed", what, ws_bytes, need.total);
   const CacheView& cv = cache->cv;
   const int64_t tokens = (int64_t)cache->B * a.n_max;
-  const ChunkLayout lay = chunk_layout(cache->plan, cache->B, a.n_max, a.layer, cache->num_sms);
+  const ChunkLayout lay = chunk_layout(cache->plan, cache->B, a.n_max, a.layer, cache->num_sms, cv.kv_format);
   if (tokens > INT32_MAX || (int64_t)kChunkSeqs * cv.Hkv * std::max(lay.w.items_q, lay.w.far_tiles) > (1 << 30))
     return fail(LK_ERR_UNSUPPORTED, "%s: %d sequences of %d tokens are too many for one call", what, cache->B, a.n_max);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1436,7 +1444,7 @@ lk_status lk_chunk_workspace_bytes(lk_plan plan, int32_t batch, int32_t n_max, s
   if (batch < 1 || (int64_t)batch * plan->d.num_kv_heads > (1 << 20))
     return fail(LK_ERR_ARG, "batch %d out of range", batch);
   if (n_max < 0) return fail(LK_ERR_ARG, "lk_chunk_workspace_bytes: n_max = %d < 0", n_max);
-  *bytes = chunk_layout(*plan, batch, n_max, -1, kChunkMaxCtas).total;
+  *bytes = chunk_layout(*plan, batch, n_max, -1, kChunkMaxCtas, kKvBf16).total;
   return LK_OK;
 }
 

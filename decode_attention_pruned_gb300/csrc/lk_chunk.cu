@@ -18,10 +18,14 @@
 //   A  region A of the cache (sinks, window ring, LOCAL ring, SPECIAL rows),
 //      full width, near pairs only
 //   C  the chunk's own k and v, full width, near pairs only
-//   M  the middle rows of the cache, kept channels
+//   M  the middle rows of the cache, kept channels (INT8 / FP8 caches: their
+//      sealed blocks)
 //   F  the tokens that leave the window within the chunk, kept channels, far
 //      pairs only: a first kernel lays their kept channels and V out in the
-//      workspace, as ready-made tile images
+//      workspace, as ready-made tile images (INT8 / FP8 caches: the middle rows
+//      that no block has sealed yet before them, and K at full width with zeros
+//      in the pruned channels, so that q on the kept channels serves the sealed
+//      blocks alone)
 // A pair that is far for an early layout of its token (ring row or chunk row)
 // is therefore scored once, on k channels, from F, and a tile needs no
 // element-by-element choice of score.
@@ -72,10 +76,14 @@ struct Item {
   int sinks;             // t < sinks: near
   int rows_a, nA;        // region-A rows the item looks at, and tiles
   int cs, c0, nC;        // chunk tiles 0 .. cs - 1, then c0 ..; nC in all
-  int mid, nM;           // middle rows and tiles (INT8 / FP8: the first nS of them sealed blocks)
-  int nS;
+  int mid, nM;           // middle rows and tiles (INT8 / FP8: of sealed blocks)
   int far0, rows_f, nF;  // position of F row 0, F rows the item looks at, tiles
 };
+// First tile of M, and of F: full-width tiles come before those on k channels.
+template <bool kQuant>
+__device__ __forceinline__ int first_m(const Item& it) { return it.nA + it.nC + (kQuant ? it.nF : 0); }
+template <bool kQuant>
+__device__ __forceinline__ int first_f(const Item& it) { return it.nA + it.nC + (kQuant ? 0 : it.nM); }
 
 struct Tile {
   int type, r0, rows;    // first row within its place, valid rows
@@ -85,13 +93,17 @@ __device__ __forceinline__ int chunk_len(const ChunkArgs& a, int i) {
   return __ldcg(&a.cv.active[a.b0 + i]) != 0 ? a.lens[i] : 0;
 }
 
-// Tokens that have left the window of a FULL head by the chunk's end, from
-// position `first` on.
-__device__ __forceinline__ int far_rows(const CacheView& cv, int N, int n, int& first) {
-  first = max(cv.S, N - cv.W);
-  return max(0, N + n - cv.W - first);
+// F rows of a FULL head with k kept channels once the chunk's first n tokens are
+// in: the tokens from position `first` on that have left the window.  bf16: those
+// that have done so within the chunk.  INT8 / FP8: those that are in no sealed
+// block (with k = 128, where every token is near, those that left before the chunk).
+template <bool kQuant>
+__device__ __forceinline__ int far_rows(const CacheView& cv, int k, int N, int n, int& first) {
+  first = kQuant ? cv.S + max(0, N - cv.S - cv.W) / kQBlockRows * kQBlockRows : max(cv.S, N - cv.W);
+  return max(0, N + (kQuant && k == kHeadDim ? 0 : n) - cv.W - first);
 }
 
+template <bool kQuant>
 __device__ __forceinline__ bool item_info(const ChunkArgs& a, const ChunkWork& w, int e, Item& it) {
   const CacheView& cv = a.cv;
   const int qi = e % w.items_q, sh = e / w.items_q;
@@ -118,11 +130,8 @@ __device__ __forceinline__ bool item_info(const ChunkArgs& a, const ChunkWork& w
       it.win = cv.W;
       it.sinks = cv.S;
     }
-    if (it.k > 0) it.mid = max(0, N - cv.S - cv.W);
-    if (it.k > 0 && it.k < kHeadDim) {
-      far_rows(cv, N, it.n, it.far0);
-      it.rows_f = max(0, N + it.i0 + it.ntok - cv.W - it.far0);
-    }
+    if (it.k > 0) it.mid = max(0, N - cv.S - cv.W) / (kQuant ? kQBlockRows : 1) * (kQuant ? kQBlockRows : 1);
+    if (it.k > 0 && (kQuant || it.k < kHeadDim)) it.rows_f = far_rows<kQuant>(cv, it.k, N, it.i0 + it.ntok, it.far0);
   } else if (hd.policy == kLocal) {
     na = min(N, cv.W_loc);
     it.win = cv.W_loc;
@@ -137,7 +146,6 @@ __device__ __forceinline__ bool item_info(const ChunkArgs& a, const ChunkWork& w
   it.cs = N < it.sinks ? min((it.sinks - N + kTile - 1) / kTile, it.c0) : 0;
   it.nC = it.cs + (it.i0 + it.ntok - 1) / kTile - it.c0 + 1;
   it.nM = (it.mid + kTile - 1) / kTile;
-  it.nS = kv_quantized(cv.kv_format) ? it.mid / kQBlockRows : 0;
   it.nF = (it.rows_f + kTile - 1) / kTile;
   return true;
 }
@@ -146,6 +154,7 @@ __device__ __forceinline__ uint32_t cost_kept(const ChunkWork& w, const Item& it
   return (uint32_t)(w.cost_kept + (it.k * w.cost_k >> 3));
 }
 
+template <bool kQuant>
 __device__ __forceinline__ Tile tile_at(const Item& it, int j) {
   Tile t;
   if (j < it.nA) {
@@ -156,21 +165,20 @@ __device__ __forceinline__ Tile tile_at(const Item& it, int j) {
     t.type = kTileC;
     t.r0 = (j < it.cs ? j : it.c0 + j - it.cs) * kTile;
     t.rows = it.n - t.r0;
-  } else if ((j -= it.nC) < it.nM) {
-    t.type = kTileM;
+  } else if ((j -= it.nC) < (kQuant ? it.nF : it.nM)) {
+    t.type = kQuant ? kTileF : kTileM;
     t.r0 = j * kTile;
-    t.rows = it.mid - t.r0;
+    t.rows = (kQuant ? it.rows_f : it.mid) - t.r0;
   } else {
-    t.type = kTileF;
-    t.r0 = (j - it.nM) * kTile;
-    t.rows = it.rows_f - t.r0;
+    t.type = kQuant ? kTileM : kTileF;
+    t.r0 = (j - (kQuant ? it.nF : it.nM)) * kTile;
+    t.rows = (kQuant ? it.mid : it.rows_f) - t.r0;
   }
   t.rows = min(t.rows, kTile);
   return t;
 }
 
-// Image of one F tile: kept channels as the middle's tiles lie in shared
-// memory, then V.
+// Image of one F tile: K as its tile lies in shared memory, then V.
 __device__ __forceinline__ uint8_t* far_tile(const ChunkArgs& a, const ChunkWork& w, int seq, int h, int tile) {
   return w.far + (((int64_t)seq * a.cv.Hkv + h) * w.far_tiles + tile) * w.far_bytes;
 }
@@ -187,13 +195,16 @@ __device__ __forceinline__ uint32_t kept_byte(int k, int r, int c, int rows = kT
 // flags the chunk's special tokens; a block per F tile lays out its image.
 constexpr int kPlanThreads = 256;
 
+template <bool kQuant>
 __device__ __forceinline__ uint64_t item_cost(const ChunkWork& w, const Item& it) {
-  return (uint64_t)w.cost_item + (uint64_t)(it.nA + it.nC) * w.cost_wide + (uint64_t)(it.nM + it.nF) * cost_kept(w, it);
+  const int m0 = first_m<kQuant>(it);
+  return (uint64_t)w.cost_item + (uint64_t)m0 * w.cost_wide + (uint64_t)(tiles_of(it) - m0) * cost_kept(w, it);
 }
 
 // Each thread sums a run of items, the block scans the sums; then a thread per
 // CTA finds the run its first offset floor(iC/P) falls into, by bisection, and
 // walks that run's items.
+template <bool kQuant>
 __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
   __shared__ uint64_t s_warp[kPlanThreads / 32];
   __shared__ uint64_t s_off[kPlanThreads + 1];
@@ -203,7 +214,7 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
   uint64_t mine = 0;
   Item it;
   for (int e = min(E, tid * per); e < min(E, (tid + 1) * per); ++e)
-    if (item_info(a, w, e, it)) mine += item_cost(w, it);
+    if (item_info<kQuant>(a, w, e, it)) mine += item_cost<kQuant>(w, it);
   uint64_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -230,14 +241,14 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
   uint64_t at = s_off[run];
   int2 start = make_int2(E, 0);
   for (int e = run * per; e < E && tid < P; ++e) {
-    if (!item_info(a, w, e, it)) continue;
-    const uint64_t end = at + item_cost(w, it);
+    if (!item_info<kQuant>(a, w, e, it)) continue;
+    const uint64_t end = at + item_cost<kQuant>(w, it);
     if (x < end) {
       // (an item's own share comes before its tiles)
-      const uint64_t r = x - at - min(x - at, (uint64_t)w.cost_item), wide = (uint64_t)(it.nA + it.nC) * w.cost_wide;
+      const uint64_t r = x - at - min(x - at, (uint64_t)w.cost_item), wide = (uint64_t)first_m<kQuant>(it) * w.cost_wide;
       const uint32_t kept = cost_kept(w, it);
       const int t = (int)(r <= wide ? (r + w.cost_wide - 1) / w.cost_wide
-                                    : it.nA + it.nC + (r - wide + kept - 1) / kept);
+                                    : first_m<kQuant>(it) + (r - wide + kept - 1) / kept);
       start = t < tiles_of(it) ? make_int2(e, t) : make_int2(e + 1, 0);
       break;
     }
@@ -292,6 +303,77 @@ __device__ void plan_special(const ChunkArgs& a, const ChunkWork& w, int seq) {
   }
 }
 
+// INT8 / FP8 caches: K at full width, zeros in the pruned channels.  A block lays
+// out half a tile's rows.
+constexpr int kPlanRows = kTile / 2;
+__device__ void plan_far_wide(const ChunkArgs& a, const ChunkWork& w, int seq, int h, int tile, int part) {
+  const CacheView& cv = a.cv;
+  const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + h];
+  const int k = hd.n_kept;
+  if (hd.policy != kFull || k == 0) return;
+  const int n = chunk_len(a, seq), b = a.b0 + seq;
+  if (n == 0) return;
+  const int N = __ldcg(&cv.len[a.layer * cv.B + b]);
+  const int tid = threadIdx.x, c = tid % 16;  // a thread's 8 channels
+  const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim;
+  int first;
+  const int row0 = tile * kTile + part * kPlanRows;
+  const int rows = min(kPlanRows, far_rows<true>(cv, k, N, n, first) - row0);
+  if (rows <= 0) return;
+  const int rows16 = (rows + 15) & ~15;       // P.V takes 16 keys at a time: the last ones are zero
+  const int open = max(0, min(rows, N - cv.W - first - row0));         // of them in the open block
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t abase = hd.row_a + (int64_t)b * hd.cap_a, bbase = (int64_t)b * hd.cap_b + row0;
+  // Every load of a thread is issued before it waits for one: its kept channel, its
+  // share of the open block's rows (kept channels side by side), its 8 channels of 4 rows.
+  const int channel = tid < k ? kept[tid] : 0;
+  const uint4* from = reinterpret_cast<const uint4*>(cv.pool[hd.pool_kb] + (hd.krow_b + bbase) * k);
+  uint4 packed[4], kx[4], vx[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int y = x * kPlanThreads + tid, r = 16 * x + tid / 16, t = first + row0 + r;
+    packed[x] = y < open * k / 8 ? from[y] : zero;
+    kx[x] = vx[x] = zero;
+    if (r >= rows) continue;
+    const int64_t ring = (abase + cv.S + (t - cv.S) % cv.W) * kHeadDim, at = (int64_t)b * a.n_max + (t - N);
+    if (r >= open)
+      kx[x] = *reinterpret_cast<const uint4*>((t < N ? cv.pool[kPoolK128] + ring
+                                                     : a.k + at * a.k_stride + h * kHeadDim) + 8 * c);
+    vx[x] = *reinterpret_cast<const uint4*>((r < open ? cv.pool[kPoolV] + (hd.vrow_b + bbase + r) * kHeadDim
+                                             : t < N  ? cv.pool[kPoolV] + ring
+                                                      : a.v + at * a.v_stride + h * kHeadDim) + 8 * c);
+  }
+  __shared__ uint4 s_open[kPlanRows * kHeadDim / 8];
+  __shared__ uint32_t s_kept[4];
+  if (tid < 4) s_kept[tid] = 0;
+  __syncthreads();
+  if (tid < k) atomicOr(&s_kept[channel >> 5], 1u << (channel & 31));
+#pragma unroll
+  for (int x = 0; x < 4; ++x) s_open[x * kPlanThreads + tid] = packed[x];
+  __syncthreads();
+  // which of this thread's channels are kept, and how many before them
+  const uint32_t word = s_kept[c >> 2], mine = word >> 8 * (c & 3) & 0xffu;
+  int before = __popc(word & ((1u << 8 * (c & 3)) - 1u));
+  for (int x = 0; x < c >> 2; ++x) before += __popc(s_kept[x]);
+  uint8_t* image = far_tile(a, w, seq, h, tile);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int r = 16 * x + tid / 16;
+    if (r >= rows16) continue;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(s_open) + r * k;
+    auto two = [&](uint32_t u, int i) -> uint32_t {
+      const uint32_t lo = mine >> i & 1u, hi = mine >> (i + 1) & 1u;
+      const int at = before + __popc(mine & ((1u << i) - 1u));
+      if (r < open) u = (uint32_t)p[min(at, k - 1)] | (uint32_t)p[min(at + (int)lo, k - 1)] << 16;
+      return u & ((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
+    };
+    const uint4 u = kx[x];
+    *reinterpret_cast<uint4*>(image + kept_byte(kHeadDim, part * kPlanRows + r, c)) =
+        make_uint4(two(u.x, 0), two(u.y, 2), two(u.z, 4), two(u.w, 6));
+    *reinterpret_cast<uint4*>(image + kTile * 2 * kHeadDim + kept_byte(kHeadDim, part * kPlanRows + r, c)) = vx[x];
+  }
+}
+
 __device__ void plan_far(const ChunkArgs& a, const ChunkWork& w, int seq, int h, int tile) {
   const CacheView& cv = a.cv;
   const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + h];
@@ -301,7 +383,7 @@ __device__ void plan_far(const ChunkArgs& a, const ChunkWork& w, int seq, int h,
   if (n == 0) return;
   const int N = __ldcg(&cv.len[a.layer * cv.B + b]);
   int first;
-  const int rows = min(kTile, far_rows(cv, N, n, first) - tile * kTile);
+  const int rows = min(kTile, far_rows<false>(cv, k, N, n, first) - tile * kTile);
   if (rows <= 0) return;
   const int rows16 = (rows + 15) & ~15;       // P.V takes 16 keys at a time: the last ones are zero
   uint8_t* image = far_tile(a, w, seq, h, tile);
@@ -348,13 +430,14 @@ __device__ void plan_far(const ChunkArgs& a, const ChunkWork& w, int seq, int h,
   }
 }
 
+template <bool kQuant>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a,
                                                                   const ChunkWork w) {
   grid_dependency_wait();
   grid_launch_dependents();
   int x = blockIdx.x;
   if (x == 0) {
-    plan_line(a, w);
+    plan_line<kQuant>(a, w);
     return;
   }
   if (--x < w.special_seqs) {
@@ -362,7 +445,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     return;
   }
   x -= w.special_seqs;
-  plan_far(a, w, x / w.far_tiles / a.cv.Hkv, x / w.far_tiles % a.cv.Hkv, x % w.far_tiles);
+  const int part = kQuant ? x & 1 : 0;
+  if (kQuant) x >>= 1;
+  const int seq = x / w.far_tiles / a.cv.Hkv, h = x / w.far_tiles % a.cv.Hkv, tile = x % w.far_tiles;
+  if (kQuant) plan_far_wide(a, w, seq, h, tile, part);
+  else plan_far(a, w, seq, h, tile);
 }
 
 // ------------------------------------------------------------- attention
@@ -376,7 +463,8 @@ constexpr int kWideBytes = kTile * kHeadDim * 2;
 // softmax group.  Else on one, and the groups take alternate key tiles.
 //
 // Shared memory: q at full width, q on the kept channels (as wide as the
-// layer's widest such head), and a byte ring that the key and value tiles go
+// layer's widest such head; over sealed blocks as f16, 128 channels among them),
+// and a byte ring that the key and value tiles go
 // through in order, each taking what it needs (a key tile on 32 channels 8 KB,
 // full-width ones and values 32 KB), so that narrow heads have the more tiles
 // in flight.
@@ -397,7 +485,11 @@ struct Smem {
   static constexpr int kML = 2048;                       // second group's (m, l)
   static constexpr int kVScale = kML + (kDual ? 0 : kTile * 8);          // of the tiles in flight, four per ring
   static constexpr int kKScale = kVScale + (kQuant ? kRings * 4 * kTile * 4 : 0);       // of the jobs
-  static constexpr int kQ = (kKScale + (kQuant ? kRings * kJobs * kTile * 4 : 0) + 1023) / 1024 * 1024;
+  // what scores are scaled back by: a factor per sealed tile in flight, and per row of
+  // this segment's q and of the next one's (one group may be a segment ahead)
+  static constexpr int kTileBack = kKScale + (kQuant ? kRings * kJobs * kTile * 4 : 0);
+  static constexpr int kRowBack = kTileBack + (kQuant ? kRings * kSlots * 4 : 0);
+  static constexpr int kQ = (kRowBack + (kQuant ? 2 * kQTiles * kTile * 4 : 0) + 1023) / 1024 * 1024;
   static constexpr int kJobBytes = 32;
   static constexpr int kMakers = kDual ? 4 : 2;          // warps that make a ring's tiles out of sealed blocks
   static constexpr int kArrivals = kQuant ? kMakers : 1; // that complete a tile
@@ -471,6 +563,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -493,7 +590,7 @@ __device__ __forceinline__ void visible(const ChunkArgs& a, const ChunkWork& w, 
   if (t.type == kTileM) {
     add_range(m, 0, t.rows);
   } else if (t.type == kTileF) {
-    add_range(m, 0, min(t.rows, it.N + i - it.win + 1 - it.far0 - t.r0));
+    add_range(m, 0, min(t.rows, it.N + i - cv.W + 1 - it.far0 - t.r0));
   } else if (t.type == kTileC) {
     const int hi = i - t.r0 + 1;
     add_range(m, hi - it.win, hi);
@@ -522,6 +619,21 @@ __device__ __forceinline__ void visible(const ChunkArgs& a, const ChunkWork& w, 
     for (int x = 0; x < 4; ++x) m[x] &= v[x];
   }
 }
+
+// 2^e, e kept to what an fp32 number can be.
+__device__ __forceinline__ float power2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+
+// Scores of sealed blocks.  A key's channel is code times scale, 8 bits times 24.
+// Rounded to bf16 it would be off by up to 2^-8 of itself, and the attention with
+// it (relative error against fp64 2.7 to 3.3e-3 instead of 2.3 to 2.4e-3, o's own
+// rounding being 1.66e-3), so these keys and the q they meet are f16: q exactly
+// (8 bits), the scale and the product to 11 bits each.  What f16 lacks in range
+// goes into exponents: a block's scales are moved so that the largest lies in
+// [2^6, 2^7) (448 times that is below f16's largest), a row of q so that its
+// largest channel lies in [2^14, 2^15), and the softmax moves the row's scores of
+// the block back.  Only channels whose scale is 2^-20 of the block's largest, or
+// whose q is 2^-31 of the row's largest, keep fewer bits.
+constexpr int kScaleExp = 6, kRowTop = 14;
 
 // The keys or the values of a sealed block, to be turned into a tile.  (Not
 // both at once: the ring may have room for the values only when the tile
@@ -620,7 +732,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
     while (true) {
       ++s.e;
       if (s.e > last.x || (s.e == last.x && last.y == 0)) return false;
-      if (!item_info(a, w, s.e, s.it)) continue;
+      if (!item_info<kQuant>(a, w, s.e, s.it)) continue;
       s.nt = tiles_of(s.it);
       s.t0 = s.e == first.x ? first.y : 0;
       s.t1 = s.e == last.x ? last.y : s.nt;
@@ -634,14 +746,14 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
   auto segment = [&](int idx) -> const Segment& {
     return *reinterpret_cast<const Segment*>(sm + L::kSeg + (idx & 1) * L::kSegBytes);
   };
-  // whether a segment has tiles on the kept channels only
-  auto gathers = [&](const Segment& s) { return s.it.k > 0 && s.it.k < kHeadDim && s.t1 > s.it.nA + s.it.nC; };
+  // whether a segment has tiles that take q on the kept channels
+  auto gathers = [&](const Segment& s) { return s.it.k > 0 && (kQuant || s.it.k < kHeadDim) && s.t1 > first_m<kQuant>(s.it); };
 
   if (kQuant && warp >= 12) {
     // ----------------------------------------------------------- the makers
-    // Turn sealed blocks into bf16 tiles: keys as code times scale, rounded
-    // once; values as their codes, which bf16 holds exactly (the weights take
-    // their scales).  The codes of a 128-channel row lie where the row's second
+    // Turn sealed blocks into tiles: keys as code times scale, rounded once to
+    // f16; values as their codes, which bf16 holds exactly (the weights take their
+    // scales).  The codes of a 128-channel row lie where the row's second
     // half will: eight lanes read the row, then write it.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     constexpr int kMade = 32 * L::kMakers;                // threads per ring
@@ -659,6 +771,16 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       const Job job = *reinterpret_cast<const Job*>(sm + L::kJob + jn * L::kJobBytes);
       if (job.width == 0) break;
       uint8_t* to = sm + job.at;
+      float to_range = 1.f;
+      if (job.values == 0) {
+        // (scales are not negative: they order as their bits do)
+        uint32_t top = 0;
+        for (int x = lane; x < job.width; x += 32)
+          top = max(top, *reinterpret_cast<const uint32_t*>(sm + job.scales + 4 * x));
+        const int e = max((int)(__reduce_max_sync(0xffffffffu, top) >> 23) - 127 - kScaleExp, -126);
+        to_range = power2(-e);
+        if (mt == 0) *reinterpret_cast<float*>(sm + L::kTileBack + 4 * (ri * L::kSlots + job.slot)) = power2(e);
+      }
       auto convert = [&](auto channels, auto values) {
         constexpr int kWidth = decltype(channels)::value, kGroups = kWidth / 16;
         constexpr bool kV = decltype(values)::value;
@@ -669,12 +791,13 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         constexpr int kRows = kMade / kGroups, kOnce = 2;
         const int c = mt % kGroups, r0 = mt < kRows * kGroups ? mt / kGroups : kTile;
         const uint4* codes = reinterpret_cast<const uint4*>(to + kTile * kWidth * (kWidth == kHeadDim ? 1 : 2));
-        float scale[kV ? 1 : 16];
+        uint32_t scale[kV ? 1 : 8];
         if (!kV) {
 #pragma unroll
-          for (int x = 0; x < 16; x += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(sm + job.scales + 4 * (16 * c + x));
-            scale[x] = f.x, scale[x + 1] = f.y, scale[x + 2] = f.z, scale[x + 3] = f.w;
+          for (int x = 0; x < 8; x += 2) {
+            const float4 f = *reinterpret_cast<const float4*>(sm + job.scales + 4 * (16 * c + 2 * x));
+            scale[x] = pack_f16x2(f.x * to_range, f.y * to_range);
+            scale[x + 1] = pack_f16x2(f.z * to_range, f.w * to_range);
           }
         }
 #pragma unroll 1
@@ -695,8 +818,13 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             for (int x = 0; x < 4; ++x) {
               uint32_t e, o;
               codes_f16<kFmt, kV>(in[x], e, o);
-              lo[x] = pack_bf16x2(f16_lo(e) * (kV ? 1.f : scale[2 * x]), f16_hi(e) * (kV ? 1.f : scale[2 * x + 1]));
-              hi[x] = pack_bf16x2(f16_lo(o) * (kV ? 1.f : scale[8 + 2 * x]), f16_hi(o) * (kV ? 1.f : scale[9 + 2 * x]));
+              if (kV) {
+                lo[x] = pack_bf16x2(f16_lo(e), f16_hi(e));
+                hi[x] = pack_bf16x2(f16_lo(o), f16_hi(o));
+              } else {
+                lo[x] = mul_f16x2(e, scale[x]);
+                hi[x] = mul_f16x2(o, scale[4 + x]);
+              }
             }
             if (kGroups != 6 || r < kTile) {
               *reinterpret_cast<uint4*>(to + kept_byte(kWidth, r, 2 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -773,7 +901,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           const int64_t krow_b = hd.krow_b, vrow_b = hd.vrow_b;
           const int64_t abase = hd.row_a + (int64_t)it.b * hd.cap_a, bbase = (int64_t)it.b * hd.cap_b;
           const int32_t* pages = cv.max_pages > 0 ? page_row(cv, a.layer, it.b, it.h) : nullptr;
-          const int m0 = it.nA + it.nC;
+          const int m0 = first_m<kQuant>(it);
           if (ri == 0) {
             if (s.idx > 0) ok = wait(base + L::kQEmpty, (s.idx - 1) & 1);
             if (!ok) break;
@@ -792,20 +920,22 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             mbar_arrive_expect_tx(bar, bytes);
           };
           auto load = [&](int j, bool isv, int32_t pg) -> bool {
-            const Tile t = tile_at(it, j);
-            const bool wide = isv || t.type <= kTileC || it.k == kHeadDim;
+            const Tile t = tile_at<kQuant>(it, j);
+            const bool wide = isv || t.type <= kTileC || it.k == kHeadDim || (kQuant && t.type == kTileF);
             // (the codes of sealed keys on part of the channels land behind the tile)
-            const bool seal = kQuant && t.type == kTileM && t.r0 < it.nS * kTile;
+            const bool seal = kQuant && t.type == kTileM;
             // A tile's keys are waited for while the values before them are in use:
-            // keys never take more than the keys before them did, whose place they
-            // then find, so full-width ones take what sealed ones on 96 channels do.
+            // keys never take more than the keys of their item before them did, whose
+            // place they then find, so full-width ones take what sealed ones on 96
+            // channels do.
             uint32_t at, bytes = wide ? (uint32_t)kWideBytes : (uint32_t)(kTile * (seal ? 3 : 2) * it.k);
-            if (kQuant && !isv && wide && w.kept_width == 96) bytes = kTile * 3 * 96;
+            if (kQuant && !isv && wide && it.k == 96) bytes = kTile * 3 * 96;
             if (!reserve(bytes, at)) return false;
             const uint32_t slot = put % L::kSlots;
             offs[slot] = at;
             // what the other threads have to know of the tile
-            info[slot] = (ring_at + at) >> 4 | (uint32_t)t.rows << 16 | (wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
+            info[slot] = (ring_at + at) >> 4 | (uint32_t)t.rows << 16 |
+                         (seal && !isv ? 3u + (uint32_t)it.k / 32 : wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
             const uint32_t dst = ring_at + at, bar = full + 8 * slot;
             ++put;
             by_job = (by_job & ~(1u << slot)) | (seal ? 1u << slot : 0u);
@@ -838,8 +968,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               expect(bar, kWideBytes);
               tma_load_3d(dst, &maps.pool[isv ? kPoolV : kPoolK128], 0, (int)(abase + t.r0), 0, bar, keep);
             } else if (t.type == kTileM) {
-              const int64_t r = !kQuant && pages != nullptr ? (int64_t)max(0, pg) * kPageRows
-                                                            : bbase + t.r0 - (kQuant ? it.nS * kTile : 0);
+              const int64_t r = pages != nullptr ? (int64_t)max(0, pg) * kPageRows : bbase + t.r0;
               if (isv) {
                 expect(bar, kWideBytes);
                 tma_load_3d(dst, &maps.pool[kPoolV], 0, (int)(vrow_b + r), 0, bar, keep);
@@ -852,10 +981,10 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               // whole 16-row groups of each run of the image
               const uint32_t rows = (uint32_t)((t.rows + 15) & ~15);
               const uint8_t* image = far_tile(a, w, it.seq, it.h, t.r0 / kTile);
-              const int width = isv ? kHeadDim : it.k;
+              const int kw = kQuant ? kHeadDim : it.k, width = isv ? kHeadDim : kw;
               const uint32_t row = (width & 63) == 0 ? 128u : 64u;
               const int runs = width * 2 / (int)row;
-              if (isv) image += kTile * 2 * it.k;
+              if (isv) image += kTile * 2 * kw;
               expect(bar, rows * row * runs);
               for (int x = 0; x < runs; ++x)
                 bulk_load(dst + x * kTile * row, image + x * kTile * row, rows * row, bar, keep);
@@ -865,14 +994,15 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           // page id of the middle tile that key tile j is, if any; read a tile
           // before the loads that need it
           auto page_at = [&](int j) -> int32_t {
-            return pages != nullptr && j >= m0 && j < m0 + (kQuant ? it.nS : it.nM) ? __ldcg(pages + (j - m0)) : 0;
+            return pages != nullptr && j >= m0 && j < m0 + it.nM ? __ldcg(pages + (j - m0)) : 0;
           };
           constexpr int kStep = kDual ? 1 : 2;
           const int j0 = s.t0 + (kDual ? 0 : ri);
           int32_t page = page_at(j0);
           for (int j = j0; ok && j < s.t1; j += kStep) {
             const int32_t after = page_at(j + kStep);
-            ok = load(j, false, page) && load(j, true, page);
+#pragma unroll 1
+            for (int isv = 0; ok && isv < 2; ++isv) ok = load(j, isv != 0, page);
             page = after;
           }
         }
@@ -913,6 +1043,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       const int st = warp - 1;
       if (elect_one()) {
         constexpr uint32_t kDescS = mma_desc(128, kHalf, false), kDescO = mma_desc(128, kHeadDim, true);
+        constexpr uint32_t kDescS16 = mma_desc(128, kHalf, false, true);
         constexpr uint32_t kWideHi = desc_hi(1024, kSwizzle128), kThinHi = desc_hi(512, kSwizzle64);
         const uint32_t full = base + L::kFull + (kDual ? 0 : st * 8 * L::kSlots);
         const uint32_t empty = base + L::kEmpty + (kDual ? 0 : st * 8 * L::kSlots);
@@ -960,23 +1091,38 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           auto scores = [&](uint32_t what, auto which) {
             constexpr int kWhich = decltype(which)::value;
             const uint32_t d = s_at + kWhich * kHalf, k0 = desc_lo(16) | (what & 0x3fff), width = what >> 24;
-            auto run = [&](auto steps, uint32_t q) {
-              constexpr int kSteps = decltype(steps)::value;
-              constexpr bool kThin = kSteps == 2 || kSteps == 6;
-              constexpr uint32_t kHi = kThin ? kThinHi : kWideHi;
-              const uint32_t k = k0 + kWhich * kHalf * (kThin ? 4 : 8);
-              mma_ss<kHi, false>(d, q, k, kDescS);
-#pragma unroll
-              for (int y = 1; y < kSteps; ++y) {
-                const uint32_t at = kThin ? (y >> 1) * (kTile * 4) + (y & 1) * 2 : (y >> 2) * (kTile * 8) + (y & 3) * 2;
-                const uint32_t q_at = kThin ? (y >> 1) * q_stripe + (y & 1) * 2 : (y >> 2) * q_half + (y & 3) * 2;
-                mma_ss<kHi, true>(d, q + q_at, k + at, kDescS);
+            if (kQuant) {
+              // (in a loop: the makers pay for every instruction that an SM's roles fetch;
+              // written out as below 16 sequences of 8192 tokens take 136 us instead of 117)
+              const bool f16 = width > 3, thin = (width & 1) == 0;         // 4 .. 7: of sealed blocks
+              const int steps = 2 * ((int)(width & 3) + 1), run = thin ? 2 : 4;
+              const uint32_t q = f16 ? q_kept : q_wide, q_run = thin ? q_stripe : q_half;
+              const uint32_t k = k0 + kWhich * kHalf * (thin ? 4 : 8), k_run = thin ? kTile * 4 : kTile * 8;
+#pragma unroll 1
+              for (int y = 0; y < steps; ++y) {
+                const uint32_t out = (uint32_t)(y / run), in = (uint32_t)(y & (run - 1)) * 2;
+                mma_ss(d, thin ? kThinHi : kWideHi, q + out * q_run + in, k + out * k_run + in,
+                       f16 ? kDescS16 : kDescS, y > 0);
               }
-            };
-            if (width == 0) run(std::integral_constant<int, 2>(), q_kept);
-            else if (width == 3) run(std::integral_constant<int, 8>(), q_wide);
-            else if (width == 1) run(std::integral_constant<int, 4>(), q_kept);
-            else run(std::integral_constant<int, 6>(), q_kept);
+            } else {
+              auto run = [&](auto steps, uint32_t q) {
+                constexpr int kSteps = decltype(steps)::value;
+                constexpr bool kThin = kSteps == 2 || kSteps == 6;
+                constexpr uint32_t kHi = kThin ? kThinHi : kWideHi;
+                const uint32_t k = k0 + kWhich * kHalf * (kThin ? 4 : 8);
+                mma_ss<kHi, false>(d, q, k, kDescS);
+#pragma unroll
+                for (int y = 1; y < kSteps; ++y) {
+                  const uint32_t at = kThin ? (y >> 1) * (kTile * 4) + (y & 1) * 2 : (y >> 2) * (kTile * 8) + (y & 3) * 2;
+                  const uint32_t q_at = kThin ? (y >> 1) * q_stripe + (y & 1) * 2 : (y >> 2) * q_half + (y & 3) * 2;
+                  mma_ss<kHi, true>(d, q + q_at, k + at, kDescS);
+                }
+              };
+              if (width == 0) run(std::integral_constant<int, 2>(), q_kept);
+              else if (width == 3) run(std::integral_constant<int, 8>(), q_wide);
+              else if (width == 1) run(std::integral_constant<int, 4>(), q_kept);
+              else run(std::integral_constant<int, 6>(), q_kept);
+            }
             mma_commit(s_full + 8 * kWhich);
           };
           auto values = [&](uint32_t what, auto which, bool accumulate) {
@@ -1054,7 +1200,10 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
     const int tok = row / G, g = row - tok * G;
     uint32_t hs = 0, ends = 0, merges = 0;          // halves, segments and merges this group has done
     uint32_t entries = 0;                 // ring tiles before this segment
-    uint32_t sealed = 0;                  // tiles made of sealed blocks so far
+    uint32_t sealed = 0, gathered = 0;    // tiles made of sealed blocks, segments with q as f16 so far
+    auto row_back = [&](uint32_t n) {     // of the n-th segment with q as f16
+      return reinterpret_cast<float*>(sm + L::kRowBack) + ((n & 1) * L::kQTiles + (kDual ? st : 0)) * kTile;
+    };
     bool ok = true;
     for (int idx = 0; ok; ++idx) {
       ok = wait.warp(base + L::kQFull, idx & 1);
@@ -1069,16 +1218,45 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         const uint8_t* q = sm + L::kQ + (kDual ? st * kWideBytes : 0);
         uint8_t* to = sm + q_kept_at + (kDual ? st * w.kept_bytes : 0);
         const int groups = it.k / 8, rows = min(tq, it.ntok - (kDual ? st * tq : 0)) * G;
-        for (int y = tid - 128 - (kDual ? st * 128 : 0); y < rows * groups; y += kDual ? 128 : 256) {
-          const int r = y / groups, c = y - r * groups;
+        // channels 8 c .. 8 c + 7 of row r
+        auto eight = [&](int r, int c) {
           const uint4 kc = *reinterpret_cast<const uint4*>(kept + 8 * c);
           auto at = [&](uint32_t ch) {
             const uint8_t* from = q + kept_byte(kHeadDim, r, (int)ch >> 3, q_rows) + (ch & 7) * 2;
             return (uint32_t)*reinterpret_cast<const uint16_t*>(from);
           };
           auto two = [&](uint32_t p) { return at(p & 0xffffu) | at(p >> 16) << 16; };
-          *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c, q_rows)) =
-              make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
+          return make_uint4(two(kc.x), two(kc.y), two(kc.z), two(kc.w));
+        };
+        if (!kQuant) {
+          for (int y = tid - 128 - (kDual ? st * 128 : 0); y < rows * groups; y += kDual ? 128 : 256) {
+            const int r = y / groups, c = y - r * groups;
+            *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c, q_rows)) = eight(r, c);
+          }
+        } else {
+          // as f16, each row by its own exponent: a row's 4, 8 or 16 lanes (of which
+          // 12 have channels where 96 are kept) find its largest channel together
+          const int wide = groups <= 4 ? 2 : groups <= 8 ? 3 : 4, c = lane & ((1 << wide) - 1);
+          const int step = 32 >> wide;                   // rows a warp takes at once
+          for (int r0 = (kDual ? warp & 3 : warp - 4) * step; r0 < rows; r0 += (kDual ? 4 : 8) * step) {
+            const int r = r0 + (lane >> wide);
+            const bool has = r < rows && c < groups;
+            const uint4 u = has ? eight(r, c) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) top = max(top, max(in[x] >> 7 & 0xffu, in[x] >> 23 & 0xffu));
+            for (int d = 1; d < 1 << wide; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const int e = max((int)top - 127 - kRowTop, -120);
+            const float f = power2(-e);
+            uint32_t out[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) out[x] = pack_f16x2(bf16_lo(in[x]) * f, bf16_hi(in[x]) * f);
+            if (has)
+              *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c, q_rows)) = make_uint4(out[0], out[1], out[2], out[3]);
+            if (has && c == 0) row_back(gathered)[r] = kScaleLog2 * power2(e);
+          }
+          ++gathered;
         }
         fence_async_smem();
         __syncwarp();
@@ -1088,7 +1266,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       if (lane == 0) mbar_arrive(base + L::kQEmpty);
       const uint32_t end = entries + 2 * (kDual ? s.t1 - s.t0 : (s.t1 - s.t0 - st + 1) / 2);
       if (idle_group) {
-        if (kQuant) sealed += max(0, min(s.t1, it.nA + it.nC + it.nS) - max(s.t0, it.nA + it.nC));
+        if (kQuant) sealed += max(0, s.t1 - max(s.t0, first_m<kQuant>(it)));
         entries = end;
         continue;
       }
@@ -1096,22 +1274,24 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       const bool mine = tok < tq && i < it.i0 + it.ntok;
       float m = -INFINITY, l = 0.f;
       bool begun = false;                 // a half of this segment is done
-      const int m0 = it.nA + it.nC, m1 = m0 + it.mid / kTile, f0 = m0 + it.nM;
+      const int m0 = first_m<kQuant>(it), m1 = m0 + it.mid / kTile, f0 = first_f<kQuant>(it);
+      bool scaled = false;                // this row's factor is known (the same for a whole warp)
+      float back = 1.f;
       const int i_first = it.i0 + (kDual ? st * tq : 0), i_last = min(i_first + tq, it.i0 + it.ntok) - 1;
-      const int f1 = f0 + max(0, it.N + i_first - it.win + 1 - it.far0) / kTile;
+      const int f1 = f0 + min(kQuant ? it.rows_f : kFar, max(0, it.N + i_first - cv.W + 1 - it.far0)) / kTile;
       for (int j = s.t0 + (kDual ? 0 : st); ok && j < s.t1; j += kDual ? 1 : 2) {
         uint32_t vis[4] = {};
         // tiles that every query of the group sees whole, the common case
         bool all = j >= m0 && j < m1;
-        if (j >= f0) {
+        if (j >= f0 && (!kQuant || j < m0)) {
           all = j < f1;
-        } else if (j >= it.nA && j < m0) {
-          const int r0 = tile_at(it, j).r0;
+        } else if (j >= it.nA && j < (kQuant ? f0 : m0)) {
+          const int r0 = tile_at<kQuant>(it, j).r0;
           all = r0 + kTile - 1 <= i_first && i_last - r0 < it.win && it.policy != kSpecial;
         }
         int halves = 2, rows = kTile;
         if (!all) {
-          const Tile t = tile_at(it, j);
+          const Tile t = tile_at<kQuant>(it, j);
           visible(a, w, it, t, i, vis);
           all = __all_sync(0xffffffffu, !mine || (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu);
           if (t.rows <= kHalf) halves = 1;      // no key in the second half
@@ -1131,14 +1311,24 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
                 make_uint4(0u, 0u, 0u, 0u);
           fence_async_smem();
         }
-        // a sealed block's values are codes: their scales, once they are there
+        // a sealed block's values are codes: their scales, once they are there, and the
+        // scores' factor (made before the values, by the same warps)
         const float* vscale = nullptr;
-        if (kQuant && j >= m0 && j < m0 + it.nS) {
+        float score_scale = kScaleLog2;
+        if (kQuant && j >= m0) {
           const uint32_t e = entries + 2 * ((j - s.t0) / (kDual ? 1 : 2)) + 1;
           const uint32_t slot = e % L::kSlots + (kDual ? 0 : st * L::kSlots);
           ok = wait.warp(base + L::kFull + 8 * slot, (e / L::kSlots) & 1);
           if (!ok) break;
           vscale = reinterpret_cast<const float*>(sm + L::kVScale) + ((kDual ? 0 : 4 * st) + (sealed++ & 3)) * kTile;
+          if (!scaled) {
+            ok = wait.warp(base + L::kQKFull + (kDual ? 8 * st : 0), (gathered - 1) & 1);
+            if (!ok) break;
+            back = row_back(gathered - 1)[row];
+            scaled = true;
+          }
+          const uint32_t k_slot = (e - 1) % L::kSlots + (kDual ? 0 : st * L::kSlots);
+          score_scale = back * *reinterpret_cast<const volatile float*>(sm + L::kTileBack + 4 * k_slot);
         }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -1169,7 +1359,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 #pragma unroll
           for (int c = 8; c < kHalf; c += 2)
             mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kQuant ? score_scale : kScaleLog2);
           // (nobody's rows score whatever lies behind q: they move no one's maximum)
           if (!kDual && !mine) top = -INFINITY;
           // The maximum moves only when a score exceeds it by 2^8: below that p
@@ -1198,7 +1388,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             }
           }
           const float off = m == -INFINITY ? 0.f : -m;
-          const uint64_t scale2 = pair(kScaleLog2, kScaleLog2), off2 = pair(off, off);
+          const float sc = kQuant ? score_scale : kScaleLog2;
+          const uint64_t scale2 = pair(sc, sc), off2 = pair(off, off);
           uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int c = 0; c < kHalf; c += 2) {
@@ -1466,8 +1657,9 @@ cudaError_t launch_attn(const ChunkMaps& maps, const ChunkArgs& args, const Chun
 }  // namespace
 
 cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& w, cudaStream_t stream) {
-  const unsigned plan_blocks = 1u + w.special_seqs + (unsigned)(args.nb * args.cv.Hkv) * w.far_tiles;
-  cudaError_t err = launch_after(chunk_plan_kernel, dim3(plan_blocks), kPlanThreads, 0, stream, args, w);
+  const unsigned parts = kv_quantized(args.cv.kv_format) ? 2u : 1u;
+  const unsigned plan_blocks = 1u + w.special_seqs + (unsigned)(args.nb * args.cv.Hkv) * w.far_tiles * parts;
+  cudaError_t err = launch_after(kv_quantized(args.cv.kv_format) ? chunk_plan_kernel<true> : chunk_plan_kernel<false>, dim3(plan_blocks), kPlanThreads, 0, stream, args, w);
   if (err != cudaSuccess) return err;
   err = args.cv.kv_format == kKvInt8  ? launch_attn<kKvInt8>(maps, args, w, stream)
         : args.cv.kv_format == kKvFp8 ? launch_attn<kKvFp8>(maps, args, w, stream)

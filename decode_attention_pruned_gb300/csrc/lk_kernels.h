@@ -125,13 +125,12 @@ struct ChunkWork {
   int32_t box_tokens;       // queries per load of q
   int32_t max_ctas;
   int32_t part_rows;        // rows of a partial
-  int32_t far_tiles;        // F tile images per (sequence, head); 0: no head has kept channels and pruned ones
+  int32_t far_tiles;        // F tile images per (sequence, head); 0: no head needs any
   int32_t far_bytes;        // of one image
   int32_t special_seqs;     // sequences whose special tokens are flagged (0: no SPECIAL head)
   int32_t special_words;    // 32-token words per sequence
   int32_t q_rows;           // of a query tile in shared memory
-  int32_t kept_width;       // channels of the widest pruned head that keeps some
-  int32_t kept_bytes;       // of a query tile on the kept channels
+  int32_t kept_bytes;       // of a query tile on the kept channels of the head that keeps most
   int32_t cost_item;        // what an item weighs on the work line, a full-width key tile, and one on k
   int32_t cost_wide;        //   channels: cost_kept + k cost_k / 8
   int32_t cost_kept, cost_k;

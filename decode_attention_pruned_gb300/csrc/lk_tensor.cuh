@@ -82,9 +82,10 @@ __host__ __device__ constexpr uint32_t desc_lo(uint32_t leading) { return (leadi
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t stride, uint32_t swizzle) {
   return stride >> 4 | 1u << 14 | swizzle << 29;
 }
-// Instruction descriptor: bf16 x bf16 -> fp32, M x N, B K-major or MN-major.
-__host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn_major) {
-  return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 |
+// Instruction descriptor: bf16 x bf16 or f16 x f16 -> fp32, M x N, B K-major or
+// MN-major.
+__host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn_major, bool f16 = false) {
+  return 1u << 4 | (f16 ? 0u : 1u << 7 | 1u << 10) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 |
          (uint32_t)(m / 16) << 24;
 }
 
@@ -98,6 +99,16 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
       "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
       "r"(a_lo), "r"(b_lo), "r"(desc), "n"(kAccumulate ? 1 : 0), "n"(kHi)
+      : "memory");
+}
+// The same with the descriptors' upper half and what to do with D known at run time.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t hi, uint32_t a_lo, uint32_t b_lo, uint32_t desc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(desc), "r"((uint32_t)accumulate), "r"(hi)
       : "memory");
 }
 template <uint32_t kHi>

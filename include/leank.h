@@ -427,8 +427,9 @@ lk_status lk_chunk_workspace_bytes(lk_plan plan, int32_t batch, int32_t n_max, s
  * local_only_window tokens; SPECIAL heads the special ones that they have rows
  * for.  One softmax runs over all of it; a query that sees nothing gives 0.
  * Middle tokens are read as the cache holds them when the call runs: sealed
- * INT8 / FP8 blocks as their dequantised values (keys rounded to bf16),
- * everything else, the chunk's own tokens included, in bf16.
+ * INT8 / FP8 blocks as their dequantised values (a key's scale and its product
+ * with the code rounded to 11 bits), everything else, the chunk's own tokens
+ * included, in bf16.
  * k, v and the cache must hold finite values; o must not overlap the inputs.
  * workspace: >= lk_chunk_workspace_bytes bytes, 256-byte aligned.  Calls on one
  * cache may overlap on the GPU if each has its own workspace and nothing

@@ -13,6 +13,7 @@ import math
 import numpy as np
 
 from .attention import decode_head
+from .quant import code_value, dequantize_per_token, middle_blocks
 
 
 def chunk_head(q, K, V, policy: int, kept, N: int, S: int, W: int, W_loc: int, special_flags=None) -> np.ndarray:
@@ -20,6 +21,30 @@ def chunk_head(q, K, V, policy: int, kept, N: int, S: int, W: int, W_loc: int, s
     K, V [N + n, d]: its dense history, the chunk's tokens last.  [n, G, d]."""
     return np.stack([decode_head(q[i], K, V, policy, kept, N + i + 1, S, W, W_loc, special_flags)
                      for i in range(len(q))])
+
+
+def sealed_keys(codes, scales, fmt: str = "int8") -> np.ndarray:
+    """The keys of a sealed block [128, k] as chunk attention takes them: the block's
+    scales moved by a power of two so that the largest lies in [2^6, 2^7), each
+    rounded to f16, and their products with the codes rounded to f16."""
+    s = np.asarray(scales, np.float32)
+    e = max(int(s.max().view(np.uint32) >> 23) - 127 - 6, -126)
+    s16 = (s * np.float32(2.0 ** -e)).astype(np.float16).astype(np.float64)
+    return (code_value(codes, fmt) * s16).astype(np.float16).astype(np.float64) * 2.0 ** e
+
+
+def sealed_history(K, V, kept, policy: int, N: int, S: int, W: int, fmt: str = "int8"):
+    """``quant.quantized_history`` with the sealed keys as chunk attention takes
+    them."""
+    Kq, Vq = np.array(K[:N], dtype=np.float64), np.array(V[:N], dtype=np.float64)
+    if policy != 0:
+        return Kq, Vq
+    kept = np.asarray(kept, dtype=np.int64)
+    for j, (kc, ks, vc, vs) in enumerate(middle_blocks(K, V, kept, N, S, W, fmt)):
+        rows = np.arange(S + 128 * j, S + 128 * (j + 1))
+        Kq[np.ix_(rows, kept)] = sealed_keys(kc, ks, fmt)
+        Vq[rows] = dequantize_per_token(vc, vs, fmt)
+    return Kq, Vq
 
 
 def rope_frequencies(dim: int, base: float, scaling: str = "none", factor: float = 1.0, trained: int = 0,

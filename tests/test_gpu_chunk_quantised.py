@@ -1,0 +1,130 @@
+"""Chunk attention over INT8 / FP8 middles, as exactly as its roundings allow.
+
+The oracle takes sealed keys as the kernel does (scales and products to f16, as
+oracle.chunk.sealed_keys says) and everything else in fp64.  What remains of an
+output o = sum p v, with A = sum p |v|:
+
+  each value:  2^-8 |o| (its rounding to bf16) + 2^-8 A (p times a value's scale
+      rounded to bf16) + 2^-12 A (fp32 scores of up to 128 products, exponentials)
+
+  all values of a head together, root mean square relative to the outputs': a
+      rounding to bf16 is off by a uniform share of half a step, on average over
+      mantissas 2^-8 / sqrt(3) * sqrt(3 / (8 ln 2)) = 1.66e-3; once for o, once for
+      the weights, whose errors are independent and meet independent values:
+      sqrt(2) * 1.66e-3 = 2.35e-3, and a fifth more for heads of a few thousand
+      outputs.
+
+Against keys in fp64 instead, f16's 2^-11 of scale and product each add at most
+sqrt(2) * 2^-11 / sqrt(3) * 0.735 = 0.3e-3 times the size of a score, sqrt(sum q^2
+k^2 / 128): 0.06e-3 more for scores of about one."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from decode_attention_pruned_gb300 import binding as lkb
+from decode_attention_pruned_gb300 import synth as S
+from helpers import Case, f64
+from oracle import chunk as OC
+from oracle import quant as OQ
+from test_gpu_chunk import _chunk, _fill, _queries
+
+pytestmark = pytest.mark.gpu
+
+TINY = S.WORKLOADS[0]
+FORMATS = [lkb.KV_INT8, lkb.KV_FP8]
+FORMAT_IDS = ["int8", "fp8"]
+RMS = 1.2 * 2.35e-3
+
+
+def _expected(case, q, held, lens, history=OC.sealed_history):
+    """{(b, h): (o, bound)} fp64 [lens[b], G, 128]."""
+    k, v = case.history(0)
+    w, G, out = case.w, case.w.group, {}
+    for b in range(w.batch):
+        N, n = int(held[b]), int(lens[b])
+        for h in range(w.num_kv_heads):
+            pol = int(case.policies[0, h])
+            kept = np.nonzero(case.masks[0, h])[0] if pol == S.POLICY_FULL else np.arange(0)
+            K, V = f64(k[b, :N + n, h]), f64(v[b, :N + n, h])
+            if case.kv_format != lkb.KV_BF16:
+                K[:N], V[:N] = history(K[:N], V[:N], kept, pol, N, w.sink, w.local,
+                                       fmt=lkb.KV_FORMAT_NAMES[case.kv_format])
+            args = (pol, kept, N, w.sink, w.local, w.local_only_window, case.flags[b][:N + n])
+            Q = f64(q[b, :n, h * G:(h + 1) * G])
+            o, A = OC.chunk_head(Q, K, V, *args), OC.chunk_head(Q, K, np.abs(V), *args)
+            out[b, h] = o, 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -12) * A
+    return out
+
+
+def _rms(got, o):
+    return math.sqrt(((got - o) ** 2).sum() / max((o ** 2).sum(), 1e-300))
+
+
+def _attend(case, held, n, lens=None, q=None, **kw):
+    q = _queries(case, n) if q is None else q
+    k, v, ids = _chunk(case, 0, held, n)
+    full = [n] * case.w.batch if lens is None else lens
+    got = f64(case.cache.chunk_attn(0, q, k, v, lens=lens, ids=ids))
+    case.cache.check()
+    G = case.w.group
+    for (b, h), (o, tol) in _expected(case, q, held, full, **kw).items():
+        x = got[b, :full[b], h * G:(h + 1) * G]
+        bad = np.abs(x - o) > tol + 1e-30
+        assert not bad.any(), (b, h, int(bad.sum()), np.argwhere(bad)[:4].tolist())
+        if o.size >= 1024:
+            assert _rms(x, o) <= RMS, (b, h, _rms(x, o))
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("k", [32, 64, 96, 128])
+@pytest.mark.parametrize("n", [3, 60])
+def test_outputs_are_as_exact_as_their_roundings(cuda, fmt, k, n):
+    """Against the dequantised values themselves: keys are not what limits o."""
+    w = TINY.scaled(num_kv_heads=2, num_q_heads=8, batch=2, sink=4, local=64)
+    case = Case(w, total=1600, masks=S.masks_with_counts(w, (k, k)), kv_format=fmt)
+    held = [1500, 1111]
+    _fill(case, held)
+    q = _queries(case, n)
+    key, v, _ = _chunk(case, 0, held, n)
+    got = f64(case.cache.chunk_attn(0, q, key, v))
+    for (b, h), (o, _) in _expected(case, q, held, [n, n], history=OQ.quantized_history).items():
+        assert _rms(got[b, :, h * 4:h * 4 + 4], o) <= RMS, (b, h)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("n", [4, 50])
+def test_keys_and_queries_of_any_size(cuda, fmt, n):
+    """Keys far outside f16's range, met by queries that bring the scores back; rows
+    of q of very different sizes side by side; blocks of very different sizes one
+    after the other; a block of zeros."""
+    w = TINY.scaled(num_kv_heads=4, num_q_heads=16, batch=3, sink=4, local=64)
+    case = Case(w, total=900, masks=S.masks_with_counts(w, (32, 64, 96, 128)), kv_format=fmt)
+    held = [800, 517, 68 + 256]
+    k, v = case.history(0)
+    by = torch.tensor([2.0 ** 60, 2.0 ** -60, 2.0 ** 17], device="cuda")
+    k *= by[:, None, None, None].to(torch.bfloat16)
+    k[:, 196:324] *= 2.0 ** -9
+    k[:, 324:400, :, ::2] *= 2.0 ** 6
+    k[1, 68:196] = 0
+    _fill(case, held)
+    q = _queries(case, n)
+    q *= (1 / by)[:, None, None, None].to(torch.bfloat16)
+    q[:, 1] *= 2.0 ** -30                          # scores of about nothing
+    q[:, 2, ::3] *= 2.0 ** 3
+    q[:, 3, 5] = 0
+    _attend(case, held, n, q=q)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("held", [[67, 68], [69, 195], [196, 197], [323, 324], [325, 451], [452, 60]], ids=str)
+@pytest.mark.parametrize("n", [1, 2, 40, 130])
+def test_open_blocks_of_every_size(cuda, fmt, held, n):
+    """Middles that end on, before and behind a block's border, where rows that no
+    block has sealed, rows that leave the window and the chunk's own follow one
+    another in the same tiles."""
+    w = TINY.scaled(num_kv_heads=4, num_q_heads=8, batch=2, sink=4, local=64)
+    case = Case(w, total=600, masks=S.masks_with_counts(w, (32, 128, 96, 0)), kv_format=fmt)
+    _fill(case, held)
+    _attend(case, held, n)
