@@ -33,9 +33,15 @@ from test_gpu_chunk import _chunk, _fill, _queries
 pytestmark = pytest.mark.gpu
 
 TINY = S.WORKLOADS[0]
+LLAMA = S.WORKLOADS[1]
+FASTGEN = S.WORKLOADS[4]
 FORMATS = [lkb.KV_INT8, lkb.KV_FP8]
 FORMAT_IDS = ["int8", "fp8"]
 RMS = 1.2 * 2.35e-3
+
+
+def _bound(o, A):
+    return 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -12) * A
 
 
 def _expected(case, q, held, lens, history=OC.sealed_history):
@@ -54,7 +60,7 @@ def _expected(case, q, held, lens, history=OC.sealed_history):
             args = (pol, kept, N, w.sink, w.local, w.local_only_window, case.flags[b][:N + n])
             Q = f64(q[b, :n, h * G:(h + 1) * G])
             o, A = OC.chunk_head(Q, K, V, *args), OC.chunk_head(Q, K, np.abs(V), *args)
-            out[b, h] = o, 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -12) * A
+            out[b, h] = o, _bound(o, A)
     return out
 
 
@@ -128,3 +134,61 @@ def test_open_blocks_of_every_size(cuda, fmt, held, n):
     case = Case(w, total=600, masks=S.masks_with_counts(w, (32, 128, 96, 0)), kv_format=fmt)
     _fill(case, held)
     _attend(case, held, n)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("paged", [False, True], ids=["contiguous", "paged"])
+def test_middles_of_every_width(cuda, fmt, paged):
+    w = LLAMA.scaled(num_kv_heads=5, num_q_heads=20, batch=2, sink=16, local=64)
+    case = Case(w, total=900, masks=S.masks_with_counts(w, (0, 32, 64, 96, 128)), kv_format=fmt,
+                middle_tokens=1800 if paged else None)
+    held = [850, 208]                 # 6 blocks and a tail; exactly one block
+    _fill(case, held)
+    _attend(case, held, 45)
+    _attend(case, held, 3, lens=[3, 1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("n", [3, 60])
+def test_policies(cuda, fmt, n):
+    w = FASTGEN.scaled(num_layers=1, batch=2, context=700, policy_counts=(2, 2, 4))
+    case = Case(w, total=800, kv_format=fmt)
+    held = [700, 301]
+    _fill(case, held)
+    _attend(case, held, n, lens=[n, n - 2])
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("n", [1, 16, 17, 100])
+def test_wide_tiles_then_sealed_ones(cuda, fmt, n):
+    w = TINY.scaled(num_kv_heads=6, num_q_heads=48, batch=3, sink=130, local=400)
+    case = Case(w, total=2200, masks=S.masks_with_counts(w, (96, 96, 128, 32, 0, 96)), kv_format=fmt)
+    held = [2100, 700, 1313]
+    _fill(case, held)
+    _attend(case, held, n)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_one_item_over_every_block(cuda, fmt, n):
+    w = TINY.scaled(num_kv_heads=1, num_q_heads=8, batch=1, sink=4, local=64)
+    case = Case(w, total=60050, masks=S.masks_with_counts(w, (64,)), gen_device="cuda", kv_format=fmt)
+    _fill(case, [60000])
+    _attend(case, [60000], n)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+def test_stale_rows_behind_an_open_block(cuda, fmt):
+    """A slot's last request left NaN in the rows behind the next one's."""
+    w = TINY.scaled(num_kv_heads=2, num_q_heads=8, batch=2, sink=4, local=40)
+    case = Case(w, total=600, masks=S.masks_with_counts(w, (32, 96)), kv_format=fmt)
+    bad = torch.full((600, 2, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    for b in range(2):
+        case.cache.prefill_sequence(0, b, bad, bad)
+        case.cache.release(b)
+    held = [233, 75]
+    k, v = case.history(0)
+    for b in range(2):
+        case.cache.prefill_sequence(0, b, k[b, :held[b]].contiguous(), v[b, :held[b]].contiguous())
+    _attend(case, held, 7)
+    _attend(case, held, 50)
