@@ -1362,9 +1362,9 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kQuant ? score_scale : kScaleLog2);
           // (nobody's rows score whatever lies behind q: they move no one's maximum)
           if (!kDual && !mine) top = -INFINITY;
-          // The maximum moves only when a score exceeds it by 2^8: below that p
-          // stays exact in fp32 and bf16 alike.  (Each row's by itself: what a row
-          // comes to does not depend on the others of its warp.)
+          // The maximum moves only when a score exceeds it by 8, p by 2^8: fp32 sums and
+          // bf16 weights lose no more of it than of one below 1.  (Each row's by itself:
+          // what a row comes to does not depend on the others of its warp.)
           if (__any_sync(0xffffffffu, top > m + 8.f)) {
             const float mn = top > m + 8.f ? top : m;
             const float f = m == -INFINITY ? 0.f : ex2(m - mn);
@@ -1387,6 +1387,12 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               }
             }
           }
+          // P goes to the tensor core in bf16, V's type, which rounds every weight by up
+          // to 2^-8 of itself, as o is rounded once more at the end; l sums the unrounded
+          // ones.  Against fp64 o is off by 2.3e-3 instead of the 1.66e-3 of its own
+          // rounding.  P as the sum of two bf16 numbers, with a second product for the
+          // lower one, gives 1.66e-3, and takes 120 us instead of 100 for 64 sequences of
+          // 4096 tokens (4 queries each), 1117 instead of 871 for 1000 queries over 131072.
           const float off = m == -INFINITY ? 0.f : -m;
           const float sc = kQuant ? score_scale : kScaleLog2;
           const uint64_t scale2 = pair(sc, sc), off2 = pair(off, off);

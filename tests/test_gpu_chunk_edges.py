@@ -295,3 +295,23 @@ def test_outputs_of_another_stream_are_its_own(cuda):
         assert all(end <= a or b <= at for a, b in spans)
     s.synchronize()
     assert torch.equal(outs[0], ref) and torch.equal(outs[1], q)
+
+
+@pytest.mark.parametrize("k", [0, 32, 128])
+@pytest.mark.parametrize("n", [3, 5, 60, 200])
+def test_outputs_are_as_exact_as_two_roundings(cuda, k, n):
+    """o and the weights are each rounded to bf16 once, off by a uniform share of half
+    a step, 1.66e-3 of the value in the root mean square, and independently of one
+    another: sqrt(2) times that over a head's outputs, and a fifth more for the few
+    thousand of them here."""
+    w = TINY.scaled(num_kv_heads=2, num_q_heads=8, batch=2, sink=4, local=64)
+    case = Case(w, total=1700, masks=S.masks_with_counts(w, (k, k)))
+    held = [1500, 1111]
+    _fill(case, held)
+    q, (key, v, _) = _queries(case, n), _chunk(case, 0, held, n)
+    got = case.cache.chunk_attn(0, q, key, v).double().cpu().numpy()
+    ref, _ = _expected(case, 0, q, held, [n, n])
+    for b in range(2):
+        for h in (slice(0, 4), slice(4, 8)):
+            x, o = got[b, :, h], ref[b, :, h]
+            assert math.sqrt(((x - o) ** 2).sum() / (o ** 2).sum()) <= 1.2 * 2.35e-3, (b, h)
