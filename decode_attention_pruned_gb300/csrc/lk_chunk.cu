@@ -61,8 +61,11 @@ constexpr int kTile = 128;                 // keys per tile, rows per query tile
 constexpr int kFar = 1 << 29;              // a window that nothing leaves
 constexpr float kScaleLog2 = 0.12751743f;  // log2(e) / sqrt(128)
 // Line a CTA takes at least: about three tiles (one sequence of 32768 tokens: 29
-// us, with three times as much 31).  More than any tile and more than an item's
-// own share weigh, so that no two CTAs start at the same tile of an item.
+// us, with three times as much 31).  More than any tile weighs (536, a sealed one on
+// 128 channels before one query tile), so that no two CTAs start at the same tile
+// inside an item, where their partials would share a place.  Two may start at an
+// item's first tile, if one's offset falls into the last tile before it and the
+// next one's into the item's own share: the first of them then has nothing to do.
 constexpr uint64_t kMinCtaCost = 768;
 
 enum TileType : int { kTileA = 0, kTileC = 1, kTileM = 2, kTileF = 3 };

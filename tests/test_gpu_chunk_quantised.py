@@ -192,3 +192,25 @@ def test_stale_rows_behind_an_open_block(cuda, fmt):
         case.cache.prefill_sequence(0, b, k[b, :held[b]].contiguous(), v[b, :held[b]].contiguous())
     _attend(case, held, 7)
     _attend(case, held, 50)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("held, n, counts", [([460, 460], 150, (128, 96)), ([200, 330], 40, (128, 96)),
+                                             ([330, 200], 150, (96, 64, 128)), ([460] * 8, 70, (128, 96)),
+                                             ([460] * 8, 150, (128, 96))], ids=str)
+def test_blocks_with_nothing_to_do(cuda, fmt, held, n, counts):
+    """Little work a block: some blocks start where the next one does, at an item's
+    first tile, and have nothing to do.  Inside an item no two start at one tile."""
+    H = len(counts)
+    w = TINY.scaled(num_kv_heads=H, num_q_heads=4 * H, batch=len(held), sink=4, local=64)
+    case = Case(w, total=max(held) + n, masks=S.masks_with_counts(w, counts), kv_format=fmt)
+    _fill(case, held)
+    _attend(case, held, n)
+    torch.cuda.synchronize()
+    ctas = min(torch.cuda.get_device_properties(0).multi_processor_count, 160)
+    starts = case.cache.chunk_workspace[:8 * (ctas + 2)].view(torch.int32).view(-1, 2).tolist()
+    blocks = starts[ctas + 1][0]
+    starts = [tuple(x) for x in starts[:blocks + 1]]
+    assert 1 < blocks <= ctas and starts[0] == (0, 0) and starts == sorted(starts)
+    same = [x for x, y in zip(starts, starts[1:]) if x == y]
+    assert same and all(tile == 0 for _, tile in same)
