@@ -1004,8 +1004,15 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           int32_t page = page_at(j0);
           for (int j = j0; ok && j < s.t1; j += kStep) {
             const int32_t after = page_at(j + kStep);
+            if (kQuant || !kDual) {
+              // (one copy of these instructions: 98 us instead of 100 for 64 sequences of
+              // 4096 tokens, 123 instead of 130 when their middles were sealed)
 #pragma unroll 1
-            for (int isv = 0; ok && isv < 2; ++isv) ok = load(j, isv != 0, page);
+              for (int isv = 0; ok && isv < 2; ++isv) ok = load(j, isv != 0, page);
+            } else {
+              // (an item's first tiles sooner: 229 us instead of 243 for two prompts of 4096)
+              ok = load(j, false, page) && load(j, true, page);
+            }
             page = after;
           }
         }
