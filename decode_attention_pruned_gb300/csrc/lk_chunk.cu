@@ -613,7 +613,7 @@ __device__ __forceinline__ void visible(const ChunkArgs& a, const ChunkWork& w, 
     if (live > 0) {
       const int z = s + (it.N - 1 - s) % wr + 1 - t.r0;      // just past the newest
       add_range(m, max(z - live, s - t.r0), z);
-      add_range(m, z + wr - live, min(s + wr - t.r0, t.rows));
+      add_range(m, z - live + wr, min(s + wr - t.r0, t.rows));     // (a window may be as long as an int32 goes)
     }
     // a full ring's last rows wrap; rows past the region hold nothing
     uint32_t v[4] = {0, 0, 0, 0};

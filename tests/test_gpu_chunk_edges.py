@@ -18,6 +18,7 @@ from test_gpu_chunk import _attend, _check, _chunk, _expected, _fill, _queries
 pytestmark = pytest.mark.gpu
 
 TINY = S.WORKLOADS[0]
+FASTGEN = S.WORKLOADS[4]
 FORMATS = [lkb.KV_BF16, lkb.KV_INT8, lkb.KV_FP8]
 FORMAT_IDS = ["bf16", "int8", "fp8"]
 
@@ -315,3 +316,20 @@ def test_outputs_are_as_exact_as_two_roundings(cuda, k, n):
         for h in (slice(0, 4), slice(4, 8)):
             x, o = got[b, :, h], ref[b, :, h]
             assert math.sqrt(((x - o) ** 2).sum() / (o ** 2).sum()) <= 1.2 * 2.35e-3, (b, h)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("n", [1, 40, 150])
+def test_windows_that_nothing_leaves(cuda, fmt, n):
+    """Windows of 2^31 - 1 tokens: every token is near, and no sum passes an int32."""
+    w = FASTGEN.scaled(num_layers=1, batch=2, num_q_heads=8, num_kv_heads=4, policy_counts=(2, 1, 1), sink=0,
+                       local=2 ** 31 - 1, local_only_window=2 ** 31 - 1, context=400)
+    masks = S.masks_with_counts(w, (32, 0, 96, 128))
+    case = Case(w, total=600, masks=masks, kv_format=fmt)
+    held = [400, 133]
+    _fill(case, held)
+    _attend(case, held, n)
+    k, v, ids = _chunk(case, 0, held, n)
+    case.cache.append_chunk(0, k, v, ids=ids)
+    case.check_layout(0, np.array(held) + n)
+    case.cache.check()
