@@ -317,8 +317,8 @@ ChunkLayout chunk_layout(const lk_plan_s& p, int B, int n_max, int layer, int ct
   w.tile_tokens = 128 / G;
   // One query tile a CTA while a chunk fits it (its two softmax groups then take
   // alternate key tiles), else two (they share every key tile).  Two for 64
-  // sequences of 4 tokens: 157 us instead of 101; one at a time for two prompts of
-  // 4096 tokens: 286 us instead of 226, for chunks of 64: 110 instead of 82.
+  // sequences of 4 tokens: 145 us instead of 98; one at a time for two prompts of
+  // 4096 tokens: 294 us instead of 229, for chunks of 64: 109 instead of 82.
   w.dual = n_max > w.tile_tokens;
   w.item_tokens = w.dual ? 2 * w.tile_tokens : w.tile_tokens;
   w.items_q = (int)(((int64_t)n_max + w.item_tokens - 1) / w.item_tokens);
@@ -1370,7 +1370,7 @@ lk_status chunk_attn_prepare(lk_cache cache, void* o, void* workspace, size_t ws
   // unit = 12 clocks): the loads set the pace.  Two (16 clocks): the softmax does,
   // and an item starts and ends slowly.  Sealed blocks (14 clocks, one tile): the
   // warps that expand them do.  (In proportion to bytes two prompts of 4096 tokens
-  // take 249 us, with these 226; FP8 middles 113 and 107.)
+  // take 251 us, with these 229; FP8 middles 143 and 114.)
   const bool sealed = kv_quantized(cv.kv_format);
   w.cost_item = w.dual ? 448 : sealed ? 112 : 216;
   w.cost_wide = w.dual ? 236 : 256;

@@ -35,13 +35,13 @@
 //
 // What bounds it.  Chunks that fill two query tiles: the softmax of 128 x 64
 // scores (1300 clocks a group, of which the tensor cores need 800); 1000 queries
-// of 28 heads over 131072 tokens on 32 kept channels take 853 us, 55% of the
+// of 28 heads over 131072 tokens on 32 kept channels take 870 us, 54% of the
 // measured bf16 matrix rate.  Chunks of a few tokens: the cache's bytes, through
 // a ring that holds two to five tiles per group; 64 sequences of 4096 tokens
-// take 101 us, 1.45 times what a plain copy's rate gives their bytes.  Sealed
+// take 98 us, 1.4 times what a plain copy's rate gives their bytes.  Sealed
 // blocks: the four warps that expand them, which share instruction caches with
-// every other role; 16 sequences of 8192 tokens take 107 us, 3.7 times their
-// bytes.  One sequence: three dependent launches, 29 us over 32768 tokens.
+// every other role; 16 sequences of 8192 tokens take 114 us, 4.0 times their
+// bytes.  One sequence: three dependent launches, 28 us over 32768 tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -60,8 +60,8 @@ namespace {
 constexpr int kTile = 128;                 // keys per tile, rows per query tile
 constexpr int kFar = 1 << 29;              // a window that nothing leaves
 constexpr float kScaleLog2 = 0.12751743f;  // log2(e) / sqrt(128)
-// Line a CTA takes at least: about three tiles (one sequence of 32768 tokens: 29
-// us, with three times as much 31).  More than any tile weighs (536, a sealed one on
+// Line a CTA takes at least: about three tiles (one sequence of 32768 tokens: 28
+// us, with three times as much 29).  More than any tile weighs (536, a sealed one on
 // 128 channels before one query tile), so that no two CTAs start at the same tile
 // inside an item, where their partials would share a place.  Two may start at an
 // item's first tile, if one's offset falls into the last tile before it and the
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         constexpr bool kV = decltype(values)::value;
         // A thread keeps to one 16-channel group (of 6 groups not all threads have
         // one); its rows are r0, r0 + kRows, ..., two of them on their way at once.
-        // (Four take 125 us instead of 108 on 16 sequences of 8192 tokens: the roles
+        // (Four take 120 us instead of 114 on 16 sequences of 8192 tokens: the roles
         // of an SM share its instruction caches, and longer code waits for them.)
         constexpr int kRows = kMade / kGroups, kOnce = 2;
         const int c = mt % kGroups, r0 = mt < kRows * kGroups ? mt / kGroups : kTile;

@@ -18,9 +18,14 @@
 // from wherever their rows still are (tail, ring or input); SPECIAL rows are
 // written.
 //
-// All of it is data movement, and short: 512 tokens of 8 heads take about 5 us,
-// launch and dependency more than bytes (8 MB).  A warp per row, 8 bytes a lane,
-// keeps every access a whole row, and the one launch advances the lengths too.
+// bf16: data movement, and short.  512 tokens of 8 heads take 8 us with the call
+// (paged 9), launch and dependency more than bytes (8 MB).  A warp per row, 8
+// bytes a lane, keeps every access a whole row, and the one launch advances the
+// lengths too.
+// INT8 / FP8: the sealing.  One warp seals a whole block, as the single append
+// does, with gathers of two bytes, so a chunk that completes a block of each head
+// takes 180 us and more (512 tokens of 8 heads, 4 blocks each: 305); one that
+// completes none, as most verified drafts do, 10 to 16.
 #include <cuda_runtime.h>
 
 #include "lk_append.cuh"

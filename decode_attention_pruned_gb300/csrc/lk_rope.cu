@@ -13,7 +13,7 @@
 // Its top 32 bits, as a signed number, go through sincospif.
 //
 // The bytes bound it: every element is read and written once (8192 tokens of
-// 32 heads, 134 MB: 28.8 us, a plain copy of them 23.5).  A block takes
+// 32 heads, 134 MB: 26.1 us, a plain copy of them 23.9).  A block takes
 // a few tokens, computes each (token, pair)'s cosine and sine once into
 // shared memory, and turns every head of q and k with them, 16 channels to a
 // thread as two 16-byte loads and stores.
@@ -44,8 +44,8 @@ __device__ __forceinline__ uint32_t turn1(uint32_t x, float2 t) {
 
 // A block of 256 threads turns kTokens tokens.  Its first loads of q and k are
 // on their way before the angles are computed.  (Loading four heads ahead
-// instead of one takes registers, and with them blocks: 28.8 -> 31.4 us for
-// 8192 tokens of 32 heads.)
+// instead of one takes registers, and with them blocks: 9% more time for 8192
+// tokens of 32 heads.)
 template <int kTokens>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float4 turn[kTokens][kHeadDim / 4];           // (cosine, sine) of two pairs each
@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 
 cudaError_t launch_rope(const RopeArgs& args, int num_sms, cudaStream_t stream) {
   // Four tokens a block once that leaves every SM four blocks (8192 tokens of 32
-  // heads: 28.8 us, one token a block 30.9), else one.
+  // heads: 26.1 us, one token a block 28.6), else one (2053 tokens of 40 heads: 8.0
+  // us on the GPU, four tokens a block 10.0).
   if (args.tokens >= 16 * (int64_t)num_sms)
     return launch_after(rope_kernel<4>, dim3((unsigned)((args.tokens + 3) / 4)), kRopeThreads, 0, stream, args);
   return launch_after(rope_kernel<1>, dim3((unsigned)args.tokens), kRopeThreads, 0, stream, args);

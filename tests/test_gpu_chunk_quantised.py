@@ -50,6 +50,8 @@ def _expected(case, q, held, lens, history=OC.sealed_history):
     w, G, out = case.w, case.w.group, {}
     for b in range(w.batch):
         N, n = int(held[b]), int(lens[b])
+        if n == 0:
+            continue
         for h in range(w.num_kv_heads):
             pol = int(case.policies[0, h])
             kept = np.nonzero(case.masks[0, h])[0] if pol == S.POLICY_FULL else np.arange(0)
