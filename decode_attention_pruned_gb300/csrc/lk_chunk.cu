@@ -491,7 +491,8 @@ struct Smem {
   // what scores are scaled back by: a factor per sealed tile in flight, and per row of
   // this segment's q and of the next one's (one group may be a segment ahead)
   static constexpr int kTileBack = kKScale + (kQuant ? kRings * kJobs * kTile * 4 : 0);
-  static constexpr int kRowBack = kTileBack + (kQuant ? kRings * kSlots * 4 : 0);
+  static constexpr int kValueLog = kTileBack + (kQuant ? kRings * kSlots * 4 : 0);      // of the values' scales
+  static constexpr int kRowBack = kValueLog + (kQuant ? kRings * 4 * 4 : 0);
   static constexpr int kQ = (kRowBack + (kQuant ? 2 * kQTiles * kTile * 4 : 0) + 1023) / 1024 * 1024;
   static constexpr int kJobBytes = 32;
   static constexpr int kMakers = kDual ? 4 : 2;          // warps that make a ring's tiles out of sealed blocks
@@ -628,8 +629,8 @@ __device__ __forceinline__ float power2(int e) { return __int_as_float((min(max(
 
 // Scores of sealed blocks.  A key's channel is code times scale, 8 bits times 24.
 // Rounded to bf16 it would be off by up to 2^-8 of itself, and the attention with
-// it (relative error against fp64 2.7 to 3.3e-3 instead of 2.3 to 2.4e-3, o's own
-// rounding being 1.66e-3), so these keys and the q they meet are f16: q exactly
+// it (by the keys alone its relative error against fp64 rises from 2.3e-3 to 2.7 and
+// 3.3e-3, o's own rounding being 1.66e-3), so these keys and the q they meet are f16: q exactly
 // (8 bits), the scale and the product to 11 bits each.  What f16 lacks in range
 // goes into exponents: a block's scales are moved so that the largest lies in
 // [2^6, 2^7) (448 times that is below f16's largest), a row of q so that its
@@ -637,6 +638,14 @@ __device__ __forceinline__ float power2(int e) { return __int_as_float((min(max(
 // the block back.  Only channels whose scale is 2^-20 of the block's largest, or
 // whose q is 2^-31 of the row's largest, keep fewer bits.
 constexpr int kScaleExp = 6, kRowTop = 14;
+// Outputs of sealed blocks.  Values are their codes, exact in f16, and the weights
+// that they meet are p times the value's scale in f16, 11 bits of it (in bf16, 8
+// bits, o would be off by 2.3e-3 instead of 1.75e-3, at the same speed).  The range is kept by the row's reference m: p = 2^(s - m), and over
+// sealed blocks m is max s + log2 of the block's largest scale - 6, so that the
+// largest weight lies about 2^6, and below 2^15 when m lags by 8 (the sums l and the
+// outputs before are in units of 2^m too, and follow).  Only weights 2^-20 of the
+// largest keep fewer bits.
+constexpr int kWeightExp = 6;
 
 // The keys or the values of a sealed block, to be turned into a tile.  (Not
 // both at once: the ring may have room for the values only when the tile
@@ -754,9 +763,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 
   if (kQuant && warp >= 12) {
     // ----------------------------------------------------------- the makers
-    // Turn sealed blocks into tiles: keys as code times scale, rounded once to
-    // f16; values as their codes, which bf16 holds exactly (the weights take their
-    // scales).  The codes of a 128-channel row lie where the row's second
+    // Turn sealed blocks into f16 tiles: keys as code times scale, values as their
+    // codes (the weights take their scales).  The codes of a 128-channel row lie where the row's second
     // half will: eight lanes read the row, then write it.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     constexpr int kMade = 32 * L::kMakers;                // threads per ring
@@ -774,24 +782,31 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       const Job job = *reinterpret_cast<const Job*>(sm + L::kJob + jn * L::kJobBytes);
       if (job.width == 0) break;
       uint8_t* to = sm + job.at;
+      // the block's largest scale (they are not negative: they order as their bits do)
+      uint32_t top = 0;
+      for (int x = lane; x < job.width; x += 32)
+        top = max(top, *reinterpret_cast<const uint32_t*>(sm + job.scales + 4 * x));
+      int top_exp = (int)(__reduce_max_sync(0xffffffffu, top) >> 23) - 127;
       float to_range = 1.f;
       if (job.values == 0) {
-        // (scales are not negative: they order as their bits do)
-        uint32_t top = 0;
-        for (int x = lane; x < job.width; x += 32)
-          top = max(top, *reinterpret_cast<const uint32_t*>(sm + job.scales + 4 * x));
-        const int e = max((int)(__reduce_max_sync(0xffffffffu, top) >> 23) - 127 - kScaleExp, -126);
-        to_range = power2(-e);
-        if (mt == 0) *reinterpret_cast<float*>(sm + L::kTileBack + 4 * (ri * L::kSlots + job.slot)) = power2(e);
+        top_exp = max(top_exp - kScaleExp, -126);
+        to_range = power2(-top_exp);
+        if (mt == 0) *reinterpret_cast<float*>(sm + L::kTileBack + 4 * (ri * L::kSlots + job.slot)) = power2(top_exp);
+      } else if (mt == 0) {
+        // (values of next to nothing need not bring the outputs before them to fp32's end)
+        *reinterpret_cast<float*>(sm + L::kValueLog + (job.scales - L::kVScale) / kTile) =
+            (float)(max(top_exp, -60) - kWeightExp);
       }
       auto convert = [&](auto channels, auto values) {
         constexpr int kWidth = decltype(channels)::value, kGroups = kWidth / 16;
         constexpr bool kV = decltype(values)::value;
         // A thread keeps to one 16-channel group (of 6 groups not all threads have
-        // one); its rows are r0, r0 + kRows, ..., two of them on their way at once.
-        // (Four take 120 us instead of 114 on 16 sequences of 8192 tokens: the roles
-        // of an SM share its instruction caches, and longer code waits for them.)
-        constexpr int kRows = kMade / kGroups, kOnce = 2;
+        // one); its rows are r0, r0 + kRows, ..., two of keys or four of values on their
+        // way at once.  (Two of values: 117 us instead of 114 on 16 sequences of 8192
+        // tokens.  The roles of an SM share its instruction caches, and code that is
+        // longer than it pays for waits for them.)
+        constexpr int kRows = kMade / kGroups, kOnce = kV ? 4 : 2;
+        static_assert(kGroups == 6 || kTile % (kOnce * kRows) == 0, "whole steps of rows");
         const int c = mt % kGroups, r0 = mt < kRows * kGroups ? mt / kGroups : kTile;
         const uint4* codes = reinterpret_cast<const uint4*>(to + kTile * kWidth * (kWidth == kHeadDim ? 1 : 2));
         uint32_t scale[kV ? 1 : 8];
@@ -821,13 +836,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             for (int x = 0; x < 4; ++x) {
               uint32_t e, o;
               codes_f16<kFmt, kV>(in[x], e, o);
-              if (kV) {
-                lo[x] = pack_bf16x2(f16_lo(e), f16_hi(e));
-                hi[x] = pack_bf16x2(f16_lo(o), f16_hi(o));
-              } else {
-                lo[x] = mul_f16x2(e, scale[x]);
-                hi[x] = mul_f16x2(o, scale[4 + x]);
-              }
+              lo[x] = kV ? e : mul_f16x2(e, scale[kV ? 0 : x]);
+              hi[x] = kV ? o : mul_f16x2(o, scale[kV ? 0 : 4 + x]);
             }
             if (kGroups != 6 || r < kTile) {
               *reinterpret_cast<uint4*>(to + kept_byte(kWidth, r, 2 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -938,7 +948,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             offs[slot] = at;
             // what the other threads have to know of the tile
             info[slot] = (ring_at + at) >> 4 | (uint32_t)t.rows << 16 |
-                         (seal && !isv ? 3u + (uint32_t)it.k / 32 : wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
+                         (seal ? 3u + (isv ? 4u : (uint32_t)it.k / 32) : wide ? 3u : (uint32_t)it.k / 32 - 1) << 24;
             const uint32_t dst = ring_at + at, bar = full + 8 * slot;
             ++put;
             by_job = (by_job & ~(1u << slot)) | (seal ? 1u << slot : 0u);
@@ -1053,7 +1063,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       const int st = warp - 1;
       if (elect_one()) {
         constexpr uint32_t kDescS = mma_desc(128, kHalf, false), kDescO = mma_desc(128, kHeadDim, true);
-        constexpr uint32_t kDescS16 = mma_desc(128, kHalf, false, true);
+        constexpr uint32_t kDescS16 = mma_desc(128, kHalf, false, true), kDescO16 = mma_desc(128, kHeadDim, true, true);
         constexpr uint32_t kWideHi = desc_hi(1024, kSwizzle128), kThinHi = desc_hi(512, kSwizzle64);
         const uint32_t full = base + L::kFull + (kDual ? 0 : st * 8 * L::kSlots);
         const uint32_t empty = base + L::kEmpty + (kDual ? 0 : st * 8 * L::kSlots);
@@ -1140,14 +1150,15 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             const uint32_t p = s_at + kWhich * kHalf;
             const uint32_t v = (desc_lo(kWideBytes / 2) | (what & 0x3fff)) + kWhich * kHalf * 8;
             const int left = (int)(what >> 16 & 0xff) - kWhich * kHalf;
+            const uint32_t desc = kQuant && what >> 24 > 3 ? kDescO16 : kDescO;
             if (left >= kHalf) {
 #pragma unroll
               for (int y = 0; y < kHalf / 16; ++y)
-                mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, kDescO, accumulate || y > 0);
+                mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, desc, accumulate || y > 0);
             } else {
 #pragma unroll 1
               for (int y = 0; y < (left + 15) / 16; ++y)
-                mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, kDescO, accumulate || y > 0);
+                mma_ts<kWideHi>(o_at, p + y * 8, v + y * 128, desc, accumulate || y > 0);
             }
             mma_commit(o_full);
           };
@@ -1287,6 +1298,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       const int m0 = first_m<kQuant>(it), m1 = m0 + it.mid / kTile, f0 = first_f<kQuant>(it);
       bool scaled = false;                // this row's factor is known (the same for a whole warp)
       float back = 1.f;
+      bool moved = false;                 // m has been moved to what sealed blocks need
       const int i_first = it.i0 + (kDual ? st * tq : 0), i_last = min(i_first + tq, it.i0 + it.ntok) - 1;
       const int f1 = f0 + min(kQuant ? it.rows_f : kFar, max(0, it.N + i_first - cv.W + 1 - it.far0)) / kTile;
       for (int j = s.t0 + (kDual ? 0 : st); ok && j < s.t1; j += kDual ? 1 : 2) {
@@ -1324,13 +1336,15 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         // a sealed block's values are codes: their scales, once they are there, and the
         // scores' factor (made before the values, by the same warps)
         const float* vscale = nullptr;
-        float score_scale = kScaleLog2;
+        float score_scale = kScaleLog2, value_log = 0.f;
         if (kQuant && j >= m0) {
           const uint32_t e = entries + 2 * ((j - s.t0) / (kDual ? 1 : 2)) + 1;
           const uint32_t slot = e % L::kSlots + (kDual ? 0 : st * L::kSlots);
           ok = wait.warp(base + L::kFull + 8 * slot, (e / L::kSlots) & 1);
           if (!ok) break;
-          vscale = reinterpret_cast<const float*>(sm + L::kVScale) + ((kDual ? 0 : 4 * st) + (sealed++ & 3)) * kTile;
+          const int v_at = (kDual ? 0 : 4 * st) + (int)(sealed++ & 3);
+          vscale = reinterpret_cast<const float*>(sm + L::kVScale) + v_at * kTile;
+          value_log = *reinterpret_cast<const volatile float*>(sm + L::kValueLog + 4 * v_at);
           if (!scaled) {
             ok = wait.warp(base + L::kQKFull + (kDual ? 8 * st : 0), (gathered - 1) & 1);
             if (!ok) break;
@@ -1342,7 +1356,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          const uint32_t at = my_s + half * kHalf;
+          const uint32_t s_half = my_s + half * kHalf;
           ok = wait.warp(base + L::kSFull + 16 * st + 8 * half, (hs >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
@@ -1352,8 +1366,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             break;
           }
           uint32_t x[kHalf];
-          tmem_ld32(at, x);
-          tmem_ld32(at + 32, x + 32);
+          tmem_ld32(s_half, x);
+          tmem_ld32(s_half + 32, x + 32);
           tmem_loaded<kHalf>(x);
           if (!all) {
             const uint32_t v0 = half == 0 ? vis[0] : vis[2], v1 = half == 0 ? vis[1] : vis[3];
@@ -1375,9 +1389,14 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           // The maximum moves only when a score exceeds it by 8, p by 2^8: fp32 sums and
           // bf16 weights lose no more of it than of one below 1.  (Each row's by itself:
           // what a row comes to does not depend on the others of its warp.)
-          if (__any_sync(0xffffffffu, top > m + 8.f)) {
-            const float mn = top > m + 8.f ? top : m;
+          // Over sealed blocks the scores count with their values' scale, and the first
+          // one moves m to what they need (see kWeightExp).
+          const bool move = kQuant && vscale != nullptr && !moved;
+          if (kQuant) top += value_log;
+          if (__any_sync(0xffffffffu, top > m + 8.f) || move) {
+            const float at = move ? m + value_log : m, mn = top > (move ? at : m + 8.f) ? top : at;
             const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+            if (kQuant) moved = moved || move;
             m = mn;
             l *= f;
             if (begun) {
@@ -1397,12 +1416,13 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               }
             }
           }
-          // P goes to the tensor core in bf16, V's type, which rounds every weight by up
+          // P goes to the tensor core in V's type, bf16, which rounds every weight by up
           // to 2^-8 of itself, as o is rounded once more at the end; l sums the unrounded
           // ones.  Against fp64 o is off by 2.3e-3 instead of the 1.66e-3 of its own
           // rounding.  P as the sum of two bf16 numbers, with a second product for the
           // lower one, gives 1.66e-3, and takes 120 us instead of 100 for 64 sequences of
           // 4096 tokens (4 queries each), 1117 instead of 871 for 1000 queries over 131072.
+          // (Sealed blocks' weights are f16: see kWeightExp.)
           const float off = m == -INFINITY ? 0.f : -m;
           const float sc = kQuant ? score_scale : kScaleLog2;
           const uint64_t scale2 = pair(sc, sc), off2 = pair(off, off);
@@ -1427,8 +1447,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               auto times = [&](int c, uint64_t y) {
                 float p0, p1;
                 unpair(mul2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), y), p0, p1);
-                x[c] = __float_as_uint(p0);
-                x[c + 1] = __float_as_uint(p1);
+                x[c >> 1] = pack_f16x2(p0, p1);
               };
 #pragma unroll
               for (int c = 0; c < kHalf; c += 4) {
@@ -1436,12 +1455,13 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
                 times(c, y.x);
                 times(c + 2, y.y);
               }
-            }
+            } else {
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 2)
-              x[c >> 1] = pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+              for (int c = 0; c < kHalf; c += 2)
+                x[c >> 1] = pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+            }
           }
-          tmem_st32(at, x);
+          tmem_st32(s_half, x);
           float l0, l1;
           unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
           l += l0 + l1;

@@ -427,8 +427,9 @@ lk_status lk_chunk_workspace_bytes(lk_plan plan, int32_t batch, int32_t n_max, s
  * local_only_window tokens; SPECIAL heads the special ones that they have rows
  * for.  One softmax runs over all of it; a query that sees nothing gives 0.
  * Scores and sums are fp32; the weights that multiply the values are rounded to
- * bf16, and so is o: its relative error is 2.3e-3 where its own rounding alone
- * would give 1.7e-3 (lk_decode_attn and lk_step hold both to more bits).
+ * bf16 (over sealed blocks, with their values' scales, to 11 bits), and o to bf16:
+ * its relative error is 2.3e-3 (1.75e-3 where sealed blocks weigh most), 1.7e-3 of
+ * which is its own rounding.  (lk_decode_attn and lk_step hold both to more bits.)
  * Middle tokens are read as the cache holds them when the call runs: sealed
  * INT8 / FP8 blocks as their dequantised values (a key's scale and its product
  * with the code rounded to 11 bits), everything else, the chunk's own tokens

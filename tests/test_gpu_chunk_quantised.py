@@ -4,8 +4,13 @@ The oracle takes sealed keys as the kernel does (scales and products to f16, as
 oracle.chunk.sealed_keys says) and everything else in fp64.  What remains of an
 output o = sum p v, with A = sum p |v|:
 
-  each value:  2^-8 |o| (its rounding to bf16) + 2^-8 A (p times a value's scale
-      rounded to bf16) + 2^-12 A (fp32 scores of up to 128 products, exponentials)
+  each value:  2^-8 |o| (its rounding to bf16) + 2^-8 A (p rounded to bf16; over
+      sealed blocks p times the value's scale to f16, 2^-11) + 2^-12 A (fp32 scores
+      of up to 128 products, exponentials)
+      and, for weights so small that f16 holds them in steps of 2^-24: a row's
+      weights are p = 2^(s - m) with m <= max s + log2(c) - 6, c the largest scale of
+      a value, so l = sum p >= 2^6 / c; half a step, 2^-25, times a code of at most
+      max |v| / c, is 2^-31 max |v| of l for each of the N tokens held
 
   all values of a head together, root mean square relative to the outputs': a
       rounding to bf16 is off by a uniform share of half a step, on average over
@@ -62,7 +67,8 @@ def _expected(case, q, held, lens, history=OC.sealed_history):
             args = (pol, kept, N, w.sink, w.local, w.local_only_window, case.flags[b][:N + n])
             Q = f64(q[b, :n, h * G:(h + 1) * G])
             o, A = OC.chunk_head(Q, K, V, *args), OC.chunk_head(Q, K, np.abs(V), *args)
-            out[b, h] = o, _bound(o, A)
+            tiny = 2.0 ** -31 * N * np.abs(V[:N]).max(initial=0.0) if case.kv_format != lkb.KV_BF16 and len(kept) else 0.0
+            out[b, h] = o, _bound(o, A) + tiny
     return out
 
 
@@ -216,3 +222,41 @@ def test_blocks_with_nothing_to_do(cuda, fmt, held, n, counts):
     assert 1 < blocks <= ctas and starts[0] == (0, 0) and starts == sorted(starts)
     same = [x for x, y in zip(starts, starts[1:]) if x == y]
     assert same and all(tile == 0 for _, tile in same)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("n", [4, 50, 130])
+def test_values_of_any_size(cuda, fmt, n):
+    """Values whose scales differ by far from block to block and from row to row, a
+    block of zeros, values near fp32's ends of what sums hold."""
+    w = TINY.scaled(num_kv_heads=4, num_q_heads=16, batch=4, sink=4, local=64)
+    case = Case(w, total=1030, masks=S.masks_with_counts(w, (32, 64, 96, 128)), kv_format=fmt)
+    held = [900, 517, 68 + 256, 700]
+    k, v = case.history(0)
+    by = torch.tensor([1.0, 2.0 ** 40, 2.0 ** -40, 2.0 ** 7], device="cuda")
+    v *= by[:, None, None, None].to(torch.bfloat16)
+    v[:, 68:196] *= 2.0 ** -12
+    v[:, 196:324] *= 2.0 ** 9
+    v[:, 200:300:7] *= 2.0 ** -18
+    v[1, 324:452] = 0
+    v[3, 324:452] *= 2.0 ** 30
+    _fill(case, held)
+    _attend(case, held, n)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("k", [32, 128])
+@pytest.mark.parametrize("n", [3, 60])
+def test_sealed_values_cost_no_precision(cuda, fmt, k, n):
+    """Where nearly every weight is a sealed block's, o is as exact as its own
+    rounding: 1.66e-3 in the root mean square, and a fifth of P's 11 bits' 0.2e-3
+    and of the near tokens' bf16 weights."""
+    w = TINY.scaled(num_kv_heads=2, num_q_heads=8, batch=1, sink=0, local=8)
+    case = Case(w, total=6200, masks=S.masks_with_counts(w, (k, k)), kv_format=fmt)
+    held = [6100]
+    _fill(case, held)
+    q = _queries(case, n, scale=0.3)
+    key, v, _ = _chunk(case, 0, held, n)
+    got = f64(case.cache.chunk_attn(0, q, key, v))
+    for (b, h), (o, _) in _expected(case, q, held, [n]).items():
+        assert _rms(got[b, :, h * 4:h * 4 + 4], o) <= 1.2 * 1.66e-3, (b, h)
