@@ -39,9 +39,9 @@
 // measured bf16 matrix rate.  Chunks of a few tokens: the cache's bytes, through
 // a ring that holds two to five tiles per group; 64 sequences of 4096 tokens
 // take 98 us, 1.4 times what a plain copy's rate gives their bytes.  Sealed
-// blocks: the four warps that expand them, which share instruction caches with
-// every other role; 16 sequences of 8192 tokens take 114 us, 4.0 times their
-// bytes.  One sequence: three dependent launches, 28 us over 32768 tokens.
+// blocks: the softmax and the four warps that expand them, which share instruction
+// caches with every other role; 16 sequences of 8192 tokens take 114 us, 4.0 times
+// their bytes.  One sequence: three dependent launches, 28 us over 32768 tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -248,10 +248,10 @@ __device__ void plan_line(const ChunkArgs& a, const ChunkWork& w) {
     const uint64_t end = at + item_cost<kQuant>(w, it);
     if (x < end) {
       // (an item's own share comes before its tiles)
-      const uint64_t r = x - at - min(x - at, (uint64_t)w.cost_item), wide = (uint64_t)first_m<kQuant>(it) * w.cost_wide;
+      const int m0 = first_m<kQuant>(it);
+      const uint64_t r = x - at - min(x - at, (uint64_t)w.cost_item), wide = (uint64_t)m0 * w.cost_wide;
       const uint32_t kept = cost_kept(w, it);
-      const int t = (int)(r <= wide ? (r + w.cost_wide - 1) / w.cost_wide
-                                    : first_m<kQuant>(it) + (r - wide + kept - 1) / kept);
+      const int t = (int)(r <= wide ? (r + w.cost_wide - 1) / w.cost_wide : m0 + (r - wide + kept - 1) / kept);
       start = t < tiles_of(it) ? make_int2(e, t) : make_int2(e + 1, 0);
       break;
     }
@@ -467,10 +467,9 @@ constexpr int kWideBytes = kTile * kHeadDim * 2;
 //
 // Shared memory: q at full width, q on the kept channels (as wide as the
 // layer's widest such head; over sealed blocks as f16, 128 channels among them),
-// and a byte ring that the key and value tiles go
-// through in order, each taking what it needs (a key tile on 32 channels 8 KB,
-// full-width ones and values 32 KB), so that narrow heads have the more tiles
-// in flight.
+// and a byte ring that the key and value tiles go through in order, each taking
+// what it needs (a key tile on 32 channels 8 KB, full-width ones and values 32 KB),
+// so that narrow heads have the more tiles in flight.
 template <bool kDual, int kFmt>
 struct Smem {
   static constexpr bool kQuant = kFmt != kKvBf16;
@@ -630,21 +629,21 @@ __device__ __forceinline__ float power2(int e) { return __int_as_float((min(max(
 // Scores of sealed blocks.  A key's channel is code times scale, 8 bits times 24.
 // Rounded to bf16 it would be off by up to 2^-8 of itself, and the attention with
 // it (by the keys alone its relative error against fp64 rises from 2.3e-3 to 2.7 and
-// 3.3e-3, o's own rounding being 1.66e-3), so these keys and the q they meet are f16: q exactly
-// (8 bits), the scale and the product to 11 bits each.  What f16 lacks in range
-// goes into exponents: a block's scales are moved so that the largest lies in
-// [2^6, 2^7) (448 times that is below f16's largest), a row of q so that its
+// 3.3e-3, o's own rounding being 1.66e-3), so these keys and the q they meet are
+// f16: q exactly (8 bits), the scale and the product to 11 bits each.  What f16
+// lacks in range goes into exponents: a block's scales are moved so that the largest
+// lies in [2^6, 2^7) (448 times that is below f16's largest), a row of q so that its
 // largest channel lies in [2^14, 2^15), and the softmax moves the row's scores of
 // the block back.  Only channels whose scale is 2^-20 of the block's largest, or
 // whose q is 2^-31 of the row's largest, keep fewer bits.
 constexpr int kScaleExp = 6, kRowTop = 14;
 // Outputs of sealed blocks.  Values are their codes, exact in f16, and the weights
 // that they meet are p times the value's scale in f16, 11 bits of it (in bf16, 8
-// bits, o would be off by 2.3e-3 instead of 1.75e-3, at the same speed).  The range is kept by the row's reference m: p = 2^(s - m), and over
-// sealed blocks m is max s + log2 of the block's largest scale - 6, so that the
-// largest weight lies about 2^6, and below 2^15 when m lags by 8 (the sums l and the
-// outputs before are in units of 2^m too, and follow).  Only weights 2^-20 of the
-// largest keep fewer bits.
+// bits, o would be off by 2.3e-3 instead of 1.75e-3, at the same speed).  The range
+// is kept by the row's reference m: p = 2^(s - m), and over sealed blocks m is max s
+// + log2 of the block's largest scale - 6, so that the largest weight lies about 2^6,
+// and below 2^15 when m lags by 8 (the sums l and the outputs before are in units of
+// 2^m too, and follow).  Only weights 2^-20 of the largest keep fewer bits.
 constexpr int kWeightExp = 6;
 
 // The keys or the values of a sealed block, to be turned into a tile.  (Not
@@ -759,7 +758,9 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
     return *reinterpret_cast<const Segment*>(sm + L::kSeg + (idx & 1) * L::kSegBytes);
   };
   // whether a segment has tiles that take q on the kept channels
-  auto gathers = [&](const Segment& s) { return s.it.k > 0 && (kQuant || s.it.k < kHeadDim) && s.t1 > first_m<kQuant>(s.it); };
+  auto gathers = [&](const Segment& s) {
+    return s.it.k > 0 && (kQuant || s.it.k < kHeadDim) && s.t1 > first_m<kQuant>(s.it);
+  };
 
   if (kQuant && warp >= 12) {
     // ----------------------------------------------------------- the makers
@@ -1133,9 +1134,9 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
                 mma_ss<kHi, false>(d, q, k, kDescS);
 #pragma unroll
                 for (int y = 1; y < kSteps; ++y) {
-                  const uint32_t at = kThin ? (y >> 1) * (kTile * 4) + (y & 1) * 2 : (y >> 2) * (kTile * 8) + (y & 3) * 2;
-                  const uint32_t q_at = kThin ? (y >> 1) * q_stripe + (y & 1) * 2 : (y >> 2) * q_half + (y & 3) * 2;
-                  mma_ss<kHi, true>(d, q + q_at, k + at, kDescS);
+                  const uint32_t out = kThin ? y >> 1 : y >> 2, in = (kThin ? y & 1 : y & 3) * 2;
+                  mma_ss<kHi, true>(d, q + out * (kThin ? q_stripe : q_half) + in,
+                                    k + out * (kTile * (kThin ? 4 : 8)) + in, kDescS);
                 }
               };
               if (width == 0) run(std::integral_constant<int, 2>(), q_kept);
@@ -1274,7 +1275,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 #pragma unroll
             for (int x = 0; x < 4; ++x) out[x] = pack_f16x2(bf16_lo(in[x]) * f, bf16_hi(in[x]) * f);
             if (has)
-              *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c, q_rows)) = make_uint4(out[0], out[1], out[2], out[3]);
+              *reinterpret_cast<uint4*>(to + kept_byte(it.k, r, c, q_rows)) =
+                  make_uint4(out[0], out[1], out[2], out[3]);
             if (has && c == 0) row_back(gathered)[r] = kScaleLog2 * power2(e);
           }
           ++gathered;
@@ -1693,9 +1695,11 @@ cudaError_t launch_attn(const ChunkMaps& maps, const ChunkArgs& args, const Chun
 }  // namespace
 
 cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& w, cudaStream_t stream) {
-  const unsigned parts = kv_quantized(args.cv.kv_format) ? 2u : 1u;
+  const bool quant = kv_quantized(args.cv.kv_format);
+  const unsigned parts = quant ? 2u : 1u;
   const unsigned plan_blocks = 1u + w.special_seqs + (unsigned)(args.nb * args.cv.Hkv) * w.far_tiles * parts;
-  cudaError_t err = launch_after(kv_quantized(args.cv.kv_format) ? chunk_plan_kernel<true> : chunk_plan_kernel<false>, dim3(plan_blocks), kPlanThreads, 0, stream, args, w);
+  cudaError_t err = launch_after(quant ? chunk_plan_kernel<true> : chunk_plan_kernel<false>, dim3(plan_blocks),
+                                 kPlanThreads, 0, stream, args, w);
   if (err != cudaSuccess) return err;
   err = args.cv.kv_format == kKvInt8  ? launch_attn<kKvInt8>(maps, args, w, stream)
         : args.cv.kv_format == kKvFp8 ? launch_attn<kKvFp8>(maps, args, w, stream)

@@ -91,6 +91,7 @@ def test_sealed_keys_are_close_to_the_dequantised_ones():
         got = OC.sealed_keys(codes, scales, fmt)
         # two roundings to 11 bits; f16's smallest step below them
         step = 2.0 ** -25 * 2.0 ** (math.floor(math.log2(float(scales.max()))) - 6)
-        assert (np.abs(got - exact) <= 2.01 * 2.0 ** -11 * np.abs(exact) + (1 + np.abs(OQ.code_value(codes, fmt))) * step).all()
+        tol = 2.01 * 2.0 ** -11 * np.abs(exact) + (1 + np.abs(OQ.code_value(codes, fmt))) * step
+        assert (np.abs(got - exact) <= tol).all()
         codes, scales = OQ.quantize_per_channel(np.zeros((128, 32)), fmt)
         assert not OC.sealed_keys(codes, scales, fmt).any()

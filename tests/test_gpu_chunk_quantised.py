@@ -67,7 +67,8 @@ def _expected(case, q, held, lens, history=OC.sealed_history):
             args = (pol, kept, N, w.sink, w.local, w.local_only_window, case.flags[b][:N + n])
             Q = f64(q[b, :n, h * G:(h + 1) * G])
             o, A = OC.chunk_head(Q, K, V, *args), OC.chunk_head(Q, K, np.abs(V), *args)
-            tiny = 2.0 ** -31 * N * np.abs(V[:N]).max(initial=0.0) if case.kv_format != lkb.KV_BF16 and len(kept) else 0.0
+            sealed = case.kv_format != lkb.KV_BF16 and len(kept) > 0
+            tiny = 2.0 ** -31 * N * np.abs(V[:N]).max(initial=0.0) if sealed else 0.0
             out[b, h] = o, _bound(o, A) + tiny
     return out
 
