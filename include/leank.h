@@ -411,8 +411,8 @@ typedef struct lk_chunk {
 } lk_chunk;
 
 /* Bytes of lk_chunk_attn's workspace for chunks of up to n_max tokens, over a
- * cache of any format.  It needs no initialisation and may be shared by calls that do not overlap on
- * the GPU. */
+ * cache of any format.  It needs no initialisation and may be shared by calls
+ * that do not overlap on the GPU. */
 lk_status lk_chunk_workspace_bytes(lk_plan plan, int32_t batch, int32_t n_max, size_t* bytes);
 
 /* Attention of a chunk's queries over the cache and the chunk itself (chunked
