@@ -53,6 +53,8 @@ class CacheOptions(ctypes.Structure):
 
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_YARN, ROPE_SCALE_BANDS = range(5)
+ROPE_AXES_BLOCKS, ROPE_AXES_CYCLIC = 0, 1
+ROPE_SPECTRUM_SHARED, ROPE_SPECTRUM_OWN = 0, 1
 
 
 class Chunk(ctypes.Structure):
@@ -65,6 +67,11 @@ class RopeDesc(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
                 ("trained_positions", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
                 ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("pairs", ctypes.c_int32 * 4), ("order", ctypes.c_int32),
+                ("spectrum", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 SIGNATURES = {
@@ -105,6 +112,7 @@ SIGNATURES = {
     "lk_append_chunk": (ctypes.c_int, [_vp, _i32, ctypes.POINTER(Chunk), _vp]),
     "lk_extend": (ctypes.c_int, [_vp, _i32, ctypes.POINTER(Chunk), _vp, _vp, _sz, _vp]),
     "lk_build_rope": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(_vp)]),
+    "lk_build_rope_axes": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(RopeAxes), ctypes.POINTER(_vp)]),
     "lk_rope_destroy": (None, [_vp]),
     "lk_rope_apply": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
     "lk_cache_length": (ctypes.c_int, [_vp, _i32, ctypes.POINTER(_i32)]),
@@ -236,21 +244,32 @@ def _same_device(device, *tensors):
 
 
 class Rope:
-    """lk_build_rope: rotary positions of heads of 128 channels."""
+    """lk_build_rope: rotary positions of heads of 128 channels.
+
+    With ``axes``, the pairs of each axis (lk_build_rope_axes), positions have a
+    leading dimension of that many axes."""
+
+    axes = ()           # leading dimensions of the positions
 
     def __init__(self, rotary_dim=128, base=10000.0, layout=ROPE_HALF, scaling=ROPE_SCALE_NONE, factor=1.0,
-                 trained_positions=0, low_turns=0.0, high_turns=0.0, magnitude=0.0):
+                 trained_positions=0, low_turns=0.0, high_turns=0.0, magnitude=0.0, axes=None,
+                 axis_order=ROPE_AXES_BLOCKS, axis_spectrum=ROPE_SPECTRUM_SHARED):
         lib = load()
         self.desc = RopeDesc(rotary_dim, layout, scaling, trained_positions, base, factor, low_turns, high_turns,
                              magnitude)
         h = ctypes.c_void_p()
-        _check(lib.lk_build_rope(ctypes.byref(self.desc), ctypes.byref(h)))
+        if axes is None:
+            _check(lib.lk_build_rope(ctypes.byref(self.desc), ctypes.byref(h)))
+        else:
+            self.axes = (len(axes),)
+            x = RopeAxes(len(axes), (ctypes.c_int32 * 4)(*axes[:4]), axis_order, axis_spectrum, 0)
+            _check(lib.lk_build_rope_axes(ctypes.byref(self.desc), ctypes.byref(x), ctypes.byref(h)))
         self._h = h
 
     def apply(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """lk_rope_apply: q [..., Hq, 128] and k [..., Hkv, 128] bf16 (tokens
         evenly spaced, e.g. views of one projection's rows), positions int32
-        [...]; q or k may be None.  Returns (q_out, k_out), new dense tensors
+        [...] ([axes, ...] with axes); q or k may be None.  Returns (q_out, k_out), new dense tensors
         unless given; q and k themselves may be given."""
         import torch
         if q is None and k is None:
@@ -262,7 +281,7 @@ class Rope:
         tokens = 1
         for n in lead:
             tokens *= n
-        _need(positions, torch.int32, lead, "positions")
+        _need(positions, torch.int32, self.axes + lead, "positions")
         args, outs = [], []
         for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
             if x is None:

@@ -63,9 +63,7 @@ struct lk_plan_s {
 };
 
 struct lk_rope_s {
-  lk_rope_desc d;
-  float magnitude;
-  uint64_t freq[kHeadDim / 2] = {};  // turns per position x 2^64
+  RopeTable table = {};
 };
 
 namespace {
@@ -1488,8 +1486,8 @@ lk_status lk_extend(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* 
 
 // ---------------------------------------------------------------------------
 // Rotary positions
-lk_status lk_build_rope(const lk_rope_desc* desc, lk_rope* out) {
-  if (!desc || !out) return fail(LK_ERR_ARG, "lk_build_rope: null argument");
+static lk_status build_rope(const lk_rope_desc* desc, const lk_rope_axes* axes, lk_rope* out, const char* what) {
+  if (!desc || !out) return fail(LK_ERR_ARG, "%s: null argument", what);
   *out = nullptr;
   const lk_rope_desc& d = *desc;
   if (d.rotary_dim < 16 || d.rotary_dim > kHeadDim || d.rotary_dim % 16 != 0)
@@ -1512,27 +1510,74 @@ lk_status lk_build_rope(const lk_rope_desc* desc, lk_rope* out) {
   }
   if (!(d.magnitude >= 0.0) || !std::isfinite(d.magnitude))
     return fail(LK_ERR_ARG, "magnitude %g must be finite and >= 0", d.magnitude);
+  const int pairs = d.rotary_dim / 2;
+  lk_rope_axes one = {};
+  one.num_axes = 1;
+  one.pairs[0] = pairs;
+  const lk_rope_axes& x = axes ? *axes : one;
+  if (x.num_axes < 1 || x.num_axes > kRopeAxes)
+    return fail(LK_ERR_UNSUPPORTED, "num_axes %d outside [1, %d]", x.num_axes, kRopeAxes);
+  if (x.order != LK_ROPE_AXES_BLOCKS && x.order != LK_ROPE_AXES_CYCLIC)
+    return fail(LK_ERR_ARG, "order %d is not LK_ROPE_AXES_BLOCKS or LK_ROPE_AXES_CYCLIC", x.order);
+  if (x.spectrum != LK_ROPE_SPECTRUM_SHARED && x.spectrum != LK_ROPE_SPECTRUM_OWN)
+    return fail(LK_ERR_ARG, "spectrum %d is not LK_ROPE_SPECTRUM_SHARED or LK_ROPE_SPECTRUM_OWN", x.spectrum);
+  if (x.reserved != 0) return fail(LK_ERR_ARG, "%s: reserved must be 0", what);
+  int64_t sum = 0;
+  for (int a = 0; a < x.num_axes; ++a) {
+    if (x.pairs[a] < 1) return fail(LK_ERR_ARG, "axis %d has %d pairs", a, x.pairs[a]);
+    sum += x.pairs[a];
+  }
+  if (sum != pairs)
+    return fail(LK_ERR_ARG, "the axes have %lld pairs; rotary_dim %d has %d", (long long)sum, d.rotary_dim, pairs);
+  for (int a = 1; x.order == LK_ROPE_AXES_CYCLIC && a < x.num_axes; ++a)
+    if (a + x.num_axes * (x.pairs[a] - 1) >= pairs)
+      return fail(LK_ERR_ARG, "axis %d cannot take %d pairs in turn out of %d", a, x.pairs[a], pairs);
   auto r = new (std::nothrow) lk_rope_s();
-  if (!r) return fail(LK_ERR_CAPACITY, "lk_build_rope: out of host memory");
-  r->d = d;
-  const double dim = d.rotary_dim, two_pi = 6.283185307179586476925;
-  const double base = d.scaling == LK_ROPE_SCALE_NTK ? d.base * std::pow(d.factor, dim / (dim - 2.0)) : d.base;
-  auto at = [&](double turns) {
-    return dim * std::log(d.trained_positions / (turns * two_pi)) / (2.0 * std::log(base));
-  };
-  const double lo = yarn ? std::max(std::floor(at(high)), 0.0) : 0.0;
-  const double hi = yarn ? std::min(std::ceil(at(low)), dim - 1.0) : 0.0;
-  for (int i = 0; i < d.rotary_dim / 2; ++i) {
-    double w = std::pow(base, -2.0 * i / dim);
+  if (!r) return fail(LK_ERR_CAPACITY, "%s: out of host memory", what);
+  const double two_pi = 6.283185307179586476925;
+  // angle per position of pair j of those that a head's first `dim` channels have
+  auto angle = [&](int j, double dim) {
+    const double base = d.scaling == LK_ROPE_SCALE_NTK ? d.base * std::pow(d.factor, dim / (dim - 2.0)) : d.base;
+    auto at = [&](double turns) {
+      return dim * std::log(d.trained_positions / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    const double lo = yarn ? std::max(std::floor(at(high)), 0.0) : 0.0;
+    const double hi = yarn ? std::min(std::ceil(at(low)), dim - 1.0) : 0.0;
+    double w = std::pow(base, -2.0 * j / dim);
     double keep = d.scaling == LK_ROPE_SCALE_LINEAR ? 0.0 : 1.0;      // share of w that is not stretched
-    if (yarn) keep = 1.0 - std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+    if (yarn) keep = 1.0 - std::min(std::max((j - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
     if (bands) keep = std::min(std::max((d.trained_positions * w / two_pi - low) / (high - low), 0.0), 1.0);
     if (scaled && d.scaling != LK_ROPE_SCALE_NTK) w = w * keep + w / d.factor * (1.0 - keep);
-    r->freq[i] = (uint64_t)std::ldexp(w / two_pi, 64);                // w <= 1: below 2^62
+    return w;
+  };
+  RopeTable& t = r->table;
+  int taken[kRopeAxes] = {}, block = 0;
+  for (int i = 0; i < pairs; ++i) {
+    while (x.order == LK_ROPE_AXES_BLOCKS && taken[block] == x.pairs[block]) ++block;
+    const int turn = i % x.num_axes;
+    const int a = x.order == LK_ROPE_AXES_BLOCKS ? block : i < x.num_axes * x.pairs[turn] ? turn : 0;
+    const bool whole = x.spectrum == LK_ROPE_SPECTRUM_SHARED;
+    const double w = whole ? angle(i, d.rotary_dim) : angle(taken[a], 2.0 * x.pairs[a]);
+    ++taken[a];
+    t.freq[i] = (uint64_t)std::ldexp(w / two_pi, 64);                // w <= 1: below 2^62
+    if (x.num_axes > 1) t.freq[i] = (t.freq[i] & ~(uint64_t)(kRopeAxes - 1)) | (uint64_t)a;
   }
-  r->magnitude = d.magnitude != 0.0 ? (float)d.magnitude : yarn ? (float)(0.1 * std::log(d.factor) + 1.0) : 1.f;
+  t.rotary_dim = d.rotary_dim;
+  t.layout = d.layout;
+  t.axes = x.num_axes;
+  t.magnitude = d.magnitude != 0.0 ? (float)d.magnitude : yarn ? (float)(0.1 * std::log(d.factor) + 1.0) : 1.f;
   *out = r;
   return LK_OK;
+}
+
+lk_status lk_build_rope(const lk_rope_desc* desc, lk_rope* out) {
+  return build_rope(desc, nullptr, out, "lk_build_rope");
+}
+
+lk_status lk_build_rope_axes(const lk_rope_desc* desc, const lk_rope_axes* axes, lk_rope* out) {
+  if (out) *out = nullptr;
+  if (!axes) return fail(LK_ERR_ARG, "lk_build_rope_axes: null axes");
+  return build_rope(desc, axes, out, "lk_build_rope_axes");
 }
 
 void lk_rope_destroy(lk_rope rope) { delete rope; }
@@ -1577,10 +1622,7 @@ lk_status lk_rope_apply(lk_rope rope, const void* q, int64_t q_stride, const voi
   a.tokens = tokens;
   a.Hq = num_q_heads;
   a.Hkv = num_kv_heads;
-  a.rotary_dim = rope->d.rotary_dim;
-  a.layout = rope->d.layout;
-  a.magnitude = rope->magnitude;
-  std::memcpy(a.freq, rope->freq, sizeof(a.freq));
+  a.rope = rope->table;
   int dev = 0, sms = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -143,18 +143,26 @@ struct ChunkWork {
 };
 
 enum RopeLayout : int32_t { kRopeHalf = 0, kRopeInterleaved = 1 };
+// What a rope turns, and by how much per position.
+constexpr int kRopeAxes = 4;       // axes at most
+struct RopeTable {
+  int32_t rotary_dim, layout;
+  int32_t axes;                  // axes of a position
+  float magnitude;               // multiplies cosine and sine
+  // turns per position x 2^64; with several axes the pair's axis stands in the
+  // two lowest bits (of 2^-62 turns, far below what w itself is known to)
+  uint64_t freq[kHeadDim / 2];
+};
 struct RopeArgs {
   const uint16_t* q;        // bf16 [tokens][Hq][128], tokens q_stride elements apart
   const uint16_t* k;
   uint16_t* q_out;
   uint16_t* k_out;
   int64_t q_stride, k_stride, q_out_stride, k_out_stride;
-  const int32_t* positions; // [tokens]
+  const int32_t* positions; // [axes][tokens]
   int64_t tokens;
   int32_t Hq, Hkv;
-  int32_t rotary_dim, layout;
-  float magnitude;          // multiplies cosine and sine
-  uint64_t freq[kHeadDim / 2];   // turns per position x 2^64
+  RopeTable rope;
 };
 
 // Raise kernel `fn`'s dynamic shared-memory limit to `bytes` on the current

@@ -501,10 +501,37 @@ typedef struct lk_rope_s* lk_rope;    /* host object owned by the library */
 lk_status lk_build_rope(const lk_rope_desc* desc, lk_rope* out);
 void lk_rope_destroy(lk_rope rope);
 
+/* Which pairs belong to which axis, where a token has a position on each of
+ * several axes (time, height and width of an image's or a video's patches): in
+ * runs, axis after axis, or in turn: axis a >= 1 takes its pairs from i mod
+ * num_axes = a, the lowest first, and axis 0 the rest. */
+typedef enum lk_rope_order { LK_ROPE_AXES_BLOCKS = 0, LK_ROPE_AXES_CYCLIC = 1 } lk_rope_order;
+
+/* Which angle w_i a pair turns per position on its axis: the pair i of the whole
+ * head has it as without axes, or the j-th pair of its axis the j-th of a rope of
+ * rotary_dim 2 pairs[axis] (scaling included). */
+typedef enum lk_rope_spectrum { LK_ROPE_SPECTRUM_SHARED = 0, LK_ROPE_SPECTRUM_OWN = 1 } lk_rope_spectrum;
+
+typedef struct lk_rope_axes {
+  int32_t num_axes;           /* 1 .. 4 */
+  int32_t pairs[4];           /* of each axis, >= 1; rotary_dim / 2 in all */
+  int32_t order;              /* lk_rope_order */
+  int32_t spectrum;           /* lk_rope_spectrum */
+  int32_t reserved;           /* 0 */
+} lk_rope_axes;
+
+/* lk_build_rope for positions of several axes (host only; touches no GPU):
+ * calls that take the rope read positions [num_axes][...], one axis after
+ * another.  One axis is what lk_build_rope gives.  (A token of text has the same
+ * position on every axis, and with LK_ROPE_SPECTRUM_SHARED turns as without
+ * axes.) */
+lk_status lk_build_rope_axes(const lk_rope_desc* desc, const lk_rope_axes* axes, lk_rope* out);
+
 /* Turn the heads of q and k by their tokens' positions, before they enter
  * lk_prefill, lk_append, lk_step, lk_chunk_attn and so on:
  *   q [tokens][num_q_heads][128], k [tokens][num_kv_heads][128]  device bf16;
- *   positions  device int32 [tokens], any value (negative ones turn back);
+ *   positions  device int32 [tokens] ([num_axes][tokens] for a rope of
+ *              several axes), any value (negative ones turn back);
  *   q_out, k_out  as q and k; may be q and k themselves (with the same
  *   stride), else must not overlap the inputs.
  * Strides are elements between consecutive tokens: at least heads * 128 and a

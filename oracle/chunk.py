@@ -83,3 +83,35 @@ def rope(x, positions, frequencies, layout: str = "half", magnitude: float = 1.0
     x[..., a] = xa * c - xb * s
     x[..., b] = xb * c + xa * s
     return x
+
+
+def rope_axes(dim: int, base: float, pairs, order: str = "blocks", spectrum: str = "shared", scaling: str = "none",
+              factor: float = 1.0, trained: int = 0, low: float = 0.0, high: float = 0.0):
+    """Positions of several axes, `pairs[a]` pairs to axis a: (angle per position of
+    each pair, float64 [dim / 2]; its axis, int [dim / 2])."""
+    A, half = len(pairs), dim // 2
+    axis = np.zeros(half, dtype=int)
+    if order == "blocks":
+        axis = np.repeat(np.arange(A), pairs)
+    else:
+        for a in range(1, A):
+            axis[np.arange(a, half, A)[:pairs[a]]] = a
+    assert [int((axis == a).sum()) for a in range(A)] == list(pairs)
+    w = rope_frequencies(dim, base, scaling, factor, trained, low, high)
+    if spectrum == "own":
+        for a in range(A):
+            w[axis == a] = rope_frequencies(2 * pairs[a], base, scaling, factor, trained, low, high)
+    return w, axis
+
+
+def rope_on_axes(x, positions, frequencies, axis, layout: str = "half", magnitude: float = 1.0) -> np.ndarray:
+    """x [tokens, heads, d] turned by positions [axes, tokens], float64."""
+    p = np.asarray(positions, np.float64)[axis].T                   # [tokens, pairs]
+    x = np.array(x, dtype=np.float64)
+    half = len(frequencies)
+    turn = magnitude * np.exp(1j * p * frequencies)[:, None]
+    a, b = (slice(0, half), slice(half, 2 * half)) if layout == "half" else \
+        (slice(0, 2 * half, 2), slice(1, 2 * half, 2))
+    y = (x[..., a] + 1j * x[..., b]) * turn
+    x[..., a], x[..., b] = y.real, y.imag
+    return x
