@@ -42,8 +42,8 @@ class RegionInfo(ctypes.Structure):
                 ("sealed_blocks", ctypes.c_int32)]
 
 
-KV_BF16, KV_INT8, KV_FP8 = 0, 1, 2
-KV_FORMAT_NAMES = {KV_BF16: "bf16", KV_INT8: "int8", KV_FP8: "fp8"}
+KV_BF16, KV_INT8, KV_FP8, KV_FP8_BLOCK = 0, 1, 2, 3
+KV_FORMAT_NAMES = {KV_BF16: "bf16", KV_INT8: "int8", KV_FP8: "fp8", KV_FP8_BLOCK: "fp8_block"}
 STEP_AUTO, STEP_FUSED, STEP_SPLIT = 0, 1, 2
 
 
@@ -115,6 +115,8 @@ SIGNATURES = {
     "lk_build_rope_axes": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(RopeAxes), ctypes.POINTER(_vp)]),
     "lk_rope_destroy": (None, [_vp]),
     "lk_rope_apply": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
+    "lk_append_rope": (ctypes.c_int, [_vp, _i32, _vp, ctypes.POINTER(Chunk), _vp, _vp, _i64, _vp]),
+    "lk_step_rope": (ctypes.c_int, [_vp, _i32, _vp, ctypes.POINTER(Chunk), _vp, _vp, _vp, _sz, _vp]),
     "lk_cache_length": (ctypes.c_int, [_vp, _i32, ctypes.POINTER(_i32)]),
     "lk_cache_lengths": (ctypes.c_int, [_vp, _i32, _vp]),
     "lk_cache_region": (ctypes.c_int, [_vp, _i32, _i32, _i32, ctypes.POINTER(RegionInfo)]),
@@ -394,7 +396,8 @@ class Cache:
     middle rows of all sequences share page pools sized for that many middle
     tokens in total.  ``kv_format=KV_INT8`` quantises complete 128-row
     blocks of the middle (lk_cache_init_ex); ``KV_FP8`` stores them as e4m3
-    codes."""
+    codes, ``KV_FP8_BLOCK`` with one scale for a block's keys and one for its
+    values."""
 
     def __init__(self, plan: Plan, batch: int, capacity: int, device=None, stream=None, middle_tokens=None,
                  kv_format=KV_BF16):
@@ -490,7 +493,7 @@ class Cache:
     def block(self, layer, b, kv_head, j, stream=None):
         """lk_cache_block: (k_codes [128, k], k_scales [k], v_codes [128, 128],
         v_scales [128]) of sealed block j, logical order; codes int8 (INT8)
-        or uint8 e4m3 bit patterns (FP8)."""
+        or uint8 e4m3 bit patterns (FP8, FP8_BLOCK)."""
         k = self.plan.head(layer, kv_head)[1]
         kc = np.zeros((128, k), np.int8)
         ks = np.zeros(k, np.float32)
@@ -498,7 +501,7 @@ class Cache:
         vs = np.zeros(128, np.float32)
         _check(_lib.lk_cache_block(self._h, layer, b, kv_head, j, kc.ctypes.data, ks.ctypes.data, vc.ctypes.data,
                                    vs.ctypes.data, _stream(stream)))
-        if self.kv_format == KV_FP8:
+        if self.kv_format != KV_INT8:
             kc, vc = kc.view(np.uint8), vc.view(np.uint8)
         return kc, ks, vc, vs
 
@@ -715,6 +718,68 @@ class Cache:
         o = self._chunk_out(q, o, stream)
         _check(_lib.lk_extend(self._h, layer, ctypes.byref(c), o.data_ptr(), self.chunk_workspace.data_ptr(),
                               self.chunk_workspace.numel(), _stream(stream)))
+        return o
+
+    # -- with the rotation on the way
+    def _rope_chunk(self, rope, q, k, v, positions, lens, ids):
+        """The lk_chunk of tokens to be turned, given as [B, n, heads, 128] or, one of
+        each sequence, [B, heads, 128]; and what it points to."""
+        import torch
+        B, H = self.batch, self.plan.num_kv_heads
+        lead = (B, k.shape[1]) if k.dim() == 4 else (B,)
+        c = Chunk()
+        c.n_max = lead[1] if len(lead) > 1 else 1
+        if q is not None:
+            c.q, c.q_stride = q.data_ptr(), _token_stride(q, self.plan.num_q_heads, lead, "q")
+        c.k, c.k_stride = k.data_ptr(), _token_stride(k, H, lead, "k")
+        c.v, c.v_stride = v.data_ptr(), _token_stride(v, H, lead, "v")
+        if ids is not None:
+            _need(ids, torch.int32, lead, "ids")
+            c.ids = ids.data_ptr()
+        if positions is not None:
+            _need(positions, torch.int32, rope.axes + lead, "positions")
+        if lens is not None:
+            lens = np.ascontiguousarray(lens, dtype=np.int32)
+            if lens.shape != (B,):
+                raise ValueError(f"lens shape {lens.shape}")
+            c.lens = lens.ctypes.data
+        _same_device(self.buffer.device, q, k, v, ids, positions)
+        return c, lens, (*lead, self.plan.num_q_heads, 128)
+
+    def append_rope(self, layer, rope, k, v, positions=None, q=None, q_out=None, lens=None, ids=None, stream=None):
+        """lk_append_rope: k, v [B, n, Hkv, 128] bf16 (tokens evenly spaced), or one
+        token of each sequence [B, Hkv, 128]; the keys enter the layer turned by
+        `positions` (int32 [B, n], with a leading dimension of the rope's axes; None:
+        the tokens' own positions in their sequences).  With q [..., Hq, 128] the
+        turned queries go to q_out, a new dense tensor unless given (q itself may be);
+        returns q_out.  Rows past a sequence's length are left as they are."""
+        import torch
+        c, lens, shape = self._rope_chunk(rope, q, k, v, positions, lens, ids)
+        out, step = None, 0
+        if q is not None:
+            if q_out is None:
+                q_out = _empty(shape, torch.bfloat16, q.device, stream)
+            out, step = q_out.data_ptr(), _token_stride(q_out, shape[-2], shape[:-2], "q_out")
+            _same_device(self.buffer.device, q_out)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        _check(_lib.lk_append_rope(self._h, layer, rope._h, ctypes.byref(c), _ptr(positions), out, step,
+                                   _stream(stream)))
+        return q_out
+
+    def step_rope(self, layer, rope, q, k, v, positions=None, ids=None, o=None, stream=None):
+        """lk_step_rope: append_rope of one token of every sequence (q [B, Hq, 128],
+        k, v [B, Hkv, 128]), then attention with the turned queries -> o fp32."""
+        import torch
+        if k.dim() != 3:
+            raise ValueError(f"k: expected [B, Hkv, 128], got {tuple(k.shape)}")
+        c, _, shape = self._rope_chunk(rope, q, k, v, positions, None, ids)
+        if o is None:
+            o = _empty(shape, torch.float32, q.device, stream)
+        _need(o, torch.float32, shape, "o")
+        _same_device(self.buffer.device, o)
+        _check(_lib.lk_step_rope(self._h, layer, rope._h, ctypes.byref(c), _ptr(positions), o.data_ptr(),
+                                 self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
         return o
 
     # -- queries

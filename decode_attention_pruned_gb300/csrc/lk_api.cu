@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/leank.h"
+#include "lk_block.h"
 #include "lk_internal.h"
 #include "lk_kernels.h"
 
@@ -172,7 +173,7 @@ lk_status compute_layout(const lk_plan_s& p, int B, int cap, int64_t middle_toke
       if (q8) {
         // sealed blocks are the pages; bf16 rows hold only the tails
         page_q[pl] = qbytes;
-        qbytes += np * qblock_bytes(pool_width(pl));
+        qbytes += np * sealed_bytes(fmt, pool_width(pl));
       } else {
         page_k[pl] = rows[pl];
         rows[pl] += np * kPageRows;
@@ -213,7 +214,7 @@ lk_status compute_layout(const lk_plan_s& p, int B, int cap, int64_t middle_toke
         } else {
           hd.qblocks = (int32_t)(mid_cap / kQBlockRows);
           hd.qoff = qbytes;
-          qbytes += (int64_t)B * hd.qblocks * qblock_bytes(hd.n_kept);
+          qbytes += (int64_t)B * hd.qblocks * sealed_bytes(fmt, hd.n_kept);
         }
       } else if (paged) {
         hd.cap_b = lay->max_pages * kPageRows;
@@ -473,7 +474,7 @@ uint64_t entry_bytes(const lk_cache_s* cache, const HeadDesc& hd, int N, int cnt
   }
   if (kv_quantized(cache->lay.kv_format) && nb > 0) {
     const uint64_t sealed = nb / kQBlockRows, tail = nb % kQBlockRows;
-    return na * (2 * kHeadDim * 2) + sealed * (uint64_t)qblock_bytes(hd.n_kept) +
+    return na * (2 * kHeadDim * 2) + sealed * (uint64_t)sealed_bytes(cache->lay.kv_format, hd.n_kept) +
            tail * (uint64_t)(hd.n_kept + kHeadDim) * 2;
   }
   return na * (2 * kHeadDim * 2) + nb * (uint64_t)(hd.n_kept + kHeadDim) * 2;
@@ -629,8 +630,8 @@ static lk_status cache_bytes_impl(lk_plan plan, int32_t batch, int32_t capacity_
     return fail(LK_ERR_ARG, "batch %d out of range", batch);
   if (capacity_tokens < 1 || capacity_tokens > (1 << 30))
     return fail(LK_ERR_ARG, "capacity_tokens %d out of [1, 2^30]", capacity_tokens);
-  if (fmt != kKvBf16 && fmt != kKvInt8 && fmt != kKvFp8)
-    return fail(LK_ERR_ARG, "kv_format %d is not LK_KV_BF16, LK_KV_INT8 or LK_KV_FP8", fmt);
+  if (fmt != kKvBf16 && fmt != kKvInt8 && fmt != kKvFp8 && fmt != kKvFp8Block)
+    return fail(LK_ERR_ARG, "kv_format %d is not LK_KV_BF16, LK_KV_INT8, LK_KV_FP8 or LK_KV_FP8_BLOCK", fmt);
   Layout lay;
   lk_status st = compute_layout(*plan, batch, capacity_tokens, middle_tokens, fmt, &lay);
   if (st != LK_OK) return st;
@@ -990,6 +991,17 @@ void append_commit(lk_cache cache, int32_t layer0, int32_t nlayers) {
       if (cache->active[b]) cache->host_len[(size_t)l * B + b] += 1;
 }
 
+// A one-token append's arguments but for its inputs and sequences.
+TokenArgs token_args(const lk_cache_s* cache, int32_t layer0, int32_t nlayers, const int32_t* ids) {
+  TokenArgs t = {};
+  t.cv = cache->cv;
+  t.layer = layer0;
+  t.nlayers = nlayers;
+  t.ids = ids;
+  t.ticket = cache->cv.active + cache->B + layer0;
+  return t;
+}
+
 void return_pages(lk_cache cache, const int64_t need[kNumPools]) {
   for (int pl = 0; pl < kNumPools; ++pl) cache->host_free[pl] += need[pl];
 }
@@ -1006,6 +1018,11 @@ void set_divisors(const lk_cache_s* cache, DecodeArgs& a) {
     a.div_cost_b[i] = make_fastdiv((uint32_t)(2 * k + 256));
     a.div_cost_q[i] = make_fastdiv((uint32_t)(qblock_bytes(k) / kQBlockRows));
   }
+}
+
+cudaError_t run_decode(const lk_cache_s* cache, const DecodeArgs& a, int ctas, cudaStream_t stream) {
+  return cache->lay.kv_format == kKvFp8Block ? launch_decode_block(a, ctas, stream)
+                                             : launch_decode(cache->maps, a, ctas, stream);
 }
 
 // Host side of a decode launch: checks, and the kernel arguments (no fused
@@ -1049,14 +1066,26 @@ lk_status lk_append_layers(lk_cache cache, int32_t layer0, int32_t nlayers, cons
   int64_t need[kNumPools];
   lk_status st = append_prepare(cache, layer0, nlayers, k, v, ids, "lk_append", need);
   if (st != LK_OK) return st;
-  AppendArgs a;
-  a.cv = cache->cv;
-  a.layer = layer0;
-  a.nlayers = nlayers;
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
-  a.ids = ids;
-  cudaError_t err = launch_append(a, static_cast<cudaStream_t>(stream));
+  cudaError_t err;
+  if (cache->lay.kv_format == kKvFp8Block) {
+    TokenArgs t = token_args(cache, layer0, nlayers, ids);
+    t.nb = cache->B;
+    t.all = 1;
+    t.k = static_cast<const uint16_t*>(k);
+    t.v = static_cast<const uint16_t*>(v);
+    t.k_stride = t.v_stride = (int64_t)cache->cv.Hkv * kHeadDim;
+    t.k_layer = t.v_layer = cache->B * t.k_stride;
+    err = launch_token_append(t, nullptr, static_cast<cudaStream_t>(stream));
+  } else {
+    AppendArgs a;
+    a.cv = cache->cv;
+    a.layer = layer0;
+    a.nlayers = nlayers;
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.ids = ids;
+    err = launch_append(a, static_cast<cudaStream_t>(stream));
+  }
   if (err != cudaSuccess) {
     return_pages(cache, need);
     return cuda_fail(err, "lk_append launch");
@@ -1076,7 +1105,7 @@ lk_status lk_decode_attn_layers(lk_cache cache, int32_t layer0, int32_t nlayers,
   int ctas = 0;
   lk_status st = decode_prepare(cache, layer0, nlayers, q, o, workspace, ws_bytes, "lk_decode_attn", a, ctas);
   if (st != LK_OK) return st;
-  cudaError_t err = launch_decode(cache->maps, a, ctas, static_cast<cudaStream_t>(stream));
+  cudaError_t err = run_decode(cache, a, ctas, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_fail(err, "lk_decode_attn launch");
   return LK_OK;
 }
@@ -1106,7 +1135,7 @@ lk_status lk_step_layers(lk_cache cache, int32_t layer0, int32_t nlayers, const 
   a.k_new = static_cast<const uint16_t*>(k);
   a.v_new = static_cast<const uint16_t*>(v);
   a.ids = ids;
-  cudaError_t err = launch_decode(cache->maps, a, ctas, static_cast<cudaStream_t>(stream));
+  cudaError_t err = run_decode(cache, a, ctas, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) {
     return_pages(cache, need);
     return cuda_fail(err, "lk_step launch");
@@ -1146,7 +1175,7 @@ static lk_status step_in_place(lk_cache cache, int32_t layer, const void* q, con
   if (st != LK_OK) return st;
   st = lk_append_layers(cache, layer, 1, k, v, ids, stream);
   if (st != LK_OK) return st;
-  cudaError_t err = launch_decode(cache->maps, a, ctas, static_cast<cudaStream_t>(stream));
+  cudaError_t err = run_decode(cache, a, ctas, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_fail(err, "lk_step_host decode launch");
   return LK_OK;
 }
@@ -1256,7 +1285,7 @@ lk_status lk_step_layers_host_packed(lk_cache cache, int32_t layer0, int32_t nla
   if (st != LK_OK) return st;
   st = lk_append_layers(cache, layer0, nlayers, in + qb, in + qb + kvb, ids, stream);
   if (st != LK_OK) return st;
-  cudaError_t err = launch_decode(cache->maps, a, ctas, static_cast<cudaStream_t>(stream));
+  cudaError_t err = run_decode(cache, a, ctas, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_fail(err, "lk_step_layers_host_packed decode launch");
   return LK_OK;
 }
@@ -1417,14 +1446,24 @@ lk_status chunk_attn_run(lk_cache cache, const lk_chunk* c, ChunkArgs& a, ChunkW
   return LK_OK;
 }
 
-lk_status chunk_append_run(lk_cache cache, const lk_chunk* c, ChunkArgs& a, const int64_t need[kNumPools],
-                           const char* what, cudaStream_t s) {
+lk_status chunk_append_run(lk_cache cache, const lk_chunk* c, ChunkArgs& a, const RopeChunk* rope,
+                           const int64_t need[kNumPools], const char* what, cudaStream_t s) {
   lk_status st = cache->take_pages(need, what);
   if (st != LK_OK) return st;
   bool middle = false;
   for (int h = 0; h < cache->cv.Hkv; ++h) middle |= cache->lay.heads[(size_t)a.layer * cache->cv.Hkv + h].cap_b > 0;
-  cudaError_t err = chunk_groups(
-      cache, c, a, [&](const ChunkArgs& g) { return launch_chunk_append(g, middle, cache->num_sms, s); });
+  cudaError_t err = chunk_groups(cache, c, a, [&](const ChunkArgs& g) {
+    if (!rope || g.n_max > 1) return launch_chunk_append(g, rope, middle, cache->num_sms, s);
+    TokenArgs t = token_args(cache, g.layer, 1, g.ids);
+    t.b0 = g.b0;
+    t.nb = g.nb;
+    t.k = g.k;
+    t.v = g.v;
+    t.k_stride = g.k_stride;
+    t.v_stride = g.v_stride;
+    for (int i = 0; i < g.nb; ++i) t.takes[i / 32] |= (uint32_t)(g.lens[i] != 0) << i % 32;
+    return launch_token_append(t, rope, s);
+  });
   if (err != cudaSuccess) {
     return_pages(cache, need);
     return cuda_fail(err, what);
@@ -1463,7 +1502,7 @@ lk_status lk_append_chunk(lk_cache cache, int32_t layer, const lk_chunk* chunk, 
   int64_t need[kNumPools];
   lk_status st = chunk_prepare(cache, layer, chunk, true, "lk_append_chunk", a, need);
   if (st != LK_OK || a.n_max == 0) return st;
-  return chunk_append_run(cache, chunk, a, need, "lk_append_chunk", static_cast<cudaStream_t>(stream));
+  return chunk_append_run(cache, chunk, a, nullptr, need, "lk_append_chunk", static_cast<cudaStream_t>(stream));
 }
 
 lk_status lk_extend(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* o, void* workspace, size_t ws_bytes,
@@ -1481,7 +1520,7 @@ lk_status lk_extend(lk_cache cache, int32_t layer, const lk_chunk* chunk, void* 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = chunk_attn_run(cache, chunk, a, w, maps, "lk_extend", s);
   if (st != LK_OK) return st;
-  return chunk_append_run(cache, chunk, write, need, "lk_extend", s);
+  return chunk_append_run(cache, chunk, write, nullptr, need, "lk_extend", s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1632,6 +1671,73 @@ lk_status lk_rope_apply(lk_rope rope, const void* q, int64_t q_stride, const voi
   return LK_OK;
 }
 
+// Checks of an append that turns its keys, and its launch arguments.
+static lk_status append_rope_prepare(lk_cache cache, int32_t layer, lk_rope rope, const lk_chunk* c,
+                                     const int32_t* positions, void* q_out, int64_t q_out_stride, const char* what,
+                                     ChunkArgs& a, RopeChunk& r, int64_t need[kNumPools]) {
+  if (!rope) return fail(LK_ERR_ARG, "%s: null rope", what);
+  lk_status st = chunk_prepare(cache, layer, c, true, what, a, need);
+  if (st != LK_OK) return st;
+  if (positions && !aligned(positions, 4)) return fail(LK_ERR_ALIGN, "%s: positions must be 4-byte aligned", what);
+  r = RopeChunk{};
+  r.rope = rope->table;
+  r.positions = positions;
+  r.axis_stride = (int64_t)cache->B * c->n_max;
+  if (!c->q != !q_out) return fail(LK_ERR_ARG, "%s: q without q_out, or q_out without q", what);
+  if (!c->q || c->n_max == 0) return LK_OK;
+  if (!aligned(c->q, 16) || !aligned(q_out, 16))
+    return fail(LK_ERR_ALIGN, "%s: q and q_out must be 16-byte aligned", what);
+  const int64_t dense = (int64_t)cache->cv.Hq * kHeadDim, given[2] = {c->q_stride, q_out_stride};
+  int64_t stride[2];
+  for (int i = 0; i < 2; ++i) {
+    stride[i] = given[i] == 0 ? dense : given[i];
+    if (stride[i] < dense || stride[i] % 8 != 0 || stride[i] > kMaxTokenStride)
+      return fail(LK_ERR_ARG, "%s: a stride of q, %lld, is not 0 or a multiple of 8 in [%lld, %lld]", what,
+                  (long long)given[i], (long long)dense, (long long)kMaxTokenStride);
+  }
+  if (q_out == c->q && stride[0] != stride[1]) return fail(LK_ERR_ARG, "%s: q in place needs equal strides", what);
+  r.q = static_cast<const uint16_t*>(c->q);
+  r.q_out = static_cast<uint16_t*>(q_out);
+  r.q_stride = stride[0];
+  r.q_out_stride = stride[1];
+  return LK_OK;
+}
+
+lk_status lk_append_rope(lk_cache cache, int32_t layer, lk_rope rope, const lk_chunk* chunk, const int32_t* positions,
+                         void* q_out, int64_t q_out_stride, void* stream) {
+  ChunkArgs a;
+  RopeChunk r;
+  int64_t need[kNumPools];
+  lk_status st =
+      append_rope_prepare(cache, layer, rope, chunk, positions, q_out, q_out_stride, "lk_append_rope", a, r, need);
+  if (st != LK_OK || a.n_max == 0) return st;
+  return chunk_append_run(cache, chunk, a, &r, need, "lk_append_rope", static_cast<cudaStream_t>(stream));
+}
+
+lk_status lk_step_rope(lk_cache cache, int32_t layer, lk_rope rope, const lk_chunk* chunk, const int32_t* positions,
+                       float* o, void* workspace, size_t ws_bytes, void* stream) {
+  if (!cache || !chunk) return fail(LK_ERR_ARG, "lk_step_rope: null cache or chunk");
+  if (chunk->n_max != 1 || chunk->lens)
+    return fail(LK_ERR_ARG, "lk_step_rope: a step takes one token of every sequence (n_max 1, no lens)");
+  if (!chunk->q) return fail(LK_ERR_ARG, "lk_step_rope: null q");
+  // the turned queries wait in the workspace, where the steps from host memory stage theirs
+  uint8_t* q = static_cast<uint8_t*>(workspace);
+  if (q) q += ws_layout(cache->plan.d, cache->B).off_q;
+  DecodeArgs d;
+  int ctas = 0;
+  lk_status st = decode_prepare(cache, layer, 1, q, o, workspace, ws_bytes, "lk_step_rope", d, ctas);
+  ChunkArgs a;
+  RopeChunk r;
+  int64_t need[kNumPools];
+  if (st == LK_OK) st = append_rope_prepare(cache, layer, rope, chunk, positions, q, 0, "lk_step_rope", a, r, need);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (st == LK_OK) st = chunk_append_run(cache, chunk, a, &r, need, "lk_step_rope", s);
+  if (st != LK_OK) return st;
+  cudaError_t err = run_decode(cache, d, ctas, s);
+  if (err != cudaSuccess) return cuda_fail(err, "lk_step_rope launch");
+  return LK_OK;
+}
+
 lk_status lk_cache_length(lk_cache cache, int32_t layer, int32_t* n) {
   if (!cache || !n) return fail(LK_ERR_ARG, "lk_cache_length: null argument");
   if (layer < 0 || layer >= cache->cv.L) return fail(LK_ERR_ARG, "lk_cache_length: layer %d out of range", layer);
@@ -1689,7 +1795,7 @@ lk_status lk_cache_block(lk_cache cache, int32_t layer, int32_t b, int32_t kv_he
                          float* k_scales, int8_t* v_codes, float* v_scales, void* stream) {
   if (!cache) return fail(LK_ERR_ARG, "lk_cache_block: null cache");
   if (!kv_quantized(cache->lay.kv_format))
-    return fail(LK_ERR_STATE, "lk_cache_block: the cache is not INT8 or FP8");
+    return fail(LK_ERR_STATE, "lk_cache_block: the cache is not INT8, FP8 or FP8_BLOCK");
   if (layer < 0 || layer >= cache->cv.L || b < 0 || b >= cache->B || kv_head < 0 || kv_head >= cache->cv.Hkv)
     return fail(LK_ERR_ARG, "lk_cache_block: (layer %d, b %d, kv_head %d) out of range", layer, b, kv_head);
   const HeadDesc& hd = cache->lay.heads[(size_t)layer * cache->cv.Hkv + kv_head];
@@ -1699,7 +1805,7 @@ lk_status lk_cache_block(lk_cache cache, int32_t layer, int32_t b, int32_t kv_he
   if (block < 0 || block >= sealed)
     return fail(LK_ERR_ARG, "lk_cache_block: block %d not in [0, %d) sealed blocks", block, sealed);
   const int k = hd.n_kept;
-  const int qb = qblock_bytes(k);
+  const int qb = sealed_bytes(cache->lay.kv_format, k);
   cudaError_t err = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   int64_t at = 0;
   if (cache->paged()) {
@@ -1715,6 +1821,17 @@ lk_status lk_cache_block(lk_cache cache, int32_t layer, int32_t b, int32_t kv_he
   std::vector<uint8_t> img(qb);
   if (err == cudaSuccess) err = cudaMemcpy(img.data(), cache->cv.qpool + at, qb, cudaMemcpyDeviceToHost);
   if (err != cudaSuccess) return cuda_fail(err, "lk_cache_block");
+  if (cache->lay.kv_format == kKvFp8Block) {
+    const float* scales = reinterpret_cast<const float*>(img.data() + block_soff(k));
+    for (int r = 0; r < kQBlockRows; ++r) {
+      for (int c = 0; k_codes && c < k; ++c) k_codes[r * k + c] = (int8_t)img[block_kbyte(k, r, c)];
+      for (int c = 0; v_codes && c < kHeadDim; ++c)
+        v_codes[r * kHeadDim + c] = (int8_t)img[block_voff(k) + block_vbyte(r, c)];
+    }
+    if (k_scales) std::fill(k_scales, k_scales + k, scales[0]);
+    if (v_scales) std::fill(v_scales, v_scales + kQBlockRows, scales[1]);
+    return LK_OK;
+  }
   for (int r = 0; r < kQBlockRows; ++r) {
     if (k_codes)
       for (int c = 0; c < k; ++c) k_codes[r * k + c] = (int8_t)img[(size_t)r * k + qbyte(k, r, c)];
@@ -1843,7 +1960,7 @@ lk_status lk_decode_attn_static(lk_cache cache, int32_t layer, const void* q, fl
   set_divisors(cache, a);
   int ctas = cache->decode_ctas > 0 ? cache->decode_ctas : default_decode_ctas(cache, 1);
   ctas = std::max(1, std::min(ctas, kMaxCtas));
-  err = launch_decode(cache->maps, a, ctas, s);
+  err = run_decode(cache, a, ctas, s);
   if (err != cudaSuccess) return cuda_fail(err, "lk_decode_attn_static launch");
   return LK_OK;
 }

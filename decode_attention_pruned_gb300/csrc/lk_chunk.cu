@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "lk_append.cuh"
+#include "lk_block.h"
 #include "lk_device.cuh"
 #include "lk_internal.h"
 #include "lk_kernels.h"
@@ -645,6 +646,10 @@ constexpr int kScaleExp = 6, kRowTop = 14;
 // and below 2^15 when m lags by 8 (the sums l and the outputs before are in units of
 // 2^m too, and follow).  Only weights 2^-20 of the largest keep fewer bits.
 constexpr int kWeightExp = 6;
+// FP8_BLOCK: keys are their codes too, exact in f16, and their block's scale is the
+// factor that the softmax moves the scores back by.  The values' scale s, one for the
+// block, goes into the weights' exponents, 2^(s' - m + log2 s), and comes out of their
+// sum l again, so that no weight is multiplied by it.
 
 // The keys or the values of a sealed block, to be turned into a tile.  (Not
 // both at once: the ring may have room for the values only when the tile
@@ -783,6 +788,67 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       const Job job = *reinterpret_cast<const Job*>(sm + L::kJob + jn * L::kJobBytes);
       if (job.width == 0) break;
       uint8_t* to = sm + job.at;
+      if constexpr (kFmt == kKvFp8Block) {
+        // A warp takes whole slabs of 16 rows: where the codes lie in the tile's second
+        // half, a slab's are where its own rows' channels 64 on go.
+        if (mt == 0) {
+          const float scale = reinterpret_cast<const float*>(sm + job.scales)[job.values];
+          if (job.values == 0) *reinterpret_cast<float*>(sm + L::kTileBack + 4 * (ri * L::kSlots + job.slot)) = scale;
+          else *reinterpret_cast<float*>(sm + L::kValueLog + (job.scales - L::kVScale) / kTile) = log2f(scale);
+        }
+        const uint8_t* codes = to + kTile * job.width * (job.width == kHeadDim ? 1 : 2);
+        const int g = lane >> 2, t = lane & 3;
+        auto pair_f16 = [](uint32_t w, uint32_t& lo, uint32_t& hi) {
+          asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+              "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+              : "=r"(lo), "=r"(hi)
+              : "r"(w));
+        };
+        auto mix = [](uint32_t a, uint32_t b, uint32_t sel) {
+          uint32_t d;
+          asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+          return d;
+        };
+#pragma unroll 1
+        for (int slab = mt >> 5; slab < kSlabs; slab += L::kMakers) {
+          const uint4* from = reinterpret_cast<const uint4*>(codes + slab * kSlabRows * job.width) + lane;
+          const int units = job.width / 32, row = slab * kSlabRows;
+          uint4 w[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (u < units) w[u] = from[32 * u];
+          __syncwarp();
+          if (job.values == 0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (u >= units) continue;
+              uint4 x, y;
+              pair_f16(w[u].x, x.x, x.y);
+              pair_f16(w[u].y, x.z, x.w);
+              pair_f16(w[u].z, y.x, y.y);
+              pair_f16(w[u].w, y.z, y.w);
+              *reinterpret_cast<uint4*>(to + kept_byte(job.width, row + g, 4 * u + t)) = x;
+              *reinterpret_cast<uint4*>(to + kept_byte(job.width, row + g + 8, 4 * u + t)) = y;
+            }
+          } else {
+            // channels 8 g .. + 7 of four rows, and 64 on: rows two by two
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+              for (int two = 0; two < 2; ++two) {
+                uint32_t x[4], y[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  pair_f16(mix(half ? w[u].y : w[u].x, half ? w[u].w : w[u].z, two ? 0x7362u : 0x5140u), x[u], y[u]);
+                const int r = row + 2 * t + 8 * two;
+                *reinterpret_cast<uint4*>(to + kept_byte(kHeadDim, r, 8 * half + g)) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4*>(to + kept_byte(kHeadDim, r + 1, 8 * half + g)) =
+                    make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            }
+          }
+        }
+      } else {
       // the block's largest scale (they are not negative: they order as their bits do)
       uint32_t top = 0;
       for (int x = lane; x < job.width; x += 32)
@@ -852,6 +918,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       else if (job.width == 64) convert(std::integral_constant<int, 64>(), std::false_type());
       else if (job.width == 96) convert(std::integral_constant<int, 96>(), std::false_type());
       else convert(std::integral_constant<int, 128>(), std::false_type());
+      }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -961,16 +1028,20 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
                   !wait(base + L::kDone + 8 * (ri * L::kJobs + jn), (jobs / L::kJobs - 1) & 1)) return false;
               const uint8_t* block = cv.qpool + hd.qoff +
                                      (pages != nullptr ? (int64_t)max(0, pg)
-                                                       : (int64_t)it.b * hd.qblocks + t.r0 / kTile) * qblock_bytes(it.k);
+                                                       : (int64_t)it.b * hd.qblocks + t.r0 / kTile) *
+                                         sealed_bytes(kFmt, it.k);
               const int width = isv ? kHeadDim : it.k, vn = (int)(sealed & 3);
-              const uint32_t codes = (uint32_t)(kTile * width), scales = isv ? kTile * 4u : (uint32_t)(4 * it.k);
+              constexpr bool kBlock = kFmt == kKvFp8Block;
+              const uint32_t codes = (uint32_t)(kTile * width),
+                             scales = kBlock ? 16u : isv ? kTile * 4u : (uint32_t)(4 * it.k);
               const uint32_t sc =
                   isv ? L::kVScale + (4 * ri + vn) * kTile * 4 : L::kKScale + (ri * L::kJobs + jn) * kTile * 4;
               *reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes) =
                   Job{width, isv ? 1 : 0, slot, dst - base, sc};
               mbar_arrive_expect_tx(landed, codes + scales);
               bulk_load(dst + (wide ? 1 : 2) * codes, block + (isv ? qblock_voff(it.k) : 0), codes, landed, keep);
-              bulk_load(base + sc, block + (isv ? qblock_vsoff(it.k) : qblock_ksoff(it.k)), scales, landed, keep);
+              bulk_load(base + sc, block + (kBlock ? block_soff(it.k) : isv ? qblock_vsoff(it.k) : qblock_ksoff(it.k)),
+                        scales, landed, keep);
               sealed += isv ? 1 : 0;
               ++jobs;
               return true;
@@ -1339,6 +1410,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         // scores' factor (made before the values, by the same warps)
         const float* vscale = nullptr;
         float score_scale = kScaleLog2, value_log = 0.f;
+        float weight_log = 0.f, weight_back = 1.f;       // FP8_BLOCK: log2 of the values' scale, and its inverse
         if (kQuant && j >= m0) {
           const uint32_t e = entries + 2 * ((j - s.t0) / (kDual ? 1 : 2)) + 1;
           const uint32_t slot = e % L::kSlots + (kDual ? 0 : st * L::kSlots);
@@ -1347,6 +1419,11 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           const int v_at = (kDual ? 0 : 4 * st) + (int)(sealed++ & 3);
           vscale = reinterpret_cast<const float*>(sm + L::kVScale) + v_at * kTile;
           value_log = *reinterpret_cast<const volatile float*>(sm + L::kValueLog + 4 * v_at);
+          if (kFmt == kKvFp8Block) {
+            weight_log = value_log;
+            weight_back = ex2(-weight_log);
+            value_log -= kWeightExp;
+          }
           if (!scaled) {
             ok = wait.warp(base + L::kQKFull + (kDual ? 8 * st : 0), (gathered - 1) & 1);
             if (!ok) break;
@@ -1425,7 +1502,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           // lower one, gives 1.66e-3, and takes 120 us instead of 100 for 64 sequences of
           // 4096 tokens (4 queries each), 1117 instead of 871 for 1000 queries over 131072.
           // (Sealed blocks' weights are f16: see kWeightExp.)
-          const float off = m == -INFINITY ? 0.f : -m;
+          const float off = m == -INFINITY ? 0.f : weight_log - m;
           const float sc = kQuant ? score_scale : kScaleLog2;
           const uint64_t scale2 = pair(sc, sc), off2 = pair(off, off);
           uint64_t sum[4] = {0, 0, 0, 0};
@@ -1444,7 +1521,11 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             }
           }
           if (kQuant) {
-            if (vscale != nullptr) {
+            if (kFmt == kKvFp8Block && vscale != nullptr) {
+#pragma unroll
+              for (int c = 0; c < kHalf; c += 2)
+                x[c >> 1] = pack_f16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+            } else if (vscale != nullptr) {
               const ulonglong2* f = reinterpret_cast<const ulonglong2*>(vscale + half * kHalf);
               auto times = [&](int c, uint64_t y) {
                 float p0, p1;
@@ -1466,7 +1547,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           tmem_st32(s_half, x);
           float l0, l1;
           unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
-          l += l0 + l1;
+          l = kFmt == kKvFp8Block ? fmaf(l0 + l1, weight_back, l) : l + (l0 + l1);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -1703,6 +1784,7 @@ cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, cons
   if (err != cudaSuccess) return err;
   err = args.cv.kv_format == kKvInt8  ? launch_attn<kKvInt8>(maps, args, w, stream)
         : args.cv.kv_format == kKvFp8 ? launch_attn<kKvFp8>(maps, args, w, stream)
+        : args.cv.kv_format == kKvFp8Block ? launch_attn<kKvFp8Block>(maps, args, w, stream)
                                       : launch_attn<kKvBf16>(maps, args, w, stream);
   if (err != cudaSuccess || w.max_ctas < 2) return err;
   // (at most max_ctas - 1 items are cut, in runs of 8 or 32 rows)

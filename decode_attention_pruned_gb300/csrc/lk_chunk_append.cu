@@ -22,16 +22,24 @@
 // (paged 9), launch and dependency more than bytes (8 MB).  A warp per row, 8
 // bytes a lane, keeps every access a whole row, and the one launch advances the
 // lengths too.
-// INT8 / FP8: the sealing.  One warp seals a whole block, as the single append
-// does, with gathers of two bytes, so a chunk that completes a block of each head
-// takes 180 us and more (512 tokens of 8 heads, 4 blocks each: 305); one that
-// completes none, as most verified drafts do, 10 to 16.
+// INT8 / FP8 / FP8_BLOCK: the sealing, a thread block to each (sequence, head,
+// 128-row block).
+//
+// With a rotation the chunk's keys are turned by their tokens' positions wherever
+// they are read: by the sealing, by the special rows' copies, and before they are
+// laid into the cache, where a block takes a run of tokens, computes each (token,
+// pair)'s cosine and sine once, turns the queries straight from input to output and
+// the keys into shared memory, from which the copies go as they do without a
+// rotation.  Keys are rounded to bf16 once, so that the cache is left as if they had
+// been turned before.
 #include <cuda_runtime.h>
 
 #include "lk_append.cuh"
 #include "lk_device.cuh"
 #include "lk_internal.h"
 #include "lk_kernels.h"
+#include "lk_rope.cuh"
+#include "lk_seal.cuh"
 
 namespace lk {
 namespace {
@@ -76,19 +84,25 @@ __global__ void __launch_bounds__(256) chunk_pages_kernel(const __grid_constant_
   pop_pages(cv, hd, last - first, page_row(cv, a.layer, a.b0 + i, h) + first);
 }
 
-// INT8 / FP8 caches: a warp per (sequence, head, block that the chunk
+// Position of the chunk's token i of sequence b, which holds N before it, on an axis.
+__device__ __forceinline__ int chunk_position(const RopeChunk& r, int64_t n_max, int b, int i, int N, int axis) {
+  return r.positions != nullptr ? __ldg(r.positions + axis * r.axis_stride + b * n_max + i) : N + i;
+}
+
+// Quantised caches: a thread block per (sequence, head, block that the chunk
 // completes) seals it.  Row r of block j is the token at t = S + 128 j + r:
 // in the tail if it has left the window already, in its ring row if it is
 // still held there, else in the chunk.
-__global__ void __launch_bounds__(256) chunk_seal_kernel(const __grid_constant__ ChunkArgs a, int max_blocks) {
+constexpr int kSealThreads = 256;
+template <bool kRope>
+__global__ void __launch_bounds__(kSealThreads)
+    chunk_seal_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ RopeChunk rc, int max_blocks) {
+  __shared__ SealSmem sm;
   grid_dependency_wait();
   grid_launch_dependents();
   const CacheView& cv = a.cv;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (w >= (int64_t)a.nb * cv.Hkv * max_blocks) return;
-  const int i = (int)(w / ((int64_t)max_blocks * cv.Hkv));
-  const int h = (int)((w / max_blocks) % cv.Hkv);
+  const int x = blockIdx.x;
+  const int i = x / max_blocks / cv.Hkv, h = x / max_blocks % cv.Hkv;
   const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + h];
   if (hd.policy != kFull || hd.n_kept == 0) return;
   int N;
@@ -96,34 +110,46 @@ __global__ void __launch_bounds__(256) chunk_seal_kernel(const __grid_constant__
   if (n == 0) return;
   const int b = a.b0 + i;
   const int m0 = max(0, N - cv.S - cv.W);
-  const int j = m0 / kQBlockRows + (int)(w % max_blocks);
+  const int j = m0 / kQBlockRows + x % max_blocks;
   if (j >= pages_at(cv, N + n)) return;
-  uint8_t* dst = qblock_addr(cv, hd, a.layer, b, h, j);
+  uint8_t* dst = sealed_addr(cv, hd, a.layer, b, h, j);
   if (dst == nullptr) return;
   const int k = hd.n_kept;
-  const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim;
   const uint16_t* kt = cv.pool[hd.pool_kb] + (hd.krow_b + (int64_t)b * hd.cap_b) * k;
   const uint16_t* vt = cv.pool[kPoolV] + (hd.vrow_b + (int64_t)b * hd.cap_b) * kHeadDim;
   const int64_t ring = hd.row_a + (int64_t)b * hd.cap_a + cv.S;
-  seal_block(
-      dst, k, cv.kv_format,
-      [&](int r, int c) {
-        const int mid = kQBlockRows * j + r, t = cv.S + mid;
-        if (mid < m0) return kt[(size_t)r * k + c];
-        return t < N ? cv.pool[kPoolK128][(ring + mid % cv.W) * kHeadDim + kept[c]] : k_token(a, b, t - N, h)[kept[c]];
-      },
-      [&](int r, int c) {
-        const int mid = kQBlockRows * j + r, t = cv.S + mid;
-        if (mid < m0) return vt[(size_t)r * kHeadDim + c];
-        return t < N ? cv.pool[kPoolV][(ring + mid % cv.W) * kHeadDim + c] : v_token(a, b, t - N, h)[c];
-      },
-      lane);
+  const RopeShare share(rc.rope, threadIdx.x & 7);
+  auto where = [&](int slot, int& c0, int& c1) {
+    c0 = kRope ? share.c0 : 16 * slot;
+    c1 = kRope ? share.c1 : 16 * slot + 8;
+  };
+  auto load = [&](int r, int slot, bool is_v, uint4& u, uint4& v) {
+    const int mid = kQBlockRows * j + r, t = cv.S + mid;
+    const bool turned = kRope && !is_v && t >= N && mid >= m0;
+    const uint16_t* row;
+    int c0 = 16 * slot, c1 = c0 + 8;
+    if (mid < m0) {
+      row = is_v ? vt + (size_t)r * kHeadDim : kt + (size_t)r * k;
+    } else {
+      if (!is_v) where(slot, c0, c1);
+      row = t < N ? (is_v ? cv.pool[kPoolV] : cv.pool[kPoolK128]) + (ring + mid % cv.W) * kHeadDim
+                  : is_v ? v_token(a, b, t - N, h) : k_token(a, b, t - N, h);
+    }
+    u = *reinterpret_cast<const uint4*>(row + c0);
+    v = *reinterpret_cast<const uint4*>(row + c1);
+    if (turned)
+      share.apply(rc.rope, [&](int axis) { return chunk_position(rc, a.n_max, b, t - N, N, axis); }, u, v);
+  };
+  seal_by_block<kSealThreads>(sm, dst, k, cv.kv_format, cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim,
+                              min(max(m0 - kQBlockRows * j, 0), kQBlockRows), load, where);
 }
 
 // Special tokens of the chunk: one block per sequence ranks them in position
 // order (ballot and warp scan per 1024 tokens), copies them to rows count,
 // count + 1, ... of the SPECIAL heads and advances the count.
-__global__ void __launch_bounds__(1024) chunk_special_kernel(const __grid_constant__ ChunkArgs a) {
+template <bool kRope>
+__global__ void __launch_bounds__(1024)
+    chunk_special_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ RopeChunk rc) {
   grid_dependency_wait();
   grid_launch_dependents();
   const CacheView& cv = a.cv;
@@ -173,7 +199,17 @@ __global__ void __launch_bounds__(1024) chunk_special_kernel(const __grid_consta
         continue;
       }
       const int64_t row = hd.row_a + (int64_t)b * hd.cap_a + r;
-      row8(cv.pool[kPoolK128], row)[lane] = reinterpret_cast<const uint2*>(k_token(a, b, s_tok[j], h))[lane];
+      const uint16_t* k_src = k_token(a, b, s_tok[j], h);
+      if (!kRope) {
+        row8(cv.pool[kPoolK128], row)[lane] = reinterpret_cast<const uint2*>(k_src)[lane];
+      } else if (lane < kRopeSlots) {
+        const RopeShare share(rc.rope, lane);
+        uint4 u = *reinterpret_cast<const uint4*>(k_src + share.c0), v = *reinterpret_cast<const uint4*>(k_src + share.c1);
+        share.apply(rc.rope, [&](int axis) { return chunk_position(rc, a.n_max, b, s_tok[j], N, axis); }, u, v);
+        uint16_t* to = cv.pool[kPoolK128] + row * kHeadDim;
+        *reinterpret_cast<uint4*>(to + share.c0) = u;
+        *reinterpret_cast<uint4*>(to + share.c1) = v;
+      }
       row8(cv.pool[kPoolV], row)[lane] = reinterpret_cast<const uint2*>(v_token(a, b, s_tok[j], h))[lane];
     }
     base += total;
@@ -182,80 +218,69 @@ __global__ void __launch_bounds__(1024) chunk_special_kernel(const __grid_consta
   if (tid == 0) *cnt = min(base, cv.spec_cap);
 }
 
-__global__ void __launch_bounds__(256) chunk_append_kernel(const __grid_constant__ ChunkArgs a) {
-  grid_dependency_wait();
-  grid_launch_dependents();
+// One warp lays token i of sequence b (N tokens held, n new ones) into kv head h,
+// which is not SPECIAL; k_src, v_src: its rows.
+__device__ __forceinline__ void place_row(const ChunkArgs& a, int b, int i, int h, int N, int n, const uint16_t* k_src,
+                                          const uint16_t* v_src, int lane) {
   const CacheView& cv = a.cv;
-  const int lane = threadIdx.x & 31;
-  const int64_t items = (int64_t)a.nb * a.n_max * cv.Hkv;
-  const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
   const bool quant = kv_quantized(cv.kv_format);
-  uint16_t* ka_pool = cv.pool[kPoolK128];
-  uint16_t* va_pool = cv.pool[kPoolV];
-  for (int64_t it = (((int64_t)blockIdx.x * blockDim.x) + threadIdx.x) >> 5; it < items; it += nwarps) {
-    const int h = (int)(it % cv.Hkv);
-    const int64_t bi = it / cv.Hkv;
-    const int i = (int)(bi % a.n_max), seq = (int)(bi / a.n_max);
-    int N;
-    const int n = chunk_len(a, seq, N);
-    if (i >= n) continue;
-    const int b = a.b0 + seq;
-    const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + h];
-    if (hd.policy == kSpecial) continue;
-    const uint16_t* k_src = k_token(a, b, i, h);
-    const uint2 kx = reinterpret_cast<const uint2*>(k_src)[lane];
-    const uint2 vx = reinterpret_cast<const uint2*>(v_token(a, b, i, h))[lane];
-    const int64_t abase = hd.row_a + (int64_t)b * hd.cap_a;
-    const int p = N + i, end = N + n;
-    int arow = -1;
-    if (hd.policy == kLocal) {
-      if (p >= end - cv.W_loc) arow = p % cv.W_loc;
+  const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + h];
+  const uint2 kx = reinterpret_cast<const uint2*>(k_src)[lane];
+  const uint2 vx = reinterpret_cast<const uint2*>(v_src)[lane];
+  const int64_t abase = hd.row_a + (int64_t)b * hd.cap_a;
+  const int p = N + i, end = N + n;
+  int arow = -1;
+  if (hd.policy == kLocal) {
+    if (p >= end - cv.W_loc) arow = p % cv.W_loc;
+  } else {
+    const int m1 = max(0, end - cv.S - cv.W);
+    const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim;
+    int mid = -1;                     // middle row to write, from
+    const uint16_t* mk = k_src;       // this K row
+    uint2 mv = vx;
+    if (p < cv.S) {
+      arow = p;
+    } else if (p >= end - cv.W) {
+      arow = cv.S + (p - cv.S) % cv.W;
+      // the held token of this ring row, if any: the latest one before N
+      const int64_t old = p - (int64_t)cv.W * (((int64_t)i + cv.W) / cv.W);
+      if (old >= cv.S) {
+        mid = (int)(old - cv.S);
+        mk = cv.pool[kPoolK128] + (abase + arow) * kHeadDim;
+        if (hd.n_kept > 0) mv = row8(cv.pool[kPoolV], abase + arow)[lane];
+      }
     } else {
-      const int m1 = max(0, end - cv.S - cv.W);
-      const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim;
-      int mid = -1;                     // middle row to write, from
-      const uint16_t* mk = k_src;       // this K row
-      uint2 mv = vx;
-      if (p < cv.S) {
-        arow = p;
-      } else if (p >= end - cv.W) {
-        arow = cv.S + (p - cv.S) % cv.W;
-        // the held token of this ring row, if any: the latest one before N
-        const int64_t old = p - (int64_t)cv.W * (((int64_t)i + cv.W) / cv.W);
-        if (old >= cv.S) {
-          mid = (int)(old - cv.S);
-          mk = ka_pool + (abase + arow) * kHeadDim;
-          if (hd.n_kept > 0) mv = row8(va_pool, abase + arow)[lane];
-        }
-      } else {
-        mid = p - cv.S;
-      }
-      // INT8 / FP8: rows of complete blocks are sealed already
-      if (mid >= 0 && hd.n_kept > 0 && !(quant && mid < m1 / kQBlockRows * kQBlockRows)) {
-        const int32_t page = cv.max_pages > 0 && !quant ? __ldcg(&page_row(cv, a.layer, b, h)[mid / kPageRows]) : -1;
-        int64_t krow, vrow;
-        if (middle_rows(cv, hd, b, mid, page, krow, vrow)) write_middle(cv, hd, kept, krow, vrow, mk, mv, lane);
-      }
-      __syncwarp();
-      // the open block of a quantised head restarts: rows not yet taken are zero
-      if (quant && i == 0 && hd.n_kept > 0 && hd.cap_b > 0 &&
-          m1 / kQBlockRows > max(0, N - cv.S - cv.W) / kQBlockRows) {
-        const int r0 = m1 % kQBlockRows, nr = hd.cap_b - r0, k = hd.n_kept;
-        uint4* kz = reinterpret_cast<uint4*>(cv.pool[hd.pool_kb] + (hd.krow_b + (int64_t)b * hd.cap_b + r0) * k);
-        uint4* vz = reinterpret_cast<uint4*>(va_pool + (hd.vrow_b + (int64_t)b * hd.cap_b + r0) * kHeadDim);
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        for (int x = lane; x < nr * k / 8; x += 32) kz[x] = zero;
-        for (int x = lane; x < nr * kHeadDim / 8; x += 32) vz[x] = zero;
-      }
+      mid = p - cv.S;
     }
-    if (arow >= 0) {
-      row8(ka_pool, abase + arow)[lane] = kx;
-      row8(va_pool, abase + arow)[lane] = vx;
+    // INT8 / FP8: rows of complete blocks are sealed already
+    if (mid >= 0 && hd.n_kept > 0 && !(quant && mid < m1 / kQBlockRows * kQBlockRows)) {
+      const int32_t page = cv.max_pages > 0 && !quant ? __ldcg(&page_row(cv, a.layer, b, h)[mid / kPageRows]) : -1;
+      int64_t krow, vrow;
+      if (middle_rows(cv, hd, b, mid, page, krow, vrow)) write_middle(cv, hd, kept, krow, vrow, mk, mv, lane);
+    }
+    __syncwarp();
+    // the open block of a quantised head restarts: rows not yet taken are zero
+    if (quant && i == 0 && hd.n_kept > 0 && hd.cap_b > 0 &&
+        m1 / kQBlockRows > max(0, N - cv.S - cv.W) / kQBlockRows) {
+      const int r0 = m1 % kQBlockRows, nr = hd.cap_b - r0, k = hd.n_kept;
+      uint4* kz = reinterpret_cast<uint4*>(cv.pool[hd.pool_kb] + (hd.krow_b + (int64_t)b * hd.cap_b + r0) * k);
+      uint4* vz = reinterpret_cast<uint4*>(cv.pool[kPoolV] + (hd.vrow_b + (int64_t)b * hd.cap_b + r0) * kHeadDim);
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      for (int x = lane; x < nr * k / 8; x += 32) kz[x] = zero;
+      for (int x = lane; x < nr * kHeadDim / 8; x += 32) vz[x] = zero;
     }
   }
-  // The lengths advance once no block reads them any more: by the last one to
-  // get here (the layer's word counts them, and is left at zero; appends to
-  // different layers may overlap).
+  if (arow >= 0) {
+    row8(cv.pool[kPoolK128], abase + arow)[lane] = kx;
+    row8(cv.pool[kPoolV], abase + arow)[lane] = vx;
+  }
+}
+
+// The lengths advance once no block reads them any more: by the last one to
+// get here (the layer's word counts them, and is left at zero; appends to
+// different layers may overlap).
+__device__ void advance_lengths(const ChunkArgs& a) {
+  const CacheView& cv = a.cv;
   __shared__ int s_last;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -271,22 +296,120 @@ __global__ void __launch_bounds__(256) chunk_append_kernel(const __grid_constant
   }
 }
 
+__global__ void __launch_bounds__(256) chunk_append_kernel(const __grid_constant__ ChunkArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const CacheView& cv = a.cv;
+  const int lane = threadIdx.x & 31;
+  const int64_t items = (int64_t)a.nb * a.n_max * cv.Hkv;
+  const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  for (int64_t it = (((int64_t)blockIdx.x * blockDim.x) + threadIdx.x) >> 5; it < items; it += nwarps) {
+    const int h = (int)(it % cv.Hkv);
+    const int64_t bi = it / cv.Hkv;
+    const int i = (int)(bi % a.n_max), seq = (int)(bi / a.n_max);
+    int N;
+    const int n = chunk_len(a, seq, N);
+    if (i >= n) continue;
+    const int b = a.b0 + seq;
+    if (cv.heads[a.layer * cv.Hkv + h].policy == kSpecial) continue;
+    place_row(a, b, i, h, N, n, k_token(a, b, i, h), v_token(a, b, i, h), lane);
+  }
+  advance_lengths(a);
+}
+
+// With a rotation: a block takes runs of kTokens tokens of a sequence, one after
+// another.  32 rows of 8 threads each are turned at once, 16 channels to a thread.
+constexpr int kRopeRows = 256 / kRopeSlots;
+template <int kTokens>
+__global__ void __launch_bounds__(256)
+    chunk_rope_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ RopeChunk rc) {
+  __shared__ float4 turn[kTokens][kHeadDim / 4];           // (cosine, sine) of two pairs each
+  __shared__ uint4 s_k[kRopeRows][kHeadDim / 8];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const CacheView& cv = a.cv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const RopeShare share(rc.rope, tid % kRopeSlots);
+  const int row = tid / kRopeSlots;
+  const int runs = (a.n_max + kTokens - 1) / kTokens, pairs = rc.rope.rotary_dim / 2;
+  for (int64_t run = blockIdx.x; run < (int64_t)a.nb * runs; run += gridDim.x) {
+    const int seq = (int)(run / runs), i0 = (int)(run - (int64_t)seq * runs) * kTokens, b = a.b0 + seq;
+    int N;
+    const int n = chunk_len(a, seq, N);
+    const int nt = min(kTokens, n - i0);
+    if (nt <= 0) continue;
+    for (int y = tid; y < nt * pairs; y += 256) {
+      const int t = y / pairs, i = y - t * pairs;
+      auto pos = [&](int axis) { return chunk_position(rc, a.n_max, b, i0 + t, N, axis); };
+      reinterpret_cast<float2*>(turn[t])[i] =
+          rc.rope.axes > 1 ? rope_turn<true>(rc.rope, i, pos) : rope_turn<false>(rc.rope, i, pos);
+    }
+    __syncthreads();
+    if (rc.q != nullptr) {
+      for (int x = row; x < nt * cv.Hq; x += kRopeRows) {
+        const int t = x / cv.Hq, h = x - t * cv.Hq;
+        const int64_t token = (int64_t)b * a.n_max + i0 + t;
+        const uint16_t* src = rc.q + token * rc.q_stride + h * kHeadDim;
+        uint16_t* dst = rc.q_out + token * rc.q_out_stride + h * kHeadDim;
+        uint4 u = *reinterpret_cast<const uint4*>(src + share.c0), v = *reinterpret_cast<const uint4*>(src + share.c1);
+        share.apply(turn[t], u, v);
+        *reinterpret_cast<uint4*>(dst + share.c0) = u;
+        *reinterpret_cast<uint4*>(dst + share.c1) = v;
+      }
+    }
+    for (int x0 = 0; x0 < nt * cv.Hkv; x0 += kRopeRows) {
+      const int x = x0 + row;
+      if (x < nt * cv.Hkv) {
+        const int t = x / cv.Hkv, h = x - t * cv.Hkv;
+        const uint16_t* src = k_token(a, b, i0 + t, h);
+        uint4 u = *reinterpret_cast<const uint4*>(src + share.c0), v = *reinterpret_cast<const uint4*>(src + share.c1);
+        share.apply(turn[t], u, v);
+        s_k[row][share.c0 / 8] = u;
+        s_k[row][share.c1 / 8] = v;
+      }
+      __syncthreads();
+      for (int y = x0 + warp; y < min(nt * cv.Hkv, x0 + kRopeRows); y += 8) {
+        const int t = y / cv.Hkv, h = y - t * cv.Hkv;
+        if (cv.heads[a.layer * cv.Hkv + h].policy == kSpecial) continue;
+        place_row(a, b, i0 + t, h, N, n, reinterpret_cast<const uint16_t*>(s_k[y - x0]), v_token(a, b, i0 + t, h),
+                  lane);
+      }
+      __syncthreads();
+    }
+  }
+  advance_lengths(a);
+}
+
 }  // namespace
 
-cudaError_t launch_chunk_append(const ChunkArgs& args, bool has_middle, int num_sms, cudaStream_t stream) {
+cudaError_t launch_chunk_append(const ChunkArgs& args, const RopeChunk* rope, bool has_middle, int num_sms,
+                                cudaStream_t stream) {
   const CacheView& cv = args.cv;
+  const RopeChunk none = {};
+  const RopeChunk& rc = rope != nullptr ? *rope : none;
+  // a chunk of n tokens completes at most this many blocks of a head
+  const int max_blocks = (args.n_max + kQBlockRows - 1) / kQBlockRows;
+  const int64_t seals = (int64_t)args.nb * cv.Hkv * max_blocks;
+  if (seals > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaError_t err = cudaSuccess;
   if (has_middle && cv.max_pages > 0)
     err = launch_after(chunk_pages_kernel, dim3((unsigned)(args.nb * cv.Hkv + 255) / 256), 256, 0, stream, args);
-  if (err == cudaSuccess && has_middle && kv_quantized(cv.kv_format)) {
-    // a chunk of n tokens completes at most this many blocks of a head
-    const int max_blocks = (args.n_max + kQBlockRows - 1) / kQBlockRows;
-    const int64_t warps = (int64_t)args.nb * cv.Hkv * max_blocks;
-    err = launch_after(chunk_seal_kernel, dim3((unsigned)((warps + 7) / 8)), 256, 0, stream, args, max_blocks);
-  }
+  if (err == cudaSuccess && has_middle && kv_quantized(cv.kv_format))
+    err = launch_after(rope != nullptr ? chunk_seal_kernel<true> : chunk_seal_kernel<false>, dim3((unsigned)seals),
+                       kSealThreads, 0, stream, args, rc, max_blocks);
   if (err == cudaSuccess && args.ids != nullptr)
-    err = launch_after(chunk_special_kernel, dim3((unsigned)args.nb), 1024, 0, stream, args);
+    err = launch_after(rope != nullptr ? chunk_special_kernel<true> : chunk_special_kernel<false>,
+                       dim3((unsigned)args.nb), 1024, 0, stream, args, rc);
   if (err != cudaSuccess) return err;
+  if (rope != nullptr) {
+    const int64_t tokens = (int64_t)args.nb * args.n_max;
+    // four tokens a block once that leaves every SM four blocks, else one
+    if (tokens >= 16 * (int64_t)num_sms) {
+      const int64_t blocks = min((int64_t)args.nb * ((args.n_max + 3) / 4), (int64_t)num_sms * 16);
+      return launch_after(chunk_rope_kernel<4>, dim3((unsigned)blocks), 256, 0, stream, args, rc);
+    }
+    return launch_after(chunk_rope_kernel<1>, dim3((unsigned)tokens), 256, 0, stream, args, rc);
+  }
   const int64_t items = (int64_t)args.nb * args.n_max * cv.Hkv;
   const int64_t blocks = min((items + 7) / 8, (int64_t)num_sms * 16);
   return launch_after(chunk_append_kernel, dim3((unsigned)blocks), 256, 0, stream, args);

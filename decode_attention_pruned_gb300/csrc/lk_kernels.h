@@ -107,6 +107,42 @@ struct ChunkArgs {
   int32_t lens[kChunkSeqs]; // new tokens of sequence b0 + i
 };
 
+enum RopeLayout : int32_t { kRopeHalf = 0, kRopeInterleaved = 1 };
+// What a rope turns, and by how much per position.
+constexpr int kRopeAxes = 4;       // axes at most
+struct RopeTable {
+  int32_t rotary_dim, layout;
+  int32_t axes;                  // axes of a position
+  float magnitude;               // multiplies cosine and sine
+  // turns per position x 2^64; with several axes the pair's axis stands in the
+  // two lowest bits (of 2^-62 turns, far below what w itself is known to)
+  uint64_t freq[kHeadDim / 2];
+};
+// Rotation of a chunk's keys on their way into the cache, and of its queries.
+struct RopeChunk {
+  const int32_t* positions; // [axes][B][n_max], or null: each token's own position in its sequence
+  int64_t axis_stride;      // B n_max
+  const uint16_t* q;        // null: no queries
+  uint16_t* q_out;
+  int64_t q_stride, q_out_stride;
+  RopeTable rope;
+};
+
+// Appends of one token to sequences b0 .. b0 + nb - 1 of layers layer .. layer +
+// nlayers - 1 (grid.y): of every format with a rotation, of FP8_BLOCK without.
+struct TokenArgs {
+  CacheView cv;
+  int32_t layer, nlayers;
+  int32_t b0, nb;
+  const uint16_t* k;        // bf16 [nlayers][B][Hkv][128], sequences k_stride elements apart
+  const uint16_t* v;
+  int64_t k_stride, v_stride, k_layer, v_layer;
+  const int32_t* ids;       // [B] or null
+  int32_t* ticket;          // the first layer's count of blocks done
+  int32_t all;              // every active sequence takes its token, else those of `takes`
+  uint32_t takes[kChunkSeqs / 32];
+};
+
 // Tensor maps of chunk attention: the chunk's tensors, and the flat maps of
 // the cache's pools.
 struct ChunkMaps {
@@ -142,17 +178,6 @@ struct ChunkWork {
   uint8_t* far;
 };
 
-enum RopeLayout : int32_t { kRopeHalf = 0, kRopeInterleaved = 1 };
-// What a rope turns, and by how much per position.
-constexpr int kRopeAxes = 4;       // axes at most
-struct RopeTable {
-  int32_t rotary_dim, layout;
-  int32_t axes;                  // axes of a position
-  float magnitude;               // multiplies cosine and sine
-  // turns per position x 2^64; with several axes the pair's axis stands in the
-  // two lowest bits (of 2^-62 turns, far below what w itself is known to)
-  uint64_t freq[kHeadDim / 2];
-};
 struct RopeArgs {
   const uint16_t* q;        // bf16 [tokens][Hq][128], tokens q_stride elements apart
   const uint16_t* k;
@@ -201,13 +226,17 @@ inline cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads,
 
 size_t decode_smem_bytes();
 cudaError_t launch_decode(const DecodeMaps& maps, const DecodeArgs& args, int ctas, cudaStream_t stream);
+cudaError_t launch_decode_block(const DecodeArgs& args, int ctas, cudaStream_t stream);    // FP8_BLOCK middles
 cudaError_t launch_append(const AppendArgs& args, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& args, bool has_special, int num_sms, cudaStream_t stream);
 cudaError_t launch_release(const CacheView& cv, int b, cudaStream_t stream);
 cudaError_t launch_build_masks(const float* alpha, const uint8_t* eligible, int nh, double pct, int align,
                                int exact, uint8_t* masks, cudaStream_t stream);
 
-cudaError_t launch_chunk_append(const ChunkArgs& args, bool has_middle, int num_sms, cudaStream_t stream);
+// rope: null, or how the chunk's keys turn on their way
+cudaError_t launch_chunk_append(const ChunkArgs& args, const RopeChunk* rope, bool has_middle, int num_sms,
+                                cudaStream_t stream);
+cudaError_t launch_token_append(const TokenArgs& args, const RopeChunk* rope, cudaStream_t stream);
 cudaError_t launch_chunk_attn(const ChunkMaps& maps, const ChunkArgs& args, const ChunkWork& work, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs& args, int num_sms, cudaStream_t stream);
 

@@ -34,9 +34,11 @@
 #include <cuda_runtime.h>
 
 #include "lk_append.cuh"
+#include "lk_block.h"
 #include "lk_device.cuh"
 #include "lk_internal.h"
 #include "lk_kernels.h"
+#include "lk_seal.cuh"
 
 namespace lk {
 namespace {
@@ -179,6 +181,33 @@ __global__ void __launch_bounds__(256) prefill_seal_kernel(const PrefillArgs a, 
       [&](int r, int c) { return vin[r * rs + c]; }, lane);
 }
 
+// FP8_BLOCK caches: a thread block for each of them instead.
+constexpr int kSealThreads = 256;
+__global__ void __launch_bounds__(kSealThreads) prefill_seal_block_kernel(const PrefillArgs a, int max_blocks) {
+  __shared__ SealSmem sm;
+  grid_dependency_wait();
+  const CacheView& cv = a.cv;
+  const int j = blockIdx.x % max_blocks, h = blockIdx.x / max_blocks % cv.Hkv, i = blockIdx.x / max_blocks / cv.Hkv;
+  const int b = a.b0 + i;
+  const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + h];
+  if (hd.policy != kFull || hd.n_kept == 0) return;
+  if (j >= pages_at(cv, __ldcg(&cv.len[a.layer * cv.B + b]))) return;
+  uint8_t* dst = sealed_addr(cv, hd, a.layer, b, h, j);
+  if (dst == nullptr) return;
+  const size_t first = (((size_t)i * a.n + cv.S + j * kQBlockRows) * cv.Hkv + h) * kHeadDim;
+  seal_by_block<kSealThreads>(
+      sm, dst, hd.n_kept, cv.kv_format, cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim, 0,
+      [&](int r, int slot, bool is_v, uint4& u, uint4& v) {
+        const uint16_t* row = (is_v ? a.v : a.k) + first + (size_t)r * cv.Hkv * kHeadDim + 16 * slot;
+        u = reinterpret_cast<const uint4*>(row)[0];
+        v = reinterpret_cast<const uint4*>(row)[1];
+      },
+      [](int slot, int& c0, int& c1) {
+        c0 = 16 * slot;
+        c1 = c0 + 8;
+      });
+}
+
 // Empties slot b in every layer (block = layer): pushes its pages back on
 // their class stacks, clears the page table, lengths and special counts, and
 // marks the slot released.
@@ -303,7 +332,10 @@ cudaError_t launch_prefill(const PrefillArgs& args, bool has_special, int num_sm
     const int max_blocks = max(0, args.n - args.cv.S - args.cv.W) / kQBlockRows;
     const int64_t warps = (int64_t)args.nb * args.cv.Hkv * max_blocks;
     if (warps > 0) {
-      prefill_seal_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(args, max_blocks);
+      if (args.cv.kv_format == kKvFp8Block)
+        prefill_seal_block_kernel<<<(unsigned)warps, kSealThreads, 0, stream>>>(args, max_blocks);
+      else
+        prefill_seal_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(args, max_blocks);
       err = cudaGetLastError();
       if (err != cudaSuccess) return err;
     }

@@ -52,14 +52,8 @@ struct RopeShare {
     c0 = half ? 8 * slot : 16 * slot;
     c1 = half ? 8 * slot + r.rotary_dim / 2 : 16 * slot + 8;
   }
-  // u, v: the two runs; turn: the token's (cosine, sine) of two pairs each
-  __device__ __forceinline__ void apply(const float4* turn, uint4& u, uint4& v) const {
-    if (!turned) return;
-    // eight pairs' cosines and sines
-    const float4* w = turn + 4 * slot;
-    const float4 w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
-    const float2 r[8] = {{w0.x, w0.y}, {w0.z, w0.w}, {w1.x, w1.y}, {w1.z, w1.w},
-                         {w2.x, w2.y}, {w2.z, w2.w}, {w3.x, w3.y}, {w3.z, w3.w}};
+  // u, v: the two runs; r: (cosine, sine) of this share's eight pairs, 8 slot on
+  __device__ __forceinline__ void apply(const float2 (&r)[8], uint4& u, uint4& v) const {
     if (half) {
       turn2(u.x, v.x, r[0], r[1], u.x, v.x);
       turn2(u.y, v.y, r[2], r[3], u.y, v.y);
@@ -69,6 +63,25 @@ struct RopeShare {
       u = make_uint4(turn1(u.x, r[0]), turn1(u.y, r[1]), turn1(u.z, r[2]), turn1(u.w, r[3]));
       v = make_uint4(turn1(v.x, r[4]), turn1(v.y, r[5]), turn1(v.z, r[6]), turn1(v.w, r[7]));
     }
+  }
+  // the same out of a token's table, two pairs to an element
+  __device__ __forceinline__ void apply(const float4* turn, uint4& u, uint4& v) const {
+    if (!turned) return;
+    const float4* w = turn + 4 * slot;
+    const float4 w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
+    const float2 r[8] = {{w0.x, w0.y}, {w0.z, w0.w}, {w1.x, w1.y}, {w1.z, w1.w},
+                         {w2.x, w2.y}, {w2.z, w2.w}, {w3.x, w3.y}, {w3.z, w3.w}};
+    apply(r, u, v);
+  }
+  // the same, computed here
+  template <typename Pos>
+  __device__ __forceinline__ void apply(const RopeTable& table, Pos pos, uint4& u, uint4& v) const {
+    if (!turned) return;
+    float2 r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      r[j] = table.axes > 1 ? rope_turn<true>(table, 8 * slot + j, pos) : rope_turn<false>(table, 8 * slot + j, pos);
+    apply(r, u, v);
   }
 };
 

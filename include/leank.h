@@ -96,7 +96,7 @@ typedef struct lk_region_info {
   int32_t max_pages;          /* entries of the head's page-table row */
   uint64_t page_table_offset; /* int32 [max_pages] */
   int32_t kv_format;          /* lk_kv_format of region B */
-  int32_t sealed_blocks;      /* INT8 / FP8: complete 128-row blocks (read them with
+  int32_t sealed_blocks;      /* quantised: complete 128-row blocks (read them with
                                  lk_cache_block); region B's offsets then give
                                  the bf16 tail: middle row m >= 128 * sealed_blocks
                                  is tail row m - 128 * sealed_blocks */
@@ -116,13 +116,19 @@ typedef struct lk_region_info {
  *               formats of the white paper's 5.2.1): OCP e4m3 (largest
  *               finite value 448), scale = max|x| / 448 (fp32), code = x /
  *               scale rounded to the nearest e4m3 value, ties to the even
- *               code, saturated at +-448; a zero code keeps the sign. */
-typedef enum { LK_KV_BF16 = 0, LK_KV_INT8 = 1, LK_KV_FP8 = 2 } lk_kv_format;
+ *               code, saturated at +-448; a zero code keeps the sign.
+ *   LK_KV_FP8_BLOCK  as LK_KV_FP8 with two scales for a whole block: the
+ *               largest |x| of the block's 128 tokens and kept K channels gives
+ *               one, of its V rows the other, scale = max(max|x| / 448, 2^-64)
+ *               (fp32).  Attention reads these blocks faster, and e4m3 codes
+ *               keep their relative precision 2^-4 for values down to 2^-15 of
+ *               the block's largest. */
+typedef enum { LK_KV_BF16 = 0, LK_KV_INT8 = 1, LK_KV_FP8 = 2, LK_KV_FP8_BLOCK = 3 } lk_kv_format;
 
 /* Cache options for lk_cache_bytes_ex / lk_cache_init_ex. */
 typedef struct lk_cache_options {
   int64_t middle_tokens;      /* < 0: contiguous region B; >= 0: paged, pools
-                                 sized as in lk_cache_bytes_paged (INT8 / FP8:
+                                 sized as in lk_cache_bytes_paged (quantised:
                                  sealed blocks are the pages,
                                  floor(middle_tokens/128) per head of a class) */
   int32_t kv_format;          /* lk_kv_format */
@@ -202,11 +208,12 @@ lk_status lk_cache_init_ex(lk_plan plan, void* dev_buf, size_t bytes, int32_t ba
                            int32_t capacity_tokens, const lk_cache_options* opt, void* stream,
                            lk_cache* out);
 
-/* Host copy of sealed block `block` of an INT8 or FP8 cache's (layer, b,
+/* Host copy of sealed block `block` of a quantised cache's (layer, b,
  * kv_head), in logical order: k_codes [128][n_kept] (kept channels
  * ascending), k_scales [n_kept], v_codes [128][128], v_scales [128]; any
  * pointer may be NULL.  Codes are one byte each: INT8 values, or e4m3 bit
- * patterns for FP8.  Synchronises `stream`.  Errors: LK_ERR_STATE (not a
+ * patterns for FP8 and FP8_BLOCK (whose k_scales are all the same, and whose
+ * v_scales are).  Synchronises `stream`.  Errors: LK_ERR_STATE (not a
  * quantised cache), LK_ERR_ARG (no such sealed block). */
 lk_status lk_cache_block(lk_cache cache, int32_t layer, int32_t b, int32_t kv_head, int32_t block,
                          int8_t* k_codes, float* k_scales, int8_t* v_codes, float* v_scales, void* stream);
@@ -541,6 +548,31 @@ lk_status lk_build_rope_axes(const lk_rope_desc* desc, const lk_rope_axes* axes,
 lk_status lk_rope_apply(lk_rope rope, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                         const int32_t* positions, int64_t tokens, int32_t num_q_heads, int32_t num_kv_heads,
                         void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/* lk_append_chunk with the rotation on the way: the chunk's keys are turned by
+ * their tokens' positions (lk_rope_apply) as they enter the layer, which is left as
+ * lk_rope_apply and lk_append_chunk would leave it, byte for byte (a paged cache
+ * may hand out its free pages in another order).
+ *   positions  device int32 [B][n_max] ([num_axes][B][n_max] for a rope of several
+ *              axes), any values; NULL: every token's own position in its sequence
+ *              (the number of tokens before it), on every axis
+ *   chunk->q, q_out  both NULL, or the chunk's queries and where they go turned:
+ *              q_out device bf16 [B][n_max][Hq][128], tokens q_out_stride
+ *              elements apart (as q_stride); it may be q itself with the same stride,
+ *              else must not overlap the inputs.  Rows past a sequence's length,
+ *              and of released slots, are left as they are.
+ * With n_max = 1 (a decode step: lk_decode_attn with q_out follows) it is one launch.
+ * k must not be q_out.  Errors as lk_append_chunk and lk_rope_apply. */
+lk_status lk_append_rope(lk_cache cache, int32_t layer, lk_rope rope, const lk_chunk* chunk, const int32_t* positions,
+                         void* q_out, int64_t q_out_stride, void* stream);
+
+/* One decode step of a layer whose queries and keys are not turned yet:
+ * lk_append_rope of one token of every sequence (chunk->n_max 1, chunk->lens
+ * NULL), then lk_decode_attn with the turned queries, which wait in the workspace.
+ *   o  device fp32 [B][Hq][128].
+ * workspace as for lk_decode_attn.  Nothing is launched on an error of either. */
+lk_status lk_step_rope(lk_cache cache, int32_t layer, lk_rope rope, const lk_chunk* chunk, const int32_t* positions,
+                       float* o, void* workspace, size_t ws_bytes, void* stream);
 
 /* Host-tracked token count of a layer: the longest sequence's length. */
 lk_status lk_cache_length(lk_cache cache, int32_t layer, int32_t* n);

@@ -30,6 +30,9 @@ variant):
   x / s rounded to the nearest e4m3 value, ties to the even code, |x / s|
   beyond 448 saturated to 448; the sign of x stays in the code, zero
   included.
+* FP8 with one scale per block ("fp8_block"; not from the pages): the same codes
+  with s = max(absmax / 448, 2^-64) over all of a block's K (kept channels), and
+  over all of its V.
 * The dequantised value is value(code) * s.
 """
 from __future__ import annotations
@@ -43,6 +46,7 @@ BLOCK_ROWS = 128
 QMAX = 127
 FP8_MAX = 448.0
 FORMATS = ("int8", "fp8")
+BLOCK_MIN_SCALE = np.float32(2.0 ** -64)
 
 
 def e4m3_value(code) -> np.ndarray:
@@ -81,12 +85,14 @@ def _quantize(x: np.ndarray, absmax: np.ndarray, fmt: str = "int8"):
     absmax = np.asarray(absmax, dtype=np.float32)
     qmax = np.float32(QMAX if fmt == "int8" else FP8_MAX)
     scale = absmax / qmax                                  # fp32, round to nearest
+    if fmt == "fp8_block":
+        scale = np.maximum(scale, BLOCK_MIN_SCALE)
     safe = np.where(scale > 0, scale, np.float32(1.0)).astype(np.float32)
     y = (x / safe).astype(np.float32)                      # fp32 quotient
     if fmt == "int8":
         q = np.where(scale > 0, np.rint(y), 0.0)           # half to even
         codes = np.clip(q, -QMAX, QMAX).astype(np.int8)
-    elif fmt == "fp8":
+    elif fmt in ("fp8", "fp8_block"):
         codes = np.where(scale > 0, encode_e4m3(y), np.uint8(0)).astype(np.uint8)
     else:
         raise ValueError(fmt)
@@ -99,17 +105,17 @@ def code_value(codes, fmt: str = "int8") -> np.ndarray:
 
 
 def quantize_per_channel(x: np.ndarray, fmt: str = "int8"):
-    """K block [R, C] -> (codes [R, C], scales fp32 [C])."""
+    """K block [R, C] -> (codes [R, C], scales fp32 [C], all the same for fp8_block)."""
     x = np.asarray(x, dtype=np.float32)
-    absmax = np.abs(x).max(axis=0)
+    absmax = np.abs(x).max(axis=0) if fmt != "fp8_block" else np.full(x.shape[1], np.abs(x).max())
     codes, scale = _quantize(x, absmax[None, :], fmt)
     return codes, scale.reshape(-1)
 
 
 def quantize_per_token(x: np.ndarray, fmt: str = "int8"):
-    """V block [R, C] -> (codes [R, C], scales fp32 [R])."""
+    """V block [R, C] -> (codes [R, C], scales fp32 [R], all the same for fp8_block)."""
     x = np.asarray(x, dtype=np.float32)
-    absmax = np.abs(x).max(axis=1)
+    absmax = np.abs(x).max(axis=1) if fmt != "fp8_block" else np.full(x.shape[0], np.abs(x).max())
     codes, scale = _quantize(x, absmax[:, None], fmt)
     return codes, scale.reshape(-1)
 
@@ -171,17 +177,17 @@ def decode_head_quantized(q, K, V, policy: int, kept, N: int, S: int, W: int, W_
 
 
 def resident_bytes_quantized(policy: int, n_kept: int, N: int, S: int, W: int, W_loc: int,
-                             n_special: int = 0, head_dim: int = 128) -> int:
+                             n_special: int = 0, head_dim: int = 128, fmt: str = "int8") -> int:
     """Bytes one decode step reads for one (b, kv head) of a cache whose
     complete middle blocks are quantised (INT8 or FP8: one byte per code): the
     bf16 bytes of every row that is not in a sealed block (sinks, window,
     LOCAL / SPECIAL rows, the open middle block) plus, per sealed block, its
     codes (128 x k for K, 128 x d for V) and fp32 scales (k for K, 128 for
-    V)."""
+    V; fp8_block: 16 bytes with two scales)."""
     bf16 = _resident_bytes_bf16(policy, n_kept, N, S, W, W_loc, n_special, head_dim)
     nb = sealed_blocks(n_kept, N, S, W) if policy == 0 and 0 < n_kept else 0
     if nb == 0:
         return bf16
     mid_row_bf16 = (n_kept + head_dim) * 2
-    block = BLOCK_ROWS * (n_kept + head_dim) + 4 * (n_kept + BLOCK_ROWS)
+    block = BLOCK_ROWS * (n_kept + head_dim) + (4 * (n_kept + BLOCK_ROWS) if fmt != "fp8_block" else 16)
     return bf16 - nb * BLOCK_ROWS * mid_row_bf16 + nb * block
