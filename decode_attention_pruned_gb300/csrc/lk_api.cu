@@ -441,6 +441,7 @@ struct lk_cache_s {
     return LK_OK;
   }
   DecodeMaps maps;
+  BlockMaps block_maps;            // FP8_BLOCK
   int device = 0, num_sms = 0, decode_ctas = 0, step_mode = LK_STEP_AUTO;
   uint64_t wait_limit_ns = kWaitLimitNs;   // decode ring and segment waits
   std::vector<uint8_t> upload;     // host image of the tables (kept alive for the async copy)
@@ -765,7 +766,8 @@ static lk_status cache_init_impl(lk_plan plan, void* dev_buf, size_t bytes, int3
   // parts}, so that a box stops at the end of its (head, sequence) block or
   // page.
   std::memset(&c->maps, 0, sizeof(c->maps));
-  auto encode_view = [&](int map, int pl, int64_t first_row, int64_t rows, int64_t blocks) -> CUresult {
+  auto encode_view = [&](CUtensorMap* to, int box_rows, int pl, int64_t first_row, int64_t rows,
+                         int64_t blocks) -> CUresult {
     const int width = pool_width(pl);
     const bool fam128 = (width % 64) == 0;
     const int inner = fam128 ? 64 : 32;              // channels per half / stripe
@@ -779,7 +781,7 @@ static lk_status cache_init_impl(lk_plan plan, void* dev_buf, size_t bytes, int3
     box[rank++] = (cuuint32_t)inner;
     dims[rank] = (cuuint64_t)rows;
     strides[rank - 1] = row_bytes;
-    box[rank++] = (cuuint32_t)kTmaBoxRows;
+    box[rank++] = (cuuint32_t)box_rows;
     if (blocked) {
       dims[rank] = (cuuint64_t)blocks;
       strides[rank - 1] = (cuuint64_t)rows * row_bytes;
@@ -791,7 +793,7 @@ static lk_status cache_init_impl(lk_plan plan, void* dev_buf, size_t bytes, int3
       box[rank++] = (cuuint32_t)parts;
     }
     const cuuint32_t estride[4] = {1, 1, 1, 1};
-    return encode(&c->maps.m[map], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, cv.pool[pl] + first_row * width, dims,
+    return encode(to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, cv.pool[pl] + first_row * width, dims,
                   strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   fam128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -799,7 +801,7 @@ static lk_status cache_init_impl(lk_plan plan, void* dev_buf, size_t bytes, int3
   for (int map = 0; map < kNumMaps; ++map) {
     CUresult r;
     if (map < kMapAK) {
-      r = encode_view(map, map - kMapFlat, 0, lay.pool_rows[map - kMapFlat], 0);
+      r = encode_view(&c->maps.m[map], kTmaBoxRows, map - kMapFlat, 0, lay.pool_rows[map - kMapFlat], 0);
     } else {
       // block views shorter than a box are never used: encode them over one
       // box of the pool so that every map is valid
@@ -811,11 +813,19 @@ static lk_status cache_init_impl(lk_plan plan, void* dev_buf, size_t bytes, int3
       const int64_t blocks = a ? lay.a_blocks[cls] : lay.b_blocks[pl];
       const bool usable = rows >= kTmaBoxRows && blocks > 0;
       c->maps.block_rows[map] = usable ? (int32_t)rows : 0;
-      r = usable ? encode_view(map, pl, first, rows, blocks) : encode_view(map, pl, 0, kTmaBoxRows, 1);
+      r = usable ? encode_view(&c->maps.m[map], kTmaBoxRows, pl, first, rows, blocks)
+                 : encode_view(&c->maps.m[map], kTmaBoxRows, pl, 0, kTmaBoxRows, 1);
     }
     if (r != CUDA_SUCCESS) {
       delete c;
       return fail(LK_ERR_CUDA, "cuTensorMapEncodeTiled failed for map %d (CUresult %d)", map, (int)r);
+    }
+  }
+  for (int pl = 0; pl < kNumPools && fmt == kKvFp8Block; ++pl) {
+    const CUresult r = encode_view(&c->block_maps.pool[pl], kBlockBoxRows, pl, 0, lay.pool_rows[pl], 0);
+    if (r != CUDA_SUCCESS) {
+      delete c;
+      return fail(LK_ERR_CUDA, "cuTensorMapEncodeTiled failed for pool %d (CUresult %d)", pl, (int)r);
     }
   }
   *out = c;
@@ -1021,7 +1031,7 @@ void set_divisors(const lk_cache_s* cache, DecodeArgs& a) {
 }
 
 cudaError_t run_decode(const lk_cache_s* cache, const DecodeArgs& a, int ctas, cudaStream_t stream) {
-  return cache->lay.kv_format == kKvFp8Block ? launch_decode_block(a, ctas, stream)
+  return cache->lay.kv_format == kKvFp8Block ? launch_decode_block(cache->block_maps, a, ctas, stream)
                                              : launch_decode(cache->maps, a, ctas, stream);
 }
 

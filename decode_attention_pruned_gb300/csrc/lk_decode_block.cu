@@ -8,33 +8,45 @@
 // accumulate) times 2^e s_K.  s_V = f 2^j, 1 <= f < 2: the weights p = 2^(s + j - m)
 // take the scale's exponent, p times f is split into f16 hi + lo (two products, 22
 // bits), and l takes p times 2^-j.  Rows in bf16 (sinks, window, LOCAL and SPECIAL
-// rows, the open block) are scored on bf16 products, p in bf16 hi + lo.
-// f16's range: m follows the largest s + j - 5, so that the largest weight lies in
-// [2^5, 2^14) and weights down to 2^-19 of it keep all their bits.  Until a segment
+// rows, the open block) are scored on bf16 products, p as three bf16 numbers.
+// f16's range: m follows the largest s + j - 12, so that the largest weight lies in
+// [2^12, 2^15) and weights down to 2^-15 of it keep all their bits.  Until a segment
 // meets its first sealed block, m follows the scores alone; there it moves by that
-// block's j - 5, and the bf16 rows after it count by the same (bf16 has the range of
+// block's j - 12, and the bf16 rows after it count by the same (bf16 has the range of
 // fp32: their weights may be far from 1).
 //
 // Tensor cores: m16n8k16 with 16 tokens (a slab) on M for S^T = K q^T, 16 channels on
 // M for O^T += V^T P^T, and the G <= 8 query heads on N.  Channels and tokens are
 // put on the products' rows and depths so that a lane's operands are whole 16-byte
-// words of memory: the codes are stored in that order (lk_block.h), the words of
-// bf16 rows are dealt out by it (K: channels 32 u + 8 t of rows g and g + 8; V: the
-// rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 at channels 8 g and 64 + 8 g, paired by byte
-// permutes).  With G <= 4 the columns 4 .. 7 hold the same heads again, and P's lo
-// halves go there beside the hi ones in the columns 0 .. 3: one product for both.
+// words: the codes are stored in that order (lk_block.h), the words of bf16 rows are
+// dealt out by it (K: channels 32 u + 8 t of rows g and g + 8; V: the rows 2 t,
+// 2 t + 1, 2 t + 8, 2 t + 9 at channels 8 g and 64 + 8 g, paired by byte permutes).
+// With G <= 4 the columns 4 .. 7 hold the same heads again, and P's lo halves go there
+// beside the hi ones in the columns 0 .. 3: one product for both.
 //
-// Work.  Slabs of all (layer, sequence, kv head) entries form a line, each costing
-// its bytes; CTA i of P takes those that start in [iC/P, (i+1)C/P), its 8 warps in
-// turn.  A warp copies each slab into a ring of its own with cp.async, every lane
-// just the words that it will read, as far ahead as the ring holds (22 KB, 8 slabs):
-// no lane waits for another and nothing is handed over, so copies of the next entry
-// are in flight while the warps of this one merge.  An entry that spans CTAs leaves
-// partials, merged in order by the last CTA to come.
+// Work.  Pieces of all (layer, sequence, kv head) entries form a line, each costing
+// its bytes: 64 full-width rows, sealed blocks, the open block.  CTA i
+// takes the pieces that start in the line's i-th part.  A thread copies them into a ring
+// of stages (up to 128 bf16 rows by TMA, two or three sealed blocks by bulk copies);
+// each of eight warps takes 16 rows of a stage, or of each of its blocks.  At the end of
+// their part of an entry they merge their (o, m, l) through shared memory; an entry that
+// spans CTAs leaves partials, merged in order by the last CTA to come.
 //
-// What bounds it: the bytes.
+// What bounds it (8 kv heads of 4 query heads, a quarter to all channels kept, from cold
+// caches): the bytes.  64 x 4096 tokens take 60 us (309 MB: 5.1 TB/s), 4 x 131072 61 us
+// (315 MB), with the copies alone and no arithmetic 55 and 53 us; 1 x 32768 18 us (45
+// MB), 14 us with the copies alone, 3 us of them before the first copy (the lengths, the
+// line, the code's own way from memory); short calls 13 us, which are those, one load
+// after another, and the merges.
+//   What went before: each lane copying its own words ahead with cp.async spent 400
+// instructions on a slab, most of them on copies and their bookkeeping (64 x 4096: 91 us).
+// Two groups of eight warps that take stages in turn have 96 registers a thread, and
+// spill (75 us); warps of their own for the merges do not pay either (70 us).
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "lk_append.cuh"
 #include "lk_block.h"
@@ -45,59 +57,82 @@
 namespace lk {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 8;                      // consumers; one more warp copies
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kUnit = 512;                     // bytes: a word of each lane
-constexpr int kRingUnits = 44;                 // per warp
-constexpr int kSlots = 8;                      // slabs in flight per warp at most
-constexpr int kQStride = kHeadDim + 8;         // padded row of q
-constexpr float kRescaleGap = 8.f;             // log2: m moves when what it follows exceeds it by more
-constexpr int kWeightExp = 5;                  // log2 of the largest sealed weight when m moves
-constexpr uint64_t kMinCtaBytes = 64 * 1024;   // line a CTA takes at least
+constexpr int kBoxRows = kBlockBoxRows;        // bf16 rows of a copy, and of a piece of the line
+constexpr int kStageBoxes = 2;
+constexpr int kSlots = 16;                     // stages in flight at most
+constexpr int kQStride = kHeadDim + 32;        // row of q: the next one's words lie in the other half of the banks
+constexpr float kRescaleGap = 2.f;             // log2: m moves when what it follows exceeds it by more
+constexpr int kFlush = 8;                      // stages whose products share accumulators
+constexpr int kWeightExp = 12;                 // log2 of the largest sealed weight when m moves
+constexpr uint32_t kMinCtaCost = 16;           // line a CTA takes at least: 64 KB, more than any piece
 constexpr int kRowTop = 14;                    // a row of q is moved so that its largest channel lies in [2^14, 2^15)
+constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the producer's wait for its copies at the end
+constexpr int kHeadsKept = 48, kLensKept = 512;            // descriptors and lengths that shared memory has places for
 
-enum SlabType : int { kWide = 0, kOpen = 1, kSealed = 2, kNone = 3 };
+enum PieceType : int { kWide = 0, kOpen = 1, kSealed = 2 };
+constexpr int kFirst = 1, kLast = 2;           // of the stages of a segment
 
+struct Stage {
+  int32_t entry;               // < 0: no more
+  int16_t type, flags;
+  int16_t count, width;        // blocks, or rows; K channels
+  uint32_t at;                 // ring offset
+  int32_t first_cta, last_cta; // that hold partials of the entry
+  int32_t pad[2];
+};
+static_assert(sizeof(Stage) == 32, "two words");
+
+template <bool kPack>
 struct Smem {
+  static constexpr int kHeads = kPack ? 4 : kMaxGroup;             // rows of a merge slot
+  static constexpr int kRingBytes = (kPack ? 185 : 169) * 1024;
   static constexpr int kRing = 0;
-  static constexpr int kMergeO = kRing + kWarps * kRingUnits * kUnit;
-  static constexpr int kMergeM = kMergeO + kWarps * kMaxGroup * kHeadDim * 4;
-  static constexpr int kMergeL = kMergeM + kWarps * kMaxGroup * 4;
-  static constexpr int kQ = kMergeL + kWarps * kMaxGroup * 4;      // of two entries: all channels, kept ones, kept ones as f16
+  static constexpr int kMergeO = kRing + kRingBytes;
+  static constexpr int kMergeM = kMergeO + kWarps * kHeads * kHeadDim * 4;
+  static constexpr int kMergeL = kMergeM + kWarps * kHeads * 4;
+  static constexpr int kQ = kMergeL + kWarps * kHeads * 4;         // two entries: all channels, kept ones, as f16
   static constexpr int kQBytes = kMaxGroup * kQStride * 2;
   static constexpr int kBack = kQ + 2 * 3 * kQBytes;               // of two entries: what scores are scaled by
-  static constexpr int kScales = kBack + 2 * kMaxGroup * 4;        // (s_K, s_V) of the slabs in flight
-  static constexpr int kScan = kScales + kWarps * kSlots * 8;
-  static constexpr int kBytes = kScan + kWarps * 8 + 32;
+  static constexpr int kStage = kBack + 2 * kMaxGroup * 4;
+  static constexpr int kHeadDescs = kStage + kSlots * (int)sizeof(Stage);
+  static constexpr int kLens = kHeadDescs + kHeadsKept * (int)sizeof(HeadDesc);
+  // the barriers: stages landed and used, the consumers' own
+  static constexpr int kFull = kLens + kLensKept * 8, kEmpty = kFull + 8 * kSlots, kMeet = kEmpty + 8 * kSlots;
+  static constexpr int kScan = kMeet + 8;
+  static constexpr int kInfo = kScan + (kWarps + 1) * 8;           // what threads tell each other
+  static constexpr int kBytes = kInfo + 32;
+  static constexpr int kAll = kBytes + 1024;                       // to align the ring
+  static_assert(kQ % 16 == 0 && kStage % 16 == 0 && kHeadDescs % 8 == 0 && kFull % 8 == 0, "alignment");
+  static_assert(kAll <= 227 * 1024, "shared memory per block");
+  static_assert(kRingBytes >= 2 * 64 * 1024, "two stages of full-width rows");
 };
-static_assert(Smem::kQ % 16 == 0 && Smem::kScales % 8 == 0 && Smem::kScan % 8 == 0, "alignment");
-static_assert(Smem::kBytes <= 227 * 1024, "shared memory per block");
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
-               : "memory");
+// Sealed blocks per stage (62 KB at k = 32 .. 66 KB at k = 128): what the copying thread
+// takes for a stage should be well below what the bytes take.
+__device__ __forceinline__ int blocks_per_stage(int k) { return k == 32 ? 3 : 2; }
+
+// The products without an order among themselves that the compiler would have to keep.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most `left` of this thread's groups are in flight.
-__device__ __forceinline__ void copy_wait(int left) {
-  static_assert(kSlots == 8, "one case per number of groups");
-  switch (left) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-  }
-}
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -118,18 +153,28 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return d;
 }
 
-// One (layer, sequence, kv head): its slabs in line order, wide ones first, then
-// sealed ones, then the open block's.
+// One (layer, sequence, kv head): its pieces in line order, boxes of full-width rows
+// first, then sealed blocks, then the open block.
 struct Entry {
-  int wide, sealed, open;      // slabs
+  int wide, sealed, open;      // boxes, blocks, 0 or 1
   int rows_wide, rows_open;
   int k;
 };
-__device__ __forceinline__ uint32_t cost_sealed(int k) { return kSlabRows * (k + kHeadDim); }
-__device__ __forceinline__ uint32_t cost_open(int k) { return 2 * kSlabRows * (k + kHeadDim); }
-constexpr uint32_t kCostWide = kSlabRows * 4 * kHeadDim;
-__device__ __forceinline__ uint64_t entry_cost(const Entry& g) {
-  return (uint64_t)kCostWide * g.wide + (uint64_t)cost_sealed(g.k) * g.sealed + (uint64_t)cost_open(g.k) * g.open;
+// The line is measured in 4 KB (no two pieces share memory: 32 bits reach 17.6 TB), the
+// open block's part rounded up.
+constexpr uint32_t kCostWide = kBoxRows * 4 * kHeadDim / 4096;
+__device__ __forceinline__ uint32_t cost_sealed(int k) { return (uint32_t)(k + kHeadDim) / 32; }
+__device__ __forceinline__ uint32_t cost_open(const Entry& g) {
+  return ((uint32_t)(g.rows_open * (g.k + kHeadDim)) + 2047) / 2048;
+}
+__device__ __forceinline__ uint32_t entry_cost(const Entry& g) {
+  return kCostWide * g.wide + cost_sealed(g.k) * g.sealed + cost_open(g);
+}
+// Line offset of the last piece of an entry that has one and starts at `off`.
+__device__ __forceinline__ uint32_t last_piece(const Entry& g, uint32_t off) {
+  const uint32_t off_s = off + kCostWide * g.wide;
+  if (g.open > 0) return off_s + cost_sealed(g.k) * g.sealed;
+  return g.sealed > 0 ? off_s + cost_sealed(g.k) * (g.sealed - 1) : off + kCostWide * (g.wide - 1);
 }
 
 struct EntryId {
@@ -148,104 +193,166 @@ __device__ __forceinline__ EntryId entry_id(const DecodeArgs& a, int e) {
   return r;
 }
 
-__device__ __forceinline__ Entry entry_geometry(const DecodeArgs& a, int e) {
+struct Lens {
+  int n, cnt;
+};
+__device__ __forceinline__ Lens entry_lens(const DecodeArgs& a, const EntryId& id) {
   const CacheView& cv = a.cv;
-  const EntryId id = entry_id(a, e);
-  const HeadDesc& hd = cv.heads[id.l * cv.Hkv + id.h];
-  const int N = __ldcg(&cv.len[id.l * cv.B + id.b]);
+  const int lb = id.l * cv.B + id.b;
+  return Lens{__ldcg(&cv.len[lb]), __ldcg(&cv.cnt[lb])};
+}
+__device__ __forceinline__ Entry entry_geometry(const CacheView& cv, const HeadDesc& hd, Lens len) {
+  const int N = len.n;
   Entry r{0, 0, 0, 0, 0, 0};
   if (hd.policy == kFull) {
     r.rows_wide = min(N, cv.S + cv.W);
     if (hd.n_kept > 0) {
       const int m = max(0, N - cv.S - cv.W);
       r.k = hd.n_kept;
-      r.sealed = kSlabs * min(m / kQBlockRows, cv.max_pages > 0 ? cv.max_pages : hd.qblocks);
+      r.sealed = min(m / kQBlockRows, cv.max_pages > 0 ? cv.max_pages : hd.qblocks);
       r.rows_open = min(m % kQBlockRows, hd.cap_b);
     }
   } else if (hd.policy == kLocal) {
     r.rows_wide = min(N, cv.W_loc);
   } else {
-    r.rows_wide = __ldcg(&cv.cnt[id.l * cv.B + id.b]);
+    r.rows_wide = len.cnt;
   }
   r.rows_wide = min(r.rows_wide, hd.cap_a);
-  r.wide = (r.rows_wide + kSlabRows - 1) / kSlabRows;
-  r.open = (r.rows_open + kSlabRows - 1) / kSlabRows;
+  r.wide = (r.rows_wide + kBoxRows - 1) / kBoxRows;
+  r.open = r.rows_open > 0 ? 1 : 0;
   return r;
 }
 
-__device__ __forceinline__ uint64_t udiv(uint64_t a, uint64_t b) {
-  return (a >> 32) == 0 && (b >> 32) == 0 ? (uint32_t)a / (uint32_t)b : a / b;
+struct Info {
+  uint32_t first_off;          // line offset of the entry the range starts in
+  int32_t first_entry;
+  int32_t last;                // this CTA is the entry's last
+  int32_t gone;                // set once some wait ran out
+};
+
+// The rest of a wait whose phase was not complete at once.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit, volatile int* gone,
+                                        DevHeader* hdr) {
+  const uint64_t t0 = global_timer_ns();
+  while (limit != 0) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*gone) return false;
+    if (global_timer_ns() - t0 > limit) break;
+  }
+  *gone = 1;
+  atomicOr(&hdr->status, (uint32_t)kStatusTimeout);
+  return false;
 }
-// Slabs r in [0, n), at line offset o0 + c r each, that start inside [start, end).
-__device__ __forceinline__ int2 slabs_in(uint64_t o0, uint32_t c, int n, uint64_t start, uint64_t end) {
-  auto first = [&](uint64_t x) { return x > o0 ? (int)min((uint64_t)n, udiv(x - o0 + c - 1, c)) : 0; };
-  return n == 0 ? make_int2(0, 0) : make_int2(first(start), first(end));
-}
-// The CTA whose range [floor(iC/P), floor((i+1)C/P)) holds offset x < C.
-__device__ __forceinline__ int range_owner(uint64_t x, uint64_t C, int P) {
-  return (int)min(udiv((x + 1) * (uint64_t)P - 1, C), (uint64_t)P - 1);
-}
+// Waits of a whole warp, with one answer: false once a wait of the CTA ran out.
+struct Wait {
+  uint64_t limit;
+  volatile int* gone;
+  DevHeader* hdr;
+  __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const {
+    return mbar_test_wait(bar, parity) || wait_on(bar, parity, limit, gone, hdr);
+  }
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, one(bar, parity));
+  }
+};
 
 template <bool kPack>
-__global__ void __launch_bounds__(kThreads, 1) decode_block_kernel(const __grid_constant__ DecodeArgs a) {
-  extern __shared__ __align__(1024) uint8_t sm[];
-  const uint32_t base = smem_addr(sm);
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_block_kernel(const __grid_constant__ BlockMaps maps, const __grid_constant__ DecodeArgs a) {
+  using L = Smem<kPack>;
+  extern __shared__ uint8_t sm_raw[];
+  const uint32_t raw = smem_addr(sm_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = sm_raw + (base - raw);
   const CacheView& cv = a.cv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
   const int G = cv.G, E = a.nlayers * cv.B * cv.Hkv;
-  constexpr int kHeads = kPack ? 4 : kMaxGroup;            // rows of a merge slot
-  float* merge_o = reinterpret_cast<float*>(sm + Smem::kMergeO);
-  float* merge_m = reinterpret_cast<float*>(sm + Smem::kMergeM);
-  float* merge_l = reinterpret_cast<float*>(sm + Smem::kMergeL);
-  uint64_t* scan = reinterpret_cast<uint64_t*>(sm + Smem::kScan);
-  volatile int* first_at = reinterpret_cast<volatile int*>(sm + Smem::kScan + kWarps * 8);        // entry; flag
-  volatile uint64_t* first_off_at = reinterpret_cast<volatile uint64_t*>(sm + Smem::kScan + kWarps * 8 + 16);
+  constexpr int kHeads = L::kHeads;
+  float* merge_o = reinterpret_cast<float*>(sm + L::kMergeO);
+  float* merge_m = reinterpret_cast<float*>(sm + L::kMergeM);
+  float* merge_l = reinterpret_cast<float*>(sm + L::kMergeL);
+  Stage* stages = reinterpret_cast<Stage*>(sm + L::kStage);
+  const uint32_t full = base + L::kFull, empty = base + L::kEmpty;
+  uint32_t* scan = reinterpret_cast<uint32_t*>(sm + L::kScan);
+  volatile Info& info = *reinterpret_cast<volatile Info*>(sm + L::kInfo);
+  static_assert(sizeof(Info) <= 32, "Info");
+  if (tid < kSlots) {
+    mbar_init(full + 8 * tid, 1);
+    mbar_init(empty + 8 * tid, kWarps);
+  } else if (tid == kSlots) {
+    mbar_init(base + L::kMeet, kWarps);
+  }
+  if (tid <= kSlots) fence_barrier_init();
   // rows of q that no head has
-  for (int i = tid; i < 2 * 3 * Smem::kQBytes / 16; i += kThreads)
-    reinterpret_cast<uint4*>(sm + Smem::kQ)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (tid < 2 * kMaxGroup) reinterpret_cast<float*>(sm + Smem::kBack)[tid] = 0.f;
-  if (tid == 0) first_at[0] = E;
-  const uint64_t policy = l2_policy_evict_first();
+  for (int i = tid; i < 2 * 3 * L::kQBytes / 16; i += kThreads)
+    reinterpret_cast<uint4*>(sm + L::kQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < 2 * kMaxGroup) reinterpret_cast<float*>(sm + L::kBack)[tid] = 0.f;
+  if (tid == 0) {
+    info.first_entry = E;
+    info.gone = 0;
+  }
+  if (warp == kWarps && lane < kNumPools) tma_prefetch_map(&maps.pool[lane]);
+  // The head table never changes: where it has room, it is here before the kernel ahead
+  // of this one is done.
+  const int nheads = a.nlayers * cv.Hkv;
+  HeadDesc* kept_heads = reinterpret_cast<HeadDesc*>(sm + L::kHeadDescs);
+  const HeadDesc* heads = cv.heads + (size_t)a.layer * cv.Hkv;       // [nlayers][Hkv]
+  if (nheads <= kHeadsKept) {
+    static_assert(sizeof(HeadDesc) % 8 == 0, "words");
+    for (int i = tid; i < nheads * (int)(sizeof(HeadDesc) / 8); i += kThreads)
+      reinterpret_cast<uint64_t*>(kept_heads)[i] = reinterpret_cast<const uint64_t*>(heads)[i];
+    heads = kept_heads;
+  }
+  Lens* kept_lens = reinterpret_cast<Lens*>(sm + L::kLens);
+  const bool keep_lens = E <= kLensKept;
+  __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
 
   // ---- the line, this CTA's range of it, and the entry the range starts in.  An
-  // entry without a slab gives 0.
+  // entry without a piece gives 0.
   const int per = (E + kThreads - 1) / kThreads, e_lo = min(E, tid * per), e_hi = min(E, e_lo + per);
-  uint64_t mine = 0;
+  auto lens_of = [&](int e, const EntryId& id) { return keep_lens ? kept_lens[e] : entry_lens(a, id); };
+  uint32_t mine = 0;
   for (int e = e_lo; e < e_hi; ++e) {
-    const uint64_t c = entry_cost(entry_geometry(a, e));
+    const EntryId id = entry_id(a, e);
+    const Lens len = entry_lens(a, id);
+    if (keep_lens) kept_lens[e] = len;
+    const uint32_t c = entry_cost(entry_geometry(cv, heads[id.lr * cv.Hkv + id.h], len));
     mine += c;
     if (c == 0 && e % (int)gridDim.x == (int)blockIdx.x) {
-      const EntryId id = entry_id(a, e);
       float4* dst = reinterpret_cast<float4*>(
           a.o + (((size_t)id.lr * cv.B + id.b) * cv.Hq + (size_t)id.h * G) * kHeadDim);
       for (int i = 0; i < G * kHeadDim / 4; ++i) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  uint64_t incl = mine;
+  uint32_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const uint64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  uint64_t C = 0, excl = incl - mine;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) excl += scan[w];
-    C += scan[w];
+  uint32_t C = 0, excl = incl - mine;
+#pragma unroll
+  for (int w = 0; w <= kWarps; ++w) {
+    const uint32_t v = scan[w];
+    if (w < warp) excl += v;
+    C += v;
   }
-  const int P = (int)max((uint64_t)1, min((uint64_t)gridDim.x, C / kMinCtaBytes));
-  const int cta = blockIdx.x;
-  const uint64_t start = cta < P ? udiv((uint64_t)cta * C, P) : C, end = cta < P ? udiv((uint64_t)(cta + 1) * C, P) : C;
+  // ranges of equal length, of kMinCtaCost at least
+  const uint32_t share = max(kMinCtaCost, (C + gridDim.x - 1) / gridDim.x), cta = blockIdx.x;
+  const uint32_t start = min(C, cta * share), end = min(C, start + share);
   if (mine > 0 && excl <= start && start < excl + mine) {
-    uint64_t at = excl;
+    uint32_t at = excl;
     for (int e = e_lo; e < e_hi; ++e) {
-      const uint64_t c = entry_cost(entry_geometry(a, e));
+      const EntryId id = entry_id(a, e);
+      const uint32_t c = entry_cost(entry_geometry(cv, heads[id.lr * cv.Hkv + id.h], lens_of(e, id)));
       if (at + c > start) {
-        first_at[0] = e;
-        *first_off_at = at;
+        info.first_entry = e;
+        info.first_off = at;
         break;
       }
       at += c;
@@ -253,192 +360,319 @@ __global__ void __launch_bounds__(kThreads, 1) decode_block_kernel(const __grid_
   }
   __syncthreads();
   if (start >= end) return;
+  const Wait wait{a.wait_limit_ns, &info.gone, cv.hdr};
 
-  // ---- the copies ahead: segments (this CTA's slabs of an entry), slab by slab
-  int next_e = first_at[0];                    // entry after the segment
-  uint64_t next_off = *first_off_at;
-  Entry g{0, 0, 0, 0, 0, 0};
-  int seg_e = -1, seg_total = 0, seg_i = 0, seg_ctas = 0;
-  int2 seg_w = make_int2(0, 0), seg_s = seg_w, seg_o = seg_w;
-  int64_t row_a = 0, row_kb = 0, row_vb = 0;   // first rows of the regions
-  int pool_kb = 0;
-  const uint8_t* blocks = nullptr;             // the sequence's blocks, or of the class's page area
-  const int32_t* pages = nullptr;
-  int page_from = 0, page = 0;                 // this lane's page id is of block page_from + lane
-  bool more = true;                            // the line has segments left
-  auto next_segment = [&]() -> bool {
-    while (next_e < E && next_off < end) {
-      seg_e = next_e++;
-      g = entry_geometry(a, seg_e);
-      const uint64_t off = next_off, off_s = off + (uint64_t)kCostWide * g.wide,
-                     off_o = off_s + (uint64_t)cost_sealed(g.k) * g.sealed;
-      next_off += entry_cost(g);
-      seg_w = slabs_in(off, kCostWide, g.wide, start, end);
-      seg_s = slabs_in(off_s, cost_sealed(g.k), g.sealed, start, end);
-      seg_o = slabs_in(off_o, cost_open(g.k), g.open, start, end);
-      seg_total = seg_w.y - seg_w.x + seg_s.y - seg_s.x + seg_o.y - seg_o.x;
-      if (seg_total == 0) continue;
-      const uint64_t last = g.open > 0     ? off_o + (uint64_t)cost_open(g.k) * (g.open - 1)
-                            : g.sealed > 0 ? off_s + (uint64_t)cost_sealed(g.k) * (g.sealed - 1)
-                                           : off + (uint64_t)kCostWide * (g.wide - 1);
-      seg_ctas = range_owner(off, C, P) | range_owner(last, C, P) << 16;
-      seg_i = warp;
-      const EntryId id = entry_id(a, seg_e);
-      const HeadDesc& hd = cv.heads[id.l * cv.Hkv + id.h];
-      row_a = hd.row_a + (int64_t)id.b * hd.cap_a;
-      row_kb = hd.krow_b + (int64_t)id.b * hd.cap_b;
-      row_vb = hd.vrow_b + (int64_t)id.b * hd.cap_b;
-      pool_kb = hd.pool_kb;
-      blocks = cv.qpool + hd.qoff;
-      if (cv.max_pages > 0) pages = cv.page_table + (((int64_t)id.l * cv.B + id.b) * cv.Hkv + id.h) * cv.max_pages;
-      else blocks += (int64_t)id.b * hd.qblocks * block_bytes(g.k);
-      page_from = -64;
-      return true;
-    }
-    return false;
-  };
-
-  // The ring is a FIFO of runs of units; the slab of number n is told by lane n mod 8.
-  const uint32_t ring = base + Smem::kRing + warp * kRingUnits * kUnit + lane * 16;
-  uint32_t put = 0, got = 0;
-  int head = 0, tail = 0;
-  bool wrapped = false;
-  int d_meta = 0, d_entry = 0, d_ctas = 0;     // place | rows - 1 << 8 | type << 12 | last << 14 | words of K << 16
-  auto push = [&](int at, int type, int rows, bool last, int kv) {
-    if (lane == (int)(put % kSlots)) {
-      d_meta = at | (rows - 1) << 8 | type << 12 | (last ? 1 : 0) << 14 | kv << 16;
-      d_entry = seg_e;
-      d_ctas = seg_ctas;
-    }
-    copy_commit();
-    ++put;
-  };
-  auto copy_ahead = [&]() {
-    while (more && put - got < kSlots) {
-      if (seg_i >= seg_total) {
-        if (!next_segment()) {
-          more = false;
-          return;
+  if (warp == kWarps) {
+    // ================================================================ producer
+    if (lane != 0) return;
+    const uint64_t policy = l2_policy_evict_first();
+    // The ring is a FIFO of runs of bytes: the oldest stage in flight starts at `tail`,
+    // the next goes to `next`, or to the ring's start when it does not fit before the end.
+    uint32_t put = 0, freed = 0, next = 0, tail = 0;
+    bool wrapped = false, ok = true;
+    auto reserve = [&](uint32_t bytes, uint32_t& at) -> bool {
+      bytes = (bytes + 1023u) & ~1023u;
+      while (true) {
+        if (put == freed) {
+          next = tail = 0;
+          wrapped = false;
         }
-        if (seg_i >= seg_total) {              // nothing of it for this warp, which takes part in the merge
-          if (put == got) head = tail = 0, wrapped = false;
-          push(head, kNone, 1, true, 0);
-          continue;
-        }
-      }
-      const int nw = seg_w.y - seg_w.x, ns = seg_s.y - seg_s.x;
-      const int type = seg_i < nw ? kWide : seg_i < nw + ns ? kSealed : kOpen;
-      const int kv = type == kWide ? 4 : g.k / 32;                // words of K per row
-      const int units = type == kSealed ? kv + 4 : 2 * kv + 8;
-      if (put == got) head = tail = 0, wrapped = false;
-      int at = head;
-      if (!wrapped && head + units > kRingUnits) {
-        if (units > tail) return;
-        at = 0;
-        wrapped = true;
-      } else if (wrapped && head + units > tail) {
-        return;
-      }
-      head = at + units;
-      const uint32_t dst = ring + at * kUnit;
-      int rows = kSlabRows;
-      if (type == kSealed) {
-        const int slab = seg_s.x + seg_i - nw, j = slab / kSlabs;
-        int64_t block = j;
-        if (pages != nullptr) {
-          if (j >= page_from + 32 || j < page_from) {
-            page_from = j;
-            page = __ldcg(pages + min(j + lane, g.sealed / kSlabs - 1));
+        if (put - freed < (uint32_t)kSlots) {
+          if (!wrapped && next + bytes <= (uint32_t)L::kRingBytes) break;
+          if (!wrapped && bytes <= tail) {
+            next = 0;
+            wrapped = true;
+            break;
           }
-          block = max(0, __shfl_sync(0xffffffffu, page, j - page_from));   // (missing: the status says so)
+          if (wrapped && next + bytes <= tail) break;
         }
-        const uint8_t* src = blocks + block * block_bytes(g.k);
-        if (lane == 0)
-          copy8(base + Smem::kScales + (warp * kSlots + put % kSlots) * 8, src + block_soff(g.k));
-        const uint8_t* ks = src + (slab % kSlabs) * kSlabRows * g.k + lane * 16;
-        const uint8_t* vs = src + block_voff(g.k) + (slab % kSlabs) * kSlabRows * kHeadDim + lane * 16;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (u < kv) copy16(dst + u * kUnit, ks + u * kUnit, policy);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) copy16(dst + (kv + u) * kUnit, vs + u * kUnit, policy);
-      } else {
-        // rows behind the last are its copies, and weigh nothing
-        const bool wide = type == kWide;
-        const int r0 = kSlabRows * (wide ? seg_w.x + seg_i : seg_o.x + seg_i - nw - ns);
-        rows = min(kSlabRows, (wide ? g.rows_wide : g.rows_open) - r0);
-        const int width = wide ? kHeadDim : g.k;
-        const uint16_t* kp = cv.pool[wide ? (int)kPoolK128 : pool_kb] + ((wide ? row_a : row_kb) + r0) * width + 8 * tig;
-        const uint16_t* vp = cv.pool[kPoolV] + ((wide ? row_a : row_vb) + r0) * kHeadDim + 8 * gid;
-#pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          const uint16_t* row = kp + min(gid + 8 * hi, rows - 1) * width;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (u < kv) copy16(dst + (2 * u + hi) * kUnit, row + 32 * u, policy);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint16_t* row = vp + min(2 * tig + (t & 1) + 4 * (t & 2), rows - 1) * kHeadDim;
-          copy16(dst + (2 * kv + 2 * t) * kUnit, row, policy);
-          copy16(dst + (2 * kv + 2 * t + 1) * kUnit, row + 64, policy);
+        if (!wait.one(empty + 8 * (freed % kSlots), freed / kSlots & 1u)) return false;
+        if (++freed != put) {
+          const uint32_t t = stages[freed % kSlots].at;
+          if (t < tail) wrapped = false;
+          tail = t;
         }
       }
-      const bool last = seg_i + kWarps >= seg_total;
-      push(at, type, rows, last, kv);
-      seg_i += kWarps;
+      at = next;
+      next += bytes;
+      return true;
+    };
+    uint32_t off = info.first_off;
+    const int e0 = info.first_entry;
+    EntryId id = entry_id(a, e0);
+    Lens len = lens_of(e0, id);
+    for (int e = e0; ok && e < E && off < end; ++e) {
+      const EntryId now = id;
+      const HeadDesc& hd = heads[now.lr * cv.Hkv + now.h];
+      const Entry g = entry_geometry(cv, hd, len);
+      const uint32_t off_s = off + kCostWide * g.wide, off_o = off_s + cost_sealed(g.k) * g.sealed;
+      // pieces of each kind that start inside the range
+      const FastDiv& by_cost = a.div_cost_b[g.k >> 5];                 // by 2 (k + 128), 64 times a block's cost
+      auto first_wide = [&](uint32_t x) {
+        return x > off ? (int)min((uint32_t)g.wide, (x - off + kCostWide - 1) / kCostWide) : 0;
+      };
+      auto first_sealed = [&](uint32_t x) {
+        const uint32_t one = cost_sealed(g.k);
+        return x > off_s ? (int)fdiv(64 * (min(x - off_s, one * g.sealed) + one - 1), by_cost) : 0;
+      };
+      const int2 w = make_int2(first_wide(start), first_wide(end));
+      const int2 s = make_int2(first_sealed(start), first_sealed(end));
+      const int open = g.open > 0 && off_o >= start && off_o < end ? 1 : 0;
+      // the next entry's lengths are on their way while this one's stages are sent
+      if (e + 1 < E) {
+        id = entry_id(a, e + 1);
+        len = lens_of(e + 1, id);
+      }
+      const int per_stage = blocks_per_stage(g.k);
+      const int nw = (w.y - w.x + kStageBoxes - 1) / kStageBoxes, ns = (s.y - s.x + per_stage - 1) / per_stage;
+      const int total = nw + ns + open;
+      if (total == 0) {
+        off = off_o + cost_open(g);
+        continue;
+      }
+      const int64_t row_a = hd.row_a + (int64_t)now.b * hd.cap_a;
+      const int64_t head = ((int64_t)now.l * cv.B + now.b) * cv.Hkv + now.h;
+      const int32_t* pages = cv.max_pages > 0 ? cv.page_table + head * cv.max_pages : nullptr;
+      const uint8_t* blocks = cv.qpool + hd.qoff;
+      const uint32_t bytes_block = (uint32_t)block_bytes(g.k);
+      if (pages == nullptr) blocks += (int64_t)now.b * hd.qblocks * bytes_block;
+      // page ids are read a stage ahead
+      int32_t ahead[3] = {0, 0, 0};
+      auto read_pages = [&](int j) {
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+          if (pages != nullptr && x < per_stage && j + x < s.y) ahead[x] = __ldcg(pages + j + x);
+      };
+      if (ns > 0) read_pages(s.x);
+      int fc = -1, lc = -1;
+      for (int j = 0; ok && j < total; ++j) {
+        Stage d;
+        d.entry = e;
+        d.flags = (int16_t)((j == 0 ? kFirst : 0) | (j + 1 == total ? kLast : 0));
+        if (j + 1 == total) {
+          fc = (int)(off / share);
+          lc = (int)(last_piece(g, off) / share);
+        }
+        d.first_cta = fc;
+        d.last_cta = lc;
+        const uint32_t slot = put % kSlots, bar = full + 8 * slot;
+        if (j >= nw && j < nw + ns) {
+          const int j0 = s.x + (j - nw) * per_stage, n = min(per_stage, s.y - j0);
+          const uint32_t bytes = (uint32_t)n * bytes_block;
+          if (!reserve(bytes, d.at)) {
+            ok = false;
+            break;
+          }
+          d.type = kSealed;
+          d.count = (int16_t)n;
+          d.width = (int16_t)g.k;
+          stages[slot] = d;
+          mbar_arrive_expect_tx(bar, bytes);
+          const uint32_t dst = base + L::kRing + d.at;
+          if (pages == nullptr) {
+            bulk_load(dst, blocks + (int64_t)j0 * bytes_block, bytes, bar, policy);
+          } else {
+            // (a missing page reads page 0: the status says so)
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+              if (x < n)
+                bulk_load(dst + x * bytes_block, blocks + (int64_t)max(0, ahead[x]) * bytes_block, bytes_block, bar,
+                          policy);
+            read_pages(j0 + n);
+          }
+        } else {
+          // whole boxes: the last may run into rows that are not this
+          // entry's, which nobody reads
+          const bool wide = j < nw;
+          const int g0 = wide ? w.x + j * kStageBoxes : 0;
+          const int boxes = wide ? min(kStageBoxes, w.y - g0) : (g.rows_open + kBoxRows - 1) / kBoxRows;
+          const int width = wide ? kHeadDim : g.k, pool = wide ? (int)kPoolK128 : hd.pool_kb;
+          const uint32_t k_bytes = (uint32_t)kBoxRows * 2 * width, v_bytes = (uint32_t)kBoxRows * 2 * kHeadDim;
+          const uint32_t bytes = (uint32_t)boxes * (k_bytes + v_bytes);
+          if (!reserve(bytes, d.at)) {
+            ok = false;
+            break;
+          }
+          d.type = (int16_t)(wide ? kWide : kOpen);
+          d.count = (int16_t)min(boxes * kBoxRows, (wide ? g.rows_wide : g.rows_open) - g0 * kBoxRows);
+          d.width = (int16_t)width;
+          stages[slot] = d;
+          mbar_arrive_expect_tx(bar, bytes);
+          const uint32_t kd = base + L::kRing + d.at, vd = kd + (uint32_t)boxes * k_bytes;
+          const int32_t kr = (int32_t)(wide ? row_a : hd.krow_b + (int64_t)now.b * hd.cap_b) + g0 * kBoxRows;
+          const int32_t vr = (int32_t)(wide ? row_a : hd.vrow_b + (int64_t)now.b * hd.cap_b) + g0 * kBoxRows;
+          for (int x = 0; x < boxes; ++x) {
+            if (width == 32 || width == 64)
+              tma_load_2d(kd + x * k_bytes, &maps.pool[pool], 0, kr + x * kBoxRows, bar, policy);
+            else
+              tma_load_3d(kd + x * k_bytes, &maps.pool[pool], 0, kr + x * kBoxRows, 0, bar, policy);
+            tma_load_3d(vd + x * v_bytes, &maps.pool[kPoolV], 0, vr + x * kBoxRows, 0, bar, policy);
+          }
+        }
+        ++put;
+      }
+      off = off_o + cost_open(g);
     }
-  };
+    uint32_t end_at;
+    if (ok && reserve(0, end_at)) {
+      stages[put % kSlots].entry = -1;
+      stages[put % kSlots].at = end_at;
+      mbar_arrive(full + 8 * (put % kSlots));
+      ++put;
+    }
+    // No copy outlives this thread, whoever gave up.
+    for (uint32_t x = freed; x != put; ++x)
+      if (!mbar_wait_bounded(full + 8 * (x % kSlots), x / kSlots & 1u, kDrainNs)) {
+        atomicOr(&cv.hdr->status, (uint32_t)kStatusTimeout);
+        break;
+      }
+    return;
+  }
 
+  // ================================================================ consumers
+  uint32_t meetings = 0;
+  auto meet = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(base + L::kMeet);
+    return wait(base + L::kMeet, meetings++ & 1u);
+  };
   // q of an entry: all channels, the kept ones in their order, and these as f16, each
-  // row by its own exponent.  A warp per query head.
-  auto stage_q = [&](int e, int buffer) {
+  // row by its own exponent.  A warp per query head; what it needs of memory is asked for
+  // a stage before it is laid out.
+  uint2 q_row = make_uint2(0u, 0u);
+  int16_t q_kept[4] = {0, 0, 0, 0};
+  int q_width = -1;                            // kept channels of the entry asked for; < 0: none
+  auto ask_q = [&](int e) {
     if (warp >= G) return;
     const EntryId id = entry_id(a, e);
-    const HeadDesc& hd = cv.heads[id.l * cv.Hkv + id.h];
-    const int k = hd.policy == kFull ? hd.n_kept : 0;
-    const uint16_t* q = a.q + (((size_t)id.lr * cv.B + id.b) * cv.Hq + (size_t)id.h * G + warp) * kHeadDim;
+    const HeadDesc& hd = heads[id.lr * cv.Hkv + id.h];
+    q_width = hd.policy == kFull ? hd.n_kept : 0;
+    q_row = reinterpret_cast<const uint2*>(
+        a.q + (((size_t)id.lr * cv.B + id.b) * cv.Hq + (size_t)id.h * G + warp) * kHeadDim)[lane];
     const int16_t* kept = cv.kept + ((size_t)id.l * cv.Hkv + id.h) * kHeadDim;
-    uint8_t* at = sm + Smem::kQ + buffer * 3 * Smem::kQBytes + warp * kQStride * 2;
-    *reinterpret_cast<uint2*>(at + 8 * lane) = reinterpret_cast<const uint2*>(q)[lane];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) q_kept[c] = kept[32 * c + lane];
+  };
+  auto lay_q = [&](int buffer) {
+    if (q_width < 0) return;
+    uint8_t* at = sm + L::kQ + buffer * 3 * L::kQBytes + warp * kQStride * 2;
+    *reinterpret_cast<uint2*>(at + 8 * lane) = q_row;
+    __syncwarp();
     uint16_t x[4];
     uint32_t top = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      x[c] = 32 * c < k ? q[kept[32 * c + lane]] : 0;
+      x[c] = 32 * c < q_width ? reinterpret_cast<const uint16_t*>(at)[q_kept[c]] : 0;
       top = max(top, (uint32_t)(x[c] >> 7 & 0xff));
     }
     const int exponent = max((int)__reduce_max_sync(0xffffffffu, top) - 127 - kRowTop, -120);
     const float f = power2(-exponent);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (32 * c >= k) continue;
-      reinterpret_cast<uint16_t*>(at + Smem::kQBytes)[32 * c + lane] = x[c];
-      reinterpret_cast<uint16_t*>(at + 2 * Smem::kQBytes)[32 * c + lane] =
-          (uint16_t)pack_f16x2(bf16_to_f32(x[c]) * f, 0.f);
+      if (32 * c >= q_width) continue;
+      reinterpret_cast<uint16_t*>(at + L::kQBytes)[32 * c + lane] = x[c];
+      const uint32_t y = pack_f16x2(bf16_to_f32(x[c]) * f, 0.f);
+      reinterpret_cast<uint16_t*>(at + 2 * L::kQBytes)[32 * c + lane] = (uint16_t)y;
     }
     if (lane == 0)
-      reinterpret_cast<float*>(sm + Smem::kBack)[buffer * kMaxGroup + warp] = power2(exponent) * a.scale_log2;
+      reinterpret_cast<float*>(sm + L::kBack)[buffer * kMaxGroup + warp] = power2(exponent) * a.scale_log2;
+    q_width = -1;
   };
-
-  copy_ahead();
   int buffer = 0;
-  stage_q(__shfl_sync(0xffffffffu, d_entry, 0), 0);
-  __syncthreads();
+  auto geometry_of = [&](int e) {
+    const EntryId id = entry_id(a, e);
+    return entry_geometry(cv, heads[id.lr * cv.Hkv + id.h], lens_of(e, id));
+  };
+  auto next_entry = [&](int e) {               // the next one that has a piece
+    for (++e; e < E && entry_cost(geometry_of(e)) == 0;) ++e;
+    return e;
+  };
+  {
+    // (the range may start behind the last piece of the entry it starts in)
+    int e = info.first_entry;
+    if (last_piece(geometry_of(e), info.first_off) < start) e = next_entry(e);
+    if (e < E) ask_q(e);
+    lay_q(0);
+  }
+  if (!meet()) return;
 
-  float o[8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  // The products' accumulators drop what lies below their last bit at every product,
+  // always towards zero; so they take a few stages', and their sums meet by fp32
+  // additions in the warp's merge slot.  (All of a segment in one accumulator: o of
+  // 131072 tokens is off by 1.1e-6.)
+  float o[8][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  bool flushed = false;                                    // the slot holds a sum
+  float* slot_o = merge_o + (warp * kHeads + 2 * tig) * kHeadDim + 8 * gid;
+  auto flush = [&]() {
+    if (kPack) {
+      // the lo halves' columns, two lanes on
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] += __shfl_down_sync(0xffffffffu, o[i][j], 2);
+    }
+    if (!kPack || tig < 2) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          float4* to = reinterpret_cast<float4*>(slot_o + (j & 1) * kHeadDim + 64 * (j >> 1) + i);
+          float4 v = make_float4(o[i][j], o[i + 1][j], o[i + 2][j], o[i + 3][j]);
+          if (flushed) {
+            const float4 w = *to;
+            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+          }
+          *to = v;
+        }
+      }
+    }
+    flushed = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  };
+  // what has been summed so far, times f0 and f1 (of this lane's columns)
+  auto rescale = [&](float f0, float f1) {
+    l0 *= f0;
+    l1 *= f1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[i][0] *= f0;
+      o[i][1] *= f1;
+      o[i][2] *= f0;
+      o[i][3] *= f1;
+    }
+    if (flushed && (!kPack || tig < 2)) {
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        const float f = j & 1 ? f1 : f0;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          float4* to = reinterpret_cast<float4*>(slot_o + (j & 1) * kHeadDim + 64 * (j >> 1) + i);
+          const float4 w = *to;
+          *to = make_float4(w.x * f, w.y * f, w.z * f, w.w * f);
+        }
+      }
+    }
+  };
+  float shift = 0.f;                                       // of m, since the segment's first sealed block
+  bool moved = false;
   const int my_q = kPack ? gid & 3 : gid;                  // the product's column of q
   const int c0 = kPack ? (2 * tig) & 3 : 2 * tig;          // head of this lane's first column
 
-  float shift = 0.f;                                       // of m, since the segment's first sealed block
-  bool moved = false;
-  // One step of the online softmax: x holds the slab's scores (log2 units, value
-  // exponents included) of rows gid (0, 1) and gid + 8 (2, 3), p receives their weights;
-  // m follows x + off.
-  auto softmax = [&](const float (&x)[4], float (&p)[4], float off) {
-    float t0 = fmaxf(x[0], x[2]) + off, t1 = fmaxf(x[1], x[3]) + off;
+  auto lds16 = [&](uint32_t at) { return *reinterpret_cast<const uint4*>(sm + at); };
+  // One step of the online softmax: x holds the scores (log2 units, value exponents
+  // included) of rows gid (0, 1) and gid + 8 (2, 3) of some slabs, p receives their
+  // weights; m follows x + off.
+  auto softmax = [&](auto slabs, const float (*x)[4], float (*p)[4], float off) {
+    constexpr int kN = decltype(slabs)::value;
+    float t0 = fmaxf(x[0][0], x[0][2]), t1 = fmaxf(x[0][1], x[0][3]);
+#pragma unroll
+    for (int n = 1; n < kN; ++n) {
+      t0 = fmaxf(t0, fmaxf(x[n][0], x[n][2]));
+      t1 = fmaxf(t1, fmaxf(x[n][1], x[n][3]));
+    }
+    t0 += off;
+    t1 += off;
     if (__any_sync(0xffffffffu, t0 > m0 + kRescaleGap || t1 > m1 + kRescaleGap)) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
@@ -449,143 +683,229 @@ __global__ void __launch_bounds__(kThreads, 1) decode_block_kernel(const __grid_
       const float f0 = m0 == n0 ? 1.f : ex2(m0 - n0), f1 = m1 == n1 ? 1.f : ex2(m1 - n1);
       m0 = n0;
       m1 = n1;
-      l0 *= f0;
-      l1 *= f1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i][0] *= f0;
-        o[i][1] *= f1;
-        o[i][2] *= f0;
-        o[i][3] *= f1;
-      }
+      rescale(f0, f1);
     }
-    p[0] = ex2(x[0] - m0);
-    p[1] = ex2(x[1] - m1);
-    p[2] = ex2(x[2] - m0);
-    p[3] = ex2(x[3] - m1);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      p[n][0] = ex2(x[n][0] - m0);
+      p[n][1] = ex2(x[n][1] - m1);
+      p[n][2] = ex2(x[n][2] - m0);
+      p[n][3] = ex2(x[n][3] - m1);
+    }
   };
 
-  while (put != got) {
-    copy_wait((int)(put - got) - 1);
-    __syncwarp();                              // (the scales are lane 0's copy)
-    const int slot = (int)(got % kSlots), meta = __shfl_sync(0xffffffffu, d_meta, slot);
-    const int type = meta >> 12 & 3, kv = meta >> 16;
-    const uint32_t at = ring + (meta & 255) * kUnit;
-    const uint32_t q_at = base + Smem::kQ + buffer * 3 * Smem::kQBytes + my_q * kQStride * 2 + 16 * tig;
-    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f}, p[4];
-    if (type == kSealed) {
-      const float2 scale =
-          *reinterpret_cast<const float2*>(sm + Smem::kScales + (warp * kSlots + slot) * 8);
-      const float* back = reinterpret_cast<const float*>(sm + Smem::kBack) + buffer * kMaxGroup + c0;
-      const float b0 = back[0] * scale.x, b1 = back[1] * scale.x;
-      const int exponent = (__float_as_int(scale.y) >> 23) - 127;        // (a scale is positive and normal)
-      const float f = scale.y * power2(-exponent), bias = (float)exponent;
+  // This warp's slab of each of kN sealed blocks: their products are independent until
+  // one softmax step joins them.
+  auto sealed = [&](auto slabs, auto words, uint32_t block0, uint32_t q_at) {
+    constexpr int kN = decltype(slabs)::value, kv = decltype(words)::value, k = 32 * kv;
+    constexpr uint32_t next = (uint32_t)block_bytes(k);
+    const uint32_t at = block0 + warp * kSlabRows * k + lane * 16,
+                   v_at = block0 + block_voff(k) + warp * kSlabRows * kHeadDim + lane * 16;
+    float s0[kN][4] = {}, s1[kN][4] = {}, x[kN][4], p[kN][4], f[kN], unit[kN];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (u >= kv) continue;
-        const uint4 w = lds16(at + u * kUnit), q = lds16(q_at + 2 * Smem::kQBytes + 64 * u);
-        uint32_t x[8];
-        codes(w.x, x[0], x[1]);
-        codes(w.y, x[2], x[3]);
-        codes(w.z, x[4], x[5]);
-        codes(w.w, x[6], x[7]);
-        mma_f16_16816(s0, x[0], x[4], x[1], x[5], q.x, q.y);
-        mma_f16_16816(s1, x[2], x[6], x[3], x[7], q.z, q.w);
+    for (int u = 0; u < kv; ++u) {
+      const uint4 q = lds16(q_at + 2 * L::kQBytes + 64 * u);
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const uint4 w = lds16(at + n * next + u * kUnit);
+        uint32_t c[8];
+        codes(w.x, c[0], c[1]);
+        codes(w.y, c[2], c[3]);
+        codes(w.z, c[4], c[5]);
+        codes(w.w, c[6], c[7]);
+        mma_f16(s0[n], c[0], c[4], c[1], c[5], q.x, q.y);
+        mma_f16(s1[n], c[2], c[6], c[3], c[7], q.z, q.w);
       }
-      const float x[4] = {fmaf(s0[0] + s1[0], b0, bias), fmaf(s0[1] + s1[1], b1, bias),
-                          fmaf(s0[2] + s1[2], b0, bias), fmaf(s0[3] + s1[3], b1, bias)};
-      if (!moved) {
+    }
+    const float* back = reinterpret_cast<const float*>(sm + L::kBack) + buffer * kMaxGroup + c0;
+    const float back0 = back[0], back1 = back[1];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const float2 scale = *reinterpret_cast<const float2*>(sm + block0 + n * next + block_soff(k));
+      const float b0 = back0 * scale.x, b1 = back1 * scale.x;
+      const int exponent = (__float_as_int(scale.y) >> 23) - 127;        // (a scale is positive and normal)
+      const float bias = (float)exponent;
+      unit[n] = power2(-exponent);
+      f[n] = scale.y * unit[n];
+      x[n][0] = fmaf(s0[n][0] + s1[n][0], b0, bias);
+      x[n][1] = fmaf(s0[n][1] + s1[n][1], b1, bias);
+      x[n][2] = fmaf(s0[n][2] + s1[n][2], b0, bias);
+      x[n][3] = fmaf(s0[n][3] + s1[n][3], b1, bias);
+      if (n == 0 && !moved) {
         moved = true;
         shift = bias - kWeightExp;
         const float up = power2(kWeightExp - exponent);
         m0 += shift;
         m1 += shift;
-        l0 *= up;
-        l1 *= up;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[i][j] *= up;
+        rescale(up, up);
       }
-      softmax(x, p, -(float)kWeightExp);
-      const float unit = power2(-exponent);
-      l0 = fmaf(p[0] + p[2], unit, l0);
-      l1 = fmaf(p[1] + p[3], unit, l1);
-      const float y0 = p[0] * f, y1 = p[1] * f, y2 = p[2] * f, y3 = p[3] * f;
+    }
+    softmax(slabs, x, p, -(float)kWeightExp);
+    uint32_t pt[kN][4];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      l0 = fmaf(p[n][0] + p[n][2], unit[n], l0);
+      l1 = fmaf(p[n][1] + p[n][3], unit[n], l1);
+      const float y0 = p[n][0] * f[n], y1 = p[n][1] * f[n], y2 = p[n][2] * f[n], y3 = p[n][3] * f[n];
       const uint32_t h01 = pack_f16x2(y0, y1), h23 = pack_f16x2(y2, y3);
       const uint32_t r01 = pack_f16x2(y0 - f16_lo(h01), y1 - f16_hi(h01));
       const uint32_t r23 = pack_f16x2(y2 - f16_lo(h23), y3 - f16_hi(h23));
-      const uint32_t p0 = movmatrix_trans(kPack && tig >= 2 ? r01 : h01);
-      const uint32_t p1 = movmatrix_trans(kPack && tig >= 2 ? r23 : h23);
-      const uint32_t p2 = kPack ? 0u : movmatrix_trans(r01), p3 = kPack ? 0u : movmatrix_trans(r23);
-      const uint32_t v_at = at + kv * kUnit;
+      pt[n][0] = transposed(kPack && tig >= 2 ? r01 : h01);
+      pt[n][1] = transposed(kPack && tig >= 2 ? r23 : h23);
+      pt[n][2] = kPack ? 0u : transposed(r01);
+      pt[n][3] = kPack ? 0u : transposed(r23);
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const uint4 w = lds16(v_at + u * kUnit);
-        uint32_t x[8];
-        codes(w.x, x[0], x[2]);
-        codes(w.y, x[1], x[3]);
-        codes(w.z, x[4], x[6]);
-        codes(w.w, x[5], x[7]);
-        mma_f16_16816(o[2 * u], x[0], x[1], x[2], x[3], p0, p1);
-        mma_f16_16816(o[2 * u + 1], x[4], x[5], x[6], x[7], p0, p1);
+        const uint4 w = lds16(v_at + n * next + u * kUnit);
+        uint32_t c[8];
+        codes(w.x, c[0], c[2]);
+        codes(w.y, c[1], c[3]);
+        codes(w.z, c[4], c[6]);
+        codes(w.w, c[5], c[7]);
+        mma_f16(o[2 * u], c[0], c[1], c[2], c[3], pt[n][0], pt[n][1]);
+        mma_f16(o[2 * u + 1], c[4], c[5], c[6], c[7], pt[n][0], pt[n][1]);
         if (!kPack) {
-          mma_f16_16816(o[2 * u], x[0], x[1], x[2], x[3], p2, p3);
-          mma_f16_16816(o[2 * u + 1], x[4], x[5], x[6], x[7], p2, p3);
+          mma_f16(o[2 * u], c[0], c[1], c[2], c[3], pt[n][2], pt[n][3]);
+          mma_f16(o[2 * u + 1], c[4], c[5], c[6], c[7], pt[n][2], pt[n][3]);
         }
       }
-    } else if (type != kNone) {
-      const int rows = (meta >> 8 & 15) + 1;
-      const uint32_t q_row = q_at + (type == kOpen ? Smem::kQBytes : 0);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (u >= kv) continue;
-        const uint4 w = lds16(at + 2 * u * kUnit), z = lds16(at + (2 * u + 1) * kUnit), q = lds16(q_row + 64 * u);
-        mma_bf16_16816(s0, w.x, z.x, w.y, z.y, q.x, q.y);
-        mma_bf16_16816(s1, w.z, z.z, w.w, z.w, q.z, q.w);
-      }
-      const bool va = gid < rows, vb = gid + 8 < rows;
-      const float x[4] = {va ? (s0[0] + s1[0]) * a.scale_log2 : -INFINITY, va ? (s0[1] + s1[1]) * a.scale_log2 : -INFINITY,
-                          vb ? (s0[2] + s1[2]) * a.scale_log2 : -INFINITY, vb ? (s0[3] + s1[3]) * a.scale_log2 : -INFINITY};
-      softmax(x, p, shift);
-      const uint32_t h01 = pack_bf16x2(p[0], p[1]), h23 = pack_bf16x2(p[2], p[3]);
-      const uint32_t r01 = pack_bf16x2(p[0] - bf16_lo(h01), p[1] - bf16_hi(h01));
-      const uint32_t r23 = pack_bf16x2(p[2] - bf16_lo(h23), p[3] - bf16_hi(h23));
-      // (the weights as the product has them, 2^-16 off at most: where one of them is
-      // nearly all, that cancels)
-      l0 += (bf16_lo(h01) + bf16_lo(r01)) + (bf16_lo(h23) + bf16_lo(r23));
-      l1 += (bf16_hi(h01) + bf16_hi(r01)) + (bf16_hi(h23) + bf16_hi(r23));
-      const uint32_t p0 = movmatrix_trans(kPack && tig >= 2 ? r01 : h01);
-      const uint32_t p1 = movmatrix_trans(kPack && tig >= 2 ? r23 : h23);
-      const uint32_t p2 = kPack ? 0u : movmatrix_trans(r01), p3 = kPack ? 0u : movmatrix_trans(r23);
-      const uint32_t v_at = at + 2 * kv * kUnit;
-      uint4 v[4][2];
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) v[t][half] = lds16(v_at + (2 * t + half) * kUnit);
-      auto word = [](const uint4& w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; };
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t sel = i & 1 ? 0x7632u : 0x5410u;
-        const uint32_t x0 = prmt(word(v[0][0], i >> 1), word(v[1][0], i >> 1), sel);
-        const uint32_t x1 = prmt(word(v[0][1], i >> 1), word(v[1][1], i >> 1), sel);
-        const uint32_t x2 = prmt(word(v[2][0], i >> 1), word(v[3][0], i >> 1), sel);
-        const uint32_t x3 = prmt(word(v[2][1], i >> 1), word(v[3][1], i >> 1), sel);
-        mma_bf16_16816(o[i], x0, x1, x2, x3, p0, p1);
-        if (!kPack) mma_bf16_16816(o[i], x0, x1, x2, x3, p2, p3);
-      }
     }
-    const int entry = __shfl_sync(0xffffffffu, d_entry, slot), ctas = __shfl_sync(0xffffffffu, d_ctas, slot);
-    // (this slab's words have been read by the lane that copies over them)
-    ++got;
-    if (put != got) {
-      const int t = __shfl_sync(0xffffffffu, d_meta, got % kSlots) & 255;
-      if (t < tail) wrapped = false;
-      tail = t;
+  };
+
+  // This warp's 16 of `count` bf16 rows on 32 kv channels.  Rows behind the last are read
+  // as that one, and weigh nothing.
+  auto rows = [&](auto words, uint32_t at, uint32_t q_at, int count, bool open) {
+    constexpr int kv = decltype(words)::value, width = 32 * kv;
+    const int n = min(count - 16 * warp, 16), boxes = (count + kBoxRows - 1) / kBoxRows;
+    const uint32_t box = (uint32_t)warp / (kBoxRows / 16), r16 = (uint32_t)warp % (kBoxRows / 16) * 16;
+    const uint32_t k_at = at + box * (kBoxRows * 2 * width),
+                   v_at = at + boxes * (kBoxRows * 2 * width) + box * (kBoxRows * 2 * kHeadDim);
+    // 16-byte word c of row r of the box: 64-channel halves with 128-byte swizzle, or
+    // 32-channel stripes with 64-byte swizzle
+    auto word128 = [&](uint32_t from, uint32_t r, uint32_t c) {
+      return from + (c >> 3) * (kBoxRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    };
+    auto key = [&](uint32_t r, uint32_t c) {
+      return (kv & 1) == 0 ? word128(k_at, r, c)
+                           : k_at + (c >> 2) * (kBoxRows * 64) + r * 64 + (((c & 3) ^ (r >> 1 & 3)) << 4);
+    };
+    // The product's row (and V's depth) j is the tile's row j, odd ones with bit 2 turned:
+    // so the eight lanes that shared memory serves at once find their words, swizzled by
+    // row, in eight different places, of K and of V.
+    const int ka = gid ^ (gid & 1) << 2, kb = ka + 8;
+    const uint32_t ra = r16 + min(ka, n - 1), rb = r16 + min(kb, n - 1);
+    const uint32_t q_from = q_at + (open ? L::kQBytes : 0);
+    uint4 w[kv], z[kv], q[kv];
+#pragma unroll
+    for (int u = 0; u < kv; ++u) {
+      w[u] = lds16(key(ra, 4 * u + tig));
+      z[u] = lds16(key(rb, 4 * u + tig));
+      q[u] = lds16(q_from + 64 * u);
     }
-    copy_ahead();
-    if ((meta >> 14 & 1) == 0) continue;
+    float s0[4] = {}, s1[4] = {};
+#pragma unroll
+    for (int u = 0; u < kv; ++u) {
+      mma_bf16(s0, w[u].x, z[u].x, w[u].y, z[u].y, q[u].x, q[u].y);
+      mma_bf16(s1, w[u].z, z[u].z, w[u].w, z[u].w, q[u].z, q[u].w);
+    }
+    uint4 v[4][2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t r = r16 + min((2 * tig ^ (t & 1) * 5) + 4 * (t & 2), n - 1);
+      v[t][0] = lds16(word128(v_at, r, gid));
+      v[t][1] = lds16(word128(v_at, r, gid + 8));
+    }
+    const bool va = ka < n, vb = kb < n;
+    float x[1][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[0][i] = (i < 2 ? va : vb) ? (s0[i] + s1[i]) * a.scale_log2 : -INFINITY;
+    float p[1][4];
+    softmax(std::integral_constant<int, 1>(), x, p, shift);
+    // P as the sum of three bf16 numbers (2^-24 of it is left; of two 2^-16, with the
+    // two columns of one product 2.5e-6 of o instead of 4e-7)
+    auto split = [](float a, float b, uint32_t (&t)[3]) {
+#pragma unroll
+      for (int y = 0; y < 3; ++y) {
+        t[y] = pack_bf16x2(a, b);
+        a -= bf16_lo(t[y]);
+        b -= bf16_hi(t[y]);
+      }
+    };
+    l0 += p[0][0] + p[0][2];
+    l1 += p[0][1] + p[0][3];
+    uint32_t t01[3], t23[3];
+    split(p[0][0], p[0][1], t01);
+    split(p[0][2], p[0][3], t23);
+    const bool low = kPack && tig >= 2;
+    const uint32_t p0 = transposed(low ? t01[1] : t01[0]), p1 = transposed(low ? t23[1] : t23[0]);
+    const uint32_t p2 = transposed(low ? 0u : t01[2]), p3 = transposed(low ? 0u : t23[2]);
+    const uint32_t p4 = kPack ? 0u : transposed(t01[1]), p5 = kPack ? 0u : transposed(t23[1]);
+    auto word = [](const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t sel = i & 1 ? 0x7632u : 0x5410u;
+      const uint32_t x0 = prmt(word(v[0][0], i >> 1), word(v[1][0], i >> 1), sel);
+      const uint32_t x1 = prmt(word(v[0][1], i >> 1), word(v[1][1], i >> 1), sel);
+      const uint32_t x2 = prmt(word(v[2][0], i >> 1), word(v[3][0], i >> 1), sel);
+      const uint32_t x3 = prmt(word(v[2][1], i >> 1), word(v[3][1], i >> 1), sel);
+      mma_bf16(o[i], x0, x1, x2, x3, p0, p1);
+      mma_bf16(o[i], x0, x1, x2, x3, p2, p3);
+      if (!kPack) mma_bf16(o[i], x0, x1, x2, x3, p4, p5);
+    }
+  };
+
+  uint32_t stage = 0;                                      // of the segment
+  for (uint32_t taken = 0;; ++taken, ++stage) {
+    const int slot = (int)(taken % kSlots);
+    if (!wait(full + 8 * slot, taken / kSlots & 1u)) return;
+    const int4 d0 = *reinterpret_cast<const int4*>(&stages[slot]);
+    const int entry = d0.x, type = d0.y & 0xffff, flags = d0.y >> 16, count = d0.z & 0xffff, width = d0.z >> 16;
+    if (entry < 0) return;
+    if (flags & kFirst) {
+      // q of the next segment's entry
+      const int e = next_entry(entry);
+      if (e < E) ask_q(e);
+    }
+    const uint32_t at = L::kRing + (uint32_t)d0.w;
+    const uint32_t q_at = L::kQ + buffer * 3 * L::kQBytes + my_q * kQStride * 2 + 16 * tig;
+    if (type == kSealed) {
+      // whole stages at once, what is left at an end block by block
+      auto blocks = [&](auto whole, auto words) {
+        constexpr int kWhole = decltype(whole)::value;
+        if (kWhole > 1 && count == kWhole) {
+          sealed(whole, words, at, q_at);
+        } else {
+#pragma unroll 1
+          for (int x = 0; x < count; ++x)
+            sealed(std::integral_constant<int, 1>(), words, at + x * block_bytes(32 * decltype(words)::value), q_at);
+        }
+      };
+      const std::integral_constant<int, 2> some;
+      if (width == 32) blocks(std::integral_constant<int, 3>(), std::integral_constant<int, 1>());
+      else if (width == 64) blocks(some, std::integral_constant<int, 2>());
+      else if (width == 96) blocks(some, std::integral_constant<int, 3>());
+      else blocks(some, std::integral_constant<int, 4>());
+    } else if (16 * warp < count) {
+      const bool open = type == kOpen;
+      if (!open) rows(std::integral_constant<int, 4>(), at, q_at, count, false);
+      else if (width == 32) rows(std::integral_constant<int, 1>(), at, q_at, count, true);
+      else if (width == 64) rows(std::integral_constant<int, 2>(), at, q_at, count, true);
+      else if (width == 96) rows(std::integral_constant<int, 3>(), at, q_at, count, true);
+      else rows(std::integral_constant<int, 4>(), at, q_at, count, true);
+    }
+    lay_q(buffer ^ 1);
+    if ((stage & (kFlush - 1)) == kFlush - 1 || (flags & kLast) != 0) flush();
+    __syncwarp();
+    if ((flags & kLast) == 0) {
+      if (lane == 0) mbar_arrive(empty + 8 * slot);
+      continue;
+    }
+    const int first_cta = stages[slot].first_cta, last_cta = stages[slot].last_cta;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + 8 * slot);
 
     // ---- end of a segment: the warps' (o, m, l) meet in shared memory
 #pragma unroll
@@ -593,85 +913,65 @@ __global__ void __launch_bounds__(kThreads, 1) decode_block_kernel(const __grid_
       l0 += __shfl_xor_sync(0xffffffffu, l0, d);
       l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
-    if (kPack) {
-      // the lo halves' columns, two lanes on
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] += __shfl_down_sync(0xffffffffu, o[i][j], 2);
-    }
-    if (!kPack || tig < 2) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float* to = merge_o + (warp * kHeads + 2 * tig + c) * kHeadDim + 8 * gid;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int j = 2 * half + c;
-          *reinterpret_cast<float4*>(to + 64 * half) = make_float4(o[0][j], o[1][j], o[2][j], o[3][j]);
-          *reinterpret_cast<float4*>(to + 64 * half + 4) = make_float4(o[4][j], o[5][j], o[6][j], o[7][j]);
-        }
-      }
-      if (gid == 0) {
-        merge_m[warp * kHeads + 2 * tig] = m0;
-        merge_m[warp * kHeads + 2 * tig + 1] = m1;
-        merge_l[warp * kHeads + 2 * tig] = l0;
-        merge_l[warp * kHeads + 2 * tig + 1] = l1;
-      }
+    if (gid == 0 && (!kPack || tig < 2)) {
+      merge_m[warp * kHeads + 2 * tig] = m0;
+      merge_m[warp * kHeads + 2 * tig + 1] = m1;
+      merge_l[warp * kHeads + 2 * tig] = l0;
+      merge_l[warp * kHeads + 2 * tig + 1] = l1;
     }
     m0 = m1 = -INFINITY;
     l0 = l1 = shift = 0.f;
-    moved = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    __syncthreads();
-    // (each warp has a slab of the next segment by now, if there is one)
-    if (put != got) stage_q(__shfl_sync(0xffffffffu, d_entry, got % kSlots), buffer ^ 1);
+    moved = flushed = false;
+    stage = (uint32_t)-1;                                  // (the next one is a segment's first)
     buffer ^= 1;
-    const int first_cta = ctas & 0xffff, last_cta = ctas >> 16;
+    if (!meet()) return;
     const EntryId id = entry_id(a, entry);
     float* dst = a.o + (((size_t)id.lr * cv.B + id.b) * cv.Hq + (size_t)id.h * G) * kHeadDim;
     const bool single = first_cta == last_cta;
-    const int head_q = tid >> 5, dd = (tid & 31) * 4;      // a warp per query head, four channels a lane
-    if (head_q < G) {
-      float M = -INFINITY, L = 0.f;
+    const int g = tid >> 5, dd = (tid & 31) * 4;           // a warp per query head, four channels a lane
+    if (g < G) {
+      float M = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, merge_m[w * kHeads + head_q]);
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, merge_m[w * kHeads + g]);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float m = merge_m[w * kHeads + head_q], f = m == -INFINITY ? 0.f : ex2(m - M);
-        const float4 v = *reinterpret_cast<const float4*>(merge_o + (w * kHeads + head_q) * kHeadDim + dd);
+        const float m = merge_m[w * kHeads + g];
+        if (m == -INFINITY) continue;                      // (and whatever its slot holds)
+        const float f = ex2(m - M);
+        const float4 v = *reinterpret_cast<const float4*>(merge_o + (w * kHeads + g) * kHeadDim + dd);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);
         acc.w = fmaf(f, v.w, acc.w);
-        L = fmaf(f, merge_l[w * kHeads + head_q], L);
+        sum = fmaf(f, merge_l[w * kHeads + g], sum);
       }
       if (single) {
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        *reinterpret_cast<float4*>(dst + head_q * kHeadDim + dd) =
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        *reinterpret_cast<float4*>(dst + g * kHeadDim + dd) =
             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       } else {
-        const size_t at_part = ((size_t)cta + entry) * G + head_q;
+        const size_t at_part = ((size_t)cta + entry) * G + g;
         *reinterpret_cast<float4*>(a.part + at_part * kHeadDim + dd) = acc;
-        if (dd == 0) a.part_ml[at_part] = make_float2(M, L);
+        if (dd == 0) a.part_ml[at_part] = make_float2(M, sum);
       }
     }
-    __syncthreads();                           // partials written, merge slots read, the next q staged
+    if (!meet()) return;                                   // slots are read, partials written, the next q is there
     if (single) continue;
     // the last of the entry's CTAs to get here merges all their partials, in order
     if (tid == 0) {
       const int done = atom_add_acq_rel_gpu(&a.counters[entry], 1);
-      first_at[1] = done == last_cta - first_cta;
+      info.last = done == last_cta - first_cta;
       if (done == last_cta - first_cta) a.counters[entry] = 0;
     }
-    __syncthreads();
-    if (first_at[1] == 0 || head_q >= G) continue;
+    if (!meet()) return;
+    if (info.last == 0 || g >= G) continue;
     const int np = last_cta - first_cta + 1;
-    const size_t part0 = ((size_t)first_cta + entry) * G + head_q;
-    constexpr int kAhead = 16;                 // partials in flight
-    float M = -INFINITY, L = 0.f;
+    const size_t part0 = ((size_t)first_cta + entry) * G + g;
+    constexpr int kAhead = 8;                              // partials in flight
+    float M = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int c = 0; c < np; c += kAhead) {
       float4 v[kAhead];
       float2 ml[kAhead];
@@ -687,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_block_kernel(const __grid_
       if (top == -INFINITY) continue;
       const float f = M == -INFINITY ? 0.f : ex2(M - top);
       acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-      L *= f;
+      sum *= f;
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const float y = c + u < np && ml[u].x != -INFINITY ? ex2(ml[u].x - top) : 0.f;
@@ -695,28 +995,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_block_kernel(const __grid_
         acc.y = fmaf(y, v[u].y, acc.y);
         acc.z = fmaf(y, v[u].z, acc.z);
         acc.w = fmaf(y, v[u].w, acc.w);
-        L = fmaf(y, ml[u].y, L);
+        sum = fmaf(y, ml[u].y, sum);
       }
       M = top;
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    *reinterpret_cast<float4*>(dst + head_q * kHeadDim + dd) =
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    *reinterpret_cast<float4*>(dst + g * kHeadDim + dd) =
         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   }
 }
 
 template <bool kPack>
-cudaError_t launch(const DecodeArgs& args, int ctas, cudaStream_t stream) {
+cudaError_t launch(const BlockMaps& maps, const DecodeArgs& args, int ctas, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t err = set_smem_limit_once(decode_block_kernel<kPack>, Smem::kBytes, done);
+  constexpr int kSmem = Smem<kPack>::kAll;
+  const cudaError_t err = set_smem_limit_once(decode_block_kernel<kPack>, kSmem, done);
   if (err != cudaSuccess) return err;
-  return launch_after(decode_block_kernel<kPack>, dim3((unsigned)ctas), kThreads, Smem::kBytes, stream, args);
+  return launch_after(decode_block_kernel<kPack>, dim3((unsigned)ctas), kThreads, kSmem, stream, maps, args);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_block(const DecodeArgs& args, int ctas, cudaStream_t stream) {
-  return args.cv.G <= 4 ? launch<true>(args, ctas, stream) : launch<false>(args, ctas, stream);
+cudaError_t launch_decode_block(const BlockMaps& maps, const DecodeArgs& args, int ctas, cudaStream_t stream) {
+  return args.cv.G <= 4 ? launch<true>(maps, args, ctas, stream) : launch<false>(maps, args, ctas, stream);
 }
 
 }  // namespace lk

@@ -68,6 +68,12 @@ struct DecodeArgs {
   FastDiv div_cost_b[5], div_cost_q[5];
 };
 
+// FP8_BLOCK caches: flat maps of the pools, 64 rows to a box.
+constexpr int kBlockBoxRows = 64;
+struct BlockMaps {
+  CUtensorMap pool[kNumPools];
+};
+
 struct AppendArgs {
   CacheView cv;
   int32_t layer;            // first layer
@@ -226,7 +232,7 @@ inline cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads,
 
 size_t decode_smem_bytes();
 cudaError_t launch_decode(const DecodeMaps& maps, const DecodeArgs& args, int ctas, cudaStream_t stream);
-cudaError_t launch_decode_block(const DecodeArgs& args, int ctas, cudaStream_t stream);    // FP8_BLOCK middles
+cudaError_t launch_decode_block(const BlockMaps& maps, const DecodeArgs& args, int ctas, cudaStream_t stream);
 cudaError_t launch_append(const AppendArgs& args, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& args, bool has_special, int num_sms, cudaStream_t stream);
 cudaError_t launch_release(const CacheView& cv, int b, cudaStream_t stream);

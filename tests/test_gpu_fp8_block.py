@@ -414,3 +414,30 @@ def test_prompt_steps_and_verification_together(cuda):
     held += np.array([3, 0], np.int32)
     case.cache.check()
     case.check_layout(0, held)
+
+
+@pytest.mark.parametrize("paged", [False, True], ids=["flat", "paged"])
+def test_waits_that_run_out(cuda, paged):
+    """With a limit of 0 every wait of a decode that is not complete at once runs
+    out: the call ends and says so, and with the limit back and the workspace
+    zeroed the next one is right."""
+    w = TINY.scaled(num_kv_heads=4, num_q_heads=16, batch=3, sink=4, local=30)
+    held = [1400, 1, 260]
+    case = _filled(w, S.masks_with_counts(w, (32, 64, 96, 128)), held, **(dict(middle_tokens=4000) if paged else {}))
+    q = case.q(0, max(held))
+    want = case.cache.decode(0, q).clone()
+    case.cache.check()
+    for ctas in (1, 4, 0):
+        case.cache.set_decode_ctas(ctas)
+        case.cache.set_wait_limit(0)
+        case.cache.decode(0, q)
+        with pytest.raises(lkb.LeankError) as e:
+            case.cache.check()
+        assert e.value.status == lkb.LK_ERR_TIMEOUT
+        case.cache.check()
+        case.cache.set_wait_limit(10 ** 9)
+        case.cache.workspace_init()
+        o = case.cache.decode(0, q)
+        case.cache.check()
+        _check_decode(case, 0, q, o, held)
+    assert torch.equal(o, want)
