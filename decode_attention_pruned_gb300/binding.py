@@ -245,6 +245,24 @@ def _same_device(device, *tensors):
             raise ValueError(f"a tensor is on {t.device}, the call on {device}")
 
 
+def _spaced(t, shape, bf16, device, what):
+    """_token_stride of a tensor on `device`, [B, n, heads, 128] or [B, heads, 128].
+    What is as it should be is seen at once: a call of one token takes the device 6 us,
+    and the host as long."""
+    try:
+        if t.dtype is bf16 and t.device == device and t.shape == shape:
+            s, dense = t.stride(), shape[-2] * 128
+            n = shape[1] if len(shape) == 4 else 1
+            step = s[1] if n > 1 else s[0] if shape[0] > 1 else dense
+            if s[-1] == 1 and s[-2] == 128 and step >= dense and (n <= 1 or shape[0] <= 1 or s[0] == n * step):
+                return step
+    except AttributeError:
+        pass
+    step = _token_stride(t, shape[-2], shape[:-2], what)
+    _same_device(device, t)
+    return step
+
+
 class Rope:
     """lk_build_rope: rotary positions of heads of 128 channels.
 
@@ -723,28 +741,26 @@ class Cache:
     # -- with the rotation on the way
     def _rope_chunk(self, rope, q, k, v, positions, lens, ids):
         """The lk_chunk of tokens to be turned, given as [B, n, heads, 128] or, one of
-        each sequence, [B, heads, 128]; and what it points to."""
+        each sequence, [B, heads, 128]; what it points to, q's shape and the device."""
         import torch
-        B, H = self.batch, self.plan.num_kv_heads
-        lead = (B, k.shape[1]) if k.dim() == 4 else (B,)
-        c = Chunk()
-        c.n_max = lead[1] if len(lead) > 1 else 1
-        if q is not None:
-            c.q, c.q_stride = q.data_ptr(), _token_stride(q, self.plan.num_q_heads, lead, "q")
-        c.k, c.k_stride = k.data_ptr(), _token_stride(k, H, lead, "k")
-        c.v, c.v_stride = v.data_ptr(), _token_stride(v, H, lead, "v")
+        B, device, plan, bf16 = self.batch, self.buffer.device, self.plan, torch.bfloat16
+        lead = (B, k.shape[1]) if k.ndim == 4 else (B,)
+        shape, q_shape = (*lead, plan.num_kv_heads, 128), (*lead, plan.num_q_heads, 128)
+        k_stride, v_stride = _spaced(k, shape, bf16, device, "k"), _spaced(v, shape, bf16, device, "v")
+        q_ptr, q_stride = (None, 0) if q is None else (q.data_ptr(), _spaced(q, q_shape, bf16, device, "q"))
         if ids is not None:
             _need(ids, torch.int32, lead, "ids")
-            c.ids = ids.data_ptr()
+            _same_device(device, ids)
         if positions is not None:
             _need(positions, torch.int32, rope.axes + lead, "positions")
+            _same_device(device, positions)
         if lens is not None:
             lens = np.ascontiguousarray(lens, dtype=np.int32)
             if lens.shape != (B,):
                 raise ValueError(f"lens shape {lens.shape}")
-            c.lens = lens.ctypes.data
-        _same_device(self.buffer.device, q, k, v, ids, positions)
-        return c, lens, (*lead, self.plan.num_q_heads, 128)
+        c = Chunk(q_ptr, k.data_ptr(), v.data_ptr(), _ptr(ids), _ptr(lens), q_stride, k_stride, v_stride,
+                  lead[1] if len(lead) > 1 else 1)
+        return c, lens, q_shape, device
 
     def append_rope(self, layer, rope, k, v, positions=None, q=None, q_out=None, lens=None, ids=None, stream=None):
         """lk_append_rope: k, v [B, n, Hkv, 128] bf16 (tokens evenly spaced), or one
@@ -754,31 +770,29 @@ class Cache:
         turned queries go to q_out, a new dense tensor unless given (q itself may be);
         returns q_out.  Rows past a sequence's length are left as they are."""
         import torch
-        c, lens, shape = self._rope_chunk(rope, q, k, v, positions, lens, ids)
+        c, lens, shape, device = self._rope_chunk(rope, q, k, v, positions, lens, ids)
         out, step = None, 0
         if q is not None:
             if q_out is None:
-                q_out = _empty(shape, torch.bfloat16, q.device, stream)
-            out, step = q_out.data_ptr(), _token_stride(q_out, shape[-2], shape[:-2], "q_out")
-            _same_device(self.buffer.device, q_out)
+                q_out = _empty(shape, torch.bfloat16, device, stream)
+            out, step = q_out.data_ptr(), _spaced(q_out, shape, torch.bfloat16, device, "q_out")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        _check(_lib.lk_append_rope(self._h, layer, rope._h, ctypes.byref(c), _ptr(positions), out, step,
-                                   _stream(stream)))
+        _check(_lib.lk_append_rope(self._h, layer, rope._h, c, _ptr(positions), out, step, _stream(stream)))
         return q_out
 
     def step_rope(self, layer, rope, q, k, v, positions=None, ids=None, o=None, stream=None):
         """lk_step_rope: append_rope of one token of every sequence (q [B, Hq, 128],
         k, v [B, Hkv, 128]), then attention with the turned queries -> o fp32."""
         import torch
-        if k.dim() != 3:
+        if k.ndim != 3:
             raise ValueError(f"k: expected [B, Hkv, 128], got {tuple(k.shape)}")
-        c, _, shape = self._rope_chunk(rope, q, k, v, positions, None, ids)
+        c, _, shape, device = self._rope_chunk(rope, q, k, v, positions, None, ids)
         if o is None:
-            o = _empty(shape, torch.float32, q.device, stream)
+            o = _empty(shape, torch.float32, device, stream)
         _need(o, torch.float32, shape, "o")
-        _same_device(self.buffer.device, o)
-        _check(_lib.lk_step_rope(self._h, layer, rope._h, ctypes.byref(c), _ptr(positions), o.data_ptr(),
+        _same_device(device, o)
+        _check(_lib.lk_step_rope(self._h, layer, rope._h, c, _ptr(positions), o.data_ptr(),
                                  self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
         return o
 
