@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -63,6 +64,10 @@ class Chunk(ctypes.Structure):
                 ("v_stride", ctypes.c_int64), ("n_max", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+# The same as bytes, made in a third of the time.
+_pack_chunk = struct.Struct("PPPPPqqqii").pack
+
+
 class RopeDesc(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
                 ("trained_positions", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
@@ -115,8 +120,8 @@ SIGNATURES = {
     "lk_build_rope_axes": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(RopeAxes), ctypes.POINTER(_vp)]),
     "lk_rope_destroy": (None, [_vp]),
     "lk_rope_apply": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
-    "lk_append_rope": (ctypes.c_int, [_vp, _i32, _vp, ctypes.POINTER(Chunk), _vp, _vp, _i64, _vp]),
-    "lk_step_rope": (ctypes.c_int, [_vp, _i32, _vp, ctypes.POINTER(Chunk), _vp, _vp, _vp, _sz, _vp]),
+    "lk_append_rope": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "lk_step_rope": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "lk_cache_length": (ctypes.c_int, [_vp, _i32, ctypes.POINTER(_i32)]),
     "lk_cache_lengths": (ctypes.c_int, [_vp, _i32, _vp]),
     "lk_cache_region": (ctypes.c_int, [_vp, _i32, _i32, _i32, ctypes.POINTER(RegionInfo)]),
@@ -740,14 +745,15 @@ class Cache:
 
     # -- with the rotation on the way
     def _rope_chunk(self, rope, q, k, v, positions, lens, ids):
-        """The lk_chunk of tokens to be turned, given as [B, n, heads, 128] or, one of
-        each sequence, [B, heads, 128]; what it points to, q's shape and the device."""
+        """The lk_chunk (as bytes) of tokens to be turned, given as [B, n, heads, 128]
+        or, one of each sequence, [B, heads, 128]; what it points to, q's shape and the
+        device."""
         import torch
         B, device, plan, bf16 = self.batch, self.buffer.device, self.plan, torch.bfloat16
         lead = (B, k.shape[1]) if k.ndim == 4 else (B,)
         shape, q_shape = (*lead, plan.num_kv_heads, 128), (*lead, plan.num_q_heads, 128)
         k_stride, v_stride = _spaced(k, shape, bf16, device, "k"), _spaced(v, shape, bf16, device, "v")
-        q_ptr, q_stride = (None, 0) if q is None else (q.data_ptr(), _spaced(q, q_shape, bf16, device, "q"))
+        q_ptr, q_stride = (0, 0) if q is None else (q.data_ptr(), _spaced(q, q_shape, bf16, device, "q"))
         if ids is not None:
             _need(ids, torch.int32, lead, "ids")
             _same_device(device, ids)
@@ -758,8 +764,9 @@ class Cache:
             lens = np.ascontiguousarray(lens, dtype=np.int32)
             if lens.shape != (B,):
                 raise ValueError(f"lens shape {lens.shape}")
-        c = Chunk(q_ptr, k.data_ptr(), v.data_ptr(), _ptr(ids), _ptr(lens), q_stride, k_stride, v_stride,
-                  lead[1] if len(lead) > 1 else 1)
+        c = _pack_chunk(q_ptr, k.data_ptr(), v.data_ptr(), 0 if ids is None else ids.data_ptr(),
+                        0 if lens is None else lens.ctypes.data, q_stride, k_stride, v_stride,
+                        lead[1] if len(lead) > 1 else 1, 0)
         return c, lens, q_shape, device
 
     def append_rope(self, layer, rope, k, v, positions=None, q=None, q_out=None, lens=None, ids=None, stream=None):
