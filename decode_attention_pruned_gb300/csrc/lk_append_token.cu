@@ -112,6 +112,7 @@ __device__ void seal_tail(const TokenArgs& a, SealSmem& sm, int layer, int b, in
         u = reinterpret_cast<const uint4*>(row)[0];
         v = reinterpret_cast<const uint4*>(row)[1];
       },
+      [](int, uint4&, uint4&) {},
       [](int slot, int& c0, int& c1) {
         c0 = 16 * slot;
         c1 = c0 + 8;

@@ -66,13 +66,14 @@ __device__ __forceinline__ const uint16_t* v_token(const ChunkArgs& a, int b, in
   return a.v + ((int64_t)b * a.n_max + i) * a.v_stride + h * kHeadDim;
 }
 
-// Paged caches: a thread per (sequence, head) pops the pages between the
-// held and the new length.
+// Paged caches: a warp per (sequence, head) pops the pages between the held and
+// the new length.  (A thread for each: 9 us for the 35 pages of a head of 4500
+// tokens, one load after another.)
 __global__ void __launch_bounds__(256) chunk_pages_kernel(const __grid_constant__ ChunkArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   const CacheView& cv = a.cv;
-  const int x = blockIdx.x * blockDim.x + threadIdx.x;
+  const int x = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (x >= a.nb * cv.Hkv) return;
   const int i = x / cv.Hkv, h = x % cv.Hkv;
   const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + h];
@@ -80,8 +81,17 @@ __global__ void __launch_bounds__(256) chunk_pages_kernel(const __grid_constant_
   int N;
   const int n = chunk_len(a, i, N);
   if (n == 0) return;
-  const int first = min(pages_at(cv, N), cv.max_pages), last = min(pages_at(cv, N + n), cv.max_pages);
-  pop_pages(cv, hd, last - first, page_row(cv, a.layer, a.b0 + i, h) + first);
+  const int first = min(pages_at(cv, N), cv.max_pages), k = min(pages_at(cv, N + n), cv.max_pages) - first;
+  if (k <= 0) return;
+  int32_t* dst = page_row(cv, a.layer, a.b0 + i, h) + first;
+  int* top = &cv.hdr->free_top[hd.pool_kb];
+  int t = lane == 0 ? atomicSub(top, k) : 0;
+  t = __shfl_sync(0xffffffffu, t, 0);
+  if (t < k && lane == 0) {
+    atomicAdd(top, k);
+    set_status(cv, kStatusCapacity);
+  }
+  for (int y = lane; y < k; y += 32) dst[y] = t < k ? -1 : __ldcg(&cv.free_list[hd.free_off + t - 1 - y]);
 }
 
 // Position of the chunk's token i of sequence b, which holds N before it, on an axis.
@@ -125,7 +135,6 @@ __global__ void __launch_bounds__(kSealThreads)
   };
   auto load = [&](int r, int slot, bool is_v, uint4& u, uint4& v) {
     const int mid = kQBlockRows * j + r, t = cv.S + mid;
-    const bool turned = kRope && !is_v && t >= N && mid >= m0;
     const uint16_t* row;
     int c0 = 16 * slot, c1 = c0 + 8;
     if (mid < m0) {
@@ -137,11 +146,14 @@ __global__ void __launch_bounds__(kSealThreads)
     }
     u = *reinterpret_cast<const uint4*>(row + c0);
     v = *reinterpret_cast<const uint4*>(row + c1);
-    if (turned)
+  };
+  auto turn = [&](int r, uint4& u, uint4& v) {             // (held rows are turned already)
+    const int t = cv.S + kQBlockRows * j + r;
+    if (kRope && t >= N)
       share.apply(rc.rope, [&](int axis) { return chunk_position(rc, a.n_max, b, t - N, N, axis); }, u, v);
   };
   seal_by_block<kSealThreads>(sm, dst, k, cv.kv_format, cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim,
-                              min(max(m0 - kQBlockRows * j, 0), kQBlockRows), load, where);
+                              min(max(m0 - kQBlockRows * j, 0), kQBlockRows), load, turn, where);
 }
 
 // Special tokens of the chunk: one block per sequence ranks them in position
@@ -204,7 +216,8 @@ __global__ void __launch_bounds__(1024)
         row8(cv.pool[kPoolK128], row)[lane] = reinterpret_cast<const uint2*>(k_src)[lane];
       } else if (lane < kRopeSlots) {
         const RopeShare share(rc.rope, lane);
-        uint4 u = *reinterpret_cast<const uint4*>(k_src + share.c0), v = *reinterpret_cast<const uint4*>(k_src + share.c1);
+        uint4 u = *reinterpret_cast<const uint4*>(k_src + share.c0);
+        uint4 v = *reinterpret_cast<const uint4*>(k_src + share.c1);
         share.apply(rc.rope, [&](int axis) { return chunk_position(rc, a.n_max, b, s_tok[j], N, axis); }, u, v);
         uint16_t* to = cv.pool[kPoolK128] + row * kHeadDim;
         *reinterpret_cast<uint4*>(to + share.c0) = u;
@@ -218,61 +231,112 @@ __global__ void __launch_bounds__(1024)
   if (tid == 0) *cnt = min(base, cv.spec_cap);
 }
 
-// One warp lays token i of sequence b (N tokens held, n new ones) into kv head h,
-// which is not SPECIAL; k_src, v_src: its rows.
-__device__ __forceinline__ void place_row(const ChunkArgs& a, int b, int i, int h, int N, int n, const uint16_t* k_src,
-                                          const uint16_t* v_src, int lane) {
-  const CacheView& cv = a.cv;
+// Where token i of n new ones (N held) goes, whatever the head.
+struct Spot {
+  int local;                   // its row in a LOCAL head, or -1
+  int full;                    // its full-width row in a FULL head, or -1
+  int mid;                     // the middle row to be written with it, or -1: its own, or that of
+  int moves;                   // the held token whose ring row it takes
+  int restart;                 // >= 0: the first row of the open block that is to be cleared
+};
+__device__ __forceinline__ Spot token_spot(const CacheView& cv, int i, int N, int n) {
   const bool quant = kv_quantized(cv.kv_format);
-  const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + h];
-  const uint2 kx = reinterpret_cast<const uint2*>(k_src)[lane];
-  const uint2 vx = reinterpret_cast<const uint2*>(v_src)[lane];
-  const int64_t abase = hd.row_a + (int64_t)b * hd.cap_a;
-  const int p = N + i, end = N + n;
-  int arow = -1;
-  if (hd.policy == kLocal) {
-    if (p >= end - cv.W_loc) arow = p % cv.W_loc;
+  const int p = N + i, end = N + n, m1 = max(0, end - cv.S - cv.W);
+  Spot s{-1, -1, -1, 0, -1};
+  if (p >= end - cv.W_loc) s.local = p % cv.W_loc;
+  if (p < cv.S) {
+    s.full = p;
+  } else if (p >= end - cv.W) {
+    s.full = cv.S + (p - cv.S) % cv.W;
+    // the held token of this ring row, if any: the latest one before N
+    const int64_t old = p - (int64_t)cv.W * (i / cv.W + 1);
+    if (old >= cv.S) {
+      s.mid = (int)(old - cv.S);
+      s.moves = 1;
+    }
   } else {
-    const int m1 = max(0, end - cv.S - cv.W);
-    const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim;
-    int mid = -1;                     // middle row to write, from
-    const uint16_t* mk = k_src;       // this K row
-    uint2 mv = vx;
-    if (p < cv.S) {
-      arow = p;
-    } else if (p >= end - cv.W) {
-      arow = cv.S + (p - cv.S) % cv.W;
-      // the held token of this ring row, if any: the latest one before N
-      const int64_t old = p - (int64_t)cv.W * (((int64_t)i + cv.W) / cv.W);
-      if (old >= cv.S) {
-        mid = (int)(old - cv.S);
-        mk = cv.pool[kPoolK128] + (abase + arow) * kHeadDim;
-        if (hd.n_kept > 0) mv = row8(cv.pool[kPoolV], abase + arow)[lane];
+    s.mid = p - cv.S;
+  }
+  // rows of complete blocks are sealed already
+  if (quant && s.mid < m1 / kQBlockRows * kQBlockRows) s.mid = -1;
+  // the open block of a quantised head restarts: rows not yet taken are zero
+  if (quant && i == 0 && m1 / kQBlockRows > max(0, N - cv.S - cv.W) / kQBlockRows) s.restart = m1 % kQBlockRows;
+  return s;
+}
+// Whether a head's row there has anything to do: sealed rows, and middle rows where no
+// channel is kept, go nowhere.
+__device__ __forceinline__ bool lands(const HeadDesc& hd, const Spot& s) {
+  if (hd.policy == kLocal) return s.local >= 0;
+  return hd.policy == kFull && (s.full >= 0 || (hd.n_kept > 0 && (s.mid >= 0 || s.restart >= 0)));
+}
+
+constexpr int kRowLanes = 8;                   // threads of a row, 16 channels each
+// Channels of V that a thread holds: 8 slot on, and 64 on.
+__device__ __forceinline__ void load_row(const uint16_t* row, int c0, int c1, uint4& u, uint4& v) {
+  u = *reinterpret_cast<const uint4*>(row + c0);
+  v = *reinterpret_cast<const uint4*>(row + c1);
+}
+__device__ __forceinline__ void store_row(uint16_t* row, int c0, int c1, const uint4& u, const uint4& v) {
+  *reinterpret_cast<uint4*>(row + c0) = u;
+  *reinterpret_cast<uint4*>(row + c1) = v;
+}
+
+// The 8 threads of a row lay a token of sequence b into kv head h, where it lands (else
+// `there` is false).  ku, kv: K channels c0 on and c1 on; vu, vv: V; s_row: 128 elements
+// of shared memory for the row.  All 32 threads of the warp call it.
+__device__ __forceinline__ void place_row(const ChunkArgs& a, int b, int h, const Spot& s, bool there, int c0, int c1,
+                                          const uint4& ku, const uint4& kv, const uint4& vu, const uint4& vv,
+                                          uint16_t* s_row) {
+  const CacheView& cv = a.cv;
+  const int lane = threadIdx.x & 31, slot = lane % kRowLanes;
+  const HeadDesc& hd = cv.heads[a.layer * cv.Hkv + h];
+  const bool full = hd.policy == kFull, has_middle = there && full && hd.n_kept > 0, middle = has_middle && s.mid >= 0;
+  const int arow = there ? (full ? s.full : s.local) : -1;
+  const int64_t row = (hd.row_a + (int64_t)b * hd.cap_a + arow) * kHeadDim;
+  uint4 mu = vu, mv = vv;
+  __syncwarp();
+  if (middle) {
+    uint4 u = ku, v = kv;
+    if (s.moves) {
+      load_row(cv.pool[kPoolK128] + row, c0, c1, u, v);
+      load_row(cv.pool[kPoolV] + row, 8 * slot, 64 + 8 * slot, mu, mv);
+    }
+    store_row(s_row, c0, c1, u, v);
+  }
+  __syncwarp();
+  if (middle) {
+    const int32_t page = cv.max_pages > 0 && !kv_quantized(cv.kv_format)
+                             ? __ldcg(&page_row(cv, a.layer, b, h)[s.mid / kPageRows])
+                             : -1;
+    int64_t krow, vrow;
+    if (middle_rows(cv, hd, b, s.mid, page, krow, vrow)) {
+      const int16_t* kept = cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim;
+      uint16_t* to = cv.pool[hd.pool_kb] + krow * hd.n_kept;
+      for (int c = 4 * slot; c < hd.n_kept; c += 4 * kRowLanes) {
+        const uint2 at = *reinterpret_cast<const uint2*>(kept + c);
+        *reinterpret_cast<uint2*>(to + c) =
+            make_uint2(s_row[at.x & 0xffffu] | (uint32_t)s_row[at.x >> 16] << 16,
+                       s_row[at.y & 0xffffu] | (uint32_t)s_row[at.y >> 16] << 16);
       }
-    } else {
-      mid = p - cv.S;
-    }
-    // INT8 / FP8: rows of complete blocks are sealed already
-    if (mid >= 0 && hd.n_kept > 0 && !(quant && mid < m1 / kQBlockRows * kQBlockRows)) {
-      const int32_t page = cv.max_pages > 0 && !quant ? __ldcg(&page_row(cv, a.layer, b, h)[mid / kPageRows]) : -1;
-      int64_t krow, vrow;
-      if (middle_rows(cv, hd, b, mid, page, krow, vrow)) write_middle(cv, hd, kept, krow, vrow, mk, mv, lane);
-    }
-    __syncwarp();
-    // the open block of a quantised head restarts: rows not yet taken are zero
-    if (quant && i == 0 && hd.n_kept > 0 && hd.cap_b > 0 &&
-        m1 / kQBlockRows > max(0, N - cv.S - cv.W) / kQBlockRows) {
-      const int r0 = m1 % kQBlockRows, nr = hd.cap_b - r0, k = hd.n_kept;
-      uint4* kz = reinterpret_cast<uint4*>(cv.pool[hd.pool_kb] + (hd.krow_b + (int64_t)b * hd.cap_b + r0) * k);
-      uint4* vz = reinterpret_cast<uint4*>(cv.pool[kPoolV] + (hd.vrow_b + (int64_t)b * hd.cap_b + r0) * kHeadDim);
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      for (int x = lane; x < nr * k / 8; x += 32) kz[x] = zero;
-      for (int x = lane; x < nr * kHeadDim / 8; x += 32) vz[x] = zero;
+      store_row(cv.pool[kPoolV] + vrow * kHeadDim, 8 * slot, 64 + 8 * slot, mu, mv);
     }
   }
   if (arow >= 0) {
-    row8(cv.pool[kPoolK128], abase + arow)[lane] = kx;
-    row8(cv.pool[kPoolV], abase + arow)[lane] = vx;
+    store_row(cv.pool[kPoolK128] + row, c0, c1, ku, kv);
+    store_row(cv.pool[kPoolV] + row, 8 * slot, 64 + 8 * slot, vu, vv);
+  }
+  // rows of the open block that its first token clears: by the whole warp
+  const uint32_t clears = __ballot_sync(0xffffffffu, has_middle && s.restart >= 0 && slot == 0);
+  for (uint32_t left = clears; left != 0; left &= left - 1) {
+    const int from = __ffs(left) - 1, ch = __shfl_sync(0xffffffffu, h, from), cb = __shfl_sync(0xffffffffu, b, from);
+    const int r0 = __shfl_sync(0xffffffffu, s.restart, from);
+    const HeadDesc& c = cv.heads[a.layer * cv.Hkv + ch];
+    const int nr = c.cap_b - r0, k = c.n_kept;
+    uint4* kz = reinterpret_cast<uint4*>(cv.pool[c.pool_kb] + (c.krow_b + (int64_t)cb * c.cap_b + r0) * k);
+    uint4* vz = reinterpret_cast<uint4*>(cv.pool[kPoolV] + (c.vrow_b + (int64_t)cb * c.cap_b + r0) * kHeadDim);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    for (int x = lane; x < nr * k / 8; x += 32) kz[x] = zero;
+    for (int x = lane; x < nr * kHeadDim / 8; x += 32) vz[x] = zero;
   }
 }
 
@@ -296,41 +360,51 @@ __device__ void advance_lengths(const ChunkArgs& a) {
   }
 }
 
+// 32 rows (token, head) of 8 threads each at once.
+constexpr int kBlockRows = 256 / kRowLanes;
 __global__ void __launch_bounds__(256) chunk_append_kernel(const __grid_constant__ ChunkArgs a) {
+  __shared__ uint4 s_k[kBlockRows][kHeadDim / 8];
   grid_dependency_wait();
   grid_launch_dependents();
   const CacheView& cv = a.cv;
-  const int lane = threadIdx.x & 31;
+  const int row = threadIdx.x / kRowLanes, slot = threadIdx.x % kRowLanes, c0 = 8 * slot, c1 = 64 + 8 * slot;
   const int64_t items = (int64_t)a.nb * a.n_max * cv.Hkv;
-  const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t it = (((int64_t)blockIdx.x * blockDim.x) + threadIdx.x) >> 5; it < items; it += nwarps) {
-    const int h = (int)(it % cv.Hkv);
-    const int64_t bi = it / cv.Hkv;
-    const int i = (int)(bi % a.n_max), seq = (int)(bi / a.n_max);
-    int N;
-    const int n = chunk_len(a, seq, N);
-    if (i >= n) continue;
+  for (int64_t it0 = (int64_t)blockIdx.x * kBlockRows; it0 < items; it0 += (int64_t)gridDim.x * kBlockRows) {
+    const int64_t it = it0 + row, bi = it / cv.Hkv;
+    const int h = (int)(it - bi * cv.Hkv), seq = (int)(bi / a.n_max), i = (int)(bi - (int64_t)seq * a.n_max);
     const int b = a.b0 + seq;
-    if (cv.heads[a.layer * cv.Hkv + h].policy == kSpecial) continue;
-    place_row(a, b, i, h, N, n, k_token(a, b, i, h), v_token(a, b, i, h), lane);
+    int N, n = 0;
+    if (it < items) n = chunk_len(a, seq, N);
+    const bool taken = i < n;
+    Spot s{-1, -1, -1, 0, -1};
+    if (taken) s = token_spot(cv, i, N, n);
+    const bool there = taken && lands(cv.heads[a.layer * cv.Hkv + h], s);
+    uint4 ku = make_uint4(0u, 0u, 0u, 0u), kv = ku, vu = ku, vv = ku;
+    if (there) {
+      load_row(k_token(a, b, i, h), c0, c1, ku, kv);
+      load_row(v_token(a, b, i, h), c0, c1, vu, vv);
+    }
+    place_row(a, b, h, s, there, c0, c1, ku, kv, vu, vv, reinterpret_cast<uint16_t*>(s_k[row]));
   }
   advance_lengths(a);
 }
 
 // With a rotation: a block takes runs of kTokens tokens of a sequence, one after
-// another.  32 rows of 8 threads each are turned at once, 16 channels to a thread.
-constexpr int kRopeRows = 256 / kRopeSlots;
+// another, and turns 32 rows at once; what is read first of q, and then of K and V, is on
+// its way before it is needed.
 template <int kTokens>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     chunk_rope_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ RopeChunk rc) {
   __shared__ float4 turn[kTokens][kHeadDim / 4];           // (cosine, sine) of two pairs each
-  __shared__ uint4 s_k[kRopeRows][kHeadDim / 8];
+  __shared__ uint4 s_k[kBlockRows][kHeadDim / 8];
+  __shared__ Spot s_spot[kTokens];
   grid_dependency_wait();
   grid_launch_dependents();
   const CacheView& cv = a.cv;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const RopeShare share(rc.rope, tid % kRopeSlots);
-  const int row = tid / kRopeSlots;
+  const HeadDesc* heads = cv.heads + a.layer * cv.Hkv;
+  static_assert(kRowLanes == kRopeSlots, "one row, one turn");
+  const int tid = threadIdx.x, row = tid / kRowLanes, slot = tid % kRowLanes;
+  const RopeShare share(rc.rope, slot);
   const int runs = (a.n_max + kTokens - 1) / kTokens, pairs = rc.rope.rotary_dim / 2;
   for (int64_t run = blockIdx.x; run < (int64_t)a.nb * runs; run += gridDim.x) {
     const int seq = (int)(run / runs), i0 = (int)(run - (int64_t)seq * runs) * kTokens, b = a.b0 + seq;
@@ -338,6 +412,31 @@ __global__ void __launch_bounds__(256)
     const int n = chunk_len(a, seq, N);
     const int nt = min(kTokens, n - i0);
     if (nt <= 0) continue;
+    const int64_t token = (int64_t)b * a.n_max + i0;
+    const int q_rows = rc.q != nullptr ? nt * cv.Hq : 0, k_rows = nt * cv.Hkv;
+    if (tid < nt) s_spot[tid] = token_spot(cv, i0 + tid, N, n);
+    // rows of q and of K, V: (token, head), in steps of kBlockRows
+    int qt = 0, qh = row, kt = 0, kh = row;
+    auto wrap = [](int& t, int& h, int heads) {
+      while (h >= heads) {
+        h -= heads;
+        ++t;
+      }
+    };
+    wrap(qt, qh, cv.Hq);
+    wrap(kt, kh, cv.Hkv);
+    uint4 u, v, ku, kv, vu, vv;
+    bool there = false;
+    auto load_q = [&](int x) {
+      if (x < q_rows) load_row(rc.q + (token + qt) * rc.q_stride + qh * kHeadDim, share.c0, share.c1, u, v);
+    };
+    auto load_kv = [&](int x) {
+      there = x < k_rows && lands(heads[kh], s_spot[kt]);
+      if (!there) return;
+      load_row(k_token(a, b, i0 + kt, kh), share.c0, share.c1, ku, kv);
+      load_row(v_token(a, b, i0 + kt, kh), 8 * slot, 64 + 8 * slot, vu, vv);
+    };
+    load_q(row);
     for (int y = tid; y < nt * pairs; y += 256) {
       const int t = y / pairs, i = y - t * pairs;
       auto pos = [&](int axis) { return chunk_position(rc, a.n_max, b, i0 + t, N, axis); };
@@ -345,37 +444,24 @@ __global__ void __launch_bounds__(256)
           rc.rope.axes > 1 ? rope_turn<true>(rc.rope, i, pos) : rope_turn<false>(rc.rope, i, pos);
     }
     __syncthreads();
-    if (rc.q != nullptr) {
-      for (int x = row; x < nt * cv.Hq; x += kRopeRows) {
-        const int t = x / cv.Hq, h = x - t * cv.Hq;
-        const int64_t token = (int64_t)b * a.n_max + i0 + t;
-        const uint16_t* src = rc.q + token * rc.q_stride + h * kHeadDim;
-        uint16_t* dst = rc.q_out + token * rc.q_out_stride + h * kHeadDim;
-        uint4 u = *reinterpret_cast<const uint4*>(src + share.c0), v = *reinterpret_cast<const uint4*>(src + share.c1);
-        share.apply(turn[t], u, v);
-        *reinterpret_cast<uint4*>(dst + share.c0) = u;
-        *reinterpret_cast<uint4*>(dst + share.c1) = v;
-      }
+    load_kv(row);
+    for (int x = row; x < q_rows;) {
+      share.apply(turn[qt], u, v);
+      store_row(rc.q_out + (token + qt) * rc.q_out_stride + qh * kHeadDim, share.c0, share.c1, u, v);
+      x += kBlockRows;
+      qh += kBlockRows;
+      wrap(qt, qh, cv.Hq);
+      load_q(x);
     }
-    for (int x0 = 0; x0 < nt * cv.Hkv; x0 += kRopeRows) {
-      const int x = x0 + row;
-      if (x < nt * cv.Hkv) {
-        const int t = x / cv.Hkv, h = x - t * cv.Hkv;
-        const uint16_t* src = k_token(a, b, i0 + t, h);
-        uint4 u = *reinterpret_cast<const uint4*>(src + share.c0), v = *reinterpret_cast<const uint4*>(src + share.c1);
-        share.apply(turn[t], u, v);
-        s_k[row][share.c0 / 8] = u;
-        s_k[row][share.c1 / 8] = v;
-      }
-      __syncthreads();
-      for (int y = x0 + warp; y < min(nt * cv.Hkv, x0 + kRopeRows); y += 8) {
-        const int t = y / cv.Hkv, h = y - t * cv.Hkv;
-        if (cv.heads[a.layer * cv.Hkv + h].policy == kSpecial) continue;
-        place_row(a, b, i0 + t, h, N, n, reinterpret_cast<const uint16_t*>(s_k[y - x0]), v_token(a, b, i0 + t, h),
-                  lane);
-      }
-      __syncthreads();
+    for (int x0 = 0; x0 < k_rows; x0 += kBlockRows) {
+      const int t = min(kt, kTokens - 1), h = min(kh, cv.Hkv - 1);       // (of rows past the last, which are not there)
+      if (there) share.apply(turn[t], ku, kv);
+      place_row(a, b, h, s_spot[t], there, share.c0, share.c1, ku, kv, vu, vv, reinterpret_cast<uint16_t*>(s_k[row]));
+      kh += kBlockRows;
+      wrap(kt, kh, cv.Hkv);
+      load_kv(x0 + kBlockRows + row);
     }
+    __syncthreads();                           // the table and the spots have been read
   }
   advance_lengths(a);
 }
@@ -393,7 +479,7 @@ cudaError_t launch_chunk_append(const ChunkArgs& args, const RopeChunk* rope, bo
   if (seals > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaError_t err = cudaSuccess;
   if (has_middle && cv.max_pages > 0)
-    err = launch_after(chunk_pages_kernel, dim3((unsigned)(args.nb * cv.Hkv + 255) / 256), 256, 0, stream, args);
+    err = launch_after(chunk_pages_kernel, dim3((unsigned)(args.nb * cv.Hkv + 7) / 8), 256, 0, stream, args);
   if (err == cudaSuccess && has_middle && kv_quantized(cv.kv_format))
     err = launch_after(rope != nullptr ? chunk_seal_kernel<true> : chunk_seal_kernel<false>, dim3((unsigned)seals),
                        kSealThreads, 0, stream, args, rc, max_blocks);
@@ -411,7 +497,7 @@ cudaError_t launch_chunk_append(const ChunkArgs& args, const RopeChunk* rope, bo
     return launch_after(chunk_rope_kernel<1>, dim3((unsigned)tokens), 256, 0, stream, args, rc);
   }
   const int64_t items = (int64_t)args.nb * args.n_max * cv.Hkv;
-  const int64_t blocks = min((items + 7) / 8, (int64_t)num_sms * 16);
+  const int64_t blocks = min((items + kBlockRows - 1) / kBlockRows, (int64_t)num_sms * 16);
   return launch_after(chunk_append_kernel, dim3((unsigned)blocks), 256, 0, stream, args);
 }
 

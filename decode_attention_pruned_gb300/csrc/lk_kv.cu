@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kSealThreads) prefill_seal_block_kernel(const 
         u = reinterpret_cast<const uint4*>(row)[0];
         v = reinterpret_cast<const uint4*>(row)[1];
       },
+      [](int, uint4&, uint4&) {},
       [](int slot, int& c0, int& c1) {
         c0 = 16 * slot;
         c1 = c0 + 8;

@@ -29,16 +29,21 @@ __device__ __forceinline__ float2 rope_turn(const RopeTable& r, int i, Pos pos) 
 }
 static_assert(kRopeAxes == 4, "two bits of a frequency");
 
+// (a, b) turned by (c, s).  The roundings are spelled out, so that every kernel leaves
+// the same bits (a compiler may round either of the two products first).
+__device__ __forceinline__ float2 turn_pair(float a, float b, float2 t) {
+  return make_float2(fmaf(a, t.x, -__fmul_rn(b, t.y)), fmaf(b, t.x, __fmul_rn(a, t.y)));
+}
 // Two bf16 pairs (x_a, x_b) in the halves of a and b turned by (c0, s0), (c1, s1).
 __device__ __forceinline__ void turn2(uint32_t a, uint32_t b, float2 t0, float2 t1, uint32_t& ya, uint32_t& yb) {
-  const float a0 = bf16_lo(a), a1 = bf16_hi(a), b0 = bf16_lo(b), b1 = bf16_hi(b);
-  ya = pack_bf16x2(a0 * t0.x - b0 * t0.y, a1 * t1.x - b1 * t1.y);
-  yb = pack_bf16x2(b0 * t0.x + a0 * t0.y, b1 * t1.x + a1 * t1.y);
+  const float2 y0 = turn_pair(bf16_lo(a), bf16_lo(b), t0), y1 = turn_pair(bf16_hi(a), bf16_hi(b), t1);
+  ya = pack_bf16x2(y0.x, y1.x);
+  yb = pack_bf16x2(y0.y, y1.y);
 }
 // The pair in the two halves of one word.
 __device__ __forceinline__ uint32_t turn1(uint32_t x, float2 t) {
-  const float a = bf16_lo(x), b = bf16_hi(x);
-  return pack_bf16x2(a * t.x - b * t.y, b * t.x + a * t.y);
+  const float2 y = turn_pair(bf16_lo(x), bf16_hi(x), t);
+  return pack_bf16x2(y.x, y.y);
 }
 
 // A thread's share of a head: 16 channels as two runs of 8, from c0 and from c1.

@@ -12,6 +12,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "lk_append.cuh"
 #include "lk_block.h"
 #include "lk_device.cuh"
@@ -25,8 +27,9 @@ struct SealSmem {
   uint4 rows[kQBlockRows * kSealStride / 8];
   float part[2][kHeadDim];                     // largest magnitudes: of channels by halves of the rows
   float scale[kHeadDim];                       // of channels (K), of rows (V)
-  uint32_t top;                                // largest magnitude of all, as bits
-  int16_t kept[kHeadDim];
+  uint32_t top[2];                             // largest magnitudes of all, as bits
+  uint32_t mask[4];                            // kept channels
+  alignas(16) int16_t kept[kHeadDim];
 };
 
 // Device address of sealed block j of (layer, b, h); null if its page is missing.
@@ -48,52 +51,94 @@ __device__ __forceinline__ uint32_t magnitude2(uint32_t w, uint32_t keep, uint32
   return top;
 }
 
+// e4m3 codes of x / s, byte y that of x[y], each that of the correctly rounded
+// quotient.  x times 1 / s is off by less than 2^-22 of it: where its neighbours to
+// both sides round to one code, the quotient does, and the division is left out.
+__device__ __forceinline__ uint32_t codes2(float x0, float x1) {
+  uint16_t w;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(w) : "f"(x1), "f"(x0));
+  return w;
+}
+__device__ __forceinline__ uint4 codes16(const float (&x)[16], float s, float inv) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u}, far = 0;
+#pragma unroll
+  for (int y = 0; y < 16; y += 2) {
+    const float a = x[y] * inv, b = x[y + 1] * inv;
+    const uint32_t lo = codes2(fmaf(a, -0x1p-22f, a), fmaf(b, -0x1p-22f, b));
+    const uint32_t hi = codes2(fmaf(a, 0x1p-22f, a), fmaf(b, 0x1p-22f, b));
+    w[y / 4] |= lo << 8 * (y & 3);
+    far |= lo ^ hi;
+  }
+  if (far != 0) {
+#pragma unroll
+    for (int y = 0; y < 16; y += 4)
+      w[y / 4] = quant_e4m3(x[y], s) | (uint32_t)quant_e4m3(x[y + 1], s) << 8 |
+                 (uint32_t)quant_e4m3(x[y + 2], s) << 16 | (uint32_t)quant_e4m3(x[y + 3], s) << 24;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // All kThreads threads of the block seal rows r = 0 .. 127 into dst.
 //   load(r, slot, is_v, u, v): two runs of 8 channels of row r, those from
 //       where(slot) on; slot = 0 .. 7
+//   turn(r, u, v): what is to be done to a row's K before it is rounded
 //   where(slot, c0, c1): the first channels of the two runs of a full row
 //   packed: rows below it hold their kept channels side by side (their runs start
 //       at 16 slot and 16 slot + 8), the others all channels
-template <int kThreads, class Load, class Where>
+template <int kThreads, class Load, class Turn, class Where>
 __device__ void seal_by_block(SealSmem& sm, uint8_t* dst, int k, int fmt, const int16_t* kept, int packed, Load load,
-                              Where where) {
+                              Turn turn, Where where) {
   static_assert(kThreads % 32 == 0 && kQBlockRows % (kThreads / 8) == 0 && kThreads >= kHeadDim, "whole passes");
-  const int tid = threadIdx.x, slot = tid & 7;
+  constexpr int kStep = kThreads / 8, kRows = kQBlockRows / kStep;     // a thread's rows: tid / 8 + y kStep
+  const int tid = threadIdx.x, slot = tid & 7, lane = tid & 31, warp = tid >> 5;
   uint16_t* rows = reinterpret_cast<uint16_t*>(sm.rows);
   const bool block = fmt == kKvFp8Block;
-  if (tid < k) sm.kept[tid] = kept[tid];
-  if (tid == 0) sm.top = 0;
-  __syncthreads();
   int f0, f1;
   where(slot, f0, f1);
-  uint32_t keep0 = 0, keep1 = 0;               // which channels of a full row's runs are kept
-  for (int j = 0; j < k; ++j) {
-    const int c = sm.kept[j];
-    if (c >= f0 && c < f0 + 8) keep0 |= 1u << (c - f0);
-    if (c >= f1 && c < f1 + 8) keep1 |= 1u << (c - f1);
+  uint4 u[kRows], v[kRows];
+  auto fetch = [&](bool is_v) {                // (V rows are as wide as packed ones of 128 channels)
+#pragma unroll
+    for (int y = 0; y < kRows; ++y) {
+      const int r = (tid >> 3) + y * kStep;
+      u[y] = v[y] = make_uint4(0u, 0u, 0u, 0u);
+      if (is_v || r >= packed || 16 * slot < k) load(r, slot, is_v, u[y], v[y]);
+    }
+  };
+  fetch(false);
+  if (tid < 4) sm.mask[tid] = 0;
+  if (tid < 2) sm.top[tid] = 0;
+  __syncthreads();
+  if (tid < k) {
+    const int c = kept[tid];
+    sm.kept[tid] = (int16_t)c;
+    atomicOr(&sm.mask[c >> 5], 1u << (c & 31));
   }
+  __syncthreads();
+  // which channels of a full row's runs are kept
+  const uint32_t keep0 = sm.mask[f0 >> 5] >> (f0 & 31) & 0xffu, keep1 = sm.mask[f1 >> 5] >> (f1 & 31) & 0xffu;
   const float qmax = fmt == kKvInt8 ? 127.f : 448.f;
-#pragma unroll 1
-  for (int is_v = 0; is_v < 2; ++is_v) {
+
+  auto pass = [&](auto values) {
+    constexpr bool is_v = decltype(values)::value != 0;
     const int width = is_v ? kHeadDim : k;
     uint32_t top = 0;
-#pragma unroll 1
-    for (int r = tid >> 3; r < kQBlockRows; r += kThreads / 8) {
-      const bool full = !is_v && r >= packed;  // (V rows are as wide as packed ones of 128 channels)
+#pragma unroll
+    for (int y = 0; y < kRows; ++y) {
+      const int r = (tid >> 3) + y * kStep;
+      const bool full = !is_v && r >= packed;
       const int c0 = full ? f0 : 16 * slot, c1 = full ? f1 : 16 * slot + 8;
-      uint4 u = make_uint4(0u, 0u, 0u, 0u), v = u;
-      if (full || 16 * slot < width) load(r, slot, is_v != 0, u, v);
+      if (full) turn(r, u[y], v[y]);
       const uint32_t m0 = full ? keep0 : 0xffu, m1 = full ? keep1 : 0xffu;
-      uint32_t t = magnitude2(u.x, m0, 0u);
-      t = magnitude2(u.y, m0 >> 2, t);
-      t = magnitude2(u.z, m0 >> 4, t);
-      t = magnitude2(u.w, m0 >> 6, t);
-      t = magnitude2(v.x, m1, t);
-      t = magnitude2(v.y, m1 >> 2, t);
-      t = magnitude2(v.z, m1 >> 4, t);
-      t = magnitude2(v.w, m1 >> 6, t);
-      *reinterpret_cast<uint4*>(rows + r * kSealStride + c0) = u;
-      *reinterpret_cast<uint4*>(rows + r * kSealStride + c1) = v;
+      uint32_t t = magnitude2(u[y].x, m0, 0u);
+      t = magnitude2(u[y].y, m0 >> 2, t);
+      t = magnitude2(u[y].z, m0 >> 4, t);
+      t = magnitude2(u[y].w, m0 >> 6, t);
+      t = magnitude2(v[y].x, m1, t);
+      t = magnitude2(v[y].y, m1 >> 2, t);
+      t = magnitude2(v[y].z, m1 >> 4, t);
+      t = magnitude2(v[y].w, m1 >> 6, t);
+      *reinterpret_cast<uint4*>(rows + r * kSealStride + c0) = u[y];
+      *reinterpret_cast<uint4*>(rows + r * kSealStride + c1) = v[y];
       if (block) {
         top = max(top, t);
       } else if (is_v) {
@@ -104,40 +149,64 @@ __device__ void seal_by_block(SealSmem& sm, uint8_t* dst, int k, int fmt, const 
     }
     if (block) {
       top = __reduce_max_sync(0xffffffffu, top);
-      if ((tid & 31) == 0) atomicMax(&sm.top, top);
+      if (lane == 0) atomicMax(&sm.top[is_v], top);
     }
+    if (!is_v) fetch(true);                    // on their way while K is rounded
     __syncthreads();
-    // row r's value in the place of channel j
-    auto at = [&](int r, int j) {
-      return bf16_to_f32(rows[r * kSealStride + (is_v || r < packed ? j : sm.kept[j])]);
-    };
-    if (!block && !is_v) {
-      for (int x = tid; x < 2 * k; x += kThreads) {
-        const int half = x >= k ? 1 : 0, c = x - half * k;
-        float m = 0.f;
-        for (int r = 64 * half; r < 64 * half + 64; ++r) m = fmaxf(m, fabsf(at(r, c)));
-        sm.part[half][c] = m;
-      }
-      __syncthreads();
-      if (tid < k) sm.scale[tid] = __fdiv_rn(fmaxf(sm.part[0][tid], sm.part[1][tid]), qmax);
-      __syncthreads();
-    }
-    const float whole = block ? fmaxf(__fdiv_rn(__uint_as_float(sm.top), qmax), kBlockMinScale) : 0.f;
     uint8_t* to = dst + (is_v ? kQBlockRows * k : 0);
+    if (block) {
+      // A warp takes 32 words of a slab of 16 rows: channels 32 u + 8 t of the rows g and
+      // g + 8 of K, channels 8 g + 2 u and 64 + 8 g + 2 u of four rows of V.
+      const float scale = fmaxf(__fdiv_rn(__uint_as_float(sm.top[is_v]), qmax), kBlockMinScale);
+      const float inv = __frcp_rn(scale);
+      const int g = lane >> 2, t = lane & 3;
 #pragma unroll 1
-    for (int x = tid; x < kQBlockRows * width / 16; x += kThreads) {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-      if (block) {
+      for (int item = warp; item < width / 4; item += kThreads / 32) {
+        const int slab = item & 7, part = item >> 3;
+        float x[16];
+        if (is_v) {
 #pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const int lane = x & 31, g = lane >> 2, t = lane & 3;
-          const int r = is_v ? 16 * (x >> 7) + 2 * t + (y & 1) + 4 * (y & 2) : 16 * (x / width) + g + y / 8 * 8;
-          const int c = is_v ? 64 * (y >> 2 & 1) + 8 * g + 2 * (x >> 5 & 3) + y / 8
-                             : x % width / 32 * 32 + 8 * t + (y & 7);
-          w[y / 4] |= (uint32_t)quant_e4m3(at(r, c), whole) << 8 * (y & 3);
+          for (int y = 0; y < 8; ++y) {
+            const int r = 16 * slab + 2 * t + (y & 1) + 4 * (y & 2);
+            const int c = 16 * (y & 4) + 8 * g + 2 * part;
+            const uint32_t two = *reinterpret_cast<const uint32_t*>(rows + r * kSealStride + c);
+            x[y] = bf16_lo(two);
+            x[y + 8] = bf16_hi(two);
+          }
+        } else {
+          const int c = 32 * part + 8 * t;
+          const uint4 at = *reinterpret_cast<const uint4*>(sm.kept + c);
+          const uint32_t ids[4] = {at.x, at.y, at.z, at.w};
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            const int r = 16 * slab + g + (y & 8);
+            const int from = r < packed ? c + (y & 7) : (int)(ids[(y & 7) / 2] >> 16 * (y & 1) & 0xffffu);
+            x[y] = bf16_to_f32(rows[r * kSealStride + from]);
+          }
         }
-        *reinterpret_cast<uint4*>(to + 16 * x) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
+        *reinterpret_cast<uint4*>(to + 16 * (slab * width + 32 * part + lane)) = codes16(x, scale, inv);
+      }
+      if (tid == 0) reinterpret_cast<float*>(dst + block_soff(k))[is_v] = scale;
+      if (tid == 1 && is_v) *reinterpret_cast<uint2*>(dst + block_soff(k) + 8) = make_uint2(0u, 0u);
+    } else {
+      // row r's value in the place of channel j
+      auto at = [&](int r, int j) {
+        return bf16_to_f32(rows[r * kSealStride + (is_v || r < packed ? j : sm.kept[j])]);
+      };
+      if (!is_v) {
+        for (int x = tid; x < 2 * k; x += kThreads) {
+          const int half = x >= k ? 1 : 0, c = x - half * k;
+          float m = 0.f;
+          for (int r = 64 * half; r < 64 * half + 64; ++r) m = fmaxf(m, fabsf(at(r, c)));
+          sm.part[half][c] = m;
+        }
+        __syncthreads();
+        if (tid < k) sm.scale[tid] = __fdiv_rn(fmaxf(sm.part[0][tid], sm.part[1][tid]), qmax);
+        __syncthreads();
+      }
+#pragma unroll 1
+      for (int x = tid; x < kQBlockRows * width / 16; x += kThreads) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
         const int groups = width / 16, r = x / groups, g = x - r * groups;
 #pragma unroll
         for (int y = 0; y < 16; ++y) {
@@ -148,17 +217,13 @@ __device__ void seal_by_block(SealSmem& sm, uint8_t* dst, int k, int fmt, const 
         }
         *reinterpret_cast<uint4*>(to + r * width + 16 * (g ^ qswz(width, r))) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-    }
-    if (block) {
-      if (tid == 0) reinterpret_cast<float*>(dst + block_soff(k))[is_v] = whole;
-      if (tid == 1 && is_v) *reinterpret_cast<uint2*>(dst + block_soff(k) + 8) = make_uint2(0u, 0u);
-    } else if (tid < width) {
-      reinterpret_cast<float*>(dst + (is_v ? qblock_vsoff(k) : qblock_ksoff(k)))[tid] = sm.scale[tid];
+      if (tid < width)
+        reinterpret_cast<float*>(dst + (is_v ? qblock_vsoff(k) : qblock_ksoff(k)))[tid] = sm.scale[tid];
     }
     __syncthreads();                           // the rows and scales have been read
-    if (tid == 0) sm.top = 0;
-    __syncthreads();
-  }
+  };
+  pass(std::integral_constant<int, 0>());
+  pass(std::integral_constant<int, 1>());
 }
 
 }  // namespace
