@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(256, 4)
     for (int y = tid; y < nt * pairs; y += 256) {
       const int t = y / pairs, i = y - t * pairs;
       auto pos = [&](int axis) { return chunk_position(rc, a.n_max, b, i0 + t, N, axis); };
-      reinterpret_cast<float2*>(turn[t])[i] =
+      reinterpret_cast<float2*>(turn[t])[rope_place(i)] =
           rc.rope.axes > 1 ? rope_turn<true>(rc.rope, i, pos) : rope_turn<false>(rc.rope, i, pos);
     }
     __syncthreads();

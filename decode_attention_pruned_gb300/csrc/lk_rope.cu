@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   if (x < units) load(x);
   for (int y = tid; y < nt * pairs; y += kRopeThreads) {
     const int t = y / pairs, i = y - t * pairs;
-    reinterpret_cast<float2*>(turn[t])[i] = rope_turn<kAxes>(
+    reinterpret_cast<float2*>(turn[t])[rope_place(i)] = rope_turn<kAxes>(
         a.rope, i, [&](int axis) { return __ldg(a.positions + (kAxes ? axis * a.tokens : 0) + t0 + t); });
   }
   __syncthreads();

@@ -29,6 +29,12 @@ __device__ __forceinline__ float2 rope_turn(const RopeTable& r, int i, Pos pos) 
 }
 static_assert(kRopeAxes == 4, "two bits of a frequency");
 
+// Place of pair i in a token's table of (cosine, sine), two pairs to an element: the
+// elements that the threads of a head read at once lie side by side.  (In the pairs'
+// order the eight of them met in two of shared memory's eight 16-byte banks: of 8192
+// tokens FIGURE.)
+__device__ __forceinline__ int rope_place(int i) { return (i >> 1 & 3) * 2 * kRopeSlots + (i >> 3) * 2 + (i & 1); }
+
 // (a, b) turned by (c, s).  The roundings are spelled out, so that every kernel leaves
 // the same bits (a compiler may round either of the two products first).
 __device__ __forceinline__ float2 turn_pair(float a, float b, float2 t) {
@@ -69,11 +75,11 @@ struct RopeShare {
       v = make_uint4(turn1(v.x, r[4]), turn1(v.y, r[5]), turn1(v.z, r[6]), turn1(v.w, r[7]));
     }
   }
-  // the same out of a token's table, two pairs to an element
+  // the same out of a token's table
   __device__ __forceinline__ void apply(const float4* turn, uint4& u, uint4& v) const {
     if (!turned) return;
-    const float4* w = turn + 4 * slot;
-    const float4 w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
+    const float4* w = turn + slot;
+    const float4 w0 = w[0], w1 = w[kRopeSlots], w2 = w[2 * kRopeSlots], w3 = w[3 * kRopeSlots];
     const float2 r[8] = {{w0.x, w0.y}, {w0.z, w0.w}, {w1.x, w1.y}, {w1.z, w1.w},
                          {w2.x, w2.y}, {w2.z, w2.w}, {w3.x, w3.y}, {w3.z, w3.w}};
     apply(r, u, v);
