@@ -105,14 +105,14 @@ __device__ void seal_tail(const TokenArgs& a, SealSmem& sm, int layer, int b, in
   if (dst == nullptr) return;
   uint16_t* kt = cv.pool[hd.pool_kb] + (hd.krow_b + (int64_t)b * hd.cap_b) * k;
   uint16_t* vt = cv.pool[kPoolV] + (hd.vrow_b + (int64_t)b * hd.cap_b) * kHeadDim;
-  seal_by_block<kTokenThreads>(
+  seal_by_block<kTokenThreads, false>(
       sm, dst, k, cv.kv_format, cv.kept + ((size_t)layer * cv.Hkv + h) * kHeadDim, kQBlockRows,
       [&](int r, int slot, bool is_v, uint4& u, uint4& v) {
         const uint16_t* row = (is_v ? vt + r * kHeadDim : kt + r * k) + 16 * slot;
         u = reinterpret_cast<const uint4*>(row)[0];
         v = reinterpret_cast<const uint4*>(row)[1];
       },
-      [](int, uint4&, uint4&) {},
+      [](uint16_t*) {},
       [](int slot, int& c0, int& c1) {
         c0 = 16 * slot;
         c1 = c0 + 8;

@@ -11,27 +11,26 @@
 //            token of that row, the one that stays there, moves it first.
 //   LOCAL    the last W_loc positions in ring row p mod W_loc
 //   SPECIAL  special tokens in arrival order
-// One warp does each (sequence, token, head); a ring row is read and
-// overwritten by one warp only, so a single launch needs no ordering.
+// Eight threads do each (sequence, token, head); a ring row is read and overwritten
+// by the same threads only, so a single launch needs no ordering.
 // Before it, as the cache asks for them: the pages that the new middle rows
-// start are popped; complete 128-row blocks of INT8 / FP8 caches are sealed
-// from wherever their rows still are (tail, ring or input); SPECIAL rows are
-// written.
+// start are popped; complete 128-row blocks of INT8 / FP8 / FP8_BLOCK caches are
+// sealed from wherever their rows still are (tail, ring or input); SPECIAL rows
+// are written.
 //
-// bf16: data movement, and short.  512 tokens of 8 heads take 8 us with the call
-// (paged 9), launch and dependency more than bytes (8 MB).  A warp per row, 8
-// bytes a lane, keeps every access a whole row, and the one launch advances the
-// lengths too.
+// bf16: data movement, and short.  Eight threads per row, two 16-byte loads and stores
+// of K and of V each, and the one launch advances the lengths too.
 // INT8 / FP8 / FP8_BLOCK: the sealing, a thread block to each (sequence, head,
-// 128-row block).
+// 128-row block); rows that it took are not read again.
 //
 // With a rotation the chunk's keys are turned by their tokens' positions wherever
 // they are read: by the sealing, by the special rows' copies, and before they are
 // laid into the cache, where a block takes a run of tokens, computes each (token,
-// pair)'s cosine and sine once, turns the queries straight from input to output and
-// the keys into shared memory, from which the copies go as they do without a
-// rotation.  Keys are rounded to bf16 once, so that the cache is left as if they had
-// been turned before.
+// pair)'s cosine and sine once, turns the queries straight from input to output, and
+// the keys in the registers of the threads that place them.  Keys are rounded to bf16
+// once, so that the cache is left as if they had been turned before.  8192 tokens of 32
+// and 8 heads take 40 us (93 MB read, 67 MB of queries and 21 MB of rows written:
+// 4.5 TB/s); with all rows by bulk copies into shared memory 43.
 #include <cuda_runtime.h>
 
 #include "lk_append.cuh"
@@ -105,9 +104,12 @@ __device__ __forceinline__ int chunk_position(const RopeChunk& r, int64_t n_max,
 // still held there, else in the chunk.
 constexpr int kSealThreads = 256;
 template <bool kRope>
-__global__ void __launch_bounds__(kSealThreads)
+__global__ void __launch_bounds__(kSealThreads, 3)
     chunk_seal_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ RopeChunk rc, int max_blocks) {
   __shared__ SealSmem sm;
+  __shared__ int16_t s_pairs[kRope ? kHeadDim / 2 : 1];    // pairs with a kept channel
+  __shared__ int s_pos[kRope ? kRopeAxes : 1][kQBlockRows];
+  __shared__ int s_count;
   grid_dependency_wait();
   grid_launch_dependents();
   const CacheView& cv = a.cv;
@@ -128,31 +130,73 @@ __global__ void __launch_bounds__(kSealThreads)
   const uint16_t* kt = cv.pool[hd.pool_kb] + (hd.krow_b + (int64_t)b * hd.cap_b) * k;
   const uint16_t* vt = cv.pool[kPoolV] + (hd.vrow_b + (int64_t)b * hd.cap_b) * kHeadDim;
   const int64_t ring = hd.row_a + (int64_t)b * hd.cap_a + cv.S;
-  const RopeShare share(rc.rope, threadIdx.x & 7);
   auto where = [&](int slot, int& c0, int& c1) {
-    c0 = kRope ? share.c0 : 16 * slot;
-    c1 = kRope ? share.c1 : 16 * slot + 8;
+    c0 = 16 * slot;
+    c1 = c0 + 8;
   };
   auto load = [&](int r, int slot, bool is_v, uint4& u, uint4& v) {
     const int mid = kQBlockRows * j + r, t = cv.S + mid;
-    const uint16_t* row;
-    int c0 = 16 * slot, c1 = c0 + 8;
-    if (mid < m0) {
-      row = is_v ? vt + (size_t)r * kHeadDim : kt + (size_t)r * k;
-    } else {
-      if (!is_v) where(slot, c0, c1);
-      row = t < N ? (is_v ? cv.pool[kPoolV] : cv.pool[kPoolK128]) + (ring + mid % cv.W) * kHeadDim
-                  : is_v ? v_token(a, b, t - N, h) : k_token(a, b, t - N, h);
+    const uint16_t* row =
+        mid < m0 ? (is_v ? vt + (size_t)r * kHeadDim : kt + (size_t)r * k)
+        : t < N  ? (is_v ? cv.pool[kPoolV] : cv.pool[kPoolK128]) + (ring + mid % cv.W) * kHeadDim
+                 : (is_v ? v_token(a, b, t - N, h) : k_token(a, b, t - N, h));
+    u = *reinterpret_cast<const uint4*>(row + 16 * slot);
+    v = *reinterpret_cast<const uint4*>(row + 16 * slot + 8);
+  };
+  if (kRope) {
+    for (int y = threadIdx.x; y < rc.rope.axes * kQBlockRows; y += kSealThreads) {
+      const int axis = y / kQBlockRows, r = y % kQBlockRows, t = cv.S + kQBlockRows * j + r;
+      s_pos[axis][r] = t >= N ? chunk_position(rc, a.n_max, b, t - N, N, axis) : 0;
     }
-    u = *reinterpret_cast<const uint4*>(row + c0);
-    v = *reinterpret_cast<const uint4*>(row + c1);
+  }
+  // Pairs with a kept channel, a lane each, of the rows that are new (the others are
+  // turned already): half the angles where 32 of 128 channels are kept.  (Blocks of 2 x
+  // 4500 tokens of 7 heads, 350 of them: 24 us with eight rows' loads before their stores,
+  // 30 with four, 46 where the compiler orders them; 34 with every channel turned by the
+  // thread that loads it, and 19 without a rotation.)
+  auto turn = [&](uint16_t* rows) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pairs = rc.rope.rotary_dim / 2;
+    const bool half = rc.rope.layout == kRopeHalf;
+    auto channels = [&](int i) { return half ? make_int2(i, i + pairs) : make_int2(2 * i, 2 * i + 1); };
+    if (warp == 0) {
+      int count = 0;
+      for (int i = lane; i < kHeadDim / 2; i += 32) {
+        const int2 c = channels(i);
+        const bool kept = i < pairs && ((sm.mask[c.x >> 5] >> (c.x & 31) | sm.mask[c.y >> 5] >> (c.y & 31)) & 1u) != 0;
+        const uint32_t those = __ballot_sync(0xffffffffu, kept);
+        if (kept) s_pairs[count + __popc(those & ((1u << lane) - 1u))] = (int16_t)i;
+        count += __popc(those);
+      }
+      if (lane == 0) s_count = count;
+    }
+    __syncthreads();
+    for (int x = lane; x < s_count; x += 32) {
+      const int i = s_pairs[x];
+      const int2 c = channels(i);
+      constexpr int kStep = kSealThreads / 32, kBatch = 8;             // rows whose loads come before their stores
+#pragma unroll 1
+      for (int r0 = warp; r0 < kQBlockRows; r0 += kBatch * kStep) {
+        float2 y[kBatch];
+#pragma unroll
+        for (int z = 0; z < kBatch; ++z) {
+          const int r = r0 + z * kStep;
+          auto pos = [&](int axis) { return s_pos[axis][r]; };
+          const float2 by = rc.rope.axes > 1 ? rope_turn<true>(rc.rope, i, pos) : rope_turn<false>(rc.rope, i, pos);
+          const uint16_t* row = rows + r * kSealStride;
+          y[z] = turn_pair(bf16_to_f32(row[c.x]), bf16_to_f32(row[c.y]), by);
+        }
+#pragma unroll
+        for (int z = 0; z < kBatch; ++z) {
+          const int r = r0 + z * kStep;
+          if (cv.S + kQBlockRows * j + r < N) continue;
+          const uint32_t w = pack_bf16x2(y[z].x, y[z].y);
+          rows[r * kSealStride + c.x] = (uint16_t)w;
+          rows[r * kSealStride + c.y] = (uint16_t)(w >> 16);
+        }
+      }
+    }
   };
-  auto turn = [&](int r, uint4& u, uint4& v) {             // (held rows are turned already)
-    const int t = cv.S + kQBlockRows * j + r;
-    if (kRope && t >= N)
-      share.apply(rc.rope, [&](int axis) { return chunk_position(rc, a.n_max, b, t - N, N, axis); }, u, v);
-  };
-  seal_by_block<kSealThreads>(sm, dst, k, cv.kv_format, cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim,
+  seal_by_block<kSealThreads, kRope>(sm, dst, k, cv.kv_format, cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim,
                               min(max(m0 - kQBlockRows * j, 0), kQBlockRows), load, turn, where);
 }
 

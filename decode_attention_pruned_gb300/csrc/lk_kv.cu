@@ -195,14 +195,14 @@ __global__ void __launch_bounds__(kSealThreads) prefill_seal_block_kernel(const 
   uint8_t* dst = sealed_addr(cv, hd, a.layer, b, h, j);
   if (dst == nullptr) return;
   const size_t first = (((size_t)i * a.n + cv.S + j * kQBlockRows) * cv.Hkv + h) * kHeadDim;
-  seal_by_block<kSealThreads>(
+  seal_by_block<kSealThreads, false>(
       sm, dst, hd.n_kept, cv.kv_format, cv.kept + ((size_t)a.layer * cv.Hkv + h) * kHeadDim, 0,
       [&](int r, int slot, bool is_v, uint4& u, uint4& v) {
         const uint16_t* row = (is_v ? a.v : a.k) + first + (size_t)r * cv.Hkv * kHeadDim + 16 * slot;
         u = reinterpret_cast<const uint4*>(row)[0];
         v = reinterpret_cast<const uint4*>(row)[1];
       },
-      [](int, uint4&, uint4&) {},
+      [](uint16_t*) {},
       [](int slot, int& c0, int& c1) {
         c0 = 16 * slot;
         c1 = c0 + 8;

@@ -3,12 +3,12 @@
 // single warp seals the first two (lk_append.cuh).  Every helper is file-local to
 // the translation unit that includes this header.
 //
-// The rows are staged in shared memory, 16 channels to a thread, K first and V
-// into the same place after it; the largest magnitudes are taken on the way (K of
-// INT8 / FP8, a scale per channel, from the staged rows), then each thread gathers
-// and rounds the 16 codes of a word and writes it whole.  What bounds it is the
-// latency of the rows' loads and the divisions (a correctly rounded one for each
-// code).
+// The rows are staged in shared memory, 16 channels to a thread, K first and V into the
+// same place after it (its loads are on their way while K is rounded); the largest
+// magnitudes are taken on the way (K of INT8 / FP8, a scale per channel, from the staged
+// rows), then each thread gathers and rounds the 16 codes of a word and writes it whole.
+// What bounds it: a block's own chain of loads, barriers and instructions (350 blocks of
+// FP8_BLOCK, 28 MB, take 19 us).
 #pragma once
 #include <cuda_runtime.h>
 
@@ -51,29 +51,27 @@ __device__ __forceinline__ uint32_t magnitude2(uint32_t w, uint32_t keep, uint32
   return top;
 }
 
-// e4m3 codes of x / s, byte y that of x[y], each that of the correctly rounded
-// quotient.  x times 1 / s is off by less than 2^-22 of it: where its neighbours to
-// both sides round to one code, the quotient does, and the division is left out.
-__device__ __forceinline__ uint32_t codes2(float x0, float x1) {
-  uint16_t w;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(w) : "f"(x1), "f"(x0));
-  return w;
-}
+// e4m3 codes of x / s, byte y that of x[y].  With inv = 1 / s, z = x inv and the
+// remainder r = x - z s, z + r inv is the correctly rounded quotient: for a scale m / 448
+// and an x with 8 significant bits each that has been computed for every pair of
+// significands, and 2^-64 divides exactly.  (Below 2^-102, where r may have lost bits, the
+// code is zero.)  A zero keeps its sign; an infinite scale gives 0, and NaN for
+// infinities.  (Correctly rounded divisions, and the code that they
+// take, made 26 us of these 19.)
 __device__ __forceinline__ uint4 codes16(const float (&x)[16], float s, float inv) {
-  uint32_t w[4] = {0u, 0u, 0u, 0u}, far = 0;
+  const float step = s <= 3.4028235e38f ? s : 0.f;
+  uint32_t w[4];
 #pragma unroll
   for (int y = 0; y < 16; y += 2) {
-    const float a = x[y] * inv, b = x[y + 1] * inv;
-    const uint32_t lo = codes2(fmaf(a, -0x1p-22f, a), fmaf(b, -0x1p-22f, b));
-    const uint32_t hi = codes2(fmaf(a, 0x1p-22f, a), fmaf(b, 0x1p-22f, b));
-    w[y / 4] |= lo << 8 * (y & 3);
-    far |= lo ^ hi;
-  }
-  if (far != 0) {
+    float q[2];
 #pragma unroll
-    for (int y = 0; y < 16; y += 4)
-      w[y / 4] = quant_e4m3(x[y], s) | (uint32_t)quant_e4m3(x[y + 1], s) << 8 |
-                 (uint32_t)quant_e4m3(x[y + 2], s) << 16 | (uint32_t)quant_e4m3(x[y + 3], s) << 24;
+    for (int i = 0; i < 2; ++i) {
+      const float z = x[y + i] * inv;
+      q[i] = copysignf(fmaf(fmaf(-z, step, x[y + i]), inv, z), x[y + i]);
+    }
+    uint16_t two;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(q[1]), "f"(q[0]));
+    w[y / 4] = y % 4 == 0 ? two : w[y / 4] | (uint32_t)two << 16;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -81,11 +79,12 @@ __device__ __forceinline__ uint4 codes16(const float (&x)[16], float s, float in
 // All kThreads threads of the block seal rows r = 0 .. 127 into dst.
 //   load(r, slot, is_v, u, v): two runs of 8 channels of row r, those from
 //       where(slot) on; slot = 0 .. 7
-//   turn(r, u, v): what is to be done to a row's K before it is rounded
+//   turn(rows): what is to be done to the staged K before it is rounded (kTurn), by all
+//       threads; channel c of row r is rows[r * kSealStride + c]
 //   where(slot, c0, c1): the first channels of the two runs of a full row
 //   packed: rows below it hold their kept channels side by side (their runs start
 //       at 16 slot and 16 slot + 8), the others all channels
-template <int kThreads, class Load, class Turn, class Where>
+template <int kThreads, bool kTurn, class Load, class Turn, class Where>
 __device__ void seal_by_block(SealSmem& sm, uint8_t* dst, int k, int fmt, const int16_t* kept, int packed, Load load,
                               Turn turn, Where where) {
   static_assert(kThreads % 32 == 0 && kQBlockRows % (kThreads / 8) == 0 && kThreads >= kHeadDim, "whole passes");
@@ -127,7 +126,9 @@ __device__ void seal_by_block(SealSmem& sm, uint8_t* dst, int k, int fmt, const 
       const int r = (tid >> 3) + y * kStep;
       const bool full = !is_v && r >= packed;
       const int c0 = full ? f0 : 16 * slot, c1 = full ? f1 : 16 * slot + 8;
-      if (full) turn(r, u[y], v[y]);
+      *reinterpret_cast<uint4*>(rows + r * kSealStride + c0) = u[y];
+      *reinterpret_cast<uint4*>(rows + r * kSealStride + c1) = v[y];
+      if (kTurn && !is_v) continue;
       const uint32_t m0 = full ? keep0 : 0xffu, m1 = full ? keep1 : 0xffu;
       uint32_t t = magnitude2(u[y].x, m0, 0u);
       t = magnitude2(u[y].y, m0 >> 2, t);
@@ -137,8 +138,6 @@ __device__ void seal_by_block(SealSmem& sm, uint8_t* dst, int k, int fmt, const 
       t = magnitude2(v[y].y, m1 >> 2, t);
       t = magnitude2(v[y].z, m1 >> 4, t);
       t = magnitude2(v[y].w, m1 >> 6, t);
-      *reinterpret_cast<uint4*>(rows + r * kSealStride + c0) = u[y];
-      *reinterpret_cast<uint4*>(rows + r * kSealStride + c1) = v[y];
       if (block) {
         top = max(top, t);
       } else if (is_v) {
@@ -147,43 +146,59 @@ __device__ void seal_by_block(SealSmem& sm, uint8_t* dst, int k, int fmt, const 
         if (slot == 0) sm.scale[r] = __fdiv_rn(__uint_as_float(t), qmax);
       }
     }
+    if (!is_v) fetch(true);                    // on their way while K is rounded
+    // 16 values of a word: a warp takes 32 words of a slab of 16 rows, channels 32 u + 8 t
+    // of the rows g and g + 8 of K, channels 8 g + 2 u and 64 + 8 g + 2 u of four rows of V
+    auto word = [&](int slab, int part, float (&x)[16]) {
+      const int g = lane >> 2, t = lane & 3;
+      if (is_v) {
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const int r = 16 * slab + 2 * t + (y & 1) + 4 * (y & 2);
+          const int c = 16 * (y & 4) + 8 * g + 2 * part;
+          const uint32_t two = *reinterpret_cast<const uint32_t*>(rows + r * kSealStride + c);
+          x[y] = bf16_lo(two);
+          x[y + 8] = bf16_hi(two);
+        }
+      } else {
+        const int c = 32 * part + 8 * t;
+        const uint4 at = *reinterpret_cast<const uint4*>(sm.kept + c);
+        const uint32_t ids[4] = {at.x, at.y, at.z, at.w};
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const int r = 16 * slab + g + (y & 8);
+          const int from = r < packed ? c + (y & 7) : (int)(ids[(y & 7) / 2] >> 16 * (y & 1) & 0xffffu);
+          x[y] = bf16_to_f32(rows[r * kSealStride + from]);
+        }
+      }
+    };
+    if (kTurn && !is_v) {
+      __syncthreads();
+      turn(rows);
+      __syncthreads();
+#pragma unroll 1
+      for (int item = warp; block && item < width / 4; item += kThreads / 32) {
+        float x[16], most = 0.f;
+        word(item & 7, item >> 3, x);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) most = fmaxf(most, fabsf(x[y]));
+        top = max(top, __float_as_uint(most));
+      }
+    }
     if (block) {
       top = __reduce_max_sync(0xffffffffu, top);
       if (lane == 0) atomicMax(&sm.top[is_v], top);
     }
-    if (!is_v) fetch(true);                    // on their way while K is rounded
     __syncthreads();
     uint8_t* to = dst + (is_v ? kQBlockRows * k : 0);
     if (block) {
-      // A warp takes 32 words of a slab of 16 rows: channels 32 u + 8 t of the rows g and
-      // g + 8 of K, channels 8 g + 2 u and 64 + 8 g + 2 u of four rows of V.
       const float scale = fmaxf(__fdiv_rn(__uint_as_float(sm.top[is_v]), qmax), kBlockMinScale);
       const float inv = __frcp_rn(scale);
-      const int g = lane >> 2, t = lane & 3;
 #pragma unroll 1
       for (int item = warp; item < width / 4; item += kThreads / 32) {
         const int slab = item & 7, part = item >> 3;
         float x[16];
-        if (is_v) {
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const int r = 16 * slab + 2 * t + (y & 1) + 4 * (y & 2);
-            const int c = 16 * (y & 4) + 8 * g + 2 * part;
-            const uint32_t two = *reinterpret_cast<const uint32_t*>(rows + r * kSealStride + c);
-            x[y] = bf16_lo(two);
-            x[y + 8] = bf16_hi(two);
-          }
-        } else {
-          const int c = 32 * part + 8 * t;
-          const uint4 at = *reinterpret_cast<const uint4*>(sm.kept + c);
-          const uint32_t ids[4] = {at.x, at.y, at.z, at.w};
-#pragma unroll
-          for (int y = 0; y < 16; ++y) {
-            const int r = 16 * slab + g + (y & 8);
-            const int from = r < packed ? c + (y & 7) : (int)(ids[(y & 7) / 2] >> 16 * (y & 1) & 0xffffu);
-            x[y] = bf16_to_f32(rows[r * kSealStride + from]);
-          }
-        }
+        word(slab, part, x);
         *reinterpret_cast<uint4*>(to + 16 * (slab * width + 32 * part + lane)) = codes16(x, scale, inv);
       }
       if (tid == 0) reinterpret_cast<float*>(dst + block_soff(k))[is_v] = scale;
