@@ -41,7 +41,10 @@
 // take 98 us, 1.4 times what a plain copy's rate gives their bytes.  Sealed
 // blocks: the softmax and the four warps that expand them, which share instruction
 // caches with every other role; 16 sequences of 8192 tokens take 114 us, 4.0 times
-// their bytes.  One sequence: three dependent launches, 28 us over 32768 tokens.
+// their bytes; as FP8_BLOCK, whose one scale is the softmax's affair, 16 sequences of
+// 8192 tokens and 16 queries each take 87 us, and 512 queries of 32 heads over 32768
+// tokens 178 (in bf16 151), paced by the loading thread and the makers: their
+// instructions come at 20 clocks each.  One sequence: three dependent launches, 28 us over 32768 tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -578,6 +581,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Bits lo .. hi - 1 of a 128-key tile.
 __device__ __forceinline__ void add_range(uint32_t (&m)[4], int lo, int hi) {
 #pragma unroll
@@ -791,10 +805,10 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       if constexpr (kFmt == kKvFp8Block) {
         // A warp takes whole slabs of 16 rows: where the codes lie in the tile's second
         // half, a slab's are where its own rows' channels 64 on go.
-        if (mt == 0) {
-          const float scale = reinterpret_cast<const float*>(sm + job.scales)[job.values];
-          if (job.values == 0) *reinterpret_cast<float*>(sm + L::kTileBack + 4 * (ri * L::kSlots + job.slot)) = scale;
-          else *reinterpret_cast<float*>(sm + L::kValueLog + (job.scales - L::kVScale) / kTile) = log2f(scale);
+        if (mt == 0 && job.values == 0) {
+          const float2 scale = *reinterpret_cast<const float2*>(sm + job.scales);
+          *reinterpret_cast<float4*>(sm + L::kVScale + 16 * (ri * L::kSlots + job.slot)) =
+              make_float4(scale.x, lg2(scale.y), rcp(scale.y), 0.f);
         }
         const uint8_t* codes = to + kTile * job.width * (job.width == kHeadDim ? 1 : 2);
         const int g = lane >> 2, t = lane & 3;
@@ -841,7 +855,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
                 for (int u = 0; u < 4; ++u)
                   pair_f16(mix(half ? w[u].y : w[u].x, half ? w[u].w : w[u].z, two ? 0x7362u : 0x5140u), x[u], y[u]);
                 const int r = row + 2 * t + 8 * two;
-                *reinterpret_cast<uint4*>(to + kept_byte(kHeadDim, r, 8 * half + g)) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4*>(to + kept_byte(kHeadDim, r, 8 * half + g)) =
+                    make_uint4(x[0], x[1], x[2], x[3]);
                 *reinterpret_cast<uint4*>(to + kept_byte(kHeadDim, r + 1, 8 * half + g)) =
                     make_uint4(y[0], y[1], y[2], y[3]);
               }
@@ -1004,7 +1019,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             const Tile t = tile_at<kQuant>(it, j);
             const bool wide = isv || t.type <= kTileC || it.k == kHeadDim || (kQuant && t.type == kTileF);
             // (the codes of sealed keys on part of the channels land behind the tile)
-            const bool seal = kQuant && t.type == kTileM;
+            const bool seal = kQuant && kFmt != kKvFp8Block && t.type == kTileM;
             // A tile's keys are waited for while the values before them are in use:
             // keys never take more than the keys of their item before them did, whose
             // place they then find, so full-width ones take what sealed ones on 96
@@ -1020,7 +1035,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             const uint32_t dst = ring_at + at, bar = full + 8 * slot;
             ++put;
             by_job = (by_job & ~(1u << slot)) | (seal ? 1u << slot : 0u);
-            if (seal) {
+            if (kFmt != kKvFp8Block && seal) {
               // The codes land in the upper half of the tile's place, or behind it,
               // their scales beside the job; the makers do the rest.
               const uint32_t jn = jobs % L::kJobs, landed = base + L::kLanded + 8 * (ri * L::kJobs + jn);
@@ -1029,19 +1044,16 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               const uint8_t* block = cv.qpool + hd.qoff +
                                      (pages != nullptr ? (int64_t)max(0, pg)
                                                        : (int64_t)it.b * hd.qblocks + t.r0 / kTile) *
-                                         sealed_bytes(kFmt, it.k);
+                                         qblock_bytes(it.k);
               const int width = isv ? kHeadDim : it.k, vn = (int)(sealed & 3);
-              constexpr bool kBlock = kFmt == kKvFp8Block;
-              const uint32_t codes = (uint32_t)(kTile * width),
-                             scales = kBlock ? 16u : isv ? kTile * 4u : (uint32_t)(4 * it.k);
+              const uint32_t codes = (uint32_t)(kTile * width), scales = isv ? kTile * 4u : (uint32_t)(4 * it.k);
               const uint32_t sc =
                   isv ? L::kVScale + (4 * ri + vn) * kTile * 4 : L::kKScale + (ri * L::kJobs + jn) * kTile * 4;
               *reinterpret_cast<Job*>(sm + L::kJob + (ri * L::kJobs + jn) * L::kJobBytes) =
                   Job{width, isv ? 1 : 0, slot, dst - base, sc};
               mbar_arrive_expect_tx(landed, codes + scales);
               bulk_load(dst + (wide ? 1 : 2) * codes, block + (isv ? qblock_voff(it.k) : 0), codes, landed, keep);
-              bulk_load(base + sc, block + (kBlock ? block_soff(it.k) : isv ? qblock_vsoff(it.k) : qblock_ksoff(it.k)),
-                        scales, landed, keep);
+              bulk_load(base + sc, block + (isv ? qblock_vsoff(it.k) : qblock_ksoff(it.k)), scales, landed, keep);
               sealed += isv ? 1 : 0;
               ++jobs;
               return true;
@@ -1084,7 +1096,9 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           constexpr int kStep = kDual ? 1 : 2;
           const int j0 = s.t0 + (kDual ? 0 : ri);
           int32_t page = page_at(j0);
-          for (int j = j0; ok && j < s.t1; j += kStep) {
+          int j = j0;
+          const int t1 = kFmt == kKvFp8Block ? min(s.t1, m0) : s.t1;
+          for (; ok && j < t1; j += kStep) {
             const int32_t after = page_at(j + kStep);
             if (kQuant || !kDual) {
               // (one copy of these instructions: 98 us instead of 100 for 64 sequences of
@@ -1096,6 +1110,43 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
               ok = load(j, false, page) && load(j, true, page);
             }
             page = after;
+          }
+          if constexpr (kFmt == kKvFp8Block) {
+            // The blocks, in as few instructions as they need: a loading thread's come from
+            // caches that it shares with every other role (20 clocks an instruction).
+            const int k = it.k;
+            const uint32_t block_size = (uint32_t)block_bytes(k), k_codes = (uint32_t)(kTile * k);
+            const uint8_t* blocks =
+                cv.qpool + hd.qoff + (pages != nullptr ? 0 : (int64_t)it.b * hd.qblocks * block_size);
+            const uint32_t k_place = k == kHeadDim ? (uint32_t)kWideBytes : 3 * k_codes;
+            // (page ids are read two blocks ahead: what is read is waited for when it moves on)
+            page = page_at(j);
+            int32_t after = page_at(j + kStep);
+            for (; ok && j < s.t1; j += kStep) {
+              const uint8_t* from = blocks + (int64_t)(pages != nullptr ? max(0, page) : j - m0) * block_size;
+              page = after;
+              after = page_at(j + 2 * kStep);
+#pragma unroll 1
+              for (uint32_t isv = 0; isv < 2; ++isv) {
+                const uint32_t codes = isv != 0 ? kTile * kHeadDim : k_codes;
+                uint32_t at;
+                ok = reserve(isv != 0 ? (uint32_t)kWideBytes : k_place, at);
+                const uint32_t jn = ri * L::kJobs + jobs % L::kJobs, landed = base + L::kLanded + 8 * jn;
+                if (ok && jobs >= L::kJobs) ok = wait(base + L::kDone + 8 * jn, (jobs / L::kJobs - 1) & 1);
+                if (!ok) break;
+                const uint32_t slot = put++ % L::kSlots, dst = ring_at + at;
+                offs[slot] = at;
+                info[slot] = dst >> 4 | (uint32_t)kTile << 16 | (3u + (isv != 0 ? 4u : (uint32_t)k / 32)) << 24;
+                by_job |= 1u << slot;
+                *reinterpret_cast<Job*>(sm + L::kJob + jn * L::kJobBytes) =
+                    Job{isv != 0 ? kHeadDim : k, (int32_t)isv, slot, dst - base, L::kKScale + jn * kTile * 4};
+                mbar_arrive_expect_tx(landed, isv != 0 ? codes : codes + 16);
+                if (isv == 0) bulk_load(base + L::kKScale + jn * kTile * 4, from + block_soff(k), 16, landed, keep);
+                bulk_load(dst + (isv != 0 || k == kHeadDim ? codes : 2 * codes), from, codes, landed, keep);
+                from += codes;
+                ++jobs;
+              }
+            }
           }
         }
         // Every copy lands before this thread ends, whether or not its wait ran out
@@ -1374,17 +1425,149 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       bool moved = false;                 // m has been moved to what sealed blocks need
       const int i_first = it.i0 + (kDual ? st * tq : 0), i_last = min(i_first + tq, it.i0 + it.ntok) - 1;
       const int f1 = f0 + min(kQuant ? it.rows_f : kFar, max(0, it.N + i_first - cv.W + 1 - it.far0)) / kTile;
-      for (int j = s.t0 + (kDual ? 0 : st); ok && j < s.t1; j += kDual ? 1 : 2) {
-        uint32_t vis[4] = {};
+      // one half of a key tile
+      bool all = false;
+      int halves = 2;
+      uint32_t vis[4] = {};
+      const float* vscale = nullptr;
+      float score_scale = kScaleLog2, value_log = 0.f;
+      float weight_log = 0.f, weight_back = 1.f;       // FP8_BLOCK: log2 of the values' scale, and its inverse
+      // kind 0: whatever the tile is; 1: keys and values in bf16; 2: a block of FP8_BLOCK
+      auto step = [&](auto kind, int half) {
+        constexpr bool kSealed = decltype(kind)::value == 2, kScaled = kQuant && decltype(kind)::value != 1;
+        const uint32_t s_half = my_s + half * kHalf;
+        ok = wait.warp(base + L::kSFull + 16 * st + 8 * half, (hs >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        if (half == halves) {
+          if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8);
+          ++hs;
+          return;
+        }
+        uint32_t x[kHalf];
+        tmem_ld32(s_half, x);
+        tmem_ld32(s_half + 32, x + 32);
+        tmem_loaded<kHalf>(x);
+        if (!kSealed && !all) {
+          const uint32_t v0 = half == 0 ? vis[0] : vis[2], v1 = half == 0 ? vis[1] : vis[3];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if ((v0 >> c & 1u) == 0) x[c] = 0xff800000u;
+            if ((v1 >> c & 1u) == 0) x[32 + c] = 0xff800000u;
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+#pragma unroll
+        for (int c = 8; c < kHalf; c += 2)
+          mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kScaled ? score_scale : kScaleLog2);
+        // (nobody's rows score whatever lies behind q: they move no one's maximum)
+        if (!kDual && !mine) top = -INFINITY;
+        // The maximum moves only when a score exceeds it by 8, p by 2^8: fp32 sums and
+        // bf16 weights lose no more of it than of one below 1.  (Each row's by itself:
+        // what a row comes to does not depend on the others of its warp.)
+        // Over sealed blocks the scores count with their values' scale, and the first
+        // one moves m to what they need (see kWeightExp).
+        const bool move = (kSealed || (kScaled && vscale != nullptr)) && !moved;
+        if (kScaled) top += value_log;
+        if (__any_sync(0xffffffffu, top > m + 8.f) || move) {
+          const float at = move ? m + value_log : m, mn = top > (move ? at : m + 8.f) ? top : at;
+          const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+          if (kScaled) moved = moved || move;
+          m = mn;
+          l *= f;
+          if (begun) {
+            // (these scores came after the product before the last one was
+            // done, so its phase is the one before this)
+            ok = wait.warp(base + L::kOFull + 8 * st, (hs - 1) & 1);
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(my_o + 32 * c, o);
+              tmem_loaded<32>(o);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st32(my_o + 32 * c, o);
+            }
+          }
+        }
+        // P goes to the tensor core in V's type, bf16, which rounds every weight by up
+        // to 2^-8 of itself, as o is rounded once more at the end; l sums the unrounded
+        // ones.  Against fp64 o is off by 2.3e-3 instead of the 1.66e-3 of its own
+        // rounding.  P as the sum of two bf16 numbers, with a second product for the
+        // lower one, gives 1.66e-3, and takes 120 us instead of 100 for 64 sequences of
+        // 4096 tokens (4 queries each), 1117 instead of 871 for 1000 queries over 131072.
+        // (Sealed blocks' weights are f16: see kWeightExp.)
+        const float off = m == -INFINITY ? 0.f : kSealed ? weight_log - m : -m;
+        const float sc = kScaled ? score_scale : kScaleLog2;
+        const uint64_t scale2 = pair(sc, sc), off2 = pair(off, off);
+        uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 2) {
+          float p0, p1;
+          unpair(fma2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, off2), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          sum[c >> 1 & 3] = add2(sum[c >> 1 & 3], pair(p0, p1));
+          if (kSealed) {
+            x[c >> 1] = pack_f16x2(p0, p1);
+          } else if (kScaled) {
+            x[c] = __float_as_uint(p0);
+            x[c + 1] = __float_as_uint(p1);
+          } else {
+            x[c >> 1] = pack_bf16x2(p0, p1);
+          }
+        }
+        if (kScaled && !kSealed) {
+          if (vscale != nullptr) {
+            const ulonglong2* f = reinterpret_cast<const ulonglong2*>(vscale + half * kHalf);
+            auto times = [&](int c, uint64_t y) {
+              float p0, p1;
+              unpair(mul2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), y), p0, p1);
+              x[c >> 1] = pack_f16x2(p0, p1);
+            };
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 4) {
+              const ulonglong2 y = f[c / 4];
+              times(c, y.x);
+              times(c + 2, y.y);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 2)
+              x[c >> 1] = pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+          }
+        }
+        tmem_st32(s_half, x);
+        float l0, l1;
+        unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+        l = kSealed ? fmaf(l0 + l1, weight_back, l) : l + (l0 + l1);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8 * half);
+        ++hs;
+        begun = true;
+      };
+      // FP8_BLOCK: the sealed blocks come last, and have a loop of their own below
+      const int t1 = kFmt == kKvFp8Block ? min(s.t1, m0) : s.t1;
+      int j = s.t0 + (kDual ? 0 : st);
+      for (; ok && j < t1; j += kDual ? 1 : 2) {
+        vis[0] = vis[1] = vis[2] = vis[3] = 0;
         // tiles that every query of the group sees whole, the common case
-        bool all = j >= m0 && j < m1;
+        all = j >= m0 && j < m1;
         if (j >= f0 && (!kQuant || j < m0)) {
           all = j < f1;
         } else if (j >= it.nA && j < (kQuant ? f0 : m0)) {
           const int r0 = tile_at<kQuant>(it, j).r0;
           all = r0 + kTile - 1 <= i_first && i_last - r0 < it.win && it.policy != kSpecial;
         }
-        int halves = 2, rows = kTile;
+        halves = 2;
+        int rows = kTile;
         if (!all) {
           const Tile t = tile_at<kQuant>(it, j);
           visible(a, w, it, t, i, vis);
@@ -1408,10 +1591,10 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         }
         // a sealed block's values are codes: their scales, once they are there, and the
         // scores' factor (made before the values, by the same warps)
-        const float* vscale = nullptr;
-        float score_scale = kScaleLog2, value_log = 0.f;
-        float weight_log = 0.f, weight_back = 1.f;       // FP8_BLOCK: log2 of the values' scale, and its inverse
-        if (kQuant && j >= m0) {
+        vscale = nullptr;
+        score_scale = kScaleLog2;
+        value_log = 0.f;
+        if (kQuant && kFmt != kKvFp8Block && j >= m0) {
           const uint32_t e = entries + 2 * ((j - s.t0) / (kDual ? 1 : 2)) + 1;
           const uint32_t slot = e % L::kSlots + (kDual ? 0 : st * L::kSlots);
           ok = wait.warp(base + L::kFull + 8 * slot, (e / L::kSlots) & 1);
@@ -1419,11 +1602,6 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           const int v_at = (kDual ? 0 : 4 * st) + (int)(sealed++ & 3);
           vscale = reinterpret_cast<const float*>(sm + L::kVScale) + v_at * kTile;
           value_log = *reinterpret_cast<const volatile float*>(sm + L::kValueLog + 4 * v_at);
-          if (kFmt == kKvFp8Block) {
-            weight_log = value_log;
-            weight_back = ex2(-weight_log);
-            value_log -= kWeightExp;
-          }
           if (!scaled) {
             ok = wait.warp(base + L::kQKFull + (kDual ? 8 * st : 0), (gathered - 1) & 1);
             if (!ok) break;
@@ -1433,127 +1611,28 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           const uint32_t k_slot = (e - 1) % L::kSlots + (kDual ? 0 : st * L::kSlots);
           score_scale = back * *reinterpret_cast<const volatile float*>(sm + L::kTileBack + 4 * k_slot);
         }
+        constexpr int kKind = kFmt == kKvFp8Block ? 1 : 0;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t s_half = my_s + half * kHalf;
-          ok = wait.warp(base + L::kSFull + 16 * st + 8 * half, (hs >> 1) & 1);
+        for (int half = 0; ok && half < 2; ++half) step(std::integral_constant<int, kKind>(), half);
+      }
+      if constexpr (kFmt == kKvFp8Block) {
+        if (ok && j < s.t1) {
+          ok = wait.warp(base + L::kQKFull + (kDual ? 8 * st : 0), (gathered - 1) & 1);
+          back = row_back(gathered - 1)[row];
+        }
+        halves = 2;
+        for (; ok && j < s.t1; j += kDual ? 1 : 2) {
+          const uint32_t e = entries + 2 * ((j - s.t0) / (kDual ? 1 : 2));
+          const uint32_t slot = e % L::kSlots + (kDual ? 0 : st * L::kSlots);
+          ok = wait.warp(base + L::kFull + 8 * slot, (e / L::kSlots) & 1);
           if (!ok) break;
-          tc_fence_after();
-          if (half == halves) {
-            if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8);
-            ++hs;
-            break;
-          }
-          uint32_t x[kHalf];
-          tmem_ld32(s_half, x);
-          tmem_ld32(s_half + 32, x + 32);
-          tmem_loaded<kHalf>(x);
-          if (!all) {
-            const uint32_t v0 = half == 0 ? vis[0] : vis[2], v1 = half == 0 ? vis[1] : vis[3];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if ((v0 >> c & 1u) == 0) x[c] = 0xff800000u;
-              if ((v1 >> c & 1u) == 0) x[32 + c] = 0xff800000u;
-            }
-          }
-          float mx[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-#pragma unroll
-          for (int c = 8; c < kHalf; c += 2)
-            mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kQuant ? score_scale : kScaleLog2);
-          // (nobody's rows score whatever lies behind q: they move no one's maximum)
-          if (!kDual && !mine) top = -INFINITY;
-          // The maximum moves only when a score exceeds it by 8, p by 2^8: fp32 sums and
-          // bf16 weights lose no more of it than of one below 1.  (Each row's by itself:
-          // what a row comes to does not depend on the others of its warp.)
-          // Over sealed blocks the scores count with their values' scale, and the first
-          // one moves m to what they need (see kWeightExp).
-          const bool move = kQuant && vscale != nullptr && !moved;
-          if (kQuant) top += value_log;
-          if (__any_sync(0xffffffffu, top > m + 8.f) || move) {
-            const float at = move ? m + value_log : m, mn = top > (move ? at : m + 8.f) ? top : at;
-            const float f = m == -INFINITY ? 0.f : ex2(m - mn);
-            if (kQuant) moved = moved || move;
-            m = mn;
-            l *= f;
-            if (begun) {
-              // (these scores came after the product before the last one was
-              // done, so its phase is the one before this)
-              ok = wait.warp(base + L::kOFull + 8 * st, (hs - 1) & 1);
-              if (!ok) break;
-              tc_fence_after();
+          const float4 scale = *reinterpret_cast<const float4*>(sm + L::kVScale + 16 * slot);
+          score_scale = back * scale.x;
+          weight_log = scale.y;
+          weight_back = scale.z;
+          value_log = weight_log - kWeightExp;
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tmem_ld32(my_o + 32 * c, o);
-                tmem_loaded<32>(o);
-#pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                tmem_st32(my_o + 32 * c, o);
-              }
-            }
-          }
-          // P goes to the tensor core in V's type, bf16, which rounds every weight by up
-          // to 2^-8 of itself, as o is rounded once more at the end; l sums the unrounded
-          // ones.  Against fp64 o is off by 2.3e-3 instead of the 1.66e-3 of its own
-          // rounding.  P as the sum of two bf16 numbers, with a second product for the
-          // lower one, gives 1.66e-3, and takes 120 us instead of 100 for 64 sequences of
-          // 4096 tokens (4 queries each), 1117 instead of 871 for 1000 queries over 131072.
-          // (Sealed blocks' weights are f16: see kWeightExp.)
-          const float off = m == -INFINITY ? 0.f : weight_log - m;
-          const float sc = kQuant ? score_scale : kScaleLog2;
-          const uint64_t scale2 = pair(sc, sc), off2 = pair(off, off);
-          uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int c = 0; c < kHalf; c += 2) {
-            float p0, p1;
-            unpair(fma2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, off2), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            sum[c >> 1 & 3] = add2(sum[c >> 1 & 3], pair(p0, p1));
-            if (kQuant) {
-              x[c] = __float_as_uint(p0);
-              x[c + 1] = __float_as_uint(p1);
-            } else {
-              x[c >> 1] = pack_bf16x2(p0, p1);
-            }
-          }
-          if (kQuant) {
-            if (kFmt == kKvFp8Block && vscale != nullptr) {
-#pragma unroll
-              for (int c = 0; c < kHalf; c += 2)
-                x[c >> 1] = pack_f16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-            } else if (vscale != nullptr) {
-              const ulonglong2* f = reinterpret_cast<const ulonglong2*>(vscale + half * kHalf);
-              auto times = [&](int c, uint64_t y) {
-                float p0, p1;
-                unpair(mul2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), y), p0, p1);
-                x[c >> 1] = pack_f16x2(p0, p1);
-              };
-#pragma unroll
-              for (int c = 0; c < kHalf; c += 4) {
-                const ulonglong2 y = f[c / 4];
-                times(c, y.x);
-                times(c + 2, y.y);
-              }
-            } else {
-#pragma unroll
-              for (int c = 0; c < kHalf; c += 2)
-                x[c >> 1] = pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-            }
-          }
-          tmem_st32(s_half, x);
-          float l0, l1;
-          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
-          l = kFmt == kKvFp8Block ? fmaf(l0 + l1, weight_back, l) : l + (l0 + l1);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8 * half);
-          ++hs;
-          begun = true;
+          for (int half = 0; ok && half < 2; ++half) step(std::integral_constant<int, 2>(), half);
         }
       }
       entries = end;
