@@ -1096,9 +1096,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           constexpr int kStep = kDual ? 1 : 2;
           const int j0 = s.t0 + (kDual ? 0 : ri);
           int32_t page = page_at(j0);
-          int j = j0;
-          const int t1 = kFmt == kKvFp8Block ? min(s.t1, m0) : s.t1;
-          for (; ok && j < t1; j += kStep) {
+          for (int j = j0; ok && j < (kFmt == kKvFp8Block ? min(s.t1, m0) : s.t1); j += kStep) {
             const int32_t after = page_at(j + kStep);
             if (kQuant || !kDual) {
               // (one copy of these instructions: 98 us instead of 100 for 64 sequences of
@@ -1119,6 +1117,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             const uint8_t* blocks =
                 cv.qpool + hd.qoff + (pages != nullptr ? 0 : (int64_t)it.b * hd.qblocks * block_size);
             const uint32_t k_place = k == kHeadDim ? (uint32_t)kWideBytes : 3 * k_codes;
+            int j = j0 + max(0, (m0 - j0 + kStep - 1) / kStep) * kStep;
             // (page ids are read two blocks ahead: what is read is waited for when it moves on)
             page = page_at(j);
             int32_t after = page_at(j + kStep);
@@ -1425,24 +1424,24 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       bool moved = false;                 // m has been moved to what sealed blocks need
       const int i_first = it.i0 + (kDual ? st * tq : 0), i_last = min(i_first + tq, it.i0 + it.ntok) - 1;
       const int f1 = f0 + min(kQuant ? it.rows_f : kFar, max(0, it.N + i_first - cv.W + 1 - it.far0)) / kTile;
-      // one half of a key tile
-      bool all = false;
-      int halves = 2;
-      uint32_t vis[4] = {};
-      const float* vscale = nullptr;
-      float score_scale = kScaleLog2, value_log = 0.f;
-      float weight_log = 0.f, weight_back = 1.f;       // FP8_BLOCK: log2 of the values' scale, and its inverse
-      // kind 0: whatever the tile is; 1: keys and values in bf16; 2: a block of FP8_BLOCK
-      auto step = [&](auto kind, int half) {
+      // How a tile's scores and weights count.
+      struct Scale {
+        const float* values;              // INT8 / FP8: scales of a block's values; null: not a block
+        float score, value_log;           // factor of scores; log2 of the values' size, where m follows it
+        float weight_log, weight_back;    // FP8_BLOCK: log2 of the values' scale, and its inverse
+      };
+      // One half of a key tile; false: no more of it.  kind 0: whatever the tile is; 1: keys
+      // and values in bf16; 2: a block of FP8_BLOCK.
+      auto step = [&](auto kind, int half, bool all, int halves, const uint32_t (&vis)[4], const Scale& sca) -> bool {
         constexpr bool kSealed = decltype(kind)::value == 2, kScaled = kQuant && decltype(kind)::value != 1;
         const uint32_t s_half = my_s + half * kHalf;
         ok = wait.warp(base + L::kSFull + 16 * st + 8 * half, (hs >> 1) & 1);
-        if (!ok) return;
+        if (!ok) return false;
         tc_fence_after();
         if (half == halves) {
           if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8);
           ++hs;
-          return;
+          return false;
         }
         uint32_t x[kHalf];
         tmem_ld32(s_half, x);
@@ -1462,7 +1461,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
 #pragma unroll
         for (int c = 8; c < kHalf; c += 2)
           mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kScaled ? score_scale : kScaleLog2);
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kScaled ? sca.score : kScaleLog2);
         // (nobody's rows score whatever lies behind q: they move no one's maximum)
         if (!kDual && !mine) top = -INFINITY;
         // The maximum moves only when a score exceeds it by 8, p by 2^8: fp32 sums and
@@ -1470,10 +1469,10 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         // what a row comes to does not depend on the others of its warp.)
         // Over sealed blocks the scores count with their values' scale, and the first
         // one moves m to what they need (see kWeightExp).
-        const bool move = (kSealed || (kScaled && vscale != nullptr)) && !moved;
-        if (kScaled) top += value_log;
+        const bool move = (kSealed || (kScaled && sca.values != nullptr)) && !moved;
+        if (kScaled) top += sca.value_log;
         if (__any_sync(0xffffffffu, top > m + 8.f) || move) {
-          const float at = move ? m + value_log : m, mn = top > (move ? at : m + 8.f) ? top : at;
+          const float at = move ? m + sca.value_log : m, mn = top > (move ? at : m + 8.f) ? top : at;
           const float f = m == -INFINITY ? 0.f : ex2(m - mn);
           if (kScaled) moved = moved || move;
           m = mn;
@@ -1482,7 +1481,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             // (these scores came after the product before the last one was
             // done, so its phase is the one before this)
             ok = wait.warp(base + L::kOFull + 8 * st, (hs - 1) & 1);
-            if (!ok) return;
+            if (!ok) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -1502,8 +1501,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         // lower one, gives 1.66e-3, and takes 120 us instead of 100 for 64 sequences of
         // 4096 tokens (4 queries each), 1117 instead of 871 for 1000 queries over 131072.
         // (Sealed blocks' weights are f16: see kWeightExp.)
-        const float off = m == -INFINITY ? 0.f : kSealed ? weight_log - m : -m;
-        const float sc = kScaled ? score_scale : kScaleLog2;
+        const float off = m == -INFINITY ? 0.f : kSealed ? sca.weight_log - m : -m;
+        const float sc = kScaled ? sca.score : kScaleLog2;
         const uint64_t scale2 = pair(sc, sc), off2 = pair(off, off);
         uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -1523,8 +1522,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           }
         }
         if (kScaled && !kSealed) {
-          if (vscale != nullptr) {
-            const ulonglong2* f = reinterpret_cast<const ulonglong2*>(vscale + half * kHalf);
+          if (sca.values != nullptr) {
+            const ulonglong2* f = reinterpret_cast<const ulonglong2*>(sca.values + half * kHalf);
             auto times = [&](int c, uint64_t y) {
               float p0, p1;
               unpair(mul2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), y), p0, p1);
@@ -1545,29 +1544,29 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         tmem_st32(s_half, x);
         float l0, l1;
         unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
-        l = kSealed ? fmaf(l0 + l1, weight_back, l) : l + (l0 + l1);
+        l = kSealed ? fmaf(l0 + l1, sca.weight_back, l) : l + (l0 + l1);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8 * half);
         ++hs;
         begun = true;
+        return true;
       };
       // FP8_BLOCK: the sealed blocks come last, and have a loop of their own below
-      const int t1 = kFmt == kKvFp8Block ? min(s.t1, m0) : s.t1;
-      int j = s.t0 + (kDual ? 0 : st);
-      for (; ok && j < t1; j += kDual ? 1 : 2) {
-        vis[0] = vis[1] = vis[2] = vis[3] = 0;
+      constexpr int kStep = kDual ? 1 : 2;
+      const int j0 = s.t0 + (kDual ? 0 : st);
+      for (int j = j0; ok && j < (kFmt == kKvFp8Block ? min(s.t1, m0) : s.t1); j += kStep) {
+        uint32_t vis[4] = {};
         // tiles that every query of the group sees whole, the common case
-        all = j >= m0 && j < m1;
+        bool all = j >= m0 && j < m1;
         if (j >= f0 && (!kQuant || j < m0)) {
           all = j < f1;
         } else if (j >= it.nA && j < (kQuant ? f0 : m0)) {
           const int r0 = tile_at<kQuant>(it, j).r0;
           all = r0 + kTile - 1 <= i_first && i_last - r0 < it.win && it.policy != kSpecial;
         }
-        halves = 2;
-        int rows = kTile;
+        int halves = 2, rows = kTile;
         if (!all) {
           const Tile t = tile_at<kQuant>(it, j);
           visible(a, w, it, t, i, vis);
@@ -1591,17 +1590,15 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         }
         // a sealed block's values are codes: their scales, once they are there, and the
         // scores' factor (made before the values, by the same warps)
-        vscale = nullptr;
-        score_scale = kScaleLog2;
-        value_log = 0.f;
+        Scale sca{nullptr, kScaleLog2, 0.f, 0.f, 1.f};
         if (kQuant && kFmt != kKvFp8Block && j >= m0) {
           const uint32_t e = entries + 2 * ((j - s.t0) / (kDual ? 1 : 2)) + 1;
           const uint32_t slot = e % L::kSlots + (kDual ? 0 : st * L::kSlots);
           ok = wait.warp(base + L::kFull + 8 * slot, (e / L::kSlots) & 1);
           if (!ok) break;
           const int v_at = (kDual ? 0 : 4 * st) + (int)(sealed++ & 3);
-          vscale = reinterpret_cast<const float*>(sm + L::kVScale) + v_at * kTile;
-          value_log = *reinterpret_cast<const volatile float*>(sm + L::kValueLog + 4 * v_at);
+          sca.values = reinterpret_cast<const float*>(sm + L::kVScale) + v_at * kTile;
+          sca.value_log = *reinterpret_cast<const volatile float*>(sm + L::kValueLog + 4 * v_at);
           if (!scaled) {
             ok = wait.warp(base + L::kQKFull + (kDual ? 8 * st : 0), (gathered - 1) & 1);
             if (!ok) break;
@@ -1609,30 +1606,30 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
             scaled = true;
           }
           const uint32_t k_slot = (e - 1) % L::kSlots + (kDual ? 0 : st * L::kSlots);
-          score_scale = back * *reinterpret_cast<const volatile float*>(sm + L::kTileBack + 4 * k_slot);
+          sca.score = back * *reinterpret_cast<const volatile float*>(sm + L::kTileBack + 4 * k_slot);
         }
         constexpr int kKind = kFmt == kKvFp8Block ? 1 : 0;
 #pragma unroll 1
-        for (int half = 0; ok && half < 2; ++half) step(std::integral_constant<int, kKind>(), half);
+        for (int half = 0; half < 2; ++half)
+          if (!step(std::integral_constant<int, kKind>(), half, all, halves, vis, sca)) break;
       }
       if constexpr (kFmt == kKvFp8Block) {
+        int j = j0 + max(0, (m0 - j0 + kStep - 1) / kStep) * kStep;
         if (ok && j < s.t1) {
           ok = wait.warp(base + L::kQKFull + (kDual ? 8 * st : 0), (gathered - 1) & 1);
           back = row_back(gathered - 1)[row];
         }
-        halves = 2;
-        for (; ok && j < s.t1; j += kDual ? 1 : 2) {
+        const uint32_t whole[4] = {};
+        for (; ok && j < s.t1; j += kStep) {
           const uint32_t e = entries + 2 * ((j - s.t0) / (kDual ? 1 : 2));
           const uint32_t slot = e % L::kSlots + (kDual ? 0 : st * L::kSlots);
           ok = wait.warp(base + L::kFull + 8 * slot, (e / L::kSlots) & 1);
           if (!ok) break;
           const float4 scale = *reinterpret_cast<const float4*>(sm + L::kVScale + 16 * slot);
-          score_scale = back * scale.x;
-          weight_log = scale.y;
-          weight_back = scale.z;
-          value_log = weight_log - kWeightExp;
+          const Scale sca{nullptr, back * scale.x, scale.y - kWeightExp, scale.y, scale.z};
 #pragma unroll 1
-          for (int half = 0; ok && half < 2; ++half) step(std::integral_constant<int, 2>(), half);
+          for (int half = 0; half < 2; ++half)
+            if (!step(std::integral_constant<int, 2>(), half, true, 2, whole, sca)) break;
         }
       }
       entries = end;

@@ -67,7 +67,7 @@ constexpr int kQStride = kHeadDim + 32;        // row of q: the next one's words
 constexpr float kRescaleGap = 2.f;             // log2: m moves when what it follows exceeds it by more
 constexpr int kFlush = 8;                      // stages whose products share accumulators
 constexpr int kWeightExp = 12;                 // log2 of the largest sealed weight when m moves
-constexpr uint32_t kMinCtaCost = 16;           // line a CTA takes at least: 64 KB, more than any piece
+constexpr uint32_t kMinCtaCost = 16;           // line a CTA takes at least: 64 KB, what the largest piece takes
 constexpr int kRowTop = 14;                    // a row of q is moved so that its largest channel lies in [2^14, 2^15)
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the producer's wait for its copies at the end
 constexpr int kHeadsKept = 48, kLensKept = 512;            // descriptors and lengths that shared memory has places for
@@ -180,8 +180,8 @@ __device__ __forceinline__ uint32_t last_piece(const Entry& g, uint32_t off) {
 struct EntryId {
   int lr, l, b, h;
 };
-__device__ __forceinline__ uint32_t fdiv(uint32_t x, const FastDiv& f) {
-  return f.m == 0 ? x : (uint32_t)__umul64hi((uint64_t)x, f.m);
+__device__ __forceinline__ uint32_t fdiv(uint64_t x, const FastDiv& f) {
+  return f.m == 0 ? (uint32_t)x : (uint32_t)__umul64hi(x, f.m);
 }
 __device__ __forceinline__ EntryId entry_id(const DecodeArgs& a, int e) {
   EntryId r;
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto first_sealed = [&](uint32_t x) {
         const uint32_t one = cost_sealed(g.k);
-        return x > off_s ? (int)fdiv(64 * (min(x - off_s, one * g.sealed) + one - 1), by_cost) : 0;
+        return x > off_s ? (int)fdiv(64ull * (min(x - off_s, one * g.sealed) + one - 1), by_cost) : 0;
       };
       const int2 w = make_int2(first_wide(start), first_wide(end));
       const int2 s = make_int2(first_sealed(start), first_sealed(end));

@@ -27,10 +27,10 @@
 // 128-row bf16 tail; the append that fills its last row seals it into a byte
 // block of the Q pool (per-channel K and per-token V scales, absmax / 127 in
 // fp32 and codes x / scale rounded half to even for INT8; absmax / 448 and
-// codes x / scale rounded to the nearest e4m3 value for FP8) and clears the
-// tail.  Prefill
-// seals complete blocks straight from its inputs, so both give the same
-// bytes; with paging the sealed blocks are the pages.
+// codes x / scale rounded to the nearest e4m3 value for FP8; for FP8_BLOCK one
+// such scale for the block's keys and one for its values, lk_block.h) and clears the
+// tail.  Prefill seals complete blocks straight from its inputs, so both give the
+// same bytes; with paging the sealed blocks are the pages.
 #include <cuda_runtime.h>
 
 #include "lk_append.cuh"

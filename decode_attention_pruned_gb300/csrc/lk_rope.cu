@@ -9,7 +9,7 @@
 // rope_turn for far positions.)
 //
 // The bytes bound it: every element is read and written once (8192 tokens of
-// 32 heads, 134 MB: 26.1 us, a plain copy of them 23.9).  A block takes
+// 32 heads, 134 MB: 23.3 us, a plain copy of them 23.9).  A block takes
 // a few tokens, computes each (token, pair)'s cosine and sine once into
 // shared memory, and turns every head of q and k with them, 16 channels to a
 // thread as two 16-byte loads and stores.
@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 template <bool kAxes>
 cudaError_t launch(const RopeArgs& args, int num_sms, cudaStream_t stream) {
   // Four tokens a block once that leaves every SM four blocks (8192 tokens of 32
-  // heads: 26.1 us, one token a block 28.6), else one (2053 tokens of 40 heads: 8.0
-  // us on the GPU, four tokens a block 10.0).
+  // heads: 22.2 us from cold caches, one token a block 23.7), else one (2053 tokens of
+  // 40 heads: 8.8 us, four tokens a block 9.3).
   if (args.tokens >= 16 * (int64_t)num_sms)
     return launch_after(rope_kernel<4, kAxes>, dim3((unsigned)((args.tokens + 3) / 4)), kRopeThreads, 0, stream, args);
   return launch_after(rope_kernel<1, kAxes>, dim3((unsigned)args.tokens), kRopeThreads, 0, stream, args);

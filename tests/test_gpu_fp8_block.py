@@ -122,6 +122,29 @@ def test_sealed_bytes_of_edge_values(cuda, mag):
     case.check_layout(0, N)
 
 
+def test_codes_of_every_significand(cuda):
+    """A block for every significand that its largest value may have, with values of every
+    significand: the codes are those of the correctly rounded quotients, byte for byte."""
+    w = TINY.scaled(batch=8, num_q_heads=2, num_kv_heads=1, context=4 + 64 + 16 * 128)
+    masks = S.masks_with_counts(w, (32,))
+    N = w.context
+    case = Case(w, total=N, masks=masks, kv_format=FMT)
+    rs = np.random.default_rng(11)
+    k, v = (rs.integers(128, 256, (8, N, 1, 128)) * 2.0 ** rs.integers(-18, -7, (8, N, 1, 128)) *
+            rs.choice([-1.0, 1.0], (8, N, 1, 128)) for _ in range(2))
+    for b in range(8):
+        for j in range(16):
+            rows = slice(w.sink + 128 * j, w.sink + 128 * (j + 1))
+            top = (128 + 16 * b + j) * 2.0 ** -7
+            for x in (k, v):
+                x[b, rows] = np.clip(x[b, rows], -top, top)
+                x[b, rows.start + 37, 0] = top
+    case.hist[0] = tuple(torch.from_numpy(x).to(torch.bfloat16).cuda() for x in (k, v))
+    case.prefill(0, N)
+    case.cache.check()
+    case.check_layout(0, N)
+
+
 @pytest.mark.parametrize("paged", [False, True], ids=["flat", "paged"])
 def test_every_way_in_gives_the_same_bytes(cuda, paged):
     """Prefill, chunks and single tokens seal the same blocks; every policy."""
