@@ -250,22 +250,28 @@ def _same_device(device, *tensors):
             raise ValueError(f"a tensor is on {t.device}, the call on {device}")
 
 
-def _spaced(t, shape, bf16, device, what):
-    """_token_stride of a tensor on `device`, [B, n, heads, 128] or [B, heads, 128].
-    What is as it should be is seen at once: a call of one token takes the device 6 us,
-    and the host as long."""
-    try:
-        if t.dtype is bf16 and t.device == device and t.shape == shape:
-            s, dense = t.stride(), shape[-2] * 128
-            n = shape[1] if len(shape) == 4 else 1
-            step = s[1] if n > 1 else s[0] if shape[0] > 1 else dense
-            if s[-1] == 1 and s[-2] == 128 and step >= dense and (n <= 1 or shape[0] <= 1 or s[0] == n * step):
-                return step
-    except AttributeError:
-        pass
-    step = _token_stride(t, shape[-2], shape[:-2], what)
-    _same_device(device, t)
-    return step
+def _token_strides(tensors, bf16, device):
+    """_token_stride of each of (tensor, shape, name), shapes [B, n, heads, 128] or [B,
+    heads, 128], on `device`; 0 for None.  What is as it should be is seen at once: a call
+    of one token takes the device 6 us, and the host as long."""
+    strides = []
+    for t, shape, what in tensors:
+        if t is None:
+            strides.append(0)
+            continue
+        try:
+            if t.dtype is bf16 and t.shape == shape and t.device == device:
+                s, dense = t.stride(), shape[-2] * 128
+                n = shape[1] if len(shape) == 4 else 1
+                step = s[1] if n > 1 else s[0] if shape[0] > 1 else dense
+                if step >= dense and s[-1] == 1 and s[-2] == 128 and (n <= 1 or shape[0] <= 1 or s[0] == n * step):
+                    strides.append(step)
+                    continue
+        except AttributeError:
+            pass
+        strides.append(_token_stride(t, shape[-2], shape[:-2], what))
+        _same_device(device, t)
+    return strides
 
 
 class Rope:
@@ -744,16 +750,15 @@ class Cache:
         return o
 
     # -- with the rotation on the way
-    def _rope_chunk(self, rope, q, k, v, positions, lens, ids):
+    def _rope_chunk(self, torch, rope, q, k, v, positions, lens, ids, q_out):
         """The lk_chunk (as bytes) of tokens to be turned, given as [B, n, heads, 128]
-        or, one of each sequence, [B, heads, 128]; what it points to, q's shape and the
-        device."""
-        import torch
-        B, device, plan, bf16 = self.batch, self.buffer.device, self.plan, torch.bfloat16
+        or, one of each sequence, [B, heads, 128]; the stride of q_out's tokens, lens, and
+        the shape of q."""
+        B, device, plan = self.batch, self.buffer.device, self.plan
         lead = (B, k.shape[1]) if k.ndim == 4 else (B,)
         shape, q_shape = (*lead, plan.num_kv_heads, 128), (*lead, plan.num_q_heads, 128)
-        k_stride, v_stride = _spaced(k, shape, bf16, device, "k"), _spaced(v, shape, bf16, device, "v")
-        q_ptr, q_stride = (0, 0) if q is None else (q.data_ptr(), _spaced(q, q_shape, bf16, device, "q"))
+        k_stride, v_stride, q_stride, out_stride = _token_strides(
+            ((k, shape, "k"), (v, shape, "v"), (q, q_shape, "q"), (q_out, q_shape, "q_out")), torch.bfloat16, device)
         if ids is not None:
             _need(ids, torch.int32, lead, "ids")
             _same_device(device, ids)
@@ -764,10 +769,10 @@ class Cache:
             lens = np.ascontiguousarray(lens, dtype=np.int32)
             if lens.shape != (B,):
                 raise ValueError(f"lens shape {lens.shape}")
-        c = _pack_chunk(q_ptr, k.data_ptr(), v.data_ptr(), 0 if ids is None else ids.data_ptr(),
-                        0 if lens is None else lens.ctypes.data, q_stride, k_stride, v_stride,
-                        lead[1] if len(lead) > 1 else 1, 0)
-        return c, lens, q_shape, device
+        c = _pack_chunk(0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                        0 if ids is None else ids.data_ptr(), 0 if lens is None else lens.ctypes.data, q_stride,
+                        k_stride, v_stride, lead[1] if len(lead) > 1 else 1, 0)
+        return c, out_stride, lens, q_shape
 
     def append_rope(self, layer, rope, k, v, positions=None, q=None, q_out=None, lens=None, ids=None, stream=None):
         """lk_append_rope: k, v [B, n, Hkv, 128] bf16 (tokens evenly spaced), or one
@@ -777,15 +782,13 @@ class Cache:
         turned queries go to q_out, a new dense tensor unless given (q itself may be);
         returns q_out.  Rows past a sequence's length are left as they are."""
         import torch
-        c, lens, shape, device = self._rope_chunk(rope, q, k, v, positions, lens, ids)
-        out, step = None, 0
-        if q is not None:
-            if q_out is None:
-                q_out = _empty(shape, torch.bfloat16, device, stream)
-            out, step = q_out.data_ptr(), _spaced(q_out, shape, torch.bfloat16, device, "q_out")
-        elif q_out is not None:
+        if q is None and q_out is not None:
             raise ValueError("q_out without q")
-        _check(_lib.lk_append_rope(self._h, layer, rope._h, c, _ptr(positions), out, step, _stream(stream)))
+        c, step, lens, shape = self._rope_chunk(torch, rope, q, k, v, positions, lens, ids, q_out)
+        if q is not None and q_out is None:
+            q_out, step = _empty(shape, torch.bfloat16, self.buffer.device, stream), shape[-2] * 128
+        _check(_lib.lk_append_rope(self._h, layer, rope._h, c, None if positions is None else positions.data_ptr(),
+                                   None if q_out is None else q_out.data_ptr(), step, _stream(stream)))
         return q_out
 
     def step_rope(self, layer, rope, q, k, v, positions=None, ids=None, o=None, stream=None):
@@ -794,11 +797,11 @@ class Cache:
         import torch
         if k.ndim != 3:
             raise ValueError(f"k: expected [B, Hkv, 128], got {tuple(k.shape)}")
-        c, _, shape, device = self._rope_chunk(rope, q, k, v, positions, None, ids)
+        c, _, _, shape = self._rope_chunk(torch, rope, q, k, v, positions, None, ids, None)
         if o is None:
-            o = _empty(shape, torch.float32, device, stream)
+            o = _empty(shape, torch.float32, self.buffer.device, stream)
         _need(o, torch.float32, shape, "o")
-        _same_device(device, o)
+        _same_device(self.buffer.device, o)
         _check(_lib.lk_step_rope(self._h, layer, rope._h, c, _ptr(positions), o.data_ptr(),
                                  self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
         return o

@@ -158,9 +158,10 @@ __global__ void __launch_bounds__(kTokenThreads)
         const int g = h0 * cv.G + x - 1;
         const uint16_t* src = x == 0 ? k_in + h0 * kHeadDim : rc.q + b * rc.q_stride + g * kHeadDim;
         uint4 u = *reinterpret_cast<const uint4*>(src + share.c0), v = *reinterpret_cast<const uint4*>(src + share.c1);
-        share.apply(rc.rope,
-                    [&](int axis) { return rc.positions != nullptr ? __ldg(rc.positions + axis * rc.axis_stride + b) : n; },
-                    u, v);
+        auto pos = [&](int axis) {
+          return rc.positions != nullptr ? __ldg(rc.positions + axis * rc.axis_stride + b) : n;
+        };
+        share.apply(rc.rope, pos, u, v);
         uint16_t* dst = x == 0 ? reinterpret_cast<uint16_t*>(s_k) : rc.q_out + b * rc.q_out_stride + g * kHeadDim;
         *reinterpret_cast<uint4*>(dst + share.c0) = u;
         *reinterpret_cast<uint4*>(dst + share.c1) = v;
