@@ -30,8 +30,8 @@ FMT = lkb.KV_FP8_BLOCK
 def _head(case, layer, b, h, N):
     k, v = case.history(layer)
     kept = np.nonzero(case.masks[layer, h])[0]
-    return (*OQ.quantized_history(f64(k[b, :N, h]), f64(v[b, :N, h]), kept, int(case.policies[layer, h]), N, case.w.sink,
-                                  case.w.local, "fp8_block"), kept)
+    return (*OQ.quantized_history(f64(k[b, :N, h]), f64(v[b, :N, h]), kept, int(case.policies[layer, h]), N,
+                                  case.w.sink, case.w.local, "fp8_block"), kept)
 
 
 def _check_decode(case, layer, q, o, held):
@@ -46,8 +46,9 @@ def _check_decode(case, layer, q, o, held):
             ref, A = OA.decode_head(qh, K, V, *args), OA.decode_head(qh, K, np.abs(V), *args)
             D = np.abs(qh) @ np.abs(K).T / np.sqrt(128.0) if N else np.zeros((G, 1))
             tol = 2 * A * (2.0 ** -19 * (1 + D.max(1, keepdims=True)) + 2.0 ** -16)
-            assert np.all(np.abs(got - ref) <= tol), (b, h, N, float((np.abs(got - ref) / np.maximum(tol, 1e-300)).max()))
-            worst = max(worst, float((np.abs(got - ref) / np.maximum(tol, 1e-300)).max()))
+            off = float((np.abs(got - ref) / np.maximum(tol, 1e-300)).max())
+            assert np.all(np.abs(got - ref) <= tol), (b, h, N, off)
+            worst = max(worst, off)
     return worst
 
 
@@ -222,6 +223,23 @@ def test_many_entries(cuda):
     o = case.cache.decode(0, q)
     case.cache.check()
     _check_decode(case, 0, q, o, held)
+
+
+@pytest.mark.parametrize("batch", [2, 11], ids=["heads", "heads and lengths"])
+def test_more_heads_and_lengths_than_shared_memory_keeps(cuda, batch):
+    """All layers in one launch: 56 (layer, head) descriptors and up to 616 lengths, of
+    which places are kept for 48 and 512."""
+    w = TINY.scaled(num_layers=7, batch=batch, num_q_heads=8, num_kv_heads=8, sink=2, local=8)
+    case = Case(w, total=300, masks=S.masks_with_counts(w, np.resize([32, 64, 0, 96, 128], 56)), kv_format=FMT)
+    held = [[(97 * b + 41 * layer) % 300 for b in range(batch)] for layer in range(7)]
+    for layer in range(7):
+        k, v = case.history(layer)
+        case.cache.prefill_ragged(layer, k, v, np.array(held[layer], np.int32))
+    q = torch.stack([case.q(layer, 300) for layer in range(7)]).contiguous()
+    o = case.cache.decode_layers(0, q)
+    case.cache.check()
+    for layer in range(7):
+        _check_decode(case, layer, q[layer], o[layer], held[layer])
 
 
 @pytest.mark.parametrize("shift", [0, 40, -40], ids=["alike", "growing", "shrinking"])
