@@ -149,7 +149,8 @@ def test_codes_of_every_significand(cuda):
 @pytest.mark.parametrize("paged", [False, True], ids=["flat", "paged"])
 def test_every_way_in_gives_the_same_bytes(cuda, paged):
     """Prefill, chunks and single tokens seal the same blocks; every policy."""
-    w = FASTGEN.scaled(num_layers=1, batch=2, context=900, policy_counts=(2, 2, 4), sink=4, local=40, local_only_window=24)
+    w = FASTGEN.scaled(num_layers=1, batch=2, context=900, policy_counts=(2, 2, 4), sink=4, local=40,
+                       local_only_window=24)
     cases = [Case(w, total=700, kv_format=FMT, middle_tokens=1400 if paged else None) for _ in range(3)]
     k, v = cases[0].history(0)
     cases[0].prefill(0, 700)
@@ -379,12 +380,17 @@ def _chunk_case(w, masks, held, n, lens=None, **kw):
     case.cache.prefill_ragged(0, k, v, np.array(held, np.int32), ids)
     at = torch.as_tensor(held, device="cuda")[:, None] + torch.arange(n, device="cuda")
     b = torch.arange(w.batch, device="cuda")[:, None]
-    q = torch.randn(w.batch, n, w.num_q_heads, 128, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
-    o = torch.full((w.batch, n, w.num_q_heads, 128), 3.0, dtype=torch.bfloat16, device="cuda")
-    case.cache.chunk_attn(0, q, k[b, at].contiguous(), v[b, at].contiguous(), lens=lens,
-                          ids=case.ids[b, at].contiguous() if ids is not None else None, o=o)
+    q = torch.randn(w.batch, n, w.num_q_heads, 128, generator=torch.Generator().manual_seed(5))
+    q, k1, v1 = q.to(torch.bfloat16).cuda(), k[b, at].contiguous(), v[b, at].contiguous()
+    id1 = case.ids[b, at].contiguous() if ids is not None else None
+
+    def call():
+        o = torch.full((w.batch, n, w.num_q_heads, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+        return case.cache.chunk_attn(0, q, k1, v1, lens=lens, ids=id1, o=o)
+    o = call()
     case.cache.check()
     _check_chunk(case, q, o, held, [n] * w.batch if lens is None else lens)
+    return case, call, o
 
 
 @pytest.mark.parametrize("G", [1, 4, 7, 8])
@@ -418,6 +424,66 @@ def test_chunks_over_scales_that_differ(cuda, shift):
     o = case.cache.chunk_attn(0, q, k[:, held:].contiguous(), v[:, held:].contiguous())
     case.cache.check()
     _check_chunk(case, q, o, [held], [n])
+
+
+@pytest.mark.parametrize("n", [1, 17, 40])
+def test_chunks_wide_tiles_then_blocks(cuda, n):
+    """Several full-width tiles before those made of blocks, for items that follow one
+    another in a thread block; blocks that come in pages."""
+    w = TINY.scaled(num_kv_heads=4, num_q_heads=32, batch=3, sink=130, local=400)
+    _chunk_case(w, S.masks_with_counts(w, (96, 128, 32, 0)), [2000, 700, 1313], n, middle_tokens=4000)
+
+
+@pytest.mark.parametrize("paged", [False, True], ids=["flat", "paged"])
+@pytest.mark.parametrize("n", [2, 60])
+def test_chunk_waits_that_run_out(cuda, n, paged):
+    """With a limit of 0, and with ones that run out on the way, a call ends and leaves
+    nothing behind: the next one, with no synchronisation between, is as before."""
+    w = TINY.scaled(num_kv_heads=4, num_q_heads=16, batch=2, sink=4, local=30)
+    masks = S.masks_with_counts(w, (32, 96, 0, 128))
+    case, call, want = _chunk_case(w, masks, [1300, 801], n, **(dict(middle_tokens=2400) if paged else {}))
+    case.cache.set_wait_limit(0)
+    call()
+    with pytest.raises(lkb.LeankError) as e:
+        case.cache.check()
+    assert e.value.status == lkb.LK_ERR_TIMEOUT
+    case.cache.check()
+    for limit in (0, 1, 300, 1000, 3000, 10000) * 2:
+        outs = []
+        for _ in range(3):
+            case.cache.set_wait_limit(limit)
+            call()
+            case.cache.set_wait_limit(10 ** 9)
+            outs.append(call())
+        for o in outs:
+            assert torch.equal(o, want), limit
+        try:
+            case.cache.check()
+        except lkb.LeankError as e:
+            assert e.status == lkb.LK_ERR_TIMEOUT
+    assert torch.equal(call(), want)
+    case.cache.check()
+
+
+def test_calls_overlap_on_two_streams(cuda):
+    """Decodes and chunks over one cache, each with its own workspace, at once."""
+    w = TINY.scaled(num_kv_heads=4, num_q_heads=16, batch=2, sink=4, local=30)
+    case, call, want = _chunk_case(w, S.masks_with_counts(w, (32, 96, 64, 128)), [1300, 801], 9)
+    q = case.q(0, 1300)
+    first = case.cache.decode(0, q).clone()
+    other = torch.zeros_like(case.cache.workspace)
+    lib, s = lkb.load(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs, chunks = [torch.empty_like(first) for _ in range(20)], []
+    for o in outs:
+        st = lib.lk_decode_attn(case.cache._h, 0, q.data_ptr(), o.data_ptr(), other.data_ptr(), other.numel(),
+                                s.cuda_stream)
+        assert st == lkb.LK_OK
+        chunks.append(call())
+        assert torch.equal(case.cache.decode(0, q), first)
+    torch.cuda.synchronize()
+    case.cache.check()
+    assert all(torch.equal(o, first) for o in outs) and all(torch.equal(o, want) for o in chunks)
 
 
 def test_prompt_steps_and_verification_together(cuda):
