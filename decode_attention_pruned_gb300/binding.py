@@ -251,8 +251,8 @@ def _same_device(device, *tensors):
 
 
 def _token_strides(tensors, bf16, device):
-    """_token_stride of each of (tensor, shape, name), shapes [B, n, heads, 128] or [B,
-    heads, 128], on `device`; 0 for None.  What is as it should be is seen at once: a call
+    """_token_stride of each of (tensor, shape, name) on `device`; 0 for None.  What is as
+    it should be, of shape [B, n, heads, 128] or [n, heads, 128], is seen at once: a call
     of one token takes the device 6 us, and the host as long."""
     strides = []
     for t, shape, what in tensors:
@@ -260,7 +260,7 @@ def _token_strides(tensors, bf16, device):
             strides.append(0)
             continue
         try:
-            if t.dtype is bf16 and t.shape == shape and t.device == device:
+            if t.dtype is bf16 and t.shape == shape and t.device == device and 3 <= len(shape) <= 4:
                 s, dense = t.stride(), shape[-2] * 128
                 n = shape[1] if len(shape) == 4 else 1
                 step = s[1] if n > 1 else s[0] if shape[0] > 1 else dense
@@ -312,26 +312,25 @@ class Rope:
         tokens = 1
         for n in lead:
             tokens *= n
+        if (q is None and q_out is not None) or (k is None and k_out is not None):
+            raise ValueError("q_out without q" if q is None else "k_out without k")
         _need(positions, torch.int32, self.axes + lead, "positions")
-        args, outs = [], []
-        for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
-            if x is None:
-                if y is not None:
-                    raise ValueError(f"{what}_out without {what}")
-                args.append((None, 0, 0, None, 0))
-                outs.append(None)
-                continue
-            heads = x.shape[-2]
-            step = _token_stride(x, heads, lead, what)
-            if y is None:
-                y = _empty((*lead, heads, 128), torch.bfloat16, x.device, stream)
-            args.append((x.data_ptr(), step, heads, y.data_ptr(), _token_stride(y, heads, lead, what + "_out")))
-            outs.append(y)
-        _same_device(torch.device("cuda", torch.cuda.current_device()), positions, q, k, *outs)
-        (qp, qs, hq, qo, qos), (kp, ks, hk, ko, kos) = args
-        _check(_lib.lk_rope_apply(self._h, qp, qs, kp, ks, positions.data_ptr(), tokens, hq, hk, qo, qos, ko, kos,
-                                  _stream(stream)))
-        return tuple(outs)
+        bf16, here = torch.bfloat16, torch.device("cuda", torch.cuda.current_device())
+        q_heads, k_heads = 0 if q is None else q.shape[-2], 0 if k is None else k.shape[-2]
+        q_shape, k_shape = (*lead, q_heads, 128), (*lead, k_heads, 128)
+        qs, ks, qos, kos = _token_strides(((q, q_shape, "q"), (k, k_shape, "k"), (q_out, q_shape, "q_out"),
+                                           (k_out, k_shape, "k_out")), bf16, here)
+        if positions.device != here:
+            _same_device(here, positions)
+        if q is not None and q_out is None:
+            q_out, qos = _empty(q_shape, bf16, here, stream), q_heads * 128
+        if k is not None and k_out is None:
+            k_out, kos = _empty(k_shape, bf16, here, stream), k_heads * 128
+        qp, qop = (None, None) if q is None else (q.data_ptr(), q_out.data_ptr())
+        kp, kop = (None, None) if k is None else (k.data_ptr(), k_out.data_ptr())
+        _check(_lib.lk_rope_apply(self._h, qp, qs, kp, ks, positions.data_ptr(), tokens, q_heads, k_heads, qop, qos,
+                                  kop, kos, _stream(stream)))
+        return q_out, k_out
 
     def __del__(self):
         if getattr(self, "_h", None) and _lib is not None:
