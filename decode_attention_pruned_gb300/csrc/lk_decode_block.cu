@@ -36,7 +36,7 @@
 // caches): the bytes.  64 x 4096 tokens take 60 us (309 MB: 5.1 TB/s), 4 x 131072 61 us
 // (315 MB), with the copies alone and no arithmetic 55 and 53 us; 1 x 32768 18 us (45
 // MB), 14 us with the copies alone, 3 us of them before the first copy (the lengths, the
-// line, the code's own way from memory); short calls 13 us, which are those, one load
+// line, the place of the first piece); short calls 13 us, which are those, one load
 // after another, and the merges.
 //   What went before: each lane copying its own words ahead with cp.async spent 400
 // instructions on a slab, most of them on copies and their bookkeeping (64 x 4096: 91 us).
