@@ -102,8 +102,9 @@ struct Smem {
   // the barriers: stages landed and used, the consumers' own
   static constexpr int kFull = kLens + kLensKept * 8, kEmpty = kFull + 8 * kSlots, kMeet = kEmpty + 8 * kSlots;
   static constexpr int kScan = kMeet + 8;
-  static constexpr int kInfo = kScan + (kWarps + 1) * 8;           // what threads tell each other
-  static constexpr int kBytes = kInfo + 32;
+  static constexpr int kBegin = (kScan + (kWarps + 1) * 4 + 15) / 16 * 16;         // what threads tell each other
+  static constexpr int kInfo = kBegin + 48;
+  static constexpr int kBytes = kInfo + 16;
   static constexpr int kAll = kBytes + 1024;                       // to align the ring
   static_assert(kQ % 16 == 0 && kStage % 16 == 0 && kHeadDescs % 8 == 0 && kFull % 8 == 0, "alignment");
   static_assert(kAll <= 227 * 1024, "shared memory per block");
@@ -224,11 +225,17 @@ __device__ __forceinline__ Entry entry_geometry(const CacheView& cv, const HeadD
 }
 
 struct Info {
-  uint32_t first_off;          // line offset of the entry the range starts in
-  int32_t first_entry;
   int32_t last;                // this CTA is the entry's last
   int32_t gone;                // set once some wait ran out
 };
+// The entry that the range starts in, from the thread that found it.
+struct alignas(16) First {
+  EntryId id;
+  int32_t entry;
+  uint32_t off;                // its line offset
+  Entry g;
+};
+static_assert(sizeof(First) == 48, "three words");
 
 // The rest of a wait whose phase was not complete at once.
 __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit, volatile int* gone,
@@ -276,7 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t full = base + L::kFull, empty = base + L::kEmpty;
   uint32_t* scan = reinterpret_cast<uint32_t*>(sm + L::kScan);
   volatile Info& info = *reinterpret_cast<volatile Info*>(sm + L::kInfo);
-  static_assert(sizeof(Info) <= 32, "Info");
   if (tid < kSlots) {
     mbar_init(full + 8 * tid, 1);
     mbar_init(empty + 8 * tid, kWarps);
@@ -288,10 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = tid; i < 2 * 3 * L::kQBytes / 16; i += kThreads)
     reinterpret_cast<uint4*>(sm + L::kQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid < 2 * kMaxGroup) reinterpret_cast<float*>(sm + L::kBack)[tid] = 0.f;
-  if (tid == 0) {
-    info.first_entry = E;
-    info.gone = 0;
-  }
+  if (tid == 0) info.gone = 0;
   if (warp == kWarps && lane < kNumPools) tma_prefetch_map(&maps.pool[lane]);
   // The head table never changes: where it has room, it is here before the kernel ahead
   // of this one is done.
@@ -349,10 +352,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t at = excl;
     for (int e = e_lo; e < e_hi; ++e) {
       const EntryId id = entry_id(a, e);
-      const uint32_t c = entry_cost(entry_geometry(cv, heads[id.lr * cv.Hkv + id.h], lens_of(e, id)));
+      const Entry g = entry_geometry(cv, heads[id.lr * cv.Hkv + id.h], lens_of(e, id));
+      const uint32_t c = entry_cost(g);
       if (at + c > start) {
-        info.first_entry = e;
-        info.first_off = at;
+        const First f{id, e, at, g};
+        const int4* from = reinterpret_cast<const int4*>(&f);
+        int4* to = reinterpret_cast<int4*>(sm + L::kBegin);
+        to[0] = from[0];
+        to[1] = from[1];
+        to[2] = from[2];
         break;
       }
       at += c;
@@ -360,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   if (start >= end) return;
+  const First first = *reinterpret_cast<const First*>(sm + L::kBegin);
   const Wait wait{a.wait_limit_ns, &info.gone, cv.hdr};
 
   if (warp == kWarps) {
@@ -397,14 +406,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       next += bytes;
       return true;
     };
-    uint32_t off = info.first_off;
-    const int e0 = info.first_entry;
-    EntryId id = entry_id(a, e0);
-    Lens len = lens_of(e0, id);
+    uint32_t off = first.off;
+    const int e0 = first.entry;
+    EntryId id = first.id;
+    Entry g = first.g;
+    Lens len{0, 0};
     for (int e = e0; ok && e < E && off < end; ++e) {
       const EntryId now = id;
       const HeadDesc& hd = heads[now.lr * cv.Hkv + now.h];
-      const Entry g = entry_geometry(cv, hd, len);
+      if (e != e0) g = entry_geometry(cv, hd, len);
       const uint32_t off_s = off + kCostWide * g.wide, off_o = off_s + cost_sealed(g.k) * g.sealed;
       // pieces of each kind that start inside the range
       const FastDiv& by_cost = a.div_cost_b[g.k >> 5];                 // by 2 (k + 128), 64 times a block's cost
@@ -589,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   {
     // (the range may start behind the last piece of the entry it starts in)
-    int e = info.first_entry;
-    if (last_piece(geometry_of(e), info.first_off) < start) e = next_entry(e);
+    int e = first.entry;
+    if (last_piece(first.g, first.off) < start) e = next_entry(e);
     if (e < E) ask_q(e);
     lay_q(0);
   }
