@@ -9,11 +9,15 @@
 // take the scale's exponent, p times f is split into f16 hi + lo (two products, 22
 // bits), and l takes p times 2^-j.  Rows in bf16 (sinks, window, LOCAL and SPECIAL
 // rows, the open block) are scored on bf16 products, p as three bf16 numbers.
-// f16's range: m follows the largest s + j - 12, so that the largest weight lies in
-// [2^12, 2^15) and weights down to 2^-15 of it keep all their bits.  Until a segment
-// meets its first sealed block, m follows the scores alone; there it moves by that
-// block's j - 12, and the bf16 rows after it count by the same (bf16 has the range of
-// fp32: their weights may be far from 1).
+// f16's range: over blocks m follows the largest s + j - 12, so that the largest weight
+// lies in [2^12, 2^15), and a weight is off by at most 2^-37 of it (weights down to 2^-15
+// of it keep all their bits).  Rows in bf16 need no such care: there m is the largest s, and at
+// their segment's first sealed block it falls to what that block asks for, so that rows
+// that score far above every block, as sinks do, cost the blocks' weights nothing.  (Had m
+// stayed where the rows left it, sinks 2^28 above the blocks and without a value would leave o
+// off by 1.7e-4 of sum p |v|.)  It falls by 24 (values of normal size ask for 19) without a
+// look at the sums so far, and further only as leaves them below 2^100: so values
+// up to 2^80 keep inside fp32's range beside blocks of next to no values.
 //
 // Tensor cores: m16n8k16 with 16 tokens (a slab) on M for S^T = K q^T, 16 channels on
 // M for O^T += V^T P^T, and the G <= 8 query heads on N.  Channels and tokens are
@@ -68,6 +72,8 @@ constexpr float kRescaleGap = 2.f;             // log2: m moves when what it fol
 constexpr int kFlush = 8;                      // stages whose products share accumulators
 constexpr int kWeightExp = 12;                 // log2 of the largest sealed weight when m moves
 constexpr uint32_t kMinCtaCost = 16;           // line a CTA takes at least: 64 KB, what the largest piece takes
+constexpr float kFreeFall = 24.f;              // log2: m falls by as much without a look at the sums
+constexpr int kTopExp = 100;                   // log2 of what sums may reach when m falls
 constexpr int kRowTop = 14;                    // a row of q is moved so that its largest channel lies in [2^14, 2^15)
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the producer's wait for its copies at the end
 constexpr int kHeadsKept = 48, kLensKept = 512;            // descriptors and lengths that shared memory has places for
@@ -609,11 +615,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The products' accumulators drop what lies below their last bit at every product,
   // always towards zero; so they take a few stages', and their sums meet by fp32
   // additions in the warp's merge slot.  (All of a segment in one accumulator: o of
-  // 131072 tokens is off by 1.1e-6.)
+  // 131072 tokens is off by 1.1e-6.)  o and l count in units of 2^m, the slot and its share
+  // of l in units of 2^mm.
   float o[8][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-  bool flushed = false;                                    // the slot holds a sum
+  float mm0 = -INFINITY, mm1 = -INFINITY, ll0 = 0.f, ll1 = 0.f;
+  bool held = false, flushed = false;                      // o holds sums, the slot does
   float* slot_o = merge_o + (warp * kHeads + 2 * tig) * kHeadDim + 8 * gid;
   auto flush = [&]() {
+    if (!held) return;
+    float f0 = 1.f, f1 = 1.f, g0 = 0.f, g1 = 0.f;
+    if (flushed) {
+      const float n0 = fmaxf(mm0, m0), n1 = fmaxf(mm1, m1);
+      f0 = m0 == n0 ? 1.f : ex2(m0 - n0);
+      f1 = m1 == n1 ? 1.f : ex2(m1 - n1);
+      g0 = mm0 == n0 ? 1.f : ex2(mm0 - n0);
+      g1 = mm1 == n1 ? 1.f : ex2(mm1 - n1);
+      ll0 = fmaf(l0, f0, ll0 * g0);
+      ll1 = fmaf(l1, f1, ll1 * g1);
+      mm0 = n0;
+      mm1 = n1;
+    } else {
+      ll0 = l0;
+      ll1 = l1;
+      mm0 = m0;
+      mm1 = m1;
+    }
     if (kPack) {
       // the lo halves' columns, two lanes on
 #pragma unroll
@@ -624,48 +650,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!kPack || tig < 2) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        const float f = j & 1 ? f1 : f0, g = j & 1 ? g1 : g0;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
           float4* to = reinterpret_cast<float4*>(slot_o + (j & 1) * kHeadDim + 64 * (j >> 1) + i);
           float4 v = make_float4(o[i][j], o[i + 1][j], o[i + 2][j], o[i + 3][j]);
           if (flushed) {
             const float4 w = *to;
-            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            v = make_float4(fmaf(v.x, f, w.x * g), fmaf(v.y, f, w.y * g), fmaf(v.z, f, w.z * g), fmaf(v.w, f, w.w * g));
           }
           *to = v;
         }
       }
     }
     flushed = true;
+    held = false;
+    l0 = l1 = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   };
-  // what has been summed so far, times f0 and f1 (of this lane's columns)
-  auto rescale = [&](float f0, float f1) {
-    l0 *= f0;
-    l1 *= f1;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      o[i][0] *= f0;
-      o[i][1] *= f1;
-      o[i][2] *= f0;
-      o[i][3] *= f1;
-    }
-    if (flushed && (!kPack || tig < 2)) {
-#pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-        const float f = j & 1 ? f1 : f0;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          float4* to = reinterpret_cast<float4*>(slot_o + (j & 1) * kHeadDim + 64 * (j >> 1) + i);
-          const float4 w = *to;
-          *to = make_float4(w.x * f, w.y * f, w.z * f, w.w * f);
-        }
-      }
-    }
-  };
-  float shift = 0.f;                                       // of m, since the segment's first sealed block
-  bool moved = false;
+  bool moved = false, fall = false;                        // the segment has met a sealed block; m is about to fall
   const int my_q = kPack ? gid & 3 : gid;                  // the product's column of q
   const int c0 = kPack ? (2 * tig) & 3 : 2 * tig;          // head of this lane's first column
 
@@ -683,18 +687,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     t0 += off;
     t1 += off;
-    if (__any_sync(0xffffffffu, t0 > m0 + kRescaleGap || t1 > m1 + kRescaleGap)) {
+    if (__any_sync(0xffffffffu, t0 > m0 + kRescaleGap || t1 > m1 + kRescaleGap) || fall) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
       }
-      const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+      float n0 = fall ? t0 : fmaxf(m0, t0), n1 = fall ? t1 : fmaxf(m1, t1);
+      if (fall && __any_sync(0xffffffffu, m0 - n0 > kFreeFall || m1 - n1 > kFreeFall)) {
+        // (as far as leaves the sums so far below 2^kTopExp)
+        uint32_t top = max(__float_as_uint(l0), __float_as_uint(l1));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(o[i][j]) & 0x7fffffffu);
+        const int room = kTopExp + 127 - (int)(__reduce_max_sync(0xffffffffu, top) >> 23);
+        n0 = fmaxf(n0, m0 - (float)min(max(room, 0), kTopExp));
+        n1 = fmaxf(n1, m1 - (float)min(max(room, 0), kTopExp));
+      }
+      fall = false;
       const float f0 = m0 == n0 ? 1.f : ex2(m0 - n0), f1 = m1 == n1 ? 1.f : ex2(m1 - n1);
       m0 = n0;
       m1 = n1;
-      rescale(f0, f1);
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i][0] *= f0;
+        o[i][1] *= f1;
+        o[i][2] *= f0;
+        o[i][3] *= f1;
+      }
     }
+    held = true;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       p[n][0] = ex2(x[n][0] - m0);
@@ -741,14 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       x[n][1] = fmaf(s0[n][1] + s1[n][1], b1, bias);
       x[n][2] = fmaf(s0[n][2] + s1[n][2], b0, bias);
       x[n][3] = fmaf(s0[n][3] + s1[n][3], b1, bias);
-      if (n == 0 && !moved) {
-        moved = true;
-        shift = bias - kWeightExp;
-        const float up = power2(kWeightExp - exponent);
-        m0 += shift;
-        m1 += shift;
-        rescale(up, up);
-      }
+      if (n == 0 && !moved) moved = fall = true;
     }
     softmax(slabs, x, p, -(float)kWeightExp);
     uint32_t pt[kN][4];
@@ -833,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[0][i] = (i < 2 ? va : vb) ? (s0[i] + s1[i]) * a.scale_log2 : -INFINITY;
     float p[1][4];
-    softmax(std::integral_constant<int, 1>(), x, p, shift);
+    softmax(std::integral_constant<int, 1>(), x, p, 0.f);
     // P as the sum of three bf16 numbers (2^-24 of it is left; of two 2^-16, with the
     // two columns of one product 2.5e-6 of o instead of 4e-7)
     auto split = [](float a, float b, uint32_t (&t)[3]) {
@@ -920,17 +938,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- end of a segment: the warps' (o, m, l) meet in shared memory
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      ll0 += __shfl_xor_sync(0xffffffffu, ll0, d);
+      ll1 += __shfl_xor_sync(0xffffffffu, ll1, d);
     }
     if (gid == 0 && (!kPack || tig < 2)) {
-      merge_m[warp * kHeads + 2 * tig] = m0;
-      merge_m[warp * kHeads + 2 * tig + 1] = m1;
-      merge_l[warp * kHeads + 2 * tig] = l0;
-      merge_l[warp * kHeads + 2 * tig + 1] = l1;
+      merge_m[warp * kHeads + 2 * tig] = mm0;
+      merge_m[warp * kHeads + 2 * tig + 1] = mm1;
+      merge_l[warp * kHeads + 2 * tig] = ll0;
+      merge_l[warp * kHeads + 2 * tig + 1] = ll1;
     }
-    m0 = m1 = -INFINITY;
-    l0 = l1 = shift = 0.f;
+    m0 = m1 = mm0 = mm1 = -INFINITY;
+    ll0 = ll1 = 0.f;
     moved = flushed = false;
     stage = (uint32_t)-1;                                  // (the next one is a segment's first)
     buffer ^= 1;

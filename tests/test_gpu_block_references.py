@@ -1,0 +1,142 @@
+"""Weights over sealed blocks with a reference of their own, and sums that meet in
+shared memory: decode over KV_FP8_BLOCK caches where full-width rows and blocks, or one block and the next, differ by far more
+than f16's range, and segments long enough that sums are flushed several times.
+
+Bounds of decode (fp32 out; A = sum p |v|).  Keys are multiples of 1/4 up to 7/4 and
+queries of +-1 (their codes times +-1 in blocks), so a score's products and sums are exact in
+fp32.  Then in units of 2^-24, y a score in log2 units and j
+a block's value exponent: the factor of y is rounded twice, y + j once, m and the difference
+once each: 3 |y| + 3 |y + j| + 64 <= 3 * 40 + 3 * 80 + 64 < 430 in the cases below, 2.6e-5 ln 2
+= 1.8e-5 of a weight.  Exponentials, three rescalings' among them, are off by 2^-22 each,
+1e-6; the sums by less than 64 roundings, 3.9e-6; P by 2^-22.  Together a weight is off by less
+than 2^-15.4, and a normalised one by twice that: 2^-14 A."""
+import numpy as np
+import pytest
+import torch
+
+from decode_attention_pruned_gb300 import binding as lkb
+from decode_attention_pruned_gb300 import synth as S
+from helpers import Case, f64
+from oracle import attention as OA
+from oracle import quant as OQ
+
+pytestmark = pytest.mark.gpu
+
+TINY = S.WORKLOADS[0]
+FMT = lkb.KV_FP8_BLOCK
+COMMON = 64                                        # channels on which the queries agree
+SINK, LOCAL = 4, 32
+
+
+def _case(G, N, counts=(32, 128), fmt=FMT, batch=1):
+    """Keys that are 0 on the common channels and small multiples of 1/4 on the others, the
+    kept ones among them; each block has a key of 7/4."""
+    H = len(counts)
+    w = TINY.scaled(num_q_heads=H * G, num_kv_heads=H, sink=SINK, local=LOCAL, batch=batch)
+    masks = np.zeros((1, H, 128), np.uint8)
+    for h, c in enumerate(counts):
+        masks[0, h, 128 - c:] = 1
+    case = Case(w, total=N, masks=masks, kv_format=fmt)
+    rs = np.random.default_rng(3)
+    k = rs.choice([-1.0, -0.5, -0.25, 0.0, 0.25, 0.5, 1.0, 1.75], (1, N, H, 128))
+    k[..., :COMMON] = 0
+    k[:, SINK::128, :, -1] = 1.75
+    v = rs.standard_normal((1, N, H, 128))
+    return case, k, v
+
+
+def _queries(case, shape=()):
+    """+-1; on the common channels +1."""
+    q = torch.from_numpy(np.random.default_rng(9).choice([-1.0, 1.0], (1, *shape, case.w.num_q_heads, 128)))
+    q[..., :COMMON] = 1
+    return q.to(torch.bfloat16).cuda()
+
+
+def _history(case, k, v):
+    case.hist[0] = tuple(torch.from_numpy(x).to(torch.bfloat16).cuda() for x in (k, v))
+    for x, y in zip(case.hist[0], (k, v)):
+        assert bool(x.isfinite().all()), y
+    return case.hist[0]
+
+
+def _expected(case, q, N, held):
+    """(o, A) of queries [Hq, 128] that see N tokens, of which blocks were sealed when `held` were there."""
+    w, G, o, A = case.w, case.w.group, [], []
+    k, v = case.history(0)
+    for h in range(w.num_kv_heads):
+        kept = np.nonzero(case.masks[0, h])[0]
+        K, V = f64(k[0, :N, h]), f64(v[0, :N, h])
+        K[:held], V[:held] = OQ.quantized_history(K, V, kept, 0, held, w.sink, w.local,
+                                                  lkb.KV_FORMAT_NAMES[case.kv_format])
+        args = (0, kept, N, w.sink, w.local, 0, case.flags[0])
+        o.append(OA.decode_head(f64(q[h * G:(h + 1) * G]), K, V, *args))
+        A.append(OA.decode_head(f64(q[h * G:(h + 1) * G]), K, np.abs(V), *args))
+    return np.concatenate(o), np.concatenate(A)
+
+
+def _check(got, o, A, tol):
+    off = np.abs(f64(got) - o)
+    assert np.all(off <= tol), (float((off / np.maximum(A, 1e-300)).max()), float((off / np.maximum(tol, 1e-300)).max()))
+
+
+def _decode(case, N, ctas=0):
+    case.prefill(0, N)
+    case.cache.set_decode_ctas(ctas)
+    q = _queries(case)
+    got = case.cache.decode(0, q)
+    case.cache.check()
+    o, A = _expected(case, q[0], N, N)
+    _check(got[0], o, A, 2.0 ** -14 * A)
+
+
+@pytest.mark.parametrize("ctas", [1, 0])
+@pytest.mark.parametrize("gap", [0, 16, 24, 28, 32])
+@pytest.mark.parametrize("G", [4, 7])
+def test_rows_that_score_far_above_the_blocks(cuda, G, gap, ctas):
+    """Sinks that take nearly all of the softmax and have no value: o is what the middle
+    and the window give, however small their weights."""
+    N = SINK + LOCAL + 128 * 6 + 50
+    case, k, v = _case(G, N)
+    k[:, :SINK, :, :COMMON] = gap / 8                  # 8.16 log2 units for each
+    v[:, :SINK] = 0
+    v[:, -LOCAL:] /= 256                               # (so that the middle is most of o)
+    _history(case, k, v)
+    _decode(case, N, ctas)
+
+
+@pytest.mark.parametrize("gap", [20, 30])
+@pytest.mark.parametrize("G", [4, 7])
+def test_a_first_block_of_far_larger_values(cuda, G, gap):
+    """The oldest block's values are 2^gap times the others', and its scores as far below
+    them, beside rows that score as the others do."""
+    N = SINK + LOCAL + 128 * 6 + 50
+    case, k, v = _case(G, N, counts=(128, 128))
+    k[:, SINK:SINK + 128, :, :COMMON] = -gap / 8
+    v[:, SINK:SINK + 128] *= 2.0 ** gap
+    _history(case, k, v)
+    _decode(case, N)
+
+
+@pytest.mark.parametrize("G", [4, 7])
+def test_a_first_block_of_zeros_and_rows_of_huge_values(cuda, G):
+    """What rows before it gave stays inside fp32's range."""
+    N = SINK + LOCAL + 128 * 3 + 50
+    case, k, v = _case(G, N)
+    v[:, SINK:SINK + 128] = 0
+    v[:, :SINK] *= 2.0 ** 90
+    v[:, -LOCAL:] *= 2.0 ** 90
+    _history(case, k, v)
+    _decode(case, N)
+
+
+@pytest.mark.parametrize("values", [0, 30, -30])
+@pytest.mark.parametrize("G", [4, 7])
+def test_maxima_that_move_after_sums_were_flushed(cuda, G, values):
+    """One thread block, 48 blocks of a head: keys that score more and more, by 31 log2
+    units in steps, and values whose size changes by 2^values on the way."""
+    N = SINK + LOCAL + 128 * 48 + 70
+    case, k, v = _case(G, N, counts=(128, 128))
+    k[..., :COMMON] = np.floor(np.linspace(0, 31, N))[None, :, None, None] / 8
+    v *= 2.0 ** np.round(np.linspace(0, values, N))[None, :, None, None]
+    _history(case, k, v)
+    _decode(case, N, ctas=1)
