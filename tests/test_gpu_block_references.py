@@ -1,15 +1,15 @@
 """Weights over sealed blocks with a reference of their own, and sums that meet in
-shared memory: decode over KV_FP8_BLOCK caches where full-width rows and blocks, or one block and the next, differ by far more
-than f16's range, and segments long enough that sums are flushed several times.
+shared memory: decode over KV_FP8_BLOCK caches where full-width rows and blocks, or one block and
+the next, differ by far more than f16's range, and segments long enough that sums are flushed several times.
 
 Bounds of decode (fp32 out; A = sum p |v|).  Keys are multiples of 1/4 up to 7/4 and
-queries of +-1 (their codes times +-1 in blocks), so a score's products and sums are exact in
-fp32.  Then in units of 2^-24, y a score in log2 units and j
-a block's value exponent: the factor of y is rounded twice, y + j once, m and the difference
-once each: 3 |y| + 3 |y + j| + 64 <= 3 * 40 + 3 * 80 + 64 < 430 in the cases below, 2.6e-5 ln 2
-= 1.8e-5 of a weight.  Exponentials, three rescalings' among them, are off by 2^-22 each,
-1e-6; the sums by less than 64 roundings, 3.9e-6; P by 2^-22.  Together a weight is off by less
-than 2^-15.4, and a normalised one by twice that: 2^-14 A."""
+queries of +-1 (their codes times +-1 in blocks), so a score's products and sums are exact
+in fp32.  Then in units of 2^-24, y a score in log2 units and j a block's value exponent:
+the factor of y is rounded twice, y + j once, m and the difference once each: 3 |y| +
+3 |y + j| + 64 <= 3 * 40 + 3 * 80 + 64 < 430 in the cases below, 2.6e-5 ln 2 = 1.8e-5 of a
+weight.  Exponentials, three rescalings' among them, are off by 2^-22 each, 1e-6; the sums
+by less than 64 roundings, 3.9e-6; P by 2^-22.  Together a weight is off by less than
+2^-15.4, and a normalised one by twice that: 2^-14 A."""
 import numpy as np
 import pytest
 import torch
@@ -25,6 +25,7 @@ pytestmark = pytest.mark.gpu
 TINY = S.WORKLOADS[0]
 FMT = lkb.KV_FP8_BLOCK
 COMMON = 64                                        # channels on which the queries agree
+LOG2 = 1.4426950408889634 / 128 ** 0.5             # of a score, per q.k
 SINK, LOCAL = 4, 32
 
 
@@ -140,3 +141,77 @@ def test_maxima_that_move_after_sums_were_flushed(cuda, G, values):
     v *= 2.0 ** np.round(np.linspace(0, values, N))[None, :, None, None]
     _history(case, k, v)
     _decode(case, N, ctas=1)
+
+
+def test_weights_over_rows_keep_24_bits(cuda):
+    """100 rows of one value, one of each 16 (a warp's) of weight 1 and the others of the same
+    weight p: o is that value whatever p is, but for what P's three bf16 numbers and some 30
+    roundings leave, 30 * 2^-24.  Two bf16 numbers would leave out up to 2^-17 of p, in 93 of
+    the 100 rows: the key is one for which they leave most."""
+    bf = lambda x: float(torch.tensor(x, dtype=torch.float64).to(torch.bfloat16))  # noqa: E731
+    tol = 30 * 2.0 ** -24
+
+    def left(key):
+        p = 2.0 ** (-key * LOG2)
+        hi = bf(p)
+        return abs(p - hi - bf(p - hi)) / p
+    key = max((x / 16 for x in range(16, 256)), key=left)
+    p = 2.0 ** (-key * LOG2)
+    assert left(key) * 93 * p / (7 + 93 * p) > 2 * tol
+    for G in (4, 7):
+        w = TINY.scaled(num_q_heads=G, num_kv_heads=1, sink=4, local=200)
+        case = Case(w, total=100, masks=S.masks_with_counts(w, (32,)), kv_format=FMT)
+        k, v = np.zeros((1, 100, 1, 128)), np.full((1, 100, 1, 128), 1.25)
+        k[..., 0] = -key
+        k[:, ::16, :, 0] = 0
+        _history(case, k, v)
+        case.prefill(0, 100)
+        q = torch.zeros(1, G, 128, dtype=torch.bfloat16, device="cuda")
+        q[..., 0] = 1
+        o = f64(case.cache.decode(0, q))
+        case.cache.check()
+        assert np.abs(o / 1.25 - 1).max() <= tol, (G, np.abs(o / 1.25 - 1).max())
+
+
+@pytest.mark.parametrize("G", [4, 7])
+def test_long_sums_are_as_exact_as_short_ones(cuda, G):
+    """131,072 tokens of one value through one thread block, with scores that rise by 36 log2 units:
+    o is that value.  The products' accumulators drop bits towards zero, up to 2^-23 of what
+    they hold with each product; they take 8 stages of 3 blocks (twice, with G > 4), half of
+    that on average: 24.5 * 2^-23.  A warp adds 64 such sums, and l's, 32 roundings each on average
+    where their sizes are alike: 64 * 2^-24; its 24 weights of a stage to l: 12 * 2^-24; merges and
+    the rest 30 * 2^-24.  In one accumulator the 2000 products would drop some 2^-14."""
+    N, V = 131072, 1.75
+    w = TINY.scaled(num_q_heads=G, num_kv_heads=1, sink=4, local=64)
+    case = Case(w, total=N, masks=S.masks_with_counts(w, (32,)), kv_format=FMT)
+    kept = int(np.nonzero(case.masks[0, 0])[0][0])
+    k = torch.zeros(1, N, 1, 128, dtype=torch.bfloat16, device="cuda")
+    k[0, :, 0, kept] = (torch.arange(N, device="cuda") * 9 // N).to(torch.bfloat16) * 32
+    case.hist[0] = (k, torch.full_like(k, V))
+    case.prefill(0, N)
+    case.cache.set_decode_ctas(1)
+    q = torch.zeros(1, G, 128, dtype=torch.bfloat16, device="cuda")
+    q[..., kept] = 1
+    for sharp in (0.0, 2.0 ** -6, 1.0):                # flat, a little, all
+        o = f64(case.cache.decode(0, q * sharp))
+        case.cache.check()
+        off = np.abs(o / V - 1).max()
+        assert off <= 24.5 * 2.0 ** -23 + 106 * 2.0 ** -24, (sharp, off)
+
+
+def test_a_stream_of_its_own(cuda):
+    """A decode on a stream that the current one does not wait for, and its output read
+    once it is done."""
+    N = 1500
+    case, k, v = _case(4, N)
+    _history(case, k, v)
+    case.prefill(0, N)
+    q = _queries(case)
+    want = case.cache.decode(0, q).clone()
+    s, o = torch.cuda.Stream(), torch.full_like(want, 3.0)
+    s.wait_stream(torch.cuda.current_stream())
+    case.cache.decode(0, q, o, stream=s)
+    new = case.cache.decode(0, q, stream=s)
+    s.synchronize()
+    assert torch.equal(o, want) and torch.equal(new, want)
+    case.cache.check()
