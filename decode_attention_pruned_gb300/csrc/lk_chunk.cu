@@ -658,8 +658,16 @@ constexpr int kScaleExp = 6, kRowTop = 14;
 // is kept by the row's reference m: p = 2^(s - m), and over sealed blocks m is max s
 // + log2 of the block's largest scale - 6, so that the largest weight lies about 2^6,
 // and below 2^15 when m lags by 8 (the sums l and the outputs before are in units of
-// 2^m too, and follow).  Only weights 2^-20 of the largest keep fewer bits.
-constexpr int kWeightExp = 6;
+// 2^m too, and follow).  Only weights 2^-20 of the largest keep fewer bits.  The tiles
+// before the blocks have no say where the first block's scores lie further below theirs
+// than kWeightGap: there m starts from the block's own, so that rows that score far above
+// every block, as sinks do, cost its weights nothing (with sinks 2^28 above the blocks and
+// without a value, o would be off by a tenth of sum p |v|).  m falls by kFreeFall (values of
+// normal size ask for 13) without a look at the outputs before and l, and further only as
+// leaves them below 2^kTopExp: so values up to 2^80 keep inside fp32's range beside blocks
+// of next to no values.
+constexpr int kWeightExp = 6, kTopExp = 100;
+constexpr float kWeightGap = 8.f, kFreeFall = 24.f;
 // FP8_BLOCK: keys are their codes too, exact in f16, and their block's scale is the
 // factor that the softmax moves the scores back by.  The values' scale s, one for the
 // block, goes into the weights' exponents, 2^(s' - m + log2 s), and comes out of their
@@ -1472,7 +1480,27 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         const bool move = (kSealed || (kScaled && sca.values != nullptr)) && !moved;
         if (kScaled) top += sca.value_log;
         if (__any_sync(0xffffffffu, top > m + 8.f) || move) {
-          const float at = move ? m + sca.value_log : m, mn = top > (move ? at : m + 8.f) ? top : at;
+          const float at = move ? m + sca.value_log : m;
+          float mn = top > (move ? at : m + 8.f) ? top : at;
+          if (kScaled && move) {
+            if (top < at - kWeightGap) mn = top;
+            if (begun && __any_sync(0xffffffffu, m - mn > kFreeFall)) {
+              ok = wait.warp(base + L::kOFull + 8 * st, (hs - 1) & 1);
+              if (!ok) return false;
+              tc_fence_after();
+              float most = l;
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld32(my_o + 32 * c, o);
+                tmem_loaded<32>(o);
+#pragma unroll
+                for (int y = 0; y < 32; ++y) most = fmaxf(most, fabsf(__uint_as_float(o[y])));
+              }
+              const int room = kTopExp - ((__float_as_int(most) >> 23) - 127);
+              mn = fmaxf(mn, m - (float)min(max(room, 0), kTopExp));
+            }
+          }
           const float f = m == -INFINITY ? 0.f : ex2(m - mn);
           if (kScaled) moved = moved || move;
           m = mn;

@@ -1,6 +1,7 @@
 """Weights over sealed blocks with a reference of their own, and sums that meet in
-shared memory: decode over KV_FP8_BLOCK caches where full-width rows and blocks, or one block and
-the next, differ by far more than f16's range, and segments long enough that sums are flushed several times.
+shared memory: decode and chunks over KV_FP8_BLOCK caches (chunks over INT8 and FP8
+too) where full-width rows and blocks, or one block and the next, differ by far more
+than f16's range, and segments long enough that sums are flushed several times.
 
 Bounds of decode (fp32 out; A = sum p |v|).  Keys are multiples of 1/4 up to 7/4 and
 queries of +-1 (their codes times +-1 in blocks), so a score's products and sums are exact
@@ -9,7 +10,11 @@ the factor of y is rounded twice, y + j once, m and the difference once each: 3 
 3 |y + j| + 64 <= 3 * 40 + 3 * 80 + 64 < 430 in the cases below, 2.6e-5 ln 2 = 1.8e-5 of a
 weight.  Exponentials, three rescalings' among them, are off by 2^-22 each, 1e-6; the sums
 by less than 64 roundings, 3.9e-6; P by 2^-22.  Together a weight is off by less than
-2^-15.4, and a normalised one by twice that: 2^-14 A."""
+2^-15.4, and a normalised one by twice that: 2^-14 A.
+
+Chunks (bf16 out): 2^-8 |o| for o, 2^-8 A for P in bf16 or f16, 2^-12 A for the rest; INT8 and
+FP8 take keys' scales and products to 11 bits: 2 * 2^-12 of sum |q k| / sqrt(128) <= 64 * 7/4 /
+11.3 = 9.9, a weight's 4.9e-3, a normalised one's 9.7e-3 A."""
 import numpy as np
 import pytest
 import torch
@@ -215,3 +220,45 @@ def test_a_stream_of_its_own(cuda):
     s.synchronize()
     assert torch.equal(o, want) and torch.equal(new, want)
     case.cache.check()
+
+
+# ------------------------------------------------------------------------------ chunks
+COPIES = 80                                        # sequences: more items than there are SMs
+
+
+def _chunk(case, k, v, held, n):
+    """A chunk of n tokens on every one of COPIES sequences that hold the same: next to no item
+    is cut, so that one softmax sees the sinks and the blocks."""
+    kd, vd = (x.expand(COPIES, -1, -1, -1).contiguous() for x in _history(case, k, v))
+    case.cache.prefill(0, kd[:, :held].contiguous(), vd[:, :held].contiguous())
+    q = _queries(case, (n,)).expand(COPIES, -1, -1, -1).contiguous()
+    got = case.cache.chunk_attn(0, q, kd[:, held:].contiguous(), vd[:, held:].contiguous())
+    case.cache.check()
+    keys = 0.0 if case.kv_format == FMT else 9.7e-3
+    for i in range(0, n, 1 if n < 8 else 7):
+        o, A = _expected(case, q[0, i], held + i + 1, held)
+        _check(got[:, i], o, A, 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -12 + keys) * A)
+
+
+@pytest.mark.parametrize("fmt", [FMT, lkb.KV_FP8, lkb.KV_INT8], ids=["fp8_block", "fp8", "int8"])
+@pytest.mark.parametrize("gap", [0, 16, 24, 28, 32, 48])
+@pytest.mark.parametrize("n", [2, 40])
+def test_chunks_whose_sinks_score_far_above_the_blocks(cuda, n, gap, fmt):
+    held = SINK + LOCAL + 128 * 6 + 50
+    case, k, v = _case(4, held + n, fmt=fmt, batch=COPIES)
+    k[:, :SINK, :, :COMMON] = gap / 8
+    v[:, :SINK] = 0
+    v[:, held - LOCAL:] /= 256
+    _chunk(case, k, v, held, n)
+
+
+@pytest.mark.parametrize("fmt", [FMT, lkb.KV_FP8, lkb.KV_INT8], ids=["fp8_block", "fp8", "int8"])
+@pytest.mark.parametrize("zeros", [False, True], ids=["tiny", "zeros"])
+@pytest.mark.parametrize("n", [2, 40])
+def test_chunks_over_a_block_of_zeros_beside_huge_values(cuda, n, zeros, fmt):
+    held = SINK + LOCAL + 128 * 3 + 50
+    case, k, v = _case(4, held + n, fmt=fmt, batch=COPIES)
+    v[:, SINK:SINK + 128] *= 0.0 if zeros else 2.0 ** -50
+    v[:, :SINK] *= 2.0 ** 90
+    v[:, held - LOCAL:] *= 2.0 ** 90
+    _chunk(case, k, v, held, n)
