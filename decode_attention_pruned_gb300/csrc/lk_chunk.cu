@@ -1438,148 +1438,150 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
         float score, value_log;           // factor of scores; log2 of the values' size, where m follows it
         float weight_log, weight_back;    // FP8_BLOCK: log2 of the values' scale, and its inverse
       };
-      // One half of a key tile; false: no more of it.  kind 0: whatever the tile is; 1: keys
-      // and values in bf16; 2: a block of FP8_BLOCK.
-      auto step = [&](auto kind, int half, bool all, int halves, const uint32_t (&vis)[4], const Scale& sca) -> bool {
+      // The halves of a key tile.  kind 0: whatever the tile is; 1: keys and values in bf16;
+      // 2: a block of FP8_BLOCK.
+      auto tile = [&](auto kind, bool all, int halves, const uint32_t (&vis)[4], const Scale& sca) {
         constexpr bool kSealed = decltype(kind)::value == 2, kScaled = kQuant && decltype(kind)::value != 1;
-        const uint32_t s_half = my_s + half * kHalf;
-        ok = wait.warp(base + L::kSFull + 16 * st + 8 * half, (hs >> 1) & 1);
-        if (!ok) return false;
-        tc_fence_after();
-        if (half == halves) {
-          if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8);
-          ++hs;
-          return false;
-        }
-        uint32_t x[kHalf];
-        tmem_ld32(s_half, x);
-        tmem_ld32(s_half + 32, x + 32);
-        tmem_loaded<kHalf>(x);
-        if (!kSealed && !all) {
-          const uint32_t v0 = half == 0 ? vis[0] : vis[2], v1 = half == 0 ? vis[1] : vis[3];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if ((v0 >> c & 1u) == 0) x[c] = 0xff800000u;
-            if ((v1 >> c & 1u) == 0) x[32 + c] = 0xff800000u;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t s_half = my_s + half * kHalf;
+          ok = wait.warp(base + L::kSFull + 16 * st + 8 * half, (hs >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (half == halves) {
+            if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8);
+            ++hs;
+            break;
           }
-        }
-        float mx[4];
+          uint32_t x[kHalf];
+          tmem_ld32(s_half, x);
+          tmem_ld32(s_half + 32, x + 32);
+          tmem_loaded<kHalf>(x);
+          if (!kSealed && !all) {
+            const uint32_t v0 = half == 0 ? vis[0] : vis[2], v1 = half == 0 ? vis[1] : vis[3];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+            for (int c = 0; c < 32; ++c) {
+              if ((v0 >> c & 1u) == 0) x[c] = 0xff800000u;
+              if ((v1 >> c & 1u) == 0) x[32 + c] = 0xff800000u;
+            }
+          }
+          float mx[4];
 #pragma unroll
-        for (int c = 8; c < kHalf; c += 2)
-          mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kScaled ? sca.score : kScaleLog2);
-        // (nobody's rows score whatever lies behind q: they move no one's maximum)
-        if (!kDual && !mine) top = -INFINITY;
-        // The maximum moves only when a score exceeds it by 8, p by 2^8: fp32 sums and
-        // bf16 weights lose no more of it than of one below 1.  (Each row's by itself:
-        // what a row comes to does not depend on the others of its warp.)
-        // Over sealed blocks the scores count with their values' scale, and the first
-        // one moves m to what they need (see kWeightExp).
-        const bool move = (kSealed || (kScaled && sca.values != nullptr)) && !moved;
-        if (kScaled) top += sca.value_log;
-        if (__any_sync(0xffffffffu, top > m + 8.f) || move) {
-          const float at = move ? m + sca.value_log : m;
-          float mn = top > (move ? at : m + 8.f) ? top : at;
-          if (kScaled && move) {
-            if (top < at - kWeightGap) mn = top;
-            if (begun && __any_sync(0xffffffffu, m - mn > kFreeFall)) {
+          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+#pragma unroll
+          for (int c = 8; c < kHalf; c += 2)
+            mx[c >> 1 & 3] = max3(mx[c >> 1 & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kScaled ? sca.score : kScaleLog2);
+          // (nobody's rows score whatever lies behind q: they move no one's maximum)
+          if (!kDual && !mine) top = -INFINITY;
+          // The maximum moves only when a score exceeds it by 8, p by 2^8: fp32 sums and
+          // bf16 weights lose no more of it than of one below 1.  (Each row's by itself:
+          // what a row comes to does not depend on the others of its warp.)
+          // Over sealed blocks the scores count with their values' scale, and the first
+          // one moves m to what they need (see kWeightExp).
+          const bool move = (kSealed || (kScaled && sca.values != nullptr)) && !moved;
+          if (kScaled) top += sca.value_log;
+          if (__any_sync(0xffffffffu, top > m + 8.f) || move) {
+            const float at = move ? m + sca.value_log : m;
+            float mn = top > (move ? at : m + 8.f) ? top : at;
+            if (kScaled && move) {
+              if (top < at - kWeightGap) mn = top;
+              if (begun && __any_sync(0xffffffffu, m - mn > kFreeFall)) {
+                ok = wait.warp(base + L::kOFull + 8 * st, (hs - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                float most = l;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t o[32];
+                  tmem_ld32(my_o + 32 * c, o);
+                  tmem_loaded<32>(o);
+#pragma unroll
+                  for (int y = 0; y < 32; ++y) most = fmaxf(most, fabsf(__uint_as_float(o[y])));
+                }
+                const int room = kTopExp - ((__float_as_int(most) >> 23) - 127);
+                mn = fmaxf(mn, m - (float)min(max(room, 0), kTopExp));
+              }
+            }
+            const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+            if (kScaled) moved = moved || move;
+            m = mn;
+            l *= f;
+            if (begun) {
+              // (these scores came after the product before the last one was
+              // done, so its phase is the one before this)
               ok = wait.warp(base + L::kOFull + 8 * st, (hs - 1) & 1);
-              if (!ok) return false;
+              if (!ok) break;
               tc_fence_after();
-              float most = l;
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
                 tmem_ld32(my_o + 32 * c, o);
                 tmem_loaded<32>(o);
 #pragma unroll
-                for (int y = 0; y < 32; ++y) most = fmaxf(most, fabsf(__uint_as_float(o[y])));
+                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                tmem_st32(my_o + 32 * c, o);
               }
-              const int room = kTopExp - ((__float_as_int(most) >> 23) - 127);
-              mn = fmaxf(mn, m - (float)min(max(room, 0), kTopExp));
             }
           }
-          const float f = m == -INFINITY ? 0.f : ex2(m - mn);
-          if (kScaled) moved = moved || move;
-          m = mn;
-          l *= f;
-          if (begun) {
-            // (these scores came after the product before the last one was
-            // done, so its phase is the one before this)
-            ok = wait.warp(base + L::kOFull + 8 * st, (hs - 1) & 1);
-            if (!ok) return false;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32(my_o + 32 * c, o);
-              tmem_loaded<32>(o);
+          // P goes to the tensor core in V's type, bf16, which rounds every weight by up
+          // to 2^-8 of itself, as o is rounded once more at the end; l sums the unrounded
+          // ones.  Against fp64 o is off by 2.3e-3 instead of the 1.66e-3 of its own
+          // rounding.  P as the sum of two bf16 numbers, with a second product for the
+          // lower one, gives 1.66e-3, and takes 120 us instead of 100 for 64 sequences of
+          // 4096 tokens (4 queries each), 1117 instead of 871 for 1000 queries over 131072.
+          // (Sealed blocks' weights are f16: see kWeightExp.)
+          const float off = m == -INFINITY ? 0.f : kSealed ? sca.weight_log - m : -m;
+          const float sc = kScaled ? sca.score : kScaleLog2;
+          const uint64_t scale2 = pair(sc, sc), off2 = pair(off, off);
+          uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_st32(my_o + 32 * c, o);
-            }
-          }
-        }
-        // P goes to the tensor core in V's type, bf16, which rounds every weight by up
-        // to 2^-8 of itself, as o is rounded once more at the end; l sums the unrounded
-        // ones.  Against fp64 o is off by 2.3e-3 instead of the 1.66e-3 of its own
-        // rounding.  P as the sum of two bf16 numbers, with a second product for the
-        // lower one, gives 1.66e-3, and takes 120 us instead of 100 for 64 sequences of
-        // 4096 tokens (4 queries each), 1117 instead of 871 for 1000 queries over 131072.
-        // (Sealed blocks' weights are f16: see kWeightExp.)
-        const float off = m == -INFINITY ? 0.f : kSealed ? sca.weight_log - m : -m;
-        const float sc = kScaled ? sca.score : kScaleLog2;
-        const uint64_t scale2 = pair(sc, sc), off2 = pair(off, off);
-        uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < kHalf; c += 2) {
-          float p0, p1;
-          unpair(fma2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, off2), p0, p1);
-          p0 = ex2(p0);
-          p1 = ex2(p1);
-          sum[c >> 1 & 3] = add2(sum[c >> 1 & 3], pair(p0, p1));
-          if (kSealed) {
-            x[c >> 1] = pack_f16x2(p0, p1);
-          } else if (kScaled) {
-            x[c] = __float_as_uint(p0);
-            x[c + 1] = __float_as_uint(p1);
-          } else {
-            x[c >> 1] = pack_bf16x2(p0, p1);
-          }
-        }
-        if (kScaled && !kSealed) {
-          if (sca.values != nullptr) {
-            const ulonglong2* f = reinterpret_cast<const ulonglong2*>(sca.values + half * kHalf);
-            auto times = [&](int c, uint64_t y) {
-              float p0, p1;
-              unpair(mul2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), y), p0, p1);
+          for (int c = 0; c < kHalf; c += 2) {
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, off2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[c >> 1 & 3] = add2(sum[c >> 1 & 3], pair(p0, p1));
+            if (kSealed) {
               x[c >> 1] = pack_f16x2(p0, p1);
-            };
-#pragma unroll
-            for (int c = 0; c < kHalf; c += 4) {
-              const ulonglong2 y = f[c / 4];
-              times(c, y.x);
-              times(c + 2, y.y);
+            } else if (kScaled) {
+              x[c] = __float_as_uint(p0);
+              x[c + 1] = __float_as_uint(p1);
+            } else {
+              x[c >> 1] = pack_bf16x2(p0, p1);
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < kHalf; c += 2)
-              x[c >> 1] = pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
           }
+          if (kScaled && !kSealed) {
+            if (sca.values != nullptr) {
+              const ulonglong2* f = reinterpret_cast<const ulonglong2*>(sca.values + half * kHalf);
+              auto times = [&](int c, uint64_t y) {
+                float p0, p1;
+                unpair(mul2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), y), p0, p1);
+                x[c >> 1] = pack_f16x2(p0, p1);
+              };
+#pragma unroll
+              for (int c = 0; c < kHalf; c += 4) {
+                const ulonglong2 y = f[c / 4];
+                times(c, y.x);
+                times(c + 2, y.y);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kHalf; c += 2)
+                x[c >> 1] = pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+            }
+          }
+          tmem_st32(s_half, x);
+          float l0, l1;
+          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+          l = kSealed ? fmaf(l0 + l1, sca.weight_back, l) : l + (l0 + l1);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8 * half);
+          ++hs;
+          begun = true;
         }
-        tmem_st32(s_half, x);
-        float l0, l1;
-        unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
-        l = kSealed ? fmaf(l0 + l1, sca.weight_back, l) : l + (l0 + l1);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(base + L::kPFull + 16 * st + 8 * half);
-        ++hs;
-        begun = true;
-        return true;
       };
       // FP8_BLOCK: the sealed blocks come last, and have a loop of their own below
       constexpr int kStep = kDual ? 1 : 2;
@@ -1637,9 +1639,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           sca.score = back * *reinterpret_cast<const volatile float*>(sm + L::kTileBack + 4 * k_slot);
         }
         constexpr int kKind = kFmt == kKvFp8Block ? 1 : 0;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half)
-          if (!step(std::integral_constant<int, kKind>(), half, all, halves, vis, sca)) break;
+        tile(std::integral_constant<int, kKind>(), all, halves, vis, sca);
       }
       if constexpr (kFmt == kKvFp8Block) {
         int j = j0 + max(0, (m0 - j0 + kStep - 1) / kStep) * kStep;
@@ -1655,9 +1655,7 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
           if (!ok) break;
           const float4 scale = *reinterpret_cast<const float4*>(sm + L::kVScale + 16 * slot);
           const Scale sca{nullptr, back * scale.x, scale.y - kWeightExp, scale.y, scale.z};
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half)
-            if (!step(std::integral_constant<int, 2>(), half, true, 2, whole, sca)) break;
+          tile(std::integral_constant<int, 2>(), true, 2, whole, sca);
         }
       }
       entries = end;
