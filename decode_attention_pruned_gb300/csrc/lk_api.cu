@@ -1409,8 +1409,8 @@ lk_status chunk_attn_prepare(lk_cache cache, void* o, void* workspace, size_t ws
   // warps that expand them do.  (In proportion to bytes two prompts of 4096 tokens
   // take 251 us, with these 229; FP8 middles 143 and 114.)  Blocks of FP8_BLOCK cost
   // less, and on few channels as much as on many before two query tiles: 512 queries over
-  // 32768 tokens 178 us instead of 232 with the other sealed blocks' weights, 16
-  // sequences of 8192 tokens and 4 queries 87 instead of 90.
+  // 32768 tokens 174 us instead of 221 with the other sealed blocks' weights, 16
+  // sequences of 8192 tokens and 4 queries 84.6 instead of 88.
   const bool sealed = kv_quantized(cv.kv_format), block = cv.kv_format == kKvFp8Block;
   w.cost_item = w.dual ? 448 : sealed ? 112 : 216;
   w.cost_wide = w.dual ? 236 : 256;

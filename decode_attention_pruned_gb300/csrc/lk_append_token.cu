@@ -11,7 +11,11 @@
 // lengths advance with the last block (the layer's word counts them, and is left at
 // zero; appends to different layers may overlap).
 //
-// Short: what bounds it is the latency of dependent loads (length, head, ring row).
+// Short: what bounds it is the latency of dependent loads (length, head, ring row) and of
+// its instructions.  8 sequences of 8 kv heads of 4 query heads, one call behind another on the
+// GPU: 6.2 us a call for bf16 caches, where a rotation and an append, two launches that
+// overlap, take 4.7; 6.5 for FP8_BLOCK ones (7.0).  What it saves is the host's second call (8.5
+// us instead of 15.8).
 #include <cuda_runtime.h>
 
 #include "lk_append.cuh"

@@ -40,11 +40,11 @@
 // a ring that holds two to five tiles per group; 64 sequences of 4096 tokens
 // take 98 us, 1.4 times what a plain copy's rate gives their bytes.  Sealed
 // blocks: the softmax and the four warps that expand them, which share instruction
-// caches with every other role; 16 sequences of 8192 tokens take 114 us, 4.0 times
-// their bytes; as FP8_BLOCK, whose one scale is the softmax's affair, 16 sequences of
-// 8192 tokens and 16 queries each take 87 us, and 512 queries of 32 heads over 32768
-// tokens 178 (in bf16 151), paced by the loading thread and the makers: their
-// instructions come at 20 clocks each.  One sequence: three dependent launches, 28 us over 32768 tokens.
+// caches with every other role; 16 sequences of 8192 tokens with 4 queries each take 113 us,
+// 4.0 times their bytes; as FP8_BLOCK, whose one scale is the softmax's affair, 84 us, and 512
+// queries of 32 heads over 32768 tokens 174 (FP8 245, bf16 150), paced by the loading thread
+// and the makers: their instructions come at 20 clocks each.  One sequence: three
+// dependent launches, 28 us over 32768 tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -558,8 +558,8 @@ cudaError_t launch_chunk_append(const ChunkArgs& args, const RopeChunk* rope, bo
       return launch_after(quant ? chunk_rope_kernel<4, true> : chunk_rope_kernel<4, false>, dim3((unsigned)blocks), 256,
                           0, stream, args, rc);
     }
-    return launch_after(quant ? chunk_rope_kernel<1, true> : chunk_rope_kernel<1, false>, dim3((unsigned)tokens), 256, 0,
-                        stream, args, rc);
+    return launch_after(quant ? chunk_rope_kernel<1, true> : chunk_rope_kernel<1, false>, dim3((unsigned)tokens), 256,
+                        0, stream, args, rc);
   }
   const int64_t items = (int64_t)args.nb * args.n_max * cv.Hkv;
   const int64_t blocks = min((items + kBlockRows - 1) / kBlockRows, (int64_t)num_sms * 16);
