@@ -960,21 +960,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool single = first_cta == last_cta;
     const int g = tid >> 5, dd = (tid & 31) * 4;           // a warp per query head, four channels a lane
     if (g < G) {
+      // (In units in which l lies in [1, 2): where m fell far, o and l are as much larger, and
+      // 2^(m - M) alone might leave nothing of them.)
+      auto exponent_of = [](float l) { return (__float_as_int(l) >> 23) - 127; };
       float M = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, merge_m[w * kHeads + g]);
+      for (int w = 0; w < kWarps; ++w)
+        M = fmaxf(M, merge_m[w * kHeads + g] + (float)exponent_of(merge_l[w * kHeads + g]));
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float m = merge_m[w * kHeads + g];
+        const float m = merge_m[w * kHeads + g], l = merge_l[w * kHeads + g];
         if (m == -INFINITY) continue;                      // (and whatever its slot holds)
-        const float f = ex2(m - M);
+        const int e = exponent_of(l);
+        const float f = ex2(m + (float)e - M), unit = power2(-e);
         const float4 v = *reinterpret_cast<const float4*>(merge_o + (w * kHeads + g) * kHeadDim + dd);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
-        sum = fmaf(f, merge_l[w * kHeads + g], sum);
+        acc.x = fmaf(f, v.x * unit, acc.x);
+        acc.y = fmaf(f, v.y * unit, acc.y);
+        acc.z = fmaf(f, v.z * unit, acc.z);
+        acc.w = fmaf(f, v.w * unit, acc.w);
+        sum = fmaf(f, l * unit, sum);
       }
       if (single) {
         const float inv = sum > 0.f ? 1.f / sum : 0.f;

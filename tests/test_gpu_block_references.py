@@ -34,11 +34,11 @@ LOG2 = 1.4426950408889634 / 128 ** 0.5             # of a score, per q.k
 SINK, LOCAL = 4, 32
 
 
-def _case(G, N, counts=(32, 128), fmt=FMT, batch=1):
+def _case(G, N, counts=(32, 128), fmt=FMT, batch=1, local=LOCAL):
     """Keys that are 0 on the common channels and small multiples of 1/4 on the others, the
     kept ones among them; each block has a key of 7/4."""
     H = len(counts)
-    w = TINY.scaled(num_q_heads=H * G, num_kv_heads=H, sink=SINK, local=LOCAL, batch=batch)
+    w = TINY.scaled(num_q_heads=H * G, num_kv_heads=H, sink=SINK, local=local, batch=batch)
     masks = np.zeros((1, H, 128), np.uint8)
     for h, c in enumerate(counts):
         masks[0, h, 128 - c:] = 1
@@ -108,6 +108,30 @@ def test_rows_that_score_far_above_the_blocks(cuda, G, gap, ctas):
     v[:, -LOCAL:] /= 256                               # (so that the middle is most of o)
     _history(case, k, v)
     _decode(case, N, ctas)
+
+
+@pytest.mark.parametrize("ctas", [0, 50, 5, 1])
+@pytest.mark.parametrize("G", [3, 6])
+def test_parts_whose_references_fell_far(cuda, G, ctas):
+    """Parts of an entry that hold a few rows and a block of zeros, for which m falls by 76, beside
+    one with sinks 2^56 above them: what they hold is still there when they meet.  (|y| <=
+    66 and |y + j| <= 140: 2.8e-5 instead of the 1.8e-5 above, 2^-13 A in all.)"""
+    N = 843
+    for counts in ((64, 64, 64), (32, 64, 128), (128, 32, 96)):
+        case, k, v = _case(G, N, counts=counts, local=200)
+        k[:, :SINK, :, :COMMON] = 7
+        v[:, :SINK] = 0
+        v[:, SINK:SINK + 128] = 0
+        _history(case, k, v)
+        case.prefill(0, N)
+        case.cache.set_decode_ctas(ctas)
+        q = _queries(case)
+        got = case.cache.decode(0, q)
+        case.cache.check()
+        for h in range(3):                             # head by head, so that none hides behind another's size
+            o, A = _expected(case, q[0], N, N)
+            rows = slice(h * G, (h + 1) * G)
+            _check(got[0, rows], o[rows], A[rows], 2.0 ** -13 * A[rows])
 
 
 @pytest.mark.parametrize("gap", [20, 30])
