@@ -286,3 +286,23 @@ def test_chunks_over_a_block_of_zeros_beside_huge_values(cuda, n, zeros, fmt):
     v[:, :SINK] *= 2.0 ** 90
     v[:, held - LOCAL:] *= 2.0 ** 90
     _chunk(case, k, v, held, n)
+
+
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("batch", [1, 7])
+def test_chunks_in_parts_whose_references_fell_far(cuda, n, batch):
+    """The same for items that are cut between thread blocks."""
+    held = 843
+    for counts in ((64, 64, 64), (32, 64, 128), (128, 32, 96)):
+        case, k, v = _case(2, held + n, counts=counts, local=200, batch=batch)
+        k[:, :SINK, :, :COMMON] = 7
+        v[:, :SINK] = 0
+        v[:, SINK:SINK + 128] = 0
+        kd, vd = (x.expand(batch, -1, -1, -1).contiguous() for x in _history(case, k, v))
+        case.cache.prefill(0, kd[:, :held].contiguous(), vd[:, :held].contiguous())
+        q = _queries(case, (n,)).expand(batch, -1, -1, -1).contiguous()
+        got = case.cache.chunk_attn(0, q, kd[:, held:].contiguous(), vd[:, held:].contiguous())
+        case.cache.check()
+        for i in range(n):
+            o, A = _expected(case, q[0, i], held + i + 1, held)
+            _check(got[:, i], o, A, 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -12) * A)
