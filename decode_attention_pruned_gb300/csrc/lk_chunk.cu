@@ -40,9 +40,9 @@
 // a ring that holds two to five tiles per group; 64 sequences of 4096 tokens
 // take 98 us, 1.4 times what a plain copy's rate gives their bytes.  Sealed
 // blocks: the softmax and the four warps that expand them, which share instruction
-// caches with every other role; 16 sequences of 8192 tokens with 4 queries each take 113 us,
+// caches with every other role; 16 sequences of 8192 tokens with 4 queries each take 114 us,
 // 4.0 times their bytes; as FP8_BLOCK, whose one scale is the softmax's affair, 84 us, and 512
-// queries of 32 heads over 32768 tokens 174 (FP8 245, bf16 150), paced by the loading thread
+// queries of 32 heads over 32768 tokens 174 (FP8 246, bf16 150), paced by the loading thread
 // and the makers: their instructions come at 20 clocks each.  One sequence: three
 // dependent launches, 28 us over 32768 tokens.
 #include <cuda.h>
@@ -1673,8 +1673,8 @@ __global__ void __launch_bounds__(kFmt == kKvBf16 ? kThreads : kThreadsQ, 1)
       }
       // (FP8_BLOCK: in units in which l lies in [1, 2): where m fell far, o and l are as much
       // larger, and 2^(m - the others' m) alone might leave nothing of them.  Values of INT8 / FP8
-      // blocks let m fall by 66 at most where they are next to nothing: there these
-      // instructions cost 16 sequences of 8192 tokens with 4 queries 1.7 us of 113.5.)
+      // blocks let m fall by 66 at most where they are next to nothing, and with these
+      // instructions 16 sequences of 8192 tokens with 4 queries take 115.3 us instead of 114.4.)
       auto unit = [](float& m, float& l) {
         if (kFmt != kKvFp8Block || !(l > 0.f)) return 1.f;
         const int e = (__float_as_int(l) >> 23) - 127;

@@ -37,11 +37,11 @@
 // spans CTAs leaves partials, merged in order by the last CTA to come.
 //
 // What bounds it (from cold caches): the bytes.  64 sequences to 4096 tokens (8 kv heads of
-// 4 query heads, 32 channels kept in five, 64 in one, none in two) take 61 us (309 MB: 5.1 TB/s),
+// 4 query heads, 32 channels kept in five, 64 in one, none in two) take 61.6 us (309 MB: 5.0 TB/s),
 // 4 x 131072 tokens (4 kv heads of 7 query heads; 32, 0, 64 and 96 channels) 60 us (315 MB),
 // with the copies alone and no arithmetic 55 and 53 us; 1 x 32768 (8 kv heads, 32 channels)
 // 19 us (45 MB), 14 us with the copies alone, 2.5 us of them before the first copy is sent
-// (the lengths, the line, the place of the first piece); 8 sequences to 777 tokens 11.3 us,
+// (the lengths, the line, the place of the first piece); 8 sequences to 777 tokens 11.4 us,
 // which are those, one load after another, and the merges.  32 layers of 64 x 4096 tokens
 // (11.9 GB) in one launch take 1856 us (6.4 TB/s), in a launch for each 2213.
 //   What went before: each lane copying its own words ahead with cp.async spent 400
